@@ -733,6 +733,180 @@ int ito_dfp16_update_bits(int16_t *W, const int16_t *g, const int32_t *d_exp_g, 
 int ito_dfp_set_bits(int16_t *W, int64_t n, int32_t bits_old, int32_t bits_new, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Float operators: the float layers, loss and optimizer that train beside the
+ * integer layers ("Mixed Precision Training of Convolutional Neural Networks
+ * using Integer Operations", sections 3 and 4: the DFP kernels produce FP32
+ * outputs for float layers, and FP32 master weights are updated in FP32 and
+ * quantised for the next step). The page gives no formulas for them; each entry
+ * point states its own. Sums, norms' and softmax statistics are held in 32 bits
+ * and a result is rounded once to its type. Row strides (ld*) count elements;
+ * the elements of a row are consecutive. Outputs must not overlap inputs or one
+ * another unless the entry point says so. Results do not depend on the order in
+ * which the GPU runs its blocks: no sum uses atomics.
+ * ---------------------------------------------------------------------- */
+
+typedef enum ito_type { ITO_F32 = 0, ITO_BF16 = 1, ITO_F16 = 2 } ito_type;
+
+typedef enum ito_act {
+    ITO_ACT_NONE = 0,
+    ITO_ACT_RELU = 1,       /* max(z, 0) */
+    ITO_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2 */
+    ITO_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    ITO_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} ito_act;
+
+/* Bytes of device workspace ito_fp_linear_fwd needs (0 on invalid sizes, and
+ * where none is needed): room for partial sums when a product with few output
+ * tiles is split along IC, and copies of operands whose rows do not start on
+ * 16-byte boundaries. The pointers are looked at for their alignment only. */
+size_t ito_fp_linear_fwd_workspace_size(const void *x, int64_t ldx, const void *W, int64_t ldw, int B, int IC,
+                                        int OC);
+
+/* Linear layer on 16-bit floats with bias, activation and residual in the
+ * product's epilogue:
+ *   v[b][oc] = sum_ic x[b][ic] * W[oc][ic] + bias[oc]     (32-bit sums)
+ *   z = v in `type` (when z != NULL: the backward pass needs it)
+ *   y = act(v) + residual[b][oc] in `out_type`
+ * type: ITO_BF16 or ITO_F16, of x [B][IC], W [OC][IC] and z [B][OC]; out_type:
+ * type or ITO_F32, of y [B][OC] and residual [B][OC] (NULL: none; it may be y
+ * itself with the same stride); bias_type: type or ITO_F32, of bias [OC] (NULL:
+ * none); act: ito_act. A few rows (B up to 16) stream W once at the memory's
+ * rate. workspace: 256-byte aligned, at least
+ * ito_fp_linear_fwd_workspace_size() bytes (may be NULL where that is 0).
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type or act,
+ * workspace), ITO_ERR_SHAPE (a size outside 1 .. 2^20, a row stride below the
+ * row's length), ITO_ERR_CUDA. */
+int ito_fp_linear_fwd(const void *x, int64_t ldx, const void *W, int64_t ldw, const void *bias, const void *residual,
+                      int64_t ldr, int type, int out_type, int bias_type, int act, int B, int IC, int OC,
+                      void *workspace, size_t workspace_bytes, void *z, int64_t ldz, void *y, int64_t ldy,
+                      void *stream);
+
+/* Bytes of device workspace ito_fp_linear_bwd needs (0 on invalid sizes): dz,
+ * the bias gradient's partial sums, and what the forward pass's takes. */
+size_t ito_fp_linear_bwd_workspace_size(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *W,
+                                        int64_t ldw, int act, int B, int IC, int OC);
+
+/* Backward pass of ito_fp_linear_fwd (the residual's gradient is dy itself):
+ *   dz[b][oc] = dy[b][oc] * act'(z[b][oc]), rounded once to `type` (it is an
+ *               operand of the products below)
+ *   dx[b][ic] = sum_oc dz[b][oc] * W[oc][ic]           in `type`
+ *   dW[oc][ic] = sum_b dz[b][oc] * x[b][ic]            in `out_type`
+ *   dbias[oc] = sum_b dz[b][oc] (before its rounding)  in 32 bits
+ * Any of dx, dW, dbias may be NULL (not computed); z may be NULL for
+ * ITO_ACT_NONE; x is read for dW only, W for dx only. The slope of ITO_ACT_RELU
+ * at 0 is 0. Errors as ito_fp_linear_fwd. */
+int ito_fp_linear_bwd(const void *dy, int64_t lddy, const void *z, int64_t ldz, const void *x, int64_t ldx,
+                      const void *W, int64_t ldw, int type, int out_type, int act, int B, int IC, int OC,
+                      void *workspace, size_t workspace_bytes, void *dx, int64_t lddx, void *dW, int64_t lddw,
+                      float *dbias, void *stream);
+
+/* Layer norm over a row of `cols` elements:
+ *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ * x, y: [rows][cols] of `type` (any ito_type; y may be x itself with the same
+ * stride); gamma, beta: [cols] of w_type (type or ITO_F32), NULL for 1 and 0;
+ * mean, rstd: float [rows] for the backward pass (either may be NULL).
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type, eps < 0),
+ * ITO_ERR_SHAPE (a size < 1, rows above 2^40, cols above 2^24, a row stride below
+ * cols), ITO_ERR_CUDA. */
+int ito_layer_norm_fwd(const void *x, int64_t ldx, int type, const void *gamma, const void *beta, int w_type,
+                       int64_t rows, int cols, float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                       void *stream);
+
+/* Bytes of device workspace for the sums of dgamma and dbeta (0 on invalid sizes). */
+size_t ito_layer_norm_bwd_workspace_size(int64_t rows, int cols);
+
+/* Backward pass of ito_layer_norm_fwd, with h = (x - mean) * rstd, a = dy * gamma:
+ *   dx = rstd * (a - sum(a) / cols - h * sum(a * h) / cols)
+ *   dgamma[c] = sum over rows of dy * h;  dbeta[c] = sum over rows of dy   (float)
+ * mean, rstd: as the forward pass wrote them. Any of dx, dgamma, dbeta may be
+ * NULL (not computed). dx may be dy itself with the same stride. workspace:
+ * 256-byte aligned, needed for dgamma or dbeta. Errors as ito_layer_norm_fwd. */
+int ito_layer_norm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx, int type, const void *gamma,
+                       int w_type, const float *mean, const float *rstd, int64_t rows, int cols, void *workspace,
+                       size_t workspace_bytes, void *dx, int64_t lddx, float *dgamma, float *dbeta, void *stream);
+
+/* Log probabilities of given tokens (class labels) under logits [rows][classes]
+ * of `type` (any ito_type), with the entropy and the k largest alternatives:
+ *   lse = log sum_j exp(x_j);  logp = x_target - lse;  entropy = -sum_j p_j log p_j
+ *   top_ids[0 .. k), top_logp: the k largest logits' classes, largest first, equal
+ *   logits in the order of their class (a NaN counts as largest), and their
+ *   log probabilities
+ * targets: int32 [rows]; -1 stands for no token (logp 0); any other value outside
+ * [0, classes) is treated the same and records ITO_ERR_ARG in the device error
+ * word (ito_get_error), as in ito_top_error. A logit of -inf is a masked class
+ * (p = 0); a row of them only has lse and log probabilities of -inf and entropy
+ * 0. A row with a NaN or +inf has NaN results. k: 0 .. 32, at most classes.
+ * logp, entropy, lse: float [rows] (each may be NULL; targets may be NULL
+ * without logp); top_ids: int32 [rows][k]; top_logp: float [rows][k].
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type, k),
+ * ITO_ERR_SHAPE (a size < 1, rows above 2^40, classes above 2^30, a row stride
+ * below classes, k above classes), ITO_ERR_CUDA. */
+int ito_token_logprobs_fwd(const void *logits, int64_t ld, int type, const int32_t *targets, int64_t rows,
+                           int classes, int k, float *logp, float *entropy, float *lse, int32_t *top_ids,
+                           float *top_logp, void *stream);
+
+/* Gradient of sum_r (g_logp[r] * logp[r] + g_entropy[r] * entropy[r]) for the
+ * logits, with p_j = exp(x_j - lse):
+ *   dlogits_j = g_logp * ([j == target] - p_j) - g_entropy * p_j * (log p_j + entropy)
+ * lse, entropy: as the forward pass wrote them; g_logp, g_entropy: float [rows],
+ * either may be NULL (no such term; entropy is read for g_entropy only, targets
+ * for g_logp only). Targets outside [0, classes) as in the forward pass: no term
+ * from g_logp. A row whose lse is -inf has a gradient of 0. dlogits: `type`, may
+ * be the logits themselves with the same stride. Errors as ito_token_logprobs_fwd. */
+int ito_token_logprobs_bwd(const void *logits, int64_t ld, int type, const int32_t *targets, const float *lse,
+                           const float *entropy, int64_t rows, int classes, const float *g_logp,
+                           const float *g_entropy, void *dlogits, int64_t ldd, void *stream);
+
+/* One tensor of an AdamW step. States in 32 bits: m, v are float [n]. In 8 bits
+ * they are bytes [n] under a shared exponent E for each 128 consecutive elements
+ * (m_exp, v_exp: int8 [ceil(n / 128)]):
+ *   m: bit 7 the sign, c = the rest: 2^(E - 15 + (c >> 3)) * (1 + (c & 7) / 8), 0 for c = 0
+ *   v: c = the byte:                 2^(E - 31 + (c >> 3)) * (1 + (c & 7) / 8), 0 for c = 0
+ * and every element of a block with E = -128 is a NaN (the block held a NaN or an
+ * infinity). Zero bytes and exponents are states of 0. */
+typedef struct ito_adamw_tensor {
+    float *w;              /* weights, updated in place */
+    const void *g;         /* gradient, of grad_type */
+    void *copy;            /* the updated weights in copy_type as well, or NULL */
+    void *m, *v;           /* first and second moment, updated in place */
+    int8_t *m_exp, *v_exp; /* 8-bit states only */
+    int64_t n;             /* elements (0: nothing to do) */
+    double weight_decay;   /* of this tensor */
+} ito_adamw_tensor;
+
+typedef struct ito_adamw_params {
+    double lr, beta1, beta2, eps;
+    double grad_scale;     /* the gradients are multiplied by it first (1: as they are) */
+    int64_t step;          /* 1 for the first step */
+    int32_t state_bits;    /* 32 or 8 */
+    int32_t grad_type;     /* ito_type of every g */
+    int32_t copy_type;     /* ITO_BF16 or ITO_F16, of every copy */
+    uint32_t seed;         /* of the 8-bit states' rounding */
+} ito_adamw_params;
+
+/* One AdamW step over n_tensors tensors (host array; it is read before the call
+ * returns):
+ *   g' = g * grad_scale;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * Each operation is rounded to 32 bits in that order. 8-bit states are rounded
+ * stochastically (up with the probability of the part cut off), by a hash of
+ * seed, step, the tensor's place in the array and the element: the same call gives
+ * the same states. A v above zero stays above zero; an m below 2^-15 of its block's
+ * largest becomes 0. The weights' step uses the moments before that rounding.
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, an unknown type or state_bits,
+ * step < 1, a beta outside [0, 1), eps < 0), ITO_ERR_SHAPE (n_tensors < 1, n
+ * outside 0 .. 2^40), ITO_ERR_CUDA. */
+int ito_adamw_step(const ito_adamw_tensor *tensors, int n_tensors, const ito_adamw_params *p, void *stream);
+
+/* The values that 8-bit states stand for, tensor after tensor: m_out and v_out
+ * (either may be NULL) of out_type ITO_F32 or ITO_BF16 (exact in both), sum of n
+ * elements each. Reads m, v, m_exp, v_exp and n of the tensors. Errors as
+ * ito_adamw_step. */
+int ito_adamw_moments(const ito_adamw_tensor *tensors, int n_tensors, int out_type, void *m_out, void *v_out,
+                      void *stream);
+
+/* ------------------------------------------------------------------------
  * Measurement hooks (no counterpart in the pages; used by the benchmark)
  * ---------------------------------------------------------------------- */
 

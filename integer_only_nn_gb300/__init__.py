@@ -23,6 +23,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 ITO_OK, ITO_ERR_ARG, ITO_ERR_SHAPE, ITO_ERR_CUDA, ITO_ERR_TIMEOUT, ITO_ERR_EXPONENT, ITO_ERR_UNSUPPORTED = range(7)
 ITO_LAYER_LINEAR, ITO_LAYER_LINEAR_RELU, ITO_LAYER_CONV3X3_RELU, ITO_LAYER_GAP = range(4)
+ITO_F32, ITO_BF16, ITO_F16 = range(3)
+ITO_ACT_NONE, ITO_ACT_RELU, ITO_ACT_GELU, ITO_ACT_GELU_TANH, ITO_ACT_SILU = range(5)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -49,6 +51,19 @@ class AptParams(ctypes.Structure):
 class LayerDesc(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
                 ("in_h", ctypes.c_int32), ("in_w", ctypes.c_int32), ("stride", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("g", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
+
+
+class AdamwParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double), ("step", ctypes.c_int64),
+                ("state_bits", ctypes.c_int32), ("grad_type", ctypes.c_int32), ("copy_type", ctypes.c_int32),
+                ("seed", ctypes.c_uint32)]
 
 
 _SIGS = {
@@ -125,6 +140,19 @@ _SIGS = {
     "ito_dfp16_model_set_precision": (_I, [_P, _I, _I32, _P]),
     "ito_dfp16_model_apt_enable": (_I, [_P, ctypes.POINTER(AptParams), _P]),
     "ito_dfp16_model_apt_epoch_end": (_I, [_P, _P, _P, _P]),
+    "ito_fp_linear_fwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _I, _I, _I]),
+    "ito_fp_linear_fwd": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P,
+                               _I64, _P]),
+    "ito_fp_linear_bwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I]),
+    "ito_fp_linear_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P,
+                               _I64, _P, _P]),
+    "ito_layer_norm_fwd": (_I, [_P, _I64, _I, _P, _P, _I, _I64, _I, ctypes.c_float, _P, _I64, _P, _P, _P]),
+    "ito_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I]),
+    "ito_layer_norm_bwd": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _I, _P, _SZ, _P, _I64, _P, _P, _P]),
+    "ito_token_logprobs_fwd": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "ito_token_logprobs_bwd": (_I, [_P, _I64, _I, _P, _P, _P, _I64, _I, _P, _P, _P, _I64, _P]),
+    "ito_adamw_step": (_I, [_P, _I, ctypes.POINTER(AdamwParams), _P]),
+    "ito_adamw_moments": (_I, [_P, _I, _I, _P, _P, _P]),
 }
 
 for _name, (_res, _args) in _SIGS.items():
@@ -769,3 +797,304 @@ def _from_ptr(ptr, n, dtype, eb):
     torch = _torch()
     typestr = {1: "|i1", 2: "<i2", 4: "<i4", 8: "<i8"}[eb]
     return torch.as_tensor(_CudaArray(ptr, n, typestr), device="cuda")
+
+
+# ---------------------------------------------------------- float operators
+
+_ACTS = {"none": ITO_ACT_NONE, "relu": ITO_ACT_RELU, "gelu": ITO_ACT_GELU, "gelu_tanh": ITO_ACT_GELU_TANH,
+         "silu": ITO_ACT_SILU}
+_TYPE_IDS = {}
+
+
+def _type_id(t, name):
+    """ito_type of a tensor; -1 (which the library rejects) is never passed on."""
+    if not _TYPE_IDS:
+        torch = _torch()
+        _TYPE_IDS.update({torch.float32: ITO_F32, torch.bfloat16: ITO_BF16, torch.float16: ITO_F16})
+    r = _TYPE_IDS.get(t.dtype)
+    if r is None:
+        raise ItoError(ITO_ERR_ARG, "%s: type %s (float32, bfloat16 and float16 are taken)" % (name, t.dtype))
+    return r
+
+
+def _act_id(act):
+    r = _ACTS.get(act, act)
+    if not isinstance(r, int):
+        raise ItoError(ITO_ERR_ARG, "unknown activation %r" % (act,))
+    return r
+
+
+def _matrix(t, name, rows=None, cols=None, dtype=None):
+    """Checks a 2-D device tensor whose rows' elements are consecutive; -> its row stride."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%s][%s]" % (
+            name, list(t.shape), "rows" if rows is None else rows, "columns" if cols is None else cols))
+    if not t.numel():
+        raise ItoError(ITO_ERR_SHAPE, "%s: no elements" % name)
+    if not t.is_cuda:
+        raise ItoError(ITO_ERR_ARG, "%s: not on the GPU" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise ItoError(ITO_ERR_ARG, "%s: type %s, expected %s" % (name, t.dtype, dtype))
+    s0, s1 = t.stride()
+    if s1 != 1 and t.shape[1] > 1:
+        raise ItoError(ITO_ERR_ARG, "%s: the elements of a row are not consecutive" % name)
+    return s0
+
+
+def _vector(t, name, n, dtypes):
+    """Checks a dense 1-D device tensor (None passes)."""
+    if t is None:
+        return
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%d]" % (name, list(t.shape), n))
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise ItoError(ITO_ERR_ARG, "%s: %s on %s" % (name, t.dtype, t.device))
+    if n > 1 and t.stride(0) != 1:
+        raise ItoError(ITO_ERR_ARG, "%s: not contiguous" % name)
+
+
+class _On:
+    """Allocations of a call belong to the stream it launches on."""
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else _torch().cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _scratch(n, device):
+    """A 256-byte aligned workspace of n bytes, and the tensor that owns it."""
+    if not n:
+        return None, None
+    t = _torch().empty(n + 255, dtype=_torch().uint8, device=device)
+    return _aligned256(t), t
+
+
+def ito_fp_linear_fwd(x, W, bias=None, act="none", residual=None, save_z=False, out_dtype=None, stream=None):
+    """y = act(x W^T + bias) + residual for bf16 or f16 x [B][IC], W [OC][IC]; -> y, or (y, z)
+    with z = x W^T + bias in x's type where save_z. out_dtype (of y and residual): x's type
+    or float32. bias: x's type or float32."""
+    torch = _torch()
+    ldx, ldw = _matrix(x, "x"), _matrix(W, "W", None, x.shape[1], x.dtype)
+    ty = _type_id(x, "x")
+    B, IC = x.shape
+    OC = W.shape[0]
+    out_dtype = out_dtype or x.dtype
+    _vector(bias, "bias", OC, (x.dtype, torch.float32))
+    ldr = 0 if residual is None else _matrix(residual, "residual", B, OC, out_dtype)
+    with _On(stream):
+        y = torch.empty((B, OC), dtype=out_dtype, device=x.device)
+        z = torch.empty((B, OC), dtype=x.dtype, device=x.device) if save_z else None
+        px, pw = _ptr(x), _ptr(W)
+        n = _lib.ito_fp_linear_fwd_workspace_size(px, ldx, pw, ldw, B, IC, OC)
+        ws, keep = _scratch(n, x.device)
+        _check(_lib.ito_fp_linear_fwd(px, ldx, pw, ldw, _ptr(bias), _ptr(residual), ldr, ty, _type_id(y, "out_dtype"),
+                                      ITO_F32 if bias is None else _type_id(bias, "bias"), _act_id(act), B, IC, OC,
+                                      ws, n, _ptr(z), OC, _ptr(y), OC, _stream(stream)))
+    return (y, z) if save_z else y
+
+
+def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, need_dbias=True, dw_dtype=None,
+                      stream=None):
+    """Gradients of ito_fp_linear_fwd -> (dx [B][IC] in x's type, dW [OC][IC] in dw_dtype (x's
+    type or float32), dbias float32 [OC]); None for those not needed."""
+    torch = _torch()
+    ldx, ldw = _matrix(x, "x"), _matrix(W, "W", None, x.shape[1], x.dtype)
+    B, IC = x.shape
+    OC = W.shape[0]
+    lddy = _matrix(dy, "dy", B, OC, x.dtype)
+    ldz = 0 if z is None else _matrix(z, "z", B, OC, x.dtype)
+    a = _act_id(act)
+    dw_dtype = dw_dtype or x.dtype
+    if not (need_dx or need_dw or need_dbias):
+        raise ItoError(ITO_ERR_ARG, "no output")
+    with _On(stream):
+        dx = torch.empty((B, IC), dtype=x.dtype, device=x.device) if need_dx else None
+        dw = torch.empty((OC, IC), dtype=dw_dtype, device=x.device) if need_dw else None
+        db = torch.empty(OC, dtype=torch.float32, device=x.device) if need_dbias else None
+        n = _lib.ito_fp_linear_bwd_workspace_size(_ptr(dy), lddy, _ptr(x), ldx, _ptr(W), ldw, a, B, IC, OC)
+        ws, keep = _scratch(n, x.device)
+        ty = _type_id(x, "x")
+        _check(_lib.ito_fp_linear_bwd(_ptr(dy), lddy, _ptr(z), ldz, _ptr(x), ldx, _ptr(W), ldw, ty,
+                                      ty if dw is None else _type_id(dw, "dw_dtype"), a, B, IC, OC, ws, n, _ptr(dx),
+                                      IC, _ptr(dw), IC, _ptr(db), _stream(stream)))
+    return dx, dw, db
+
+
+def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
+    """x [rows][cols] of float32, bfloat16 or float16 -> (y, mean float32 [rows], rstd float32 [rows])"""
+    torch = _torch()
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
+    _vector(beta, "beta", cols, (x.dtype, torch.float32))
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
+    w = gamma if gamma is not None else beta
+    with _On(stream):
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        st = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+        p = st.data_ptr()
+        _check(_lib.ito_layer_norm_fwd(_ptr(x), ldx, _type_id(x, "x"), _ptr(gamma), _ptr(beta),
+                                       ITO_F32 if w is None else _type_id(w, "gamma"), rows, cols, eps, _ptr(y), cols,
+                                       p, p + 4 * rows, _stream(stream)))
+    return y, st[0], st[1]
+
+
+def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, stream=None):
+    """-> (dx in x's type, dgamma float32 [cols], dbeta float32 [cols]); None for those not needed."""
+    torch = _torch()
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    lddy = _matrix(dy, "dy", rows, cols, x.dtype)
+    _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
+    _vector(mean, "mean", rows, (torch.float32,))
+    _vector(rstd, "rstd", rows, (torch.float32,))
+    with _On(stream):
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if need_dx else None
+        dw = torch.empty((2, cols), dtype=torch.float32, device=x.device) if need_dw else None
+        n = _lib.ito_layer_norm_bwd_workspace_size(rows, cols) if need_dw else 0
+        ws, keep = _scratch(n, x.device)
+        p = dw.data_ptr() if need_dw else None
+        _check(_lib.ito_layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _type_id(x, "x"), _ptr(gamma),
+                                       ITO_F32 if gamma is None else _type_id(gamma, "gamma"), _ptr(mean), _ptr(rstd),
+                                       rows, cols, ws, n, _ptr(dx), cols, p, p + 4 * cols if need_dw else None,
+                                       _stream(stream)))
+    return (dx, dw[0], dw[1]) if need_dw else (dx, None, None)
+
+
+def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
+    """logits [rows][classes] (float32, bfloat16, float16), targets int32 [rows] or None ->
+    (logp (None without targets), entropy, lse float32 [rows], top_ids int32 [rows][k], top_logp float32 [rows][k])"""
+    torch = _torch()
+    ld = _matrix(logits, "logits")
+    rows, classes = logits.shape
+    _vector(targets, "targets", rows, (torch.int32,))
+    dev = logits.device
+    with _On(stream):
+        st = torch.empty((3, rows), dtype=torch.float32, device=dev)
+        ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
+        top = torch.empty((rows, k), dtype=torch.float32, device=dev)
+        p = st.data_ptr()
+        _check(_lib.ito_token_logprobs_fwd(_ptr(logits), ld, _type_id(logits, "logits"), _ptr(targets), rows, classes,
+                                           k, None if targets is None else p, p + 4 * rows, p + 8 * rows, _ptr(ids),
+                                           _ptr(top), _stream(stream)))
+    return (None if targets is None else st[0]), st[1], st[2], ids, top
+
+
+def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy=None, out=None, stream=None):
+    """-> dlogits in the logits' type (out: a tensor to write it to, which may be the logits)."""
+    torch = _torch()
+    ld = _matrix(logits, "logits")
+    rows, classes = logits.shape
+    _vector(targets, "targets", rows, (torch.int32,))
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy")):
+        _vector(t, name, rows, (torch.float32,))
+    with _On(stream):
+        d = torch.empty((rows, classes), dtype=logits.dtype, device=logits.device) if out is None else out
+        ldd = _matrix(d, "out", rows, classes, logits.dtype)
+        _check(_lib.ito_token_logprobs_bwd(_ptr(logits), ld, _type_id(logits, "logits"), _ptr(targets), _ptr(lse),
+                                           _ptr(entropy), rows, classes, _ptr(g_logp), _ptr(g_entropy), _ptr(d), ldd,
+                                           _stream(stream)))
+    return d
+
+
+class AdamW:
+    """AdamW over many weight tensors (float32, dense, updated in place), one launch a step
+    for up to a few dozen of them, with moments in 32 bits or in 8 (see include/ito.h).
+
+    copies: bfloat16 or float16 tensors that receive the updated weights (None: none).
+    weight_decay: a number, or one for each tensor. states: [m, v] lists (bits=32: float32) or
+    [m, v, m_exp, v_exp] lists (bits=8: uint8 codes and int8 exponents); None starts from zero.
+    step: steps taken so far. The object keeps the tensors and their addresses: they must not
+    be reallocated (Tensor.set_ or resize_) while it lives."""
+
+    def __init__(self, weights, bits=32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, states=None,
+                 step=0, seed=0):
+        import numpy as np
+        torch = _torch()
+        if bits not in (32, 8):
+            raise ItoError(ITO_ERR_ARG, "bits must be 32 or 8")
+        if not weights:
+            raise ItoError(ITO_ERR_SHAPE, "no weights")
+        self.bits, self.betas, self.eps, self.seed, self.steps = bits, tuple(betas), eps, seed, int(step)
+        self.weights = list(weights)
+        sizes = [w.numel() for w in self.weights]
+        blocks = [(n + 127) // 128 for n in sizes]
+        dev = self.weights[0].device
+        if states is None:
+            if bits == 32:
+                states = [[torch.zeros(n, dtype=torch.float32, device=dev) for n in sizes] for _ in range(2)]
+            else:
+                states = [[torch.zeros(n, dtype=torch.uint8, device=dev) for n in sizes] for _ in range(2)] + \
+                         [[torch.zeros(n, dtype=torch.int8, device=dev) for n in blocks] for _ in range(2)]
+        kinds = [(torch.float32, sizes)] * 2 if bits == 32 else [(torch.uint8, sizes)] * 2 + [(torch.int8, blocks)] * 2
+        if len(states) != len(kinds):
+            raise ItoError(ITO_ERR_ARG, "%d state lists, expected %d" % (len(states), len(kinds)))
+        self.states = [list(s) for s in states]
+        self.copies = None if copies is None else list(copies)
+        decays = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * len(sizes)
+        groups = [(self.weights, torch.float32, sizes, "weights")]
+        groups += [(s, d, n, "states") for s, (d, n) in zip(self.states, kinds)]
+        if self.copies is not None:
+            if not self.copies or self.copies[0].dtype not in (torch.bfloat16, torch.float16):
+                raise ItoError(ITO_ERR_ARG, "copies must be bfloat16 or float16")
+            groups.append((self.copies, self.copies[0].dtype, sizes, "copies"))
+        for ts, dtype, lengths, name in groups:
+            if len(ts) != len(sizes):
+                raise ItoError(ITO_ERR_SHAPE, "%s: %d tensors, expected %d" % (name, len(ts), len(sizes)))
+            self._dense(ts, dtype, lengths, name)
+        if len(decays) != len(sizes):
+            raise ItoError(ITO_ERR_SHAPE, "weight_decay: %d values, expected %d" % (len(decays), len(sizes)))
+        self._copy_type = ITO_BF16 if self.copies is None else _type_id(self.copies[0], "copies")
+        self._n, self._sizes, self.total = len(sizes), sizes, sum(sizes)
+        self._table = (AdamwTensor * self._n)()
+        tab = self._fields = np.frombuffer(self._table, dtype=np.dtype(
+            [(f, np.float64 if f == "weight_decay" else np.int64) for f, _ in AdamwTensor._fields_]))
+        tab["w"] = [w.data_ptr() for w in self.weights]
+        if self.copies is not None:
+            tab["copy"] = [c.data_ptr() for c in self.copies]
+        for f, s in zip(("m", "v", "m_exp", "v_exp"), self.states):
+            tab[f] = [t.data_ptr() for t in s]
+        tab["n"] = sizes
+        tab["weight_decay"] = decays
+
+    @staticmethod
+    def _dense(ts, dtype, lengths, name):
+        for i, (t, n) in enumerate(zip(ts, lengths)):
+            if t.numel() != n:
+                raise ItoError(ITO_ERR_SHAPE, "%s[%d]: %d elements, expected %d" % (name, i, t.numel(), n))
+            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+                raise ItoError(ITO_ERR_ARG, "%s[%d]: a dense %s tensor on the GPU is expected" % (name, i, dtype))
+
+    def step(self, grads, lr, grad_scale=1.0, stream=None):
+        """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16)."""
+        if len(grads) != self._n:
+            raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
+        self._dense(grads, grads[0].dtype, self._sizes, "grads")
+        self._fields["g"] = [g.data_ptr() for g in grads]
+        p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
+                        _type_id(grads[0], "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
+        _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), _stream(stream)))
+        self.steps += 1
+
+    def moments(self, dtype=None, stream=None):
+        """The moments' values (m, v), the tensors' one after another: bfloat16 (exact; default)
+        or float32 for 8-bit states, float32 for 32-bit ones."""
+        torch = _torch()
+        with _On(stream):
+            if self.bits == 32:
+                return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)
+            dtype = dtype or torch.bfloat16
+            dev = self.weights[0].device
+            m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
+            if self.total:
+                _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(m, "dtype"), _ptr(m), _ptr(v),
+                                              _stream(stream)))
+        return m, v

@@ -1,0 +1,368 @@
+// The AdamW step over many tensors in one launch, its moments held in 32 bits or in 8.
+//
+//   m = b1 m + (1 - b1) g           v = b2 v + (1 - b2) g^2
+//   w = w (1 - lr wd) - (m lr / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Every operation is one IEEE operation in 32 bits, in this order (no contraction into fused
+// multiply-adds), so a plain program that rounds after each operation gets the same bits.
+//
+// Moments in 8 bits: blocks of 128 consecutive elements of a tensor share a signed 8-bit
+// exponent E, as the Blocked-DFP tensors do, and an element is a byte under it:
+//   m: sign, 4 exponent bits, 3 mantissa bits:  +-2^(E - 15 + (c >> 3)) (1 + (c & 7) / 8)
+//   v: 5 exponent bits, 3 mantissa bits:           2^(E - 31 + (c >> 3)) (1 + (c & 7) / 8)
+// with c = 0 standing for zero, and E = -128 for a block that held an infinity or a NaN (all
+// its elements read NaN). E is the exponent of the block's largest magnitude, rounded up to
+// four significant bits, so that no element rounds past the largest code. The exponent field
+// gives v 31 binades below the block's largest value, m 15: an element whose m survives has
+// a v that survives, and a v above zero never becomes zero (its code is at least 1), so a
+// small denominator cannot appear by rounding.
+// A code's step is 1/8 to 1/16 of its value; nearest rounding would leave v where it stands,
+// because (1 - b2) g^2 moves it by about 1/1000 a step. So both moments round
+// stochastically: up with the probability of the part cut off, from a 32-bit mix of seed,
+// step, tensor and element. The weight's own step uses the moments before they are rounded.
+#include <cmath>
+#include <cstring>
+
+#include "ito_float.cuh"
+
+namespace ito {
+
+constexpr int kAdamBlock = 128;      // elements that share an exponent
+constexpr int kAdamThreads = 256;
+constexpr int kAdamChunk = 8192;     // elements a CTA takes
+
+struct AdamEntry {
+    float* w;
+    const void* g;
+    void* copy;
+    void* m;
+    void* v;
+    int8_t* m_exp;
+    int8_t* v_exp;
+    int64_t n;
+    uint32_t first_chunk;   // of this launch's chunks
+    float decay;            // 1 - lr wd
+    int32_t vec;            // the pointers allow four elements at a time
+    uint32_t salt;          // the tensor's share of the rounding's key
+};
+
+constexpr int kAdamEntries = 48;     // of 80 bytes: the table is a kernel argument (4 KB at most)
+
+struct AdamTable {
+    int32_t n;
+    AdamEntry e[kAdamEntries];
+};
+
+struct AdamConst {
+    float b1, c1, b2, c2, eps, inv_sqrt_bc2, alpha, grad_scale;
+    uint32_t key;
+};
+
+// ------------------------------------------------------------- 8-bit moments
+
+// A 32-bit mix (multiply, fold the high half down; the multipliers are the fractional parts
+// of the square roots of 2, 3 and 11): the low 20 bits round m, another 20 round v.
+__device__ __forceinline__ void round_bits(uint32_t key, int64_t i, uint32_t& um, uint32_t& uv)
+{
+    uint32_t h = (uint32_t)i * 0x6A09E667u + (uint32_t)((uint64_t)i >> 32) * 0xBB67AE85u + key;
+    h ^= h >> 16;
+    h *= 0xBB67AE85u;
+    h ^= h >> 15;
+    h *= 0x6A09E667u;
+    h ^= h >> 16;
+    um = h & 0xFFFFFu;
+    uv = (h * 0x510E527Fu) >> 12;
+}
+
+template <bool SECOND>
+__device__ __forceinline__ float moment_value(uint32_t code, int e)
+{
+    const uint32_t mag = SECOND ? code : code & 127u;
+    float r = mag ? __uint_as_float(((uint32_t)(e + (SECOND ? 96 : 112)) << 23) + (mag << 20)) : 0.0f;
+    if (!SECOND && code >= 128u) r = -r;
+    return e == -128 ? __uint_as_float(0x7FC00000u) : r;
+}
+
+// the shared exponent of a block whose largest magnitude has these bits
+template <bool SECOND>
+__device__ __forceinline__ int moment_exponent(uint32_t top)
+{
+    if (top >= 0x7F800000u) return -128;
+    const int e = (int)((min(top, 0x7F700000u) + 0xFFFFFu) >> 23) - 127;
+    return max(e, SECOND ? -95 : -111);
+}
+
+template <bool SECOND>
+__device__ __forceinline__ uint32_t moment_code(float x, int e, uint32_t u)
+{
+    if (e == -128) return 0u;
+    const uint32_t bits = __float_as_uint(x), mag = bits & 0x7FFFFFFFu;
+    const int t = (int)min(mag, 0x7F700000u) - ((e + (SECOND ? 96 : 112)) << 23);
+    uint32_t c = t >= 0 ? ((uint32_t)t + u) >> 20 : 0u;
+    if (SECOND) return mag ? max(c, 1u) : 0u;
+    return c && bits != mag ? c + 128u : c;
+}
+
+// ------------------------------------------------------------------- the step
+
+__device__ __forceinline__ void adam_element(const AdamConst& k, float decay, float g, float& w, float& m, float& v)
+{
+    g = __fmul_rn(g, k.grad_scale);
+    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
+    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
+    const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), k.inv_sqrt_bc2), k.eps);
+    w = __fsub_rn(__fmul_rn(w, decay), __fdiv_rn(__fmul_rn(m, k.alpha), den));
+}
+
+template <typename G, typename C, int BITS>
+__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamTable tab, const AdamConst k)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    int lo = 0, hi = tab.n - 1;          // the tensor whose chunks hold this CTA's
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.e[mid].first_chunk <= blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const AdamEntry& e = tab.e[lo];
+    const int64_t base = (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
+    const int64_t end = min(e.n, base + kAdamChunk);
+    const G* g = static_cast<const G*>(e.g);
+    C* copy = static_cast<C*>(e.copy);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a warp takes 128 elements, one block of an 8-bit state, four to a lane
+    for (int64_t b = base + warp * kAdamBlock; b < end; b += (kAdamThreads / 32) * kAdamBlock) {
+        float w[4], m[4], v[4], gr[4];
+        uint32_t mc[4], vc[4];
+        int64_t at[4];
+        const int64_t blk = b / kAdamBlock;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            at[j] = b + j * 32 + lane;
+            const bool in = at[j] < end;
+            gr[j] = in ? to_f32(g[at[j]]) : 0.0f;
+            w[j] = in ? e.w[at[j]] : 0.0f;
+            if (BITS == 32) {
+                m[j] = in ? static_cast<const float*>(e.m)[at[j]] : 0.0f;
+                v[j] = in ? static_cast<const float*>(e.v)[at[j]] : 0.0f;
+            } else {
+                mc[j] = in ? static_cast<const uint8_t*>(e.m)[at[j]] : 0u;
+                vc[j] = in ? static_cast<const uint8_t*>(e.v)[at[j]] : 0u;
+            }
+        }
+        if (BITS == 8) {
+            const int em = e.m_exp[blk], ev = e.v_exp[blk];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[j] = at[j] < end ? moment_value<false>(mc[j], em) : 0.0f;
+                v[j] = at[j] < end ? moment_value<true>(vc[j], ev) : 0.0f;
+            }
+        }
+        uint32_t tm = 0, tv = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            adam_element(k, e.decay, gr[j], w[j], m[j], v[j]);
+            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+        if (BITS == 8) {
+            const int em = moment_exponent<false>(__reduce_max_sync(0xffffffffu, tm));
+            const int ev = moment_exponent<true>(__reduce_max_sync(0xffffffffu, tv));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t um, uv;
+                round_bits(k.key + e.salt, at[j], um, uv);
+                mc[j] = moment_code<false>(m[j], em, um);
+                vc[j] = moment_code<true>(v[j], ev, uv);
+            }
+            if (lane == 0) {
+                e.m_exp[blk] = (int8_t)em;
+                e.v_exp[blk] = (int8_t)ev;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (at[j] >= end) continue;
+            e.w[at[j]] = w[j];
+            if (copy) copy[at[j]] = from_f32<C>(w[j]);
+            if (BITS == 32) {
+                static_cast<float*>(e.m)[at[j]] = m[j];
+                static_cast<float*>(e.v)[at[j]] = v[j];
+            } else {
+                static_cast<uint8_t*>(e.m)[at[j]] = (uint8_t)mc[j];
+                static_cast<uint8_t*>(e.v)[at[j]] = (uint8_t)vc[j];
+            }
+        }
+    }
+}
+
+// The values of 8-bit moments, the tensors one after another in m_out and v_out.
+struct MomentEntry {
+    const uint8_t* m;
+    const uint8_t* v;
+    const int8_t* m_exp;
+    const int8_t* v_exp;
+    int64_t n, out;         // first element of this tensor's values
+    uint32_t first_chunk;
+};
+constexpr int kMomentEntries = 64;
+struct MomentTable {
+    int32_t n;
+    MomentEntry e[kMomentEntries];
+};
+
+template <typename O>
+__global__ void __launch_bounds__(kAdamThreads)
+    k_moments(const __grid_constant__ MomentTable tab, O* __restrict__ m_out, O* __restrict__ v_out)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    int lo = 0, hi = tab.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.e[mid].first_chunk <= blockIdx.x) lo = mid; else hi = mid - 1;
+    }
+    const MomentEntry& e = tab.e[lo];
+    const int64_t base = (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
+    const int64_t end = min(e.n, base + kAdamChunk);
+    for (int64_t i = base + threadIdx.x; i < end; i += kAdamThreads) {
+        if (m_out) m_out[e.out + i] = from_f32<O>(moment_value<false>(e.m[i], e.m_exp[i / kAdamBlock]));
+        if (v_out) v_out[e.out + i] = from_f32<O>(moment_value<true>(e.v[i], e.v_exp[i / kAdamBlock]));
+    }
+}
+
+// ------------------------------------------------------------------- launchers
+
+template <typename G, typename C>
+static void launch_adamw(const AdamTable& t, const AdamConst& k, int bits, uint32_t chunks, cudaStream_t s)
+{
+    if (bits == 8) launch_pdl(k_adamw<G, C, 8>, chunks, kAdamThreads, 0, s, t, k);
+    else launch_pdl(k_adamw<G, C, 32>, chunks, kAdamThreads, 0, s, t, k);
+}
+
+template <typename G>
+static void launch_adamw(const AdamTable& t, const AdamConst& k, int bits, int copy_type, uint32_t chunks,
+                         cudaStream_t s)
+{
+    if (copy_type == ITO_F16) launch_adamw<G, __half>(t, k, bits, chunks, s);
+    else launch_adamw<G, __nv_bfloat16>(t, k, bits, chunks, s);
+}
+
+static int check_tensor(const ito_adamw_tensor& a, int i, int bits)
+{
+    if (a.n < 0 || a.n > (int64_t(1) << 40)) return set_error(ITO_ERR_SHAPE, "tensor %d: n outside 0 .. 2^40", i);
+    if (a.n == 0) return ITO_OK;
+    if (!a.m || !a.v) return set_error(ITO_ERR_ARG, "tensor %d: NULL state pointer", i);
+    if (bits == 8 && (!a.m_exp || !a.v_exp)) return set_error(ITO_ERR_ARG, "tensor %d: NULL exponent pointer", i);
+    if (bits == 32 && (!aligned_to(a.m, 4) || !aligned_to(a.v, 4)))
+        return set_error(ITO_ERR_ARG, "tensor %d: misaligned state pointer", i);
+    return ITO_OK;
+}
+
+}  // namespace ito
+
+using namespace ito;
+
+extern "C" {
+
+int ito_adamw_step(const ito_adamw_tensor* tensors, int n_tensors, const ito_adamw_params* p, void* stream)
+{
+    if (!tensors || !p) return set_error(ITO_ERR_ARG, "NULL argument");
+    if (n_tensors < 1) return set_error(ITO_ERR_SHAPE, "n_tensors must be >= 1");
+    if (p->state_bits != 32 && p->state_bits != 8) return set_error(ITO_ERR_ARG, "state_bits must be 32 or 8");
+    if (!type_known(p->grad_type)) return set_error(ITO_ERR_ARG, "unknown grad_type");
+    if (p->copy_type != ITO_BF16 && p->copy_type != ITO_F16)
+        return set_error(ITO_ERR_ARG, "copy_type must be ITO_BF16 or ITO_F16");
+    if (p->step < 1) return set_error(ITO_ERR_ARG, "step must be >= 1");
+    if (!(p->beta1 >= 0 && p->beta1 < 1) || !(p->beta2 >= 0 && p->beta2 < 1))
+        return set_error(ITO_ERR_ARG, "betas must be in [0, 1)");
+    if (!(p->eps >= 0)) return set_error(ITO_ERR_ARG, "eps must be >= 0");
+    for (int i = 0; i < n_tensors; ++i) {
+        const ito_adamw_tensor& a = tensors[i];
+        const int r = check_tensor(a, i, p->state_bits);
+        if (r) return r;
+        if (a.n == 0) continue;
+        if (!a.w || !a.g) return set_error(ITO_ERR_ARG, "tensor %d: NULL weight or gradient pointer", i);
+        if (!aligned_to(a.w, 4) || !aligned_to(a.g, type_bytes(p->grad_type)) || !aligned_to(a.copy, 2))
+            return set_error(ITO_ERR_ARG, "tensor %d: misaligned pointer", i);
+    }
+    AdamConst k;
+    const double t = (double)p->step;
+    k.b1 = (float)p->beta1;
+    k.c1 = (float)(1.0 - p->beta1);
+    k.b2 = (float)p->beta2;
+    k.c2 = (float)(1.0 - p->beta2);
+    k.eps = (float)p->eps;
+    k.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(p->beta2, t)));
+    k.alpha = (float)(p->lr / (1.0 - std::pow(p->beta1, t)));
+    k.grad_scale = (float)p->grad_scale;
+    k.key = p->seed + (uint32_t)(uint64_t)p->step * 0x9E3779B1u;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AdamTable tab;
+    for (int i = 0; i < n_tensors;) {
+        tab.n = 0;
+        uint64_t chunks = 0;
+        for (; i < n_tensors && tab.n < kAdamEntries; ++i) {
+            const ito_adamw_tensor& a = tensors[i];
+            const uint64_t c = ((uint64_t)a.n + kAdamChunk - 1) / kAdamChunk;
+            if (chunks + c > 0x7fffffffu) break;
+            if (!c) continue;
+            AdamEntry& e = tab.e[tab.n++];
+            e = AdamEntry{a.w, a.g, a.copy, a.m, a.v, a.m_exp, a.v_exp, a.n, (uint32_t)chunks,
+                          (float)(1.0 - p->lr * a.weight_decay), 0, (uint32_t)i * 0x510E527Fu};
+            chunks += c;
+        }
+        if (!chunks) continue;
+        if (p->grad_type == ITO_F32) launch_adamw<float>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
+        else if (p->grad_type == ITO_BF16)
+            launch_adamw<__nv_bfloat16>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
+        else launch_adamw<__half>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
+        const int r = launch_status("adamw");
+        if (r) return r;
+    }
+    return ITO_OK;
+}
+
+int ito_adamw_moments(const ito_adamw_tensor* tensors, int n_tensors, int out_type, void* m_out, void* v_out,
+                      void* stream)
+{
+    if (!tensors || (!m_out && !v_out)) return set_error(ITO_ERR_ARG, "NULL argument");
+    if (n_tensors < 1) return set_error(ITO_ERR_SHAPE, "n_tensors must be >= 1");
+    if (out_type != ITO_F32 && out_type != ITO_BF16)
+        return set_error(ITO_ERR_ARG, "out_type must be ITO_F32 or ITO_BF16");
+    if (!aligned_to(m_out, type_bytes(out_type)) || !aligned_to(v_out, type_bytes(out_type)))
+        return set_error(ITO_ERR_ARG, "misaligned output pointer");
+    for (int i = 0; i < n_tensors; ++i) {
+        const int r = check_tensor(tensors[i], i, 8);
+        if (r) return r;
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MomentTable tab;
+    int64_t out = 0;
+    for (int i = 0; i < n_tensors;) {
+        tab.n = 0;
+        uint64_t chunks = 0;
+        for (; i < n_tensors && tab.n < kMomentEntries; ++i) {
+            const ito_adamw_tensor& a = tensors[i];
+            const uint64_t c = ((uint64_t)a.n + kAdamChunk - 1) / kAdamChunk;
+            if (chunks + c > 0x7fffffffu) break;
+            if (!c) continue;
+            tab.e[tab.n++] = MomentEntry{static_cast<const uint8_t*>(a.m), static_cast<const uint8_t*>(a.v), a.m_exp,
+                                         a.v_exp, a.n, out, (uint32_t)chunks};
+            chunks += c;
+            out += a.n;
+        }
+        if (!chunks) continue;
+        if (out_type == ITO_F32)
+            launch_pdl(k_moments<float>, (uint32_t)chunks, kAdamThreads, 0, s, tab, static_cast<float*>(m_out),
+                       static_cast<float*>(v_out));
+        else
+            launch_pdl(k_moments<__nv_bfloat16>, (uint32_t)chunks, kAdamThreads, 0, s, tab,
+                       static_cast<__nv_bfloat16*>(m_out), static_cast<__nv_bfloat16*>(v_out));
+        const int r = launch_status("moments");
+        if (r) return r;
+    }
+    return ITO_OK;
+}
+
+}  // extern "C"
