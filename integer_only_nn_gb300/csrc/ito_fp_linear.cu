@@ -5,148 +5,231 @@
 //
 // x [B][IC], W [OC][IC], z, y, dy [B][OC]; products are summed in 32 bits. dz is rounded once
 // to the operands' type, because it is an operand of the two products that follow; dbias sums
-// it before that rounding.
-#include <cmath>
+// it before that rounding. Products run on the tensor cores (ito_fp_gemm.cu) except for a few
+// rows of x, which stream W (k_fp_rows below). TMA reads operands whose rows start on 16-byte
+// boundaries; others are copied into the workspace first, with rows padded to 8 elements.
+#include <algorithm>
 
-#include "ito_float.cuh"
+#include "ito_fp_epilogue.cuh"
 
 namespace ito {
 
-// ----------------------------------------------------------------- activations
+// ------------------------------------------------------------- a few rows of x
+//
+// With up to 32 rows the product reads W once and does little with it: W's bytes bound it.
+// A warp takes 16 rows of W as the 16 x 16 operand of mma.sync and eight rows of x (a token
+// each; missing ones are 0) as the 16 x 8 one. The sum over k may be taken in any order, so
+// the fragments' k are assigned such that each lane reads 16 consecutive bytes of a row of W
+// (k0 + 8 t .. + 7 for lane t of a quad) and the same k of its row of x: two products of
+// 16 k from one wide load each. A block's warps share the 16 rows and take turns along k; their
+// sums meet in shared memory, in the warps' order.
 
-__device__ __forceinline__ float act_value(int act, float z)
+constexpr int kRowsMost = 32;        // rows of x this kernel takes
+
+__device__ __forceinline__ void mma_16816(int type, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
 {
-    switch (act) {
-    case ITO_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case ITO_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case ITO_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    case ITO_ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
-    }
+    if (type == ITO_BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float act_slope(int act, float z)
+// elements k .. k + 7 of a row of n (0 beyond it)
+__device__ __forceinline__ uint4 load_eight(const uint16_t* row, int k, int n, bool vec)
 {
-    switch (act) {
-    case ITO_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-    case ITO_ACT_GELU:
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    case ITO_ACT_GELU_TANH: {
-        const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * (0.79788456080286536f * (1.0f + 0.134145f * z * z));
-    }
-    case ITO_ACT_SILU: {
-        const float q = 1.0f / (1.0f + expf(-z));
-        return q * (1.0f + z * (1.0f - q));
-    }
-    default: return 1.0f;
-    }
+    if (vec && k + 8 <= n) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < n) w[i >> 1] |= (uint32_t)__ldg(row + k + i) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// What the product's epilogue does with a sum.
-struct FpEpilogue {
-    const void* bias;
-    int bias_type, act;
-    const void* residual;
-    int64_t ldr;
-    int out_type;          // of y and residual
-    void* y;
-    int64_t ldy;
-    void* z;               // the operands' type, may be null
-    int64_t ldz;
-};
-
-template <typename T>
-__device__ __forceinline__ void fp_finish(const FpEpilogue& e, int64_t r, int64_t c, float v)
+template <int NT>
+__global__ void __launch_bounds__(512)
+    k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, int x_vec, const uint16_t* __restrict__ W, int64_t ldw,
+              int w_vec, int B, int IC, int OC, const __grid_constant__ FpEpilogue e)
 {
-    if (e.bias) v += load_typed(e.bias, e.bias_type, c);
-    if (e.z) static_cast<T*>(e.z)[r * e.ldz + c] = from_f32<T>(v);
-    v = act_value(e.act, v);
-    if (e.residual) v += load_typed(e.residual, e.out_type, r * e.ldr + c);
-    if (e.out_type == ITO_F32) static_cast<float*>(e.y)[r * e.ldy + c] = v;
-    else static_cast<T*>(e.y)[r * e.ldy + c] = from_f32<T>(v);
-}
-
-// ------------------------------------------------------------ the product, simply
-
-// C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = A[m sam + k sak], B(n, k) = B[n sbn + k sbk]:
-// 64 x 64 tiles, 16 of K at a time in shared memory, 4 x 4 sums to a thread.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_fp_product(const T* __restrict__ A, int64_t sam, int64_t sak, const T* __restrict__ B, int64_t sbn, int64_t sbk,
-                 int M, int N, int K, const FpEpilogue e)
-{
+    constexpr int U = NT == 1 ? 8 : 4;      // steps of 32 k whose loads are in flight together
+    __shared__ float part[16][16 * 8 * NT];
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ float sa[16][65], sb[16][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int tiles_n = (N + 63) / 64;
-    const int64_t tiles = (int64_t)((M + 63) / 64) * tiles_n;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int m0 = (int)(t / tiles_n) * 64, n0 = (int)(t % tiles_n) * 64;
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < K; k0 += 16) {
-            for (int i = threadIdx.x; i < 1024; i += 256) {
-                const int r = sak == 1 ? i >> 4 : i & 63, c = sak == 1 ? i & 15 : i >> 6;
-                sa[c][r] = m0 + r < M && k0 + c < K ? to_f32(A[(m0 + r) * sam + (k0 + c) * sak]) : 0.0f;
-                const int r2 = sbk == 1 ? i >> 4 : i & 63, c2 = sbk == 1 ? i & 15 : i >> 6;
-                sb[c2][r2] = n0 + r2 < N && k0 + c2 < K ? to_f32(B[(n0 + r2) * sbn + (k0 + c2) * sbk]) : 0.0f;
-            }
-            __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warps = blockDim.x >> 5;
+    const int oc0 = blockIdx.x * 16;
+    const bool in0 = oc0 + g < OC, in1 = oc0 + g + 8 < OC;
+    const uint16_t* w0 = W + (int64_t)(in0 ? oc0 + g : 0) * ldw;
+    const uint16_t* w1 = W + (int64_t)(in1 ? oc0 + g + 8 : 0) * ldw;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float c[NT][4];
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+    for (int k0 = warp * U * 32; k0 < IC; k0 += warps * U * 32) {
+        uint4 a[U], b[U];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
-            __syncthreads();
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * 32 + t * 8;
+            a[u] = in0 && k < IC ? load_eight(w0, k, IC, w_vec) : zero;
+            b[u] = in1 && k < IC ? load_eight(w1, k, IC, w_vec) : zero;
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-                if (m0 + ty + 16 * i < M && n0 + tx + 16 * j < N)
-                    fp_finish<T>(e, m0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bool in = n * 8 + g < B;
+            const uint16_t* xr = x + (int64_t)(in ? n * 8 + g : 0) * ldx;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * 32 + t * 8;
+                const uint4 v = in && k < IC ? load_eight(xr, k, IC, x_vec) : zero;
+                mma_16816(e.type, c[n], a[u].x, b[u].x, a[u].y, b[u].y, v.x, v.y);
+                mma_16816(e.type, c[n], a[u].z, b[u].z, a[u].w, b[u].w, v.z, v.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][(n * 8 + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = c[n][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * 8 * NT; i += blockDim.x) {
+        const int b = i >> 4, oc = oc0 + (i & 15);
+        if (b >= B || oc >= OC) continue;
+        float s = part[0][i];
+        for (int w = 1; w < warps; ++w) s += part[w][i];
+        fp_finish(e, b, oc, s);
     }
 }
 
-// dz = dy act'(z), rounded to T, and the columns' sums of the unrounded dz over rows
-// [blockIdx.y rows_per, ...), each share in its own row of the partials.
-template <typename T>
+// --------------------------------------------------------- element-wise passes
+
+// rows whose starts TMA cannot address, copied to rows padded to 8 elements
 __global__ void __launch_bounds__(256)
-    k_fp_dz(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ z, int64_t ldz, int act, int B, int OC,
-            int rows_per, T* __restrict__ dz, int64_t lddz, float* __restrict__ part)
+    k_fp_align(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
+               int64_t ldd)
 {
     griddep_wait();
     griddep_launch_dependents();
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int c = blockIdx.x * 1024 + threadIdx.x; c < min(cols, ((int)blockIdx.x + 1) * 1024); c += 256)
+            dst[r * ldd + c] = src[r * ld + c];
+}
+
+// dz = dy act'(z), rounded to the operands' type (dz may be null), and this block's share of
+// the columns' sums before that rounding (part may be null). A block takes 256 columns (eight
+// to a lane) of the rows blockIdx.y rows_per .. ; its eight warps take every eighth row and
+// their sums meet in shared memory in the warps' order.
+__global__ void __launch_bounds__(256)
+    k_fp_dz(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz, int type,
+            int act, int B, int OC, int rows_per, int vec, uint16_t* __restrict__ dz, int64_t lddz,
+            float* __restrict__ part)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    __shared__ float sums[8][256];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = blockIdx.x * 256 + lane * 8;
+    const int r1 = min(B, ((int)blockIdx.y + 1) * rows_per);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+    if (c0 < OC)
+        for (int r = blockIdx.y * rows_per + warp; r < r1; r += 8) {
+            const uint4 d = load_eight(dy + r * lddy, c0, OC, vec);
+            const uint4 q = act != ITO_ACT_NONE ? load_eight(z + r * ldz, c0, OC, vec) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, qw[4] = {q.x, q.y, q.z, q.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 v = unpack16(type, dw[i]);
+                if (act != ITO_ACT_NONE) {
+                    const float2 zz = unpack16(type, qw[i]);
+                    v.x *= act_slope(act, zz.x);
+                    v.y *= act_slope(act, zz.y);
+                }
+                s[2 * i] += v.x;
+                s[2 * i + 1] += v.y;
+                o[i] = pack16(type, v.x, v.y);
+            }
+            // dz's rows are padded to 8 elements: a whole vector always fits
+            if (dz) *reinterpret_cast<uint4*>(dz + r * lddz + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    if (!part) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = s[i];
+    __syncthreads();
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (c >= OC) return;
-    const int r1 = min(B, ((int)blockIdx.y + 1) * rows_per);
-    float s = 0.0f;
-    for (int r = blockIdx.y * rows_per; r < r1; ++r) {
-        float v = to_f32(dy[r * lddy + c]);
-        if (act != ITO_ACT_NONE) v *= act_slope(act, to_f32(z[r * ldz + c]));
-        s += v;
-        if (dz) dz[r * lddz + c] = from_f32<T>(v);
-    }
-    if (part) part[(int64_t)blockIdx.y * OC + c] = s;
+    float v = sums[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += sums[w][threadIdx.x];
+    part[(int64_t)blockIdx.y * OC + c] = v;
 }
 
+// out[c] = the parts' sum in a fixed order: a warp's lanes take 32 columns, eight warps every
+// eighth part
 __global__ void __launch_bounds__(256)
     k_fp_column_sums(const float* __restrict__ part, int parts, int n, float* __restrict__ out)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
+    __shared__ float sums[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int p = 0; p < parts; ++p) s += part[(int64_t)p * n + c];
-    out[c] = s;
+    if (c < n)
+        for (int p = warp; p < parts; p += 8) s += part[(int64_t)p * n + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < n) {
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s += sums[w][lane];
+        out[c] = s;
+    }
 }
 
-constexpr int kDzParts = 64;         // shares of the batch in the bias gradient's sum
+// ------------------------------------------------------------------------ host
 
-static int dz_rows_per(int B) { return (B + kDzParts - 1) / kDzParts; }
+constexpr int kDzRows = 64;          // rows of the batch to a share of the bias gradient's sum, at least
+
+static int dz_rows_per(int B) { return std::max(kDzRows, ((B + 255) / 256 + 7) / 8 * 8); }
 static int dz_parts(int B) { return (B + dz_rows_per(B) - 1) / dz_rows_per(B); }
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// A row's stride says nothing about a single row.
+static int64_t row_stride(int64_t ld, int rows, int cols) { return rows == 1 ? pad8(cols) : ld; }
+
+static bool tma_rows(const void* p, int64_t ld, int rows, int cols)
+{
+    return aligned_to(p, 16) && row_stride(ld, rows, cols) % 8 == 0;
+}
+
+static size_t copy_bytes(const void* p, int64_t ld, int rows, int cols)
+{
+    return tma_rows(p, ld, rows, cols) ? 0 : align256((size_t)rows * pad8(cols) * 2);
+}
+
+// the operand itself, or its aligned copy at *ws (which moves on)
+static const void* aligned_operand(const void* p, int64_t* ld, int rows, int cols, char** ws, cudaStream_t s)
+{
+    if (tma_rows(p, *ld, rows, cols)) {
+        *ld = row_stride(*ld, rows, cols);
+        return p;
+    }
+    uint16_t* dst = reinterpret_cast<uint16_t*>(*ws);
+    *ws += copy_bytes(p, *ld, rows, cols);
+    launch_pdl(k_fp_align, dim3((cols + 1023) / 1024, rows < 16384 ? rows : 16384), 256, 0, s,
+               static_cast<const uint16_t*>(p), *ld, (int64_t)rows, cols, dst, pad8(cols));
+    *ld = pad8(cols);
+    return dst;
+}
 
 static int check_sizes(int B, int IC, int OC)
 {
@@ -179,34 +262,17 @@ static int check_ws(const void* ws, size_t bytes, size_t need)
     return ITO_OK;
 }
 
-template <typename T>
-static int product(const void* A, int64_t sam, int64_t sak, const void* B, int64_t sbn, int64_t sbk, int M, int N,
-                   int K, const FpEpilogue& e, cudaStream_t s)
+template <int NT>
+static int run_rows(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC,
+                    const FpEpilogue& e, cudaStream_t s)
 {
-    const int64_t tiles = (int64_t)((M + 63) / 64) * ((N + 63) / 64);
-    launch_pdl(k_fp_product<T>, (unsigned)(tiles < 65535 ? tiles : 65535), 256, 0, s, static_cast<const T*>(A), sam,
-               sak, static_cast<const T*>(B), sbn, sbk, M, N, K, e);
+    // as many warps as have two steps of 128 or 256 k each, at most 16
+    const int step = 2 * 32 * (NT == 1 ? 8 : 4);
+    const int warps = std::min(16, std::max(1, IC / step));
+    launch_pdl(k_fp_rows<NT>, (OC + 15) / 16, warps * 32, 0, s, static_cast<const uint16_t*>(x), ldx,
+               (int)tma_rows(x, ldx, B, IC), static_cast<const uint16_t*>(W), ldw, (int)tma_rows(W, ldw, OC, IC), B, IC,
+               OC, e);
     return launch_status("linear");
-}
-
-template <typename T>
-static int run_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x, int64_t ldx,
-                   const void* W, int64_t ldw, int type, int out_type, int act, int B, int IC, int OC, void* ws,
-                   void* dx, int64_t lddx, void* dW, int64_t lddw, float* dbias, cudaStream_t s)
-{
-    T* dz = static_cast<T*>(ws);
-    const int64_t lddz = pad8(OC);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)B * lddz * 2));
-    launch_pdl(k_fp_dz<T>, dim3((OC + 255) / 256, dz_parts(B)), 256, 0, s, static_cast<const T*>(dy), lddy,
-               static_cast<const T*>(z), ldz, act, B, OC, dz_rows_per(B), dz, lddz, part);
-    if (dbias) launch_pdl(k_fp_column_sums, (OC + 255) / 256, 256, 0, s, part, dz_parts(B), OC, dbias);
-    int r = launch_status("linear backward");
-    if (!r && dx)
-        r = product<T>(dz, lddz, 1, W, 1, ldw, B, IC, OC,
-                       FpEpilogue{nullptr, 0, 0, nullptr, 0, type, dx, lddx, nullptr, 0}, s);
-    if (!r && dW)
-        r = product<T>(dz, 1, lddz, x, 1, ldx, OC, IC, B, FpEpilogue{nullptr, 0, 0, nullptr, 0, out_type, dW, lddw, nullptr, 0}, s);
-    return r;
 }
 
 }  // namespace ito
@@ -217,9 +283,8 @@ extern "C" {
 
 size_t ito_fp_linear_fwd_workspace_size(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC)
 {
-    (void)x; (void)ldx; (void)W; (void)ldw;
-    if (check_sizes(B, IC, OC)) return 0;
-    return 0;
+    if (check_sizes(B, IC, OC) || B <= kRowsMost) return 0;
+    return copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) + align256(fp_gemm_ws_bytes(B, OC, IC));
 }
 
 int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* bias, const void* residual,
@@ -241,18 +306,25 @@ int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, co
     if (!r) r = check_tensor(y, out_type, ldy, B, OC, "y");
     if (!r) r = check_ws(workspace, workspace_bytes, ito_fp_linear_fwd_workspace_size(x, ldx, W, ldw, B, IC, OC));
     if (r) return r;
-    const FpEpilogue e{bias, bias_type, act, residual, ldr, out_type, y, ldy, z, ldz};
+    const FpEpilogue e{bias, bias_type, act, residual, ldr, type, out_type, y, ldy, z, ldz};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (type == ITO_BF16) return product<__nv_bfloat16>(x, ldx, 1, W, ldw, 1, B, OC, IC, e, s);
-    return product<__half>(x, ldx, 1, W, ldw, 1, B, OC, IC, e, s);
+    if (B <= 8) return run_rows<1>(x, ldx, W, ldw, B, IC, OC, e, s);
+    if (B <= 16) return run_rows<2>(x, ldx, W, ldw, B, IC, OC, e, s);
+    if (B <= kRowsMost) return run_rows<4>(x, ldx, W, ldw, B, IC, OC, e, s);
+    char* ws = static_cast<char*>(workspace);
+    const void* xa = aligned_operand(x, &ldx, B, IC, &ws, s);
+    const void* wa = aligned_operand(W, &ldw, OC, IC, &ws, s);
+    return fp_gemm(FpOperand{xa, ldx, false}, FpOperand{wa, ldw, false}, B, OC, IC, e, ws, s);
 }
 
 size_t ito_fp_linear_bwd_workspace_size(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* W,
                                         int64_t ldw, int act, int B, int IC, int OC)
 {
-    (void)dy; (void)lddy; (void)x; (void)ldx; (void)W; (void)ldw; (void)act;
     if (check_sizes(B, IC, OC)) return 0;
-    return align256((size_t)B * pad8(OC) * 2) + align256((size_t)dz_parts(B) * OC * 4);
+    const bool dz = act != ITO_ACT_NONE || !tma_rows(dy, lddy, B, OC);
+    return (dz ? align256((size_t)B * pad8(OC) * 2) : 0) + align256((size_t)dz_parts(B) * OC * 4) +
+           copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) +
+           align256(std::max(fp_gemm_ws_bytes(B, IC, OC), fp_gemm_ws_bytes(OC, IC, B)));
 }
 
 int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x, int64_t ldx,
@@ -278,11 +350,47 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
                      ito_fp_linear_bwd_workspace_size(dy, lddy, x, ldx, W, ldw, act, B, IC, OC));
     if (r) return r;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (type == ITO_BF16)
-        return run_bwd<__nv_bfloat16>(dy, lddy, z, ldz, x, ldx, W, ldw, type, out_type, act, B, IC, OC, workspace, dx,
-                                      lddx, dW, lddw, dbias, s);
-    return run_bwd<__half>(dy, lddy, z, ldz, x, ldx, W, ldw, type, out_type, act, B, IC, OC, workspace, dx, lddx, dW,
-                           lddw, dbias, s);
+    char* ws = static_cast<char*>(workspace);
+    // dz is dy itself where nothing changes it and TMA can read it
+    const bool own_dz = act != ITO_ACT_NONE || !tma_rows(dy, lddy, B, OC);
+    uint16_t* dz = nullptr;
+    if (own_dz) {
+        dz = reinterpret_cast<uint16_t*>(ws);
+        ws += align256((size_t)B * pad8(OC) * 2);
+    }
+    float* part = reinterpret_cast<float*>(ws);
+    ws += align256((size_t)dz_parts(B) * OC * 4);
+    if (dbias || (own_dz && (dx || dW))) {
+        const int vec = tma_rows(dy, lddy, B, OC) && (act == ITO_ACT_NONE || tma_rows(z, ldz, B, OC));
+        launch_pdl(k_fp_dz, dim3((OC + 255) / 256, dz_parts(B)), 256, 0, s, static_cast<const uint16_t*>(dy), lddy,
+                   static_cast<const uint16_t*>(z), ldz, type, act, B, OC, dz_rows_per(B), vec,
+                   dx || dW ? dz : static_cast<uint16_t*>(nullptr), pad8(OC), dbias ? part : static_cast<float*>(nullptr));
+        if (dbias) launch_pdl(k_fp_column_sums, (OC + 31) / 32, 256, 0, s, part, dz_parts(B), OC, dbias);
+    }
+    const void* d = own_dz ? dz : dy;
+    const int64_t ldd = own_dz ? pad8(OC) : row_stride(lddy, B, OC);
+    // copies of x and W keep their places in the workspace whether or not both are made
+    char* wx = ws;
+    char* ww = wx + copy_bytes(x, ldx, B, IC);
+    char* wp = ww + copy_bytes(W, ldw, OC, IC);
+    if (dx) {
+        const void* wa = aligned_operand(W, &ldw, OC, IC, &ww, s);
+        FpEpilogue e{};
+        e.type = e.out_type = type;
+        e.y = dx;
+        e.ldy = lddx;
+        r = fp_gemm(FpOperand{d, ldd, false}, FpOperand{wa, ldw, true}, B, IC, OC, e, wp, s);
+    }
+    if (!r && dW) {
+        const void* xa = aligned_operand(x, &ldx, B, IC, &wx, s);
+        FpEpilogue e{};
+        e.type = type;
+        e.out_type = out_type;
+        e.y = dW;
+        e.ldy = lddw;
+        r = fp_gemm(FpOperand{d, ldd, true}, FpOperand{xa, ldx, true}, OC, IC, B, e, wp, s);
+    }
+    return r ? r : launch_status("linear backward");
 }
 
 }  // extern "C"
