@@ -852,8 +852,11 @@ int ito_token_logprobs_fwd(const void *logits, int64_t ld, int type, const int32
  * lse, entropy: as the forward pass wrote them; g_logp, g_entropy: float [rows],
  * either may be NULL (no such term; entropy is read for g_entropy only, targets
  * for g_logp only). Targets outside [0, classes) as in the forward pass: no term
- * from g_logp. A row whose lse is -inf has a gradient of 0. dlogits: `type`, may
- * be the logits themselves with the same stride. Errors as ito_token_logprobs_fwd. */
+ * from g_logp. A row whose lse is -inf has a gradient of 0. log p_j carries lse's
+ * own rounding, |lse| * 2^-24; from |lse| = 2^16 on (rows masked with the type's
+ * lowest value) the row's sums are taken again from the logits instead, except
+ * where dlogits are the logits of rows above 8192 classes. dlogits: `type`, may be
+ * the logits themselves with the same stride. Errors as ito_token_logprobs_fwd. */
 int ito_token_logprobs_bwd(const void *logits, int64_t ld, int type, const int32_t *targets, const float *lse,
                            const float *entropy, int64_t rows, int classes, const float *g_logp,
                            const float *g_entropy, void *dlogits, int64_t ldd, void *stream);

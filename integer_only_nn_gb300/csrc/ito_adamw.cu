@@ -114,12 +114,162 @@ __device__ __forceinline__ void adam_element(const AdamConst& k, float decay, fl
     w = __fsub_rn(__fmul_rn(w, decay), __fdiv_rn(__fmul_rn(m, k.alpha), den));
 }
 
+// Four consecutive elements (VEC: the pointers allow wide accesses) or four a warp apart of one
+// block of 128 elements for each lane of a warp.
+template <typename G, typename C, int BITS, bool VEC>
+struct AdamPiece {
+    float4 w, m32, v32;
+    float g[4];
+    uint32_t m8, v8;
+    int em, ev;
+
+    static __device__ __forceinline__ int64_t at(int64_t b, int lane, int j)
+    {
+        return VEC ? b + lane * 4 + j : b + j * 32 + lane;
+    }
+    __device__ __forceinline__ void load(const AdamEntry& e, int64_t b, int64_t end, int lane)
+    {
+        const G* gp = static_cast<const G*>(e.g);
+        if (BITS == 8) {
+            em = e.m_exp[b / kAdamBlock];
+            ev = e.v_exp[b / kAdamBlock];
+        }
+        if (VEC && b + kAdamBlock <= end) {
+            const int64_t i = b + lane * 4;
+            w = *reinterpret_cast<const float4*>(e.w + i);
+            if constexpr (sizeof(G) == 4) {
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(gp + i));
+                g[0] = q.x; g[1] = q.y; g[2] = q.z; g[3] = q.w;
+            } else {
+                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(gp + i));
+                g[0] = to_f32(Vec<G>::lane16(q.x, 0));
+                g[1] = to_f32(Vec<G>::lane16(q.x, 1));
+                g[2] = to_f32(Vec<G>::lane16(q.y, 0));
+                g[3] = to_f32(Vec<G>::lane16(q.y, 1));
+            }
+            if (BITS == 32) {
+                m32 = *reinterpret_cast<const float4*>(static_cast<const float*>(e.m) + i);
+                v32 = *reinterpret_cast<const float4*>(static_cast<const float*>(e.v) + i);
+            } else {
+                m8 = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + i);
+                v8 = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + i);
+            }
+            return;
+        }
+        float wf[4], mf[4], vf[4];
+        m8 = v8 = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = at(b, lane, j);
+            const bool in = i < end;
+            wf[j] = in ? e.w[i] : 0.0f;
+            g[j] = in ? to_f32(gp[i]) : 0.0f;
+            if (BITS == 32) {
+                mf[j] = in ? static_cast<const float*>(e.m)[i] : 0.0f;
+                vf[j] = in ? static_cast<const float*>(e.v)[i] : 0.0f;
+            } else if (in) {
+                m8 |= (uint32_t)static_cast<const uint8_t*>(e.m)[i] << (8 * j);
+                v8 |= (uint32_t)static_cast<const uint8_t*>(e.v)[i] << (8 * j);
+            }
+        }
+        w = make_float4(wf[0], wf[1], wf[2], wf[3]);
+        if (BITS == 32) {
+            m32 = make_float4(mf[0], mf[1], mf[2], mf[3]);
+            v32 = make_float4(vf[0], vf[1], vf[2], vf[3]);
+        }
+    }
+    __device__ __forceinline__ void step(const AdamEntry& e, const AdamConst& k, int64_t b, int64_t end, int lane)
+    {
+        float wf[4] = {w.x, w.y, w.z, w.w}, m[4], v[4];
+        if (BITS == 32) {
+            m[0] = m32.x; m[1] = m32.y; m[2] = m32.z; m[3] = m32.w;
+            v[0] = v32.x; v[1] = v32.y; v[2] = v32.z; v[3] = v32.w;
+        }
+        uint32_t tm = 0, tv = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (BITS == 8) {
+                // beyond the tensor's end the codes are 0; a NaN block's are not to reach the maxima
+                const bool in = at(b, lane, j) < end;
+                m[j] = in ? moment_value<false>((m8 >> (8 * j)) & 255u, em) : 0.0f;
+                v[j] = in ? moment_value<true>((v8 >> (8 * j)) & 255u, ev) : 0.0f;
+            }
+            adam_element(k, e.decay, g[j], wf[j], m[j], v[j]);
+            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+        if (BITS == 8) {
+            em = moment_exponent<false>(__reduce_max_sync(0xffffffffu, tm));
+            ev = moment_exponent<true>(__reduce_max_sync(0xffffffffu, tv));
+            m8 = v8 = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t um, uv;
+                round_bits(k.key + e.salt, at(b, lane, j), um, uv);
+                m8 |= moment_code<false>(m[j], em, um) << (8 * j);
+                v8 |= moment_code<true>(v[j], ev, uv) << (8 * j);
+            }
+            if (lane == 0) {
+                e.m_exp[b / kAdamBlock] = (int8_t)em;
+                e.v_exp[b / kAdamBlock] = (int8_t)ev;
+            }
+        }
+        C* copy = static_cast<C*>(e.copy);
+        if (VEC && b + kAdamBlock <= end) {
+            const int64_t i = b + lane * 4;
+            *reinterpret_cast<float4*>(e.w + i) = make_float4(wf[0], wf[1], wf[2], wf[3]);
+            if (copy)
+                *reinterpret_cast<uint2*>(copy + i) =
+                    make_uint2(Vec<C>::pair16(wf[0], wf[1]), Vec<C>::pair16(wf[2], wf[3]));
+            if (BITS == 32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(e.m) + i) = make_float4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<float4*>(static_cast<float*>(e.v) + i) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + i) = m8;
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + i) = v8;
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t i = at(b, lane, j);
+            if (i >= end) continue;
+            e.w[i] = wf[j];
+            if (copy) copy[i] = from_f32<C>(wf[j]);
+            if (BITS == 32) {
+                static_cast<float*>(e.m)[i] = m[j];
+                static_cast<float*>(e.v)[i] = v[j];
+            } else {
+                static_cast<uint8_t*>(e.m)[i] = (uint8_t)(m8 >> (8 * j));
+                static_cast<uint8_t*>(e.v)[i] = (uint8_t)(v8 >> (8 * j));
+            }
+        }
+    }
+};
+
+// A warp takes UNROLL blocks of 128 elements at a time, all their loads before the first step.
+template <typename G, typename C, int BITS, bool VEC, int UNROLL>
+__device__ __forceinline__ void adam_chunk(const AdamEntry& e, const AdamConst& k, int64_t base, int64_t end)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int64_t kStep = (kAdamThreads / 32) * kAdamBlock;
+    for (int64_t b = base + warp * kAdamBlock; b < end; b += UNROLL * kStep) {
+        AdamPiece<G, C, BITS, VEC> p[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (b + u * kStep < end) p[u].load(e, b + u * kStep, end, lane);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (b + u * kStep < end) p[u].step(e, k, b + u * kStep, end, lane);
+    }
+}
+
 template <typename G, typename C, int BITS>
 __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamTable tab, const AdamConst k)
 {
     griddep_wait();
     griddep_launch_dependents();
-    int lo = 0, hi = tab.n - 1;          // the tensor whose chunks hold this CTA's
+    int lo = 0, hi = tab.n - 1;          // the tensor whose chunks hold this block's
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tab.e[mid].first_chunk <= blockIdx.x) lo = mid; else hi = mid - 1;
@@ -127,73 +277,8 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
     const AdamEntry& e = tab.e[lo];
     const int64_t base = (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
     const int64_t end = min(e.n, base + kAdamChunk);
-    const G* g = static_cast<const G*>(e.g);
-    C* copy = static_cast<C*>(e.copy);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a warp takes 128 elements, one block of an 8-bit state, four to a lane
-    for (int64_t b = base + warp * kAdamBlock; b < end; b += (kAdamThreads / 32) * kAdamBlock) {
-        float w[4], m[4], v[4], gr[4];
-        uint32_t mc[4], vc[4];
-        int64_t at[4];
-        const int64_t blk = b / kAdamBlock;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            at[j] = b + j * 32 + lane;
-            const bool in = at[j] < end;
-            gr[j] = in ? to_f32(g[at[j]]) : 0.0f;
-            w[j] = in ? e.w[at[j]] : 0.0f;
-            if (BITS == 32) {
-                m[j] = in ? static_cast<const float*>(e.m)[at[j]] : 0.0f;
-                v[j] = in ? static_cast<const float*>(e.v)[at[j]] : 0.0f;
-            } else {
-                mc[j] = in ? static_cast<const uint8_t*>(e.m)[at[j]] : 0u;
-                vc[j] = in ? static_cast<const uint8_t*>(e.v)[at[j]] : 0u;
-            }
-        }
-        if (BITS == 8) {
-            const int em = e.m_exp[blk], ev = e.v_exp[blk];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[j] = at[j] < end ? moment_value<false>(mc[j], em) : 0.0f;
-                v[j] = at[j] < end ? moment_value<true>(vc[j], ev) : 0.0f;
-            }
-        }
-        uint32_t tm = 0, tv = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            adam_element(k, e.decay, gr[j], w[j], m[j], v[j]);
-            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        }
-        if (BITS == 8) {
-            const int em = moment_exponent<false>(__reduce_max_sync(0xffffffffu, tm));
-            const int ev = moment_exponent<true>(__reduce_max_sync(0xffffffffu, tv));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t um, uv;
-                round_bits(k.key + e.salt, at[j], um, uv);
-                mc[j] = moment_code<false>(m[j], em, um);
-                vc[j] = moment_code<true>(v[j], ev, uv);
-            }
-            if (lane == 0) {
-                e.m_exp[blk] = (int8_t)em;
-                e.v_exp[blk] = (int8_t)ev;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (at[j] >= end) continue;
-            e.w[at[j]] = w[j];
-            if (copy) copy[at[j]] = from_f32<C>(w[j]);
-            if (BITS == 32) {
-                static_cast<float*>(e.m)[at[j]] = m[j];
-                static_cast<float*>(e.v)[at[j]] = v[j];
-            } else {
-                static_cast<uint8_t*>(e.m)[at[j]] = (uint8_t)mc[j];
-                static_cast<uint8_t*>(e.v)[at[j]] = (uint8_t)vc[j];
-            }
-        }
-    }
+    if (e.vec) adam_chunk<G, C, BITS, true, 2>(e, k, base, end);
+    else adam_chunk<G, C, BITS, false, 1>(e, k, base, end);
 }
 
 // The values of 8-bit moments, the tensors one after another in m_out and v_out.
@@ -204,12 +289,23 @@ struct MomentEntry {
     const int8_t* v_exp;
     int64_t n, out;         // first element of this tensor's values
     uint32_t first_chunk;
+    int32_t vec;            // four elements at a time
 };
 constexpr int kMomentEntries = 64;
 struct MomentTable {
     int32_t n;
     MomentEntry e[kMomentEntries];
 };
+
+__device__ __forceinline__ void store_four(float* p, const float (&v)[4])
+{
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_four(__nv_bfloat16* p, const float (&v)[4])
+{
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(Vec<__nv_bfloat16>::pair16(v[0], v[1]), Vec<__nv_bfloat16>::pair16(v[2], v[3]));
+}
 
 template <typename O>
 __global__ void __launch_bounds__(kAdamThreads)
@@ -225,6 +321,21 @@ __global__ void __launch_bounds__(kAdamThreads)
     const MomentEntry& e = tab.e[lo];
     const int64_t base = (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
     const int64_t end = min(e.n, base + kAdamChunk);
+    if (e.vec) {
+        for (int64_t i = base + threadIdx.x * 4; i < end; i += kAdamThreads * 4) {
+            const uint32_t m = *reinterpret_cast<const uint32_t*>(e.m + i), v = *reinterpret_cast<const uint32_t*>(e.v + i);
+            const int em = e.m_exp[i / kAdamBlock], ev = e.v_exp[i / kAdamBlock];
+            float mf[4], vf[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mf[j] = moment_value<false>((m >> (8 * j)) & 255u, em);
+                vf[j] = moment_value<true>((v >> (8 * j)) & 255u, ev);
+            }
+            if (m_out) store_four(m_out + e.out + i, mf);
+            if (v_out) store_four(v_out + e.out + i, vf);
+        }
+        return;
+    }
     for (int64_t i = base + threadIdx.x; i < end; i += kAdamThreads) {
         if (m_out) m_out[e.out + i] = from_f32<O>(moment_value<false>(e.m[i], e.m_exp[i / kAdamBlock]));
         if (v_out) v_out[e.out + i] = from_f32<O>(moment_value<true>(e.v[i], e.v_exp[i / kAdamBlock]));
@@ -307,9 +418,12 @@ int ito_adamw_step(const ito_adamw_tensor* tensors, int n_tensors, const ito_ada
             const uint64_t c = ((uint64_t)a.n + kAdamChunk - 1) / kAdamChunk;
             if (chunks + c > 0x7fffffffu) break;
             if (!c) continue;
+            const size_t state = p->state_bits == 32 ? 16 : 4;
+            const int vec = aligned_to(a.w, 16) && aligned_to(a.g, 4 * type_bytes(p->grad_type)) && aligned_to(a.copy, 8) &&
+                            aligned_to(a.m, state) && aligned_to(a.v, state);
             AdamEntry& e = tab.e[tab.n++];
             e = AdamEntry{a.w, a.g, a.copy, a.m, a.v, a.m_exp, a.v_exp, a.n, (uint32_t)chunks,
-                          (float)(1.0 - p->lr * a.weight_decay), 0, (uint32_t)i * 0x510E527Fu};
+                          (float)(1.0 - p->lr * a.weight_decay), vec, (uint32_t)i * 0x510E527Fu};
             chunks += c;
         }
         if (!chunks) continue;
@@ -347,8 +461,11 @@ int ito_adamw_moments(const ito_adamw_tensor* tensors, int n_tensors, int out_ty
             const uint64_t c = ((uint64_t)a.n + kAdamChunk - 1) / kAdamChunk;
             if (chunks + c > 0x7fffffffu) break;
             if (!c) continue;
+            const int64_t at = out * (int64_t)type_bytes(out_type);
+            const int vec = a.n % 4 == 0 && aligned_to(a.m, 4) && aligned_to(a.v, 4) && at % 16 == 0 &&
+                            aligned_to(m_out, 16) && aligned_to(v_out, 16);
             tab.e[tab.n++] = MomentEntry{static_cast<const uint8_t*>(a.m), static_cast<const uint8_t*>(a.v), a.m_exp,
-                                         a.v_exp, a.n, out, (uint32_t)chunks};
+                                         a.v_exp, a.n, out, (uint32_t)chunks, vec};
             chunks += c;
             out += a.n;
         }

@@ -33,6 +33,100 @@ __device__ __forceinline__ float load_typed(const void* p, int type, int64_t i)
     return __half2float(static_cast<const __half*>(p)[i]);
 }
 
+// 16 bytes of a tensor: kPer elements
+template <typename T>
+struct Vec {
+    static constexpr int kPer = 16 / sizeof(T);
+    uint4 raw;
+
+    __device__ __forceinline__ void get(float (&v)[kPer]) const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = to_f32(lane16(w[i], 0));
+                v[2 * i + 1] = to_f32(lane16(w[i], 1));
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[kPer])
+    {
+        uint32_t w[4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pair16(v[2 * i], v[2 * i + 1]);
+        }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ T lane16(uint32_t w, int hi)
+    {
+        const uint16_t h = hi ? (uint16_t)(w >> 16) : (uint16_t)w;
+        return *reinterpret_cast<const T*>(&h);
+    }
+    static __device__ __forceinline__ uint32_t pair16(float lo, float hi)
+    {
+        const T a = from_f32<T>(lo), b = from_f32<T>(hi);
+        return (uint32_t)*reinterpret_cast<const uint16_t*>(&a) |
+               (uint32_t)*reinterpret_cast<const uint16_t*>(&b) << 16;
+    }
+    // elements c .. c + kPer - 1 of a row of n, 0 beyond it; vec: the row starts on 16 bytes
+    // (c is a multiple of kPer)
+    __device__ __forceinline__ void load(const T* row, int c, int n, bool vec)
+    {
+        if (vec && c + kPer <= n) {
+            raw = *reinterpret_cast<const uint4*>(row + c);
+            return;
+        }
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (c + i < n) {
+                if constexpr (sizeof(T) == 4) w[i] = *reinterpret_cast<const uint32_t*>(row + c + i);
+                else w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + c + i) << (16 * (i & 1));
+            }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void load_row(const T* row, int c, int n, bool vec)
+    {
+        if (FULL) raw = *reinterpret_cast<const uint4*>(row + c);
+        else load(row, c, n, vec);
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void store_row(T* row, int c, int n, bool vec) const
+    {
+        if (FULL) *reinterpret_cast<uint4*>(row + c) = raw;
+        else store(row, c, n, vec);
+    }
+    __device__ __forceinline__ void store(T* row, int c, int n, bool vec) const
+    {
+        if (vec && c + kPer <= n) {
+            *reinterpret_cast<uint4*>(row + c) = raw;
+            return;
+        }
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (c + i < n) {
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(row + c + i) = w[i];
+                else *reinterpret_cast<uint16_t*>(row + c + i) = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
+    }
+};
+
+// rows that 16-byte accesses can take: every row starts on a 16-byte boundary
+inline bool rows_vec(const void* p, int64_t ld, size_t size, int64_t rows)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows == 1 || ld * (int64_t)size % 16 == 0);
+}
+
 inline size_t type_bytes(int type) { return type == ITO_F32 ? 4 : 2; }
 inline bool type_known(int type) { return type == ITO_F32 || type == ITO_BF16 || type == ITO_F16; }
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

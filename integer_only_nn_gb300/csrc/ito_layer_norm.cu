@@ -7,102 +7,454 @@
 //
 // The variance is taken from the centred values (a second pass over the row), not as the
 // difference of two large sums. Sums are held in 32 bits.
+#include <algorithm>
+
 #include "ito_float.cuh"
 
 namespace ito {
 
-constexpr int kLnThreads = 256;
+// A row's elements stay in registers between the passes over them: each of the row's threads
+// holds VPT vectors of 16 bytes, vector i * tpr + its place. Rows of up to 32 threads' vectors
+// belong to parts of a warp (tpr 1, 2, .. 32 lanes, several rows to a block, sums by shuffles);
+// longer ones to a whole block, whose R rows at a time share each exchange of sums through
+// shared memory and keep R * VPT loads a thread in flight. A thread's columns are the same in
+// every row, so gamma, beta and the sums of dgamma and dbeta are registers too.
+constexpr int kLnBlock = 256;        // threads of a block of short rows
+constexpr int kLnMostThreads = 1024;
 
-template <typename T>
-__global__ void __launch_bounds__(kLnThreads)
-    k_layer_norm_fwd(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
-                     const void* __restrict__ beta, int w_type, int64_t rows, int cols, float eps, T* __restrict__ y,
-                     int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd)
+// threads of a block whose threads hold VPT vectors (ln_shape), which bounds their registers
+constexpr int ln_threads(int vpt) { return vpt == 1 ? 256 : vpt == 2 ? 512 : kLnMostThreads; }
+constexpr int ln_bwd_threads(int vpt) { return vpt == 1 ? 256 : 512; }
+
+// Sums R values over the threads of a row: lanes of a warp (tpr <= 32) or the block. `red` holds
+// two banks of R * 32 floats; the caller alternates them, so that one barrier is enough.
+template <int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], int tpr, float* red)
 {
-    griddep_wait();
-    griddep_launch_dependents();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* xr = x + r * ldx;
-        float s = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kLnThreads) s += to_f32(xr[c]);
-        const float mu = block_reduce(s, AddOp()) / (float)cols;
-        float q = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kLnThreads) {
-            const float d = to_f32(xr[c]) - mu;
-            q += d * d;
-        }
-        const float rs = 1.0f / sqrtf(block_reduce(q, AddOp()) / (float)cols + eps);
-        for (int c = threadIdx.x; c < cols; c += kLnThreads) {
-            const float h = (to_f32(xr[c]) - mu) * rs;
-            const float g = gamma ? load_typed(gamma, w_type, c) : 1.0f;
-            const float b = beta ? load_typed(beta, w_type, c) : 0.0f;
-            y[r * ldy + c] = from_f32<T>(h * g + b);
-        }
-        if (threadIdx.x == 0) {
-            if (mean) mean[r] = mu;
-            if (rstd) rstd[r] = rs;
-        }
-    }
+    const int top = tpr < 32 ? tpr : 32;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        for (int o = top >> 1; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+    if (tpr <= 32) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[r * 32 + warp] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = warp_sum(lane < warps ? red[r * 32 + lane] : 0.0f);
 }
 
-// dx, and this CTA's share of dgamma and dbeta: rows blockIdx.x, + gridDim.x, ... summed
-// into its own row of the partials, which k_layer_norm_wgrad adds in a fixed order.
-template <typename T>
-__global__ void __launch_bounds__(kLnThreads)
-    k_layer_norm_bwd(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
-                     const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
-                     const float* __restrict__ rstd, int64_t rows, int cols, T* __restrict__ dx, int64_t lddx,
-                     float* __restrict__ part)
+// N weights from column c, a multiple of N (`fill` where there are none)
+template <bool FULL, int N>
+__device__ __forceinline__ void load_weights(const void* p, int type, int c, int n, float fill, float (&v)[N])
+{
+    if (FULL && p && c < n) {
+        if (type == ITO_F32) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + i);
+                v[4 * i] = f.x;
+                v[4 * i + 1] = f.y;
+                v[4 * i + 2] = f.z;
+                v[4 * i + 3] = f.w;
+            }
+        } else if constexpr (N == 8) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + c));
+            if (type == ITO_BF16) Vec<__nv_bfloat16>{w}.get(v);
+            else Vec<__half>{w}.get(v);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = !FULL && p && c + i < n ? load_typed(p, type, c + i) : fill;
+}
+
+// FULL: rows are whole vectors on 16-byte boundaries, gamma and beta too (no element is looked at alone).
+template <typename T, int VPT, int R, bool FULL>
+__global__ void __launch_bounds__(ln_threads(VPT))
+    k_layer_norm_fwd(const T* __restrict__ x, int64_t ldx, int x_vec, const void* __restrict__ gamma,
+                     const void* __restrict__ beta, int w_type, int64_t rows, int cols, int tpr, float eps,
+                     T* __restrict__ y, int64_t ldy, int y_vec, float* __restrict__ mean, float* __restrict__ rstd)
 {
     griddep_wait();
     griddep_launch_dependents();
-    float* pg = part ? part + (int64_t)blockIdx.x * 2 * cols : nullptr;
-    float* pb = part ? pg + cols : nullptr;
-    bool first = true;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const float mu = mean[r], rs = rstd[r];
-        float sa = 0.0f, sh = 0.0f;
-        for (int c = threadIdx.x; c < cols; c += kLnThreads) {
-            const float d = to_f32(dy[r * lddy + c]);
-            const float h = (to_f32(x[r * ldx + c]) - mu) * rs;
-            const float a = d * (gamma ? load_typed(gamma, w_type, c) : 1.0f);
-            sa += a;
-            sh += a * h;
-            if (part) {
-                pg[c] = (first ? 0.0f : pg[c]) + d * h;
-                pb[c] = (first ? 0.0f : pb[c]) + d;
+    constexpr int PER = Vec<T>::kPer;
+    __shared__ float red[2][R * 32];
+    const int at = threadIdx.x % tpr, groups = blockDim.x / tpr;
+    const float inv = 1.0f / (float)cols;
+    const int64_t step = (int64_t)gridDim.x * groups * R;
+    // every thread of the block passes the barriers of every round
+    for (int64_t r0 = (int64_t)blockIdx.x * groups * R; r0 < rows; r0 += step) {
+        const int64_t first = r0 + (int64_t)(threadIdx.x / tpr) * R;
+        Vec<T> v[R][VPT];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                if (first + r < rows && c < cols) v[r][i].template load_row<FULL>(x + (first + r) * ldx, c, cols, x_vec);
+                else v[r][i].raw = make_uint4(0u, 0u, 0u, 0u);
+            }
+        float mu[R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mu[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float f[PER];
+                v[r][i].get(f);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) mu[r] += f[j];
             }
         }
-        first = false;
-        if (!dx) continue;
-        sa = block_reduce(sa, AddOp()) / (float)cols;
-        sh = block_reduce(sh, AddOp()) / (float)cols;
-        for (int c = threadIdx.x; c < cols; c += kLnThreads) {
-            const float h = (to_f32(x[r * ldx + c]) - mu) * rs;
-            const float a = to_f32(dy[r * lddy + c]) * (gamma ? load_typed(gamma, w_type, c) : 1.0f);
-            dx[r * lddx + c] = from_f32<T>(rs * (a - sa - h * sh));
+        row_sums<R>(mu, tpr, red[0]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mu[r] *= inv;
+            rs[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float f[PER];
+                v[r][i].get(f);
+                const int c = (i * tpr + at) * PER;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const float d = (FULL ? c : c + j) < cols ? f[j] - mu[r] : 0.0f;
+                    rs[r] += d * d;
+                }
+            }
+        }
+        row_sums<R>(rs, tpr, red[1]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            rs[r] = 1.0f / sqrtf(rs[r] * inv + eps);
+            if (at == 0 && first + r < rows) {
+                if (mean) mean[first + r] = mu[r];
+                if (rstd) rstd[first + r] = rs[r];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = (i * tpr + at) * PER;
+            if (c >= cols) continue;
+            float g[PER], b[PER];
+            load_weights<FULL>(gamma, w_type, c, cols, 1.0f, g);
+            load_weights<FULL>(beta, w_type, c, cols, 0.0f, b);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (first + r >= rows) continue;
+                float f[PER];
+                v[r][i].get(f);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) f[j] = (f[j] - mu[r]) * rs[r] * g[j] + b[j];
+                v[r][i].set(f);
+                v[r][i].template store_row<FULL>(y + (first + r) * ldy, c, cols, y_vec);
+            }
         }
     }
 }
 
-__global__ void __launch_bounds__(kLnThreads)
+// Rows beyond a block's registers: the row is read in each pass (from L2 after the first).
+template <typename T>
+__global__ void __launch_bounds__(kLnMostThreads)
+    k_layer_norm_fwd_long(const T* __restrict__ x, int64_t ldx, int x_vec, const void* __restrict__ gamma,
+                          const void* __restrict__ beta, int w_type, int64_t rows, int cols, float eps,
+                          T* __restrict__ y, int64_t ldy, int y_vec, float* __restrict__ mean,
+                          float* __restrict__ rstd)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int PER = Vec<T>::kPer;
+    __shared__ float red[2][32];
+    const float inv = 1.0f / (float)cols;
+    const int stride = blockDim.x * PER;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T* xr = x + r * ldx;
+        Vec<T> v;
+        float f[PER], mu[1] = {0.0f}, rs[1] = {0.0f};
+        for (int c = threadIdx.x * PER; c < cols; c += stride) {
+            v.load(xr, c, cols, x_vec);
+            v.get(f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) mu[0] += f[j];
+        }
+        row_sums<1>(mu, blockDim.x, red[0]);
+        mu[0] *= inv;
+        for (int c = threadIdx.x * PER; c < cols; c += stride) {
+            v.load(xr, c, cols, x_vec);
+            v.get(f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const float d = c + j < cols ? f[j] - mu[0] : 0.0f;
+                rs[0] += d * d;
+            }
+        }
+        row_sums<1>(rs, blockDim.x, red[1]);
+        rs[0] = 1.0f / sqrtf(rs[0] * inv + eps);
+        if (threadIdx.x == 0) {
+            if (mean) mean[r] = mu[0];
+            if (rstd) rstd[r] = rs[0];
+        }
+        for (int c = threadIdx.x * PER; c < cols; c += stride) {
+            float g[PER], b[PER];
+            load_weights<false>(gamma, w_type, c, cols, 1.0f, g);
+            load_weights<false>(beta, w_type, c, cols, 0.0f, b);
+            v.load(xr, c, cols, x_vec);
+            v.get(f);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) f[j] = (f[j] - mu[0]) * rs[0] * g[j] + b[j];
+            v.set(f);
+            v.store(y + r * ldy, c, cols, y_vec);
+        }
+    }
+}
+
+// dx, and each row group's share of dgamma and dbeta (part: [shares][2][cols], may be null),
+// which k_layer_norm_wgrad adds in a fixed order.
+template <typename T, int VPT, int R, bool FULL>
+__global__ void __launch_bounds__(ln_bwd_threads(VPT))
+    k_layer_norm_bwd(const T* __restrict__ dy, int64_t lddy, int dy_vec, const T* __restrict__ x, int64_t ldx,
+                     int x_vec, const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
+                     const float* __restrict__ rstd, int64_t rows, int cols, int tpr, T* __restrict__ dx,
+                     int64_t lddx, int dx_vec, float* __restrict__ part)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int PER = Vec<T>::kPer;
+    __shared__ float red[2][2 * R * 32];
+    const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+    const float inv = 1.0f / (float)cols;
+    float g[VPT][PER], sg[VPT][PER], sb[VPT][PER];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        load_weights<FULL>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[i]);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sg[i][j] = sb[i][j] = 0.0f;
+    }
+    const int64_t step = (int64_t)gridDim.x * groups * R;
+    int bank = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * groups * R; r0 < rows; r0 += step, bank ^= 1) {
+        const int64_t first = r0 + (int64_t)group * R;
+        Vec<T> vd[R][VPT], vx[R][VPT];
+        float mu[R], rs[R], s[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = first + r < rows;
+            mu[r] = in ? mean[first + r] : 0.0f;
+            rs[r] = in ? rstd[first + r] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                if (in && c < cols) {
+                    vd[r][i].template load_row<FULL>(dy + (first + r) * lddy, c, cols, dy_vec);
+                    vx[r][i].template load_row<FULL>(x + (first + r) * ldx, c, cols, x_vec);
+                } else {
+                    vd[r][i].raw = vx[r][i].raw = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[2 * r] = s[2 * r + 1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float d[PER], h[PER];
+                vd[r][i].get(d);
+                vx[r][i].get(h);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    // beyond the row's end dy is 0, and with it every term
+                    const float hh = (h[j] - mu[r]) * rs[r], dh = d[j] * hh;
+                    sg[i][j] += dh;
+                    sb[i][j] += d[j];
+                    s[2 * r] += d[j] * g[i][j];
+                    s[2 * r + 1] += dh * g[i][j];
+                }
+            }
+        }
+        if (!dx) continue;
+        row_sums<2 * R>(s, tpr, red[bank]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (first + r >= rows) continue;
+            const float sa = s[2 * r] * inv, sh = s[2 * r + 1] * inv;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                if (c >= cols) continue;
+                float d[PER], h[PER];
+                vd[r][i].get(d);
+                vx[r][i].get(h);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) d[j] = rs[r] * (d[j] * g[i][j] - sa - (h[j] - mu[r]) * rs[r] * sh);
+                vd[r][i].set(d);
+                vd[r][i].template store_row<FULL>(dx + (first + r) * lddx, c, cols, dx_vec);
+            }
+        }
+    }
+    if (!part) return;
+    float* pg = part + ((int64_t)blockIdx.x * groups + group) * 2 * cols;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int c = (i * tpr + at) * PER + j;
+            if (c < cols) {
+                pg[c] = sg[i][j];
+                pg[cols + c] = sb[i][j];
+            }
+        }
+}
+
+// Longer rows: dx in two passes over the row.
+template <typename T>
+__global__ void __launch_bounds__(kLnMostThreads)
+    k_layer_norm_dx_long(const T* __restrict__ dy, int64_t lddy, int dy_vec, const T* __restrict__ x, int64_t ldx,
+                         int x_vec, const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
+                         const float* __restrict__ rstd, int64_t rows, int cols, T* __restrict__ dx, int64_t lddx,
+                         int dx_vec)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int PER = Vec<T>::kPer;
+    __shared__ float red[2][2 * 32];
+    const float inv = 1.0f / (float)cols;
+    int bank = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, bank ^= 1) {
+        const float mu = mean[r], rs = rstd[r];
+        float s[2] = {0.0f, 0.0f};
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int c = threadIdx.x * PER; c < cols; c += blockDim.x * PER) {
+                Vec<T> vd, vx;
+                float d[PER], h[PER], g[PER];
+                vd.load(dy + r * lddy, c, cols, dy_vec);
+                vx.load(x + r * ldx, c, cols, x_vec);
+                vd.get(d);
+                vx.get(h);
+                load_weights<false>(gamma, w_type, c, cols, 1.0f, g);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const float hh = (h[j] - mu) * rs, a = d[j] * g[j];
+                    if (pass == 0) {
+                        s[0] += a;
+                        s[1] += a * hh;
+                    } else {
+                        d[j] = rs * (a - s[0] - hh * s[1]);
+                    }
+                }
+                if (pass == 1) {
+                    vd.set(d);
+                    vd.store(dx + r * lddx, c, cols, dx_vec);
+                }
+            }
+            if (pass == 0) {
+                row_sums<2>(s, blockDim.x, red[bank]);
+                s[0] *= inv;
+                s[1] *= inv;
+            }
+        }
+    }
+}
+
+// Longer rows: shares of dgamma and dbeta, a block for 256 columns of the rows blockIdx.y, + gridDim.y, ...
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_layer_norm_shares_long(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                             const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int cols,
+                             float* __restrict__ part)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    float sg = 0.0f, sb = 0.0f;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const float d = to_f32(dy[r * lddy + c]);
+        sg += d * ((to_f32(x[r * ldx + c]) - mean[r]) * rstd[r]);
+        sb += d;
+    }
+    part[(int64_t)blockIdx.y * 2 * cols + c] = sg;
+    part[((int64_t)blockIdx.y * 2 + 1) * cols + c] = sb;
+}
+
+// The shares' sums: a lane takes a column, a block's warps every eighth share.
+__global__ void __launch_bounds__(256)
     k_layer_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* __restrict__ dgamma,
                        float* __restrict__ dbeta)
 {
     griddep_wait();
     griddep_launch_dependents();
-    for (int c = blockIdx.x * kLnThreads + threadIdx.x; c < cols; c += gridDim.x * kLnThreads) {
-        float g = 0.0f, b = 0.0f;
-        for (int p = 0; p < parts; ++p) {
-            g += part[(int64_t)p * 2 * cols + c];
-            b += part[(int64_t)p * 2 * cols + cols + c];
+    __shared__ float sums[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < 2 * cols) {
+        int p = warp;
+        for (; p + 24 < parts; p += 32) {
+            const float a = part[(int64_t)p * 2 * cols + c], b = part[(int64_t)(p + 8) * 2 * cols + c];
+            const float d = part[(int64_t)(p + 16) * 2 * cols + c], e = part[(int64_t)(p + 24) * 2 * cols + c];
+            s += (a + b) + (d + e);
         }
-        if (dgamma) dgamma[c] = g;
-        if (dbeta) dbeta[c] = b;
+        for (; p < parts; p += 8) s += part[(int64_t)p * 2 * cols + c];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp || c >= 2 * cols) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    if (c < cols) {
+        if (dgamma) dgamma[c] = s;
+    } else if (dbeta) {
+        dbeta[c - cols] = s;
     }
 }
 
-static int ln_parts(int64_t rows) { return rows < 2 * kNumSMsHint ? (int)rows : 2 * kNumSMsHint; }
+// ------------------------------------------------------------------------ host
+
+// How rows of `cols` elements are shared out among threads.
+struct LnShape {
+    int vpt;          // vectors a thread holds (0: the row does not fit a block)
+    int tpr, block;   // threads of a row and of a block
+};
+
+static LnShape ln_shape(int cols, int size, int most)
+{
+    const int per = 16 / size, vectors = (cols + per - 1) / per;
+    LnShape s;
+    if (vectors <= 64) {
+        // part of a warp, or a warp with two vectors a lane
+        s.vpt = vectors <= 32 ? 1 : 2;
+        s.tpr = 1;
+        while (s.tpr * s.vpt < vectors) s.tpr *= 2;
+        s.block = kLnBlock;
+        return s;
+    }
+    // a block: two vectors a thread from 128 threads on, four from 512
+    s.vpt = vectors <= 128 ? 1 : vectors <= 1024 ? 2 : 4;
+    s.tpr = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    s.block = s.tpr;
+    if (s.tpr > most) s = LnShape{0, kLnMostThreads, kLnMostThreads};
+    return s;
+}
+
+// Blocks of the backward pass, and the shares of dgamma and dbeta they leave.
+static int ln_bwd_rows(const LnShape& s) { return s.vpt == 1 ? 4 : s.vpt == 2 ? 2 : 1; }
+
+static int ln_bwd_grid(const LnShape& s, int64_t rows)
+{
+    if (!s.vpt) return (int)std::min<int64_t>(rows, num_sms());
+    const int64_t per = (int64_t)(s.block / s.tpr) * ln_bwd_rows(s);
+    const int64_t want = (rows + per - 1) / per, most = (int64_t)num_sms() * std::max(1, 768 / s.block);
+    return (int)std::min(want, most);
+}
+
+static int ln_parts(int64_t rows, int cols, int size)
+{
+    const LnShape s = ln_shape(cols, size, ln_bwd_threads(4));
+    if (!s.vpt) return (int)std::min<int64_t>(rows, 32);
+    return ln_bwd_grid(s, rows) * (s.block / s.tpr);
+}
 
 static int check_ln(const void* x, int64_t ldx, int type, int64_t rows, int cols, const char* name)
 {
@@ -122,27 +474,71 @@ static int check_ln_sizes(int type, int w_type, bool weighted, int64_t rows, int
 }
 
 template <typename T>
-static int run_fwd(const void* x, int64_t ldx, const void* gamma, const void* beta, int w_type, int64_t rows,
-                   int cols, float eps, void* y, int64_t ldy, float* mean, float* rstd, cudaStream_t s)
+static int run_fwd(const void* xp, int64_t ldx, const void* gamma, const void* beta, int w_type, int64_t rows,
+                   int cols, float eps, void* yp, int64_t ldy, float* mean, float* rstd, cudaStream_t s)
 {
-    const int64_t grid = rows < 8 * num_sms() ? rows : 8 * num_sms();
-    launch_pdl(k_layer_norm_fwd<T>, (unsigned)grid, kLnThreads, 0, s, static_cast<const T*>(x), ldx, gamma, beta,
-               w_type, rows, cols, eps, static_cast<T*>(y), ldy, mean, rstd);
+    const LnShape sh = ln_shape(cols, sizeof(T), kLnMostThreads);
+    const T* x = static_cast<const T*>(xp);
+    T* y = static_cast<T*>(yp);
+    const int xv = rows_vec(x, ldx, sizeof(T), rows), yv = rows_vec(y, ldy, sizeof(T), rows);
+    const int64_t most = (int64_t)num_sms() * (2048 / sh.block);
+    if (!sh.vpt) {
+        launch_pdl(k_layer_norm_fwd_long<T>, (unsigned)std::min(rows, most), sh.block, 0, s, x, ldx, xv, gamma, beta,
+                   w_type, rows, cols, eps, y, ldy, yv, mean, rstd);
+        return launch_status("layer norm");
+    }
+    // several rows at a time once every SM has its blocks of them
+    const int groups = sh.block / sh.tpr;
+    const int R = sh.vpt <= 2 && rows > (int64_t)4 * groups * num_sms() ? 4 / sh.vpt : 1;
+    const int64_t want = (rows + (int64_t)groups * R - 1) / ((int64_t)groups * R);
+    const unsigned grid = (unsigned)std::min(want, most);
+    const bool full = cols % Vec<T>::kPer == 0 && xv && yv && aligned_to(gamma, 16) && aligned_to(beta, 16);
+#define ITO_LN_AS(V, RR, F)                                                                                       \
+    launch_pdl(k_layer_norm_fwd<T, V, RR, F>, grid, sh.block, 0, s, x, ldx, xv, gamma, beta, w_type, rows, cols, \
+               sh.tpr, eps, y, ldy, yv, mean, rstd)
+#define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
+    if (sh.vpt == 1) { if (R > 1) ITO_LN(1, 4); else ITO_LN(1, 1); }
+    else if (sh.vpt == 2) { if (R > 1) ITO_LN(2, 2); else ITO_LN(2, 1); }
+    else ITO_LN(4, 1);
+#undef ITO_LN
+#undef ITO_LN_AS
     return launch_status("layer norm");
 }
 
 template <typename T>
-static int run_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* gamma, int w_type,
-                   const float* mean, const float* rstd, int64_t rows, int cols, float* part, void* dx, int64_t lddx,
+static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, const void* gamma, int w_type,
+                   const float* mean, const float* rstd, int64_t rows, int cols, float* part, void* dxp, int64_t lddx,
                    float* dgamma, float* dbeta, cudaStream_t s)
 {
-    const int parts = ln_parts(rows);
-    launch_pdl(k_layer_norm_bwd<T>, parts, kLnThreads, 0, s, static_cast<const T*>(dy), lddy,
-               static_cast<const T*>(x), ldx, gamma, w_type, mean, rstd, rows, cols, static_cast<T*>(dx), lddx,
-               dgamma || dbeta ? part : static_cast<float*>(nullptr));
-    if (dgamma || dbeta)
-        launch_pdl(k_layer_norm_wgrad, (cols + kLnThreads - 1) / kLnThreads, kLnThreads, 0, s, part, parts, cols,
-                   dgamma, dbeta);
+    const LnShape sh = ln_shape(cols, sizeof(T), ln_bwd_threads(4));
+    const T *dy = static_cast<const T*>(dyp), *x = static_cast<const T*>(xp);
+    T* dx = static_cast<T*>(dxp);
+    const int dyv = rows_vec(dy, lddy, sizeof(T), rows), xv = rows_vec(x, ldx, sizeof(T), rows);
+    const int dxv = rows_vec(dx, lddx, sizeof(T), rows);
+    const bool wgrad = dgamma || dbeta;
+    float* share = wgrad ? part : nullptr;
+    const int grid = ln_bwd_grid(sh, rows);
+    const bool full = cols % Vec<T>::kPer == 0 && dyv && xv && dxv && aligned_to(gamma, 16);
+#define ITO_LN_AS(V, RR, F)                                                                                         \
+    launch_pdl(k_layer_norm_bwd<T, V, RR, F>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean, \
+               rstd, rows, cols, sh.tpr, dx, lddx, dxv, share)
+#define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
+    if (sh.vpt == 1) ITO_LN(1, 4);
+    else if (sh.vpt == 2) ITO_LN(2, 2);
+    else if (sh.vpt == 4) ITO_LN(4, 1);
+    else {
+        if (dx)
+            launch_pdl(k_layer_norm_dx_long<T>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean,
+                       rstd, rows, cols, dx, lddx, dxv);
+        if (wgrad)
+            launch_pdl(k_layer_norm_shares_long<T>, dim3((cols + 255) / 256, ln_parts(rows, cols, sizeof(T))), 256, 0,
+                       s, dy, lddy, x, ldx, mean, rstd, rows, cols, share);
+    }
+#undef ITO_LN
+#undef ITO_LN_AS
+    if (wgrad)
+        launch_pdl(k_layer_norm_wgrad, (2 * cols + 31) / 32, 256, 0, s, static_cast<const float*>(part),
+                   ln_parts(rows, cols, sizeof(T)), cols, dgamma, dbeta);
     return launch_status("layer norm");
 }
 
@@ -175,7 +571,8 @@ int ito_layer_norm_fwd(const void* x, int64_t ldx, int type, const void* gamma, 
 size_t ito_layer_norm_bwd_workspace_size(int64_t rows, int cols)
 {
     if (rows < 1 || cols < 1 || rows > (int64_t(1) << 40) || cols > (1 << 24)) return 0;
-    return (size_t)ln_parts(rows) * 2 * cols * sizeof(float);
+    // the shares of either element size
+    return (size_t)std::max(ln_parts(rows, cols, 2), ln_parts(rows, cols, 4)) * 2 * cols * sizeof(float);
 }
 
 int ito_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int type, const void* gamma,

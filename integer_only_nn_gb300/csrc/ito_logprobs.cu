@@ -8,6 +8,8 @@
 // Masked classes hold -inf: they have p = 0 and take no part. A row whose every class is
 // masked has lse = -inf, log probabilities of -inf, entropy 0 and a gradient of 0. A target
 // of -1 stands for no token: logp 0 and no gradient from it.
+#include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -15,8 +17,10 @@
 
 namespace ito {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpMaxTop = 32;
+constexpr int kLpMaxTop = 32;        // alternatives: a warp's list holds one to a lane
+constexpr int kLpWarps = 8;          // warps of a block
+constexpr int kLpCluster = 8;        // blocks that share a long row, at most
+constexpr float kLog2e = 1.4426950408889634f;
 
 // larger values first, equal values in the order of their index; a NaN above all
 __device__ __forceinline__ bool comes_before(float a, int ia, float b, int ib)
@@ -28,136 +32,385 @@ __device__ __forceinline__ bool comes_before(float a, int ia, float b, int ib)
     return ia < ib;
 }
 
-// the sums of a part of a row: its largest value, sum exp(x - top), sum (x - top) exp(x - top)
-struct Sums {
-    float top, s, t;
-};
-
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b)
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    if (b.s == 0.0f) return a;
-    if (a.s == 0.0f) return b;
-    const float top = fmaxf(a.top, b.top);
-    const float ea = expf(a.top - top), eb = expf(b.top - top);
-    return Sums{top, a.s * ea + b.s * eb, (a.t + (a.top - top) * a.s) * ea + (b.t + (b.top - top) * b.s) * eb};
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads)
-    k_logprobs_fwd(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows, int classes,
-                   int k, float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ lse,
-                   int32_t* __restrict__ top_ids, float* __restrict__ top_logp, int* __restrict__ err)
+// ---------------------------------------------------------- sums of a part of a row
+//
+// One pass: a running maximum `top`, s = sum exp(x - top) and t = sum (x - top) exp(x - top),
+// brought to a new maximum when a vector raises it (rarely, after the first few). `top` starts
+// at the lowest finite value, so that -inf adds 0 and the lowest value itself adds 1.
+struct Sums {
+    float top, s, t;
+
+    __device__ __forceinline__ void rise(float m)
+    {
+        if (!(m > top)) return;
+        const float d = fmaxf(top - m, -FLT_MAX), e = exp2_fast(d * kLog2e);
+        t = e != 0.0f ? (t + d * s) * e : 0.0f;
+        s = s != s ? s : e != 0.0f ? s * e : 0.0f;
+        top = m;
+    }
+    __device__ __forceinline__ void add(float x)
+    {
+        const float d = x - top, e = exp2_fast(d * kLog2e);
+        s += e;
+        t += fmaxf(d, -200.0f) * e;      // (-inf times 0 would be a NaN; a NaN reaches s)
+    }
+    __device__ __forceinline__ void join(Sums o)
+    {
+        const float m = fmaxf(top, o.top);
+        rise(m);
+        o.rise(m);
+        s += o.s;
+        t += o.t;
+    }
+};
+
+// ------------------------------------------------------------- a warp's alternatives
+//
+// Lane i holds the i-th best of what the warp has seen. `low` (uniform) is the k-th: only
+// elements that come before it are looked at closer, about k ln(n / k) of n in random order.
+struct Alternatives {
+    float value;
+    int id;
+    float low;
+    int low_id;
+
+    __device__ __forceinline__ void clear()
+    {
+        value = low = -INFINITY;
+        id = low_id = INT_MAX;
+    }
+    __device__ __forceinline__ bool wants(float v, int i) const { return comes_before(v, i, low, low_id); }
+    // all lanes, with the same v and i
+    __device__ __forceinline__ void insert(float v, int i, int k)
+    {
+        const int lane = threadIdx.x & 31;
+        const unsigned better = __ballot_sync(0xffffffffu, comes_before(value, id, v, i));
+        const int place = __popc(better);
+        const float pv = __shfl_up_sync(0xffffffffu, value, 1);
+        const int pi = __shfl_up_sync(0xffffffffu, id, 1);
+        if (lane == place) {
+            value = v;
+            id = i;
+        } else if (lane > place) {
+            value = pv;
+            id = pi;
+        }
+        low = __shfl_sync(0xffffffffu, value, k - 1);
+        low_id = __shfl_sync(0xffffffffu, id, k - 1);
+    }
+    // all lanes, each with an element of its own (take false: none)
+    __device__ __forceinline__ void offer(float v, int i, bool take, int k)
+    {
+        unsigned m = __ballot_sync(0xffffffffu, take && wants(v, i));
+        while (m) {
+            const int src = __ffs(m) - 1;
+            const float cv = __shfl_sync(0xffffffffu, v, src);
+            const int ci = __shfl_sync(0xffffffffu, i, src);
+            if (wants(cv, ci)) insert(cv, ci, k);
+            m &= m - 1;
+        }
+    }
+};
+
+// Elements [begin, end) of a row for thread `at` of `threads`: UNROLL vectors in flight. A
+// vector's elements are `skip` apart: neighbours (vec; begin on 16 bytes) or a warp's width
+// apart, where rows start anywhere and a warp's single loads are still consecutive.
+template <typename T, bool TOP>
+__device__ __forceinline__ void scan_part(const T* __restrict__ row, int begin, int end, int at, int threads, bool vec,
+                                          int k, Sums& sums, Alternatives& alt)
+{
+    constexpr int PER = Vec<T>::kPer, UNROLL = 4;
+    const int lane = threadIdx.x & 31;
+    const int skip = vec ? 1 : 32;
+    const int64_t round = (int64_t)threads * PER * UNROLL;
+    for (int64_t base = begin; base < end; base += round) {
+        Vec<T> v[UNROLL];
+        int first[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int64_t block = base + ((int64_t)u * threads + (at - lane)) * PER;     // the warp's elements
+            const int64_t c = block + (vec ? lane * PER : lane);
+            first[u] = (int)(c < end ? c : end);
+            if (vec && c + PER <= end) {
+                v[u].raw = __ldg(reinterpret_cast<const uint4*>(row + c));
+            } else {
+                float f[PER];
+#pragma unroll
+                for (int j = 0; j < PER; ++j) f[j] = c + j * skip < end ? to_f32(row[c + j * skip]) : -INFINITY;
+                v[u].set(f);             // exact: the values came from T
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            float f[PER];
+            v[u].get(f);
+            float m = f[0];
+#pragma unroll
+            for (int j = 1; j < PER; ++j) m = fmaxf(m, f[j]);
+            sums.rise(m);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) sums.add(f[j]);
+            if (TOP) {
+                // beyond the end the elements are -inf: there may be none better than that
+                bool look = m > alt.low || (m == alt.low && first[u] < alt.low_id);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) look |= f[j] != f[j];
+                if (__any_sync(0xffffffffu, look && first[u] < end)) {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) alt.offer(f[j], first[u] + j * skip, first[u] + j * skip < end, k);
+                }
+            }
+        }
+    }
+}
+
+struct LpOut {
+    float *logp, *entropy, *lse;
+    int32_t* top_ids;
+    float* top_logp;
+};
+
+// the row's results from its sums and (lane i: the i-th) alternatives; one warp
+template <typename T, bool TOP>
+__device__ __forceinline__ void write_row(const T* row, const int32_t* targets, int64_t r, int classes, int k,
+                                          const Sums& a, const Alternatives& alt, const LpOut& o, int* err)
+{
+    const int lane = threadIdx.x & 31;
+    const bool none = a.s == 0.0f;
+    const float ls = logf(a.s);
+    if (lane == 0) {
+        if (o.lse) o.lse[r] = none ? -INFINITY : a.top + ls;
+        if (o.entropy) o.entropy[r] = none ? 0.0f : ls - a.t / a.s;
+        if (o.logp) {
+            const int t = targets[r];
+            if (t < -1 || t >= classes) raise_device_error(err, ITO_ERR_ARG);
+            o.logp[r] = t < 0 || t >= classes ? 0.0f : none ? -INFINITY : (to_f32(row[t]) - a.top) - ls;
+        }
+    }
+    if (TOP && lane < k) {
+        o.top_ids[r * k + lane] = alt.id;
+        o.top_logp[r * k + lane] = none ? -INFINITY : (alt.value - a.top) - ls;
+    }
+}
+
+__device__ __forceinline__ Sums warp_join(Sums a)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a.join(Sums{__shfl_xor_sync(0xffffffffu, a.top, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                    __shfl_xor_sync(0xffffffffu, a.t, o)});
+    return a;
+}
+
+// Short rows: a warp to a row.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpWarps * 32)
+    k_logprobs_short(const T* __restrict__ x, int64_t ld, int vec, const int32_t* __restrict__ targets, int64_t rows,
+                     int classes, int k, const LpOut o, int* __restrict__ err)
 {
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ Sums part[kLpThreads];
-    __shared__ float bv[kLpThreads];
-    __shared__ int bi[kLpThreads];
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* xr = x + r * ld;
-        Sums a{0.0f, 0.0f, 0.0f};
-        float top = -INFINITY;
-        for (int c = threadIdx.x; c < classes; c += kLpThreads) {
-            const float v = to_f32(xr[c]);
-            top = v > top || v != v ? v : top;
+    const int64_t step = (int64_t)gridDim.x * kLpWarps;
+    for (int64_t r = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5); r < rows; r += step) {
+        Sums a{-FLT_MAX, 0.0f, 0.0f};
+        Alternatives alt;
+        alt.clear();
+        scan_part<T, TOP>(x + r * ld, 0, classes, threadIdx.x & 31, 32, vec, k, a, alt);
+        write_row<T, TOP>(x + r * ld, targets, r, classes, k, warp_join(a), alt, o, err);
+    }
+}
+
+// Longer rows: a cluster of blocks to a row (of one block, where there are rows enough), each
+// with a stretch of it. The warps' sums and alternatives meet in their block's shared memory, the
+// blocks' in the first one's, read across the cluster.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpWarps * 32)
+    k_logprobs_long(const T* __restrict__ x, int64_t ld, int vec, const int32_t* __restrict__ targets, int64_t rows,
+                    int classes, int k, int parts, int stretch, const LpOut o, int* __restrict__ err)
+{
+    __shared__ Sums sums[kLpWarps];
+    __shared__ float values[kLpWarps][kLpMaxTop];
+    __shared__ int ids[kLpWarps][kLpMaxTop];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = parts > 1 ? (int)cluster_ctarank() : 0;
+    const int begin = min(classes, part * stretch), end = min(classes, begin + stretch);
+    for (int64_t r = blockIdx.x / parts; r < rows; r += gridDim.x / parts) {
+        Sums a{-FLT_MAX, 0.0f, 0.0f};
+        Alternatives alt;
+        alt.clear();
+        scan_part<T, TOP>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, vec, k, a, alt);
+        a = warp_join(a);
+        if (lane == 0) sums[warp] = a;
+        if (TOP) {
+            values[warp][lane] = alt.value;
+            ids[warp][lane] = alt.id;
         }
-        bv[threadIdx.x] = top;
         __syncthreads();
-        for (int o = kLpThreads / 2; o > 0; o >>= 1) {
-            if (threadIdx.x < o) {
-                const float b = bv[threadIdx.x + o];
-                if (b > bv[threadIdx.x] || b != b) bv[threadIdx.x] = b;
-            }
-            __syncthreads();
+        if (warp == 0) {
+            a = lane < kLpWarps ? sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
+            a = warp_join(a);
+            if (TOP)
+                for (int w = 1; w < kLpWarps; ++w) alt.offer(values[w][lane], ids[w][lane], lane < k, k);
         }
-        top = bv[0];
-        a.top = top;
-        for (int c = threadIdx.x; c < classes; c += kLpThreads) {
-            const float v = to_f32(xr[c]);
-            if (v == -INFINITY) continue;
-            const float e = expf(v - top);
-            a.s += e;
-            a.t += e != 0.0f ? (v - top) * e : 0.0f;
-        }
-        part[threadIdx.x] = a;
-        __syncthreads();
-        for (int o = kLpThreads / 2; o > 0; o >>= 1) {
-            if (threadIdx.x < o) part[threadIdx.x] = join(part[threadIdx.x], part[threadIdx.x + o]);
-            __syncthreads();
-        }
-        a = part[0];
-        const float ls = logf(a.s);
-        const bool none = a.s == 0.0f;
-        const float z = none ? -INFINITY : a.top + ls;
-        if (threadIdx.x == 0) {
-            if (lse) lse[r] = z;
-            if (entropy) entropy[r] = none ? 0.0f : ls - a.t / a.s;
-            if (logp) {
-                const int t = targets[r];
-                if (t < -1 || t >= classes) raise_device_error(err, ITO_ERR_ARG);
-                logp[r] = t < 0 || t >= classes ? 0.0f : none ? -INFINITY : to_f32(xr[t]) - z;
-            }
-        }
-        float last = 0.0f;
-        int last_i = -1;
-        for (int j = 0; j < k; ++j) {
-            float best = -INFINITY;
-            int best_i = INT_MAX;
-            for (int c = threadIdx.x; c < classes; c += kLpThreads) {
-                const float v = to_f32(xr[c]);
-                if (j && !comes_before(last, last_i, v, c)) continue;
-                if (comes_before(v, c, best, best_i)) { best = v; best_i = c; }
-            }
-            __syncthreads();
-            bv[threadIdx.x] = best;
-            bi[threadIdx.x] = best_i;
-            __syncthreads();
-            for (int o = kLpThreads / 2; o > 0; o >>= 1) {
-                if (threadIdx.x < o && comes_before(bv[threadIdx.x + o], bi[threadIdx.x + o], bv[threadIdx.x], bi[threadIdx.x])) {
-                    bv[threadIdx.x] = bv[threadIdx.x + o];
-                    bi[threadIdx.x] = bi[threadIdx.x + o];
+        if (parts > 1) {
+            if (warp == 0) {
+                if (lane == 0) sums[0] = a;
+                if (TOP) {
+                    values[0][lane] = alt.value;
+                    ids[0][lane] = alt.id;
                 }
-                __syncthreads();
             }
-            last = bv[0];
-            last_i = bi[0];
-            if (threadIdx.x == 0) {
-                top_ids[r * k + j] = last_i;
-                top_logp[r * k + j] = none ? -INFINITY : last - z;
+            cluster_sync();
+            if (part == 0 && warp == 0) {
+                for (int p = 1; p < parts; ++p) {
+                    const uint32_t sa = mapa_shared(smem_u32(&sums[0]), p);
+                    Sums q;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.top) : "r"(sa) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(sa + 4) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.t) : "r"(sa + 8) : "memory");
+                    a.join(q);
+                    if (TOP) {
+                        float v;
+                        int i;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(v) : "r"(mapa_shared(smem_u32(&values[0][lane]), p)) : "memory");
+                        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                     : "=r"(i) : "r"(mapa_shared(smem_u32(&ids[0][lane]), p)) : "memory");
+                        alt.offer(v, i, lane < k, k);
+                    }
+                }
             }
+            cluster_sync();              // the first block has read the others' shared memory
         }
+        if (part == 0 && warp == 0) write_row<T, TOP>(x + r * ld, targets, r, classes, k, a, alt, o, err);
         __syncthreads();
     }
 }
 
+// ------------------------------------------------------------------- the gradient
+//
+// A block takes a stretch of a row (or its warps a row each, where rows are short). Where the
+// row and its gradient start equally far from a 16-byte boundary, the elements up to the first
+// boundary and after the last go alone and the rest in 16-byte vectors.
+
+//
+// log p = x - lse is as good as lse, whose own rounding grows with it: from 2^16 on (rows of
+// masks of the type's lowest value) the row's sums are taken again, and log p is
+// (x - top) - log s. (Not where the gradient replaces the logits of a row that several blocks
+// share: there the row is being overwritten.)
+struct LpRow {
+    float top, ls, g, gh, h;
+    int t;
+};
+constexpr float kLpFar = 65536.0f;
+
+// dx_j: the factor of p is one sum, so p (which may lie below the normal range) is rounded once
+__device__ __forceinline__ float lp_slope(const LpRow& w, float x, int c)
+{
+    float d = c == w.t ? w.g : 0.0f;
+    if (x != -INFINITY) {
+        const float lp = (x - w.top) - w.ls;
+        d -= __expf(lp) * (w.g + w.gh * (lp + w.h));
+    }
+    return d;
+}
+
+constexpr int kLpStretch = 8192;     // elements of a row that a block takes, at most
+
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads)
+__global__ void __launch_bounds__(256)
     k_logprobs_bwd(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets,
                    const float* __restrict__ lse, const float* __restrict__ entropy, int64_t rows, int classes,
                    const float* __restrict__ g_logp, const float* __restrict__ g_entropy, T* __restrict__ dx,
-                   int64_t ldd, int* __restrict__ err)
+                   int64_t ldd, int per_warp, int stretches, int* __restrict__ err)
 {
     griddep_wait();
     griddep_launch_dependents();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    constexpr int PER = Vec<T>::kPer, UNROLL = 4;
+    __shared__ Sums sums[kLpWarps];
+    const int at = per_warp ? threadIdx.x & 31 : threadIdx.x, threads = per_warp ? 32 : 256;
+    const int64_t work = per_warp ? rows : rows * stretches;
+    const int64_t first = per_warp ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = per_warp ? (int64_t)gridDim.x * 8 : gridDim.x;
+    for (int64_t i = first; i < work; i += step) {
+        const int64_t r = per_warp ? i : i / stretches;
         const float z = lse[r];
-        int t = targets ? targets[r] : -1;
-        if (t < -1 || t >= classes) {
-            if (threadIdx.x == 0) raise_device_error(err, ITO_ERR_ARG);
-            t = -1;
+        LpRow w;
+        w.top = z;
+        w.ls = 0.0f;
+        w.t = targets ? targets[r] : -1;
+        if (w.t < -1 || w.t >= classes) {
+            if (at == 0) raise_device_error(err, ITO_ERR_ARG);
+            w.t = -1;
         }
-        const float g = t >= 0 && g_logp ? g_logp[r] : 0.0f;
-        const float gh = g_entropy ? g_entropy[r] : 0.0f, h = g_entropy ? entropy[r] : 0.0f;
-        for (int c = threadIdx.x; c < classes; c += kLpThreads) {
-            const float v = to_f32(x[r * ld + c]);
-            float d = 0.0f;
-            if (z != -INFINITY) {
-                const float lp = v - z;
-                d = c == t ? g : 0.0f;
-                if (v != -INFINITY) d -= expf(lp) * (g + gh * (lp + h));
+        w.g = w.t >= 0 && g_logp ? g_logp[r] : 0.0f;
+        w.gh = g_entropy ? g_entropy[r] : 0.0f;
+        w.h = g_entropy ? entropy[r] : 0.0f;
+        const T* xr = x + r * ld;
+        T* dr = dx + r * ldd;
+        if (fabsf(z) >= kLpFar && fabsf(z) < INFINITY && (stretches == 1 || dx != x)) {
+            Sums a{-FLT_MAX, 0.0f, 0.0f};
+            Alternatives none;
+            scan_part<T, false>(xr, 0, classes, at, threads, false, 0, a, none);
+            a = warp_join(a);
+            if (!per_warp) {
+                __syncthreads();         // (the row is the block's: every thread is here)
+                if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = a;
+                __syncthreads();
+                a = warp_join((threadIdx.x & 31) < kLpWarps ? sums[threadIdx.x & 31] : Sums{-FLT_MAX, 0.0f, 0.0f});
             }
-            dx[r * ldd + c] = from_f32<T>(d);
+            w.top = a.top;
+            w.ls = logf(a.s);
         }
+        const int lead_x = (int)((16 - (reinterpret_cast<uintptr_t>(xr) & 15)) & 15) / (int)sizeof(T);
+        const int lead_d = (int)((16 - (reinterpret_cast<uintptr_t>(dr) & 15)) & 15) / (int)sizeof(T);
+        const int lead = min(lead_x, classes);
+        const bool vec = lead_x == lead_d;
+        const int64_t s = per_warp ? 0 : i - r * stretches;
+        // stretch s of the row counts from the first boundary; the first one takes the lead too
+        const int64_t b0 = lead + s * kLpStretch;
+        const int begin = (int)min((int64_t)classes, b0);
+        const int end = per_warp || s == stretches - 1 ? classes : (int)min((int64_t)classes, b0 + kLpStretch);
+        if (z == -INFINITY) {
+            for (int c = (s == 0 ? 0 : begin) + at; c < end; c += threads) dr[c] = from_f32<T>(0.0f);
+            continue;
+        }
+        if (s == 0 && at < lead) dr[at] = from_f32<T>(lp_slope(w, to_f32(xr[at]), at));
+        int c = begin;
+        if (vec) {
+            const int whole = begin + (end - begin) / PER * PER;
+            for (; c < whole; c += threads * PER * UNROLL) {
+                Vec<T> v[UNROLL];
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int k = c + (u * threads + at) * PER;
+                    if (k < whole) v[u].raw = __ldcs(reinterpret_cast<const uint4*>(xr + k));
+                }
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int k = c + (u * threads + at) * PER;
+                    if (k >= whole) continue;
+                    float f[PER];
+                    v[u].get(f);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) f[j] = lp_slope(w, f[j], k + j);
+                    v[u].set(f);
+                    __stcs(reinterpret_cast<uint4*>(dr + k), v[u].raw);
+                }
+            }
+            c = whole;
+        }
+#pragma unroll 4
+        for (int k = c + at; k < end; k += threads) dr[k] = from_f32<T>(lp_slope(w, to_f32(xr[k]), k));
     }
 }
 
@@ -172,14 +425,50 @@ static int check_lp(const void* x, int64_t ld, int type, int64_t rows, int class
     return ITO_OK;
 }
 
-template <typename T>
-static int run_fwd(const void* x, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k, float* logp,
-                   float* entropy, float* lse, int32_t* top_ids, float* top_logp, int* err, cudaStream_t s)
+template <typename T, bool TOP>
+static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
+                   const LpOut& o, int* err, cudaStream_t s)
 {
-    const int64_t grid = rows < 8 * num_sms() ? rows : 8 * num_sms();
-    launch_pdl(k_logprobs_fwd<T>, (unsigned)grid, kLpThreads, 0, s, static_cast<const T*>(x), ld, targets, rows,
-               classes, k, logp, entropy, lse, top_ids, top_logp, err);
-    return launch_status("log probabilities");
+    const T* x = static_cast<const T*>(xp);
+    const int vec = rows_vec(x, ld, sizeof(T), rows);
+    const int sms = num_sms();
+    // a warp to a row up to four rounds of its loads, or where warps of whole rows fill the device
+    const int round = 32 * Vec<T>::kPer * 4;
+    if (classes <= round || (classes <= 4 * round && rows >= 16 * sms)) {
+        const int64_t want = (rows + kLpWarps - 1) / kLpWarps, most = (int64_t)sms * 8;
+        launch_pdl(k_logprobs_short<T, TOP>, (unsigned)std::min(want, most), kLpWarps * 32, 0, s, x, ld, vec, targets,
+                   rows, classes, k, o, err);
+        return launch_status("log probabilities");
+    }
+    // blocks of a row: enough that all rows' blocks occupy the SMs, each with a round of loads at least
+    int parts = 1;
+    while (parts < kLpCluster && rows * parts * 2 <= 2 * sms && classes / (2 * parts) >= kLpWarps * round / 4) parts *= 2;
+    const int stretch = ((classes + parts - 1) / parts + 15) / 16 * 16;
+    const int64_t most = (int64_t)sms * 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(rows * parts, most) / parts * parts));
+    cfg.blockDim = dim3(kLpWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = parts;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP>, x, ld, vec, targets, rows, classes, k, parts,
+                                             stretch, o, err);
+    return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "log probabilities launch: %s", cudaGetErrorString(e));
+}
+
+template <typename T>
+static int run_fwd_any(const void* x, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
+                       const LpOut& o, int* err, cudaStream_t s)
+{
+    if (k) return run_fwd<T, true>(x, ld, targets, rows, classes, k, o, err, s);
+    return run_fwd<T, false>(x, ld, targets, rows, classes, k, o, err, s);
 }
 
 template <typename T>
@@ -187,9 +476,12 @@ static int run_bwd(const void* x, int64_t ld, const int32_t* targets, const floa
                    int64_t rows, int classes, const float* g_logp, const float* g_entropy, void* dx, int64_t ldd,
                    int* err, cudaStream_t s)
 {
-    const int64_t grid = rows < 8 * num_sms() ? rows : 8 * num_sms();
-    launch_pdl(k_logprobs_bwd<T>, (unsigned)grid, kLpThreads, 0, s, static_cast<const T*>(x), ld, targets, lse,
-               entropy, rows, classes, g_logp, g_entropy, static_cast<T*>(dx), ldd, err);
+    const int per_warp = classes <= 32 * Vec<T>::kPer * 4;
+    const int stretches = (classes + kLpStretch - 1) / kLpStretch;
+    const int64_t blocks = per_warp ? (rows + 7) / 8 : rows * stretches;
+    launch_pdl(k_logprobs_bwd<T>, (unsigned)std::min<int64_t>(blocks, 1 << 30), 256, 0, s, static_cast<const T*>(x),
+               ld, targets, lse, entropy, rows, classes, g_logp, g_entropy, static_cast<T*>(dx), ldd, per_warp,
+               stretches, err);
     return launch_status("log probabilities");
 }
 
@@ -216,12 +508,10 @@ int ito_token_logprobs_fwd(const void* logits, int64_t ld, int type, const int32
     int* err = device_error_word();
     if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (type == ITO_F32)
-        return run_fwd<float>(logits, ld, targets, rows, classes, k, logp, entropy, lse, top_ids, top_logp, err, s);
-    if (type == ITO_BF16)
-        return run_fwd<__nv_bfloat16>(logits, ld, targets, rows, classes, k, logp, entropy, lse, top_ids, top_logp,
-                                      err, s);
-    return run_fwd<__half>(logits, ld, targets, rows, classes, k, logp, entropy, lse, top_ids, top_logp, err, s);
+    const LpOut o{logp, entropy, lse, top_ids, top_logp};
+    if (type == ITO_F32) return run_fwd_any<float>(logits, ld, targets, rows, classes, k, o, err, s);
+    if (type == ITO_BF16) return run_fwd_any<__nv_bfloat16>(logits, ld, targets, rows, classes, k, o, err, s);
+    return run_fwd_any<__half>(logits, ld, targets, rows, classes, k, o, err, s);
 }
 
 int ito_token_logprobs_bwd(const void* logits, int64_t ld, int type, const int32_t* targets, const float* lse,

@@ -527,6 +527,26 @@ def test_logprobs_masks(torch, ito, dtype, n):
     check_logprobs(torch, ito, x, tgt, 1, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [10, 4000, 50000])
+def test_logprobs_gradient_of_rows_at_the_lowest_value(torch, ito, dtype, n):
+    """A row masked with the type's lowest value throughout is a uniform distribution, whatever its lse
+    absorbs: p = 1 / n to the accuracy of n's logarithm in 32 bits, 16 u (1 + log n)."""
+    low = torch.finfo(dt(torch, dtype)).min
+    x = torch.full((3, n), low, dtype=dt(torch, dtype), device="cuda")
+    x[1] = 100000.0
+    x[2] = normal(torch, (n,), 1, 1.0, dtype)
+    tgt = torch.tensor([1, 2, 3], dtype=torch.int32, device="cuda")
+    logp, ent, lse, _, _ = ito.ito_token_logprobs_fwd(x, tgt)
+    gl = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+    d = ito.ito_token_logprobs_bwd(x, tgt, lse, ent, gl)
+    for r in (0, 1):
+        want = np.full(n, -float(gl[r]) / n)
+        want[r + 1] += float(gl[r])
+        within_rounded(d[r], want, np.abs(float(gl[r])) * 16 * U * (1 + math.log(n)) * (1.0 / n + (want * float(gl[r]) > 0)), dtype)
+        assert abs(float(logp[r]) + math.log(n)) <= 16 * U * (1 + math.log(n)) + n / 32 * U
+
+
 @pytest.mark.parametrize("order", ["rising", "falling", "equal", "saw"])
 @pytest.mark.parametrize("n", [100, 5000, 70000])
 def test_logprobs_alternatives_in_any_order(torch, ito, order, n):
