@@ -826,17 +826,18 @@ def _act_id(act):
 
 def _matrix(t, name, rows=None, cols=None, dtype=None):
     """Checks a 2-D device tensor whose rows' elements are consecutive; -> its row stride."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%s][%s]" % (
-            name, list(t.shape), "rows" if rows is None else rows, "columns" if cols is None else cols))
-    if not t.numel():
+            name, list(shape), "rows" if rows is None else rows, "columns" if cols is None else cols))
+    if not shape[0] or not shape[1]:
         raise ItoError(ITO_ERR_SHAPE, "%s: no elements" % name)
     if not t.is_cuda:
         raise ItoError(ITO_ERR_ARG, "%s: not on the GPU" % name)
     if dtype is not None and t.dtype != dtype:
         raise ItoError(ITO_ERR_ARG, "%s: type %s, expected %s" % (name, t.dtype, dtype))
     s0, s1 = t.stride()
-    if s1 != 1 and t.shape[1] > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ItoError(ITO_ERR_ARG, "%s: the elements of a row are not consecutive" % name)
     return s0
 
@@ -845,58 +846,71 @@ def _vector(t, name, n, dtypes):
     """Checks a dense 1-D device tensor (None passes)."""
     if t is None:
         return
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%d]" % (name, list(t.shape), n))
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != n:
+        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%d]" % (name, list(shape), n))
     if not t.is_cuda or t.dtype not in dtypes:
         raise ItoError(ITO_ERR_ARG, "%s: %s on %s" % (name, t.dtype, t.device))
     if n > 1 and t.stride(0) != 1:
         raise ItoError(ITO_ERR_ARG, "%s: not contiguous" % name)
 
 
-class _On:
-    """Allocations of a call belong to the stream it launches on."""
+def _raw_stream(device):
+    """The current stream's handle (torch.cuda.current_stream() makes an object for it, which
+    takes as long as a small kernel's launch)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
 
-    def __init__(self, stream):
-        self.ctx = None if stream is None else _torch().cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+def _on_stream(call, stream):
+    """Runs a call with `stream` as torch's current stream (None: as it is), so that what it
+    allocates belongs to the stream that it launches on."""
+    if stream is None:
+        return call()
+    with _torch().cuda.stream(stream):
+        return call()
 
 
 def _scratch(n, device):
-    """A 256-byte aligned workspace of n bytes, and the tensor that owns it."""
+    """A 256-byte aligned workspace of n bytes: its address, and the tensor that owns it."""
     if not n:
         return None, None
     t = _torch().empty(n + 255, dtype=_torch().uint8, device=device)
-    return _aligned256(t), t
+    return (t.data_ptr() + 255) & ~255, t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def ito_fp_linear_fwd(x, W, bias=None, act="none", residual=None, save_z=False, out_dtype=None, stream=None):
     """y = act(x W^T + bias) + residual for bf16 or f16 x [B][IC], W [OC][IC]; -> y, or (y, z)
     with z = x W^T + bias in x's type where save_z. out_dtype (of y and residual): x's type
     or float32. bias: x's type or float32."""
+    if stream is not None:
+        return _on_stream(lambda: ito_fp_linear_fwd(x, W, bias, act, residual, save_z, out_dtype), stream)
     torch = _torch()
-    ldx, ldw = _matrix(x, "x"), _matrix(W, "W", None, x.shape[1], x.dtype)
-    ty = _type_id(x, "x")
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x")
     B, IC = x.shape
+    ldw = _matrix(W, "W", None, IC, dtype)
     OC = W.shape[0]
-    out_dtype = out_dtype or x.dtype
-    _vector(bias, "bias", OC, (x.dtype, torch.float32))
+    ty = _type_id(x, "x")
+    if out_dtype is None:
+        out_dtype = dtype
+    bt = ITO_F32
+    if bias is not None:
+        _vector(bias, "bias", OC, (dtype, torch.float32))
+        bt = _type_id(bias, "bias")
     ldr = 0 if residual is None else _matrix(residual, "residual", B, OC, out_dtype)
-    with _On(stream):
-        y = torch.empty((B, OC), dtype=out_dtype, device=x.device)
-        z = torch.empty((B, OC), dtype=x.dtype, device=x.device) if save_z else None
-        px, pw = _ptr(x), _ptr(W)
-        n = _lib.ito_fp_linear_fwd_workspace_size(px, ldx, pw, ldw, B, IC, OC)
-        ws, keep = _scratch(n, x.device)
-        _check(_lib.ito_fp_linear_fwd(px, ldx, pw, ldw, _ptr(bias), _ptr(residual), ldr, ty, _type_id(y, "out_dtype"),
-                                      ITO_F32 if bias is None else _type_id(bias, "bias"), _act_id(act), B, IC, OC,
-                                      ws, n, _ptr(z), OC, _ptr(y), OC, _stream(stream)))
+    y = torch.empty((B, OC), dtype=out_dtype, device=dev)
+    z = torch.empty((B, OC), dtype=dtype, device=dev) if save_z else None
+    px, pw = x.data_ptr(), W.data_ptr()
+    n = _lib.ito_fp_linear_fwd_workspace_size(px, ldx, pw, ldw, B, IC, OC)
+    ws, keep = _scratch(n, dev)
+    _check(_lib.ito_fp_linear_fwd(px, ldx, pw, ldw, _addr(bias), _addr(residual), ldr, ty, _type_id(y, "out_dtype"), bt,
+                                  _act_id(act), B, IC, OC, ws, n, _addr(z), OC, y.data_ptr(), OC, _raw_stream(dev)))
     return (y, z) if save_z else y
 
 
@@ -904,104 +918,122 @@ def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, 
                       stream=None):
     """Gradients of ito_fp_linear_fwd -> (dx [B][IC] in x's type, dW [OC][IC] in dw_dtype (x's
     type or float32), dbias float32 [OC]); None for those not needed."""
+    if stream is not None:
+        return _on_stream(lambda: ito_fp_linear_bwd(dy, x, W, z, act, need_dx, need_dw, need_dbias, dw_dtype), stream)
     torch = _torch()
-    ldx, ldw = _matrix(x, "x"), _matrix(W, "W", None, x.shape[1], x.dtype)
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x")
     B, IC = x.shape
+    ldw = _matrix(W, "W", None, IC, dtype)
     OC = W.shape[0]
-    lddy = _matrix(dy, "dy", B, OC, x.dtype)
-    ldz = 0 if z is None else _matrix(z, "z", B, OC, x.dtype)
+    lddy = _matrix(dy, "dy", B, OC, dtype)
+    ldz = 0 if z is None else _matrix(z, "z", B, OC, dtype)
     a = _act_id(act)
-    dw_dtype = dw_dtype or x.dtype
     if not (need_dx or need_dw or need_dbias):
         raise ItoError(ITO_ERR_ARG, "no output")
-    with _On(stream):
-        dx = torch.empty((B, IC), dtype=x.dtype, device=x.device) if need_dx else None
-        dw = torch.empty((OC, IC), dtype=dw_dtype, device=x.device) if need_dw else None
-        db = torch.empty(OC, dtype=torch.float32, device=x.device) if need_dbias else None
-        n = _lib.ito_fp_linear_bwd_workspace_size(_ptr(dy), lddy, _ptr(x), ldx, _ptr(W), ldw, a, B, IC, OC)
-        ws, keep = _scratch(n, x.device)
-        ty = _type_id(x, "x")
-        _check(_lib.ito_fp_linear_bwd(_ptr(dy), lddy, _ptr(z), ldz, _ptr(x), ldx, _ptr(W), ldw, ty,
-                                      ty if dw is None else _type_id(dw, "dw_dtype"), a, B, IC, OC, ws, n, _ptr(dx),
-                                      IC, _ptr(dw), IC, _ptr(db), _stream(stream)))
+    dx = torch.empty((B, IC), dtype=dtype, device=dev) if need_dx else None
+    dw = torch.empty((OC, IC), dtype=dw_dtype or dtype, device=dev) if need_dw else None
+    db = torch.empty(OC, dtype=torch.float32, device=dev) if need_dbias else None
+    pd, px, pw = dy.data_ptr(), x.data_ptr(), W.data_ptr()
+    n = _lib.ito_fp_linear_bwd_workspace_size(pd, lddy, px, ldx, pw, ldw, a, B, IC, OC)
+    ws, keep = _scratch(n, dev)
+    ty = _type_id(x, "x")
+    _check(_lib.ito_fp_linear_bwd(pd, lddy, _addr(z), ldz, px, ldx, pw, ldw, ty,
+                                  ty if dw is None else _type_id(dw, "dw_dtype"), a, B, IC, OC, ws, n, _addr(dx), IC,
+                                  _addr(dw), IC, _addr(db), _raw_stream(dev)))
     return dx, dw, db
 
 
 def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """x [rows][cols] of float32, bfloat16 or float16 -> (y, mean float32 [rows], rstd float32 [rows])"""
+    if stream is not None:
+        return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream)
     torch = _torch()
+    dev = x.device
     ldx = _matrix(x, "x")
     rows, cols = x.shape
-    _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
-    _vector(beta, "beta", cols, (x.dtype, torch.float32))
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
-    w = gamma if gamma is not None else beta
-    with _On(stream):
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        st = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-        p = st.data_ptr()
-        _check(_lib.ito_layer_norm_fwd(_ptr(x), ldx, _type_id(x, "x"), _ptr(gamma), _ptr(beta),
-                                       ITO_F32 if w is None else _type_id(w, "gamma"), rows, cols, eps, _ptr(y), cols,
-                                       p, p + 4 * rows, _stream(stream)))
-    return y, st[0], st[1]
+    w = ITO_F32
+    if gamma is not None:
+        _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
+        w = _type_id(gamma, "gamma")
+    if beta is not None:
+        _vector(beta, "beta", cols, (x.dtype, torch.float32))
+        if gamma is not None and beta.dtype != gamma.dtype:
+            raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
+        w = _type_id(beta, "beta")
+    y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(_lib.ito_layer_norm_fwd(x.data_ptr(), ldx, _type_id(x, "x"), _addr(gamma), _addr(beta), w, rows, cols, eps,
+                                   y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev)))
+    return y, mean, rstd
 
 
 def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, stream=None):
     """-> (dx in x's type, dgamma float32 [cols], dbeta float32 [cols]); None for those not needed."""
+    if stream is not None:
+        return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream)
     torch = _torch()
+    dev = x.device
     ldx = _matrix(x, "x")
     rows, cols = x.shape
     lddy = _matrix(dy, "dy", rows, cols, x.dtype)
-    _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
+    w = ITO_F32
+    if gamma is not None:
+        _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
+        w = _type_id(gamma, "gamma")
     _vector(mean, "mean", rows, (torch.float32,))
     _vector(rstd, "rstd", rows, (torch.float32,))
-    with _On(stream):
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if need_dx else None
-        dw = torch.empty((2, cols), dtype=torch.float32, device=x.device) if need_dw else None
-        n = _lib.ito_layer_norm_bwd_workspace_size(rows, cols) if need_dw else 0
-        ws, keep = _scratch(n, x.device)
-        p = dw.data_ptr() if need_dw else None
-        _check(_lib.ito_layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _type_id(x, "x"), _ptr(gamma),
-                                       ITO_F32 if gamma is None else _type_id(gamma, "gamma"), _ptr(mean), _ptr(rstd),
-                                       rows, cols, ws, n, _ptr(dx), cols, p, p + 4 * cols if need_dw else None,
-                                       _stream(stream)))
-    return (dx, dw[0], dw[1]) if need_dw else (dx, None, None)
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=dev) if need_dx else None
+    dg = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
+    db = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
+    n = _lib.ito_layer_norm_bwd_workspace_size(rows, cols) if need_dw else 0
+    ws, keep = _scratch(n, dev)
+    _check(_lib.ito_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _type_id(x, "x"), _addr(gamma), w,
+                                   mean.data_ptr(), rstd.data_ptr(), rows, cols, ws, n, _addr(dx), cols, _addr(dg),
+                                   _addr(db), _raw_stream(dev)))
+    return dx, dg, db
 
 
 def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     """logits [rows][classes] (float32, bfloat16, float16), targets int32 [rows] or None ->
     (logp (None without targets), entropy, lse float32 [rows], top_ids int32 [rows][k], top_logp float32 [rows][k])"""
+    if stream is not None:
+        return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream)
     torch = _torch()
+    dev = logits.device
     ld = _matrix(logits, "logits")
     rows, classes = logits.shape
-    _vector(targets, "targets", rows, (torch.int32,))
-    dev = logits.device
-    with _On(stream):
-        st = torch.empty((3, rows), dtype=torch.float32, device=dev)
-        ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
-        top = torch.empty((rows, k), dtype=torch.float32, device=dev)
-        p = st.data_ptr()
-        _check(_lib.ito_token_logprobs_fwd(_ptr(logits), ld, _type_id(logits, "logits"), _ptr(targets), rows, classes,
-                                           k, None if targets is None else p, p + 4 * rows, p + 8 * rows, _ptr(ids),
-                                           _ptr(top), _stream(stream)))
-    return (None if targets is None else st[0]), st[1], st[2], ids, top
+    if targets is not None:
+        _vector(targets, "targets", rows, (torch.int32,))
+    logp, entropy, lse = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind()
+    ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
+    top = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    _check(_lib.ito_token_logprobs_fwd(logits.data_ptr(), ld, _type_id(logits, "logits"), _addr(targets), rows, classes,
+                                       k, None if targets is None else logp.data_ptr(), entropy.data_ptr(),
+                                       lse.data_ptr(), ids.data_ptr(), top.data_ptr(), _raw_stream(dev)))
+    return (None if targets is None else logp), entropy, lse, ids, top
 
 
 def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy=None, out=None, stream=None):
     """-> dlogits in the logits' type (out: a tensor to write it to, which may be the logits)."""
+    if stream is not None:
+        return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream)
     torch = _torch()
+    dev = logits.device
     ld = _matrix(logits, "logits")
     rows, classes = logits.shape
+    f32 = (torch.float32,)
     _vector(targets, "targets", rows, (torch.int32,))
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (g_logp, "g_logp"), (g_entropy, "g_entropy")):
-        _vector(t, name, rows, (torch.float32,))
-    with _On(stream):
-        d = torch.empty((rows, classes), dtype=logits.dtype, device=logits.device) if out is None else out
-        ldd = _matrix(d, "out", rows, classes, logits.dtype)
-        _check(_lib.ito_token_logprobs_bwd(_ptr(logits), ld, _type_id(logits, "logits"), _ptr(targets), _ptr(lse),
-                                           _ptr(entropy), rows, classes, _ptr(g_logp), _ptr(g_entropy), _ptr(d), ldd,
-                                           _stream(stream)))
+    _vector(lse, "lse", rows, f32)
+    _vector(entropy, "entropy", rows, f32)
+    _vector(g_logp, "g_logp", rows, f32)
+    _vector(g_entropy, "g_entropy", rows, f32)
+    d = torch.empty((rows, classes), dtype=logits.dtype, device=dev) if out is None else out
+    ldd = classes if out is None else _matrix(d, "out", rows, classes, logits.dtype)
+    _check(_lib.ito_token_logprobs_bwd(logits.data_ptr(), ld, _type_id(logits, "logits"), _addr(targets),
+                                       lse.data_ptr(), _addr(entropy), rows, classes, _addr(g_logp), _addr(g_entropy),
+                                       d.data_ptr(), ldd, _raw_stream(dev)))
     return d
 
 
@@ -1077,24 +1109,29 @@ class AdamW:
         """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16)."""
         if len(grads) != self._n:
             raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
-        self._dense(grads, grads[0].dtype, self._sizes, "grads")
+        dtype = grads[0].dtype
+        for g, n in zip(grads, self._sizes):
+            if g.numel() != n or g.dtype != dtype or not g.is_cuda or not g.is_contiguous():
+                self._dense(grads, dtype, self._sizes, "grads")     # says which and why
         self._fields["g"] = [g.data_ptr() for g in grads]
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
                         _type_id(grads[0], "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
-        _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), _stream(stream)))
+        s = _raw_stream(self.weights[0].device) if stream is None else stream.cuda_stream
+        _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), s))
         self.steps += 1
 
     def moments(self, dtype=None, stream=None):
         """The moments' values (m, v), the tensors' one after another: bfloat16 (exact; default)
         or float32 for 8-bit states, float32 for 32-bit ones."""
+        if stream is not None:
+            return _on_stream(lambda: self.moments(dtype), stream)
         torch = _torch()
-        with _On(stream):
-            if self.bits == 32:
-                return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)
-            dtype = dtype or torch.bfloat16
-            dev = self.weights[0].device
-            m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
-            if self.total:
-                _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(m, "dtype"), _ptr(m), _ptr(v),
-                                              _stream(stream)))
+        if self.bits == 32:
+            return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)
+        dtype = dtype or torch.bfloat16
+        dev = self.weights[0].device
+        m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
+        if self.total:
+            _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(m, "dtype"), m.data_ptr(), v.data_ptr(),
+                                          _raw_stream(dev)))
         return m, v

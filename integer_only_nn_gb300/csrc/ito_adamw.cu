@@ -62,9 +62,16 @@ struct AdamConst {
 
 // A 32-bit mix (multiply, fold the high half down; the multipliers are the fractional parts
 // of the square roots of 2, 3 and 11): the low 20 bits round m, another 20 round v.
-__device__ __forceinline__ void round_bits(uint32_t key, int64_t i, uint32_t& um, uint32_t& uv)
+constexpr uint32_t kMixIndex = 0x6A09E667u;
+
+// the element's index and the key, mixed: linear in the index's low half
+__device__ __forceinline__ uint32_t round_key(uint32_t key, int64_t i)
 {
-    uint32_t h = (uint32_t)i * 0x6A09E667u + (uint32_t)((uint64_t)i >> 32) * 0xBB67AE85u + key;
+    return (uint32_t)i * kMixIndex + (uint32_t)((uint64_t)i >> 32) * 0xBB67AE85u + key;
+}
+
+__device__ __forceinline__ void round_bits(uint32_t h, uint32_t& um, uint32_t& uv)
+{
     h ^= h >> 16;
     h *= 0xBB67AE85u;
     h ^= h >> 15;
@@ -74,13 +81,15 @@ __device__ __forceinline__ void round_bits(uint32_t key, int64_t i, uint32_t& um
     uv = (h * 0x510E527Fu) >> 12;
 }
 
+// the value of byte j of four codes under the exponent e (not -128)
 template <bool SECOND>
-__device__ __forceinline__ float moment_value(uint32_t code, int e)
+__device__ __forceinline__ float moment_value(uint32_t codes, int j, int e)
 {
-    const uint32_t mag = SECOND ? code : code & 127u;
-    float r = mag ? __uint_as_float(((uint32_t)(e + (SECOND ? 96 : 112)) << 23) + (mag << 20)) : 0.0f;
-    if (!SECOND && code >= 128u) r = -r;
-    return e == -128 ? __uint_as_float(0x7FC00000u) : r;
+    // the byte at the top of a word, moved down to the exponent's and mantissa's place
+    const uint32_t c = codes << (24 - 8 * j);
+    const uint32_t mag = SECOND ? c >> 4 & 0x0FF00000u : c >> 4 & 0x07F00000u;
+    const uint32_t r = mag ? mag + ((uint32_t)(e + (SECOND ? 96 : 112)) << 23) : 0u;
+    return __uint_as_float(SECOND ? r : r | (c & 0x80000000u));
 }
 
 // the shared exponent of a block whose largest magnitude has these bits
@@ -92,15 +101,17 @@ __device__ __forceinline__ int moment_exponent(uint32_t top)
     return max(e, SECOND ? -95 : -111);
 }
 
+// The code of x under the exponent e: its bits, counted from the lowest binade, plus a random
+// part of the step that is cut off. Below the lowest binade the count is negative and the code
+// 0, or 1 for a v above zero.
 template <bool SECOND>
 __device__ __forceinline__ uint32_t moment_code(float x, int e, uint32_t u)
 {
-    if (e == -128) return 0u;
-    const uint32_t bits = __float_as_uint(x), mag = bits & 0x7FFFFFFFu;
+    const uint32_t bits = __float_as_uint(x), mag = SECOND ? bits : bits & 0x7FFFFFFFu;
     const int t = (int)min(mag, 0x7F700000u) - ((e + (SECOND ? 96 : 112)) << 23);
-    uint32_t c = t >= 0 ? ((uint32_t)t + u) >> 20 : 0u;
-    if (SECOND) return mag ? max(c, 1u) : 0u;
-    return c && bits != mag ? c + 128u : c;
+    const int c = (t + (int)u) >> 20;
+    if (SECOND) return (uint32_t)max(c, (int)min(mag, 1u));
+    return c > 0 ? (uint32_t)c | (bits >> 24 & 128u) : 0u;
 }
 
 // ------------------------------------------------------------------- the step
@@ -142,10 +153,10 @@ struct AdamPiece {
                 g[0] = q.x; g[1] = q.y; g[2] = q.z; g[3] = q.w;
             } else {
                 const uint2 q = __ldcs(reinterpret_cast<const uint2*>(gp + i));
-                g[0] = to_f32(Vec<G>::lane16(q.x, 0));
-                g[1] = to_f32(Vec<G>::lane16(q.x, 1));
-                g[2] = to_f32(Vec<G>::lane16(q.y, 0));
-                g[3] = to_f32(Vec<G>::lane16(q.y, 1));
+                g[0] = Vec<G>::lane16(q.x, 0);
+                g[1] = Vec<G>::lane16(q.x, 1);
+                g[2] = Vec<G>::lane16(q.y, 0);
+                g[3] = Vec<G>::lane16(q.y, 1);
             }
             if (BITS == 32) {
                 m32 = *reinterpret_cast<const float4*>(static_cast<const float*>(e.m) + i);
@@ -184,31 +195,48 @@ struct AdamPiece {
         if (BITS == 32) {
             m[0] = m32.x; m[1] = m32.y; m[2] = m32.z; m[3] = m32.w;
             v[0] = v32.x; v[1] = v32.y; v[2] = v32.z; v[3] = v32.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[j] = moment_value<false>(m8, j, em);
+                v[j] = moment_value<true>(v8, j, ev);
+            }
+            if (em == -128 || ev == -128) {
+                // a NaN block; elements beyond the tensor's end are not to reach the maxima
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = at(b, lane, j) < end;
+                    if (em == -128) m[j] = in ? __uint_as_float(0x7FC00000u) : 0.0f;
+                    if (ev == -128) v[j] = in ? __uint_as_float(0x7FC00000u) : 0.0f;
+                }
+            }
         }
         uint32_t tm = 0, tv = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (BITS == 8) {
-                // beyond the tensor's end the codes are 0; a NaN block's are not to reach the maxima
-                const bool in = at(b, lane, j) < end;
-                m[j] = in ? moment_value<false>((m8 >> (8 * j)) & 255u, em) : 0.0f;
-                v[j] = in ? moment_value<true>((v8 >> (8 * j)) & 255u, ev) : 0.0f;
-            }
             adam_element(k, e.decay, g[j], wf[j], m[j], v[j]);
             tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
             tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
         }
         if (BITS == 8) {
-            em = moment_exponent<false>(__reduce_max_sync(0xffffffffu, tm));
-            ev = moment_exponent<true>(__reduce_max_sync(0xffffffffu, tv));
-            m8 = v8 = 0u;
+            tm = __reduce_max_sync(0xffffffffu, tm);
+            tv = __reduce_max_sync(0xffffffffu, tv);
+            em = moment_exponent<false>(tm);
+            ev = moment_exponent<true>(tv);
+            const uint32_t h0 = round_key(k.key + e.salt, b);
+            uint32_t mc[4], vc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t um, uv;
-                round_bits(k.key + e.salt, at(b, lane, j), um, uv);
-                m8 |= moment_code<false>(m[j], em, um) << (8 * j);
-                v8 |= moment_code<true>(v[j], ev, uv) << (8 * j);
+                // (the low half of the element's index is below its block's end: no carry)
+                round_bits(h0 + (uint32_t)(VEC ? lane * 4 + j : j * 32 + lane) * kMixIndex, um, uv);
+                mc[j] = moment_code<false>(m[j], em, um);
+                vc[j] = moment_code<true>(v[j], ev, uv);
             }
+            m8 = mc[0] | mc[1] << 8 | mc[2] << 16 | mc[3] << 24;
+            v8 = vc[0] | vc[1] << 8 | vc[2] << 16 | vc[3] << 24;
+            if (em == -128) m8 = 0u;
+            if (ev == -128) v8 = 0u;
             if (lane == 0) {
                 e.m_exp[b / kAdamBlock] = (int8_t)em;
                 e.v_exp[b / kAdamBlock] = (int8_t)ev;
@@ -281,6 +309,12 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
     else adam_chunk<G, C, BITS, false, 1>(e, k, base, end);
 }
 
+template <bool SECOND>
+__device__ __forceinline__ float moment_or_nan(uint32_t codes, int j, int e)
+{
+    return e == -128 ? __uint_as_float(0x7FC00000u) : moment_value<SECOND>(codes, j, e);
+}
+
 // The values of 8-bit moments, the tensors one after another in m_out and v_out.
 struct MomentEntry {
     const uint8_t* m;
@@ -328,8 +362,8 @@ __global__ void __launch_bounds__(kAdamThreads)
             float mf[4], vf[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                mf[j] = moment_value<false>((m >> (8 * j)) & 255u, em);
-                vf[j] = moment_value<true>((v >> (8 * j)) & 255u, ev);
+                mf[j] = moment_or_nan<false>(m, j, em);
+                vf[j] = moment_or_nan<true>(v, j, ev);
             }
             if (m_out) store_four(m_out + e.out + i, mf);
             if (v_out) store_four(v_out + e.out + i, vf);
@@ -337,8 +371,8 @@ __global__ void __launch_bounds__(kAdamThreads)
         return;
     }
     for (int64_t i = base + threadIdx.x; i < end; i += kAdamThreads) {
-        if (m_out) m_out[e.out + i] = from_f32<O>(moment_value<false>(e.m[i], e.m_exp[i / kAdamBlock]));
-        if (v_out) v_out[e.out + i] = from_f32<O>(moment_value<true>(e.v[i], e.v_exp[i / kAdamBlock]));
+        if (m_out) m_out[e.out + i] = from_f32<O>(moment_or_nan<false>(e.m[i], 0, e.m_exp[i / kAdamBlock]));
+        if (v_out) v_out[e.out + i] = from_f32<O>(moment_or_nan<true>(e.v[i], 0, e.v_exp[i / kAdamBlock]));
     }
 }
 

@@ -2,6 +2,8 @@
 // beside the integer layers): element types, conversions, vector loads and block sums.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "ito_device.cuh"
@@ -48,8 +50,8 @@ struct Vec {
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = to_f32(lane16(w[i], 0));
-                v[2 * i + 1] = to_f32(lane16(w[i], 1));
+                v[2 * i] = lane16(w[i], 0);
+                v[2 * i + 1] = lane16(w[i], 1);
             }
         }
     }
@@ -65,16 +67,36 @@ struct Vec {
         }
         raw = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ T lane16(uint32_t w, int hi)
+    // the low or the high half of a word as a 32-bit float, and two of them as a word
+    static __device__ __forceinline__ float lane16(uint32_t w, int hi)
     {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(hi ? w & 0xFFFF0000u : w << 16);
         const uint16_t h = hi ? (uint16_t)(w >> 16) : (uint16_t)w;
-        return *reinterpret_cast<const T*>(&h);
+        return to_f32(*reinterpret_cast<const T*>(&h));
     }
     static __device__ __forceinline__ uint32_t pair16(float lo, float hi)
     {
-        const T a = from_f32<T>(lo), b = from_f32<T>(hi);
-        return (uint32_t)*reinterpret_cast<const uint16_t*>(&a) |
-               (uint32_t)*reinterpret_cast<const uint16_t*>(&b) << 16;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+            return *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+            const __half2 v = __floats2half2_rn(lo, hi);
+            return *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    // the first element; the others move up
+    __device__ __forceinline__ float take_first()
+    {
+        float r;
+        if constexpr (sizeof(T) == 4) {
+            r = __uint_as_float(raw.x);
+            raw = make_uint4(raw.y, raw.z, raw.w, 0u);
+        } else {
+            r = lane16(raw.x, 0);
+            raw = make_uint4(__funnelshift_r(raw.x, raw.y, 16), __funnelshift_r(raw.y, raw.z, 16),
+                             __funnelshift_r(raw.z, raw.w, 16), raw.w >> 16);
+        }
+        return r;
     }
     // elements c .. c + kPer - 1 of a row of n, 0 beyond it; vec: the row starts on 16 bytes
     // (c is a multiple of kPer)
@@ -138,6 +160,18 @@ __device__ __forceinline__ float warp_sum(float v)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// ------------------------------------------------------------------ bulk copies
+//
+// `bytes` (a multiple of 16) from global to shared memory by the copy engine, both on 16-byte
+// boundaries, completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
 }
 
 inline int launch_status(const char* what)

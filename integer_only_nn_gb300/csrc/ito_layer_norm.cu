@@ -26,23 +26,45 @@ constexpr int kLnMostThreads = 1024;
 constexpr int ln_threads(int vpt) { return vpt == 1 ? 256 : vpt == 2 ? 512 : kLnMostThreads; }
 constexpr int ln_bwd_threads(int vpt) { return vpt == 1 ? 256 : 512; }
 
+// The warp's sums of N values (a power of two) in every lane's v[0], value (lane * N) / 32: each
+// exchange halves the values a lane carries, so that N sums take N + 3 or so exchanges, not 5 N.
+template <int N, int M>
+__device__ __forceinline__ void fold_sums(float (&v)[N])
+{
+    constexpr int o = 16 * M / N;
+    const bool high = threadIdx.x & o;
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) {
+        const float keep = high ? v[i + M / 2] : v[i], give = high ? v[i] : v[i + M / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+    if constexpr (M > 2) fold_sums<N, M / 2>(v);
+}
+
 // Sums R values over the threads of a row: lanes of a warp (tpr <= 32) or the block. `red` holds
 // two banks of R * 32 floats; the caller alternates them, so that one barrier is enough.
 template <int R>
 __device__ __forceinline__ void row_sums(float (&v)[R], int tpr, float* red)
 {
-    const int top = tpr < 32 ? tpr : 32;
+    if (tpr <= 32) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        for (int o = top >> 1; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
-    if (tpr <= 32) return;
+        for (int r = 0; r < R; ++r)
+            for (int o = tpr >> 1; o > 0; o >>= 1) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
+    if constexpr (R > 1) fold_sums<R, R>(v);
 #pragma unroll
-        for (int r = 0; r < R; ++r) red[r * 32 + warp] = v[r];
+    for (int o = 16 / R; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    if (lane % (32 / R) == 0) red[lane / (32 / R) * 32 + warp] = v[0];
     __syncthreads();
+    int top = 2;                         // the warps' number, to the next power of two
+    while (top < warps) top *= 2;
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = warp_sum(lane < warps ? red[r * 32 + lane] : 0.0f);
+    for (int r = 0; r < R; ++r) v[r] = (lane & (top - 1)) < warps ? red[r * 32 + (lane & (top - 1))] : 0.0f;
+    for (int o = top >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
 }
 
 // N weights from column c, a multiple of N (`fill` where there are none)
@@ -378,6 +400,281 @@ __global__ void __launch_bounds__(256)
     part[((int64_t)blockIdx.y * 2 + 1) * cols + c] = sb;
 }
 
+// ------------------------------------------------------------- a ring of rows
+//
+// Many long FULL rows: a block walks over groups of R rows that the copy engine brings into a
+// ring of stages in shared memory, so that the loads in flight (about 100 KB a block) do not
+// depend on registers or on how far the block is in its sums. A stage is free once every
+// thread has its part in registers, which the barrier of the row's sums tells. Per element two
+// conversions and five or six packed operations remain; with one element to an instruction
+// (26 of them) the forward pass took 45 us at 8192 x 4096 bf16, bound by issue.
+//
+// A wait that runs out (mbar_wait) leaves a wrong result and ITO_ERR_TIMEOUT; later waits
+// return at once, and every thread still passes every barrier.
+struct LnRing {
+    int stages;
+    uint32_t row_bytes;
+};
+
+template <int N>
+__device__ __forceinline__ float2 pair_of(const float (&v)[N], int i) { return make_float2(v[2 * i], v[2 * i + 1]); }
+
+template <typename T, int VPT, int R>
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512)
+    k_layer_norm_fwd_ring(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
+                          const void* __restrict__ beta, int w_type, int64_t rows, int cols, float eps,
+                          T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
+                          LnRing ring, int* __restrict__ err)
+{
+    constexpr int PER = Vec<T>::kPer;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][R * 32];
+    __shared__ uint64_t full[16];
+    __shared__ int abort_flag;
+    const int at = threadIdx.x, tpr = blockDim.x;
+    if (at == 0) {
+        for (int s = 0; s < ring.stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t groups = (rows + R - 1) / R;
+    auto fill = [&](int64_t g, int s) {
+        if (g >= groups) return;
+        const int n = (int)min((int64_t)R, rows - g * R);
+        mbar_arrive_expect_tx(&full[s], n * ring.row_bytes);
+        for (int r = 0; r < n; ++r)
+            bulk_load(smem + (s * R + r) * ring.row_bytes, x + (g * R + r) * ldx, ring.row_bytes, &full[s]);
+    };
+    if (at == 0)
+        for (int s = 0; s < ring.stages; ++s) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
+    // a thread's columns stay the same: gamma and beta are registers, where there are enough
+    constexpr bool KEEP = VPT <= 2;
+    float g[KEEP ? VPT : 1][PER], b[KEEP ? VPT : 1][PER];
+    if (KEEP)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            load_weights<true>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[KEEP ? i : 0]);
+            load_weights<true>(beta, w_type, (i * tpr + at) * PER, cols, 0.0f, b[KEEP ? i : 0]);
+        }
+    const float inv = 1.0f / (float)cols;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x) {
+        mbar_wait(&full[stage], phase, &abort_flag, err);
+        float f[R][VPT][PER], mu[R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                Vec<T> v;
+                v.raw = make_uint4(0u, 0u, 0u, 0u);
+                if (c < cols)
+                    v.raw = *reinterpret_cast<const uint4*>(smem + (stage * R + r) * ring.row_bytes + c * sizeof(T));
+                v.get(f[r][i]);
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) s = __fadd2_rn(s, pair_of(f[r][i], j));
+            }
+            mu[r] = s.x + s.y;
+        }
+        row_sums<R>(mu, tpr, red[0]);
+        if (at == 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mu[r] *= inv;
+            float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if ((i * tpr + at) * PER >= cols) continue;
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) {
+                    const float2 d = __fadd2_rn(pair_of(f[r][i], j), make_float2(-mu[r], -mu[r]));
+                    s = __ffma2_rn(d, d, s);
+                    f[r][i][2 * j] = d.x;
+                    f[r][i][2 * j + 1] = d.y;
+                }
+            }
+            rs[r] = s.x + s.y;
+        }
+        row_sums<R>(rs, tpr, red[1]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = grp * R + r;
+            if (row >= rows) continue;
+            rs[r] = 1.0f / sqrtf(rs[r] * inv + eps);
+            if (at == 0) {
+                if (mean) mean[row] = mu[r];
+                if (rstd) rstd[row] = rs[r];
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                if (c >= cols) continue;
+                if (!KEEP) {
+                    load_weights<true>(gamma, w_type, c, cols, 1.0f, g[0]);
+                    load_weights<true>(beta, w_type, c, cols, 0.0f, b[0]);
+                }
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) {
+                    const float2 h = __fmul2_rn(pair_of(f[r][i], j), make_float2(rs[r], rs[r]));
+                    const float2 o = __ffma2_rn(h, pair_of(g[KEEP ? i : 0], j), pair_of(b[KEEP ? i : 0], j));
+                    f[r][i][2 * j] = o.x;
+                    f[r][i][2 * j + 1] = o.y;
+                }
+                Vec<T> v;
+                v.set(f[r][i]);
+                *reinterpret_cast<uint4*>(y + row * ldy + c) = v.raw;
+            }
+        }
+        if (++stage == ring.stages) { stage = 0; phase ^= 1; }
+    }
+}
+
+template <typename T, int VPT, int R>
+__global__ void __launch_bounds__(512)
+    k_layer_norm_bwd_ring(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                          const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
+                          const float* __restrict__ rstd, int64_t rows, int cols, T* __restrict__ dx, int64_t lddx,
+                          float* __restrict__ part, LnRing ring, int* __restrict__ err)
+{
+    constexpr int PER = Vec<T>::kPer;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2][2 * R * 32];
+    __shared__ uint64_t full[16];
+    __shared__ int abort_flag;
+    const int at = threadIdx.x, tpr = blockDim.x;
+    if (at == 0) {
+        for (int s = 0; s < ring.stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t groups = (rows + R - 1) / R;
+    // a stage: R rows of dy, then R rows of x
+    auto fill = [&](int64_t g, int s) {
+        if (g >= groups) return;
+        const int n = (int)min((int64_t)R, rows - g * R);
+        mbar_arrive_expect_tx(&full[s], 2 * n * ring.row_bytes);
+        for (int r = 0; r < n; ++r) {
+            bulk_load(smem + (2 * s * R + r) * ring.row_bytes, dy + (g * R + r) * lddy, ring.row_bytes, &full[s]);
+            bulk_load(smem + ((2 * s + 1) * R + r) * ring.row_bytes, x + (g * R + r) * ldx, ring.row_bytes, &full[s]);
+        }
+    };
+    if (at == 0)
+        for (int s = 0; s < ring.stages; ++s) fill(blockIdx.x + (int64_t)s * gridDim.x, s);
+    constexpr bool KEEP = VPT <= 2;
+    float g[KEEP ? VPT : 1][PER];
+    float2 sg[VPT][PER / 2], sb[VPT][PER / 2];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (KEEP) load_weights<true>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[KEEP ? i : 0]);
+#pragma unroll
+        for (int j = 0; j < PER / 2; ++j) sg[i][j] = sb[i][j] = make_float2(0.0f, 0.0f);
+    }
+    const float inv = 1.0f / (float)cols;
+    int stage = 0, bank = 0;
+    uint32_t phase = 0;
+    for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, bank ^= 1) {
+        float mu[R], rs[R], s[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = grp * R + r < rows;
+            mu[r] = in ? mean[grp * R + r] : 0.0f;
+            rs[r] = in ? rstd[grp * R + r] : 0.0f;
+        }
+        mbar_wait(&full[stage], phase, &abort_flag, err);
+        Vec<T> vd[R][VPT], vx[R][VPT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = grp * R + r < rows;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                vd[r][i].raw = vx[r][i].raw = make_uint4(0u, 0u, 0u, 0u);
+                if (in && c < cols) {
+                    vd[r][i].raw =
+                        *reinterpret_cast<const uint4*>(smem + (2 * stage * R + r) * ring.row_bytes + c * sizeof(T));
+                    vx[r][i].raw = *reinterpret_cast<const uint4*>(smem + ((2 * stage + 1) * R + r) * ring.row_bytes +
+                                                                  c * sizeof(T));
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 sa = make_float2(0.0f, 0.0f), sh = make_float2(0.0f, 0.0f);
+            const float2 rs2 = make_float2(rs[r], rs[r]), mu2 = make_float2(-mu[r], -mu[r]);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float d[PER], h[PER];
+                vd[r][i].get(d);
+                vx[r][i].get(h);
+                if (!KEEP) load_weights<true>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[0]);
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) {
+                    // beyond the rows' and the row's end dy is 0, and with it every term
+                    const float2 dd = pair_of(d, j);
+                    const float2 hh = __fmul2_rn(__fadd2_rn(pair_of(h, j), mu2), rs2);
+                    const float2 dh = __fmul2_rn(dd, hh);
+                    sg[i][j] = __fadd2_rn(sg[i][j], dh);
+                    sb[i][j] = __fadd2_rn(sb[i][j], dd);
+                    sa = __ffma2_rn(dd, pair_of(g[KEEP ? i : 0], j), sa);
+                    sh = __ffma2_rn(dh, pair_of(g[KEEP ? i : 0], j), sh);
+                }
+            }
+            s[2 * r] = sa.x + sa.y;
+            s[2 * r + 1] = sh.x + sh.y;
+        }
+        row_sums<2 * R>(s, tpr, red[bank]);
+        if (at == 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
+        if (++stage == ring.stages) { stage = 0; phase ^= 1; }
+        if (!dx) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = grp * R + r;
+            if (row >= rows) continue;
+            const float2 rs2 = make_float2(rs[r], rs[r]), mu2 = make_float2(-mu[r], -mu[r]);
+            const float2 sa = make_float2(-s[2 * r] * inv, -s[2 * r] * inv);
+            const float2 sh = make_float2(-s[2 * r + 1] * inv, -s[2 * r + 1] * inv);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = (i * tpr + at) * PER;
+                if (c >= cols) continue;
+                float d[PER], h[PER];
+                vd[r][i].get(d);
+                vx[r][i].get(h);
+                if (!KEEP) load_weights<true>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[0]);
+#pragma unroll
+                for (int j = 0; j < PER / 2; ++j) {
+                    const float2 hh = __fmul2_rn(__fadd2_rn(pair_of(h, j), mu2), rs2);
+                    const float2 o = __fmul2_rn(__ffma2_rn(hh, sh, __ffma2_rn(pair_of(d, j), pair_of(g[KEEP ? i : 0], j), sa)), rs2);
+                    d[2 * j] = o.x;
+                    d[2 * j + 1] = o.y;
+                }
+                vd[r][i].set(d);
+                *reinterpret_cast<uint4*>(dx + row * lddx + c) = vd[r][i].raw;
+            }
+        }
+    }
+    if (!part) return;
+    float* pg = part + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < PER / 2; ++j) {
+            const int c = (i * tpr + at) * PER + 2 * j;
+            if (c < cols) {
+                *reinterpret_cast<float2*>(pg + c) = sg[i][j];
+                *reinterpret_cast<float2*>(pg + cols + c) = sb[i][j];
+            }
+        }
+}
+
 // The shares' sums: a lane takes a column, a block's warps every eighth share.
 __global__ void __launch_bounds__(256)
     k_layer_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* __restrict__ dgamma,
@@ -438,6 +735,34 @@ static LnShape ln_shape(int cols, int size, int most)
     return s;
 }
 
+// The ring takes long FULL rows in numbers: `rows_each` of a stage are `loads` rows of bytes each.
+constexpr int kLnRingBytes = 100 * 1024;     // of a block of up to 256 threads: two of them to an SM
+constexpr int kLnRingRows = 4;               // rows for each SM from which the ring pays
+
+static bool ln_ring_rows(const LnShape& s, int cols, int size, int64_t rows)
+{
+    return s.vpt && s.tpr > 32 && cols % (16 / size) == 0 && rows >= (int64_t)kLnRingRows * num_sms();
+}
+
+static int ln_ring_blocks(const LnShape& s) { return s.block <= 256 ? 2 : 1; }
+
+static LnRing ln_ring(const LnShape& s, int cols, int size, int stage_rows)
+{
+    LnRing r;
+    r.row_bytes = (uint32_t)cols * size;
+    const int room = ln_ring_blocks(s) == 2 ? kLnRingBytes : 2 * kLnRingBytes;
+    r.stages = std::max(2, std::min(16, room / (int)(r.row_bytes * stage_rows)));
+    return r;
+}
+
+template <typename K>
+static int ln_ring_smem(K kern, int bytes)
+{
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
+    return ITO_OK;
+}
+
 // Blocks of the backward pass, and the shares of dgamma and dbeta they leave.
 static int ln_bwd_rows(const LnShape& s) { return s.vpt == 1 ? 4 : s.vpt == 2 ? 2 : 1; }
 
@@ -493,6 +818,26 @@ static int run_fwd(const void* xp, int64_t ldx, const void* gamma, const void* b
     const int64_t want = (rows + (int64_t)groups * R - 1) / ((int64_t)groups * R);
     const unsigned grid = (unsigned)std::min(want, most);
     const bool full = cols % Vec<T>::kPer == 0 && xv && yv && aligned_to(gamma, 16) && aligned_to(beta, 16);
+    if (full && ln_ring_rows(sh, cols, sizeof(T), rows)) {
+        const int RR = sh.vpt <= 2 ? 2 : 1;
+        const LnRing ring = ln_ring(sh, cols, sizeof(T), RR);
+        const int smem = ring.stages * RR * (int)ring.row_bytes;
+        const unsigned blocks = (unsigned)std::min<int64_t>((rows + RR - 1) / RR, (int64_t)num_sms() * ln_ring_blocks(sh));
+        int* err = device_error_word();
+        if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
+#define ITO_LN_RING(V, RN)                                                                                     \
+    do {                                                                                                       \
+        const int st = ln_ring_smem(k_layer_norm_fwd_ring<T, V, RN>, smem);                                    \
+        if (st) return st;                                                                                     \
+        launch_pdl(k_layer_norm_fwd_ring<T, V, RN>, blocks, sh.block, smem, s, x, ldx, gamma, beta, w_type, rows, \
+                   cols, eps, y, ldy, mean, rstd, ring, err);                                                  \
+    } while (0)
+        if (sh.vpt == 1) ITO_LN_RING(1, 2);
+        else if (sh.vpt == 2) ITO_LN_RING(2, 2);
+        else ITO_LN_RING(4, 1);
+#undef ITO_LN_RING
+        return launch_status("layer norm");
+    }
 #define ITO_LN_AS(V, RR, F)                                                                                       \
     launch_pdl(k_layer_norm_fwd<T, V, RR, F>, grid, sh.block, 0, s, x, ldx, xv, gamma, beta, w_type, rows, cols, \
                sh.tpr, eps, y, ldy, yv, mean, rstd)
@@ -523,7 +868,24 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
     launch_pdl(k_layer_norm_bwd<T, V, RR, F>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean, \
                rstd, rows, cols, sh.tpr, dx, lddx, dxv, share)
 #define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
-    if (sh.vpt == 1) ITO_LN(1, 4);
+#define ITO_LN_RING(V, RN)                                                                                          \
+    do {                                                                                                            \
+        const LnRing ring = ln_ring(sh, cols, sizeof(T), 2 * RN);                                                   \
+        const int smem = ring.stages * 2 * RN * (int)ring.row_bytes;                                                \
+        const int st = ln_ring_smem(k_layer_norm_bwd_ring<T, V, RN>, smem);                                         \
+        if (st) return st;                                                                                          \
+        parts = (int)std::min<int64_t>((rows + RN - 1) / RN, std::min(parts, num_sms() * ln_ring_blocks(sh)));      \
+        launch_pdl(k_layer_norm_bwd_ring<T, V, RN>, parts, sh.block, smem, s, dy, lddy, x, ldx, gamma, w_type, mean, \
+                   rstd, rows, cols, dx, lddx, share, ring, err);                                                   \
+    } while (0)
+    int parts = ln_parts(rows, cols, sizeof(T));
+    if (full && ln_ring_rows(sh, cols, sizeof(T), rows)) {
+        int* err = device_error_word();
+        if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
+        if (sh.vpt == 1) ITO_LN_RING(1, 2);
+        else if (sh.vpt == 2) ITO_LN_RING(2, 2);
+        else ITO_LN_RING(4, 1);
+    } else if (sh.vpt == 1) ITO_LN(1, 4);
     else if (sh.vpt == 2) ITO_LN(2, 2);
     else if (sh.vpt == 4) ITO_LN(4, 1);
     else {
@@ -531,14 +893,15 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
             launch_pdl(k_layer_norm_dx_long<T>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean,
                        rstd, rows, cols, dx, lddx, dxv);
         if (wgrad)
-            launch_pdl(k_layer_norm_shares_long<T>, dim3((cols + 255) / 256, ln_parts(rows, cols, sizeof(T))), 256, 0,
+            launch_pdl(k_layer_norm_shares_long<T>, dim3((cols + 255) / 256, parts), 256, 0,
                        s, dy, lddy, x, ldx, mean, rstd, rows, cols, share);
     }
 #undef ITO_LN
 #undef ITO_LN_AS
+#undef ITO_LN_RING
     if (wgrad)
         launch_pdl(k_layer_norm_wgrad, (2 * cols + 31) / 32, 256, 0, s, static_cast<const float*>(part),
-                   ln_parts(rows, cols, sizeof(T)), cols, dgamma, dbeta);
+                   parts, cols, dgamma, dbeta);
     return launch_status("layer norm");
 }
 

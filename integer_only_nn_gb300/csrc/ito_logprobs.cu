@@ -55,12 +55,6 @@ struct Sums {
         s = s != s ? s : e != 0.0f ? s * e : 0.0f;
         top = m;
     }
-    __device__ __forceinline__ void add(float x)
-    {
-        const float d = x - top, e = exp2_fast(d * kLog2e);
-        s += e;
-        t += fmaxf(d, -200.0f) * e;      // (-inf times 0 would be a NaN; a NaN reaches s)
-    }
     __device__ __forceinline__ void join(Sums o)
     {
         const float m = fmaxf(top, o.top);
@@ -71,74 +65,157 @@ struct Sums {
     }
 };
 
-// ------------------------------------------------------------- a warp's alternatives
-//
-// Lane i holds the i-th best of what the warp has seen. `low` (uniform) is the k-th: only
-// elements that come before it are looked at closer, about k ln(n / k) of n in random order.
-struct Alternatives {
-    float value;
-    int id;
-    float low;
-    int low_id;
+// A thread's sums, two elements at a time: at about nine instructions an element the forward
+// pass would be bound by their issue, not by memory.
+struct PairSums {
+    float top;
+    float2 s, t;
 
     __device__ __forceinline__ void clear()
     {
+        top = -FLT_MAX;
+        s = t = make_float2(0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void rise(float m)
+    {
+        if (!(m > top)) return;
+        Sums a{top, s.x, t.x}, b{top, s.y, t.y};
+        a.rise(m);
+        b.rise(m);
+        top = m;
+        s = make_float2(a.s, b.s);
+        t = make_float2(a.t, b.t);
+    }
+    __device__ __forceinline__ void add(float2 x)
+    {
+        const float2 d = __fadd2_rn(x, make_float2(-top, -top));
+        const float2 y = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+        s = __fadd2_rn(s, e);
+        // (-inf times 0 would be a NaN; a NaN reaches s)
+        t = __ffma2_rn(make_float2(fmaxf(d.x, -200.0f), fmaxf(d.y, -200.0f)), e, t);
+    }
+    __device__ __forceinline__ Sums total() const { return Sums{top, s.x + s.y, t.x + t.y}; }
+};
+
+// ------------------------------------------------------------- a warp's alternatives
+//
+// Lane i holds the i-th best of what the warp has taken in. Elements that come before `low` go
+// to a buffer of 64 in shared memory; 32 of them at a time are sorted and merged with the list
+// by shuffles, and its k-th best becomes `low`. The first `low` is the k-th largest of the lanes'
+// largest elements of the first round: at least k elements are no smaller, and in random order
+// few more than k of that round and of each following one come before it.
+struct Alternatives {
+    float value, low;
+    int id, low_id, count;
+    float* buf_v;
+    int* buf_i;
+
+    __device__ __forceinline__ void clear(float* v, int* i)
+    {
         value = low = -INFINITY;
         id = low_id = INT_MAX;
+        count = 0;
+        buf_v = v;
+        buf_i = i;
     }
-    __device__ __forceinline__ bool wants(float v, int i) const { return comes_before(v, i, low, low_id); }
-    // all lanes, with the same v and i
-    __device__ __forceinline__ void insert(float v, int i, int k)
+    // the k-th largest of the lanes' m (a NaN counts as lowest here)
+    __device__ __forceinline__ void first_low(float m, int k)
     {
         const int lane = threadIdx.x & 31;
-        const unsigned better = __ballot_sync(0xffffffffu, comes_before(value, id, v, i));
-        const int place = __popc(better);
-        const float pv = __shfl_up_sync(0xffffffffu, value, 1);
-        const int pi = __shfl_up_sync(0xffffffffu, id, 1);
-        if (lane == place) {
-            value = v;
-            id = i;
-        } else if (lane > place) {
-            value = pv;
-            id = pi;
+        if (m != m) m = -INFINITY;
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int j = size / 2; j > 0; j /= 2) {
+                const float o = __shfl_xor_sync(0xffffffffu, m, j);
+                m = ((lane & j) == 0) == ((lane & size) == 0) ? fmaxf(m, o) : fminf(m, o);
+            }
+        low = __shfl_sync(0xffffffffu, m, k - 1);
+        low_id = INT_MAX;
+    }
+    // (v, i) of the partner lane ^ j, if it is the better and the better is wanted, or the other way
+    static __device__ __forceinline__ void exchange(float& v, int& i, int j, bool better)
+    {
+        const float ov = __shfl_xor_sync(0xffffffffu, v, j);
+        const int oi = __shfl_xor_sync(0xffffffffu, i, j);
+        if (comes_before(v, i, ov, oi) != better) {
+            v = ov;
+            i = oi;
         }
+    }
+    // 32 sorted elements, one to a lane
+    __device__ __forceinline__ void merge(float v, int i, int k)
+    {
+        const int lane = threadIdx.x & 31;
+        const float rv = __shfl_sync(0xffffffffu, v, 31 - lane);
+        const int ri = __shfl_sync(0xffffffffu, i, 31 - lane);
+        if (comes_before(rv, ri, value, id)) {
+            value = rv;
+            id = ri;
+        }
+#pragma unroll
+        for (int j = 16; j > 0; j /= 2) exchange(value, id, j, (lane & j) == 0);
         low = __shfl_sync(0xffffffffu, value, k - 1);
         low_id = __shfl_sync(0xffffffffu, id, k - 1);
+    }
+    __device__ __forceinline__ void flush(int k)
+    {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        float v = lane < count ? buf_v[lane] : -INFINITY;
+        int i = lane < count ? buf_i[lane] : INT_MAX;
+        const float more_v = buf_v[32 + lane];
+        const int more_i = buf_i[32 + lane];
+        __syncwarp();
+        buf_v[lane] = more_v;
+        buf_i[lane] = more_i;
+        count = max(count - 32, 0);
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int j = size / 2; j > 0; j /= 2)
+                exchange(v, i, j, ((lane & j) == 0) == ((lane & size) == 0));
+        merge(v, i, k);
     }
     // all lanes, each with an element of its own (take false: none)
     __device__ __forceinline__ void offer(float v, int i, bool take, int k)
     {
-        unsigned m = __ballot_sync(0xffffffffu, take && wants(v, i));
-        while (m) {
-            const int src = __ffs(m) - 1;
-            const float cv = __shfl_sync(0xffffffffu, v, src);
-            const int ci = __shfl_sync(0xffffffffu, i, src);
-            if (wants(cv, ci)) insert(cv, ci, k);
-            m &= m - 1;
+        take = take && comes_before(v, i, low, low_id);
+        const unsigned m = __ballot_sync(0xffffffffu, take);
+        if (!m) return;
+        const int at = count + __popc(m & ((1u << (threadIdx.x & 31)) - 1u));
+        if (take) {
+            buf_v[at] = v;
+            buf_i[at] = i;
         }
+        count += __popc(m);
+        if (count >= 32) flush(k);
     }
 };
 
 // Elements [begin, end) of a row for thread `at` of `threads`: UNROLL vectors in flight. A
-// vector's elements are `skip` apart: neighbours (vec; begin on 16 bytes) or a warp's width
+// vector's elements are `skip` apart: neighbours (VEC; begin on 16 bytes) or a warp's width
 // apart, where rows start anywhere and a warp's single loads are still consecutive.
-template <typename T, bool TOP>
-__device__ __forceinline__ void scan_part(const T* __restrict__ row, int begin, int end, int at, int threads, bool vec,
-                                          int k, Sums& sums, Alternatives& alt)
+template <typename T, bool TOP, bool VEC>
+__device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, int end, int at, int threads, int k,
+                                          Alternatives& alt)
 {
     constexpr int PER = Vec<T>::kPer, UNROLL = 4;
+    constexpr int skip = VEC ? 1 : 32;
     const int lane = threadIdx.x & 31;
-    const int skip = vec ? 1 : 32;
-    const int64_t round = (int64_t)threads * PER * UNROLL;
+    const int round = threads * PER * UNROLL;
+    PairSums sums;
+    sums.clear();
     for (int64_t base = begin; base < end; base += round) {
         Vec<T> v[UNROLL];
         int first[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const int64_t block = base + ((int64_t)u * threads + (at - lane)) * PER;     // the warp's elements
-            const int64_t c = block + (vec ? lane * PER : lane);
+            const int64_t block = base + (u * threads + (at - lane)) * PER;     // the warp's elements
+            const int64_t c = block + (VEC ? lane * PER : lane);
             first[u] = (int)(c < end ? c : end);
-            if (vec && c + PER <= end) {
+            if (VEC && c + PER <= end) {
                 v[u].raw = __ldg(reinterpret_cast<const uint4*>(row + c));
             } else {
                 float f[PER];
@@ -147,28 +224,51 @@ __device__ __forceinline__ void scan_part(const T* __restrict__ row, int begin, 
                 v[u].set(f);             // exact: the values came from T
             }
         }
+        float most[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             float f[PER];
             v[u].get(f);
-            float m = f[0];
+            most[u] = f[0];
 #pragma unroll
-            for (int j = 1; j < PER; ++j) m = fmaxf(m, f[j]);
-            sums.rise(m);
+            for (int j = 1; j < PER; ++j) most[u] = fmaxf(most[u], f[j]);
+        }
+        const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+        sums.rise(m);
+        if (TOP && base == begin) alt.first_low(m, k);
+        unsigned pending = 0;            // vectors with an element to look at closer, in any lane
 #pragma unroll
-            for (int j = 0; j < PER; ++j) sums.add(f[j]);
+        for (int u = 0; u < UNROLL; ++u) {
+            float f[PER];
+            v[u].get(f);
+#pragma unroll
+            for (int j = 0; j < PER; j += 2) sums.add(make_float2(f[j], f[j + 1]));
             if (TOP) {
-                // beyond the end the elements are -inf: there may be none better than that
-                bool look = m > alt.low || (m == alt.low && first[u] < alt.low_id);
+                // a NaN is not in `most`, but it is in the sum; beyond the end nothing is offered
+                const bool look = most[u] >= alt.low || sums.s.x != sums.s.x || sums.s.y != sums.s.y;
+                if (__any_sync(0xffffffffu, look && first[u] < end)) pending |= 1u << u;
+            }
+        }
+        // one copy of this in the code: unrolled, its sorts would not fit the instruction cache
+        while (TOP && pending) {
+            const int u = __ffs(pending) - 1;
+            pending &= pending - 1;
+            Vec<T> w = v[0];
+            int c = first[0];
 #pragma unroll
-                for (int j = 0; j < PER; ++j) look |= f[j] != f[j];
-                if (__any_sync(0xffffffffu, look && first[u] < end)) {
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) alt.offer(f[j], first[u] + j * skip, first[u] + j * skip < end, k);
+            for (int q = 1; q < UNROLL; ++q)
+                if (u == q) {
+                    w = v[q];
+                    c = first[q];
                 }
+#pragma unroll 1
+            for (int j = 0; j < PER; ++j, c += skip) {
+                alt.offer(w.take_first(), c, c < end, k);
             }
         }
     }
+    if (TOP && alt.count) alt.flush(k);
+    return sums.total();
 }
 
 struct LpOut {
@@ -210,19 +310,20 @@ __device__ __forceinline__ Sums warp_join(Sums a)
 }
 
 // Short rows: a warp to a row.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpWarps * 32)
-    k_logprobs_short(const T* __restrict__ x, int64_t ld, int vec, const int32_t* __restrict__ targets, int64_t rows,
+template <typename T, bool TOP, bool VEC>
+__global__ void __launch_bounds__(kLpWarps * 32, 3)
+    k_logprobs_short(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
                      int classes, int k, const LpOut o, int* __restrict__ err)
 {
+    __shared__ float buf_v[kLpWarps][TOP ? 64 : 1];
+    __shared__ int buf_i[kLpWarps][TOP ? 64 : 1];
     griddep_wait();
     griddep_launch_dependents();
     const int64_t step = (int64_t)gridDim.x * kLpWarps;
     for (int64_t r = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5); r < rows; r += step) {
-        Sums a{-FLT_MAX, 0.0f, 0.0f};
         Alternatives alt;
-        alt.clear();
-        scan_part<T, TOP>(x + r * ld, 0, classes, threadIdx.x & 31, 32, vec, k, a, alt);
+        alt.clear(buf_v[threadIdx.x >> 5], buf_i[threadIdx.x >> 5]);
+        const Sums a = scan_part<T, TOP, VEC>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt);
         write_row<T, TOP>(x + r * ld, targets, r, classes, k, warp_join(a), alt, o, err);
     }
 }
@@ -230,25 +331,23 @@ __global__ void __launch_bounds__(kLpWarps * 32)
 // Longer rows: a cluster of blocks to a row (of one block, where there are rows enough), each
 // with a stretch of it. The warps' sums and alternatives meet in their block's shared memory, the
 // blocks' in the first one's, read across the cluster.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpWarps * 32)
-    k_logprobs_long(const T* __restrict__ x, int64_t ld, int vec, const int32_t* __restrict__ targets, int64_t rows,
+template <typename T, bool TOP, bool VEC>
+__global__ void __launch_bounds__(kLpWarps * 32, 3)
+    k_logprobs_long(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
                     int classes, int k, int parts, int stretch, const LpOut o, int* __restrict__ err)
 {
     __shared__ Sums sums[kLpWarps];
-    __shared__ float values[kLpWarps][kLpMaxTop];
-    __shared__ int ids[kLpWarps][kLpMaxTop];
+    __shared__ float buf_v[kLpWarps][TOP ? 64 : 1], values[kLpWarps][TOP ? kLpMaxTop : 1];
+    __shared__ int buf_i[kLpWarps][TOP ? 64 : 1], ids[kLpWarps][TOP ? kLpMaxTop : 1];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = parts > 1 ? (int)cluster_ctarank() : 0;
     const int begin = min(classes, part * stretch), end = min(classes, begin + stretch);
     for (int64_t r = blockIdx.x / parts; r < rows; r += gridDim.x / parts) {
-        Sums a{-FLT_MAX, 0.0f, 0.0f};
         Alternatives alt;
-        alt.clear();
-        scan_part<T, TOP>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, vec, k, a, alt);
-        a = warp_join(a);
+        alt.clear(buf_v[warp], buf_i[warp]);
+        Sums a = warp_join(scan_part<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt));
         if (lane == 0) sums[warp] = a;
         if (TOP) {
             values[warp][lane] = alt.value;
@@ -259,7 +358,8 @@ __global__ void __launch_bounds__(kLpWarps * 32)
             a = lane < kLpWarps ? sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
             a = warp_join(a);
             if (TOP)
-                for (int w = 1; w < kLpWarps; ++w) alt.offer(values[w][lane], ids[w][lane], lane < k, k);
+#pragma unroll 1
+                for (int w = 1; w < kLpWarps; ++w) alt.merge(values[w][lane], ids[w][lane], k);
         }
         if (parts > 1) {
             if (warp == 0) {
@@ -271,6 +371,7 @@ __global__ void __launch_bounds__(kLpWarps * 32)
             }
             cluster_sync();
             if (part == 0 && warp == 0) {
+#pragma unroll 1
                 for (int p = 1; p < parts; ++p) {
                     const uint32_t sa = mapa_shared(smem_u32(&sums[0]), p);
                     Sums q;
@@ -285,7 +386,7 @@ __global__ void __launch_bounds__(kLpWarps * 32)
                                      : "=f"(v) : "r"(mapa_shared(smem_u32(&values[0][lane]), p)) : "memory");
                         asm volatile("ld.shared::cluster.s32 %0, [%1];"
                                      : "=r"(i) : "r"(mapa_shared(smem_u32(&ids[0][lane]), p)) : "memory");
-                        alt.offer(v, i, lane < k, k);
+                        alt.merge(v, i, k);
                     }
                 }
             }
@@ -324,10 +425,18 @@ __device__ __forceinline__ float lp_slope(const LpRow& w, float x, int c)
     return d;
 }
 
+// (rare: kept out of the main path's registers)
+template <typename T>
+__device__ __noinline__ Sums sums_again(const T* row, int classes, int at, int threads)
+{
+    Alternatives none;
+    return warp_join(scan_part<T, false, false>(row, 0, classes, at, threads, 0, none));
+}
+
 constexpr int kLpStretch = 8192;     // elements of a row that a block takes, at most
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     k_logprobs_bwd(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets,
                    const float* __restrict__ lse, const float* __restrict__ entropy, int64_t rows, int classes,
                    const float* __restrict__ g_logp, const float* __restrict__ g_entropy, T* __restrict__ dx,
@@ -358,10 +467,7 @@ __global__ void __launch_bounds__(256)
         const T* xr = x + r * ld;
         T* dr = dx + r * ldd;
         if (fabsf(z) >= kLpFar && fabsf(z) < INFINITY && (stretches == 1 || dx != x)) {
-            Sums a{-FLT_MAX, 0.0f, 0.0f};
-            Alternatives none;
-            scan_part<T, false>(xr, 0, classes, at, threads, false, 0, a, none);
-            a = warp_join(a);
+            Sums a = sums_again(xr, classes, at, threads);
             if (!per_warp) {
                 __syncthreads();         // (the row is the block's: every thread is here)
                 if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = a;
@@ -425,18 +531,17 @@ static int check_lp(const void* x, int64_t ld, int type, int64_t rows, int class
     return ITO_OK;
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, bool VEC>
 static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
                    const LpOut& o, int* err, cudaStream_t s)
 {
     const T* x = static_cast<const T*>(xp);
-    const int vec = rows_vec(x, ld, sizeof(T), rows);
     const int sms = num_sms();
     // a warp to a row up to four rounds of its loads, or where warps of whole rows fill the device
     const int round = 32 * Vec<T>::kPer * 4;
     if (classes <= round || (classes <= 4 * round && rows >= 16 * sms)) {
         const int64_t want = (rows + kLpWarps - 1) / kLpWarps, most = (int64_t)sms * 8;
-        launch_pdl(k_logprobs_short<T, TOP>, (unsigned)std::min(want, most), kLpWarps * 32, 0, s, x, ld, vec, targets,
+        launch_pdl(k_logprobs_short<T, TOP, VEC>, (unsigned)std::min(want, most), kLpWarps * 32, 0, s, x, ld, targets,
                    rows, classes, k, o, err);
         return launch_status("log probabilities");
     }
@@ -458,7 +563,7 @@ static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t r
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = parts > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP>, x, ld, vec, targets, rows, classes, k, parts,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP, VEC>, x, ld, targets, rows, classes, k, parts,
                                              stretch, o, err);
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "log probabilities launch: %s", cudaGetErrorString(e));
 }
@@ -467,8 +572,12 @@ template <typename T>
 static int run_fwd_any(const void* x, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
                        const LpOut& o, int* err, cudaStream_t s)
 {
-    if (k) return run_fwd<T, true>(x, ld, targets, rows, classes, k, o, err, s);
-    return run_fwd<T, false>(x, ld, targets, rows, classes, k, o, err, s);
+    if (rows_vec(x, ld, sizeof(T), rows)) {
+        if (k) return run_fwd<T, true, true>(x, ld, targets, rows, classes, k, o, err, s);
+        return run_fwd<T, false, true>(x, ld, targets, rows, classes, k, o, err, s);
+    }
+    if (k) return run_fwd<T, true, false>(x, ld, targets, rows, classes, k, o, err, s);
+    return run_fwd<T, false, false>(x, ld, targets, rows, classes, k, o, err, s);
 }
 
 template <typename T>
