@@ -781,8 +781,9 @@ int ito_fp_linear_fwd(const void *x, int64_t ldx, const void *W, int64_t ldw, co
                       void *workspace, size_t workspace_bytes, void *z, int64_t ldz, void *y, int64_t ldy,
                       void *stream);
 
-/* Bytes of device workspace ito_fp_linear_bwd needs (0 on invalid sizes): dz,
- * the bias gradient's partial sums, and what the forward pass's takes. */
+/* Bytes of device workspace ito_fp_linear_bwd needs (0 on invalid sizes, and
+ * where none is needed): dz, where an activation or an alignment asks for one, and what the
+ * forward pass's takes. */
 size_t ito_fp_linear_bwd_workspace_size(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *W,
                                         int64_t ldw, int act, int B, int IC, int OC);
 

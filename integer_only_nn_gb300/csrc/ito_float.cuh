@@ -84,20 +84,6 @@ struct Vec {
             return *reinterpret_cast<const uint32_t*>(&v);
         }
     }
-    // the first element; the others move up
-    __device__ __forceinline__ float take_first()
-    {
-        float r;
-        if constexpr (sizeof(T) == 4) {
-            r = __uint_as_float(raw.x);
-            raw = make_uint4(raw.y, raw.z, raw.w, 0u);
-        } else {
-            r = lane16(raw.x, 0);
-            raw = make_uint4(__funnelshift_r(raw.x, raw.y, 16), __funnelshift_r(raw.y, raw.z, 16),
-                             __funnelshift_r(raw.z, raw.w, 16), raw.w >> 16);
-        }
-        return r;
-    }
     // elements c .. c + kPer - 1 of a row of n, 0 beyond it; vec: the row starts on 16 bytes
     // (c is a multiple of kPer)
     __device__ __forceinline__ void load(const T* row, int c, int n, bool vec)

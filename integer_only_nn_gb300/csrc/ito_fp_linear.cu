@@ -122,85 +122,126 @@ __global__ void __launch_bounds__(256)
             dst[r * ldd + c] = src[r * ld + c];
 }
 
-// dz = dy act'(z), rounded to the operands' type (dz may be null), and this block's share of
-// the columns' sums before that rounding (part may be null). A block takes 256 columns (eight
-// to a lane) of the rows blockIdx.y rows_per .. ; its eight warps take every eighth row and
-// their sums meet in shared memory in the warps' order.
+// dz = dy act'(z), rounded to the operands' type (dz may be null), and the columns' sums before
+// that rounding (dbias may be null). A block takes 64 columns, eight lanes of a warp to a row,
+// and a share of the batch; the shares of the same columns are a cluster, whose first block adds
+// their sums in order out of the others' shared memory. So the bias gradient takes no second
+// kernel, which at batch 2048 took 5 us before the products could start.
+constexpr int kDzColumns = 64;
+constexpr int kDzCluster = 8;
+
+template <int ACT>
 __global__ void __launch_bounds__(256)
     k_fp_dz(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz, int type,
-            int act, int B, int OC, int rows_per, int vec, uint16_t* __restrict__ dz, int64_t lddz,
-            float* __restrict__ part)
+            int B, int OC, int shares, int vec, uint16_t* __restrict__ dz, int64_t lddz, float* __restrict__ dbias)
 {
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ float sums[8][256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = blockIdx.x * 256 + lane * 8;
-    const int r1 = min(B, ((int)blockIdx.y + 1) * rows_per);
+    __shared__ float sums[32][kDzColumns];
+    __shared__ float total[kDzColumns];
+    const int row = threadIdx.x >> 3, lane = threadIdx.x & 7;
+    const int share = shares > 1 ? (int)cluster_ctarank() : 0;
+    const int rows_per = (B + shares - 1) / shares;
+    const int c0 = (blockIdx.x / shares) * kDzColumns + lane * 8;
+    const int r1 = min(B, (share + 1) * rows_per);
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    if (c0 < OC)
-        for (int r = blockIdx.y * rows_per + warp; r < r1; r += 8) {
-            const uint4 d = load_eight(dy + r * lddy, c0, OC, vec);
-            const uint4 q = act != ITO_ACT_NONE ? load_eight(z + r * ldz, c0, OC, vec) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, qw[4] = {q.x, q.y, q.z, q.w};
-            uint32_t o[4];
+    if (c0 < OC) {
+        constexpr int U = 4;             // rows whose loads are in flight together
+        for (int r0 = share * rows_per + row; r0 < r1; r0 += 32 * U) {
+            uint4 d[U], q[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float2 v = unpack16(type, dw[i]);
-                if (act != ITO_ACT_NONE) {
-                    const float2 zz = unpack16(type, qw[i]);
-                    v.x *= act_slope(act, zz.x);
-                    v.y *= act_slope(act, zz.y);
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + 32 * u;
+                d[u] = q[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < r1) {
+                    d[u] = load_eight(dy + r * lddy, c0, OC, vec);
+                    if (ACT != ITO_ACT_NONE) q[u] = load_eight(z + r * ldz, c0, OC, vec);
                 }
-                s[2 * i] += v.x;
-                s[2 * i + 1] += v.y;
-                o[i] = pack16(type, v.x, v.y);
             }
-            // dz's rows are padded to 8 elements: a whole vector always fits
-            if (dz) *reinterpret_cast<uint4*>(dz + r * lddz + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = r0 + 32 * u;
+                if (r >= r1) break;
+                const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, qw[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float2 v = unpack16(type, dw[i]);
+                    if (ACT != ITO_ACT_NONE) {
+                        const float2 zz = unpack16(type, qw[i]);
+                        v.x *= act_slope(ACT, zz.x);
+                        v.y *= act_slope(ACT, zz.y);
+                    }
+                    s[2 * i] += v.x;
+                    s[2 * i + 1] += v.y;
+                    o[i] = pack16(type, v.x, v.y);
+                }
+                // dz's rows are padded to 8 elements: a whole vector always fits
+                if (dz) *reinterpret_cast<uint4*>(dz + r * lddz + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
-    if (!part) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = s[i];
-    __syncthreads();
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= OC) return;
-    float v = sums[0][threadIdx.x];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) v += sums[w][threadIdx.x];
-    part[(int64_t)blockIdx.y * OC + c] = v;
-}
-
-// out[c] = the parts' sum in a fixed order: a warp's lanes take 32 columns, eight warps every
-// eighth part
-__global__ void __launch_bounds__(256)
-    k_fp_column_sums(const float* __restrict__ part, int parts, int n, float* __restrict__ out)
-{
-    griddep_wait();
-    griddep_launch_dependents();
-    __shared__ float sums[8][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (c < n)
-        for (int p = warp; p < parts; p += 8) s += part[(int64_t)p * n + c];
-    sums[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < n) {
-#pragma unroll
-        for (int w = 1; w < 8; ++w) s += sums[w][lane];
-        out[c] = s;
     }
+    if (!dbias) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[row][lane * 8 + i] = s[i];
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c < kDzColumns) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) v += sums[w][c];
+        total[c] = v;
+    }
+    if (shares > 1) cluster_sync();
+    const int column = (blockIdx.x / shares) * kDzColumns + c;
+    if (share == 0 && c < kDzColumns && column < OC) {
+        float v = total[c];
+        for (int p = 1; p < shares; ++p) {
+            float o;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(mapa_shared(smem_u32(&total[c]), p)) : "memory");
+            v += o;
+        }
+        dbias[column] = v;
+    }
+    if (shares > 1) cluster_sync();      // the first block has read the others' shared memory
 }
 
 // ------------------------------------------------------------------------ host
 
-constexpr int kDzRows = 64;          // rows of the batch to a share of the bias gradient's sum, at least
+// shares of the batch: of at least 64 rows each, as many as a cluster has blocks
+static int dz_shares(int B)
+{
+    int n = 1;
+    while (n < kDzCluster && B >= 128 * n) n *= 2;
+    return n;
+}
 
-static int dz_rows_per(int B) { return std::max(kDzRows, ((B + 255) / 256 + 7) / 8 * 8); }
-static int dz_parts(int B) { return (B + dz_rows_per(B) - 1) / dz_rows_per(B); }
+template <int ACT>
+static int run_dz(const void* dy, int64_t lddy, const void* z, int64_t ldz, int type, int B, int OC, int vec,
+                  uint16_t* dz, int64_t lddz, float* dbias, cudaStream_t s)
+{
+    const int shares = dz_shares(B);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((OC + kDzColumns - 1) / kDzColumns * shares);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = shares;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = shares > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp_dz<ACT>, static_cast<const uint16_t*>(dy), lddy,
+                                             static_cast<const uint16_t*>(z), ldz, type, B, OC, shares, vec, dz, lddz,
+                                             dbias);
+    return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "linear backward launch: %s", cudaGetErrorString(e));
+}
+
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // A row's stride says nothing about a single row.
@@ -322,8 +363,7 @@ size_t ito_fp_linear_bwd_workspace_size(const void* dy, int64_t lddy, const void
 {
     if (check_sizes(B, IC, OC)) return 0;
     const bool dz = act != ITO_ACT_NONE || !tma_rows(dy, lddy, B, OC);
-    return (dz ? align256((size_t)B * pad8(OC) * 2) : 0) + align256((size_t)dz_parts(B) * OC * 4) +
-           copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) +
+    return (dz ? align256((size_t)B * pad8(OC) * 2) : 0) + copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) +
            align256(std::max(fp_gemm_ws_bytes(B, IC, OC), fp_gemm_ws_bytes(OC, IC, B)));
 }
 
@@ -358,14 +398,19 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
         dz = reinterpret_cast<uint16_t*>(ws);
         ws += align256((size_t)B * pad8(OC) * 2);
     }
-    float* part = reinterpret_cast<float*>(ws);
-    ws += align256((size_t)dz_parts(B) * OC * 4);
     if (dbias || (own_dz && (dx || dW))) {
         const int vec = tma_rows(dy, lddy, B, OC) && (act == ITO_ACT_NONE || tma_rows(z, ldz, B, OC));
-        launch_pdl(k_fp_dz, dim3((OC + 255) / 256, dz_parts(B)), 256, 0, s, static_cast<const uint16_t*>(dy), lddy,
-                   static_cast<const uint16_t*>(z), ldz, type, act, B, OC, dz_rows_per(B), vec,
-                   dx || dW ? dz : static_cast<uint16_t*>(nullptr), pad8(OC), dbias ? part : static_cast<float*>(nullptr));
-        if (dbias) launch_pdl(k_fp_column_sums, (OC + 31) / 32, 256, 0, s, part, dz_parts(B), OC, dbias);
+        uint16_t* out = dx || dW ? dz : nullptr;
+        switch (act) {
+        case ITO_ACT_RELU: r = run_dz<ITO_ACT_RELU>(dy, lddy, z, ldz, type, B, OC, vec, out, pad8(OC), dbias, s); break;
+        case ITO_ACT_GELU: r = run_dz<ITO_ACT_GELU>(dy, lddy, z, ldz, type, B, OC, vec, out, pad8(OC), dbias, s); break;
+        case ITO_ACT_GELU_TANH:
+            r = run_dz<ITO_ACT_GELU_TANH>(dy, lddy, z, ldz, type, B, OC, vec, out, pad8(OC), dbias, s);
+            break;
+        case ITO_ACT_SILU: r = run_dz<ITO_ACT_SILU>(dy, lddy, z, ldz, type, B, OC, vec, out, pad8(OC), dbias, s); break;
+        default: r = run_dz<ITO_ACT_NONE>(dy, lddy, z, ldz, type, B, OC, vec, out, pad8(OC), dbias, s); break;
+        }
+        if (r) return r;
     }
     const void* d = own_dz ? dz : dy;
     const int64_t ldd = own_dz ? pad8(OC) : row_stride(lddy, B, OC);

@@ -103,11 +103,14 @@ struct PairSums {
 // Lane i holds the i-th best of what the warp has taken in. Elements that come before `low` go
 // to a buffer of 64 in shared memory; 32 of them at a time are sorted and merged with the list
 // by shuffles, and its k-th best becomes `low`. The first `low` is the k-th largest of the lanes'
-// largest elements of the first round: at least k elements are no smaller, and in random order
-// few more than k of that round and of each following one come before it.
+// largest elements of the first round, and of the block's warps the largest such: at least k
+// elements are no smaller, and in random order few more than k of that round and of each
+// following one come before it. So the sorts are few: at 4096 x 32768 with k = 4 a warp's
+// instructions fell from 5400 to 1500, 1100 of them for the sums.
 struct Alternatives {
     float value, low;
     int id, low_id, count;
+    bool sorted;                 // the list holds elements
     float* buf_v;
     int* buf_i;
 
@@ -116,6 +119,7 @@ struct Alternatives {
         value = low = -INFINITY;
         id = low_id = INT_MAX;
         count = 0;
+        sorted = false;
         buf_v = v;
         buf_i = i;
     }
@@ -154,7 +158,7 @@ struct Alternatives {
             value = rv;
             id = ri;
         }
-#pragma unroll
+#pragma unroll 1
         for (int j = 16; j > 0; j /= 2) exchange(value, id, j, (lane & j) == 0);
         low = __shfl_sync(0xffffffffu, value, k - 1);
         low_id = __shfl_sync(0xffffffffu, id, k - 1);
@@ -171,12 +175,18 @@ struct Alternatives {
         buf_v[lane] = more_v;
         buf_i[lane] = more_i;
         count = max(count - 32, 0);
-#pragma unroll
+        merge_unsorted(v, i, k);
+    }
+    __device__ __forceinline__ void merge_unsorted(float v, int i, int k)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
         for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
+#pragma unroll 1
             for (int j = size / 2; j > 0; j /= 2)
                 exchange(v, i, j, ((lane & j) == 0) == ((lane & size) == 0));
         merge(v, i, k);
+        sorted = true;
     }
     // all lanes, each with an element of its own (take false: none)
     __device__ __forceinline__ void offer(float v, int i, bool take, int k)
@@ -196,10 +206,11 @@ struct Alternatives {
 
 // Elements [begin, end) of a row for thread `at` of `threads`: UNROLL vectors in flight. A
 // vector's elements are `skip` apart: neighbours (VEC; begin on 16 bytes) or a warp's width
-// apart, where rows start anywhere and a warp's single loads are still consecutive.
+// apart, where rows start anywhere and a warp's single loads are still consecutive. lows: the
+// block's first thresholds, where its warps share the row (then every warp passes here).
 template <typename T, bool TOP, bool VEC>
 __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, int end, int at, int threads, int k,
-                                          Alternatives& alt)
+                                          Alternatives& alt, float* lows)
 {
     constexpr int PER = Vec<T>::kPer, UNROLL = 4;
     constexpr int skip = VEC ? 1 : 32;
@@ -235,7 +246,16 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
         }
         const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         sums.rise(m);
-        if (TOP && base == begin) alt.first_low(m, k);
+        if (TOP && base == begin) {
+            alt.first_low(m, k);
+            if (lows) {
+                if (lane == 0) lows[at >> 5] = alt.low;
+                __syncthreads();
+                alt.low = lows[0];
+#pragma unroll
+                for (int w = 1; w < kLpWarps; ++w) alt.low = fmaxf(alt.low, lows[w]);
+            }
+        }
         unsigned pending = 0;            // vectors with an element to look at closer, in any lane
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
@@ -261,13 +281,24 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
                     w = v[q];
                     c = first[q];
                 }
-#pragma unroll 1
-            for (int j = 0; j < PER; ++j, c += skip) {
-                alt.offer(w.take_first(), c, c < end, k);
+            float f[PER];
+            w.get(f);
+            unsigned wanted = 0;         // of this lane's elements
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (c + j * skip < end && !(f[j] < alt.low)) wanted |= 1u << j;
+            unsigned turns = __reduce_or_sync(0xffffffffu, wanted);
+            while (turns) {
+                const int j = __ffs(turns) - 1;
+                turns &= turns - 1;
+                float x = f[0];
+#pragma unroll
+                for (int q = 1; q < PER; ++q)
+                    if (j == q) x = f[q];
+                alt.offer(x, c + j * skip, wanted >> j & 1u, k);
             }
         }
     }
-    if (TOP && alt.count) alt.flush(k);
     return sums.total();
 }
 
@@ -323,7 +354,8 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
     for (int64_t r = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5); r < rows; r += step) {
         Alternatives alt;
         alt.clear(buf_v[threadIdx.x >> 5], buf_i[threadIdx.x >> 5]);
-        const Sums a = scan_part<T, TOP, VEC>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt);
+        const Sums a = scan_part<T, TOP, VEC>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt, nullptr);
+        if (TOP && alt.count) alt.flush(k);
         write_row<T, TOP>(x + r * ld, targets, r, classes, k, warp_join(a), alt, o, err);
     }
 }
@@ -337,6 +369,8 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
                     int classes, int k, int parts, int stretch, const LpOut o, int* __restrict__ err)
 {
     __shared__ Sums sums[kLpWarps];
+    __shared__ float lows[kLpWarps];
+    __shared__ int counts[kLpWarps];
     __shared__ float buf_v[kLpWarps][TOP ? 64 : 1], values[kLpWarps][TOP ? kLpMaxTop : 1];
     __shared__ int buf_i[kLpWarps][TOP ? 64 : 1], ids[kLpWarps][TOP ? kLpMaxTop : 1];
     griddep_wait();
@@ -347,19 +381,42 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
     for (int64_t r = blockIdx.x / parts; r < rows; r += gridDim.x / parts) {
         Alternatives alt;
         alt.clear(buf_v[warp], buf_i[warp]);
-        Sums a = warp_join(scan_part<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt));
-        if (lane == 0) sums[warp] = a;
-        if (TOP) {
-            values[warp][lane] = alt.value;
-            ids[warp][lane] = alt.id;
+        Sums a = warp_join(scan_part<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt, lows));
+        if (lane == 0) {
+            sums[warp] = a;
+            counts[warp] = alt.sorted ? 64 : alt.count;
         }
         __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kLpWarps; ++w) total += counts[w];
+        if (TOP && total > 32) {
+            // each warp's own list, and the lists one after another
+            if (alt.count) alt.flush(k);
+            values[warp][lane] = alt.value;
+            ids[warp][lane] = alt.id;
+            __syncthreads();
+        }
         if (warp == 0) {
             a = lane < kLpWarps ? sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
             a = warp_join(a);
-            if (TOP)
+            if (TOP && total > 32) {
 #pragma unroll 1
                 for (int w = 1; w < kLpWarps; ++w) alt.merge(values[w][lane], ids[w][lane], k);
+            } else if (TOP) {
+                // all the warps' elements fit one sort
+                float v = -INFINITY;
+                int i = INT_MAX, before = 0;
+#pragma unroll
+                for (int w = 0; w < kLpWarps; ++w) {
+                    if (lane >= before && lane < before + counts[w]) {
+                        v = buf_v[w][lane - before];
+                        i = buf_i[w][lane - before];
+                    }
+                    before += counts[w];
+                }
+                alt.merge_unsorted(v, i, k);
+            }
         }
         if (parts > 1) {
             if (warp == 0) {
@@ -430,7 +487,7 @@ template <typename T>
 __device__ __noinline__ Sums sums_again(const T* row, int classes, int at, int threads)
 {
     Alternatives none;
-    return warp_join(scan_part<T, false, false>(row, 0, classes, at, threads, 0, none));
+    return warp_join(scan_part<T, false, false>(row, 0, classes, at, threads, 0, none, nullptr));
 }
 
 constexpr int kLpStretch = 8192;     // elements of a row that a block takes, at most
