@@ -1006,7 +1006,8 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     rows, classes = logits.shape
     if targets is not None:
         _vector(targets, "targets", rows, (torch.int32,))
-    logp, entropy, lse = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind()
+    logp = torch.empty(rows, dtype=torch.float32, device=dev)
+    entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
     ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
     top = torch.empty((rows, k), dtype=torch.float32, device=dev)
     _check(_lib.ito_token_logprobs_fwd(logits.data_ptr(), ld, _type_id(logits, "logits"), _addr(targets), rows, classes,

@@ -84,6 +84,27 @@ struct Vec {
             return *reinterpret_cast<const uint32_t*>(&v);
         }
     }
+    // the largest element (a NaN counts only where there is nothing else)
+    __device__ __forceinline__ float largest() const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                         fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+        } else {
+            const uint32_t m = max_pair(max_pair(w[0], w[1]), max_pair(w[2], w[3]));
+            return fmaxf(lane16(m, 0), lane16(m, 1));
+        }
+    }
+    static __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else
+            asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
     // elements c .. c + kPer - 1 of a row of n, 0 beyond it; vec: the row starts on 16 bytes
     // (c is a multiple of kPer)
     __device__ __forceinline__ void load(const T* row, int c, int n, bool vec)

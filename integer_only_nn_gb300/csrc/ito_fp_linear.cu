@@ -131,7 +131,7 @@ constexpr int kDzColumns = 64;
 constexpr int kDzCluster = 8;
 
 template <int ACT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     k_fp_dz(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz, int type,
             int B, int OC, int shares, int vec, uint16_t* __restrict__ dz, int64_t lddz, float* __restrict__ dbias)
 {

@@ -9,7 +9,6 @@
 // masked has lse = -inf, log probabilities of -inf, entropy 0 and a gradient of 0. A target
 // of -1 stands for no token: logp 0 and no gradient from it.
 #include <algorithm>
-#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -41,39 +40,51 @@ __device__ __forceinline__ float exp2_fast(float x)
 
 // ---------------------------------------------------------- sums of a part of a row
 //
-// One pass: a running maximum `top`, s = sum exp(x - top) and t = sum (x - top) exp(x - top),
-// brought to a new maximum when a vector raises it (rarely, after the first few). `top` starts
-// at the lowest finite value, so that -inf adds 0 and the lowest value itself adds 1.
-struct Sums {
-    float top, s, t;
+// One pass in powers of two: with L = log2 e and c = top L (rounded), y = x L - c in one rounding,
+// s = sum 2^y and t = sum y 2^y, brought to a new `top` when a round of elements raises it
+// (rarely, after the first few). c's own rounding cancels in H = ln 2 (log2 s - t / s) and in
+// log p = ln 2 (y - log2 s), while it is small beside 1: `top` starts at -2^20, where masked
+// elements of -inf add 0 and so do finite ones far below, and a row whose largest element lies
+// outside +-2^20 (s stays below 1/2, or top ends above) is taken again by FarSums.
+constexpr float kLpReach = 1048576.0f;
+constexpr float kLpStart = -kLpReach;
+constexpr float kLn2 = 0.69314718055994531f;
 
+__device__ __forceinline__ float max_nan(float a, float b)      // a NaN wins
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+struct Sums {
+    float top, s, t;             // t: of y 2^y, y counted from top
+
+    __device__ __forceinline__ void clear()
+    {
+        top = kLpStart;
+        s = t = 0.0f;
+    }
+    // to a top no smaller
     __device__ __forceinline__ void rise(float m)
     {
         if (!(m > top)) return;
-        const float d = fmaxf(top - m, -FLT_MAX), e = exp2_fast(d * kLog2e);
-        t = e != 0.0f ? (t + d * s) * e : 0.0f;
-        s = s != s ? s : e != 0.0f ? s * e : 0.0f;
+        const float d = fmaxf(top * kLog2e - m * kLog2e, -300.0f), e = exp2_fast(d);
+        t = (t + d * s) * e;
+        s *= e;
         top = m;
-    }
-    __device__ __forceinline__ void join(Sums o)
-    {
-        const float m = fmaxf(top, o.top);
-        rise(m);
-        o.rise(m);
-        s += o.s;
-        t += o.t;
     }
 };
 
-// A thread's sums, two elements at a time: at about nine instructions an element the forward
-// pass would be bound by their issue, not by memory.
+// A thread's sums, two elements at a time: five instructions an element, so that memory and not
+// their issue bounds the forward pass.
 struct PairSums {
     float top;
     float2 s, t;
 
     __device__ __forceinline__ void clear()
     {
-        top = -FLT_MAX;
+        top = kLpStart;
         s = t = make_float2(0.0f, 0.0f);
     }
     __device__ __forceinline__ void rise(float m)
@@ -88,15 +99,50 @@ struct PairSums {
     }
     __device__ __forceinline__ void add(float2 x)
     {
-        const float2 d = __fadd2_rn(x, make_float2(-top, -top));
-        const float2 y = __fmul2_rn(d, make_float2(kLog2e, kLog2e));
+        const float c = -top * kLog2e;
+        float2 y = __ffma2_rn(x, make_float2(kLog2e, kLog2e), make_float2(c, c));
+        y = make_float2(max_nan(y.x, -200.0f), max_nan(y.y, -200.0f));      // (-inf times 0 would be a NaN)
         const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
         s = __fadd2_rn(s, e);
-        // (-inf times 0 would be a NaN; a NaN reaches s)
-        t = __ffma2_rn(make_float2(fmaxf(d.x, -200.0f), fmaxf(d.y, -200.0f)), e, t);
+        t = __ffma2_rn(y, e, t);
     }
     __device__ __forceinline__ Sums total() const { return Sums{top, s.x + s.y, t.x + t.y}; }
 };
+
+// the sums of 32 lanes, in every lane
+__device__ __forceinline__ Sums warp_join(Sums a)
+{
+    float m = a.top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    a.rise(m);
+    a.s = warp_sum(a.s);
+    a.t = warp_sum(a.t);
+    return a;
+}
+
+// The same sums for rows far from 0, in natural units: x - top is exact enough anywhere. All lanes of a warp, the whole row.
+struct FarSums {
+    float top, s, t;             // t: of (x - top) exp(x - top)
+};
+
+template <typename T>
+__device__ __noinline__ FarSums far_sums(const T* row, int classes)
+{
+    const int lane = threadIdx.x & 31;
+    FarSums f{-INFINITY, 0.0f, 0.0f};
+    for (int c = lane; c < classes; c += 32) f.top = fmaxf(f.top, to_f32(row[c]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f.top = fmaxf(f.top, __shfl_xor_sync(0xffffffffu, f.top, o));
+    for (int c = lane; c < classes && f.top > -INFINITY; c += 32) {
+        const float d = max_nan(to_f32(row[c]) - f.top, -1000.0f), e = expf(d);
+        f.s += e;
+        f.t += d * e;
+    }
+    f.s = warp_sum(f.s);
+    f.t = warp_sum(f.t);
+    return f;
+}
 
 // ------------------------------------------------------------- a warp's alternatives
 //
@@ -215,19 +261,19 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
     constexpr int PER = Vec<T>::kPer, UNROLL = 4;
     constexpr int skip = VEC ? 1 : 32;
     const int lane = threadIdx.x & 31;
-    const int round = threads * PER * UNROLL;
     PairSums sums;
     sums.clear();
-    for (int64_t base = begin; base < end; base += round) {
+    // (classes are at most 2^30: no index overflows)
+    for (int base = begin; base < end; base += threads * PER * UNROLL) {
         Vec<T> v[UNROLL];
         int first[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const int64_t block = base + (u * threads + (at - lane)) * PER;     // the warp's elements
-            const int64_t c = block + (VEC ? lane * PER : lane);
-            first[u] = (int)(c < end ? c : end);
+            const int block = base + (u * threads + (at - lane)) * PER;     // the warp's elements
+            const int c = block + (VEC ? lane * PER : lane);
+            first[u] = min(c, end);
             if (VEC && c + PER <= end) {
-                v[u].raw = __ldg(reinterpret_cast<const uint4*>(row + c));
+                v[u].raw = __ldcs(reinterpret_cast<const uint4*>(row + c));
             } else {
                 float f[PER];
 #pragma unroll
@@ -237,13 +283,7 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
         }
         float most[UNROLL];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            float f[PER];
-            v[u].get(f);
-            most[u] = f[0];
-#pragma unroll
-            for (int j = 1; j < PER; ++j) most[u] = fmaxf(most[u], f[j]);
-        }
+        for (int u = 0; u < UNROLL; ++u) most[u] = v[u].largest();
         const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         sums.rise(m);
         if (TOP && base == begin) {
@@ -256,21 +296,21 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
                 for (int w = 1; w < kLpWarps; ++w) alt.low = fmaxf(alt.low, lows[w]);
             }
         }
-        unsigned pending = 0;            // vectors with an element to look at closer, in any lane
+        unsigned pending = 0;            // this lane's vectors with an element to look at closer
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             float f[PER];
             v[u].get(f);
 #pragma unroll
             for (int j = 0; j < PER; j += 2) sums.add(make_float2(f[j], f[j + 1]));
-            if (TOP) {
-                // a NaN is not in `most`, but it is in the sum; beyond the end nothing is offered
-                const bool look = most[u] >= alt.low || sums.s.x != sums.s.x || sums.s.y != sums.s.y;
-                if (__any_sync(0xffffffffu, look && first[u] < end)) pending |= 1u << u;
-            }
+            // a NaN is not in `most`, but it is in the sum
+            if (TOP && (most[u] >= alt.low || sums.s.x != sums.s.x || sums.s.y != sums.s.y) && first[u] < end)
+                pending |= 1u << u;
         }
+        if (!TOP) continue;
+        pending = __reduce_or_sync(0xffffffffu, pending);
         // one copy of this in the code: unrolled, its sorts would not fit the instruction cache
-        while (TOP && pending) {
+        while (pending) {
             const int u = __ffs(pending) - 1;
             pending &= pending - 1;
             Vec<T> w = v[0];
@@ -283,7 +323,7 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
                 }
             float f[PER];
             w.get(f);
-            unsigned wanted = 0;         // of this lane's elements
+            unsigned wanted = 0;         // of this lane's elements; beyond the end none
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 if (c + j * skip < end && !(f[j] < alt.low)) wanted |= 1u << j;
@@ -314,30 +354,42 @@ __device__ __forceinline__ void write_row(const T* row, const int32_t* targets, 
                                           const Sums& a, const Alternatives& alt, const LpOut& o, int* err)
 {
     const int lane = threadIdx.x & 31;
-    const bool none = a.s == 0.0f;
-    const float ls = logf(a.s);
+    float lse, entropy, top, ls;
+    bool none = false, far = false;
+    if (!(a.s < 0.5f) && (a.top <= kLpReach || a.s != a.s)) {
+        const float l2 = log2f(a.s);
+        top = a.top;
+        ls = l2 * kLn2;
+        lse = a.top + ls;
+        entropy = (l2 - a.t / a.s) * kLn2;
+    } else {
+        const FarSums f = far_sums(row, classes);
+        none = f.top == -INFINITY;
+        far = true;
+        top = f.top;
+        ls = logf(f.s);
+        lse = none ? -INFINITY : f.top + ls;
+        entropy = none ? 0.0f : ls - f.t / f.s;
+    }
+    // counted from top as the sums were, whose c is rounded; far below it that does not matter
+    auto log_p = [&](float x) {
+        const float d = x - top;
+        if (none) return -INFINITY;
+        return (far || d < -kLpReach ? d : fmaf(x, kLog2e, -(top * kLog2e)) * kLn2) - ls;
+    };
     if (lane == 0) {
-        if (o.lse) o.lse[r] = none ? -INFINITY : a.top + ls;
-        if (o.entropy) o.entropy[r] = none ? 0.0f : ls - a.t / a.s;
+        if (o.lse) o.lse[r] = lse;
+        if (o.entropy) o.entropy[r] = entropy;
         if (o.logp) {
             const int t = targets[r];
             if (t < -1 || t >= classes) raise_device_error(err, ITO_ERR_ARG);
-            o.logp[r] = t < 0 || t >= classes ? 0.0f : none ? -INFINITY : (to_f32(row[t]) - a.top) - ls;
+            o.logp[r] = t < 0 || t >= classes ? 0.0f : log_p(to_f32(row[t]));
         }
     }
     if (TOP && lane < k) {
         o.top_ids[r * k + lane] = alt.id;
-        o.top_logp[r * k + lane] = none ? -INFINITY : (alt.value - a.top) - ls;
+        o.top_logp[r * k + lane] = log_p(alt.value);
     }
-}
-
-__device__ __forceinline__ Sums warp_join(Sums a)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        a.join(Sums{__shfl_xor_sync(0xffffffffu, a.top, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                    __shfl_xor_sync(0xffffffffu, a.t, o)});
-    return a;
 }
 
 // Short rows: a warp to a row.
@@ -364,7 +416,7 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
 // with a stretch of it. The warps' sums and alternatives meet in their block's shared memory, the
 // blocks' in the first one's, read across the cluster.
 template <typename T, bool TOP, bool VEC>
-__global__ void __launch_bounds__(kLpWarps * 32, 3)
+__global__ void __launch_bounds__(kLpWarps * 32, 4)
     k_logprobs_long(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
                     int classes, int k, int parts, int stretch, const LpOut o, int* __restrict__ err)
 {
@@ -398,7 +450,7 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
             __syncthreads();
         }
         if (warp == 0) {
-            a = lane < kLpWarps ? sums[lane] : Sums{-FLT_MAX, 0.0f, 0.0f};
+            a = lane < kLpWarps ? sums[lane] : Sums{kLpStart, 0.0f, 0.0f};
             a = warp_join(a);
             if (TOP && total > 32) {
 #pragma unroll 1
@@ -428,24 +480,29 @@ __global__ void __launch_bounds__(kLpWarps * 32, 3)
             }
             cluster_sync();
             if (part == 0 && warp == 0) {
-#pragma unroll 1
-                for (int p = 1; p < parts; ++p) {
-                    const uint32_t sa = mapa_shared(smem_u32(&sums[0]), p);
-                    Sums q;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.top) : "r"(sa) : "memory");
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(sa + 4) : "memory");
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.t) : "r"(sa + 8) : "memory");
-                    a.join(q);
-                    if (TOP) {
-                        float v;
-                        int i;
+                // all the blocks' results are asked for before the first is used
+                const uint32_t sa = mapa_shared(smem_u32(&sums[0]), lane < parts ? lane : 0);
+                Sums q;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.top) : "r"(sa) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(sa + 4) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.t) : "r"(sa + 8) : "memory");
+                float v[kLpCluster];
+                int i[kLpCluster];
+                if (TOP)
+#pragma unroll
+                    for (int p = 1; p < kLpCluster; ++p) {
+                        const int from = p < parts ? p : 0;
                         asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(v) : "r"(mapa_shared(smem_u32(&values[0][lane]), p)) : "memory");
+                                     : "=f"(v[p]) : "r"(mapa_shared(smem_u32(&values[0][lane]), from)) : "memory");
                         asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                                     : "=r"(i) : "r"(mapa_shared(smem_u32(&ids[0][lane]), p)) : "memory");
-                        alt.merge(v, i, k);
+                                     : "=r"(i[p]) : "r"(mapa_shared(smem_u32(&ids[0][lane]), from)) : "memory");
                     }
-                }
+                if (lane >= parts) q.clear();
+                a = warp_join(q);
+                if (TOP)
+#pragma unroll
+                    for (int p = 1; p < kLpCluster; ++p)
+                        if (p < parts) alt.merge(v[p], i[p], k);
             }
             cluster_sync();              // the first block has read the others' shared memory
         }
@@ -482,14 +539,6 @@ __device__ __forceinline__ float lp_slope(const LpRow& w, float x, int c)
     return d;
 }
 
-// (rare: kept out of the main path's registers)
-template <typename T>
-__device__ __noinline__ Sums sums_again(const T* row, int classes, int at, int threads)
-{
-    Alternatives none;
-    return warp_join(scan_part<T, false, false>(row, 0, classes, at, threads, 0, none, nullptr));
-}
-
 constexpr int kLpStretch = 8192;     // elements of a row that a block takes, at most
 
 template <typename T>
@@ -502,7 +551,6 @@ __global__ void __launch_bounds__(256, 4)
     griddep_wait();
     griddep_launch_dependents();
     constexpr int PER = Vec<T>::kPer, UNROLL = 4;
-    __shared__ Sums sums[kLpWarps];
     const int at = per_warp ? threadIdx.x & 31 : threadIdx.x, threads = per_warp ? 32 : 256;
     const int64_t work = per_warp ? rows : rows * stretches;
     const int64_t first = per_warp ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
@@ -524,15 +572,10 @@ __global__ void __launch_bounds__(256, 4)
         const T* xr = x + r * ld;
         T* dr = dx + r * ldd;
         if (fabsf(z) >= kLpFar && fabsf(z) < INFINITY && (stretches == 1 || dx != x)) {
-            Sums a = sums_again(xr, classes, at, threads);
-            if (!per_warp) {
-                __syncthreads();         // (the row is the block's: every thread is here)
-                if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = a;
-                __syncthreads();
-                a = warp_join((threadIdx.x & 31) < kLpWarps ? sums[threadIdx.x & 31] : Sums{-FLT_MAX, 0.0f, 0.0f});
-            }
-            w.top = a.top;
-            w.ls = logf(a.s);
+            const FarSums f = far_sums(xr, classes);    // each warp for itself
+            w.top = f.top;
+            w.ls = logf(f.s);
+            if (!per_warp) __syncthreads();             // (the row is the block's; dx may be x)
         }
         const int lead_x = (int)((16 - (reinterpret_cast<uintptr_t>(xr) & 15)) & 15) / (int)sizeof(T);
         const int lead_d = (int)((16 - (reinterpret_cast<uintptr_t>(dr) & 15)) & 15) / (int)sizeof(T);
