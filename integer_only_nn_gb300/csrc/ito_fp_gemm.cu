@@ -8,7 +8,7 @@
 // tcgen05.mma, and the epilogue warps drain one of two accumulators while the other fills.
 //
 // Two kernels: a CTA pair works on 256 x 256 tiles (each SM stages half of B, so a byte from L2
-// feeds twice the work), for results with enough such tiles to occupy the device; 128 x 128 and
+// feeds twice the work), or narrower ones, for results with enough of them to occupy the device; 128 x 128 and
 // 128 x 64 tiles of one CTA, with K cut into slices where there are few tiles, for the rest.
 // Slices write their sums in 32 bits to the workspace, and a second kernel adds them in a fixed
 // order and does the epilogue.
@@ -45,25 +45,38 @@ struct FpGemmArgs {
     int M, N, K;
     int a_mn, b_mn;
     uint32_t idesc;
-    int group;
+    int group, bn;              // row tiles of a raster group; columns of a pair's tile
     int splits, kb_per_split;   // K slices (1: none); slices go to mapS
     int y_tma, z_tma;           // rows of y and z that TMA stores can take
-    int r_vec;                  // rows of the residual that 16-byte loads can take
+    int r_vec, b_vec;           // rows of the residual, and a bias, that 16-byte loads can take
     int* err;
 };
 
 // ------------------------------------------------------------------ epilogue
 //
-// A warp holds 32 rows (its lanes) of 64 columns of sums at a time. Its results go through its
-// own 4 KB of shared memory (32 rows of 128 bytes, 16-byte chunk j of row r at j ^ (r % 8), the
-// 128-byte swizzle) and leave by TMA, which clips them at the tensor's edges, or, where rows do
-// not start on 16-byte boundaries, by coalesced plain stores.
+// A warp holds 32 rows (its lanes) of 32 columns of sums at a time. Its results go through its
+// own buffers of shared memory, 32 rows of 64 bytes (16-byte chunk j of row r at j ^ (r / 2 % 4),
+// the 64-byte swizzle), and leave by TMA, which clips them at the tensor's edges, or, where rows
+// do not start on 16-byte boundaries, by coalesced plain stores. Four buffers to a warp: with
+// one, each box waited for the one before to be read, and a last tile's epilogue with
+// activation, residual and z took 35 us.
+constexpr int kFpBox = 2048, kFpBoxes = 4;
 
-__device__ __forceinline__ void box_begin(int lane)
-{
-    if (lane == 0) bulk_wait_read_all();
-    __syncwarp();
-}
+struct FpStage {
+    uint8_t* p;
+    int lane, turn;
+
+    // the next buffer. Every box is one group of bulk stores (an empty one, where it went by plain
+    // stores), so the buffer's last box is kFpBoxes groups back.
+    __device__ __forceinline__ uint8_t* begin()
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kFpBoxes - 1) : "memory");
+        __syncwarp();
+        uint8_t* r = p + turn * kFpBox;
+        turn = (turn + 1) % kFpBoxes;
+        return r;
+    }
+};
 
 __device__ __forceinline__ void box_end_tma(const CUtensorMap* map, const uint8_t* stg, int lane, int col, int row)
 {
@@ -75,75 +88,153 @@ __device__ __forceinline__ void box_end_tma(const CUtensorMap* map, const uint8_
     }
 }
 
-// the staged box by plain stores: a lane takes one 4-byte word of every row
-__device__ __forceinline__ void box_end_plain(void* out, bool wide, int64_t ld, const uint8_t* stg, int lane, int col,
-                                              int row, int M, int N)
+// the 4-byte word `w` of a box's row r
+__device__ __forceinline__ uint32_t box_word(const uint8_t* stg, int r, int w)
 {
-    __syncwarp();
-    for (int r = 0; r < 32 && row + r < M; ++r) {
-        const uint32_t w =
-            *reinterpret_cast<const uint32_t*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-        if (wide) {
-            if (col + lane < N) static_cast<uint32_t*>(out)[(row + r) * ld + col + lane] = w;
-        } else {
-            uint16_t* dst = static_cast<uint16_t*>(out) + (row + r) * ld + col + 2 * lane;
-            if (col + 2 * lane < N) dst[0] = (uint16_t)w;
-            if (col + 2 * lane + 1 < N) dst[1] = (uint16_t)(w >> 16);
-        }
-    }
-    __syncwarp();
+    return *reinterpret_cast<const uint32_t*>(stg + r * 64 + (((w >> 2) ^ (r >> 1 & 3)) << 4) + (w & 3) * 4);
 }
 
-__device__ __forceinline__ void box16(const float (&v)[64], int type, const CUtensorMap* map, bool tma, void* out,
-                                      int64_t ld, uint8_t* stg, int lane, int col, int row, int M, int N)
+// 32 columns as 16-bit floats: one box
+__device__ __forceinline__ void store16(const float (&v)[32], int type, const CUtensorMap* map, bool tma, void* out,
+                                        int64_t ld, FpStage& st, int col, int row, int M, int N)
 {
-    box_begin(lane);
-    const uint32_t at = smem_u32(stg) + lane * 128;
+    uint8_t* stg = st.begin();
+    const int lane = st.lane;
+    const uint32_t at = smem_u32(stg) + lane * 64;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        st_shared_v4(at + ((j ^ (lane & 7)) << 4), (int)pack16(type, v[8 * j], v[8 * j + 1]),
+    for (int j = 0; j < 4; ++j)
+        st_shared_v4(at + ((j ^ (lane >> 1 & 3)) << 4), (int)pack16(type, v[8 * j], v[8 * j + 1]),
                      (int)pack16(type, v[8 * j + 2], v[8 * j + 3]), (int)pack16(type, v[8 * j + 4], v[8 * j + 5]),
                      (int)pack16(type, v[8 * j + 6], v[8 * j + 7]));
-    if (tma) box_end_tma(map, stg, lane, col, row);
-    else box_end_plain(out, false, ld, stg, lane, col, row, M, N);
+    if (tma) {
+        box_end_tma(map, stg, lane, col, row);
+        return;
+    }
+    __syncwarp();
+    // half a warp to a row, a word of two columns to a lane
+    const int w = lane & 15;
+    for (int r = lane >> 4; r < 32 && row + r < M; r += 2) {
+        const uint32_t x = box_word(stg, r, w);
+        uint16_t* dst = static_cast<uint16_t*>(out) + (row + r) * ld + col + 2 * w;
+        if (col + 2 * w < N) dst[0] = (uint16_t)x;
+        if (col + 2 * w + 1 < N) dst[1] = (uint16_t)(x >> 16);
+    }
+    __syncwarp();
+    if (lane == 0) bulk_commit();
 }
 
-// 64 columns in 32 bits are two boxes
-__device__ __forceinline__ void stage32(const float (&v)[64], int h, uint8_t* stg, int lane)
+// 16 of the columns (half h) as 32-bit floats, staged
+__device__ __forceinline__ uint8_t* stage32(const float (&v)[32], int h, FpStage& st)
 {
-    box_begin(lane);
-    const uint32_t at = smem_u32(stg) + lane * 128;
+    uint8_t* stg = st.begin();
+    const int lane = st.lane;
+    const uint32_t at = smem_u32(stg) + lane * 64;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int i = 32 * h + 4 * j;
-        st_shared_v4(at + ((j ^ (lane & 7)) << 4), __float_as_int(v[i]), __float_as_int(v[i + 1]),
+    for (int j = 0; j < 4; ++j) {
+        const int i = 16 * h + 4 * j;
+        st_shared_v4(at + ((j ^ (lane >> 1 & 3)) << 4), __float_as_int(v[i]), __float_as_int(v[i + 1]),
                      __float_as_int(v[i + 2]), __float_as_int(v[i + 3]));
+    }
+    return stg;
+}
+
+// 32 columns as 32-bit floats: two boxes
+__device__ __forceinline__ void store32(const float (&v)[32], const CUtensorMap* map, bool tma, void* out, int64_t ld,
+                                        FpStage& st, int col, int row, int M, int N)
+{
+    const int lane = st.lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = col + 16 * h;
+        if (c >= N) break;
+        uint8_t* stg = stage32(v, h, st);
+        if (tma) {
+            box_end_tma(map, stg, lane, c, row);
+            continue;
+        }
+        __syncwarp();
+        const int w = lane & 15;
+        for (int r = lane >> 4; r < 32 && row + r < M; r += 2)
+            if (c + w < N) static_cast<uint32_t*>(out)[(row + r) * ld + c + w] = box_word(stg, r, w);
+        __syncwarp();
+        if (lane == 0) bulk_commit();
     }
 }
 
 template <int ACT>
-__device__ __forceinline__ void activate(float (&v)[64])
+__device__ __forceinline__ void activate(float (&v)[32])
 {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = act_value(ACT, v[i]);
+    for (int i = 0; i < 32; ++i) v[i] = act_value(ACT, v[i]);
+}
+
+// this lane's row of a 16-bit residual, 32 columns (0 beyond the edges); asked for before the
+// sums are there
+__device__ __forceinline__ void load_residual16(const FpGemmArgs& a, int col, int row, uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+    if (row >= a.M || col >= a.N) return;
+    const uint16_t* r = static_cast<const uint16_t*>(a.e.residual) + row * a.e.ldr + col;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (a.r_vec && col + 8 * j + 8 <= a.N) {
+            const uint4 q = *reinterpret_cast<const uint4*>(r + 8 * j);
+            w[4 * j] = q.x;
+            w[4 * j + 1] = q.y;
+            w[4 * j + 2] = q.z;
+            w[4 * j + 3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + 8 * j + i < a.N) w[4 * j + (i >> 1)] |= (uint32_t)r[8 * j + i] << (16 * (i & 1));
+        }
+    }
+}
+
+// the columns' biases, the same for every lane
+__device__ __forceinline__ void add_bias(const FpGemmArgs& a, float (&v)[32], int col)
+{
+    const FpEpilogue& e = a.e;
+    if (a.b_vec && col + 32 <= a.N && e.bias_type != ITO_F32) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + col);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 q = __ldg(p + j);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16(e.bias_type, w[i]);
+                v[8 * j + 2 * i] += f.x;
+                v[8 * j + 2 * i + 1] += f.y;
+            }
+        }
+    } else if (a.b_vec && col + 32 <= a.N) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 q = __ldg(p + j);
+            v[4 * j] += q.x;
+            v[4 * j + 1] += q.y;
+            v[4 * j + 2] += q.z;
+            v[4 * j + 3] += q.w;
+        }
+    } else {
+        const int c = col + (threadIdx.x & 31);
+        const float mine = c < a.N ? load_typed(e.bias, e.bias_type, c) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
+    }
 }
 
 __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
-                                             float (&v)[64], const float* bias, uint8_t* stg, int lane, int col,
+                                             float (&v)[32], const uint32_t (&res)[16], FpStage& st, int col,
                                              int row)
 {
     const FpEpilogue& e = a.e;
-    if (e.bias) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float4 b = *reinterpret_cast<const float4*>(bias + 4 * j);
-            v[4 * j] += b.x;
-            v[4 * j + 1] += b.y;
-            v[4 * j + 2] += b.z;
-            v[4 * j + 3] += b.w;
-        }
-    }
-    if (e.z) box16(v, e.type, mapZ, a.z_tma, e.z, e.ldz, stg, lane, col, row, a.M, a.N);
+    const int lane = st.lane;
+    if (e.bias) add_bias(a, v, col);
+    if (e.z) store16(v, e.type, mapZ, a.z_tma, e.z, e.ldz, st, col, row, a.M, a.N);
     switch (e.act) {
     case ITO_ACT_RELU: activate<ITO_ACT_RELU>(v); break;
     case ITO_ACT_GELU: activate<ITO_ACT_GELU>(v); break;
@@ -151,76 +242,83 @@ __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensor
     case ITO_ACT_SILU: activate<ITO_ACT_SILU>(v); break;
     default: break;
     }
-    if (e.residual && row + lane < a.M) {
-        if (e.out_type == ITO_F32) {
-            const float* r = static_cast<const float*>(e.residual) + (row + lane) * e.ldr + col;
+    if (e.out_type != ITO_F32) {
+        if (e.residual) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (a.r_vec && col + 4 * j + 4 <= a.N) {
-                    const float4 q = *reinterpret_cast<const float4*>(r + 4 * j);
-                    v[4 * j] += q.x;
-                    v[4 * j + 1] += q.y;
-                    v[4 * j + 2] += q.z;
-                    v[4 * j + 3] += q.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (col + 4 * j + i < a.N) v[4 * j + i] += r[4 * j + i];
-                }
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = unpack16(e.out_type, res[i]);
+                v[2 * i] += f.x;
+                v[2 * i + 1] += f.y;
             }
-        } else {
-            const uint16_t* r = static_cast<const uint16_t*>(e.residual) + (row + lane) * e.ldr + col;
+        }
+        store16(v, e.out_type, mapY, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
+        return;
+    }
+    if (e.residual && row + lane < a.M) {
+        const float* r = static_cast<const float*>(e.residual) + (row + lane) * e.ldr + col;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (a.r_vec && col + 8 * j + 8 <= a.N) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(r + 8 * j);
-                    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-                } else {
+        for (int j = 0; j < 8; ++j) {
+            if (a.r_vec && col + 4 * j + 4 <= a.N) {
+                const float4 q = *reinterpret_cast<const float4*>(r + 4 * j);
+                v[4 * j] += q.x;
+                v[4 * j + 1] += q.y;
+                v[4 * j + 2] += q.z;
+                v[4 * j + 3] += q.w;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + 8 * j + i < a.N) w[i >> 1] |= (uint32_t)r[8 * j + i] << (16 * (i & 1));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack16(e.out_type, w[i]);
-                    v[8 * j + 2 * i] += f.x;
-                    v[8 * j + 2 * i + 1] += f.y;
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (col + 4 * j + i < a.N) v[4 * j + i] += r[4 * j + i];
             }
         }
     }
-    if (e.out_type != ITO_F32) {
-        box16(v, e.out_type, mapY, a.y_tma, e.y, e.ldy, stg, lane, col, row, a.M, a.N);
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (col + 32 * h >= a.N) continue;
-        stage32(v, h, stg, lane);
-        if (a.y_tma) box_end_tma(mapY, stg, lane, col + 32 * h, row);
-        else box_end_plain(e.y, true, e.ldy, stg, lane, col + 32 * h, row, a.M, a.N);
-    }
+    store32(v, mapY, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
 }
 
-// this warp's columns of the bias, in 32 bits, into shared memory (0 beyond the edge)
-__device__ __forceinline__ void stage_bias(const FpGemmArgs& a, float* bias, int cols, int col, int lane)
+// a warp's wait: one lane asks
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err)
 {
-    if (!a.e.bias) return;
-    __syncwarp();
-    for (int i = lane; i < cols; i += 32) bias[i] = col + i < a.N ? load_typed(a.e.bias, a.e.bias_type, col + i) : 0.0f;
-    __syncwarp();
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err);
+    return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-__device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[64])
+__device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32])
 {
     uint32_t r[32];
+    tmem_ld32(taddr, r);
+    tmem_ld_wait();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        tmem_ld32(taddr + 32 * h, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[32 * h + i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
+// (row, col0), sums at `taddr`; `done` tells the MMA thread that the accumulator is drained.
+template <typename Wait, typename Done>
+__device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
+                                           FpStage& st, int first, int step, int columns, int col0,
+                                           int row, uint32_t taddr, Wait wait, Done done, bool& ok)
+{
+    // a 16-bit residual comes while the sums are still being made
+    const bool res16 = a.e.residual && a.e.out_type != ITO_F32;
+    uint32_t res[16];
+    if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
+    if (!wait()) {
+        ok = false;
+        return;
+    }
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = first * 32; c < columns; c += step * 32) {
+        float v[32];
+        load_sums(taddr + c, v);
+        if (c + step * 32 >= columns) {
+            tc_fence_before();
+            __syncwarp();
+            done();
+        }
+        if (row >= a.M || col0 + c >= a.N) continue;
+        if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
+        finish_group(a, mapY, mapZ, v, res, st, col0 + c, row);
     }
 }
 
@@ -230,11 +328,12 @@ template <int BN>
 struct FpCfg {
     static constexpr int BM = 128, BK = 64;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int EPI_WARPS = BN / 16;            // 64 columns to a warp
+    static constexpr int EPI_WARPS = 8;                  // two to a quarter of the rows
+    static constexpr int GROUPS = BN / 64;               // of 32 columns to a warp
     static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int STAGES = BN == 128 ? 5 : 8;
-    static constexpr int STAGING_BYTES = EPI_WARPS * (4096 + 256);
+    static constexpr int STAGES = BN == 128 ? 5 : 6;
+    static constexpr int STAGING_BYTES = EPI_WARPS * kFpBoxes * kFpBox;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 };
 
@@ -249,7 +348,6 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + STAGES * Cfg::STAGE_BYTES;
-    float* biases = reinterpret_cast<float*>(staging + Cfg::EPI_WARPS * 4096);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING_BYTES);
     uint64_t* empty_bar = full_bar + STAGES;
     uint64_t* accf_bar = empty_bar + STAGES;
@@ -348,39 +446,48 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
         }
     } else {
         const int e = warp - 2, quad = warp & 3, part = e >> 2;
-        uint8_t* stg = staging + e * 4096;
-        float* bias = biases + e * 64;
+        FpStage st{staging + e * kFpBoxes * kFpBox, lane, 0};
         int buf = 0;
         uint32_t buf_phase = 0;
-        for (int w = blockIdx.x; w < num_items; w += gridDim.x) {
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
-            const int row = tm * BM + quad * 32, col = tn * BN + part * 64;
-            stage_bias(a, bias, 64, col, lane);
-            if (!mbar_wait(&accf_bar[buf], buf_phase, abort_flag, a.err)) break;
-            tc_fence_after();
-            float v[64];
-            load_sums(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN + part * 64), v);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acce_bar[buf]);
-            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
-            if (row >= a.M || col >= a.N) continue;
+            const int row = tm * BM + quad * 32, col = tn * BN;
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
             if (a.splits > 1) {
+                if (!warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err)) break;
+                tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (col + 32 * h >= a.N) continue;
-                    stage32(v, h, stg, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_3d(&mapS, stg, col + 32 * h, row, w % a.splits);
-                        bulk_commit();
+                for (int g = 0; g < Cfg::GROUPS; ++g) {
+                    const int c = (part + 2 * g) * 32;
+                    float v[32];
+                    load_sums(taddr + c, v);
+                    if (g + 1 == Cfg::GROUPS) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acce_bar[buf]);
+                    }
+                    if (row >= a.M || col + c >= a.N) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (col + c + 16 * h >= a.N) break;
+                        uint8_t* stg = stage32(v, h, st);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&mapS, stg, col + c + 16 * h, row, w % a.splits);
+                            bulk_commit();
+                        }
                     }
                 }
             } else {
-                finish_group(a, &mapY, &mapZ, v, bias, stg, lane, col, row);
+                drain_tile(
+                    a, &mapY, &mapZ, st, part, 2, BN, col, row, taddr,
+                    [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
+                    [&] { if (lane == 0) mbar_arrive(&acce_bar[buf]); }, ok);
             }
+            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
         if (lane == 0) bulk_wait_all();
     }
@@ -394,14 +501,17 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
 
 // ---------------------------------------------------------------- CTA pair
 
+// A tile is 256 rows by a.bn columns, 256 or fewer (a multiple of 32), so that the tiles of a
+// result come out near whole waves: 2048 x 4096 is 128 tiles of 256 columns, two waves of the
+// 76 pairs of which the second is two thirds full, or 152 tiles of 224 columns, two full ones.
 struct FpPairCfg {
-    static constexpr int BM = 128, BN = 256, BK = 64;
-    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = (BN / 2) * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int BM = 128, MAX_BN = 256, BK = 64;
+    static constexpr int A_BYTES = BM * BK * 2, B_BYTES = (MAX_BN / 2) * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 5;
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static constexpr int TMEM_COLS = 512;
-    static constexpr int STAGING_BYTES = EPI_WARPS * (4096 + 512);
+    static constexpr int STAGING_BYTES = EPI_WARPS * kFpBoxes * kFpBox;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 };
 
@@ -411,11 +521,11 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                    const __grid_constant__ FpGemmArgs a)
 {
     using Cfg = FpPairCfg;
-    constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, STAGES = Cfg::STAGES;
+    constexpr int BM = Cfg::BM, BK = Cfg::BK, STAGES = Cfg::STAGES;
+    const int bn = a.bn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + STAGES * Cfg::STAGE_BYTES;
-    float* biases = reinterpret_cast<float*>(staging + Cfg::EPI_WARPS * 4096);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING_BYTES);
     uint64_t* empty_bar = full_bar + STAGES;
     uint64_t* accf_bar = empty_bar + STAGES;
@@ -426,7 +536,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-    const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + BN - 1) / BN, a.group};
+    const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + bn - 1) / bn, a.group};
     const int num_tiles = tiles.num_m * tiles.num_n;
     const int num_kb = (a.K + BK - 1) / BK;
 
@@ -456,18 +566,20 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     griddep_launch_dependents();
 
     if (warp == 0) {
-        // both CTAs load; every load completes on the leader's barrier
+        // both CTAs load; every load completes on the leader's barrier. (An MN-major B comes in
+        // whole boxes of 64 columns, some beyond a narrow tile's half.)
         if (lane == 0) {
+            const uint32_t stage_bytes = 2 * (Cfg::A_BYTES + (a.b_mn ? Cfg::B_BYTES : (bn / 2) * BK * 2));
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int w = cluster; ok && w < num_tiles; w += nclusters) {
                 int tm, tn;
                 tiles.coords(w, tm, tn);
-                const int rowA = tm * 2 * BM + (int)rank * BM, rowB = tn * BN + (int)rank * (BN / 2);
+                const int rowA = tm * 2 * BM + (int)rank * BM, rowB = tn * bn + (int)rank * (bn / 2);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, a.err)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * Cfg::STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
                     const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
                     uint8_t* sA = smem + stage * Cfg::STAGE_BYTES;
                     uint8_t* sB = sA + Cfg::A_BYTES;
@@ -497,7 +609,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
             for (int w = cluster; ok && w < num_tiles; w += nclusters) {
                 if (!mbar_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * BN);
+                const uint32_t d = tmem_base + (uint32_t)(buf * Cfg::MAX_BN);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mbar_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
                     tc_fence_after();
@@ -516,31 +628,20 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
             }
         }
     } else {
-        // both CTAs: this CTA's 128 rows of the pair's tile, 128 columns to a warp
+        // both CTAs: this CTA's 128 rows of the pair's tile, two warps to 32 of them
         const int e = warp - 2, quad = warp & 3, part = e >> 2;
-        uint8_t* stg = staging + e * 4096;
-        float* bias = biases + e * 128;
+        FpStage st{staging + e * kFpBoxes * kFpBox, lane, 0};
         int buf = 0;
         uint32_t buf_phase = 0;
-        for (int w = cluster; w < num_tiles; w += nclusters) {
+        bool ok = true;
+        for (int w = cluster; ok && w < num_tiles; w += nclusters) {
             int tm, tn;
             tiles.coords(w, tm, tn);
-            const int row = tm * 2 * BM + (int)rank * BM + quad * 32, col = tn * BN + part * 128;
-            stage_bias(a, bias, 128, col, lane);
-            if (!mbar_wait(&accf_bar[buf], buf_phase, abort_flag, a.err)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                float v[64];
-                load_sums(tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN + part * 128 + g * 64), v);
-                if (g == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0));
-                }
-                if (row < a.M && col + 64 * g < a.N)
-                    finish_group(a, &mapY, &mapZ, v, bias + 64 * g, stg, lane, col + 64 * g, row);
-            }
+            drain_tile(
+                a, &mapY, &mapZ, st, part, Cfg::EPI_WARPS / 4, bn, tn * bn, tm * 2 * BM + (int)rank * BM + quad * 32,
+                tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN),
+                [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
+                [&] { if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
             if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
         if (lane == 0) bulk_wait_all();
@@ -590,7 +691,10 @@ struct FpPlan {
 };
 
 // A pair's tile takes four times a 128 x 128 tile's work on two SMs; pairs win once their tiles
-// occupy at least half of the device's pairs.
+// occupy at least half of the device's pairs. Their width is the one whose waves read the
+// fewest operand rows (256 of A and bn of B a tile: L2's rate paces the products), the wider one
+// among equals. 2048 x 4096 x 4096: 42.5 us with 224 columns, 47.6 with 256; 8192 x 4096 x 4096: 143 us
+// with 256, 199 with 160, whose waves compute fewer columns.
 static FpPlan fp_plan(int M, int N, int K)
 {
     FpPlan p{};
@@ -599,7 +703,19 @@ static FpPlan fp_plan(int M, int N, int K)
     p.kb_per_split = num_kb;
     const int64_t pair_tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
     p.pair = M > 128 && N > 128 && 4 * pair_tiles >= num_sms();
-    if (p.pair) return p;
+    if (p.pair) {
+        const int64_t pairs = num_sms() / 2;
+        int64_t best = INT64_MAX;
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + bn - 1) / bn);
+            const int64_t cost = (tiles + pairs - 1) / pairs * (256 + bn);
+            if (cost < best) {
+                best = cost;
+                p.bn = bn;
+            }
+        }
+        return p;
+    }
     const int64_t row_tiles = (M + 127) / 128;
     p.bn = row_tiles * ((N + 127) / 128) * 2 <= num_sms() || N <= 64 ? 64 : 128;
     const int64_t tiles = row_tiles * ((N + p.bn - 1) / p.bn);
@@ -621,18 +737,21 @@ size_t fp_gemm_ws_bytes(int M, int N, int K)
     return p.splits > 1 ? (size_t)p.splits * M * pad4(N) * sizeof(float) : 0;
 }
 
-// 2-D box map (128-byte swizzle) over a row-major tensor of 16-bit or 32-bit elements
-static int box_map(CUtensorMap* map, void* p, bool wide, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+// 2-D box map over a row-major tensor of 16-bit or 32-bit elements: rows of 128 bytes with the
+// 128-byte swizzle, or of 64 bytes with the 64-byte one
+static int box_map(CUtensorMap* map, void* p, bool wide, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                   int row_bytes = 128)
 {
     auto enc = get_encode();
     if (!enc) return set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     const int size = wide ? 4 : 2;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld * size};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / size), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p, dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ITO_OK : set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
@@ -706,19 +825,21 @@ int fp_gemm(const FpOperand& A, const FpOperand& B, int M, int N, int K, const F
     const bool wide = e.out_type == ITO_F32;
     a.y_tma = rows_aligned(e.y, e.ldy, wide ? 4 : 2, M);
     a.z_tma = e.z && rows_aligned(e.z, e.ldz, 2, M);
+    a.b_vec = aligned_to(e.bias, 16);
     a.r_vec = e.residual && rows_aligned(e.residual, e.ldr, wide ? 4 : 2, M);
-    a.idesc = fp_idesc(p.pair ? 256 : 128, p.pair ? 256 : p.bn, A.mn, B.mn, e.type == ITO_BF16);
+    a.bn = p.bn;
+    a.idesc = fp_idesc(p.pair ? 256 : 128, p.bn, A.mn, B.mn, e.type == ITO_BF16);
     CUtensorMap mA, mB, mY, mZ, mS;
     memset(&mY, 0, sizeof(mY));
     memset(&mZ, 0, sizeof(mZ));
     memset(&mS, 0, sizeof(mS));
     int r = box_map(&mA, const_cast<void*>(A.p), false, A.mn ? K : M, A.mn ? M : K, A.ld, A.mn ? 64 : 128);
-    if (!r) r = box_map(&mB, const_cast<void*>(B.p), false, B.mn ? K : N, B.mn ? N : K, B.ld, B.mn ? 64 : p.pair ? 128 : p.bn);
-    if (!r && a.y_tma) r = box_map(&mY, e.y, wide, M, N, e.ldy, 32);
-    if (!r && a.z_tma) r = box_map(&mZ, e.z, false, M, N, e.ldz, 32);
+    if (!r) r = box_map(&mB, const_cast<void*>(B.p), false, B.mn ? K : N, B.mn ? N : K, B.ld, B.mn ? 64 : p.pair ? p.bn / 2 : p.bn);
+    if (!r && a.y_tma) r = box_map(&mY, e.y, wide, M, N, e.ldy, 32, 64);
+    if (!r && a.z_tma) r = box_map(&mZ, e.z, false, M, N, e.ldz, 32, 64);
     if (r) return r;
     if (p.pair) {
-        const int tiles = ((M + 255) / 256) * ((N + 255) / 256), most = max_pairs();
+        const int tiles = ((M + 255) / 256) * ((N + p.bn - 1) / p.bn), most = max_pairs();
         if (!most) return set_error(ITO_ERR_CUDA, "no CTA pair fits on this device");
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (tiles < most ? tiles : most));
@@ -742,10 +863,10 @@ int fp_gemm(const FpOperand& A, const FpOperand& B, int M, int N, int K, const F
         auto enc = get_encode();
         cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)M, (cuuint64_t)p.splits};
         cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * M * 4};
-        cuuint32_t box[3] = {32, 32, 1};
+        cuuint32_t box[3] = {16, 32, 1};
         cuuint32_t estr[3] = {1, 1, 1};
         const CUresult cr = enc(&mS, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (cr != CUDA_SUCCESS) return set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled (partials) failed (%d)", (int)cr);
     }
