@@ -26,9 +26,17 @@ struct FpOperand {
     bool mn;
 };
 
-// C[m][n] = sum_k A(m, k) B(n, k) through the epilogue, on the tensor cores; ws: the bytes that
-// fp_gemm_ws_bytes names (partial sums of a product split along K), 256-byte aligned.
+// C[m][n] = sum_k A(m, k) B(n, k), m < M, n < N, k < K, through the epilogue
+struct FpProduct {
+    FpOperand A, B;
+    int M, N, K;
+    FpEpilogue e;
+};
+
+// One or two products that do not depend on one another, on the tensor cores; ws: the bytes that
+// fp_gemm_ws_bytes names for the larger need (partial sums of a product split along K), 256-byte
+// aligned.
 size_t fp_gemm_ws_bytes(int M, int N, int K);
-int fp_gemm(const FpOperand& A, const FpOperand& B, int M, int N, int K, const FpEpilogue& e, void* ws, cudaStream_t s);
+int fp_gemm(const FpProduct* products, int n, void* ws, cudaStream_t s);
 
 }  // namespace ito

@@ -52,15 +52,51 @@ struct FpGemmArgs {
     int* err;
 };
 
+// The producer's and the issuer's warps run their loops whole, so that what they count is uniform
+// over the warp, and one elected lane issues: loops of a single lane keep it in ordinary
+// registers, and moving it to the uniform ones that copies and products take their operands from
+// cost up to a tenth of a product's time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
+    return r != 0;
+}
+
+// all lanes wait; whether it came, for all of them alike
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+}
+
+// Shared-memory descriptors of the K steps of 16 in a stage: 32 bytes on inside the swizzled row
+// (K-major), 16 rows of 128 bytes on (MN-major). Addresses count 16 bytes in the descriptor's low
+// bits, so a step is one addition; the thread that issues the products has little time to spare.
+struct FpSteps {
+    uint64_t a0, b0;
+    uint32_t a_step, b_step;
+
+    __device__ __forceinline__ FpSteps(const FpGemmArgs& g, uint32_t smem, uint32_t a_bytes)
+    {
+        a0 = smem_desc_sw128(smem, g.a_mn ? 8192 : 16, 1024);
+        b0 = smem_desc_sw128(smem + a_bytes, g.b_mn ? 8192 : 16, 1024);
+        a_step = g.a_mn ? 2048 >> 4 : 32 >> 4;
+        b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
+    }
+    __device__ __forceinline__ uint64_t a(uint32_t at, int k) const { return a0 + (at + k * a_step); }
+    __device__ __forceinline__ uint64_t b(uint32_t at, int k) const { return b0 + (at + k * b_step); }
+};
+
 // ------------------------------------------------------------------ epilogue
 //
 // A warp holds 32 rows (its lanes) of 32 columns of sums at a time. Its results go through its
 // own buffers of shared memory, 32 rows of 64 bytes (16-byte chunk j of row r at j ^ (r / 2 % 4),
 // the 64-byte swizzle), and leave by TMA, which clips them at the tensor's edges, or, where rows
-// do not start on 16-byte boundaries, by coalesced plain stores. Four buffers to a warp: with
-// one, each box waited for the one before to be read, and a last tile's epilogue with
-// activation, residual and z took 35 us.
-constexpr int kFpBox = 2048, kFpBoxes = 4;
+// do not start on 16-byte boundaries, by coalesced plain stores. Two buffers to a warp (four
+// measured the same), because the operands' ring needs the room: its loads take about as long
+// as four stages' products, and 8192 x 4096 x 4096 took 220 us with four stages, 156 with five,
+// 144 with six.
+constexpr int kFpBox = 2048, kFpBoxes = 2;
 
 struct FpStage {
     uint8_t* p;
@@ -332,7 +368,7 @@ struct FpCfg {
     static constexpr int GROUPS = BN / 64;               // of 32 columns to a warp
     static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static constexpr int TMEM_COLS = 2 * BN;
-    static constexpr int STAGES = BN == 128 ? 5 : 6;
+    static constexpr int STAGES = BN == 128 ? 6 : 8;
     static constexpr int STAGING_BYTES = EPI_WARPS * kFpBoxes * kFpBox;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 };
@@ -385,16 +421,16 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
     griddep_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
-                int tm, tn;
-                tiles.coords(w / a.splits, tm, tn);
-                const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
-                for (int kb = lo; kb < hi; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, a.err)) { ok = false; break; }
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
+            int tm, tn;
+            tiles.coords(w / a.splits, tm, tn);
+            const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
+            for (int kb = lo; kb < hi; ++kb) {
+                if (!ring_wait(&empty_bar[stage], phase ^ 1, abort_flag, a.err)) { ok = false; break; }
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&full_bar[stage], Cfg::STAGE_BYTES);
                     uint8_t* sA = smem + stage * Cfg::STAGE_BYTES;
                     uint8_t* sB = sA + Cfg::A_BYTES;
@@ -411,38 +447,37 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
                         for (int j = 0; j < BN / 64; ++j)
                             tma_load_2d(&mapB, &full_bar[stage], sB + j * 8192, tn * BN + j * 64, kb * BK);
                     }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
+                __syncwarp();
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            bool ok = true;
-            // a 16-element K step: 32 bytes inside the swizzled row (K-major), 16 rows of 128 bytes (MN-major)
-            const uint32_t a_step = a.a_mn ? 2048 : 32, a_lbo = a.a_mn ? 8192 : 16;
-            const uint32_t b_step = a.b_mn ? 2048 : 32, b_lbo = a.b_mn ? 8192 : 16;
-            for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
-                const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
-                if (!mbar_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) break;
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true;
+        const FpSteps step(a, smem_u32(smem), Cfg::A_BYTES);
+        const uint32_t idesc = a.idesc;
+        for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
+            const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
+            if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(buf * BN);
+            for (int kb = lo; kb < hi; ++kb) {
+                if (!ring_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * BN);
-                for (int kb = lo; kb < hi; ++kb) {
-                    if (!mbar_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + stage * Cfg::STAGE_BYTES), b0 = a0 + Cfg::A_BYTES;
+                const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        tc_mma_bf16(d, smem_desc_sw128(a0 + k * a_step, a_lbo, 1024),
-                                    smem_desc_sw128(b0 + k * b_step, b_lbo, 1024), a.idesc, (kb > lo || k > 0) ? 1u : 0u);
+                        tc_mma_bf16(d, step.a(at, k), step.b(at, k), idesc, (kb > lo || k > 0) ? 1u : 0u);
                     tc_commit(&empty_bar[stage]);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                    if (kb + 1 == hi) tc_commit(&accf_bar[buf]);
                 }
-                if (!ok) break;
-                tc_commit(&accf_bar[buf]);
-                if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+                __syncwarp();
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
+            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
     } else {
         const int e = warp - 2, quad = warp & 3, part = e >> 2;
@@ -507,7 +542,7 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
 struct FpPairCfg {
     static constexpr int BM = 128, MAX_BN = 256, BK = 64;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = (MAX_BN / 2) * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 5;
+    static constexpr int STAGES = 6;
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static constexpr int TMEM_COLS = 512;
@@ -515,14 +550,54 @@ struct FpPairCfg {
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 };
 
+struct FpProblem {
+    CUtensorMap A, B, Y, Z;
+    FpGemmArgs a;
+};
+
+// One product, or two in one launch (the backward pass's), so that the second's tiles fill the
+// first's last wave. The tiles of problem 0, the one with the longer K, go round the pairs; of
+// its last round `rest` pairs have one, and the others meanwhile take `gap` tiles each of
+// problem 1, whose remaining tiles go round all pairs. At 2048 x 4096 x 4096 the two products
+// are 2 + 4 waves one by one, 7/8 of that together. A launch of one product has a kernel of its
+// own: with the second one's branches 8192 x 4096 x 4096 took 156 us instead of 144.
+template <int PROBLEMS>
+struct FpPairWork {
+    FpProblem p[PROBLEMS];
+    int tiles[2];
+    int rest, gap;
+
+    // item k of pair c of C
+    __device__ __forceinline__ bool item(int k, int c, int C, int& problem, int& tile) const
+    {
+        if (PROBLEMS == 1) {
+            problem = 0;
+            tile = c + k * C;
+            return tile < tiles[0];
+        }
+        const int n = c < tiles[0] ? (tiles[0] - 1 - c) / C + 1 : 0;
+        problem = 0;
+        tile = c + k * C;
+        if (k < n) return true;
+        k -= n;
+        problem = 1;
+        if (gap && c >= rest) {
+            tile = k * (C - rest) + c - rest;
+            if (k < gap) return tile < tiles[1];
+            k -= gap;
+        }
+        tile = gap * (C - rest) + k * C + c;
+        return tile < tiles[1];
+    }
+};
+
+template <int PROBLEMS>
 __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
-    k_fp_gemm_pair(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                   const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapZ,
-                   const __grid_constant__ FpGemmArgs a)
+    k_fp_gemm_pair(const __grid_constant__ FpPairWork<PROBLEMS> work)
 {
+    constexpr int LAST = PROBLEMS - 1;
     using Cfg = FpPairCfg;
     constexpr int BM = Cfg::BM, BK = Cfg::BK, STAGES = Cfg::STAGES;
-    const int bn = a.bn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + STAGES * Cfg::STAGE_BYTES;
@@ -536,9 +611,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-    const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + bn - 1) / bn, a.group};
-    const int num_tiles = tiles.num_m * tiles.num_n;
-    const int num_kb = (a.K + BK - 1) / BK;
+    int* const err = work.p[0].a.err;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -551,8 +624,11 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
         }
         *abort_flag = 0;
         fence_mbar_init();
-        prefetch_tensormap(&mapA);
-        prefetch_tensormap(&mapB);
+#pragma unroll
+        for (int i = 0; i < PROBLEMS; ++i) {
+            prefetch_tensormap(&work.p[i].A);
+            prefetch_tensormap(&work.p[i].B);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -565,65 +641,87 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
+    // a tile's place in its result
+    auto place = [&](const FpGemmArgs& a, int tile, int& row, int& col) {
+        const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + a.bn - 1) / a.bn, a.group};
+        int tm, tn;
+        tiles.coords(tile, tm, tn);
+        row = tm * 2 * BM + (int)rank * BM;
+        col = tn * a.bn;
+    };
+    int problem, tile;
     if (warp == 0) {
         // both CTAs load; every load completes on the leader's barrier. (An MN-major B comes in
         // whole boxes of 64 columns, some beyond a narrow tile's half.)
-        if (lane == 0) {
-            const uint32_t stage_bytes = 2 * (Cfg::A_BYTES + (a.b_mn ? Cfg::B_BYTES : (bn / 2) * BK * 2));
+        {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int w = cluster; ok && w < num_tiles; w += nclusters) {
-                int tm, tn;
-                tiles.coords(w, tm, tn);
-                const int rowA = tm * 2 * BM + (int)rank * BM, rowB = tn * bn + (int)rank * (bn / 2);
+            const uint32_t bar0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+            auto load = [&](const FpProblem& p) {
+                const FpGemmArgs& a = p.a;
+                const bool a_mn = a.a_mn, b_mn = a.b_mn;
+                const uint32_t stage_bytes = 2 * (Cfg::A_BYTES + (b_mn ? Cfg::B_BYTES : (a.bn / 2) * BK * 2));
+                const int num_kb = (a.K + BK - 1) / BK;
+                int rowA, rowB;
+                place(a, tile, rowA, rowB);
+                rowB += (int)rank * (a.bn / 2);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, abort_flag, a.err)) { ok = false; break; }
-                    if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
-                    const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
-                    uint8_t* sA = smem + stage * Cfg::STAGE_BYTES;
-                    uint8_t* sB = sA + Cfg::A_BYTES;
-                    if (!a.a_mn) {
-                        tma_load_2d_pair(&mapA, fb, sA, kb * BK, rowA);
-                    } else {
-                        tma_load_2d_pair(&mapA, fb, sA, rowA, kb * BK);
-                        tma_load_2d_pair(&mapA, fb, sA + 8192, rowA + 64, kb * BK);
+                    if (!ring_wait(&empty_bar[stage], phase ^ 1, abort_flag, err)) { ok = false; break; }
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
+                        const uint32_t fb = bar0 + stage * 8;
+                        uint8_t* sA = smem + stage * Cfg::STAGE_BYTES;
+                        uint8_t* sB = sA + Cfg::A_BYTES;
+                        if (!a_mn) {
+                            tma_load_2d_pair(&p.A, fb, sA, kb * BK, rowA);
+                        } else {
+                            tma_load_2d_pair(&p.A, fb, sA, rowA, kb * BK);
+                            tma_load_2d_pair(&p.A, fb, sA + 8192, rowA + 64, kb * BK);
+                        }
+                        if (!b_mn) {
+                            tma_load_2d_pair(&p.B, fb, sB, kb * BK, rowB);
+                        } else {
+                            tma_load_2d_pair(&p.B, fb, sB, rowB, kb * BK);
+                            tma_load_2d_pair(&p.B, fb, sB + 8192, rowB + 64, kb * BK);
+                        }
                     }
-                    if (!a.b_mn) {
-                        tma_load_2d_pair(&mapB, fb, sB, kb * BK, rowB);
-                    } else {
-                        tma_load_2d_pair(&mapB, fb, sB, rowB, kb * BK);
-                        tma_load_2d_pair(&mapB, fb, sB + 8192, rowB + 64, kb * BK);
-                    }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
+            };
+            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+                if (PROBLEMS == 1 || problem == 0) load(work.p[0]);
+                else load(work.p[LAST]);
             }
         }
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        if (leader) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
-            const uint32_t a_step = a.a_mn ? 2048 : 32, a_lbo = a.a_mn ? 8192 : 16;
-            const uint32_t b_step = a.b_mn ? 2048 : 32, b_lbo = a.b_mn ? 8192 : 16;
-            for (int w = cluster; ok && w < num_tiles; w += nclusters) {
-                if (!mbar_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) break;
+            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+                const FpGemmArgs& a = PROBLEMS == 1 || problem == 0 ? work.p[0].a : work.p[LAST].a;
+                const FpSteps step(a, smem_u32(smem), Cfg::A_BYTES);
+                const uint32_t idesc = a.idesc;
+                const int num_kb = (a.K + BK - 1) / BK;
+                if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, err)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(buf * Cfg::MAX_BN);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
+                    if (!ring_wait(&full_bar[stage], phase, abort_flag, err)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + stage * Cfg::STAGE_BYTES), b0 = a0 + Cfg::A_BYTES;
+                    const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        tc_mma_bf16_pair(d, smem_desc_sw128(a0 + k * a_step, a_lbo, 1024),
-                                         smem_desc_sw128(b0 + k * b_step, b_lbo, 1024), a.idesc,
-                                         (kb > 0 || k > 0) ? 1u : 0u);
-                    tc_commit_pair_mc(&empty_bar[stage], 0x3);
+                        for (int q = 0; q < BK / 16; ++q)
+                            tc_mma_bf16_pair(d, step.a(at, q), step.b(at, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
+                        tc_commit_pair_mc(&empty_bar[stage], 0x3);
+                        if (kb + 1 == num_kb) tc_commit_pair_mc(&accf_bar[buf], 0x3);
+                    }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                if (!ok) break;
-                tc_commit_pair_mc(&accf_bar[buf], 0x3);
                 if (++buf == 2) { buf = 0; buf_phase ^= 1; }
             }
         }
@@ -634,13 +732,14 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
         int buf = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
-        for (int w = cluster; ok && w < num_tiles; w += nclusters) {
-            int tm, tn;
-            tiles.coords(w, tm, tn);
+        for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+            const FpProblem& p = PROBLEMS == 1 || problem == 0 ? work.p[0] : work.p[LAST];
+            int row, col;
+            place(p.a, tile, row, col);
             drain_tile(
-                a, &mapY, &mapZ, st, part, Cfg::EPI_WARPS / 4, bn, tn * bn, tm * 2 * BM + (int)rank * BM + quad * 32,
+                p.a, &p.Y, &p.Z, st, part, Cfg::EPI_WARPS / 4, p.a.bn, col, row + quad * 32,
                 tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN),
-                [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
+                [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err); },
                 [&] { if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
             if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
@@ -692,10 +791,10 @@ struct FpPlan {
 
 // A pair's tile takes four times a 128 x 128 tile's work on two SMs; pairs win once their tiles
 // occupy at least half of the device's pairs. Their width is the one whose waves read the
-// fewest operand rows (256 of A and bn of B a tile: L2's rate paces the products), the wider one
-// among equals. 2048 x 4096 x 4096: 42.5 us with 224 columns, 47.6 with 256; 8192 x 4096 x 4096: 143 us
+// fewest operand rows (256 of A and bn of B a tile, an MN-major B in boxes of 64 to each block:
+// L2's rate paces the products), the wider one among equals. 2048 x 4096 x 4096: 42.5 us with 224 columns, 47.6 with 256; 8192 x 4096 x 4096: 143 us
 // with 256, 199 with 160, whose waves compute fewer columns.
-static FpPlan fp_plan(int M, int N, int K)
+static FpPlan fp_plan(int M, int N, int K, bool b_mn)
 {
     FpPlan p{};
     const int num_kb = (K + 63) / 64;
@@ -708,7 +807,7 @@ static FpPlan fp_plan(int M, int N, int K)
         int64_t best = INT64_MAX;
         for (int bn = 256; bn >= 128; bn -= 32) {
             const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + bn - 1) / bn);
-            const int64_t cost = (tiles + pairs - 1) / pairs * (256 + bn);
+            const int64_t cost = (tiles + pairs - 1) / pairs * (256 + (b_mn ? (bn + 127) / 128 * 128 : bn));
             if (cost < best) {
                 best = cost;
                 p.bn = bn;
@@ -733,7 +832,7 @@ static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
 size_t fp_gemm_ws_bytes(int M, int N, int K)
 {
-    const FpPlan p = fp_plan(M, N, K);
+    const FpPlan p = fp_plan(M, N, K, false);      // (slices do not depend on the operands' order)
     return p.splits > 1 ? (size_t)p.splits * M * pad4(N) * sizeof(float) : 0;
 }
 
@@ -771,12 +870,14 @@ static cudaError_t allow_smem(K kern, int bytes, bool* done)
     return e;
 }
 
+template <int PROBLEMS>
 static int max_pairs()
 {
     static int n = 0;
     static bool ready = false;
     if (n) return n;
-    if (allow_smem(k_fp_gemm_pair, FpPairCfg::SMEM_BYTES, &ready) != cudaSuccess) return 0;
+    const auto kern = k_fp_gemm_pair<PROBLEMS>;
+    if (allow_smem(kern, FpPairCfg::SMEM_BYTES, &ready) != cudaSuccess) return 0;
     cudaLaunchConfig_t q = {};
     q.gridDim = dim3(2 * num_sms());
     q.blockDim = dim3(FpPairCfg::THREADS);
@@ -789,7 +890,7 @@ static int max_pairs()
     q.attrs = at;
     q.numAttrs = 1;
     int got = 0;
-    if (cudaOccupancyMaxActiveClusters(&got, k_fp_gemm_pair, &q) == cudaSuccess && got > 0) n = got;
+    if (cudaOccupancyMaxActiveClusters(&got, kern, &q) == cudaSuccess && got > 0) n = got;
     return n;
 }
 
@@ -806,75 +907,127 @@ static int launch_single(const CUtensorMap& A, const CUtensorMap& B, const CUten
     return launch_status("linear product");
 }
 
-int fp_gemm(const FpOperand& A, const FpOperand& B, int M, int N, int K, const FpEpilogue& e, void* ws, cudaStream_t s)
+// the arguments and tensor maps that both kernels take
+static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p)
 {
-    const FpPlan p = fp_plan(M, N, K);
-    FpGemmArgs a;
-    memset(&a, 0, sizeof(a));
+    const FpEpilogue& e = c.e;
+    FpGemmArgs& a = q->a;
     a.e = e;
-    a.M = M;
-    a.N = N;
-    a.K = K;
-    a.a_mn = A.mn;
-    a.b_mn = B.mn;
+    a.M = c.M;
+    a.N = c.N;
+    a.K = c.K;
+    a.a_mn = c.A.mn;
+    a.b_mn = c.B.mn;
     a.group = 16;
+    a.bn = p.bn;
     a.splits = p.splits;
     a.kb_per_split = p.kb_per_split;
     a.err = device_error_word();
     if (!a.err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const bool wide = e.out_type == ITO_F32;
-    a.y_tma = rows_aligned(e.y, e.ldy, wide ? 4 : 2, M);
-    a.z_tma = e.z && rows_aligned(e.z, e.ldz, 2, M);
+    a.y_tma = rows_aligned(e.y, e.ldy, wide ? 4 : 2, c.M);
+    a.z_tma = e.z && rows_aligned(e.z, e.ldz, 2, c.M);
     a.b_vec = aligned_to(e.bias, 16);
-    a.r_vec = e.residual && rows_aligned(e.residual, e.ldr, wide ? 4 : 2, M);
-    a.bn = p.bn;
-    a.idesc = fp_idesc(p.pair ? 256 : 128, p.bn, A.mn, B.mn, e.type == ITO_BF16);
-    CUtensorMap mA, mB, mY, mZ, mS;
-    memset(&mY, 0, sizeof(mY));
-    memset(&mZ, 0, sizeof(mZ));
-    memset(&mS, 0, sizeof(mS));
-    int r = box_map(&mA, const_cast<void*>(A.p), false, A.mn ? K : M, A.mn ? M : K, A.ld, A.mn ? 64 : 128);
-    if (!r) r = box_map(&mB, const_cast<void*>(B.p), false, B.mn ? K : N, B.mn ? N : K, B.ld, B.mn ? 64 : p.pair ? p.bn / 2 : p.bn);
-    if (!r && a.y_tma) r = box_map(&mY, e.y, wide, M, N, e.ldy, 32, 64);
-    if (!r && a.z_tma) r = box_map(&mZ, e.z, false, M, N, e.ldz, 32, 64);
-    if (r) return r;
-    if (p.pair) {
-        const int tiles = ((M + 255) / 256) * ((N + p.bn - 1) / p.bn), most = max_pairs();
-        if (!most) return set_error(ITO_ERR_CUDA, "no CTA pair fits on this device");
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (tiles < most ? tiles : most));
-        cfg.blockDim = dim3(FpPairCfg::THREADS);
-        cfg.dynamicSmemBytes = FpPairCfg::SMEM_BYTES;
-        cfg.stream = s;
-        cudaLaunchAttribute at[2];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2;
-        at[0].val.clusterDim.y = 1;
-        at[0].val.clusterDim.z = 1;
-        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 2;
-        const cudaError_t ce = cudaLaunchKernelEx(&cfg, k_fp_gemm_pair, mA, mB, mY, mZ, a);
-        return ce == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "linear product launch: %s", cudaGetErrorString(ce));
+    a.r_vec = e.residual && rows_aligned(e.residual, e.ldr, wide ? 4 : 2, c.M);
+    a.idesc = fp_idesc(p.pair ? 256 : 128, p.bn, c.A.mn, c.B.mn, e.type == ITO_BF16);
+    int r = box_map(&q->A, const_cast<void*>(c.A.p), false, c.A.mn ? c.K : c.M, c.A.mn ? c.M : c.K, c.A.ld,
+                    c.A.mn ? 64 : 128);
+    if (!r)
+        r = box_map(&q->B, const_cast<void*>(c.B.p), false, c.B.mn ? c.K : c.N, c.B.mn ? c.N : c.K, c.B.ld,
+                    c.B.mn ? 64 : p.pair ? p.bn / 2 : p.bn);
+    if (!r && a.y_tma) r = box_map(&q->Y, e.y, wide, c.M, c.N, e.ldy, 32, 64);
+    if (!r && a.z_tma) r = box_map(&q->Z, e.z, false, c.M, c.N, e.ldz, 32, 64);
+    return r;
+}
+
+static int pair_tiles(const FpProblem& q) { return ((q.a.M + 255) / 256) * ((q.a.N + q.a.bn - 1) / q.a.bn); }
+
+template <int PROBLEMS>
+static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
+{
+    const int most = max_pairs<PROBLEMS>();
+    if (!most) return set_error(ITO_ERR_CUDA, "no CTA pair fits on this device");
+    const int tiles = w.tiles[0] + w.tiles[1], pairs = tiles < most ? tiles : most;
+    w.rest = w.gap = 0;
+    if (PROBLEMS == 2) {
+        w.rest = w.tiles[0] % pairs;
+        // (K blocks tell a tile's time: both problems' tiles have the same width or nearly)
+        if (w.rest) w.gap = ((w.p[0].a.K + 63) / 64) / ((w.p[PROBLEMS - 1].a.K + 63) / 64);
     }
-    const int64_t pitch = pad4(N);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(FpPairCfg::THREADS);
+    cfg.dynamicSmemBytes = FpPairCfg::SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp_gemm_pair<PROBLEMS>, w);
+    return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "linear product launch: %s", cudaGetErrorString(e));
+}
+
+static int run_single(const FpProduct& c, const FpPlan& p, void* ws, cudaStream_t s)
+{
+    FpProblem q;
+    memset(&q, 0, sizeof(q));
+    int r = fill_problem(&q, c, p);
+    if (r) return r;
+    CUtensorMap S;
+    memset(&S, 0, sizeof(S));
+    const int64_t pitch = pad4(c.N);
     if (p.splits > 1) {
         auto enc = get_encode();
-        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)M, (cuuint64_t)p.splits};
-        cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * M * 4};
+        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)c.M, (cuuint64_t)p.splits};
+        cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * c.M * 4};
         cuuint32_t box[3] = {16, 32, 1};
         cuuint32_t estr[3] = {1, 1, 1};
-        const CUresult cr = enc(&mS, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
+        const CUresult cr = enc(&S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (cr != CUDA_SUCCESS) return set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled (partials) failed (%d)", (int)cr);
     }
-    r = p.bn == 128 ? launch_single<128>(mA, mB, mY, mZ, mS, a, s) : launch_single<64>(mA, mB, mY, mZ, mS, a, s);
+    r = p.bn == 128 ? launch_single<128>(q.A, q.B, q.Y, q.Z, S, q.a, s) : launch_single<64>(q.A, q.B, q.Y, q.Z, S, q.a, s);
     if (r || p.splits == 1) return r;
-    launch_pdl(k_fp_join, launch_grid_blocks((int64_t)M * (pitch / 4), 256), 256, 0, s, static_cast<const float*>(ws),
-               p.splits, pitch * M, (int)pitch, M, N, e);
+    launch_pdl(k_fp_join, launch_grid_blocks((int64_t)c.M * (pitch / 4), 256), 256, 0, s, static_cast<const float*>(ws),
+               p.splits, pitch * c.M, (int)pitch, c.M, c.N, c.e);
     return launch_status("linear join");
+}
+
+int fp_gemm(const FpProduct* c, int n, void* ws, cudaStream_t s)
+{
+    FpPlan p[2];
+    for (int i = 0; i < n; ++i) p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn);
+    if (n == 2 && p[0].pair && p[1].pair) {
+        FpPairWork<2> w;
+        memset(&w, 0, sizeof(w));
+        const int first = c[0].K >= c[1].K ? 0 : 1;
+        for (int i = 0; i < 2; ++i) {
+            const int r = fill_problem(&w.p[i], c[first ^ i], p[first ^ i]);
+            if (r) return r;
+            w.tiles[i] = pair_tiles(w.p[i]);
+        }
+        return launch_pairs(w, s);
+    }
+    for (int i = 0; i < n; ++i) {
+        int r;
+        if (p[i].pair) {
+            FpPairWork<1> w;
+            memset(&w, 0, sizeof(w));
+            r = fill_problem(&w.p[0], c[i], p[i]);
+            w.tiles[0] = pair_tiles(w.p[0]);
+            if (!r) r = launch_pairs(w, s);
+        } else {
+            r = run_single(c[i], p[i], ws, s);
+        }
+        if (r) return r;
+    }
+    return ITO_OK;
 }
 
 }  // namespace ito

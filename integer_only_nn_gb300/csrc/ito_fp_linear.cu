@@ -355,7 +355,8 @@ int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, co
     char* ws = static_cast<char*>(workspace);
     const void* xa = aligned_operand(x, &ldx, B, IC, &ws, s);
     const void* wa = aligned_operand(W, &ldw, OC, IC, &ws, s);
-    return fp_gemm(FpOperand{xa, ldx, false}, FpOperand{wa, ldw, false}, B, OC, IC, e, ws, s);
+    const FpProduct product{FpOperand{xa, ldx, false}, FpOperand{wa, ldw, false}, B, OC, IC, e};
+    return fp_gemm(&product, 1, ws, s);
 }
 
 size_t ito_fp_linear_bwd_workspace_size(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* W,
@@ -418,23 +419,26 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
     char* wx = ws;
     char* ww = wx + copy_bytes(x, ldx, B, IC);
     char* wp = ww + copy_bytes(W, ldw, OC, IC);
+    FpProduct products[2];
+    int n = 0;
     if (dx) {
         const void* wa = aligned_operand(W, &ldw, OC, IC, &ww, s);
         FpEpilogue e{};
         e.type = e.out_type = type;
         e.y = dx;
         e.ldy = lddx;
-        r = fp_gemm(FpOperand{d, ldd, false}, FpOperand{wa, ldw, true}, B, IC, OC, e, wp, s);
+        products[n++] = FpProduct{FpOperand{d, ldd, false}, FpOperand{wa, ldw, true}, B, IC, OC, e};
     }
-    if (!r && dW) {
+    if (dW) {
         const void* xa = aligned_operand(x, &ldx, B, IC, &wx, s);
         FpEpilogue e{};
         e.type = type;
         e.out_type = out_type;
         e.y = dW;
         e.ldy = lddw;
-        r = fp_gemm(FpOperand{d, ldd, true}, FpOperand{xa, ldx, true}, OC, IC, B, e, wp, s);
+        products[n++] = FpProduct{FpOperand{d, ldd, true}, FpOperand{xa, ldx, true}, OC, IC, B, e};
     }
+    if (n) r = fp_gemm(products, n, wp, s);
     return r ? r : launch_status("linear backward");
 }
 
