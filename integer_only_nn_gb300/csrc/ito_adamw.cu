@@ -20,6 +20,7 @@
 // because (1 - b2) g^2 moves it by about 1/1000 a step. So both moments round
 // stochastically: up with the probability of the part cut off, from a 32-bit mix of seed,
 // step, tensor and element. The weight's own step uses the moments before they are rounded.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -39,19 +40,29 @@ struct AdamEntry {
     void* v;
     int8_t* m_exp;
     int8_t* v_exp;
-    int64_t n;
+    int64_t n, from;        // elements; the first that this launch takes (a multiple of 128)
     uint32_t first_chunk;   // of this launch's chunks
     float decay;            // 1 - lr wd
     int32_t vec;            // the pointers allow four elements at a time
     uint32_t salt;          // the tensor's share of the rounding's key
 };
 
-constexpr int kAdamEntries = 48;     // of 80 bytes: the table is a kernel argument (4 KB at most)
+constexpr int kAdamEntries = 44;     // of 88 bytes: the table is a kernel argument (4 KB at most)
 
 struct AdamTable {
     int32_t n;
     AdamEntry e[kAdamEntries];
 };
+
+__device__ __forceinline__ int find_entry(const AdamTable& tab, uint32_t chunk)
+{
+    int lo = 0, hi = tab.n - 1;          // the tensor that holds the chunk
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tab.e[mid].first_chunk <= chunk) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
 
 struct AdamConst {
     float b1, c1, b2, c2, eps, inv_sqrt_bc2, alpha, grad_scale;
@@ -81,14 +92,21 @@ __device__ __forceinline__ void round_bits(uint32_t h, uint32_t& um, uint32_t& u
     uv = (h * 0x510E527Fu) >> 12;
 }
 
-// the value of byte j of four codes under the exponent e (not -128)
+// What a byte's exponent and mantissa are added to under the exponent e (not -128).
 template <bool SECOND>
-__device__ __forceinline__ float moment_value(uint32_t codes, int j, int e)
+__device__ __forceinline__ uint32_t moment_base(int e)
 {
-    // the byte at the top of a word, moved down to the exponent's and mantissa's place
-    const uint32_t c = codes << (24 - 8 * j);
-    const uint32_t mag = SECOND ? c >> 4 & 0x0FF00000u : c >> 4 & 0x07F00000u;
-    const uint32_t r = mag ? mag + ((uint32_t)(e + (SECOND ? 96 : 112)) << 23) : 0u;
+    return (uint32_t)(e + (SECOND ? 96 : 112)) << 23;
+}
+
+// the value of byte j of four codes
+template <bool SECOND>
+__device__ __forceinline__ float moment_value(uint32_t codes, int j, uint32_t base)
+{
+    // the byte at the top of a word; its exponent and mantissa belong four bits lower
+    const uint32_t c = __byte_perm(codes, 0u, (uint32_t)j << 12 | 0x0444u);
+    const uint32_t mag = SECOND ? c : c & 0x7F000000u;
+    const uint32_t r = mag ? __umulhi(mag, 0x10000000u) + base : 0u;
     return __uint_as_float(SECOND ? r : r | (c & 0x80000000u));
 }
 
@@ -101,17 +119,27 @@ __device__ __forceinline__ int moment_exponent(uint32_t top)
     return max(e, SECOND ? -95 : -111);
 }
 
-// The code of x under the exponent e: its bits, counted from the lowest binade, plus a random
+// The code of x: its bits, counted from the lowest binade (base: moment_base), plus a random
 // part of the step that is cut off. Below the lowest binade the count is negative and the code
-// 0, or 1 for a v above zero.
+// 0, or 1 for a v above zero. Finite values above 1.875 * 2^127 are clamped to it first (top:
+// the block's largest, the same for all of its lanes).
 template <bool SECOND>
-__device__ __forceinline__ uint32_t moment_code(float x, int e, uint32_t u)
+__device__ __forceinline__ uint32_t moment_code(float x, uint32_t top, uint32_t base, uint32_t u)
 {
-    const uint32_t bits = __float_as_uint(x), mag = SECOND ? bits : bits & 0x7FFFFFFFu;
-    const int t = (int)min(mag, 0x7F700000u) - ((e + (SECOND ? 96 : 112)) << 23);
-    const int c = (t + (int)u) >> 20;
+    const uint32_t bits = __float_as_uint(x);
+    uint32_t mag = SECOND ? bits : bits & 0x7FFFFFFFu;
+    if (top > 0x7F700000u) mag = min(mag, 0x7F700000u);
+    const int c = (int)(mag - base + u) >> 20;
     if (SECOND) return (uint32_t)max(c, (int)min(mag, 1u));
     return c > 0 ? (uint32_t)c | (bits >> 24 & 128u) : 0u;
+}
+
+// the larger magnitude; a NaN wins
+__device__ __forceinline__ float larger(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
 // ------------------------------------------------------------------- the step
@@ -198,8 +226,8 @@ struct AdamPiece {
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                m[j] = moment_value<false>(m8, j, em);
-                v[j] = moment_value<true>(v8, j, ev);
+                m[j] = moment_value<false>(m8, j, moment_base<false>(em));
+                v[j] = moment_value<true>(v8, j, moment_base<true>(ev));
             }
             if (em == -128 || ev == -128) {
                 // a NaN block; elements beyond the tensor's end are not to reach the maxima
@@ -211,16 +239,16 @@ struct AdamPiece {
                 }
             }
         }
-        uint32_t tm = 0, tv = 0;
+        float most_m = 0.0f, most_v = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             adam_element(k, e.decay, g[j], wf[j], m[j], v[j]);
-            tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            tv = max(tv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            most_m = larger(most_m, m[j]);
+            most_v = larger(most_v, v[j]);
         }
         if (BITS == 8) {
-            tm = __reduce_max_sync(0xffffffffu, tm);
-            tv = __reduce_max_sync(0xffffffffu, tv);
+            const uint32_t tm = __reduce_max_sync(0xffffffffu, __float_as_uint(most_m));
+            const uint32_t tv = __reduce_max_sync(0xffffffffu, __float_as_uint(most_v));
             em = moment_exponent<false>(tm);
             ev = moment_exponent<true>(tv);
             const uint32_t h0 = round_key(k.key + e.salt, b);
@@ -230,8 +258,8 @@ struct AdamPiece {
                 uint32_t um, uv;
                 // (the low half of the element's index is below its block's end: no carry)
                 round_bits(h0 + (uint32_t)(VEC ? lane * 4 + j : j * 32 + lane) * kMixIndex, um, uv);
-                mc[j] = moment_code<false>(m[j], em, um);
-                vc[j] = moment_code<true>(v[j], ev, uv);
+                mc[j] = moment_code<false>(m[j], tm, moment_base<false>(em), um);
+                vc[j] = moment_code<true>(v[j], tv, moment_base<true>(ev), uv);
             }
             m8 = mc[0] | mc[1] << 8 | mc[2] << 16 | mc[3] << 24;
             v8 = vc[0] | vc[1] << 8 | vc[2] << 16 | vc[3] << 24;
@@ -297,22 +325,183 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
 {
     griddep_wait();
     griddep_launch_dependents();
-    int lo = 0, hi = tab.n - 1;          // the tensor whose chunks hold this block's
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tab.e[mid].first_chunk <= blockIdx.x) lo = mid; else hi = mid - 1;
-    }
-    const AdamEntry& e = tab.e[lo];
-    const int64_t base = (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
+    const AdamEntry& e = tab.e[find_entry(tab, blockIdx.x)];
+    const int64_t base = e.from + (int64_t)(blockIdx.x - e.first_chunk) * kAdamChunk;
     const int64_t end = min(e.n, base + kAdamChunk);
     if (e.vec) adam_chunk<G, C, BITS, true, 2>(e, k, base, end);
     else adam_chunk<G, C, BITS, false, 1>(e, k, base, end);
 }
 
+// ------------------------------------------------------ whole chunks, 8-bit moments
+//
+// The step reads 8 and writes 8 bytes an element (bf16 gradients and copies), with about 85
+// instructions between: memory and issue take about the same time, so loads may not wait for
+// arithmetic. A producer thread keeps a ring of chunks of 4096 elements coming into shared
+// memory by bulk copies, and sixteen warps walk over them, half a warp to a block of 128
+// elements, eight elements to a lane. Chunks whose arrays start on 16-byte boundaries come here;
+// the rest (a tensor's last part, odd places) takes k_adamw.
+constexpr int kRingChunk = 4096;
+constexpr int kRingTensor = 16 * kRingChunk;     // elements of a tensor from which it goes this way
+constexpr int kRingWarps = 16;
+constexpr int kRingThreads = (kRingWarps + 1) * 32;
+
+template <typename G>
+struct RingCfg {
+    static constexpr int G_AT = kRingChunk * 4, M_AT = G_AT + kRingChunk * (int)sizeof(G), V_AT = M_AT + kRingChunk;
+    static constexpr int BYTES = V_AT + kRingChunk;
+    static constexpr int STAGES = 200 * 1024 / BYTES;
+};
+
+template <typename G, typename C>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    k_adamw_ring(const __grid_constant__ AdamTable tab, const AdamConst k, uint32_t chunks, int* __restrict__ err)
+{
+    using Cfg = RingCfg<G>;
+    constexpr int STAGES = Cfg::STAGES;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t full[STAGES], empty[STAGES];
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kRingWarps);
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    int stage = 0;
+    uint32_t phase = 0;
+    if (warp == kRingWarps) {
+        if (lane) return;
+        for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+            const AdamEntry& e = tab.e[find_entry(tab, c)];
+            const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
+            if (!mbar_wait(&empty[stage], phase ^ 1, &abort_flag, err)) return;
+            uint8_t* p = smem + stage * Cfg::BYTES;
+            mbar_arrive_expect_tx(&full[stage], Cfg::BYTES);
+            bulk_load(p, e.w + base, kRingChunk * 4, &full[stage]);
+            bulk_load(p + Cfg::G_AT, static_cast<const G*>(e.g) + base, kRingChunk * sizeof(G), &full[stage]);
+            bulk_load(p + Cfg::M_AT, static_cast<const uint8_t*>(e.m) + base, kRingChunk, &full[stage]);
+            bulk_load(p + Cfg::V_AT, static_cast<const uint8_t*>(e.v) + base, kRingChunk, &full[stage]);
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        return;
+    }
+    const int half = lane >> 4, hl = lane & 15;
+    const int block = warp * 2 + half, at = block * kAdamBlock + hl * 4;     // and at + 64
+    int em = 0, ev = 0;                  // the next chunk's exponents come one chunk ahead
+    if (blockIdx.x < chunks) {
+        const AdamEntry& e = tab.e[find_entry(tab, blockIdx.x)];
+        const int64_t b = (int64_t)(blockIdx.x - e.first_chunk) * (kRingChunk / kAdamBlock) + block;
+        em = e.m_exp[b];
+        ev = e.v_exp[b];
+    }
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const AdamEntry& e = tab.e[find_entry(tab, c)];
+        const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
+        int em_next = 0, ev_next = 0;
+        if (c + gridDim.x < chunks) {
+            const AdamEntry& n = tab.e[find_entry(tab, c + gridDim.x)];
+            const int64_t b = (int64_t)(c + gridDim.x - n.first_chunk) * (kRingChunk / kAdamBlock) + block;
+            em_next = n.m_exp[b];
+            ev_next = n.v_exp[b];
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, &abort_flag, err))) return;
+        const uint8_t* p = smem + stage * Cfg::BYTES;
+        float w[8], g[8], m[8], v[8];
+        uint32_t mc[2], vc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = at + 64 * h;
+            const float4 q = *reinterpret_cast<const float4*>(p + i * 4);
+            w[4 * h] = q.x; w[4 * h + 1] = q.y; w[4 * h + 2] = q.z; w[4 * h + 3] = q.w;
+            if constexpr (sizeof(G) == 4) {
+                const float4 r = *reinterpret_cast<const float4*>(p + Cfg::G_AT + i * 4);
+                g[4 * h] = r.x; g[4 * h + 1] = r.y; g[4 * h + 2] = r.z; g[4 * h + 3] = r.w;
+            } else {
+                const uint2 r = *reinterpret_cast<const uint2*>(p + Cfg::G_AT + i * 2);
+                g[4 * h] = Vec<G>::lane16(r.x, 0);
+                g[4 * h + 1] = Vec<G>::lane16(r.x, 1);
+                g[4 * h + 2] = Vec<G>::lane16(r.y, 0);
+                g[4 * h + 3] = Vec<G>::lane16(r.y, 1);
+            }
+            mc[h] = *reinterpret_cast<const uint32_t*>(p + Cfg::M_AT + i);
+            vc[h] = *reinterpret_cast<const uint32_t*>(p + Cfg::V_AT + i);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        const uint32_t base_m = moment_base<false>(em), base_v = moment_base<true>(ev);
+        float most_m = 0.0f, most_v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = moment_value<false>(mc[j >> 2], j & 3, base_m);
+            v[j] = moment_value<true>(vc[j >> 2], j & 3, base_v);
+        }
+        if (em == -128 || ev == -128)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (em == -128) m[j] = __uint_as_float(0x7FC00000u);
+                if (ev == -128) v[j] = __uint_as_float(0x7FC00000u);
+            }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            adam_element(k, e.decay, g[j], w[j], m[j], v[j]);
+            most_m = larger(most_m, m[j]);
+            most_v = larger(most_v, v[j]);
+        }
+        uint32_t tm = __float_as_uint(most_m), tv = __float_as_uint(most_v);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            tm = max(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+            tv = max(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+        }
+        em = moment_exponent<false>(tm);
+        ev = moment_exponent<true>(tv);
+        const uint32_t to_m = moment_base<false>(em), to_v = moment_base<true>(ev);
+        const uint32_t h0 = round_key(k.key + e.salt, base + at);
+        C* copy = static_cast<C*>(e.copy);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t cm[4], cv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t um, uv;
+                // (chunks do not straddle a multiple of 2^32: no carry)
+                round_bits(h0 + (uint32_t)(64 * h + j) * kMixIndex, um, uv);
+                cm[j] = moment_code<false>(m[4 * h + j], tm, to_m, um);
+                cv[j] = moment_code<true>(v[4 * h + j], tv, to_v, uv);
+            }
+            uint32_t m8 = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410);
+            uint32_t v8 = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
+            if (em == -128) m8 = 0u;
+            if (ev == -128) v8 = 0u;
+            const int64_t i = base + at + 64 * h;
+            *reinterpret_cast<float4*>(e.w + i) = make_float4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+            if (copy)
+                *reinterpret_cast<uint2*>(copy + i) = make_uint2(Vec<C>::pair16(w[4 * h], w[4 * h + 1]),
+                                                                 Vec<C>::pair16(w[4 * h + 2], w[4 * h + 3]));
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + i) = m8;
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + i) = v8;
+        }
+        if (hl == 0) {
+            const int64_t b = base / kAdamBlock + block;
+            e.m_exp[b] = (int8_t)em;
+            e.v_exp[b] = (int8_t)ev;
+        }
+        em = em_next;
+        ev = ev_next;
+    }
+}
+
 template <bool SECOND>
 __device__ __forceinline__ float moment_or_nan(uint32_t codes, int j, int e)
 {
-    return e == -128 ? __uint_as_float(0x7FC00000u) : moment_value<SECOND>(codes, j, e);
+    return e == -128 ? __uint_as_float(0x7FC00000u) : moment_value<SECOND>(codes, j, moment_base<SECOND>(e));
 }
 
 // The values of 8-bit moments, the tensors one after another in m_out and v_out.
@@ -379,18 +568,72 @@ __global__ void __launch_bounds__(kAdamThreads)
 // ------------------------------------------------------------------- launchers
 
 template <typename G, typename C>
-static void launch_adamw(const AdamTable& t, const AdamConst& k, int bits, uint32_t chunks, cudaStream_t s)
+static int launch_ring(const AdamTable& t, const AdamConst& k, uint32_t chunks, cudaStream_t s)
 {
+    constexpr int kBytes = RingCfg<G>::STAGES * RingCfg<G>::BYTES;
+    if (cudaFuncSetAttribute(k_adamw_ring<G, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
+        return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
+    int* err = device_error_word();
+    if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
+    launch_pdl(k_adamw_ring<G, C>, std::min<uint32_t>(chunks, num_sms()), kRingThreads, kBytes, s, t, k, chunks, err);
+    return launch_status("adamw");
+}
+
+// ring: whole chunks of 8-bit states
+template <typename G, typename C>
+static int launch_adamw(const AdamTable& t, const AdamConst& k, int bits, bool ring, uint32_t chunks, cudaStream_t s)
+{
+    if (ring) return launch_ring<G, C>(t, k, chunks, s);
     if (bits == 8) launch_pdl(k_adamw<G, C, 8>, chunks, kAdamThreads, 0, s, t, k);
     else launch_pdl(k_adamw<G, C, 32>, chunks, kAdamThreads, 0, s, t, k);
+    return launch_status("adamw");
 }
 
 template <typename G>
-static void launch_adamw(const AdamTable& t, const AdamConst& k, int bits, int copy_type, uint32_t chunks,
-                         cudaStream_t s)
+static int launch_adamw(const AdamTable& t, const AdamConst& k, int bits, bool ring, int copy_type, uint32_t chunks,
+                        cudaStream_t s)
 {
-    if (copy_type == ITO_F16) launch_adamw<G, __half>(t, k, bits, chunks, s);
-    else launch_adamw<G, __nv_bfloat16>(t, k, bits, chunks, s);
+    if (copy_type == ITO_F16) return launch_adamw<G, __half>(t, k, bits, ring, chunks, s);
+    return launch_adamw<G, __nv_bfloat16>(t, k, bits, ring, chunks, s);
+}
+
+// The parts of the tensors that one kernel takes, in launches of up to kAdamEntries tensors: the
+// whole chunks of `whole` tensors (ring), or what that leaves.
+static int run_adamw(const ito_adamw_tensor* tensors, int n_tensors, const ito_adamw_params* p, const AdamConst& k,
+                     bool ring, int64_t ring_from, cudaStream_t s)
+{
+    const size_t g_size = type_bytes(p->grad_type);
+    AdamTable tab;
+    for (int i = 0; i < n_tensors;) {
+        tab.n = 0;
+        uint64_t chunks = 0;
+        for (; i < n_tensors && tab.n < kAdamEntries; ++i) {
+            const ito_adamw_tensor& a = tensors[i];
+            const bool aligned = aligned_to(a.w, 16) && aligned_to(a.g, 16) && aligned_to(a.m, 16) &&
+                                 aligned_to(a.v, 16) && aligned_to(a.copy, 8);
+            // elements that the ring takes of this tensor
+            const int64_t whole = ring_from && aligned && a.n >= ring_from ? a.n / kRingChunk * kRingChunk : 0;
+            const int64_t from = ring ? 0 : whole, n = ring ? whole : a.n;
+            const uint64_t c = ring ? (uint64_t)(n / kRingChunk) : (uint64_t)(n - from + kAdamChunk - 1) / kAdamChunk;
+            if (chunks + c > 0x7fffffffu) break;
+            if (!c) continue;
+            const size_t state = p->state_bits == 32 ? 16 : 4;
+            const int vec = aligned_to(a.w, 16) && aligned_to(a.g, 4 * g_size) && aligned_to(a.copy, 8) &&
+                            aligned_to(a.m, state) && aligned_to(a.v, state);
+            AdamEntry& e = tab.e[tab.n++];
+            e = AdamEntry{a.w, a.g, a.copy, a.m, a.v, a.m_exp, a.v_exp, n, from, (uint32_t)chunks,
+                          (float)(1.0 - p->lr * a.weight_decay), vec, (uint32_t)i * 0x510E527Fu};
+            chunks += c;
+        }
+        if (!chunks) continue;
+        int r;
+        if (p->grad_type == ITO_F32) r = launch_adamw<float>(tab, k, p->state_bits, ring, p->copy_type, (uint32_t)chunks, s);
+        else if (p->grad_type == ITO_BF16)
+            r = launch_adamw<__nv_bfloat16>(tab, k, p->state_bits, ring, p->copy_type, (uint32_t)chunks, s);
+        else r = launch_adamw<__half>(tab, k, p->state_bits, ring, p->copy_type, (uint32_t)chunks, s);
+        if (r) return r;
+    }
+    return ITO_OK;
 }
 
 static int check_tensor(const ito_adamw_tensor& a, int i, int bits)
@@ -443,32 +686,16 @@ int ito_adamw_step(const ito_adamw_tensor* tensors, int n_tensors, const ito_ada
     k.grad_scale = (float)p->grad_scale;
     k.key = p->seed + (uint32_t)(uint64_t)p->step * 0x9E3779B1u;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    AdamTable tab;
-    for (int i = 0; i < n_tensors;) {
-        tab.n = 0;
-        uint64_t chunks = 0;
-        for (; i < n_tensors && tab.n < kAdamEntries; ++i) {
-            const ito_adamw_tensor& a = tensors[i];
-            const uint64_t c = ((uint64_t)a.n + kAdamChunk - 1) / kAdamChunk;
-            if (chunks + c > 0x7fffffffu) break;
-            if (!c) continue;
-            const size_t state = p->state_bits == 32 ? 16 : 4;
-            const int vec = aligned_to(a.w, 16) && aligned_to(a.g, 4 * type_bytes(p->grad_type)) && aligned_to(a.copy, 8) &&
-                            aligned_to(a.m, state) && aligned_to(a.v, state);
-            AdamEntry& e = tab.e[tab.n++];
-            e = AdamEntry{a.w, a.g, a.copy, a.m, a.v, a.m_exp, a.v_exp, a.n, (uint32_t)chunks,
-                          (float)(1.0 - p->lr * a.weight_decay), vec, (uint32_t)i * 0x510E527Fu};
-            chunks += c;
-        }
-        if (!chunks) continue;
-        if (p->grad_type == ITO_F32) launch_adamw<float>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
-        else if (p->grad_type == ITO_BF16)
-            launch_adamw<__nv_bfloat16>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
-        else launch_adamw<__half>(tab, k, p->state_bits, p->copy_type, (uint32_t)chunks, s);
-        const int r = launch_status("adamw");
+    // the ring pays for tensors of many chunks, where all of them together keep it full
+    int64_t total = 0;
+    for (int i = 0; i < n_tensors; ++i)
+        if (tensors[i].n >= kRingTensor) total += tensors[i].n;
+    const int64_t ring_from = p->state_bits == 8 && total >= (int64_t)4 * kRingChunk * num_sms() ? kRingTensor : 0;
+    if (ring_from) {
+        const int r = run_adamw(tensors, n_tensors, p, k, true, ring_from, s);
         if (r) return r;
     }
-    return ITO_OK;
+    return run_adamw(tensors, n_tensors, p, k, false, ring_from, s);
 }
 
 int ito_adamw_moments(const ito_adamw_tensor* tensors, int n_tensors, int out_type, void* m_out, void* v_out,

@@ -771,6 +771,62 @@ def test_adamw_steps(torch, ito, bits, grad, copies):
         assert np.array_equal(m.cpu().numpy(), np.concatenate(ms)) and np.array_equal(v.cpu().numpy(), np.concatenate(vs))
 
 
+def encode_whole(x, rnd, first):
+    """encode() for whole blocks, all at once."""
+    low, bias = (-111, 112) if first else (-95, 96)
+    mag = np.abs(x).view(np.uint32).astype(np.int64).reshape(-1, 128)
+    top = mag.max(1)
+    e = np.maximum(low, ((np.minimum(top, 0x7F700000) + 0xFFFFF) >> 23) - 127)
+    t = np.minimum(mag, 0x7F700000) - ((e[:, None] + bias) << 23)
+    c = np.where(t >= 0, (t + rnd.astype(np.int64).reshape(-1, 128)) >> 20, 0)
+    if first:
+        c = np.where((x.reshape(-1, 128) < 0) & (c > 0), c + 128, c)
+    else:
+        c = np.where(mag > 0, np.maximum(c, 1), c)
+    bad = top >= 0x7F800000
+    return np.where(bad[:, None], 0, c).reshape(-1).astype(np.uint8), np.where(bad, -128, e).astype(np.int8)
+
+
+@pytest.mark.parametrize("grad,copies", [("bfloat16", "bfloat16"), ("float32", None), ("float16", "float16")])
+def test_adamw_large_tensors_in_8_bits(torch, ito, grad, copies):
+    """Tensors of many chunks, their ends and odd neighbours: three steps equal the program that
+    rounds after every operation; a NaN and an infinity stay in their blocks."""
+    sizes = [1 << 20, 128, 65536 + 4096 + 256, 1 << 21, 640, 65536]
+    n = sum(sizes)
+    at = np.concatenate([[0], np.cumsum(sizes)])
+    rng = np.random.default_rng(3)
+    w = rng.normal(0, 0.1, n).astype(np.float32)
+    flat = torch.from_numpy(w.copy()).cuda()
+    cf = None if copies is None else torch.zeros(n, dtype=dt(torch, copies), device="cuda")
+    opt = ito.AdamW(list(torch.split(flat, sizes)), bits=8, weight_decay=0.1, seed=9,
+                    copies=None if cf is None else list(torch.split(cf, sizes)))
+    m, v = np.zeros(n, np.float32), np.zeros(n, np.float32)
+    for t in range(1, 4):
+        g = (rng.normal(0, 1, n) * 10.0 ** rng.integers(-4, 1, n)).astype(np.float32)
+        if t == 2:
+            g[5000], g[(1 << 20) + 200 + 70000] = np.nan, np.inf
+        g = torch.from_numpy(g).cuda().to(dt(torch, grad))
+        opt.step(list(torch.split(g, sizes)), lr=1e-2)
+        k = dict(b1=0.9, b2=0.999, eps=1e-8, lr=1e-2, grad_scale=1.0, t=t)
+        w, m, v = adamw32(w, g.float().cpu().numpy(), m, v, k, 0.1)
+        codes = []
+        for i, s in enumerate(sizes):
+            sl = slice(at[i], at[i + 1])
+            um, uv = mix(9, t, i, s)
+            (mc, me), (vc, ve) = encode_whole(m[sl], um, True), encode_whole(v[sl], uv, False)
+            codes.append((mc, vc, me, ve))
+            m[sl], v[sl] = decode(mc, me, True).astype(np.float32), decode(vc, ve, False).astype(np.float32)
+    for i in range(len(sizes)):
+        for got, want in zip((st[i] for st in opt.states), codes[i]):
+            assert np.array_equal(got.cpu().numpy(), want), i
+    assert same_bits(torch, flat, w)
+    if cf is not None:
+        ok = torch.from_numpy(np.isfinite(w))
+        assert torch.equal(cf.cpu()[ok], bf16_of(torch, w, dt(torch, copies))[ok])
+    bad = np.isnan(m)
+    assert bad.sum() == 256 and bad[4992:5120].all()
+
+
 def test_adamw_against_64_bits(torch, ito):
     """One step's formula in 64 bits. Each moment is two rounded products and a rounded sum; the step
     is a root, two products, a sum, a product and a quotient of them: 12 units of its size."""
