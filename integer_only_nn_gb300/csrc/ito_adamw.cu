@@ -336,14 +336,14 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
 //
 // The step reads 8 and writes 8 bytes an element (bf16 gradients and copies), with about 85
 // instructions between: memory and issue take about the same time, so loads may not wait for
-// arithmetic. A producer thread keeps a ring of chunks of 4096 elements coming into shared
-// memory by bulk copies, and sixteen warps walk over them, half a warp to a block of 128
-// elements, eight elements to a lane. Chunks whose arrays start on 16-byte boundaries come here;
+// arithmetic. A producer thread keeps a ring of chunks of 2048 elements coming into shared
+// memory by bulk copies, and three teams of eight warps take them in turn, half a warp to a
+// block of 128 elements, eight elements to a lane. Chunks whose arrays start on 16-byte boundaries come here;
 // the rest (a tensor's last part, odd places) takes k_adamw.
-constexpr int kRingChunk = 4096;
-constexpr int kRingTensor = 16 * kRingChunk;     // elements of a tensor from which it goes this way
-constexpr int kRingWarps = 16;
-constexpr int kRingThreads = (kRingWarps + 1) * 32;
+constexpr int kRingChunk = 2048;
+constexpr int kRingTensor = 32 * kRingChunk;     // elements of a tensor from which it goes this way
+constexpr int kRingWarps = 8, kRingTeams = 3;
+constexpr int kRingThreads = (kRingTeams * kRingWarps + 1) * 32;
 
 template <typename G>
 struct RingCfg {
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     griddep_launch_dependents();
     int stage = 0;
     uint32_t phase = 0;
-    if (warp == kRingWarps) {
+    if (warp == kRingTeams * kRingWarps) {
         if (lane) return;
         for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
             const AdamEntry& e = tab.e[find_entry(tab, c)];
@@ -391,22 +391,25 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         return;
     }
-    const int half = lane >> 4, hl = lane & 15;
-    const int block = warp * 2 + half, at = block * kAdamBlock + hl * 4;     // and at + 64
+    const int team = warp / kRingWarps, half = lane >> 4, hl = lane & 15;
+    const int block = warp % kRingWarps * 2 + half, at = block * kAdamBlock + hl * 4;     // and at + 64
+    const uint32_t stride = kRingTeams * gridDim.x;
+    uint32_t c = blockIdx.x + team * gridDim.x;
+    stage = team;
     int em = 0, ev = 0;                  // the next chunk's exponents come one chunk ahead
-    if (blockIdx.x < chunks) {
-        const AdamEntry& e = tab.e[find_entry(tab, blockIdx.x)];
-        const int64_t b = (int64_t)(blockIdx.x - e.first_chunk) * (kRingChunk / kAdamBlock) + block;
+    if (c < chunks) {
+        const AdamEntry& e = tab.e[find_entry(tab, c)];
+        const int64_t b = (int64_t)(c - e.first_chunk) * (kRingChunk / kAdamBlock) + block;
         em = e.m_exp[b];
         ev = e.v_exp[b];
     }
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    for (; c < chunks; c += stride) {
         const AdamEntry& e = tab.e[find_entry(tab, c)];
         const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
         int em_next = 0, ev_next = 0;
-        if (c + gridDim.x < chunks) {
-            const AdamEntry& n = tab.e[find_entry(tab, c + gridDim.x)];
-            const int64_t b = (int64_t)(c + gridDim.x - n.first_chunk) * (kRingChunk / kAdamBlock) + block;
+        if (c + stride < chunks) {
+            const AdamEntry& n = tab.e[find_entry(tab, c + stride)];
+            const int64_t b = (int64_t)(c + stride - n.first_chunk) * (kRingChunk / kAdamBlock) + block;
             em_next = n.m_exp[b];
             ev_next = n.v_exp[b];
         }
@@ -434,7 +437,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        stage += kRingTeams;
+        if (stage >= STAGES) { stage -= STAGES; phase ^= 1; }
         const uint32_t base_m = moment_base<false>(em), base_v = moment_base<true>(ev);
         float most_m = 0.0f, most_v = 0.0f;
 #pragma unroll
@@ -690,7 +694,7 @@ int ito_adamw_step(const ito_adamw_tensor* tensors, int n_tensors, const ito_ada
     int64_t total = 0;
     for (int i = 0; i < n_tensors; ++i)
         if (tensors[i].n >= kRingTensor) total += tensors[i].n;
-    const int64_t ring_from = p->state_bits == 8 && total >= (int64_t)4 * kRingChunk * num_sms() ? kRingTensor : 0;
+    const int64_t ring_from = p->state_bits == 8 && total >= (int64_t)8 * kRingChunk * num_sms() ? kRingTensor : 0;
     if (ring_from) {
         const int r = run_adamw(tensors, n_tensors, p, k, true, ring_from, s);
         if (r) return r;

@@ -84,6 +84,15 @@ struct Vec {
             return *reinterpret_cast<const uint32_t*>(&v);
         }
     }
+    // element i, where i differs from lane to lane
+    __device__ __forceinline__ float element(int i) const
+    {
+        const int word = sizeof(T) == 4 ? i : i >> 1;
+        const uint32_t lo = word & 1 ? raw.y : raw.x, hi = word & 1 ? raw.w : raw.z;
+        const uint32_t w = word & 2 ? hi : lo;
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+        else return lane16(i & 1 ? w >> 16 : w, 0);
+    }
     // the largest element (a NaN counts only where there is nothing else)
     __device__ __forceinline__ float largest() const
     {

@@ -416,11 +416,17 @@ struct LnRing {
     uint32_t row_bytes;
 };
 
+// Blocks of up to 256 threads: three to an SM forward (8192 x 4096 bf16: 28.5 us, 30.4 with two,
+// 37.7 with four), two backward (46.3 us, 53.9 with three, whose registers spill).
+constexpr int kLnTight = 3;
+constexpr int ln_ring_threads(int vpt, bool tight) { return tight ? 256 : vpt == 4 ? 1024 : 512; }
+
 template <int N>
 __device__ __forceinline__ float2 pair_of(const float (&v)[N], int i) { return make_float2(v[2 * i], v[2 * i + 1]); }
 
-template <typename T, int VPT, int R>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512)
+// TIGHT: blocks of up to 256 threads, three to an SM
+template <typename T, int VPT, int R, bool TIGHT>
+__global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight : 1)
     k_layer_norm_fwd_ring(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
                           const void* __restrict__ beta, int w_type, int64_t rows, int cols, float eps,
                           T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
@@ -735,8 +741,8 @@ static LnShape ln_shape(int cols, int size, int most)
     return s;
 }
 
-// The ring takes long FULL rows in numbers: `rows_each` of a stage are `loads` rows of bytes each.
-constexpr int kLnRingBytes = 100 * 1024;     // of a block of up to 256 threads: two of them to an SM
+// The ring takes long FULL rows in numbers.
+constexpr int kLnRingBytes = 200 * 1024;     // of an SM's blocks together
 constexpr int kLnRingRows = 4;               // rows for each SM from which the ring pays
 
 static bool ln_ring_rows(const LnShape& s, int cols, int size, int64_t rows)
@@ -744,14 +750,13 @@ static bool ln_ring_rows(const LnShape& s, int cols, int size, int64_t rows)
     return s.vpt && s.tpr > 32 && cols % (16 / size) == 0 && rows >= (int64_t)kLnRingRows * num_sms();
 }
 
-static int ln_ring_blocks(const LnShape& s) { return s.block <= 256 ? 2 : 1; }
+static int ln_ring_blocks(const LnShape& s, bool forward) { return s.block > 256 ? 1 : forward ? kLnTight : 2; }
 
-static LnRing ln_ring(const LnShape& s, int cols, int size, int stage_rows)
+static LnRing ln_ring(const LnShape& s, int cols, int size, int stage_rows, int blocks)
 {
     LnRing r;
     r.row_bytes = (uint32_t)cols * size;
-    const int room = ln_ring_blocks(s) == 2 ? kLnRingBytes : 2 * kLnRingBytes;
-    r.stages = std::max(2, std::min(16, room / (int)(r.row_bytes * stage_rows)));
+    r.stages = std::max(2, std::min(16, kLnRingBytes / blocks / (int)(r.row_bytes * stage_rows)));
     return r;
 }
 
@@ -820,21 +825,23 @@ static int run_fwd(const void* xp, int64_t ldx, const void* gamma, const void* b
     const bool full = cols % Vec<T>::kPer == 0 && xv && yv && aligned_to(gamma, 16) && aligned_to(beta, 16);
     if (full && ln_ring_rows(sh, cols, sizeof(T), rows)) {
         const int RR = sh.vpt <= 2 ? 2 : 1;
-        const LnRing ring = ln_ring(sh, cols, sizeof(T), RR);
+        const int each = ln_ring_blocks(sh, true);
+        const LnRing ring = ln_ring(sh, cols, sizeof(T), RR, each);
         const int smem = ring.stages * RR * (int)ring.row_bytes;
-        const unsigned blocks = (unsigned)std::min<int64_t>((rows + RR - 1) / RR, (int64_t)num_sms() * ln_ring_blocks(sh));
+        const unsigned blocks = (unsigned)std::min<int64_t>((rows + RR - 1) / RR, (int64_t)num_sms() * each);
         int* err = device_error_word();
         if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
-#define ITO_LN_RING(V, RN)                                                                                     \
-    do {                                                                                                       \
-        const int st = ln_ring_smem(k_layer_norm_fwd_ring<T, V, RN>, smem);                                    \
-        if (st) return st;                                                                                     \
-        launch_pdl(k_layer_norm_fwd_ring<T, V, RN>, blocks, sh.block, smem, s, x, ldx, gamma, beta, w_type, rows, \
-                   cols, eps, y, ldy, mean, rstd, ring, err);                                                  \
+#define ITO_LN_RING(V, RN, TIGHT)                                                                               \
+    do {                                                                                                        \
+        const int st = ln_ring_smem(k_layer_norm_fwd_ring<T, V, RN, TIGHT>, smem);                              \
+        if (st) return st;                                                                                      \
+        launch_pdl(k_layer_norm_fwd_ring<T, V, RN, TIGHT>, blocks, sh.block, smem, s, x, ldx, gamma, beta, w_type, \
+                   rows, cols, eps, y, ldy, mean, rstd, ring, err);                                             \
     } while (0)
-        if (sh.vpt == 1) ITO_LN_RING(1, 2);
-        else if (sh.vpt == 2) ITO_LN_RING(2, 2);
-        else ITO_LN_RING(4, 1);
+        if (sh.vpt == 1) ITO_LN_RING(1, 2, true);
+        else if (sh.vpt == 2 && sh.block <= 256) ITO_LN_RING(2, 2, true);
+        else if (sh.vpt == 2) ITO_LN_RING(2, 2, false);
+        else ITO_LN_RING(4, 1, false);
 #undef ITO_LN_RING
         return launch_status("layer norm");
     }
@@ -870,11 +877,11 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
 #define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
 #define ITO_LN_RING(V, RN)                                                                                          \
     do {                                                                                                            \
-        const LnRing ring = ln_ring(sh, cols, sizeof(T), 2 * RN);                                                   \
+        const LnRing ring = ln_ring(sh, cols, sizeof(T), 2 * RN, ln_ring_blocks(sh, false));                                                   \
         const int smem = ring.stages * 2 * RN * (int)ring.row_bytes;                                                \
         const int st = ln_ring_smem(k_layer_norm_bwd_ring<T, V, RN>, smem);                                         \
         if (st) return st;                                                                                          \
-        parts = (int)std::min<int64_t>((rows + RN - 1) / RN, std::min(parts, num_sms() * ln_ring_blocks(sh)));      \
+        parts = (int)std::min<int64_t>((rows + RN - 1) / RN, std::min(parts, num_sms() * ln_ring_blocks(sh, false)));      \
         launch_pdl(k_layer_norm_bwd_ring<T, V, RN>, parts, sh.block, smem, s, dy, lddy, x, ldx, gamma, w_type, mean, \
                    rstd, rows, cols, dx, lddx, share, ring, err);                                                   \
     } while (0)
