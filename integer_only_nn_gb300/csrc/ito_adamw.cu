@@ -64,6 +64,13 @@ __device__ __forceinline__ int find_entry(const AdamTable& tab, uint32_t chunk)
     return lo;
 }
 
+// the tensor of a later chunk, from an earlier one's
+__device__ __forceinline__ int next_entry(const AdamTable& tab, int i, uint32_t chunk)
+{
+    while (i + 1 < tab.n && tab.e[i + 1].first_chunk <= chunk) ++i;
+    return i;
+}
+
 struct AdamConst {
     float b1, c1, b2, c2, eps, inv_sqrt_bc2, alpha, grad_scale;
     uint32_t key;
@@ -106,32 +113,40 @@ __device__ __forceinline__ float moment_value(uint32_t codes, int j, uint32_t ba
     // the byte at the top of a word; its exponent and mantissa belong four bits lower
     const uint32_t c = __byte_perm(codes, 0u, (uint32_t)j << 12 | 0x0444u);
     const uint32_t mag = SECOND ? c : c & 0x7F000000u;
-    const uint32_t r = mag ? __umulhi(mag, 0x10000000u) + base : 0u;
+    const uint32_t r = mag ? (mag >> 4) + base : 0u;
     return __uint_as_float(SECOND ? r : r | (c & 0x80000000u));
 }
+
+// the largest finite value that a code under the largest exponent stands for, 1.875 * 2^127
+constexpr uint32_t kMomentTop = 0x7F700000u;
 
 // the shared exponent of a block whose largest magnitude has these bits
 template <bool SECOND>
 __device__ __forceinline__ int moment_exponent(uint32_t top)
 {
     if (top >= 0x7F800000u) return -128;
-    const int e = (int)((min(top, 0x7F700000u) + 0xFFFFFu) >> 23) - 127;
+    const int e = (int)((min(top, kMomentTop) + 0xFFFFFu) >> 23) - 127;
     return max(e, SECOND ? -95 : -111);
 }
 
 // The code of x: its bits, counted from the lowest binade (base: moment_base), plus a random
 // part of the step that is cut off. Below the lowest binade the count is negative and the code
-// 0, or 1 for a v above zero. Finite values above 1.875 * 2^127 are clamped to it first (top:
-// the block's largest, the same for all of its lanes).
+// 0, or 1 for a v above zero. |x| is at most moment_top.
 template <bool SECOND>
-__device__ __forceinline__ uint32_t moment_code(float x, uint32_t top, uint32_t base, uint32_t u)
+__device__ __forceinline__ uint32_t moment_code(float x, uint32_t base, uint32_t u)
 {
-    const uint32_t bits = __float_as_uint(x);
-    uint32_t mag = SECOND ? bits : bits & 0x7FFFFFFFu;
-    if (top > 0x7F700000u) mag = min(mag, 0x7F700000u);
+    const uint32_t bits = __float_as_uint(x), mag = SECOND ? bits : bits & 0x7FFFFFFFu;
     const int c = (int)(mag - base + u) >> 20;
     if (SECOND) return (uint32_t)max(c, (int)min(mag, 1u));
     return c > 0 ? (uint32_t)c | (bits >> 24 & 128u) : 0u;
+}
+
+template <int N>
+__device__ __forceinline__ void clamp_moments(float (&x)[N])
+{
+    const float top = __uint_as_float(kMomentTop);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = fminf(fmaxf(x[j], -top), top);
 }
 
 // the larger magnitude; a NaN wins
@@ -252,14 +267,16 @@ struct AdamPiece {
             em = moment_exponent<false>(tm);
             ev = moment_exponent<true>(tv);
             const uint32_t h0 = round_key(k.key + e.salt, b);
+            if (tm > kMomentTop) clamp_moments(m);
+            if (tv > kMomentTop) clamp_moments(v);
             uint32_t mc[4], vc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t um, uv;
                 // (the low half of the element's index is below its block's end: no carry)
                 round_bits(h0 + (uint32_t)(VEC ? lane * 4 + j : j * 32 + lane) * kMixIndex, um, uv);
-                mc[j] = moment_code<false>(m[j], tm, moment_base<false>(em), um);
-                vc[j] = moment_code<true>(v[j], tv, moment_base<true>(ev), uv);
+                mc[j] = moment_code<false>(m[j], moment_base<false>(em), um);
+                vc[j] = moment_code<true>(v[j], moment_base<true>(ev), uv);
             }
             m8 = mc[0] | mc[1] << 8 | mc[2] << 16 | mc[3] << 24;
             v8 = vc[0] | vc[1] << 8 | vc[2] << 16 | vc[3] << 24;
@@ -334,8 +351,9 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
 
 // ------------------------------------------------------ whole chunks, 8-bit moments
 //
-// The step reads 8 and writes 8 bytes an element (bf16 gradients and copies), with about 85
-// instructions between: memory and issue take about the same time, so loads may not wait for
+// The step reads 8 and writes 8 bytes an element (bf16 gradients and copies), with about 105
+// instructions between, and their issue bounds it (138M weights: 477 us, 290 at the memory's rate;
+// roots and quotients take 7 % of it, the rounding's hash 9 %), so loads may not wait for
 // arithmetic. A producer thread keeps a ring of chunks of 2048 elements coming into shared
 // memory by bulk copies, and three teams of eight warps take them in turn, half a warp to a
 // block of 128 elements, eight elements to a lane. Chunks whose arrays start on 16-byte boundaries come here;
@@ -377,8 +395,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     uint32_t phase = 0;
     if (warp == kRingTeams * kRingWarps) {
         if (lane) return;
+        int entry = 0;
         for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-            const AdamEntry& e = tab.e[find_entry(tab, c)];
+            entry = next_entry(tab, entry, c);
+            const AdamEntry& e = tab.e[entry];
             const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
             if (!mbar_wait(&empty[stage], phase ^ 1, &abort_flag, err)) return;
             uint8_t* p = smem + stage * Cfg::BYTES;
@@ -397,18 +417,21 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     uint32_t c = blockIdx.x + team * gridDim.x;
     stage = team;
     int em = 0, ev = 0;                  // the next chunk's exponents come one chunk ahead
+    int entry = 0;
     if (c < chunks) {
-        const AdamEntry& e = tab.e[find_entry(tab, c)];
+        entry = find_entry(tab, c);
+        const AdamEntry& e = tab.e[entry];
         const int64_t b = (int64_t)(c - e.first_chunk) * (kRingChunk / kAdamBlock) + block;
         em = e.m_exp[b];
         ev = e.v_exp[b];
     }
     for (; c < chunks; c += stride) {
-        const AdamEntry& e = tab.e[find_entry(tab, c)];
+        const AdamEntry& e = tab.e[entry];
         const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
         int em_next = 0, ev_next = 0;
         if (c + stride < chunks) {
-            const AdamEntry& n = tab.e[find_entry(tab, c + stride)];
+            entry = next_entry(tab, entry, c + stride);
+            const AdamEntry& n = tab.e[entry];
             const int64_t b = (int64_t)(c + stride - n.first_chunk) * (kRingChunk / kAdamBlock) + block;
             em_next = n.m_exp[b];
             ev_next = n.v_exp[b];
@@ -466,6 +489,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         em = moment_exponent<false>(tm);
         ev = moment_exponent<true>(tv);
+        if (tm > kMomentTop) clamp_moments(m);
+        if (tv > kMomentTop) clamp_moments(v);
         const uint32_t to_m = moment_base<false>(em), to_v = moment_base<true>(ev);
         const uint32_t h0 = round_key(k.key + e.salt, base + at);
         C* copy = static_cast<C*>(e.copy);
@@ -477,8 +502,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 uint32_t um, uv;
                 // (chunks do not straddle a multiple of 2^32: no carry)
                 round_bits(h0 + (uint32_t)(64 * h + j) * kMixIndex, um, uv);
-                cm[j] = moment_code<false>(m[4 * h + j], tm, to_m, um);
-                cv[j] = moment_code<true>(v[4 * h + j], tv, to_v, uv);
+                cm[j] = moment_code<false>(m[4 * h + j], to_m, um);
+                cv[j] = moment_code<true>(v[4 * h + j], to_v, uv);
             }
             uint32_t m8 = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410);
             uint32_t v8 = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
