@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libito.so")
@@ -800,20 +801,34 @@ def _from_ptr(ptr, n, dtype, eb):
 
 
 # ---------------------------------------------------------- float operators
+#
+# Checks and marshalling here are on the path of calls whose kernels take 2 to 10 us, so they
+# stay few: one look at each tensor, one allocation for each result.
 
 _ACTS = {"none": ITO_ACT_NONE, "relu": ITO_ACT_RELU, "gelu": ITO_ACT_GELU, "gelu_tanh": ITO_ACT_GELU_TANH,
          "silu": ITO_ACT_SILU}
-_TYPE_IDS = {}
+_TYPE_IDS = {}          # torch dtype -> ito_type
+_F32 = None             # torch.float32, once torch is there
+_raw_stream_of = None   # device index -> the current stream's handle
 
 
-def _type_id(t, name):
-    """ito_type of a tensor; -1 (which the library rejects) is never passed on."""
-    if not _TYPE_IDS:
-        torch = _torch()
-        _TYPE_IDS.update({torch.float32: ITO_F32, torch.bfloat16: ITO_BF16, torch.float16: ITO_F16})
-    r = _TYPE_IDS.get(t.dtype)
+def _float_setup():
+    """torch, and what this part needs of it."""
+    global _F32, _raw_stream_of
+    import torch
+    _TYPE_IDS.update({torch.float32: ITO_F32, torch.bfloat16: ITO_BF16, torch.float16: ITO_F16})
+    # (torch.cuda.current_stream() makes an object, which takes as long as a small kernel's launch)
+    _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _F32 = torch.float32
+    return torch
+
+
+def _type_id(dtype, name):
+    """ito_type of a torch dtype."""
+    r = _TYPE_IDS.get(dtype)
     if r is None:
-        raise ItoError(ITO_ERR_ARG, "%s: type %s (float32, bfloat16 and float16 are taken)" % (name, t.dtype))
+        raise ItoError(ITO_ERR_ARG, "%s: type %s (float32, bfloat16 and float16 are taken)" % (name, dtype))
     return r
 
 
@@ -824,8 +839,9 @@ def _act_id(act):
     return r
 
 
-def _matrix(t, name, rows=None, cols=None, dtype=None):
-    """Checks a 2-D device tensor whose rows' elements are consecutive; -> its row stride."""
+def _matrix(t, name, rows, cols, dtype):
+    """Checks a 2-D device tensor whose rows' elements are consecutive (rows, cols, dtype: None
+    for any); -> its row stride."""
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%s][%s]" % (
@@ -834,7 +850,7 @@ def _matrix(t, name, rows=None, cols=None, dtype=None):
         raise ItoError(ITO_ERR_SHAPE, "%s: no elements" % name)
     if not t.is_cuda:
         raise ItoError(ITO_ERR_ARG, "%s: not on the GPU" % name)
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ItoError(ITO_ERR_ARG, "%s: type %s, expected %s" % (name, t.dtype, dtype))
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
@@ -842,75 +858,82 @@ def _matrix(t, name, rows=None, cols=None, dtype=None):
     return s0
 
 
-def _vector(t, name, n, dtypes):
-    """Checks a dense 1-D device tensor (None passes)."""
+def _vector(t, name, n, dtype, other=None):
+    """Checks a dense 1-D device tensor of one of two types (None passes); -> its address."""
     if t is None:
-        return
+        return None
     shape = t.shape
     if len(shape) != 1 or shape[0] != n:
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%d]" % (name, list(shape), n))
-    if not t.is_cuda or t.dtype not in dtypes:
+    if not t.is_cuda or (t.dtype is not dtype and t.dtype is not other):
         raise ItoError(ITO_ERR_ARG, "%s: %s on %s" % (name, t.dtype, t.device))
     if n > 1 and t.stride(0) != 1:
         raise ItoError(ITO_ERR_ARG, "%s: not contiguous" % name)
-
-
-def _raw_stream(device):
-    """The current stream's handle (torch.cuda.current_stream() makes an object for it, which
-    takes as long as a small kernel's launch)."""
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(device.index) if get is not None else torch.cuda.current_stream(device).cuda_stream
+    return t.data_ptr()
 
 
 def _on_stream(call, stream):
-    """Runs a call with `stream` as torch's current stream (None: as it is), so that what it
-    allocates belongs to the stream that it launches on."""
-    if stream is None:
-        return call()
+    """Runs a call with `stream` as torch's current stream, so that what it allocates belongs to
+    the stream that it launches on."""
     with _torch().cuda.stream(stream):
         return call()
 
 
-def _scratch(n, device):
-    """A 256-byte aligned workspace of n bytes: its address, and the tensor that owns it."""
-    if not n:
-        return None, None
-    t = _torch().empty(n + 255, dtype=_torch().uint8, device=device)
-    return (t.data_ptr() + 255) & ~255, t
+class _Scratch(threading.local):
+    """Workspaces kept from call to call: one for each host thread and stream, because calls
+    that share one have to be in order, on the GPU and between a call's own launches."""
+
+    KEEP = 32 << 20     # a larger one is the allocator's, call by call
+
+    def __init__(self):
+        self.kept = {}
+
+    def get(self, n, device, stream, torch):
+        """-> (the 256-byte aligned address of n bytes, their owner to hold until the launch)"""
+        key = (device.index, stream)
+        have = self.kept.get(key)
+        if have is not None and have[1] >= n and not torch.cuda.is_current_stream_capturing():
+            return have[0], None
+        t = torch.empty(n + 255, dtype=torch.uint8, device=device)
+        at = (t.data_ptr() + 255) & ~255
+        # (a graph's replays may run beside other calls: what it uses is its own)
+        if n <= self.KEEP and not torch.cuda.is_current_stream_capturing():
+            self.kept[key] = (at, n, t)
+        return at, t
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+_scratch = _Scratch()
 
 
 def ito_fp_linear_fwd(x, W, bias=None, act="none", residual=None, save_z=False, out_dtype=None, stream=None):
     """y = act(x W^T + bias) + residual for bf16 or f16 x [B][IC], W [OC][IC]; -> y, or (y, z)
     with z = x W^T + bias in x's type where save_z. out_dtype (of y and residual): x's type
     or float32. bias: x's type or float32."""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_fp_linear_fwd(x, W, bias, act, residual, save_z, out_dtype), stream)
-    torch = _torch()
     dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x")
+    ldx = _matrix(x, "x", None, None, None)
     B, IC = x.shape
     ldw = _matrix(W, "W", None, IC, dtype)
     OC = W.shape[0]
-    ty = _type_id(x, "x")
-    if out_dtype is None:
-        out_dtype = dtype
-    bt = ITO_F32
-    if bias is not None:
-        _vector(bias, "bias", OC, (dtype, torch.float32))
-        bt = _type_id(bias, "bias")
-    ldr = 0 if residual is None else _matrix(residual, "residual", B, OC, out_dtype)
-    y = torch.empty((B, OC), dtype=out_dtype, device=dev)
+    ty = _type_id(dtype, "x")
+    out = dtype if out_dtype is None else out_dtype
+    pb = _vector(bias, "bias", OC, dtype, _F32)
+    pr, ldr = (None, 0) if residual is None else (residual.data_ptr(), _matrix(residual, "residual", B, OC, out))
+    y = torch.empty((B, OC), dtype=out, device=dev)
     z = torch.empty((B, OC), dtype=dtype, device=dev) if save_z else None
+    s = _raw_stream_of(dev.index)
     px, pw = x.data_ptr(), W.data_ptr()
+    ws, hold = None, None
     n = _lib.ito_fp_linear_fwd_workspace_size(px, ldx, pw, ldw, B, IC, OC)
-    ws, keep = _scratch(n, dev)
-    _check(_lib.ito_fp_linear_fwd(px, ldx, pw, ldw, _addr(bias), _addr(residual), ldr, ty, _type_id(y, "out_dtype"), bt,
-                                  _act_id(act), B, IC, OC, ws, n, _addr(z), OC, y.data_ptr(), OC, _raw_stream(dev)))
+    if n:
+        ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_fp_linear_fwd(px, ldx, pw, ldw, pb, pr, ldr, ty, _type_id(out, "out_dtype"),
+                               ITO_F32 if bias is None else _TYPE_IDS[bias.dtype], _act_id(act), B, IC, OC, ws, n,
+                               z.data_ptr() if save_z else None, OC, y.data_ptr(), OC, s)
+    if r:
+        _check(r)
     return (y, z) if save_z else y
 
 
@@ -918,123 +941,131 @@ def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, 
                       stream=None):
     """Gradients of ito_fp_linear_fwd -> (dx [B][IC] in x's type, dW [OC][IC] in dw_dtype (x's
     type or float32), dbias float32 [OC]); None for those not needed."""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_fp_linear_bwd(dy, x, W, z, act, need_dx, need_dw, need_dbias, dw_dtype), stream)
-    torch = _torch()
     dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x")
+    ldx = _matrix(x, "x", None, None, None)
     B, IC = x.shape
     ldw = _matrix(W, "W", None, IC, dtype)
     OC = W.shape[0]
     lddy = _matrix(dy, "dy", B, OC, dtype)
-    ldz = 0 if z is None else _matrix(z, "z", B, OC, dtype)
+    pz, ldz = (None, 0) if z is None else (z.data_ptr(), _matrix(z, "z", B, OC, dtype))
+    ty = _type_id(dtype, "x")
     a = _act_id(act)
-    if not (need_dx or need_dw or need_dbias):
-        raise ItoError(ITO_ERR_ARG, "no output")
+    dwt = dtype if dw_dtype is None else dw_dtype
     dx = torch.empty((B, IC), dtype=dtype, device=dev) if need_dx else None
-    dw = torch.empty((OC, IC), dtype=dw_dtype or dtype, device=dev) if need_dw else None
-    db = torch.empty(OC, dtype=torch.float32, device=dev) if need_dbias else None
+    dw = torch.empty((OC, IC), dtype=dwt, device=dev) if need_dw else None
+    db = torch.empty(OC, dtype=_F32, device=dev) if need_dbias else None
+    s = _raw_stream_of(dev.index)
     pd, px, pw = dy.data_ptr(), x.data_ptr(), W.data_ptr()
+    ws, hold = None, None
     n = _lib.ito_fp_linear_bwd_workspace_size(pd, lddy, px, ldx, pw, ldw, a, B, IC, OC)
-    ws, keep = _scratch(n, dev)
-    ty = _type_id(x, "x")
-    _check(_lib.ito_fp_linear_bwd(pd, lddy, _addr(z), ldz, px, ldx, pw, ldw, ty,
-                                  ty if dw is None else _type_id(dw, "dw_dtype"), a, B, IC, OC, ws, n, _addr(dx), IC,
-                                  _addr(dw), IC, _addr(db), _raw_stream(dev)))
+    if n:
+        ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_fp_linear_bwd(pd, lddy, pz, ldz, px, ldx, pw, ldw, ty, _type_id(dwt, "dw_dtype"), a, B, IC, OC, ws, n,
+                               dx.data_ptr() if need_dx else None, IC, dw.data_ptr() if need_dw else None, IC,
+                               db.data_ptr() if need_dbias else None, s)
+    if r:
+        _check(r)
     return dx, dw, db
 
 
 def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """x [rows][cols] of float32, bfloat16 or float16 -> (y, mean float32 [rows], rstd float32 [rows])"""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream)
-    torch = _torch()
-    dev = x.device
-    ldx = _matrix(x, "x")
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x", None, None, None)
     rows, cols = x.shape
-    w = ITO_F32
-    if gamma is not None:
-        _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
-        w = _type_id(gamma, "gamma")
-    if beta is not None:
-        _vector(beta, "beta", cols, (x.dtype, torch.float32))
-        if gamma is not None and beta.dtype != gamma.dtype:
-            raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
-        w = _type_id(beta, "beta")
-    y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    _check(_lib.ito_layer_norm_fwd(x.data_ptr(), ldx, _type_id(x, "x"), _addr(gamma), _addr(beta), w, rows, cols, eps,
-                                   y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev)))
+    pg, pb = _vector(gamma, "gamma", cols, dtype, _F32), _vector(beta, "beta", cols, dtype, _F32)
+    if pg is not None and pb is not None and gamma.dtype is not beta.dtype:
+        raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
+    w = gamma if gamma is not None else beta
+    ty = _type_id(dtype, "x")
+    y = torch.empty((rows, cols), dtype=dtype, device=dev)
+    mean = torch.empty(rows, dtype=_F32, device=dev)
+    rstd = torch.empty_like(mean)
+    r = _lib.ito_layer_norm_fwd(x.data_ptr(), ldx, ty, pg, pb, ITO_F32 if w is None else _TYPE_IDS[w.dtype], rows, cols,
+                                eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), _raw_stream_of(dev.index))
+    if r:
+        _check(r)
     return y, mean, rstd
 
 
 def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, stream=None):
     """-> (dx in x's type, dgamma float32 [cols], dbeta float32 [cols]); None for those not needed."""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream)
-    torch = _torch()
-    dev = x.device
-    ldx = _matrix(x, "x")
+    dtype, dev = x.dtype, x.device
+    ldx = _matrix(x, "x", None, None, None)
     rows, cols = x.shape
-    lddy = _matrix(dy, "dy", rows, cols, x.dtype)
-    w = ITO_F32
-    if gamma is not None:
-        _vector(gamma, "gamma", cols, (x.dtype, torch.float32))
-        w = _type_id(gamma, "gamma")
-    _vector(mean, "mean", rows, (torch.float32,))
-    _vector(rstd, "rstd", rows, (torch.float32,))
-    dx = torch.empty((rows, cols), dtype=x.dtype, device=dev) if need_dx else None
-    dg = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
-    db = torch.empty(cols, dtype=torch.float32, device=dev) if need_dw else None
-    n = _lib.ito_layer_norm_bwd_workspace_size(rows, cols) if need_dw else 0
-    ws, keep = _scratch(n, dev)
-    _check(_lib.ito_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, _type_id(x, "x"), _addr(gamma), w,
-                                   mean.data_ptr(), rstd.data_ptr(), rows, cols, ws, n, _addr(dx), cols, _addr(dg),
-                                   _addr(db), _raw_stream(dev)))
+    lddy = _matrix(dy, "dy", rows, cols, dtype)
+    pg = _vector(gamma, "gamma", cols, dtype, _F32)
+    pm, ps = _vector(mean, "mean", rows, _F32), _vector(rstd, "rstd", rows, _F32)
+    ty = _type_id(dtype, "x")
+    dx = torch.empty((rows, cols), dtype=dtype, device=dev) if need_dx else None
+    s = _raw_stream_of(dev.index)
+    dg = db = ws = hold = None
+    n = 0
+    if need_dw:
+        dg = torch.empty(cols, dtype=_F32, device=dev)
+        db = torch.empty_like(dg)
+        n = _lib.ito_layer_norm_bwd_workspace_size(rows, cols)
+        ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, ty, pg,
+                                ITO_F32 if gamma is None else _TYPE_IDS[gamma.dtype], pm, ps, rows, cols, ws, n,
+                                dx.data_ptr() if need_dx else None, cols, dg.data_ptr() if need_dw else None,
+                                db.data_ptr() if need_dw else None, s)
+    if r:
+        _check(r)
     return dx, dg, db
 
 
 def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     """logits [rows][classes] (float32, bfloat16, float16), targets int32 [rows] or None ->
     (logp (None without targets), entropy, lse float32 [rows], top_ids int32 [rows][k], top_logp float32 [rows][k])"""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream)
-    torch = _torch()
     dev = logits.device
-    ld = _matrix(logits, "logits")
+    ld = _matrix(logits, "logits", None, None, None)
     rows, classes = logits.shape
-    if targets is not None:
-        _vector(targets, "targets", rows, (torch.int32,))
-    logp = torch.empty(rows, dtype=torch.float32, device=dev)
-    entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
+    pt = _vector(targets, "targets", rows, torch.int32)
+    ty = _type_id(logits.dtype, "logits")
+    entropy = torch.empty(rows, dtype=_F32, device=dev)
+    lse = torch.empty_like(entropy)
+    logp = None if pt is None else torch.empty_like(entropy)
+    top = torch.empty((rows, k), dtype=_F32, device=dev)
     ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
-    top = torch.empty((rows, k), dtype=torch.float32, device=dev)
-    _check(_lib.ito_token_logprobs_fwd(logits.data_ptr(), ld, _type_id(logits, "logits"), _addr(targets), rows, classes,
-                                       k, None if targets is None else logp.data_ptr(), entropy.data_ptr(),
-                                       lse.data_ptr(), ids.data_ptr(), top.data_ptr(), _raw_stream(dev)))
-    return (None if targets is None else logp), entropy, lse, ids, top
+    r = _lib.ito_token_logprobs_fwd(logits.data_ptr(), ld, ty, pt, rows, classes, k,
+                                    None if pt is None else logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                                    ids.data_ptr(), top.data_ptr(), _raw_stream_of(dev.index))
+    if r:
+        _check(r)
+    return logp, entropy, lse, ids, top
 
 
 def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy=None, out=None, stream=None):
     """-> dlogits in the logits' type (out: a tensor to write it to, which may be the logits)."""
+    torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream)
-    torch = _torch()
-    dev = logits.device
-    ld = _matrix(logits, "logits")
+    dtype, dev = logits.dtype, logits.device
+    ld = _matrix(logits, "logits", None, None, None)
     rows, classes = logits.shape
-    f32 = (torch.float32,)
-    _vector(targets, "targets", rows, (torch.int32,))
-    _vector(lse, "lse", rows, f32)
-    _vector(entropy, "entropy", rows, f32)
-    _vector(g_logp, "g_logp", rows, f32)
-    _vector(g_entropy, "g_entropy", rows, f32)
-    d = torch.empty((rows, classes), dtype=logits.dtype, device=dev) if out is None else out
-    ldd = classes if out is None else _matrix(d, "out", rows, classes, logits.dtype)
-    _check(_lib.ito_token_logprobs_bwd(logits.data_ptr(), ld, _type_id(logits, "logits"), _addr(targets),
-                                       lse.data_ptr(), _addr(entropy), rows, classes, _addr(g_logp), _addr(g_entropy),
-                                       d.data_ptr(), ldd, _raw_stream(dev)))
+    pt = _vector(targets, "targets", rows, torch.int32)
+    pl, pe = _vector(lse, "lse", rows, _F32), _vector(entropy, "entropy", rows, _F32)
+    pg, ph = _vector(g_logp, "g_logp", rows, _F32), _vector(g_entropy, "g_entropy", rows, _F32)
+    ty = _type_id(dtype, "logits")
+    d = torch.empty((rows, classes), dtype=dtype, device=dev) if out is None else out
+    ldd = classes if out is None else _matrix(d, "out", rows, classes, dtype)
+    r = _lib.ito_token_logprobs_bwd(logits.data_ptr(), ld, ty, pt, pl, pe, rows, classes, pg, ph, d.data_ptr(), ldd,
+                                    _raw_stream_of(dev.index))
+    if r:
+        _check(r)
     return d
 
 
@@ -1051,7 +1082,7 @@ class AdamW:
     def __init__(self, weights, bits=32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, states=None,
                  step=0, seed=0):
         import numpy as np
-        torch = _torch()
+        torch = _float_setup()
         if bits not in (32, 8):
             raise ItoError(ITO_ERR_ARG, "bits must be 32 or 8")
         if not weights:
@@ -1085,7 +1116,7 @@ class AdamW:
             self._dense(ts, dtype, lengths, name)
         if len(decays) != len(sizes):
             raise ItoError(ITO_ERR_SHAPE, "weight_decay: %d values, expected %d" % (len(decays), len(sizes)))
-        self._copy_type = ITO_BF16 if self.copies is None else _type_id(self.copies[0], "copies")
+        self._copy_type = ITO_BF16 if self.copies is None else _type_id(self.copies[0].dtype, "copies")
         self._n, self._sizes, self.total = len(sizes), sizes, sum(sizes)
         self._table = (AdamwTensor * self._n)()
         tab = self._fields = np.frombuffer(self._table, dtype=np.dtype(
@@ -1116,8 +1147,8 @@ class AdamW:
                 self._dense(grads, dtype, self._sizes, "grads")     # says which and why
         self._fields["g"] = [g.data_ptr() for g in grads]
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
-                        _type_id(grads[0], "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
-        s = _raw_stream(self.weights[0].device) if stream is None else stream.cuda_stream
+                        _type_id(dtype, "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
+        s = _raw_stream_of(self.weights[0].device.index) if stream is None else stream.cuda_stream
         _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), s))
         self.steps += 1
 
@@ -1133,6 +1164,6 @@ class AdamW:
         dev = self.weights[0].device
         m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
         if self.total:
-            _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(m, "dtype"), m.data_ptr(), v.data_ptr(),
-                                          _raw_stream(dev)))
+            _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(dtype, "dtype"), m.data_ptr(), v.data_ptr(),
+                                          _raw_stream_of(dev.index)))
         return m, v
