@@ -818,9 +818,10 @@ static FpPlan fp_plan(int M, int N, int K, bool b_mn)
     const int64_t row_tiles = (M + 127) / 128;
     p.bn = row_tiles * ((N + 127) / 128) * 2 <= num_sms() || N <= 64 ? 64 : 128;
     const int64_t tiles = row_tiles * ((N + p.bn - 1) / p.bn);
-    // few tiles: slices of at least four K blocks, up to one item per SM
+    // few tiles: slices of at least 16 K blocks, up to one item per SM (a shorter K is done before
+    // the join's launch would be)
     int64_t splits = num_sms() / tiles;
-    if (splits > num_kb / 4) splits = num_kb / 4;
+    if (splits > num_kb / 16) splits = num_kb / 16;
     if (splits > 1) {
         p.kb_per_split = (num_kb + (int)splits - 1) / (int)splits;
         p.splits = (num_kb + p.kb_per_split - 1) / p.kb_per_split;

@@ -16,7 +16,7 @@ namespace ito {
 
 // ------------------------------------------------------------- a few rows of x
 //
-// With up to 32 rows the product reads W once and does little with it: W's bytes bound it.
+// With up to 16 rows the product reads W once and does little with it: W's bytes bound it.
 // A warp takes 16 rows of W as the 16 x 16 operand of mma.sync and eight rows of x (a token
 // each; missing ones are 0) as the 16 x 8 one. The sum over k may be taken in any order, so
 // the fragments' k are assigned such that each lane reads 16 consecutive bytes of a row of W
@@ -24,7 +24,8 @@ namespace ito {
 // 16 k from one wide load each. A block's warps share the 16 rows and take turns along k; their
 // sums meet in shared memory, in the warps' order.
 
-constexpr int kRowsMost = 32;        // rows of x this kernel takes
+constexpr int kRowsMost = 16;        // rows of x this kernel takes (4096 x 4096: 7.4 us with 8, 12.7 with 16, 20 with
+                                     // 32, where the tensor cores' kernel takes 14)
 
 __device__ __forceinline__ void mma_16816(int type, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
@@ -110,16 +111,27 @@ __global__ void __launch_bounds__(512)
 
 // --------------------------------------------------------- element-wise passes
 
-// rows whose starts TMA cannot address, copied to rows padded to 8 elements
-__global__ void __launch_bounds__(256)
-    k_fp_align(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
-               int64_t ldd)
+// Rows whose starts TMA cannot address, copied to rows padded to 8 elements; up to two tensors
+// (blockIdx.z).
+struct FpCopy {
+    const uint16_t* src[2];
+    uint16_t* dst[2];
+    int64_t ld[2], ldd[2];
+    int rows[2], cols[2];
+    int n;
+};
+
+__global__ void __launch_bounds__(256) k_fp_align(const __grid_constant__ FpCopy c)
 {
     griddep_wait();
     griddep_launch_dependents();
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        for (int c = blockIdx.x * 1024 + threadIdx.x; c < min(cols, ((int)blockIdx.x + 1) * 1024); c += 256)
-            dst[r * ldd + c] = src[r * ld + c];
+    const int z = blockIdx.z;
+    const uint16_t* src = c.src[z];
+    uint16_t* dst = c.dst[z];
+    const int end = min(c.cols[z], ((int)blockIdx.x + 1) * 1024);
+    for (int64_t r = blockIdx.y; r < c.rows[z]; r += gridDim.y)
+#pragma unroll 4
+        for (int i = blockIdx.x * 1024 + threadIdx.x; i < end; i += 256) dst[r * c.ldd[z] + i] = src[r * c.ld[z] + i];
 }
 
 // dz = dy act'(z), rounded to the operands' type (dz may be null), and the columns' sums before
@@ -257,8 +269,8 @@ static size_t copy_bytes(const void* p, int64_t ld, int rows, int cols)
     return tma_rows(p, ld, rows, cols) ? 0 : align256((size_t)rows * pad8(cols) * 2);
 }
 
-// the operand itself, or its aligned copy at *ws (which moves on)
-static const void* aligned_operand(const void* p, int64_t* ld, int rows, int cols, char** ws, cudaStream_t s)
+// The operand itself, or where its aligned copy will be (at *ws, which moves on), noted in `c`.
+static const void* aligned_operand(const void* p, int64_t* ld, int rows, int cols, char** ws, FpCopy* c)
 {
     if (tma_rows(p, *ld, rows, cols)) {
         *ld = row_stride(*ld, rows, cols);
@@ -266,10 +278,27 @@ static const void* aligned_operand(const void* p, int64_t* ld, int rows, int col
     }
     uint16_t* dst = reinterpret_cast<uint16_t*>(*ws);
     *ws += copy_bytes(p, *ld, rows, cols);
-    launch_pdl(k_fp_align, dim3((cols + 1023) / 1024, rows < 16384 ? rows : 16384), 256, 0, s,
-               static_cast<const uint16_t*>(p), *ld, (int64_t)rows, cols, dst, pad8(cols));
+    c->src[c->n] = static_cast<const uint16_t*>(p);
+    c->dst[c->n] = dst;
+    c->ld[c->n] = *ld;
+    c->ldd[c->n] = pad8(cols);
+    c->rows[c->n] = rows;
+    c->cols[c->n] = cols;
+    ++c->n;
     *ld = pad8(cols);
     return dst;
+}
+
+static int run_copies(const FpCopy& c, cudaStream_t s)
+{
+    if (!c.n) return ITO_OK;
+    int rows = 0, cols = 0;
+    for (int i = 0; i < c.n; ++i) {
+        rows = std::max(rows, c.rows[i]);
+        cols = std::max(cols, c.cols[i]);
+    }
+    launch_pdl(k_fp_align, dim3((cols + 1023) / 1024, std::min(rows, 16384), c.n), 256, 0, s, c);
+    return launch_status("linear operand copy");
 }
 
 static int check_sizes(int B, int IC, int OC)
@@ -350,11 +379,13 @@ int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, co
     const FpEpilogue e{bias, bias_type, act, residual, ldr, type, out_type, y, ldy, z, ldz};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (B <= 8) return run_rows<1>(x, ldx, W, ldw, B, IC, OC, e, s);
-    if (B <= 16) return run_rows<2>(x, ldx, W, ldw, B, IC, OC, e, s);
-    if (B <= kRowsMost) return run_rows<4>(x, ldx, W, ldw, B, IC, OC, e, s);
+    if (B <= kRowsMost) return run_rows<2>(x, ldx, W, ldw, B, IC, OC, e, s);
     char* ws = static_cast<char*>(workspace);
-    const void* xa = aligned_operand(x, &ldx, B, IC, &ws, s);
-    const void* wa = aligned_operand(W, &ldw, OC, IC, &ws, s);
+    FpCopy copies{};
+    const void* xa = aligned_operand(x, &ldx, B, IC, &ws, &copies);
+    const void* wa = aligned_operand(W, &ldw, OC, IC, &ws, &copies);
+    r = run_copies(copies, s);
+    if (r) return r;
     const FpProduct product{FpOperand{xa, ldx, false}, FpOperand{wa, ldw, false}, B, OC, IC, e};
     return fp_gemm(&product, 1, ws, s);
 }
@@ -420,9 +451,10 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
     char* ww = wx + copy_bytes(x, ldx, B, IC);
     char* wp = ww + copy_bytes(W, ldw, OC, IC);
     FpProduct products[2];
+    FpCopy copies{};
     int n = 0;
     if (dx) {
-        const void* wa = aligned_operand(W, &ldw, OC, IC, &ww, s);
+        const void* wa = aligned_operand(W, &ldw, OC, IC, &ww, &copies);
         FpEpilogue e{};
         e.type = e.out_type = type;
         e.y = dx;
@@ -430,7 +462,7 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
         products[n++] = FpProduct{FpOperand{d, ldd, false}, FpOperand{wa, ldw, true}, B, IC, OC, e};
     }
     if (dW) {
-        const void* xa = aligned_operand(x, &ldx, B, IC, &wx, s);
+        const void* xa = aligned_operand(x, &ldx, B, IC, &wx, &copies);
         FpEpilogue e{};
         e.type = type;
         e.out_type = out_type;
@@ -438,7 +470,8 @@ int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, 
         e.ldy = lddw;
         products[n++] = FpProduct{FpOperand{d, ldd, true}, FpOperand{xa, ldx, true}, OC, IC, B, e};
     }
-    if (n) r = fp_gemm(products, n, wp, s);
+    r = run_copies(copies, s);
+    if (!r && n) r = fp_gemm(products, n, wp, s);
     return r ? r : launch_status("linear backward");
 }
 
