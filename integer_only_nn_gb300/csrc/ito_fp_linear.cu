@@ -16,7 +16,7 @@ namespace ito {
 
 // ------------------------------------------------------------- a few rows of x
 //
-// With up to 16 rows the product reads W once and does little with it: W's bytes bound it.
+// With a few rows the product reads W once and does little with it: W's bytes bound it.
 // A warp takes 16 rows of W as the 16 x 16 operand of mma.sync and eight rows of x (a token
 // each; missing ones are 0) as the 16 x 8 one. The sum over k may be taken in any order, so
 // the fragments' k are assigned such that each lane reads 16 consecutive bytes of a row of W
@@ -24,8 +24,15 @@ namespace ito {
 // 16 k from one wide load each. A block's warps share the 16 rows and take turns along k; their
 // sums meet in shared memory, in the warps' order.
 
-constexpr int kRowsMost = 16;        // rows of x this kernel takes (4096 x 4096: 7.4 us with 8, 12.7 with 16, 20 with
-                                     // 32, where the tensor cores' kernel takes 14)
+// Rows of x this kernel takes: 16, and 32 up to 2^24 elements of W. us against the tensor cores'
+// kernel's: 4096 x 4096 with 32 rows 12.4 : 14.0, 1024 x 1000 4.3 : 6.9, 8192 x 8192 49 : 36 (the
+// blocks' reads of x, which grow with both, pass through L2).
+// 4096 x 4096: 5.6 us with one row (W at the memory's rate: 5.0), 8.2 with 16; 8192 x 8192 24.5
+// with one (20.1). With each step's loads waiting for the step before, one row took 7.4.
+static bool rows_kernel(int B, int IC, int OC)
+{
+    return B <= 16 || (B <= 32 && (int64_t)IC * OC <= (1 << 24));
+}
 
 __device__ __forceinline__ void mma_16816(int type, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
@@ -53,13 +60,25 @@ __device__ __forceinline__ uint4 load_eight(const uint16_t* row, int k, int n, b
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(512)
-    k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, int x_vec, const uint16_t* __restrict__ W, int64_t ldw,
-              int w_vec, int B, int IC, int OC, const __grid_constant__ FpEpilogue e)
+__device__ __forceinline__ uint4 load_once(const uint16_t* p)      // (read by one block: not for L1)
 {
-    constexpr int U = NT == 1 ? 8 : 4;      // steps of 32 k whose loads are in flight together
-    __shared__ float part[16][16 * 8 * NT];
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+constexpr int kRowsSteps = 4;        // steps of 32 k whose loads of W are in flight together
+constexpr int kRowsWarps = 8;        // of a block, at most
+
+// VEC: both operands' rows start on 16-byte boundaries and IC is a multiple of 8
+template <int NT, bool VEC>
+__global__ void __launch_bounds__(kRowsWarps * 32)
+    k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ W, int64_t ldw, int B, int IC,
+              int OC, const __grid_constant__ FpEpilogue e)
+{
+    constexpr int U = kRowsSteps;
+    __shared__ float part[kRowsWarps][16 * 8 * NT];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -69,30 +88,51 @@ __global__ void __launch_bounds__(512)
     const uint16_t* w0 = W + (int64_t)(in0 ? oc0 + g : 0) * ldw;
     const uint16_t* w1 = W + (int64_t)(in1 ? oc0 + g + 8 : 0) * ldw;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    auto load = [&](const uint16_t* row, int k, bool in) {
+        if (VEC) return in && k < IC ? load_once(row + k) : zero;
+        return in && k < IC ? load_eight(row, k, IC, false) : zero;
+    };
     float c[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
-    for (int k0 = warp * U * 32; k0 < IC; k0 += warps * U * 32) {
-        uint4 a[U], b[U];
+    uint4 a[U], b[U];
+    const int stride = warps * U * 32;
+    int k0 = warp * U * 32;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        a[u] = load(w0, k0 + u * 32 + t * 8, in0);
+        b[u] = load(w1, k0 + u * 32 + t * 8, in1);
+    }
+    for (; k0 < IC; k0 += stride) {
+        // the next steps' rows of W are on their way while these are multiplied
+        uint4 an[U], bn[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * 32 + t * 8;
-            a[u] = in0 && k < IC ? load_eight(w0, k, IC, w_vec) : zero;
-            b[u] = in1 && k < IC ? load_eight(w1, k, IC, w_vec) : zero;
+            an[u] = load(w0, k0 + stride + u * 32 + t * 8, in0);
+            bn[u] = load(w1, k0 + stride + u * 32 + t * 8, in1);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const bool in = n * 8 + g < B;
             const uint16_t* xr = x + (int64_t)(in ? n * 8 + g : 0) * ldx;
+            uint4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = k0 + u * 32 + t * 8;
-                const uint4 v = in && k < IC ? load_eight(xr, k, IC, x_vec) : zero;
-                mma_16816(e.type, c[n], a[u].x, b[u].x, a[u].y, b[u].y, v.x, v.y);
-                mma_16816(e.type, c[n], a[u].z, b[u].z, a[u].w, b[u].w, v.z, v.w);
+                v[u] = in && k < IC ? load_eight(xr, k, IC, VEC) : zero;
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                mma_16816(e.type, c[n], a[u].x, b[u].x, a[u].y, b[u].y, v[u].x, v[u].y);
+                mma_16816(e.type, c[n], a[u].z, b[u].z, a[u].w, b[u].w, v[u].z, v[u].w);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            a[u] = an[u];
+            b[u] = bn[u];
         }
     }
 #pragma unroll
@@ -336,12 +376,10 @@ template <int NT>
 static int run_rows(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC,
                     const FpEpilogue& e, cudaStream_t s)
 {
-    // as many warps as have two steps of 128 or 256 k each, at most 16
-    const int step = 2 * 32 * (NT == 1 ? 8 : 4);
-    const int warps = std::min(16, std::max(1, IC / step));
-    launch_pdl(k_fp_rows<NT>, (OC + 15) / 16, warps * 32, 0, s, static_cast<const uint16_t*>(x), ldx,
-               (int)tma_rows(x, ldx, B, IC), static_cast<const uint16_t*>(W), ldw, (int)tma_rows(W, ldw, OC, IC), B, IC,
-               OC, e);
+    const int warps = std::min(kRowsWarps, std::max(1, (IC + 32 * kRowsSteps - 1) / (32 * kRowsSteps)));
+    const bool vec = IC % 8 == 0 && tma_rows(x, ldx, B, IC) && tma_rows(W, ldw, OC, IC);
+    launch_pdl(vec ? k_fp_rows<NT, true> : k_fp_rows<NT, false>, (OC + 15) / 16, warps * 32, 0, s,
+               static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(W), ldw, B, IC, OC, e);
     return launch_status("linear");
 }
 
@@ -353,7 +391,7 @@ extern "C" {
 
 size_t ito_fp_linear_fwd_workspace_size(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC)
 {
-    if (check_sizes(B, IC, OC) || B <= kRowsMost) return 0;
+    if (check_sizes(B, IC, OC) || rows_kernel(B, IC, OC)) return 0;
     return copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) + align256(fp_gemm_ws_bytes(B, OC, IC));
 }
 
@@ -378,8 +416,12 @@ int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, co
     if (r) return r;
     const FpEpilogue e{bias, bias_type, act, residual, ldr, type, out_type, y, ldy, z, ldz};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (B <= 8) return run_rows<1>(x, ldx, W, ldw, B, IC, OC, e, s);
-    if (B <= kRowsMost) return run_rows<2>(x, ldx, W, ldw, B, IC, OC, e, s);
+    if (rows_kernel(B, IC, OC)) {
+        if (B <= 8) return run_rows<1>(x, ldx, W, ldw, B, IC, OC, e, s);
+        if (B <= 16) return run_rows<2>(x, ldx, W, ldw, B, IC, OC, e, s);
+        if (B <= 24) return run_rows<3>(x, ldx, W, ldw, B, IC, OC, e, s);
+        return run_rows<4>(x, ldx, W, ldw, B, IC, OC, e, s);
+    }
     char* ws = static_cast<char*>(workspace);
     FpCopy copies{};
     const void* xa = aligned_operand(x, &ldx, B, IC, &ws, &copies);
