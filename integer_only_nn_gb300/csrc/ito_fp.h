@@ -33,10 +33,10 @@ struct FpProduct {
     FpEpilogue e;
 };
 
-// One or two products that do not depend on one another, on the tensor cores; ws: the bytes that
-// fp_gemm_ws_bytes names for the larger need (partial sums of a product split along K), 256-byte
-// aligned.
-size_t fp_gemm_ws_bytes(int M, int N, int K);
+// One or two products that do not depend on one another, on the tensor cores; ws: the sum of the
+// bytes that fp_gemm_ws_bytes names for each (sums of a product cut into slices of K; b_mn: B.mn),
+// 256-byte aligned.
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn);
 int fp_gemm(const FpProduct* products, int n, void* ws, cudaStream_t s);
 
 }  // namespace ito

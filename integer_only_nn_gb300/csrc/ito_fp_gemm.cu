@@ -11,7 +11,8 @@
 // feeds twice the work), or narrower ones, for results with enough of them to occupy the device; 128 x 128 and
 // 128 x 64 tiles of one CTA, with K cut into slices where there are few tiles, for the rest.
 // Slices write their sums in 32 bits to the workspace, and a second kernel adds them in a fixed
-// order and does the epilogue.
+// order and does the epilogue. A weight gradient over a long batch is such a product too.
+#include <algorithm>
 #include <cstring>
 
 #include "ito_fp_epilogue.cuh"
@@ -328,14 +329,16 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32])
 }
 
 // The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
-// (row, col0), sums at `taddr`; `done` tells the MMA thread that the accumulator is drained.
+// (row, col0), sums at `taddr`; `done` tells the issuing warp that the accumulator is drained. A
+// slice of K (slice >= 0) leaves its sums as they are, in mapS.
 template <typename Wait, typename Done>
 __device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
-                                           FpStage& st, int first, int step, int columns, int col0,
-                                           int row, uint32_t taddr, Wait wait, Done done, bool& ok)
+                                           const CUtensorMap* mapS, int slice, FpStage& st, int first, int step,
+                                           int columns, int col0, int row, uint32_t taddr, Wait wait, Done done,
+                                           bool& ok)
 {
     // a 16-bit residual comes while the sums are still being made
-    const bool res16 = a.e.residual && a.e.out_type != ITO_F32;
+    const bool res16 = slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
     uint32_t res[16];
     if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
     if (!wait()) {
@@ -353,6 +356,20 @@ __device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMa
             done();
         }
         if (row >= a.M || col0 + c >= a.N) continue;
+        if (slice >= 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (col0 + c + 16 * h >= a.N) break;
+                uint8_t* stg = stage32(v, h, st);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (st.lane == 0) {
+                    tma_store_3d(mapS, stg, col0 + c + 16 * h, row, slice);
+                    bulk_commit();
+                }
+            }
+            continue;
+        }
         if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
         finish_group(a, mapY, mapZ, v, res, st, col0 + c, row);
     }
@@ -365,7 +382,6 @@ struct FpCfg {
     static constexpr int BM = 128, BK = 64;
     static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARPS = 8;                  // two to a quarter of the rows
-    static constexpr int GROUPS = BN / 64;               // of 32 columns to a warp
     static constexpr int THREADS = 64 + EPI_WARPS * 32;
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int STAGES = BN == 128 ? 6 : 8;
@@ -488,40 +504,11 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
         for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
-            const int row = tm * BM + quad * 32, col = tn * BN;
-            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
-            if (a.splits > 1) {
-                if (!warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int g = 0; g < Cfg::GROUPS; ++g) {
-                    const int c = (part + 2 * g) * 32;
-                    float v[32];
-                    load_sums(taddr + c, v);
-                    if (g + 1 == Cfg::GROUPS) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acce_bar[buf]);
-                    }
-                    if (row >= a.M || col + c >= a.N) continue;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (col + c + 16 * h >= a.N) break;
-                        uint8_t* stg = stage32(v, h, st);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_3d(&mapS, stg, col + c + 16 * h, row, w % a.splits);
-                            bulk_commit();
-                        }
-                    }
-                }
-            } else {
-                drain_tile(
-                    a, &mapY, &mapZ, st, part, 2, BN, col, row, taddr,
-                    [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
-                    [&] { if (lane == 0) mbar_arrive(&acce_bar[buf]); }, ok);
-            }
+            drain_tile(
+                a, &mapY, &mapZ, &mapS, a.splits > 1 ? w % a.splits : -1, st, part, 2, BN, tn * BN, tm * BM + quad * 32,
+                tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN),
+                [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
+                [&] { if (lane == 0) mbar_arrive(&acce_bar[buf]); }, ok);
             if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
         if (lane == 0) bulk_wait_all();
@@ -551,43 +538,43 @@ struct FpPairCfg {
 };
 
 struct FpProblem {
-    CUtensorMap A, B, Y, Z;
+    CUtensorMap A, B, Y, Z, S;
     FpGemmArgs a;
 };
 
-// One product, or two in one launch (the backward pass's), so that the second's tiles fill the
-// first's last wave. The tiles of problem 0, the one with the longer K, go round the pairs; of
-// its last round `rest` pairs have one, and the others meanwhile take `gap` tiles each of
-// problem 1, whose remaining tiles go round all pairs. At 2048 x 4096 x 4096 the two products
+// One product, or two in one launch (the backward pass's), so that the second's items (tiles, or
+// their K slices) fill the first's last wave. The items of problem 0, whose K range is the longer
+// one, go round the pairs; of its last round `rest` pairs have one, and the others meanwhile take
+// `gap` items each of problem 1, whose remaining items go round all pairs. At 2048 x 4096 x 4096 the two products
 // are 2 + 4 waves one by one, 7/8 of that together. A launch of one product has a kernel of its
 // own: with the second one's branches 8192 x 4096 x 4096 took 156 us instead of 144.
 template <int PROBLEMS>
 struct FpPairWork {
     FpProblem p[PROBLEMS];
-    int tiles[2];
+    int items[2];
     int rest, gap;
 
     // item k of pair c of C
-    __device__ __forceinline__ bool item(int k, int c, int C, int& problem, int& tile) const
+    __device__ __forceinline__ bool item(int k, int c, int C, int& problem, int& i) const
     {
         if (PROBLEMS == 1) {
             problem = 0;
-            tile = c + k * C;
-            return tile < tiles[0];
+            i = c + k * C;
+            return i < items[0];
         }
-        const int n = c < tiles[0] ? (tiles[0] - 1 - c) / C + 1 : 0;
+        const int n = c < items[0] ? (items[0] - 1 - c) / C + 1 : 0;
         problem = 0;
-        tile = c + k * C;
+        i = c + k * C;
         if (k < n) return true;
         k -= n;
         problem = 1;
         if (gap && c >= rest) {
-            tile = k * (C - rest) + c - rest;
-            if (k < gap) return tile < tiles[1];
+            i = k * (C - rest) + c - rest;
+            if (k < gap) return i < items[1];
             k -= gap;
         }
-        tile = gap * (C - rest) + k * C + c;
-        return tile < tiles[1];
+        i = gap * (C - rest) + k * C + c;
+        return i < items[1];
     }
 };
 
@@ -641,15 +628,19 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // a tile's place in its result
-    auto place = [&](const FpGemmArgs& a, int tile, int& row, int& col) {
+    // an item's place in its result, and its K blocks
+    auto place = [&](const FpGemmArgs& a, int item, int& row, int& col) {
         const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + a.bn - 1) / a.bn, a.group};
         int tm, tn;
-        tiles.coords(tile, tm, tn);
+        tiles.coords(item / a.splits, tm, tn);
         row = tm * 2 * BM + (int)rank * BM;
         col = tn * a.bn;
     };
-    int problem, tile;
+    auto k_range = [&](const FpGemmArgs& a, int item, int& lo, int& hi) {
+        lo = item % a.splits * a.kb_per_split;
+        hi = min((a.K + BK - 1) / BK, lo + a.kb_per_split);
+    };
+    int problem, item;
     if (warp == 0) {
         // both CTAs load; every load completes on the leader's barrier. (An MN-major B comes in
         // whole boxes of 64 columns, some beyond a narrow tile's half.)
@@ -662,11 +653,11 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                 const FpGemmArgs& a = p.a;
                 const bool a_mn = a.a_mn, b_mn = a.b_mn;
                 const uint32_t stage_bytes = 2 * (Cfg::A_BYTES + (b_mn ? Cfg::B_BYTES : (a.bn / 2) * BK * 2));
-                const int num_kb = (a.K + BK - 1) / BK;
-                int rowA, rowB;
-                place(a, tile, rowA, rowB);
+                int rowA, rowB, lo, hi;
+                place(a, item, rowA, rowB);
+                k_range(a, item, lo, hi);
                 rowB += (int)rank * (a.bn / 2);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = lo; kb < hi; ++kb) {
                     if (!ring_wait(&empty_bar[stage], phase ^ 1, abort_flag, err)) { ok = false; break; }
                     if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_bytes);
@@ -690,7 +681,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
             };
-            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, item); ++k) {
                 if (PROBLEMS == 1 || problem == 0) load(work.p[0]);
                 else load(work.p[LAST]);
             }
@@ -700,24 +691,25 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
-            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+            for (int k = 0; ok && work.item(k, cluster, nclusters, problem, item); ++k) {
                 const FpGemmArgs& a = PROBLEMS == 1 || problem == 0 ? work.p[0].a : work.p[LAST].a;
                 const FpSteps step(a, smem_u32(smem), Cfg::A_BYTES);
                 const uint32_t idesc = a.idesc;
-                const int num_kb = (a.K + BK - 1) / BK;
+                int lo, hi;
+                k_range(a, item, lo, hi);
                 if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, err)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(buf * Cfg::MAX_BN);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = lo; kb < hi; ++kb) {
                     if (!ring_wait(&full_bar[stage], phase, abort_flag, err)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int q = 0; q < BK / 16; ++q)
-                            tc_mma_bf16_pair(d, step.a(at, q), step.b(at, q), idesc, (kb > 0 || q > 0) ? 1u : 0u);
+                            tc_mma_bf16_pair(d, step.a(at, q), step.b(at, q), idesc, (kb > lo || q > 0) ? 1u : 0u);
                         tc_commit_pair_mc(&empty_bar[stage], 0x3);
-                        if (kb + 1 == num_kb) tc_commit_pair_mc(&accf_bar[buf], 0x3);
+                        if (kb + 1 == hi) tc_commit_pair_mc(&accf_bar[buf], 0x3);
                     }
                     __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -732,12 +724,12 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
         int buf = 0;
         uint32_t buf_phase = 0;
         bool ok = true;
-        for (int k = 0; ok && work.item(k, cluster, nclusters, problem, tile); ++k) {
+        for (int k = 0; ok && work.item(k, cluster, nclusters, problem, item); ++k) {
             const FpProblem& p = PROBLEMS == 1 || problem == 0 ? work.p[0] : work.p[LAST];
             int row, col;
-            place(p.a, tile, row, col);
+            place(p.a, item, row, col);
             drain_tile(
-                p.a, &p.Y, &p.Z, st, part, Cfg::EPI_WARPS / 4, p.a.bn, col, row + quad * 32,
+                p.a, &p.Y, &p.Z, &p.S, p.a.splits > 1 ? item % p.a.splits : -1, st, part, Cfg::EPI_WARPS / 4, p.a.bn, col, row + quad * 32,
                 tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN),
                 [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err); },
                 [&] { if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
@@ -789,53 +781,56 @@ struct FpPlan {
     int bn, splits, kb_per_split;
 };
 
-// A pair's tile takes four times a 128 x 128 tile's work on two SMs; pairs win once their tiles
-// occupy at least half of the device's pairs. Their width is the one whose waves read the
-// fewest operand rows (256 of A and bn of B a tile, an MN-major B in boxes of 64 to each block:
-// L2's rate paces the products), the wider one among equals. 2048 x 4096 x 4096: 42.5 us with 224 columns, 47.6 with 256; 8192 x 4096 x 4096: 143 us
-// with 256, 199 with 160, whose waves compute fewer columns.
+// Which kernel, tile width and number of K slices take the least estimated time. An SM takes
+// operands from L2 at about 100 KB a us (8192 x 4096 x 4096: a K block of a 256-column pair's tile is
+// 32 KB an SM and took 0.32 us), a K block of products takes at least 0.27 us for 256 columns,
+// and a block's loads and their waits about 0.12; a join takes 2.5 us and the slices' sums pass
+// through memory at 4 TB/s. It orders the measured choices (us): 8192 x 4096 x 4096 144 with
+// 256 columns, 199 with 160; 2048 x 4096 x 4096 39.5 with 224, 47 with 256; 512 x 4096 x 4096 20 in
+// 128 x 128 tiles, 18 in pairs of 128 columns; 33 x 6080 x 5824 27 whole, 20 in three slices.
 static FpPlan fp_plan(int M, int N, int K, bool b_mn)
 {
-    FpPlan p{};
-    const int num_kb = (K + 63) / 64;
-    p.splits = 1;
-    p.kb_per_split = num_kb;
-    const int64_t pair_tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-    p.pair = M > 128 && N > 128 && 4 * pair_tiles >= num_sms();
-    if (p.pair) {
-        const int64_t pairs = num_sms() / 2;
-        int64_t best = INT64_MAX;
-        for (int bn = 256; bn >= 128; bn -= 32) {
-            const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + bn - 1) / bn);
-            const int64_t cost = (tiles + pairs - 1) / pairs * (256 + (b_mn ? (bn + 127) / 128 * 128 : bn));
-            if (cost < best) {
-                best = cost;
-                p.bn = bn;
+    const int num_kb = (K + 63) / 64, sms = num_sms(), pairs = sms / 2;
+    FpPlan best{};
+    double best_us = 1e30;
+    // `tiles` tiles on `workers` SMs or pairs, whole and in up to 16 slices of at least four K blocks
+    auto consider = [&](bool pair, int bn, int64_t tiles, int workers, double kb_us, double fixed) {
+        for (int s = 1; s <= 16 && (s == 1 || num_kb / s >= 4); ++s) {
+            const int per = (num_kb + s - 1) / s;
+            if ((num_kb + per - 1) / per != s) continue;
+            const double join = s > 1 ? 2.5 + 2.0 * s * M * N * 4 / 4e6 : 0;
+            const double us = fixed + (double)((tiles * s + workers - 1) / workers) * per * kb_us + join;
+            if (us < best_us) {
+                best_us = us;
+                best = FpPlan{pair, bn, s, per};
             }
         }
-        return p;
-    }
+    };
+    if (M > 128 && N > 64)
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + bn - 1) / bn);
+            const int loaded = b_mn ? (bn + 127) / 128 * 128 : bn;
+            const double kb_us = std::max(0.27 * bn / 256, (16.0 + loaded / 16.0) / 100);
+            consider(true, bn, tiles, pairs, kb_us, 3);
+        }
     const int64_t row_tiles = (M + 127) / 128;
-    p.bn = row_tiles * ((N + 127) / 128) * 2 <= num_sms() || N <= 64 ? 64 : 128;
-    const int64_t tiles = row_tiles * ((N + p.bn - 1) / p.bn);
-    // few tiles: slices of at least 16 K blocks, up to one item per SM (a shorter K is done before
-    // the join's launch would be)
-    int64_t splits = num_sms() / tiles;
-    if (splits > num_kb / 16) splits = num_kb / 16;
-    if (splits > 1) {
-        p.kb_per_split = (num_kb + (int)splits - 1) / (int)splits;
-        p.splits = (num_kb + p.kb_per_split - 1) / p.kb_per_split;
+    const double a_kb = 16.0 * std::min(M, 128) / 128;
+    for (int bn = 128; bn >= 64; bn -= 64) {
+        const int64_t tiles = row_tiles * ((N + bn - 1) / bn);
+        const double kb_us = std::max(0.12, (a_kb + bn / 8.0) / 100);
+        consider(false, bn, tiles, sms, kb_us, 4);
     }
-    return p;
+    return best;
 }
 
 static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
-size_t fp_gemm_ws_bytes(int M, int N, int K)
+static size_t plan_bytes(const FpPlan& p, int M, int N)
 {
-    const FpPlan p = fp_plan(M, N, K, false);      // (slices do not depend on the operands' order)
-    return p.splits > 1 ? (size_t)p.splits * M * pad4(N) * sizeof(float) : 0;
+    return p.splits > 1 ? ((size_t)p.splits * M * pad4(N) * sizeof(float) + 255) & ~size_t(255) : 0;
 }
+
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn) { return plan_bytes(fp_plan(M, N, K, b_mn), M, N); }
 
 // 2-D box map over a row-major tensor of 16-bit or 32-bit elements: rows of 128 bytes with the
 // 128-byte swizzle, or of 64 bytes with the 64-byte one
@@ -909,7 +904,7 @@ static int launch_single(const CUtensorMap& A, const CUtensorMap& B, const CUten
 }
 
 // the arguments and tensor maps that both kernels take
-static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p)
+static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p, void* ws)
 {
     const FpEpilogue& e = c.e;
     FpGemmArgs& a = q->a;
@@ -938,22 +933,46 @@ static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p)
                     c.B.mn ? 64 : p.pair ? p.bn / 2 : p.bn);
     if (!r && a.y_tma) r = box_map(&q->Y, e.y, wide, c.M, c.N, e.ldy, 32, 64);
     if (!r && a.z_tma) r = box_map(&q->Z, e.z, false, c.M, c.N, e.ldz, 32, 64);
+    if (!r && p.splits > 1) {
+        // the slices' sums [splits][M][pitch]
+        const int64_t pitch = pad4(c.N);
+        auto enc = get_encode();
+        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)c.M, (cuuint64_t)p.splits};
+        cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * c.M * 4};
+        cuuint32_t box[3] = {16, 32, 1};
+        cuuint32_t estr[3] = {1, 1, 1};
+        const CUresult cr = enc(&q->S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (cr != CUDA_SUCCESS) r = set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled (partials) failed (%d)", (int)cr);
+    }
     return r;
 }
 
-static int pair_tiles(const FpProblem& q) { return ((q.a.M + 255) / 256) * ((q.a.N + q.a.bn - 1) / q.a.bn); }
+static int run_join(const FpProduct& c, const FpPlan& p, const void* ws, cudaStream_t s)
+{
+    const int64_t pitch = pad4(c.N);
+    launch_pdl(k_fp_join, launch_grid_blocks((int64_t)c.M * (pitch / 4), 256), 256, 0, s, static_cast<const float*>(ws),
+               p.splits, pitch * c.M, (int)pitch, c.M, c.N, c.e);
+    return launch_status("linear join");
+}
+
+static int pair_items(const FpProblem& q)
+{
+    return ((q.a.M + 255) / 256) * ((q.a.N + q.a.bn - 1) / q.a.bn) * q.a.splits;
+}
 
 template <int PROBLEMS>
 static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
 {
     const int most = max_pairs<PROBLEMS>();
     if (!most) return set_error(ITO_ERR_CUDA, "no CTA pair fits on this device");
-    const int tiles = w.tiles[0] + w.tiles[1], pairs = tiles < most ? tiles : most;
+    const int items = w.items[0] + w.items[1], pairs = items < most ? items : most;
     w.rest = w.gap = 0;
     if (PROBLEMS == 2) {
-        w.rest = w.tiles[0] % pairs;
-        // (K blocks tell a tile's time: both problems' tiles have the same width or nearly)
-        if (w.rest) w.gap = ((w.p[0].a.K + 63) / 64) / ((w.p[PROBLEMS - 1].a.K + 63) / 64);
+        w.rest = w.items[0] % pairs;
+        // (K blocks tell an item's time: both problems' tiles have the same width or nearly)
+        if (w.rest) w.gap = w.p[0].a.kb_per_split / w.p[PROBLEMS - 1].a.kb_per_split;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
@@ -973,59 +992,44 @@ static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "linear product launch: %s", cudaGetErrorString(e));
 }
 
-static int run_single(const FpProduct& c, const FpPlan& p, void* ws, cudaStream_t s)
-{
-    FpProblem q;
-    memset(&q, 0, sizeof(q));
-    int r = fill_problem(&q, c, p);
-    if (r) return r;
-    CUtensorMap S;
-    memset(&S, 0, sizeof(S));
-    const int64_t pitch = pad4(c.N);
-    if (p.splits > 1) {
-        auto enc = get_encode();
-        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)c.M, (cuuint64_t)p.splits};
-        cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * c.M * 4};
-        cuuint32_t box[3] = {16, 32, 1};
-        cuuint32_t estr[3] = {1, 1, 1};
-        const CUresult cr = enc(&S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (cr != CUDA_SUCCESS) return set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled (partials) failed (%d)", (int)cr);
-    }
-    r = p.bn == 128 ? launch_single<128>(q.A, q.B, q.Y, q.Z, S, q.a, s) : launch_single<64>(q.A, q.B, q.Y, q.Z, S, q.a, s);
-    if (r || p.splits == 1) return r;
-    launch_pdl(k_fp_join, launch_grid_blocks((int64_t)c.M * (pitch / 4), 256), 256, 0, s, static_cast<const float*>(ws),
-               p.splits, pitch * c.M, (int)pitch, c.M, c.N, c.e);
-    return launch_status("linear join");
-}
-
 int fp_gemm(const FpProduct* c, int n, void* ws, cudaStream_t s)
 {
     FpPlan p[2];
-    for (int i = 0; i < n; ++i) p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn);
-    if (n == 2 && p[0].pair && p[1].pair) {
+    void* at[2];
+    for (int i = 0; i < n; ++i) {
+        p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn);
+        at[i] = ws;
+        ws = static_cast<char*>(ws) + plan_bytes(p[i], c[i].M, c[i].N);
+    }
+    const bool both = n == 2 && p[0].pair && p[1].pair;
+    if (both) {
         FpPairWork<2> w;
         memset(&w, 0, sizeof(w));
-        const int first = c[0].K >= c[1].K ? 0 : 1;
+        const int first = p[0].kb_per_split >= p[1].kb_per_split ? 0 : 1;
         for (int i = 0; i < 2; ++i) {
-            const int r = fill_problem(&w.p[i], c[first ^ i], p[first ^ i]);
+            const int r = fill_problem(&w.p[i], c[first ^ i], p[first ^ i], at[first ^ i]);
             if (r) return r;
-            w.tiles[i] = pair_tiles(w.p[i]);
+            w.items[i] = pair_items(w.p[i]);
         }
-        return launch_pairs(w, s);
+        const int r = launch_pairs(w, s);
+        if (r) return r;
     }
     for (int i = 0; i < n; ++i) {
-        int r;
-        if (p[i].pair) {
+        int r = ITO_OK;
+        if (!both && p[i].pair) {
             FpPairWork<1> w;
             memset(&w, 0, sizeof(w));
-            r = fill_problem(&w.p[0], c[i], p[i]);
-            w.tiles[0] = pair_tiles(w.p[0]);
+            r = fill_problem(&w.p[0], c[i], p[i], at[i]);
+            w.items[0] = pair_items(w.p[0]);
             if (!r) r = launch_pairs(w, s);
-        } else {
-            r = run_single(c[i], p[i], ws, s);
+        } else if (!both) {
+            FpProblem q;
+            memset(&q, 0, sizeof(q));
+            r = fill_problem(&q, c[i], p[i], at[i]);
+            if (!r && p[i].bn == 128) r = launch_single<128>(q.A, q.B, q.Y, q.Z, q.S, q.a, s);
+            else if (!r) r = launch_single<64>(q.A, q.B, q.Y, q.Z, q.S, q.a, s);
         }
+        if (!r && p[i].splits > 1) r = run_join(c[i], p[i], at[i], s);
         if (r) return r;
     }
     return ITO_OK;

@@ -392,7 +392,7 @@ extern "C" {
 size_t ito_fp_linear_fwd_workspace_size(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC)
 {
     if (check_sizes(B, IC, OC) || rows_kernel(B, IC, OC)) return 0;
-    return copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) + align256(fp_gemm_ws_bytes(B, OC, IC));
+    return copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) + fp_gemm_ws_bytes(B, OC, IC, false);
 }
 
 int ito_fp_linear_fwd(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* bias, const void* residual,
@@ -438,7 +438,7 @@ size_t ito_fp_linear_bwd_workspace_size(const void* dy, int64_t lddy, const void
     if (check_sizes(B, IC, OC)) return 0;
     const bool dz = act != ITO_ACT_NONE || !tma_rows(dy, lddy, B, OC);
     return (dz ? align256((size_t)B * pad8(OC) * 2) : 0) + copy_bytes(x, ldx, B, IC) + copy_bytes(W, ldw, OC, IC) +
-           align256(std::max(fp_gemm_ws_bytes(B, IC, OC), fp_gemm_ws_bytes(OC, IC, B)));
+           fp_gemm_ws_bytes(B, IC, OC, true) + fp_gemm_ws_bytes(OC, IC, B, true);
 }
 
 int ito_fp_linear_bwd(const void* dy, int64_t lddy, const void* z, int64_t ldz, const void* x, int64_t ldx,
