@@ -20,65 +20,88 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+// Activations and their slopes are computed for two elements at a time with packed operations:
+// one at a time they bound the backward pass's element-wise kernel (30 instructions an element,
+// most of them the GELU's).
+
 // 1 / (1 + exp(-v)), to a few units of a 32-bit float
-__device__ __forceinline__ float logistic(float v) { return rcp_approx(1.0f + exp2_approx(-1.4426950408889634f * v)); }
+__device__ __forceinline__ float2 logistic(float2 v)
+{
+    const float2 y = __fmul2_rn(v, splat(-1.4426950408889634f));
+    const float2 d = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), splat(1.0f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
 
 // The normal distribution function Phi(z) = (1 + erf(z / sqrt 2)) / 2 and exp(-z^2 / 2), by the
 // rational approximation of erf in Abramowitz and Stegun, formula 7.1.26 (error below 1.5e-7):
-//   1 - erf(a) = (a1 t + .. + a5 t^5) exp(-a^2),  t = 1 / (1 + p a),  a >= 0
-// One exponential serves both; erff and expf took about twice the instructions, and the
-// backward pass's element-wise kernel was bound by them.
-__device__ __forceinline__ float normal_cdf(float z, float& bell)
+//   1 - erf(a) = (a1 t + .. + a5 t^5) exp(-a^2),  t = 1 / (1 + p a),  a = |z| / sqrt 2
+// (the coefficients below are halved, p divided by sqrt 2). One exponential serves both.
+__device__ __forceinline__ float2 normal_cdf(float2 z, float2& bell)
 {
-    const float a = fabsf(z) * 0.70710678118654752f;
-    const float t = rcp_approx(fmaf(0.3275911f, a, 1.0f));
-    bell = exp2_approx(z * z * -0.72134752044448170f);
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * bell;
-    return z < 0.0f ? tail : 1.0f - tail;
+    const float2 d = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), splat(0.23164189f), splat(1.0f));
+    const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    const float2 y = __fmul2_rn(__fmul2_rn(z, z), splat(-0.72134752044448170f));
+    bell = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+    float2 q = __ffma2_rn(splat(0.5307027145f), t, splat(-0.7265760135f));
+    q = __ffma2_rn(q, t, splat(0.7107068705f));
+    q = __ffma2_rn(q, t, splat(-0.142248368f));
+    q = __ffma2_rn(q, t, splat(0.127414796f));
+    const float2 tail = __fmul2_rn(__fmul2_rn(q, t), bell);
+    const float2 rest = __ffma2_rn(tail, splat(-1.0f), splat(1.0f));
+    return make_float2(z.x < 0.0f ? tail.x : rest.x, z.y < 0.0f ? tail.y : rest.y);
 }
 
-// tanh's argument in the approximate GELU, twice (z (1 + tanh u) / 2 = z / (1 + exp(-2u)))
-__device__ __forceinline__ float gelu_tanh_argument(float z)
+// twice tanh's argument in the approximate GELU (z (1 + tanh u) / 2 = z / (1 + exp(-2u))), over z
+__device__ __forceinline__ float2 gelu_tanh_factor(float2 z2)
 {
-    return z * fmaf(0.07135481627260025f, z * z, 1.5957691216057308f);
+    return __ffma2_rn(z2, splat(0.07135481627260025f), splat(1.5957691216057308f));
 }
 
+template <int ACT>
+__device__ __forceinline__ float2 act_value(float2 z)
+{
+    if (ACT == ITO_ACT_RELU) return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
+    if (ACT == ITO_ACT_GELU) {
+        float2 bell;
+        return __fmul2_rn(z, normal_cdf(z, bell));
+    }
+    if (ACT == ITO_ACT_GELU_TANH) return __fmul2_rn(z, logistic(__fmul2_rn(z, gelu_tanh_factor(__fmul2_rn(z, z)))));
+    if (ACT == ITO_ACT_SILU) return __fmul2_rn(z, logistic(z));
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_slope(float2 z)
+{
+    if (ACT == ITO_ACT_RELU)
+        return make_float2(z.x > 0.0f ? 1.0f : z.x <= 0.0f ? 0.0f : z.x, z.y > 0.0f ? 1.0f : z.y <= 0.0f ? 0.0f : z.y);
+    if (ACT == ITO_ACT_GELU) {
+        float2 bell;
+        const float2 cdf = normal_cdf(z, bell);
+        return __ffma2_rn(__fmul2_rn(z, bell), splat(0.39894228040143268f), cdf);
+    }
+    if (ACT == ITO_ACT_GELU_TANH || ACT == ITO_ACT_SILU) {
+        // q + z u' q (1 - q) with q = logistic(u)
+        const float2 z2 = __fmul2_rn(z, z);
+        const bool silu = ACT == ITO_ACT_SILU;
+        const float2 q = logistic(silu ? z : __fmul2_rn(z, gelu_tanh_factor(z2)));
+        const float2 zu = silu ? z : __fmul2_rn(z, __ffma2_rn(z2, splat(0.21406444881780075f), splat(1.5957691216057308f)));
+        return __ffma2_rn(zu, __fmul2_rn(q, __ffma2_rn(q, splat(-1.0f), splat(1.0f))), q);
+    }
+    return splat(1.0f);
+}
+
+// an activation that is known at run time only
 __device__ __forceinline__ float act_value(int act, float z)
 {
     switch (act) {
-    case ITO_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case ITO_ACT_GELU: {
-        float bell;
-        return z * normal_cdf(z, bell);
-    }
-    case ITO_ACT_GELU_TANH: return z * logistic(gelu_tanh_argument(z));
-    case ITO_ACT_SILU: return z * logistic(z);
+    case ITO_ACT_RELU: return act_value<ITO_ACT_RELU>(splat(z)).x;
+    case ITO_ACT_GELU: return act_value<ITO_ACT_GELU>(splat(z)).x;
+    case ITO_ACT_GELU_TANH: return act_value<ITO_ACT_GELU_TANH>(splat(z)).x;
+    case ITO_ACT_SILU: return act_value<ITO_ACT_SILU>(splat(z)).x;
     default: return z;
-    }
-}
-
-__device__ __forceinline__ float act_slope(int act, float z)
-{
-    switch (act) {
-    case ITO_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-    case ITO_ACT_GELU: {
-        float bell;
-        const float cdf = normal_cdf(z, bell);
-        return fmaf(z * bell, 0.39894228040143268f, cdf);
-    }
-    case ITO_ACT_GELU_TANH: {
-        const float q = logistic(gelu_tanh_argument(z));
-        return fmaf(z * fmaf(0.21406444881780075f, z * z, 1.5957691216057308f), q * (1.0f - q), q);
-    }
-    case ITO_ACT_SILU: {
-        const float q = logistic(z);
-        return fmaf(z, q * (1.0f - q), q);
-    }
-    default: return 1.0f;
     }
 }
 

@@ -202,7 +202,11 @@ template <int ACT>
 __device__ __forceinline__ void activate(float (&v)[32])
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value(ACT, v[i]);
+    for (int i = 0; i < 32; i += 2) {
+        const float2 y = act_value<ACT>(make_float2(v[i], v[i + 1]));
+        v[i] = y.x;
+        v[i + 1] = y.y;
+    }
 }
 
 // this lane's row of a 16-bit residual, 32 columns (0 beyond the edges); asked for before the

@@ -176,23 +176,24 @@ __global__ void __launch_bounds__(256) k_fp_align(const __grid_constant__ FpCopy
 
 // dz = dy act'(z), rounded to the operands' type (dz may be null), and the columns' sums before
 // that rounding (dbias may be null). A block takes 64 columns, eight lanes of a warp to a row,
-// and a share of the batch; the shares of the same columns are a cluster, whose first block adds
-// their sums in order out of the others' shared memory. So the bias gradient takes no second
+// and a share of the batch; with dbias the shares of the same columns are a cluster, whose first
+// block adds their sums in order out of the others' shared memory. So the bias gradient takes no second
 // kernel, which at batch 2048 took 5 us before the products could start.
 constexpr int kDzColumns = 64;
+constexpr int kDzThreads = 256, kDzRows = kDzThreads / 8;    // rows at a time
 constexpr int kDzCluster = 8;
 
 template <int ACT>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(kDzThreads, 1024 / kDzThreads)
     k_fp_dz(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz, int type,
             int B, int OC, int shares, int vec, uint16_t* __restrict__ dz, int64_t lddz, float* __restrict__ dbias)
 {
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ float sums[32][kDzColumns];
+    __shared__ float sums[kDzRows][kDzColumns];
     __shared__ float total[kDzColumns];
     const int row = threadIdx.x >> 3, lane = threadIdx.x & 7;
-    const int share = shares > 1 ? (int)cluster_ctarank() : 0;
+    const int share = blockIdx.x % shares;     // (its place in the cluster, where there is one)
     const int rows_per = (B + shares - 1) / shares;
     const int c0 = (blockIdx.x / shares) * kDzColumns + lane * 8;
     const int r1 = min(B, (share + 1) * rows_per);
@@ -201,11 +202,11 @@ __global__ void __launch_bounds__(256, 4)
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
     if (c0 < OC) {
         constexpr int U = 4;             // rows whose loads are in flight together
-        for (int r0 = share * rows_per + row; r0 < r1; r0 += 32 * U) {
+        for (int r0 = share * rows_per + row; r0 < r1; r0 += kDzRows * U) {
             uint4 d[U], q[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t r = r0 + 32 * u;
+                const int64_t r = r0 + kDzRows * u;
                 d[u] = q[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (r < r1) {
                     d[u] = load_eight(dy + r * lddy, c0, OC, vec);
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(256, 4)
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t r = r0 + 32 * u;
+                const int64_t r = r0 + kDzRows * u;
                 if (r >= r1) break;
                 const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w}, qw[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
                 uint32_t o[4];
@@ -222,9 +223,7 @@ __global__ void __launch_bounds__(256, 4)
                 for (int i = 0; i < 4; ++i) {
                     float2 v = unpack16(type, dw[i]);
                     if (ACT != ITO_ACT_NONE) {
-                        const float2 zz = unpack16(type, qw[i]);
-                        v.x *= act_slope(ACT, zz.x);
-                        v.y *= act_slope(ACT, zz.y);
+                        v = __fmul2_rn(v, act_slope<ACT>(unpack16(type, qw[i])));
                     }
                     s[2 * i] += v.x;
                     s[2 * i + 1] += v.y;
@@ -242,8 +241,8 @@ __global__ void __launch_bounds__(256, 4)
     const int c = threadIdx.x;
     if (c < kDzColumns) {
         float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 32; ++w) v += sums[w][c];
+#pragma unroll 32
+        for (int w = 0; w < kDzRows; ++w) v += sums[w][c];
         total[c] = v;
     }
     if (shares > 1) cluster_sync();
@@ -274,10 +273,10 @@ template <int ACT>
 static int run_dz(const void* dy, int64_t lddy, const void* z, int64_t ldz, int type, int B, int OC, int vec,
                   uint16_t* dz, int64_t lddz, float* dbias, cudaStream_t s)
 {
-    const int shares = dz_shares(B);
+    const int shares = dbias ? dz_shares(B) : (B + 63) / 64;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((OC + kDzColumns - 1) / kDzColumns * shares);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)((OC + kDzColumns - 1) / kDzColumns) * shares);
+    cfg.blockDim = dim3(kDzThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -287,7 +286,7 @@ static int run_dz(const void* dy, int64_t lddy, const void* z, int64_t ldz, int 
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = shares > 1 ? 2 : 1;
+    cfg.numAttrs = dbias && shares > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp_dz<ACT>, static_cast<const uint16_t*>(dy), lddy,
                                              static_cast<const uint16_t*>(z), ldz, type, B, OC, shares, vec, dz, lddz,
                                              dbias);
