@@ -154,8 +154,10 @@ __device__ __noinline__ FarSums far_sums(const T* row, int classes)
 // ------------------------------------------------------------- a warp's alternatives
 //
 // Lane i holds the i-th best of what the warp has taken in. Elements that come before `low` go
-// to a buffer of 64 in shared memory; 32 of them at a time are sorted and merged with the list
-// by shuffles, and its k-th best becomes `low`. The first `low` is the k-th largest of the lanes'
+// to a buffer of 64 in shared memory; when 2 k + 2 of them (32 at most) are there, flush() brings
+// them to the list, and its k-th best becomes `low`. (For 4 of 32768 in random order that is 3
+// times a row, with 22 vectors looked at; waiting for 32 elements it was 32 vectors. 4096 x 32768
+// bf16: 73 us with 4 alternatives, 75 us with sorts only.) The first `low` is the k-th largest of the lanes'
 // largest elements of the first round, and of a block's warps the largest such: at least k
 // elements are no smaller, and in random order few more than k of that round and of each
 // following one come before it.
@@ -207,6 +209,10 @@ struct Alternatives {
         best = r > best ? r : best;
 #pragma unroll
         for (int j = 16; j > 0; j /= 2) best = exchange(best, j, (lane & j) == 0);
+        take_low(k);
+    }
+    __device__ __forceinline__ void take_low(int k)
+    {
         low = __shfl_sync(0xffffffffu, best, k - 1);
         low_value = low ? key_value(low) : -INFINITY;
         sorted = true;
@@ -220,9 +226,27 @@ struct Alternatives {
             for (int j = size / 2; j > 0; j /= 2) a = exchange(a, j, ((lane & j) == 0) == ((lane & size) == 0));
         merge(a, k);
     }
+    // The k best of lists and buffer. Where they fit a warp each lane counts the elements before its
+    // own: as many broadcast reads as elements, where a sort is 40 shuffles one after another.
     __device__ __forceinline__ void flush(int k)
     {
         const int lane = threadIdx.x & 31;
+        if (count + k <= 32) {
+            if (lane < k) buf[count + lane] = best;
+            __syncwarp();
+            const int n = count + k;
+            const Key a = lane < n ? buf[lane] : 0;
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += buf[j] > a;
+            if (a) buf[32 + rank] = a;
+            const int there = __popc(__ballot_sync(0xffffffffu, a != 0));
+            __syncwarp();
+            best = lane < min(k, there) ? buf[32 + lane] : 0;
+            __syncwarp();
+            count = 0;
+            take_low(k);
+            return;
+        }
         __syncwarp();
         const Key a = lane < count ? buf[lane] : 0, more = buf[32 + lane];
         __syncwarp();
@@ -238,7 +262,7 @@ struct Alternatives {
         if (!m) return;
         if (take) buf[count + __popc(m & ((1u << (threadIdx.x & 31)) - 1u))] = a;
         count += __popc(m);
-        if (count >= 32) flush(k);
+        if (count >= min(32, 2 * k + 2)) flush(k);
     }
     // `lists` sorted lists of `n` elements each, list p's at get(p, i): as many of them to a
     // sort as a warp has lanes for
@@ -260,41 +284,126 @@ struct Alternatives {
     }
 };
 
-// Elements [begin, end) of a row for thread `at` of `threads`: UNROLL vectors in flight. A
-// vector's elements are `skip` apart: neighbours (VEC; begin on 16 bytes) or a warp's width
-// apart, where rows start anywhere and a warp's single loads are still consecutive. lows: the
-// block's first thresholds, where its warps share the row (then every warp passes here).
-template <typename T, bool TOP, bool VEC>
-__device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, int end, int at, int threads, int k,
-                                          Alternatives& alt, float* lows)
+// Offers the elements of a warp's vectors that may be alternatives: v[u] of this lane starts at
+// element first + u pitch, its elements are `skip` apart. ALL: every vector, not only those whose
+// largest element is no smaller than `low` (a NaN is in no largest).
+template <bool ALL, typename T, int UNROLL>
+__device__ __forceinline__ void offer_vectors(const Vec<T> (&v)[UNROLL], int first, int pitch, int skip, int end, int k,
+                                              Alternatives& alt)
 {
-    constexpr int PER = Vec<T>::kPer, UNROLL = 4;
-    constexpr int skip = VEC ? 1 : 32;
+    constexpr int PER = Vec<T>::kPer;
+    const int lane = threadIdx.x & 31;
+    unsigned pending = 0;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+        if (ALL || v[u].largest() >= alt.low_value) pending |= 1u << u;
+    unsigned turns = __reduce_or_sync(0xffffffffu, pending);
+    // one copy of this in the code: unrolled, its sorts would not fit the instruction cache
+    while (turns) {
+        const int u = __ffs(turns) - 1;
+        turns &= turns - 1;
+        Vec<T> w = v[0];
+#pragma unroll
+        for (int q = 1; q < UNROLL; ++q)
+            if (u == q) w = v[q];
+        // one such vector at a time, its elements to the first lanes; beyond the end are none
+        unsigned from = __ballot_sync(0xffffffffu, pending >> u & 1u);
+        while (from) {
+            const int src = __ffs(from) - 1;
+            from &= from - 1;
+            Vec<T> b;
+            b.raw = make_uint4(__shfl_sync(0xffffffffu, w.raw.x, src), __shfl_sync(0xffffffffu, w.raw.y, src),
+                               __shfl_sync(0xffffffffu, w.raw.z, src), __shfl_sync(0xffffffffu, w.raw.w, src));
+            const int i = __shfl_sync(0xffffffffu, first, src) + u * pitch + (lane & (PER - 1)) * skip;
+            alt.offer(make_key(b.element(lane & (PER - 1)), i), lane < PER && i < end, k);
+        }
+    }
+}
+
+constexpr int kLpUnroll = 4;         // vectors of a lane in a round
+
+template <typename T>
+__device__ __forceinline__ float largest_of(const Vec<T> (&v)[kLpUnroll])
+{
+    return fmaxf(fmaxf(v[0].largest(), v[1].largest()), fmaxf(v[2].largest(), v[3].largest()));
+}
+
+template <typename T>
+__device__ __forceinline__ void add_vectors(PairSums& sums, const Vec<T> (&v)[kLpUnroll])
+{
+    constexpr int PER = Vec<T>::kPer;
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+        float f[PER];
+        v[u].get(f);
+#pragma unroll
+        for (int j = 0; j < PER; j += 2) sums.add(make_float2(f[j], f[j + 1]));
+    }
+}
+
+// A round of elements [base, end) of a row for thread `at` of `threads`. A vector's elements are
+// neighbours (VEC; base on 16 bytes), or a warp's width apart where rows start anywhere: a warp's
+// single loads are still consecutive.
+template <bool VEC, typename T>
+__device__ __forceinline__ int load_round(Vec<T> (&v)[kLpUnroll], const T* __restrict__ row, int base, int end, int at,
+                                          int threads)
+{
+    constexpr int PER = Vec<T>::kPer, skip = VEC ? 1 : 32;
+    const int lane = threadIdx.x & 31, first = base + (at - lane) * PER + (VEC ? lane * PER : lane);
+#pragma unroll
+    for (int u = 0; u < kLpUnroll; ++u) {
+        const int c = first + u * threads * PER;
+        if (VEC && c + PER <= end) {
+            v[u].raw = __ldcs(reinterpret_cast<const uint4*>(row + c));
+        } else {
+            float f[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) f[j] = c + j * skip < end ? to_f32(row[c + j * skip]) : -INFINITY;
+            v[u].set(f);                 // exact: the values came from T
+        }
+    }
+    return first;
+}
+
+// The alternatives of a warp's part of a row that holds a NaN (or an infinity that made one).
+template <typename T, bool VEC>
+__device__ __noinline__ void scan_every(const T* row, int begin, int end, int at, int threads, int k, Alternatives* alt)
+{
+    constexpr int PER = Vec<T>::kPer;
+    Alternatives a;
+    a.clear(alt->buf);
+    __syncwarp();
+    for (int base = begin; base < end; base += threads * PER * kLpUnroll) {
+        Vec<T> v[kLpUnroll];
+        const int first = load_round<VEC>(v, row, base, end, at, threads);
+        offer_vectors<true>(v, first, threads * PER, VEC ? 1 : 32, end, k, a);
+    }
+    *alt = a;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void scan_again(const T* row, int begin, int end, int at, int threads, int k, Alternatives& alt)
+{
+    Alternatives a;
+    a.buf = alt.buf;
+    scan_every<T, VEC>(row, begin, end, at, threads, k, &a);
+    alt = a;
+}
+
+// Elements [begin, end) of a row for thread `at` of `threads`. lows: the block's first
+// thresholds, where its warps share the row (then every warp passes here).
+template <typename T, bool TOP, bool VEC>
+__device__ __forceinline__ Sums scan(const T* __restrict__ row, int begin, int end, int at, int threads, int k,
+                                     Alternatives& alt, float* lows)
+{
+    constexpr int PER = Vec<T>::kPer;
     const int lane = threadIdx.x & 31;
     PairSums sums;
     sums.clear();
     // (classes are at most 2^30: no index overflows)
-    for (int base = begin; base < end; base += threads * PER * UNROLL) {
-        Vec<T> v[UNROLL];
-        int first[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int block = base + (u * threads + (at - lane)) * PER;     // the warp's elements
-            const int c = block + (VEC ? lane * PER : lane);
-            first[u] = min(c, end);
-            if (VEC && c + PER <= end) {
-                v[u].raw = __ldcs(reinterpret_cast<const uint4*>(row + c));
-            } else {
-                float f[PER];
-#pragma unroll
-                for (int j = 0; j < PER; ++j) f[j] = c + j * skip < end ? to_f32(row[c + j * skip]) : -INFINITY;
-                v[u].set(f);             // exact: the values came from T
-            }
-        }
-        float most[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) most[u] = v[u].largest();
-        const float m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    for (int base = begin; base < end; base += threads * PER * kLpUnroll) {
+        Vec<T> v[kLpUnroll];
+        const int first = load_round<VEC>(v, row, base, end, at, threads);
+        const float m = largest_of(v);
         sums.rise(m);
         if (TOP && base == begin) {
             alt.first_low(m, k);
@@ -307,45 +416,13 @@ __device__ __forceinline__ Sums scan_part(const T* __restrict__ row, int begin, 
                 alt.from_value(low);
             }
         }
-        unsigned pending = 0;            // this lane's vectors with an element to look at closer
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            float f[PER];
-            v[u].get(f);
-#pragma unroll
-            for (int j = 0; j < PER; j += 2) sums.add(make_float2(f[j], f[j + 1]));
-            // a NaN is not in `most`, but it is in the sum
-            if (TOP && (most[u] >= alt.low_value || sums.s.x != sums.s.x || sums.s.y != sums.s.y) && first[u] < end)
-                pending |= 1u << u;
-        }
-        if (!TOP) continue;
-        unsigned turns = __reduce_or_sync(0xffffffffu, pending);
-        // one copy of this in the code: unrolled, its sorts would not fit the instruction cache
-        while (turns) {
-            const int u = __ffs(turns) - 1;
-            turns &= turns - 1;
-            Vec<T> w = v[0];
-            int c = first[0];
-#pragma unroll
-            for (int q = 1; q < UNROLL; ++q)
-                if (u == q) {
-                    w = v[q];
-                    c = first[q];
-                }
-            // one such vector at a time, its elements to the first lanes
-            unsigned from = __ballot_sync(0xffffffffu, pending >> u & 1u);
-            while (from) {
-                const int src = __ffs(from) - 1;
-                from &= from - 1;
-                Vec<T> b;
-                b.raw = make_uint4(__shfl_sync(0xffffffffu, w.raw.x, src), __shfl_sync(0xffffffffu, w.raw.y, src),
-                                   __shfl_sync(0xffffffffu, w.raw.z, src), __shfl_sync(0xffffffffu, w.raw.w, src));
-                const int i = __shfl_sync(0xffffffffu, c, src) + (lane & (PER - 1)) * skip;
-                alt.offer(make_key(b.element(lane & (PER - 1)), i), lane < PER && i < end, k);
-            }
-        }
+        add_vectors(sums, v);
+        if (TOP && __any_sync(0xffffffffu, m >= alt.low_value))
+            offer_vectors<false>(v, first, threads * PER, VEC ? 1 : 32, end, k, alt);
     }
-    return sums.total();
+    const Sums s = sums.total();
+    if (TOP && __any_sync(0xffffffffu, s.s != s.s)) scan_again<T, VEC>(row, begin, end, at, threads, k, alt);
+    return s;
 }
 
 struct LpOut {
@@ -398,8 +475,8 @@ __device__ __forceinline__ void write_row(const T* row, const int32_t* targets, 
     }
 }
 
-// Short rows: a warp to a row.
-template <typename T, bool TOP, bool VEC>
+// Short rows and rows enough: a warp to a row, the warps of all blocks with nearly as many rows.
+template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpWarps * 32, 4)
     k_logprobs_short(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
                      int classes, int k, const LpOut o, int* __restrict__ err)
@@ -407,13 +484,128 @@ __global__ void __launch_bounds__(kLpWarps * 32, 4)
     __shared__ Key buf[kLpWarps][TOP ? 64 : 1];
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t step = (int64_t)gridDim.x * kLpWarps;
-    for (int64_t r = (int64_t)blockIdx.x * kLpWarps + (threadIdx.x >> 5); r < rows; r += step) {
+    const int warp = threadIdx.x >> 5;
+    for (int64_t r = (int64_t)warp * gridDim.x + blockIdx.x; r < rows; r += (int64_t)gridDim.x * kLpWarps) {
         Alternatives alt;
-        alt.clear(buf[threadIdx.x >> 5]);
-        const Sums a = scan_part<T, TOP, VEC>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt, nullptr);
+        alt.clear(buf[warp]);
+        const Sums a = scan<T, TOP, false>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt, nullptr);
         if (TOP && alt.count) alt.flush(k);
         write_row<T, TOP>(x + r * ld, targets, r, classes, k, warp_join(a), alt, o, err);
+    }
+}
+
+// The same for rows on 16 bytes, their loads ahead of the work: each warp keeps a ring of
+// kLpSlots rounds in shared memory, filled by bulk copies, and the vectors that may hold
+// alternatives are read again there, four at a time. 4096 x 32768 bf16 with 4 alternatives: 59 us
+// (without any 44, the row's bytes at the device's copy rate 40), 80 with loads to registers and
+// shuffles. What bounds it: 11500 instructions a warp and row, 8500 of them for the sums.
+// A block is of few warps with alternatives, so that an SM holds 28 at 72 registers (32 at 64
+// spill: 73 us), else of 8 with 32 to an SM. Either way shared memory or registers let no SM take
+// more blocks than its share of the grid, while the previous launch's end: 75 us where they did.
+// A wait that runs out (mbar_wait) leaves a wrong result and ITO_ERR_TIMEOUT.
+constexpr int ring_warps(bool top) { return top ? 4 : 8; }         // of a block
+constexpr int ring_blocks(bool top) { return top ? 7 : 4; }        // of an SM
+constexpr int kLpSlots = 3, kLpRound = 32 * kLpUnroll * 16;      // bytes of a round
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
+    k_logprobs_ring(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
+                    int classes, int k, const LpOut o, int* __restrict__ err)
+{
+    constexpr int WARPS = ring_warps(TOP), PER = Vec<T>::kPer, EACH = kLpRound / (int)sizeof(T);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Key buf[WARPS][TOP ? 64 : 1];
+    __shared__ uint64_t full[WARPS][kLpSlots];
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* const ring = smem + warp * (kLpSlots * kLpRound);
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0) {
+        for (int s = 0; s < kLpSlots; ++s) mbar_init(&full[warp][s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = (int64_t)gridDim.x * WARPS;
+    int64_t r = (int64_t)warp * gridDim.x + blockIdx.x, ahead = r;
+    int ahead_base = 0;
+    auto fetch = [&](int s) {            // the next round of this warp's rows
+        if (ahead >= rows) return;
+        const uint32_t bytes = (uint32_t)(min(EACH, classes - ahead_base) * (int)sizeof(T)) & ~15u;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&full[warp][s], bytes);
+            if (bytes) bulk_load(ring + s * kLpRound, x + ahead * ld + ahead_base, bytes, &full[warp][s]);
+        }
+        ahead_base += EACH;
+        if (ahead_base >= classes) ahead_base = 0, ahead += step;
+    };
+    for (int s = 0; s < kLpSlots; ++s) fetch(s);
+    int slot = 0;
+    uint32_t phase = 0;
+    for (; r < rows; r += step) {
+        const T* const row = x + r * ld;
+        Alternatives alt;
+        alt.clear(buf[warp]);
+        PairSums sums;
+        sums.clear();
+        for (int base = 0; base < classes; base += EACH) {
+            mbar_wait(&full[warp][slot], phase, &abort_flag, err);
+            uint8_t* const at = ring + slot * kLpRound;
+            Vec<T> v[kLpUnroll];
+            float m[kLpUnroll];
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) v[u].raw = *reinterpret_cast<const uint4*>(at + (u * 32 + lane) * 16);
+            if (base + EACH > classes) {
+                // the row's end: what is no whole vector, and nothing beyond it
+#pragma unroll
+                for (int u = 0; u < kLpUnroll; ++u) {
+                    const int c = base + (u * 32 + lane) * PER;
+                    float f[PER];
+                    if (c + PER <= classes) continue;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) f[j] = c + j < classes ? to_f32(row[c + j]) : -INFINITY;
+                    v[u].set(f);
+                    if (TOP) *reinterpret_cast<uint4*>(at + (u * 32 + lane) * 16) = v[u].raw;
+                }
+                if (TOP) fence_proxy_async_smem();
+            }
+#pragma unroll
+            for (int u = 0; u < kLpUnroll; ++u) m[u] = v[u].largest();
+            const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            sums.rise(most);
+            if (TOP && base == 0) alt.first_low(most, k);
+            add_vectors(sums, v);
+            __syncwarp();
+            if (TOP && __any_sync(0xffffffffu, most >= alt.low_value)) {
+                unsigned pending = 0;    // this lane's vectors to look at closer
+#pragma unroll
+                for (int u = 0; u < kLpUnroll; ++u) pending |= m[u] >= alt.low_value ? 1u << u : 0u;
+                // four lanes' vectors at a time, their elements from shared memory
+                for (unsigned from; (from = __ballot_sync(0xffffffffu, pending != 0)) != 0;) {
+                    unsigned mine = from, rest = from;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (lane / PER > q) mine &= mine - 1;
+                        rest &= rest - 1;
+                    }
+                    const int src = (__ffs(mine) - 1) & 31, u = __shfl_sync(0xffffffffu, __ffs(pending) - 1, src);
+                    if ((from ^ rest) >> lane & 1u) pending &= pending - 1;
+                    const bool there = mine != 0 && lane < 4 * PER;
+                    const int e = (u * 32 + src) * PER + (lane & (PER - 1));
+                    float f = 0.0f;
+                    if (there) f = to_f32(reinterpret_cast<const T*>(at)[e]);
+                    alt.offer(make_key(f, base + e), there && base + e < classes, k);
+                }
+                __syncwarp();
+            }
+            fetch(slot);
+            if (++slot == kLpSlots) slot = 0, phase ^= 1;
+        }
+        const Sums a = sums.total();
+        if (TOP && __any_sync(0xffffffffu, a.s != a.s)) scan_again<T, true>(row, 0, classes, lane, 32, k, alt);
+        if (TOP && alt.count) alt.flush(k);
+        write_row<T, TOP>(row, targets, r, classes, k, warp_join(a), alt, o, err);
     }
 }
 
@@ -437,7 +629,7 @@ __global__ void __launch_bounds__(kLpWarps * 32, 4)
     for (int64_t r = blockIdx.x / parts; r < rows; r += gridDim.x / parts) {
         Alternatives alt;
         alt.clear(buf[warp]);
-        Sums a = warp_join(scan_part<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt, lows));
+        Sums a = warp_join(scan<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt, lows));
         if (lane == 0) {
             sums[warp] = a;
             counts[warp] = alt.sorted ? 64 : alt.count;
@@ -624,13 +816,27 @@ static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t r
 {
     const T* x = static_cast<const T*>(xp);
     const int sms = num_sms();
-    // a warp to a row up to four rounds of its loads, or where warps of whole rows fill the device
-    // (4096 x 32768 bf16: 46 us, 56 with a block to a row; 2500 x 32768: 41 us, 36)
+    // A warp to a row up to four vectors a lane, or where rows are enough to fill the device with
+    // warps: the alternatives' sorts are then one row's, and wait for no other warp. Without them
+    // the loads alone decide. 4096 x 32768 bf16 without: 44 us, 56 with a block to a row; 2500 rows
+    // without 39 and 36, with 1 alternative 50 and 44, with 4 55 and 59, with 8 60 and 78; 1200
+    // rows with 4 33 and 28.
     const int round = 32 * Vec<T>::kPer * 4;
-    if (classes <= round || rows >= 24 * sms) {
-        const int64_t want = (rows + kLpWarps - 1) / kLpWarps, most = (int64_t)sms * 8;
-        launch_pdl(k_logprobs_short<T, TOP, VEC>, (unsigned)std::min(want, most), kLpWarps * 32, 0, s, x, ld, targets,
-                   rows, classes, k, o, err);
+    if (classes <= round || rows >= (k < 4 ? 24 : 16) * sms) {
+        // (a block's warps take rows a grid apart, so SMs differ by a row at most)
+        // (a block's warps take rows a grid apart, so SMs differ by a row at most)
+        const int warps = VEC ? ring_warps(TOP) : kLpWarps, blocks = VEC ? ring_blocks(TOP) : 4;
+        const int64_t want = (rows + warps - 1) / warps;
+        const unsigned grid = (unsigned)(want < sms ? want : std::min((want + sms - 1) / sms, (int64_t)blocks) * sms);
+        if constexpr (VEC) {
+            const auto kernel = k_logprobs_ring<T, TOP>;
+            constexpr int smem = ring_warps(TOP) * kLpSlots * kLpRound;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
+            launch_pdl(kernel, grid, warps * 32, smem, s, x, ld, targets, rows, classes, k, o, err);
+        } else {
+            launch_pdl(k_logprobs_short<T, TOP>, grid, warps * 32, 0, s, x, ld, targets, rows, classes, k, o, err);
+        }
         return launch_status("log probabilities");
     }
     // blocks of a row: enough that all rows' blocks occupy the SMs, each with a round of loads at least

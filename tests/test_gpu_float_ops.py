@@ -570,6 +570,33 @@ def test_logprobs_of_nan_and_infinity(torch, ito, n):
         assert all(torch.equal(a[r], b[r]) for a, b in zip((logp, ent, lse, ids, top), clean))
 
 
+@pytest.mark.parametrize("dtype,n,pad,k", [("float32", 1537, 3, 3), ("bfloat16", 2500, 4, 9), ("float16", 1031, 1, 32),
+                                           ("bfloat16", 2049, 0, 4), ("bfloat16", 3000, 0, 0)])
+def test_logprobs_of_many_rows(torch, ito, dtype, n, pad, k):
+    """Rows enough for several to a warp, on 16 bytes or not, with rows in order, masked ends and whole masks."""
+    rows = 30 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    x = normal(torch, (rows, n + pad), 3, 2.0, dtype)[:, :n]
+    x[0::7] = x[0::7].sort(dim=1)[0]
+    x[1::7] = x[1::7].sort(dim=1, descending=True)[0]
+    x[2::7, n // 3:] = -math.inf
+    x[3::70] = -math.inf
+    x[4::70] = torch.finfo(x.dtype).min
+    check_logprobs(torch, ito, x, torch.arange(rows, device="cuda", dtype=torch.int32) % n, k, dtype)
+
+
+def test_logprobs_of_nan_among_many_rows(torch, ito):
+    rows, n = 30 * torch.cuda.get_device_properties(0).multi_processor_count, 1500
+    x = normal(torch, (rows, n), 1, 1.0, "bfloat16")
+    clean = ito.ito_token_logprobs_fwd(x, None, k=4)[3:]
+    x[1::2, 1234] = math.nan
+    x[rows - 1] = math.nan
+    ids, top = ito.ito_token_logprobs_fwd(x, None, k=4)[3:]
+    assert all(torch.equal(a[0::2], b[0::2]) for a, b in zip((ids, top), clean))
+    assert bool(torch.isnan(top[1::2]).all()) and bool((ids[1:-1:2, 0] == 1234).all())
+    assert torch.equal(ids[1:-2:2, 1:], x[1:-2:2].nan_to_num(nan=-math.inf).float().sort(dim=1, descending=True, stable=True)[1][:, :3].int())
+    assert ids[rows - 1].cpu().tolist() == [0, 1, 2, 3]
+
+
 def test_logprobs_negative_zero_ties_with_zero(torch, ito):
     x = torch.full((1, 64), -1.0, device="cuda")
     x[0, 9], x[0, 4], x[0, 30] = 0.0, -0.0, 0.0
