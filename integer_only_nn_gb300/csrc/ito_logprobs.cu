@@ -157,10 +157,16 @@ __device__ __noinline__ FarSums far_sums(const T* row, int classes)
 // to a buffer of 64 in shared memory; when 2 k + 2 of them (32 at most) are there, flush() brings
 // them to the list, and its k-th best becomes `low`. (For 4 of 32768 in random order that is 3
 // times a row, with 22 vectors looked at; waiting for 32 elements it was 32 vectors. 4096 x 32768
-// bf16: 73 us with 4 alternatives, 75 us with sorts only.) The first `low` is the k-th largest of the lanes'
-// largest elements of the first round, and of a block's warps the largest such: at least k
+// bf16: 73 us with 4 alternatives, 75 us with sorts only.) The first `low` is the k-th largest of the
+// lanes' largest elements of the first round, of all warps that share the row's part: at least k
 // elements are no smaller, and in random order few more than k of that round and of each
-// following one come before it.
+// following one come before it. (With each warp's own, and the largest of them, 1200 x 32768 bf16
+// with 8 and 32 alternatives took 34 and 83 us instead of 30 and 51.)
+struct FirstLows {
+    alignas(16) float v[kLpWarps * kLpMaxTop];
+    float low;
+};
+
 struct Alternatives {
     Key best, low;
     float low_value;
@@ -176,8 +182,33 @@ struct Alternatives {
         sorted = false;
         buf = b;
     }
-    // the k-th largest of the lanes' m (a NaN counts as lowest here)
+    // the first `low` of a warp that has a row for itself, from its lanes' largest elements in order
     __device__ __forceinline__ void first_low(float m, int k)
+    {
+        from_value(__shfl_sync(0xffffffffu, in_order(m), k - 1));
+    }
+    // of a block that shares a row: the k-th of its lanes'. All threads.
+    __device__ __forceinline__ void first_low_of_block(float m, int k, int warp, FirstLows* f)
+    {
+        const int lane = threadIdx.x & 31;
+        m = in_order(m);
+        if (lane < k) f->v[warp * k + lane] = m;
+        __syncthreads();
+        if (lane < k) {
+            const int me = warp * k + lane;
+            int before = 0;
+            for (int j = 0; j < kLpWarps * k; j += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(f->v + j);
+                before += (o.x > m || (o.x == m && j < me)) + (o.y > m || (o.y == m && j + 1 < me)) +
+                          (o.z > m || (o.z == m && j + 2 < me)) + (o.w > m || (o.w == m && j + 3 < me));
+            }
+            if (before == k - 1) f->low = m;
+        }
+        __syncthreads();
+        from_value(f->low);
+    }
+    // the i-th largest of the lanes' m, in lane i (a NaN counts as lowest here)
+    static __device__ __forceinline__ float in_order(float m)
     {
         const int lane = threadIdx.x & 31;
         if (m != m) m = -INFINITY;
@@ -188,7 +219,7 @@ struct Alternatives {
                 const float o = __shfl_xor_sync(0xffffffffu, m, j);
                 m = ((lane & j) == 0) == ((lane & size) == 0) ? fmaxf(m, o) : fminf(m, o);
             }
-        from_value(__shfl_sync(0xffffffffu, m, k - 1));
+        return m;
     }
     __device__ __forceinline__ void from_value(float v)
     {
@@ -264,25 +295,46 @@ struct Alternatives {
         count += __popc(m);
         if (count >= min(32, 2 * k + 2)) flush(k);
     }
-    // `lists` sorted lists of `n` elements each, list p's at get(p, i): as many of them to a
-    // sort as a warp has lanes for
-    template <typename Get>
-    __device__ __forceinline__ void merge_lists(int lists, int n, int k, Get get)
+    // leaves everything in the buffer, -> how many (32 at most)
+    __device__ __forceinline__ int gather(int k)
     {
         const int lane = threadIdx.x & 31;
-        if (n > 16) {
-#pragma unroll 1
-            for (int p = 0; p < lists; ++p) merge(lane < n ? get(p, lane) : 0, k);
-            return;
-        }
-        const int each = 32 / n;
-#pragma unroll 1
-        for (int p = 0; p < lists; p += each) {
-            const int q = p + lane / n;
-            merge_unsorted(lane < each * n && q < lists ? get(q, lane % n) : 0, k);
-        }
+        if (!sorted) return count;
+        if (count + k > 32) flush(k);
+        if (lane < k) buf[count + lane] = best;
+        return count + k;
     }
 };
+
+// The k best of several buffers' elements, counts[i] (or each) of them in buffer i, into `out` (of
+// 32 zeros): warp i takes buffer i, each thread counts the elements before its own.
+__device__ __forceinline__ void rank_all(const Key (*buf)[64], int buffers, const int* counts, int each, int k, Key* out)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= buffers) return;
+    const int n = counts ? counts[warp] : each;
+    const Key mine = lane < n ? buf[warp][lane] : 0;
+    if (!__any_sync(0xffffffffu, mine != 0)) return;
+    int rank = 0;
+    for (int w = 0; w < buffers; ++w) {
+        const int m = counts ? counts[w] : each;
+        for (int j = 0; j < m; ++j) rank += buf[w][j] > mine;
+    }
+    if (mine && rank < k) out[rank] = mine;
+}
+
+// The q-th lane of a set (-1: none), and in `from` its first four.
+__device__ __forceinline__ int four_lanes(unsigned& from, int q)
+{
+    unsigned mine = from, rest = from;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (q > i) mine &= mine - 1;
+        rest &= rest - 1;
+    }
+    from ^= rest;
+    return __ffs(mine) - 1;
+}
 
 // Offers the elements of a warp's vectors that may be alternatives: v[u] of this lane starts at
 // element first + u pitch, its elements are `skip` apart. ALL: every vector, not only those whose
@@ -297,26 +349,19 @@ __device__ __forceinline__ void offer_vectors(const Vec<T> (&v)[UNROLL], int fir
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
         if (ALL || v[u].largest() >= alt.low_value) pending |= 1u << u;
-    unsigned turns = __reduce_or_sync(0xffffffffu, pending);
-    // one copy of this in the code: unrolled, its sorts would not fit the instruction cache
-    while (turns) {
-        const int u = __ffs(turns) - 1;
-        turns &= turns - 1;
-        Vec<T> w = v[0];
+    // four lanes' first such vectors at a time, their elements side by side; beyond the end are none
+    for (unsigned from; (from = __ballot_sync(0xffffffffu, pending != 0)) != 0;) {
+        const int src = four_lanes(from, lane / PER), u = __ffs(pending) - 1;
+        Vec<T> w = v[0], b;
 #pragma unroll
         for (int q = 1; q < UNROLL; ++q)
             if (u == q) w = v[q];
-        // one such vector at a time, its elements to the first lanes; beyond the end are none
-        unsigned from = __ballot_sync(0xffffffffu, pending >> u & 1u);
-        while (from) {
-            const int src = __ffs(from) - 1;
-            from &= from - 1;
-            Vec<T> b;
-            b.raw = make_uint4(__shfl_sync(0xffffffffu, w.raw.x, src), __shfl_sync(0xffffffffu, w.raw.y, src),
-                               __shfl_sync(0xffffffffu, w.raw.z, src), __shfl_sync(0xffffffffu, w.raw.w, src));
-            const int i = __shfl_sync(0xffffffffu, first, src) + u * pitch + (lane & (PER - 1)) * skip;
-            alt.offer(make_key(b.element(lane & (PER - 1)), i), lane < PER && i < end, k);
-        }
+        const int at = src & 31;
+        b.raw = make_uint4(__shfl_sync(0xffffffffu, w.raw.x, at), __shfl_sync(0xffffffffu, w.raw.y, at),
+                           __shfl_sync(0xffffffffu, w.raw.z, at), __shfl_sync(0xffffffffu, w.raw.w, at));
+        const int i = __shfl_sync(0xffffffffu, first + u * pitch, at) + (lane & (PER - 1)) * skip;
+        if (from >> lane & 1u) pending &= pending - 1;
+        alt.offer(make_key(b.element(lane & (PER - 1)), i), src >= 0 && lane < 4 * PER && i < end, k);
     }
 }
 
@@ -393,10 +438,9 @@ __device__ __forceinline__ void scan_again(const T* row, int begin, int end, int
 // thresholds, where its warps share the row (then every warp passes here).
 template <typename T, bool TOP, bool VEC>
 __device__ __forceinline__ Sums scan(const T* __restrict__ row, int begin, int end, int at, int threads, int k,
-                                     Alternatives& alt, float* lows)
+                                     Alternatives& alt, FirstLows* lows)
 {
     constexpr int PER = Vec<T>::kPer;
-    const int lane = threadIdx.x & 31;
     PairSums sums;
     sums.clear();
     // (classes are at most 2^30: no index overflows)
@@ -406,15 +450,8 @@ __device__ __forceinline__ Sums scan(const T* __restrict__ row, int begin, int e
         const float m = largest_of(v);
         sums.rise(m);
         if (TOP && base == begin) {
-            alt.first_low(m, k);
-            if (lows) {
-                if (lane == 0) lows[at >> 5] = alt.low_value;
-                __syncthreads();
-                float low = lows[0];
-#pragma unroll
-                for (int w = 1; w < kLpWarps; ++w) low = fmaxf(low, lows[w]);
-                alt.from_value(low);
-            }
+            if (lows) alt.first_low_of_block(m, k, at >> 5, lows);
+            else alt.first_low(m, k);
         }
         add_vectors(sums, v);
         if (TOP && __any_sync(0xffffffffu, m >= alt.low_value))
@@ -476,29 +513,13 @@ __device__ __forceinline__ void write_row(const T* row, const int32_t* targets, 
 }
 
 // Short rows and rows enough: a warp to a row, the warps of all blocks with nearly as many rows.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpWarps * 32, 4)
-    k_logprobs_short(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
-                     int classes, int k, const LpOut o, int* __restrict__ err)
-{
-    __shared__ Key buf[kLpWarps][TOP ? 64 : 1];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int warp = threadIdx.x >> 5;
-    for (int64_t r = (int64_t)warp * gridDim.x + blockIdx.x; r < rows; r += (int64_t)gridDim.x * kLpWarps) {
-        Alternatives alt;
-        alt.clear(buf[warp]);
-        const Sums a = scan<T, TOP, false>(x + r * ld, 0, classes, threadIdx.x & 31, 32, k, alt, nullptr);
-        if (TOP && alt.count) alt.flush(k);
-        write_row<T, TOP>(x + r * ld, targets, r, classes, k, warp_join(a), alt, o, err);
-    }
-}
-
-// The same for rows on 16 bytes, their loads ahead of the work: each warp keeps a ring of
-// kLpSlots rounds in shared memory, filled by bulk copies, and the vectors that may hold
-// alternatives are read again there, four at a time. 4096 x 32768 bf16 with 4 alternatives: 59 us
-// (without any 44, the row's bytes at the device's copy rate 40), 80 with loads to registers and
-// shuffles. What bounds it: 11500 instructions a warp and row, 8500 of them for the sums.
+// The loads are ahead of the work: each warp keeps a ring of kLpSlots rounds in shared memory,
+// filled by bulk copies, and the vectors that may hold alternatives are read again there, four at
+// a time. A row is taken from the 16-byte boundary before it, `lead` elements early; its first and
+// last elements that fill no vector are loaded singly. 4096 x 32768 bf16 with 4
+// alternatives: 60 us (without any 45, the rows' bytes at the device's copy rate 40), 80 with loads
+// to registers and shuffles; rows of 32001 63 us, 104 with single loads. What bounds it: 11500
+// instructions a warp and row, 8500 of them for the sums.
 // A block is of few warps with alternatives, so that an SM holds 28 at 72 registers (32 at 64
 // spill: 73 us), else of 8 with 32 to an SM. Either way shared memory or registers let no SM take
 // more blocks than its share of the grid, while the previous launch's end: 75 us where they did.
@@ -506,6 +527,12 @@ __global__ void __launch_bounds__(kLpWarps * 32, 4)
 constexpr int ring_warps(bool top) { return top ? 4 : 8; }         // of a block
 constexpr int ring_blocks(bool top) { return top ? 7 : 4; }        // of an SM
 constexpr int kLpSlots = 3, kLpRound = 32 * kLpUnroll * 16;      // bytes of a round
+
+template <typename T>
+__device__ __forceinline__ int elements_before(const T* p)
+{
+    return (int)(reinterpret_cast<uintptr_t>(p) & 15u) / (int)sizeof(T);
+}
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
@@ -532,13 +559,16 @@ __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
     int ahead_base = 0;
     auto fetch = [&](int s) {            // the next round of this warp's rows
         if (ahead >= rows) return;
-        const uint32_t bytes = (uint32_t)(min(EACH, classes - ahead_base) * (int)sizeof(T)) & ~15u;
+        const T* const row = x + ahead * ld;
+        const int lead = elements_before<T>(row), end = min(ahead_base + EACH, classes + lead) / PER * PER;
+        const int from = ahead_base || !lead ? ahead_base : PER;
+        const uint32_t bytes = (uint32_t)(max(end - from, 0) * (int)sizeof(T));
         if (lane == 0) {
             mbar_arrive_expect_tx(&full[warp][s], bytes);
-            if (bytes) bulk_load(ring + s * kLpRound, x + ahead * ld + ahead_base, bytes, &full[warp][s]);
+            if (bytes) bulk_load(ring + s * kLpRound + (from - ahead_base) * (int)sizeof(T), row - lead + from, bytes, &full[warp][s]);
         }
         ahead_base += EACH;
-        if (ahead_base >= classes) ahead_base = 0, ahead += step;
+        if (ahead_base >= classes + lead) ahead_base = 0, ahead += step;
     };
     for (int s = 0; s < kLpSlots; ++s) fetch(s);
     int slot = 0;
@@ -549,22 +579,23 @@ __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
         alt.clear(buf[warp]);
         PairSums sums;
         sums.clear();
-        for (int base = 0; base < classes; base += EACH) {
+        const int lead = elements_before<T>(row), end = classes + lead;
+        for (int base = 0; base < end; base += EACH) {
             mbar_wait(&full[warp][slot], phase, &abort_flag, err);
             uint8_t* const at = ring + slot * kLpRound;
             Vec<T> v[kLpUnroll];
             float m[kLpUnroll];
 #pragma unroll
             for (int u = 0; u < kLpUnroll; ++u) v[u].raw = *reinterpret_cast<const uint4*>(at + (u * 32 + lane) * 16);
-            if (base + EACH > classes) {
-                // the row's end: what is no whole vector, and nothing beyond it
+            if (base + EACH > end || (base == 0 && lead)) {
+                // what is no whole vector, and nothing before the row or beyond it
 #pragma unroll
                 for (int u = 0; u < kLpUnroll; ++u) {
                     const int c = base + (u * 32 + lane) * PER;
                     float f[PER];
-                    if (c + PER <= classes) continue;
+                    if (c >= lead && c + PER <= end) continue;
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) f[j] = c + j < classes ? to_f32(row[c + j]) : -INFINITY;
+                    for (int j = 0; j < PER; ++j) f[j] = c + j >= lead && c + j < end ? to_f32(row[c + j - lead]) : -INFINITY;
                     v[u].set(f);
                     if (TOP) *reinterpret_cast<uint4*>(at + (u * 32 + lane) * 16) = v[u].raw;
                 }
@@ -583,19 +614,15 @@ __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
                 for (int u = 0; u < kLpUnroll; ++u) pending |= m[u] >= alt.low_value ? 1u << u : 0u;
                 // four lanes' vectors at a time, their elements from shared memory
                 for (unsigned from; (from = __ballot_sync(0xffffffffu, pending != 0)) != 0;) {
-                    unsigned mine = from, rest = from;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (lane / PER > q) mine &= mine - 1;
-                        rest &= rest - 1;
-                    }
-                    const int src = (__ffs(mine) - 1) & 31, u = __shfl_sync(0xffffffffu, __ffs(pending) - 1, src);
-                    if ((from ^ rest) >> lane & 1u) pending &= pending - 1;
-                    const bool there = mine != 0 && lane < 4 * PER;
-                    const int e = (u * 32 + src) * PER + (lane & (PER - 1));
+                    const int src = four_lanes(from, lane / PER), at_src = src & 31;
+                    const int u = __shfl_sync(0xffffffffu, __ffs(pending) - 1, at_src);
+                    if (from >> lane & 1u) pending &= pending - 1;
+                    const bool there = src >= 0 && lane < 4 * PER;
+                    const int e = (u * 32 + at_src) * PER + (lane & (PER - 1));
                     float f = 0.0f;
                     if (there) f = to_f32(reinterpret_cast<const T*>(at)[e]);
-                    alt.offer(make_key(f, base + e), there && base + e < classes, k);
+                    const int i = base + e - lead;
+                    alt.offer(make_key(f, i), there && i >= 0 && i < classes, k);
                 }
                 __syncwarp();
             }
@@ -603,7 +630,7 @@ __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
             if (++slot == kLpSlots) slot = 0, phase ^= 1;
         }
         const Sums a = sums.total();
-        if (TOP && __any_sync(0xffffffffu, a.s != a.s)) scan_again<T, true>(row, 0, classes, lane, 32, k, alt);
+        if (TOP && __any_sync(0xffffffffu, a.s != a.s)) scan_again<T, false>(row, 0, classes, lane, 32, k, alt);
         if (TOP && alt.count) alt.flush(k);
         write_row<T, TOP>(row, targets, r, classes, k, warp_join(a), alt, o, err);
     }
@@ -617,10 +644,11 @@ __global__ void __launch_bounds__(kLpWarps * 32, 4)
     k_logprobs_long(const T* __restrict__ x, int64_t ld, const int32_t* __restrict__ targets, int64_t rows,
                     int classes, int k, int parts, int stretch, const LpOut o, int* __restrict__ err)
 {
+    static_assert(kLpCluster <= kLpWarps, "a warp to each block of the cluster");
     __shared__ Sums sums[kLpWarps];
-    __shared__ float lows[kLpWarps];
+    __shared__ FirstLows lows;
     __shared__ int counts[kLpWarps];
-    __shared__ Key buf[kLpWarps][TOP ? 64 : 1], list[kLpWarps][TOP ? kLpMaxTop : 1];
+    __shared__ Key buf[TOP ? kLpWarps : 1][64], list[2][32];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -628,64 +656,52 @@ __global__ void __launch_bounds__(kLpWarps * 32, 4)
     const int begin = min(classes, part * stretch), end = min(classes, begin + stretch);
     for (int64_t r = blockIdx.x / parts; r < rows; r += gridDim.x / parts) {
         Alternatives alt;
-        alt.clear(buf[warp]);
-        Sums a = warp_join(scan<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt, lows));
-        if (lane == 0) {
-            sums[warp] = a;
-            counts[warp] = alt.sorted ? 64 : alt.count;
+        alt.clear(buf[TOP ? warp : 0]);
+        if (TOP && warp < 2) list[warp][lane] = 0;
+        Sums a = warp_join(scan<T, TOP, VEC>(x + r * ld, begin, end, threadIdx.x, kLpWarps * 32, k, alt, &lows));
+        if (TOP) {
+            const int n = alt.gather(k);
+            if (lane == 0) counts[warp] = n;
         }
+        if (lane == 0) sums[warp] = a;
         __syncthreads();
-        int total = 0;
-#pragma unroll
-        for (int w = 0; w < kLpWarps; ++w) total += counts[w];
-        if (TOP && total > 32) {
-            // each warp's own list, and the lists one after another
-            if (alt.count) alt.flush(k);
-            list[warp][lane] = alt.best;
+        if (warp == 0) a = warp_join(lane < kLpWarps ? sums[lane] : Sums{kLpStart, 0.0f, 0.0f});
+        if (TOP) {
+            rank_all(buf, kLpWarps, counts, 0, k, list[0]);
             __syncthreads();
         }
-        if (warp == 0) {
-            a = lane < kLpWarps ? sums[lane] : Sums{kLpStart, 0.0f, 0.0f};
-            a = warp_join(a);
-            if (TOP && total > 32) {
-                alt.merge_lists(kLpWarps - 1, k, k, [&](int p, int i) { return list[p + 1][i]; });
-            } else if (TOP) {
-                // all the warps' elements fit one sort
-                Key v = 0;
-                int before = 0;
-#pragma unroll
-                for (int w = 0; w < kLpWarps; ++w) {
-                    if (lane >= before && lane < before + counts[w]) v = buf[w][lane - before];
-                    before += counts[w];
-                }
-                alt.merge_unsorted(v, k);
-            }
-        }
         if (parts > 1) {
-            if (warp == 0) {
-                if (lane == 0) sums[0] = a;
-                if (TOP) list[0][lane] = alt.best;
-            }
+            if (threadIdx.x == 0) sums[0] = a;
             cluster_sync();
-            if (part == 0 && warp == 0) {
-                const uint32_t sa = mapa_shared(smem_u32(&sums[0]), lane < parts ? lane : 0);
-                Sums q;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.top) : "r"(sa) : "memory");
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(sa + 4) : "memory");
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.t) : "r"(sa + 8) : "memory");
-                if (lane >= parts) q.clear();
-                if (TOP)
-                    alt.merge_lists(parts - 1, k, k, [&](int p, int i) {
-                        Key v;
+            if (part == 0) {
+                if (TOP && warp < parts) {
+                    Key v = 0;
+                    if (lane < k)
                         asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                                     : "=l"(v) : "r"(mapa_shared(smem_u32(&list[0][i]), p + 1)) : "memory");
-                        return v;
-                    });
-                a = warp_join(q);
+                                     : "=l"(v) : "r"(mapa_shared(smem_u32(&list[0][lane]), warp)) : "memory");
+                    buf[warp][lane] = v;
+                }
+                if (warp == 0) {
+                    const uint32_t sa = mapa_shared(smem_u32(&sums[0]), lane < parts ? lane : 0);
+                    Sums q;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.top) : "r"(sa) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.s) : "r"(sa + 4) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q.t) : "r"(sa + 8) : "memory");
+                    if (lane >= parts) q.clear();
+                    a = warp_join(q);
+                }
+                if (TOP) {
+                    __syncthreads();
+                    rank_all(buf, parts, nullptr, k, k, list[1]);
+                    __syncthreads();
+                }
             }
             cluster_sync();              // the first block has read the others' shared memory
         }
-        if (part == 0 && warp == 0) write_row<T, TOP>(x + r * ld, targets, r, classes, k, a, alt, o, err);
+        if (part == 0 && warp == 0) {
+            alt.best = list[parts > 1][lane];
+            write_row<T, TOP>(x + r * ld, targets, r, classes, k, a, alt, o, err);
+        }
         __syncthreads();
     }
 }
@@ -810,33 +826,25 @@ static int check_lp(const void* x, int64_t ld, int type, int64_t rows, int class
     return ITO_OK;
 }
 
-template <typename T, bool TOP, bool VEC>
+template <typename T, bool TOP>
 static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
                    const LpOut& o, int* err, cudaStream_t s)
 {
     const T* x = static_cast<const T*>(xp);
     const int sms = num_sms();
-    // A warp to a row up to four vectors a lane, or where rows are enough to fill the device with
-    // warps: the alternatives' sorts are then one row's, and wait for no other warp. Without them
-    // the loads alone decide. 4096 x 32768 bf16 without: 44 us, 56 with a block to a row; 2500 rows
-    // without 39 and 36, with 1 alternative 50 and 44, with 4 55 and 59, with 8 60 and 78; 1200
-    // rows with 4 33 and 28.
-    const int round = 32 * Vec<T>::kPer * 4;
-    if (classes <= round || rows >= (k < 4 ? 24 : 16) * sms) {
+    // A warp to a row up to four vectors a lane, or with eight rows to an SM: no warp waits for
+    // another then. bf16 with 0, 1, 4, 8 alternatives, against a block to a row:
+    // 2500 x 32768 31, 44, 49, 53 us, 36, 46, 53, 61; 1500 x 5000 5, 9, 10, 12 us, 9, 14, 17, 21.
+    // Fewer rows leave too few loads in flight (1200 x 32768 18, 29, 32, 35 us, 17, 22, 26, 30).
+    const int round = 32 * Vec<T>::kPer * kLpUnroll;
+    if (classes <= round || rows >= 8 * sms) {
         // (a block's warps take rows a grid apart, so SMs differ by a row at most)
-        // (a block's warps take rows a grid apart, so SMs differ by a row at most)
-        const int warps = VEC ? ring_warps(TOP) : kLpWarps, blocks = VEC ? ring_blocks(TOP) : 4;
-        const int64_t want = (rows + warps - 1) / warps;
-        const unsigned grid = (unsigned)(want < sms ? want : std::min((want + sms - 1) / sms, (int64_t)blocks) * sms);
-        if constexpr (VEC) {
-            const auto kernel = k_logprobs_ring<T, TOP>;
-            constexpr int smem = ring_warps(TOP) * kLpSlots * kLpRound;
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-                return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
-            launch_pdl(kernel, grid, warps * 32, smem, s, x, ld, targets, rows, classes, k, o, err);
-        } else {
-            launch_pdl(k_logprobs_short<T, TOP>, grid, warps * 32, 0, s, x, ld, targets, rows, classes, k, o, err);
-        }
+        const unsigned grid = (unsigned)std::min(rows, (int64_t)ring_blocks(TOP) * sms);
+        const auto kernel = k_logprobs_ring<T, TOP>;
+        constexpr int smem = ring_warps(TOP) * kLpSlots * kLpRound;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
+        launch_pdl(kernel, grid, ring_warps(TOP) * 32, smem, s, x, ld, targets, rows, classes, k, o, err);
         return launch_status("log probabilities");
     }
     // blocks of a row: enough that all rows' blocks occupy the SMs, each with a round of loads at least
@@ -857,8 +865,10 @@ static int run_fwd(const void* xp, int64_t ld, const int32_t* targets, int64_t r
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = parts > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP, VEC>, x, ld, targets, rows, classes, k, parts,
-                                             stretch, o, err);
+    const cudaError_t e =
+        rows_vec(x, ld, sizeof(T), rows)
+            ? cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP, true>, x, ld, targets, rows, classes, k, parts, stretch, o, err)
+            : cudaLaunchKernelEx(&cfg, k_logprobs_long<T, TOP, false>, x, ld, targets, rows, classes, k, parts, stretch, o, err);
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "log probabilities launch: %s", cudaGetErrorString(e));
 }
 
@@ -866,12 +876,8 @@ template <typename T>
 static int run_fwd_any(const void* x, int64_t ld, const int32_t* targets, int64_t rows, int classes, int k,
                        const LpOut& o, int* err, cudaStream_t s)
 {
-    if (rows_vec(x, ld, sizeof(T), rows)) {
-        if (k) return run_fwd<T, true, true>(x, ld, targets, rows, classes, k, o, err, s);
-        return run_fwd<T, false, true>(x, ld, targets, rows, classes, k, o, err, s);
-    }
-    if (k) return run_fwd<T, true, false>(x, ld, targets, rows, classes, k, o, err, s);
-    return run_fwd<T, false, false>(x, ld, targets, rows, classes, k, o, err, s);
+    if (k) return run_fwd<T, true>(x, ld, targets, rows, classes, k, o, err, s);
+    return run_fwd<T, false>(x, ld, targets, rows, classes, k, o, err, s);
 }
 
 template <typename T>

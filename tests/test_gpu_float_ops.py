@@ -571,7 +571,8 @@ def test_logprobs_of_nan_and_infinity(torch, ito, n):
 
 
 @pytest.mark.parametrize("dtype,n,pad,k", [("float32", 1537, 3, 3), ("bfloat16", 2500, 4, 9), ("float16", 1031, 1, 32),
-                                           ("bfloat16", 2049, 0, 4), ("bfloat16", 3000, 0, 0)])
+                                           ("bfloat16", 2049, 0, 4), ("bfloat16", 3000, 0, 0),
+                                           ("bfloat16", 1, 0, 1), ("float16", 5, 2, 3)])
 def test_logprobs_of_many_rows(torch, ito, dtype, n, pad, k):
     """Rows enough for several to a warp, on 16 bytes or not, with rows in order, masked ends and whole masks."""
     rows = 30 * torch.cuda.get_device_properties(0).multi_processor_count + 5
