@@ -42,7 +42,10 @@ __device__ __forceinline__ void fold_sums(float (&v)[N])
 }
 
 // Sums R values over the threads of a row: lanes of a warp (tpr <= 32) or the block. `red` holds
-// two banks of R * 32 floats; the caller alternates them, so that one barrier is enough.
+// two banks of R * 32 floats; the caller alternates them, so that one barrier is enough. (Eight
+// warps have steps of their own: with the loops of any number the layer norm of 8192 x 4096 bf16
+// took 28.4 us forward and 46.6 backward instead of 26.2 and 44.8; with 16-byte loads of the
+// warps' parts and additions instead of shuffles 31.0 and 48.8.)
 template <int R>
 __device__ __forceinline__ void row_sums(float (&v)[R], int tpr, float* red)
 {
@@ -58,6 +61,15 @@ __device__ __forceinline__ void row_sums(float (&v)[R], int tpr, float* red)
     for (int o = 16 / R; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
     if (lane % (32 / R) == 0) red[lane / (32 / R) * 32 + warp] = v[0];
     __syncthreads();
+    if (warps == 8) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] = red[r * 32 + (lane & 7)];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+        return;
+    }
     int top = 2;                         // the warps' number, to the next power of two
     while (top < warps) top *= 2;
 #pragma unroll
@@ -432,6 +444,7 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
                           T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd,
                           LnRing ring, int* __restrict__ err)
 {
+    static_assert(R <= 2, "rows' roots are taken by every other lane");
     constexpr int PER = Vec<T>::kPer;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2][R * 32];
@@ -507,11 +520,18 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
             rs[r] = s.x + s.y;
         }
         row_sums<R>(rs, tpr, red[1]);
+        if constexpr (R == 2) {
+            // one root and quotient a lane, each row's in every other one
+            const float q = 1.0f / sqrtf((threadIdx.x & 1 ? rs[R - 1] : rs[0]) * inv + eps);
+            rs[0] = __shfl_sync(0xffffffffu, q, 0);
+            rs[R - 1] = __shfl_sync(0xffffffffu, q, 1);
+        } else {
+            rs[0] = 1.0f / sqrtf(rs[0] * inv + eps);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = grp * R + r;
             if (row >= rows) continue;
-            rs[r] = 1.0f / sqrtf(rs[r] * inv + eps);
             if (at == 0) {
                 if (mean) mean[row] = mu[r];
                 if (rstd) rstd[row] = rs[r];
