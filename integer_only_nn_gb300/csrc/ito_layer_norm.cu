@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kLnMostThreads)
     }
 }
 
-// dx, and each row group's share of dgamma and dbeta (part: [shares][2][cols], may be null),
+// dx, and each block's share of dgamma and dbeta (part: [shares][2][cols], may be null),
 // which k_layer_norm_wgrad adds in a fixed order.
 template <typename T, int VPT, int R, bool FULL>
 __global__ void __launch_bounds__(ln_bwd_threads(VPT))
@@ -328,7 +328,34 @@ __global__ void __launch_bounds__(ln_bwd_threads(VPT))
         }
     }
     if (!part) return;
-    float* pg = part + ((int64_t)blockIdx.x * groups + group) * 2 * cols;
+    float* pg = part + (int64_t)blockIdx.x * 2 * cols;
+    if (groups > 1) {
+        // the block's rows side by side: lanes of a warp by shuffles, the warps one after another
+        __shared__ float sum[2][64 * PER];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                for (int o = tpr; o < 32; o *= 2) {
+                    sg[i][j] += __shfl_xor_sync(0xffffffffu, sg[i][j], o);
+                    sb[i][j] += __shfl_xor_sync(0xffffffffu, sb[i][j], o);
+                }
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+            if ((int)threadIdx.x / 32 == w && (int)(threadIdx.x & 31) < tpr)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const int c = (i * tpr + at) * PER + j;
+                        if (c >= cols) continue;
+                        sum[0][c] = w ? sum[0][c] + sg[i][j] : sg[i][j];
+                        sum[1][c] = w ? sum[1][c] + sb[i][j] : sb[i][j];
+                    }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) pg[c] = c < cols ? sum[0][c] : sum[1][c - cols];
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -701,31 +728,27 @@ __global__ void __launch_bounds__(512)
         }
 }
 
-// The shares' sums: a lane takes a column, a block's warps every eighth share.
-__global__ void __launch_bounds__(256)
+// The shares' sums: a lane takes a column, a block's warps every 32nd share. (With eight warps
+// 304 shares of 4096 columns took as long, 456 of 64 columns 8 us more.)
+__global__ void __launch_bounds__(1024)
     k_layer_norm_wgrad(const float* __restrict__ part, int parts, int cols, float* __restrict__ dgamma,
                        float* __restrict__ dbeta)
 {
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ float sums[8][32];
+    __shared__ float sums[32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < 2 * cols) {
-        int p = warp;
-        for (; p + 24 < parts; p += 32) {
-            const float a = part[(int64_t)p * 2 * cols + c], b = part[(int64_t)(p + 8) * 2 * cols + c];
-            const float d = part[(int64_t)(p + 16) * 2 * cols + c], e = part[(int64_t)(p + 24) * 2 * cols + c];
-            s += (a + b) + (d + e);
-        }
-        for (; p < parts; p += 8) s += part[(int64_t)p * 2 * cols + c];
+#pragma unroll 4
+        for (int p = warp; p < parts; p += 32) s += part[(int64_t)p * 2 * cols + c];
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp || c >= 2 * cols) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    for (int w = 1; w < 32; ++w) s += sums[w][lane];
     if (c < cols) {
         if (dgamma) dgamma[c] = s;
     } else if (dbeta) {
@@ -770,7 +793,13 @@ static bool ln_ring_rows(const LnShape& s, int cols, int size, int64_t rows)
     return s.vpt && s.tpr > 32 && cols % (16 / size) == 0 && rows >= (int64_t)kLnRingRows * num_sms();
 }
 
-static int ln_ring_blocks(const LnShape& s, bool forward) { return s.block > 256 ? 1 : forward ? kLnTight : 2; }
+// Blocks of an SM: as many threads whatever the rows' length (20000 x 768 bf16: 15.5 us forward and
+// 26 backward, 30 and 36 with three and two blocks; 8192 x 1024 10 and 17, 13.5 and 19).
+static int ln_ring_blocks(const LnShape& s, bool forward)
+{
+    if (s.block > 256) return 1;
+    return (forward ? kLnTight : 2) * 256 / s.block;
+}
 
 static LnRing ln_ring(const LnShape& s, int cols, int size, int stage_rows, int blocks)
 {
@@ -803,7 +832,7 @@ static int ln_parts(int64_t rows, int cols, int size)
 {
     const LnShape s = ln_shape(cols, size, ln_bwd_threads(4));
     if (!s.vpt) return (int)std::min<int64_t>(rows, 32);
-    return ln_bwd_grid(s, rows) * (s.block / s.tpr);
+    return ln_bwd_grid(s, rows);
 }
 
 static int check_ln(const void* x, int64_t ldx, int type, int64_t rows, int cols, const char* name)
@@ -927,7 +956,7 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
 #undef ITO_LN_AS
 #undef ITO_LN_RING
     if (wgrad)
-        launch_pdl(k_layer_norm_wgrad, (2 * cols + 31) / 32, 256, 0, s, static_cast<const float*>(part),
+        launch_pdl(k_layer_norm_wgrad, (2 * cols + 31) / 32, 1024, 0, s, static_cast<const float*>(part),
                    parts, cols, dgamma, dbeta);
     return launch_status("layer norm");
 }
