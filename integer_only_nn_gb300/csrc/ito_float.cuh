@@ -131,17 +131,27 @@ struct Vec {
             }
         raw = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    template <bool FULL>
-    __device__ __forceinline__ void load_row(const T* row, int c, int n, bool vec)
+    // elements c, c + step, .. of a row of n
+    __device__ __forceinline__ void load_apart(const T* row, int c, int step, int n)
     {
-        if (FULL) raw = *reinterpret_cast<const uint4*>(row + c);
-        else load(row, c, n, vec);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (c + i * step < n) {
+                if constexpr (sizeof(T) == 4) w[i] = *reinterpret_cast<const uint32_t*>(row + c + i * step);
+                else w[i >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + c + i * step) << (16 * (i & 1));
+            }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    template <bool FULL>
-    __device__ __forceinline__ void store_row(T* row, int c, int n, bool vec) const
+    __device__ __forceinline__ void store_apart(T* row, int c, int step, int n) const
     {
-        if (FULL) *reinterpret_cast<uint4*>(row + c) = raw;
-        else store(row, c, n, vec);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (c + i * step < n) {
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(row + c + i * step) = w[i];
+                else *reinterpret_cast<uint16_t*>(row + c + i * step) = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
     }
     __device__ __forceinline__ void store(T* row, int c, int n, bool vec) const
     {

@@ -104,18 +104,52 @@ __device__ __forceinline__ void load_weights(const void* p, int type, int c, int
     for (int i = 0; i < N; ++i) v[i] = !FULL && p && c + i < n ? load_typed(p, type, c + i) : fill;
 }
 
-// FULL: rows are whole vectors on 16-byte boundaries, gamma and beta too (no element is looked at alone).
+// FULL: rows are whole vectors on 16-byte boundaries, gamma and beta too (no element is looked at
+// alone). Else a thread's elements are a row's threads apart, so that a warp's single accesses are
+// still consecutive (5000 x 2500 bf16: 25 us forward and 37 backward, 41 and 75 with neighbours;
+// 65536 x 30 8 and 12, 19 and 17).
+template <bool FULL, int PER>
+struct LnColumns {
+    int tpr, at;
+    __device__ __forceinline__ int first(int i) const { return FULL ? (i * tpr + at) * PER : i * PER * tpr + at; }
+    __device__ __forceinline__ int step() const { return FULL ? 1 : tpr; }
+    __device__ __forceinline__ int column(int i, int j) const { return first(i) + j * step(); }
+
+    template <typename T>
+    __device__ __forceinline__ void load(Vec<T>& v, const T* row, int i, int cols) const
+    {
+        if (FULL) v.raw = *reinterpret_cast<const uint4*>(row + first(i));
+        else v.load_apart(row, first(i), tpr, cols);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(const Vec<T>& v, T* row, int i, int cols) const
+    {
+        if (FULL) *reinterpret_cast<uint4*>(row + first(i)) = v.raw;
+        else v.store_apart(row, first(i), tpr, cols);
+    }
+    __device__ __forceinline__ void weights(const void* p, int type, int i, int cols, float fill, float (&v)[PER]) const
+    {
+        if constexpr (FULL) {
+            load_weights<true>(p, type, first(i), cols, fill, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] = p && column(i, j) < cols ? load_typed(p, type, column(i, j)) : fill;
+        }
+    }
+};
+
 template <typename T, int VPT, int R, bool FULL>
-__global__ void __launch_bounds__(ln_threads(VPT))
-    k_layer_norm_fwd(const T* __restrict__ x, int64_t ldx, int x_vec, const void* __restrict__ gamma,
+__global__ void __launch_bounds__(ln_threads(VPT), 1024 / ln_threads(VPT))
+    k_layer_norm_fwd(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
                      const void* __restrict__ beta, int w_type, int64_t rows, int cols, int tpr, float eps,
-                     T* __restrict__ y, int64_t ldy, int y_vec, float* __restrict__ mean, float* __restrict__ rstd)
+                     T* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd)
 {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int PER = Vec<T>::kPer;
     __shared__ float red[2][R * 32];
     const int at = threadIdx.x % tpr, groups = blockDim.x / tpr;
+    const LnColumns<FULL, PER> part{tpr, at};
     const float inv = 1.0f / (float)cols;
     const int64_t step = (int64_t)gridDim.x * groups * R;
     // every thread of the block passes the barriers of every round
@@ -126,8 +160,7 @@ __global__ void __launch_bounds__(ln_threads(VPT))
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = (i * tpr + at) * PER;
-                if (first + r < rows && c < cols) v[r][i].template load_row<FULL>(x + (first + r) * ldx, c, cols, x_vec);
+                if (first + r < rows && part.first(i) < cols) part.load(v[r][i], x + (first + r) * ldx, i, cols);
                 else v[r][i].raw = make_uint4(0u, 0u, 0u, 0u);
             }
         float mu[R], rs[R];
@@ -151,10 +184,9 @@ __global__ void __launch_bounds__(ln_threads(VPT))
             for (int i = 0; i < VPT; ++i) {
                 float f[PER];
                 v[r][i].get(f);
-                const int c = (i * tpr + at) * PER;
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
-                    const float d = (FULL ? c : c + j) < cols ? f[j] - mu[r] : 0.0f;
+                    const float d = (FULL ? part.first(i) : part.column(i, j)) < cols ? f[j] - mu[r] : 0.0f;
                     rs[r] += d * d;
                 }
             }
@@ -170,11 +202,10 @@ __global__ void __launch_bounds__(ln_threads(VPT))
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = (i * tpr + at) * PER;
-            if (c >= cols) continue;
+            if (part.first(i) >= cols) continue;
             float g[PER], b[PER];
-            load_weights<FULL>(gamma, w_type, c, cols, 1.0f, g);
-            load_weights<FULL>(beta, w_type, c, cols, 0.0f, b);
+            part.weights(gamma, w_type, i, cols, 1.0f, g);
+            part.weights(beta, w_type, i, cols, 0.0f, b);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (first + r >= rows) continue;
@@ -183,7 +214,7 @@ __global__ void __launch_bounds__(ln_threads(VPT))
 #pragma unroll
                 for (int j = 0; j < PER; ++j) f[j] = (f[j] - mu[r]) * rs[r] * g[j] + b[j];
                 v[r][i].set(f);
-                v[r][i].template store_row<FULL>(y + (first + r) * ldy, c, cols, y_vec);
+                part.store(v[r][i], y + (first + r) * ldy, i, cols);
             }
         }
     }
@@ -248,21 +279,22 @@ __global__ void __launch_bounds__(kLnMostThreads)
 // which k_layer_norm_wgrad adds in a fixed order.
 template <typename T, int VPT, int R, bool FULL>
 __global__ void __launch_bounds__(ln_bwd_threads(VPT))
-    k_layer_norm_bwd(const T* __restrict__ dy, int64_t lddy, int dy_vec, const T* __restrict__ x, int64_t ldx,
-                     int x_vec, const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
+    k_layer_norm_bwd(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                     const void* __restrict__ gamma, int w_type, const float* __restrict__ mean,
                      const float* __restrict__ rstd, int64_t rows, int cols, int tpr, T* __restrict__ dx,
-                     int64_t lddx, int dx_vec, float* __restrict__ part)
+                     int64_t lddx, float* __restrict__ part)
 {
     griddep_wait();
     griddep_launch_dependents();
     constexpr int PER = Vec<T>::kPer;
     __shared__ float red[2][2 * R * 32];
     const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+    const LnColumns<FULL, PER> mine{tpr, at};
     const float inv = 1.0f / (float)cols;
     float g[VPT][PER], sg[VPT][PER], sb[VPT][PER];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        load_weights<FULL>(gamma, w_type, (i * tpr + at) * PER, cols, 1.0f, g[i]);
+        mine.weights(gamma, w_type, i, cols, 1.0f, g[i]);
 #pragma unroll
         for (int j = 0; j < PER; ++j) sg[i][j] = sb[i][j] = 0.0f;
     }
@@ -279,10 +311,9 @@ __global__ void __launch_bounds__(ln_bwd_threads(VPT))
             rs[r] = in ? rstd[first + r] : 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = (i * tpr + at) * PER;
-                if (in && c < cols) {
-                    vd[r][i].template load_row<FULL>(dy + (first + r) * lddy, c, cols, dy_vec);
-                    vx[r][i].template load_row<FULL>(x + (first + r) * ldx, c, cols, x_vec);
+                if (in && mine.first(i) < cols) {
+                    mine.load(vd[r][i], dy + (first + r) * lddy, i, cols);
+                    mine.load(vx[r][i], x + (first + r) * ldx, i, cols);
                 } else {
                     vd[r][i].raw = vx[r][i].raw = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -315,15 +346,14 @@ __global__ void __launch_bounds__(ln_bwd_threads(VPT))
             const float sa = s[2 * r] * inv, sh = s[2 * r + 1] * inv;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int c = (i * tpr + at) * PER;
-                if (c >= cols) continue;
+                if (mine.first(i) >= cols) continue;
                 float d[PER], h[PER];
                 vd[r][i].get(d);
                 vx[r][i].get(h);
 #pragma unroll
                 for (int j = 0; j < PER; ++j) d[j] = rs[r] * (d[j] * g[i][j] - sa - (h[j] - mu[r]) * rs[r] * sh);
                 vd[r][i].set(d);
-                vd[r][i].template store_row<FULL>(dx + (first + r) * lddx, c, cols, dx_vec);
+                mine.store(vd[r][i], dx + (first + r) * lddx, i, cols);
             }
         }
     }
@@ -346,7 +376,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(VPT))
                 for (int i = 0; i < VPT; ++i)
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
-                        const int c = (i * tpr + at) * PER + j;
+                        const int c = mine.column(i, j);
                         if (c >= cols) continue;
                         sum[0][c] = w ? sum[0][c] + sg[i][j] : sg[i][j];
                         sum[1][c] = w ? sum[1][c] + sb[i][j] : sb[i][j];
@@ -360,7 +390,7 @@ __global__ void __launch_bounds__(ln_bwd_threads(VPT))
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int c = (i * tpr + at) * PER + j;
+            const int c = mine.column(i, j);
             if (c < cols) {
                 pg[c] = sg[i][j];
                 pg[cols + c] = sb[i][j];
@@ -455,8 +485,8 @@ struct LnRing {
     uint32_t row_bytes;
 };
 
-// Blocks of up to 256 threads: three to an SM forward (8192 x 4096 bf16: 28.5 us, 30.4 with two,
-// 37.7 with four), two backward (46.3 us, 53.9 with three, whose registers spill).
+// Blocks of up to 256 threads: three to an SM forward (8192 x 4096 bf16: 25.6 us, 28.6 with four),
+// two backward (43 us, 51 with three, whose registers spill).
 constexpr int kLnTight = 3;
 constexpr int ln_ring_threads(int vpt, bool tight) { return tight ? 256 : vpt == 4 ? 1024 : 512; }
 
@@ -793,12 +823,13 @@ static bool ln_ring_rows(const LnShape& s, int cols, int size, int64_t rows)
     return s.vpt && s.tpr > 32 && cols % (16 / size) == 0 && rows >= (int64_t)kLnRingRows * num_sms();
 }
 
-// Blocks of an SM: as many threads whatever the rows' length (20000 x 768 bf16: 15.5 us forward and
-// 26 backward, 30 and 36 with three and two blocks; 8192 x 1024 10 and 17, 13.5 and 19).
+// Blocks of an SM: as many threads as the kernel's registers allow, whatever the rows' length
+// (20000 x 768 bf16: 15.5 us forward and 26 backward, 30 and 36 with three and two blocks; 8192 x
+// 1024 10 and 17, 13.5 and 19; forward 3000 x 10000 35, 59 with one block; 5000 x 2500 f32 18, 27).
 static int ln_ring_blocks(const LnShape& s, bool forward)
 {
-    if (s.block > 256) return 1;
-    return (forward ? kLnTight : 2) * 256 / s.block;
+    const int threads = !forward ? 512 : s.vpt == 4 ? 1024 : s.block > 256 ? 640 : kLnTight * 256;   // by their registers
+    return std::max(1, threads / s.block);
 }
 
 static LnRing ln_ring(const LnShape& s, int cols, int size, int stage_rows, int blocks)
@@ -895,8 +926,8 @@ static int run_fwd(const void* xp, int64_t ldx, const void* gamma, const void* b
         return launch_status("layer norm");
     }
 #define ITO_LN_AS(V, RR, F)                                                                                       \
-    launch_pdl(k_layer_norm_fwd<T, V, RR, F>, grid, sh.block, 0, s, x, ldx, xv, gamma, beta, w_type, rows, cols, \
-               sh.tpr, eps, y, ldy, yv, mean, rstd)
+    launch_pdl(k_layer_norm_fwd<T, V, RR, F>, grid, sh.block, 0, s, x, ldx, gamma, beta, w_type, rows, cols, \
+               sh.tpr, eps, y, ldy, mean, rstd)
 #define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
     if (sh.vpt == 1) { if (R > 1) ITO_LN(1, 4); else ITO_LN(1, 1); }
     else if (sh.vpt == 2) { if (R > 1) ITO_LN(2, 2); else ITO_LN(2, 1); }
@@ -921,8 +952,8 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
     const int grid = ln_bwd_grid(sh, rows);
     const bool full = cols % Vec<T>::kPer == 0 && dyv && xv && dxv && aligned_to(gamma, 16);
 #define ITO_LN_AS(V, RR, F)                                                                                         \
-    launch_pdl(k_layer_norm_bwd<T, V, RR, F>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean, \
-               rstd, rows, cols, sh.tpr, dx, lddx, dxv, share)
+    launch_pdl(k_layer_norm_bwd<T, V, RR, F>, grid, sh.block, 0, s, dy, lddy, x, ldx, gamma, w_type, mean, \
+               rstd, rows, cols, sh.tpr, dx, lddx, share)
 #define ITO_LN(V, RR) do { if (full) ITO_LN_AS(V, RR, true); else ITO_LN_AS(V, RR, false); } while (0)
 #define ITO_LN_RING(V, RN)                                                                                          \
     do {                                                                                                            \
