@@ -169,7 +169,7 @@ struct FirstLows {
 
 struct Alternatives {
     Key best, low;
-    float low_value;
+    float low_value;             // the smallest value that may still come before `low`
     int count;
     bool sorted;                 // the list holds elements
     Key* buf;
@@ -245,7 +245,10 @@ struct Alternatives {
     __device__ __forceinline__ void take_low(int k)
     {
         low = __shfl_sync(0xffffffffu, best, k - 1);
-        low_value = low ? key_value(low) : -INFINITY;
+        // Later elements of the same value have higher indexes: only larger ones come before it. (4096 x
+        // 32768 bf16 with 4 alternatives, all elements equal: 60 us, 388 with equal ones looked at;
+        // half of them masked 83, 243.)
+        low_value = low ? key_value(((low >> 32) + 1) << 32) : -INFINITY;
         sorted = true;
     }
     __device__ __forceinline__ void merge_unsorted(Key a, int k)
