@@ -361,6 +361,15 @@ def test_layer_norm(torch, ito, i, size, dtype):
     check_layer_norm(torch, ito, x, gamma, beta, normal(torch, size, i + 300, 1.0, dtype), 1e-5, dtype)
 
 
+@pytest.mark.parametrize("size", [(1300, 768), (1251, 1000), (700, 2600), (650, 10000), (700, 5001), (2500, 300), (40000, 24)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_layer_norm_of_many_rows(torch, ito, size, dtype):
+    """Rows enough for rings and for several to a block, of lengths for each of the block sizes."""
+    x = (normal(torch, size, 1, 1.5) + normal(torch, (size[0], 1), 2, 1.0)).to(dt(torch, dtype))
+    check_layer_norm(torch, ito, x, 1 + normal(torch, (size[1],), 3, 0.2), normal(torch, (size[1],), 4, 0.5),
+                     normal(torch, size, 5, 1.0, dtype), 1e-5, dtype)
+
+
 @pytest.mark.parametrize("cols", [64, 100, 2048])
 def test_layer_norm_of_flat_and_far_rows(torch, ito, cols):
     """Rows of one value (no variance but eps), and rows whose mean is large beside their spread."""
