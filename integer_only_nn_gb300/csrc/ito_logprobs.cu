@@ -726,14 +726,14 @@ struct LpRow {
 };
 constexpr float kLpFar = 65536.0f;
 
-// dx_j: the factor of p is one sum, so p (which may lie below the normal range) is rounded once
+// dx_j: the factor of p is one sum, so p (which may lie below the normal range) is rounded once.
+// A p of 0 takes no part: the log p of a class masked with the type's lowest value, times a
+// g_H above 1, would be infinite.
 __device__ __forceinline__ float lp_slope(const LpRow& w, float x, int c)
 {
     float d = c == w.t ? w.g : 0.0f;
-    if (x != -INFINITY) {
-        const float lp = (x - w.top) - w.ls;
-        d -= __expf(lp) * (w.g + w.gh * (lp + w.h));
-    }
+    const float lp = (x - w.top) - w.ls, p = __expf(lp);
+    if (x != -INFINITY && p != 0.0f) d -= p * (w.g + w.gh * (lp + w.h));
     return d;
 }
 

@@ -44,3 +44,33 @@ def test_layer_norm_backward_in_place(torch, ito, rows, cols, dtype):
     assert torch.equal(db, dbeta)
     assert torch.equal(dg, dgamma)
     assert torch.equal(dy, dx)
+
+
+# --------------------------------------------------------- log probabilities
+
+@pytest.mark.parametrize("factor", [2.0, -3.0, 65536.0, -65536.0])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [16, 1000, 40000])
+def test_logprobs_gradient_of_lowest_values_under_large_factors(torch, ito, n, dtype, factor):
+    """Classes masked with the type's lowest value have p = 0 and so a gradient of 0, however large
+    the entropy's gradient; the others follow the formula, to the bounds of their 32-bit terms."""
+    x = normal(torch, (4, n), n, 2.0, dtype)
+    low = torch.finfo(x.dtype).min
+    x[0, n // 2:] = low
+    x[1, 1:] = low
+    x[2, ::3] = low
+    x[2, 1::3] = -math.inf
+    tgt = torch.tensor([0, 0, 2, n - 1], dtype=torch.int32, device="cuda")
+    _, ent, lse, _, _ = ito.ito_token_logprobs_fwd(x, tgt)
+    gl, gh = torch.full((4,), -0.5, device="cuda"), torch.full((4,), factor, device="cuda")
+    d = ito.ito_token_logprobs_bwd(x, tgt, lse, ent, gl, gh)
+    X, L, H = f64(x), f64(lse)[:, None], f64(ent)[:, None]
+    lp = np.maximum(X - L, -1e4)
+    p = np.exp(lp)
+    hot = (np.arange(n) == f64(tgt)[:, None]).astype(np.float64)
+    want = -0.5 * (hot - p) - factor * p * (lp + H)
+    size = 0.5 * (hot + p) + abs(factor) * p * (np.abs(lp) + np.abs(H))
+    e = 8 * U * size + (0.5 + abs(factor) * (np.abs(lp) + np.abs(H) + 1)) * p * (np.abs(lp) + np.abs(L) + 4) * 2 * U
+    e = e + 4 * TINY * (1 + abs(factor) * (np.abs(np.where(p > 0, lp, 0)) + np.abs(H)))
+    within_rounded(d, want, e, dtype, "dlogits")
+    assert bool((d[0, n // 2:] == 0).all()) and bool((d[1, 1:] == 0).all())
