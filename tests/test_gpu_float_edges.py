@@ -74,3 +74,28 @@ def test_logprobs_gradient_of_lowest_values_under_large_factors(torch, ito, n, d
     e = e + 4 * TINY * (1 + abs(factor) * (np.abs(np.where(p > 0, lp, 0)) + np.abs(H)))
     within_rounded(d, want, e, dtype, "dlogits")
     assert bool((d[0, n // 2:] == 0).all()) and bool((d[1, 1:] == 0).all())
+
+
+@pytest.mark.parametrize("offset", [0.0, 1000.0, 100000.0, -100000.0, 1000000.0])
+@pytest.mark.parametrize("n,many", [(500, False), (2048, False), (2048, True), (70000, False)])
+def test_logprobs_of_rows_far_from_zero(torch, ito, n, many, offset):
+    """Entropy and log p depend on differences of logits alone, so their bounds do not grow with the
+    row's offset. A lane adds n / 64 terms to each of its sums, then some ten sums are joined. A term
+    2^y errs by y's rounding (|y| u), the exponential (4 u), and the changes of `top` after it: 60 u for
+    the products of ten of them, 40 u for their exponents, whose sum is the lane's range of y."""
+    rows = 8 * torch.cuda.get_device_properties(0).multi_processor_count + 3 if many else 3
+    x = normal(torch, (rows, n), 5, 2.5) + offset
+    tgt = torch.arange(rows, device="cuda", dtype=torch.int32) % n
+    logp, ent, _, _, _ = ito.ito_token_logprobs_fwd(x, tgt)
+    X = f64(x)
+    d = X - X.max(1, keepdims=True)
+    s = np.exp(d).sum(1, keepdims=True)
+    p, lp = np.exp(d) / s, d - np.log(s)
+    y = np.abs(d) / math.log(2)
+    rho = (n / 64 + 10 + y + 4 + 60 + 40) * U
+    e_s, mean = (p * rho).sum(1), (p * -d).sum(1)
+    want = -(p * lp).sum(1)
+    within(ent, want, e_s + math.log(2) * (p * y * (rho + U)).sum(1) + mean * e_s + 8 * U * (1 + want + mean), "entropy")
+    at = np.arange(rows) % n
+    dt_, lt = np.abs(d[np.arange(rows), at]), lp[np.arange(rows), at]
+    within(logp, lt, e_s + U * (2 * dt_ + 4) + 4 * U * (np.log(s[:, 0]) + np.abs(lt)), "logp")
