@@ -83,11 +83,16 @@ __device__ __forceinline__ float2 act_slope(float2 z)
         return __ffma2_rn(__fmul2_rn(z, bell), splat(0.39894228040143268f), cdf);
     }
     if (ACT == ITO_ACT_GELU_TANH || ACT == ITO_ACT_SILU) {
-        // q + z u' q (1 - q) with q = logistic(u)
+        // q + z u' q (1 - q) with q = logistic(u). From |z| = 11 on q (1 - q) is 0 in the approximate
+        // GELU, and z u' is taken at +-16 at most: a cube, it would be infinite from 1e13 on.
         const float2 z2 = __fmul2_rn(z, z);
         const bool silu = ACT == ITO_ACT_SILU;
         const float2 q = logistic(silu ? z : __fmul2_rn(z, gelu_tanh_factor(z2)));
-        const float2 zu = silu ? z : __fmul2_rn(z, __ffma2_rn(z2, splat(0.21406444881780075f), splat(1.5957691216057308f)));
+        float2 zu = z;
+        if (!silu) {
+            const float2 c = make_float2(fminf(fmaxf(z.x, -16.0f), 16.0f), fminf(fmaxf(z.y, -16.0f), 16.0f));
+            zu = __fmul2_rn(c, __ffma2_rn(__fmul2_rn(c, c), splat(0.21406444881780075f), splat(1.5957691216057308f)));
+        }
         return __ffma2_rn(zu, __fmul2_rn(q, __ffma2_rn(q, splat(-1.0f), splat(1.0f))), q);
     }
     return splat(1.0f);

@@ -99,3 +99,34 @@ def test_logprobs_of_rows_far_from_zero(torch, ito, n, many, offset):
     at = np.arange(rows) % n
     dt_, lt = np.abs(d[np.arange(rows), at]), lp[np.arange(rows), at]
     within(logp, lt, e_s + U * (2 * dt_ + 4) + 4 * U * (np.log(s[:, 0]) + np.abs(lt)), "logp")
+
+
+# ------------------------------------------------------------------ linear
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("B", [1, 200])
+def test_activations_of_large_finite_values(torch, ito, act, dtype, B):
+    """From |z| = 16 on an activation is z or 0 and its slope 1 or 0, to far below a unit, up to the type's largest
+    value; below, the slope's 32-bit evaluation errs by 16 u (1 + |z|) and the activation's by 8 u (1 + |z|)."""
+    big = [12.0, 60.0, 1000.0, 65504.0] + [10.0 ** k for k in (10, 13, 13.5, 14, 16, 19, 20, 30, 38)] * (dtype == "bfloat16")
+    z = torch.tensor([s * v for v in [0.0, 0.5, 3.0] + big for s in (1, -1)], device="cuda").to(dt(torch, dtype))
+    n = z.numel()
+    Z = f64(z)
+    with np.errstate(over="ignore"):
+        slope = slope64(act, Z)
+    near = np.minimum(np.abs(Z), 16)
+    x, W = torch.zeros((B, 8), dtype=z.dtype, device="cuda"), torch.zeros((n, 8), dtype=z.dtype, device="cuda")
+    dy = torch.zeros((B, n), dtype=z.dtype, device="cuda")
+    dy[B - 1] = 1.0
+    _, _, db = ito.ito_fp_linear_bwd(dy, x, W, z=z.expand(B, n).contiguous(), act=act)
+    within(db, slope, 16 * U * (1 + near), "slope")
+    y = ito.ito_fp_linear_fwd(x, W, bias=z, act=act, out_dtype=torch.float32)
+    want = np.where(np.abs(Z) > 16, np.maximum(Z, 0), Z * slope) if act == "relu" else None
+    if want is None:
+        cdf = {"gelu": lambda v: 0.5 * math.erfc(-v / math.sqrt(2)),
+               "gelu_tanh": lambda v: 0.5 * (1 + math.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3))),
+               "silu": lambda v: 1 / (1 + math.exp(-v))}[act]
+        want = np.array([max(v, 0.0) if abs(v) > 60 else v * cdf(v) for v in Z])
+    tol = 8 * U * (1 + np.where(Z > 0, Z, near))
+    within(y, np.broadcast_to(want, (B, n)), np.broadcast_to(tol, (B, n)), "activation")
