@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             entry = next_entry(tab, entry, c);
             const AdamEntry& e = tab.e[entry];
             const int64_t base = (int64_t)(c - e.first_chunk) * kRingChunk;
-            if (!mbar_wait(&empty[stage], phase ^ 1, &abort_flag, err)) return;
+            if (!mbar_wait(&empty[stage], phase ^ 1, &abort_flag, err)) break;
             uint8_t* p = smem + stage * Cfg::BYTES;
             mbar_arrive_expect_tx(&full[stage], Cfg::BYTES);
             bulk_load(p, e.w + base, kRingChunk * 4, &full[stage]);
@@ -409,6 +409,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             bulk_load(p + Cfg::V_AT, static_cast<const uint8_t*>(e.v) + base, kRingChunk, &full[stage]);
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
+        // (the teams may have given up: the block stays until every copy has landed)
+        ring_landed(full, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
         return;
     }
     const int team = warp / kRingWarps, half = lane >> 4, hl = lane & 15;

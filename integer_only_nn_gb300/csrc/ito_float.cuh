@@ -200,6 +200,34 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
         : "memory");
 }
 
+// A place in a ring of `stages` buffers, each with an mbarrier on which its copies complete, and the
+// parity of that barrier's phase for the copy at this place.
+struct RingPlace {
+    int stage;
+    uint32_t phase;
+
+    __host__ __device__ __forceinline__ void next(int stages)
+    {
+        if (++stage < stages) return;
+        stage = 0;
+        phase ^= 1;
+    }
+    // One lap back: where a producer whose next copy would go here began its last `stages` copies. (A
+    // stage that has had none counts as landed: the phase before a barrier's first is a completed one.)
+    __host__ __device__ __forceinline__ RingPlace lap_before() const { return RingPlace{stage, phase ^ 1}; }
+};
+
+// Waits, by one thread, until the `copies` copies from `at` on have landed. A block whose waits ran out
+// must not leave before: its shared memory would be another's while copies still write to it. All of them
+// within the limit of one wait; nothing more can be done for what has not come by then.
+static __device__ __noinline__ void ring_landed(uint64_t* full, int stages, RingPlace at, int copies)
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < copies; ++i, at.next(stages))
+        while (!mbar_try_wait(&full[at.stage], at.phase))
+            if (globaltimer_ns() - t0 > kWaitTimeoutNs) return;
+}
+
 inline int launch_status(const char* what)
 {
     const cudaError_t e = cudaGetLastError();
