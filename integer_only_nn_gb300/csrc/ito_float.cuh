@@ -220,7 +220,7 @@ struct RingPlace {
 // Waits, by one thread, until the `copies` copies from `at` on have landed. A block whose waits ran out
 // must not leave before: its shared memory would be another's while copies still write to it. All of them
 // within the limit of one wait; nothing more can be done for what has not come by then.
-static __device__ __noinline__ void ring_landed(uint64_t* full, int stages, RingPlace at, int copies)
+inline __device__ __noinline__ void ring_landed(uint64_t* full, int stages, RingPlace at, int copies)
 {
     const uint64_t t0 = globaltimer_ns();
     for (int i = 0; i < copies; ++i, at.next(stages))

@@ -478,12 +478,22 @@ __global__ void __launch_bounds__(256)
 // conversions and five or six packed operations remain; with one element to an instruction
 // (26 of them) the forward pass took 45 us at 8192 x 4096 bf16, bound by issue.
 //
-// A wait that runs out (mbar_wait) leaves a wrong result and ITO_ERR_TIMEOUT; later waits
-// return at once, and every thread still passes every barrier.
+// A wait that runs out (mbar_wait) leaves a wrong result and ITO_ERR_TIMEOUT: later waits return at
+// once, every thread still passes every barrier, and the one that asks for copies asks for no more
+// and leaves when those under way have landed.
 struct LnRing {
     int stages;
     uint32_t row_bytes;
 };
+
+// After the last group: the thread that asked for copies gave up at the group `lost`, with a ring's
+// worth from that one on under way (as far as there were groups).
+__device__ __forceinline__ void ln_unwind(const LnRing& ring, uint64_t* full, int64_t lost, int64_t groups)
+{
+    const int64_t turn = (lost - blockIdx.x) / gridDim.x, left = (groups - 1 - lost) / gridDim.x + 1;
+    ring_landed(full, ring.stages, RingPlace{(int)(turn % ring.stages), (uint32_t)(turn / ring.stages & 1)},
+                (int)min((int64_t)ring.stages, left));
+}
 
 // Blocks of up to 256 threads: three to an SM forward (8192 x 4096 bf16: 25.6 us, 28.6 with four),
 // two backward (43 us, 51 with three, whose registers spill).
@@ -507,10 +517,12 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
     __shared__ float red[2][R * 32];
     __shared__ uint64_t full[16];
     __shared__ int abort_flag;
+    __shared__ int64_t lost;
     const int at = threadIdx.x, tpr = blockDim.x;
     if (at == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(&full[s], 1);
         abort_flag = 0;
+        lost = -1;
         fence_mbar_init();
     }
     __syncthreads();
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-        mbar_wait(&full[stage], phase, &abort_flag, err);
+        if (!mbar_wait(&full[stage], phase, &abort_flag, err) && at == 0 && lost < 0) lost = grp;
         float f[R][VPT][PER], mu[R], rs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
             mu[r] = s.x + s.y;
         }
         row_sums<R>(mu, tpr, red[0]);
-        if (at == 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
+        if (at == 0 && lost < 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mu[r] *= inv;
@@ -615,6 +627,7 @@ __global__ void __launch_bounds__(ln_ring_threads(VPT, TIGHT), TIGHT ? kLnTight 
         }
         if (++stage == ring.stages) { stage = 0; phase ^= 1; }
     }
+    if (at == 0 && lost >= 0) ln_unwind(ring, full, lost, groups);
 }
 
 template <typename T, int VPT, int R>
@@ -629,10 +642,12 @@ __global__ void __launch_bounds__(512)
     __shared__ float red[2][2 * R * 32];
     __shared__ uint64_t full[16];
     __shared__ int abort_flag;
+    __shared__ int64_t lost;
     const int at = threadIdx.x, tpr = blockDim.x;
     if (at == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(&full[s], 1);
         abort_flag = 0;
+        lost = -1;
         fence_mbar_init();
     }
     __syncthreads();
@@ -671,7 +686,7 @@ __global__ void __launch_bounds__(512)
             mu[r] = in ? mean[grp * R + r] : 0.0f;
             rs[r] = in ? rstd[grp * R + r] : 0.0f;
         }
-        mbar_wait(&full[stage], phase, &abort_flag, err);
+        if (!mbar_wait(&full[stage], phase, &abort_flag, err) && at == 0 && lost < 0) lost = grp;
         Vec<T> vd[R][VPT], vx[R][VPT];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -714,7 +729,7 @@ __global__ void __launch_bounds__(512)
             s[2 * r + 1] = sh.x + sh.y;
         }
         row_sums<2 * R>(s, tpr, red[bank]);
-        if (at == 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
+        if (at == 0 && lost < 0) fill(grp + (int64_t)ring.stages * gridDim.x, stage);
         if (++stage == ring.stages) { stage = 0; phase ^= 1; }
         if (!dx) continue;
 #pragma unroll
@@ -744,6 +759,7 @@ __global__ void __launch_bounds__(512)
             }
         }
     }
+    if (at == 0 && lost >= 0) ln_unwind(ring, full, lost, groups);
     if (!part) return;
     float* pg = part + (int64_t)blockIdx.x * 2 * cols;
 #pragma unroll

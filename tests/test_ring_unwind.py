@@ -83,11 +83,11 @@ def kernels(name):
     return bodies
 
 
-@pytest.mark.parametrize("name", ["ito_adamw.cu"])
+@pytest.mark.parametrize("name", ["ito_adamw.cu", "ito_layer_norm.cu"])
 def test_kernels_that_copy_wait_for_their_copies(name):
     found = 0
     for kernel, body in kernels(name).items():
         if "bulk_load(" in body or "tma_load_2d" in body:
-            assert "ring_landed(" in body, kernel
+            assert "ring_landed(" in body or "ln_unwind(" in body, kernel
             found += 1
     assert found
