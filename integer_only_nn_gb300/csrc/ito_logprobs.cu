@@ -529,7 +529,8 @@ __device__ __forceinline__ void write_row(const T* row, const int32_t* targets, 
 // A block is of few warps with alternatives, so that an SM holds 28 at 72 registers (32 at 64
 // spill: 73 us), else of 8 with 32 to an SM. Either way shared memory or registers let no SM take
 // more blocks than its share of the grid, while the previous launch's end: 75 us where they did.
-// A wait that runs out (mbar_wait) leaves a wrong result and ITO_ERR_TIMEOUT.
+// After a wait that runs out (mbar_wait, ITO_ERR_TIMEOUT) a warp writes no more rows and leaves when its
+// copies under way have landed.
 constexpr int ring_warps(bool top) { return top ? 4 : 8; }         // of a block
 constexpr int ring_blocks(bool top) { return top ? 7 : 4; }        // of an SM
 constexpr int kLpSlots = 3, kLpRound = 32 * kLpUnroll * 16;      // bytes of a round
@@ -587,7 +588,10 @@ __global__ void __launch_bounds__(ring_warps(TOP) * 32, ring_blocks(TOP))
         sums.clear();
         const int lead = elements_before<T>(row), end = classes + lead;
         for (int base = 0; base < end; base += EACH) {
-            mbar_wait(&full[warp][slot], phase, &abort_flag, err);
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][slot], phase, &abort_flag, err))) {
+                if (lane == 0) ring_landed(full[warp], kLpSlots, RingPlace{slot, phase}, kLpSlots);
+                return;
+            }
             uint8_t* const at = ring + slot * kLpRound;
             Vec<T> v[kLpUnroll];
             float m[kLpUnroll];

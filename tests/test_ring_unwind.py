@@ -83,7 +83,7 @@ def kernels(name):
     return bodies
 
 
-@pytest.mark.parametrize("name", ["ito_adamw.cu", "ito_layer_norm.cu"])
+@pytest.mark.parametrize("name", ["ito_adamw.cu", "ito_layer_norm.cu", "ito_logprobs.cu"])
 def test_kernels_that_copy_wait_for_their_copies(name):
     found = 0
     for kernel, body in kernels(name).items():
