@@ -64,7 +64,11 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-// all lanes wait; whether it came, for all of them alike
+// All lanes wait; whether it came, for all of them alike. Where a wait has run out, in these warps or
+// another, the loops end early; then as otherwise the producer stays until its copies have landed
+// (ring_landed) and the issuer until the products that free the stages are done, so that no block
+// gives its shared or tensor memory back while they are in use. (Of a pair the leader's barrier counts both blocks'
+// copies, and the pair leaves together.)
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err)
 {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
@@ -472,6 +476,7 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
                 if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
         }
+        if (lane == 0) ring_landed(full_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
     } else if (warp == 1) {
         int stage = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 0;
@@ -499,6 +504,7 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
             }
             if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
+        if (lane == 0) ring_landed(empty_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
     } else {
         const int e = warp - 2, quad = warp & 3, part = e >> 2;
         FpStage st{staging + e * kFpBoxes * kFpBox, lane, 0};
@@ -689,6 +695,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                 if (PROBLEMS == 1 || problem == 0) load(work.p[0]);
                 else load(work.p[LAST]);
             }
+            if (leader && lane == 0) ring_landed(full_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
         }
     } else if (warp == 1) {
         if (leader) {
@@ -720,6 +727,7 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                 }
                 if (++buf == 2) { buf = 0; buf_phase ^= 1; }
             }
+            if (lane == 0) ring_landed(empty_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
         }
     } else {
         // both CTAs: this CTA's 128 rows of the pair's tile, two warps to 32 of them

@@ -83,11 +83,13 @@ def kernels(name):
     return bodies
 
 
-@pytest.mark.parametrize("name", ["ito_adamw.cu", "ito_layer_norm.cu", "ito_logprobs.cu"])
+@pytest.mark.parametrize("name", ["ito_adamw.cu", "ito_layer_norm.cu", "ito_logprobs.cu", "ito_fp_gemm.cu"])
 def test_kernels_that_copy_wait_for_their_copies(name):
     found = 0
     for kernel, body in kernels(name).items():
         if "bulk_load(" in body or "tma_load_2d" in body:
             assert "ring_landed(" in body or "ln_unwind(" in body, kernel
+            if "tc_commit" in body:      # the products that read the stages as well
+                assert "ring_landed(full_bar" in body and "ring_landed(empty_bar" in body, kernel
             found += 1
     assert found
