@@ -803,23 +803,26 @@ def _from_ptr(ptr, n, dtype, eb):
 # ---------------------------------------------------------- float operators
 #
 # Checks and marshalling here are on the path of calls whose kernels take 2 to 10 us, so they
-# stay few: one look at each tensor, one allocation for each result.
+# stay few: one look at each tensor, one allocation for each result. All tensors of a call are on the
+# current device.
 
 _ACTS = {"none": ITO_ACT_NONE, "relu": ITO_ACT_RELU, "gelu": ITO_ACT_GELU, "gelu_tanh": ITO_ACT_GELU_TANH,
          "silu": ITO_ACT_SILU}
 _TYPE_IDS = {}          # torch dtype -> ito_type
 _F32 = None             # torch.float32, once torch is there
 _raw_stream_of = None   # device index -> the current stream's handle
+_current_device = None  # -> the current device's index
 
 
 def _float_setup():
     """torch, and what this part needs of it."""
-    global _F32, _raw_stream_of
+    global _F32, _raw_stream_of, _current_device
     import torch
     _TYPE_IDS.update({torch.float32: ITO_F32, torch.bfloat16: ITO_BF16, torch.float16: ITO_F16})
     # (torch.cuda.current_stream() makes an object, which takes as long as a small kernel's launch)
     _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _F32 = torch.float32
     return torch
 
@@ -839,17 +842,32 @@ def _act_id(act):
     return r
 
 
-def _matrix(t, name, rows, cols, dtype):
-    """Checks a 2-D device tensor whose rows' elements are consecutive (rows, cols, dtype: None
-    for any); -> its row stride."""
+def _device_index(t, name):
+    """The device that a call runs on: that of its first tensor, which has to be the current one (the
+    library launches there)."""
+    index = t.get_device()
+    if index < 0:
+        raise ItoError(ITO_ERR_ARG, "%s: not on the GPU" % name)
+    if index != _current_device():
+        raise ItoError(ITO_ERR_ARG, "%s: on device %d, the current one is %d" % (name, index, _current_device()))
+    return index
+
+
+def _elsewhere(t, name, index):
+    raise ItoError(ITO_ERR_ARG, "%s: on %s, expected cuda:%d" % (name, t.device, index))
+
+
+def _matrix(t, name, rows, cols, dtype, index):
+    """Checks a 2-D tensor on the device `index` whose rows' elements are consecutive (rows, cols,
+    dtype: None for any); -> its row stride."""
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%s][%s]" % (
             name, list(shape), "rows" if rows is None else rows, "columns" if cols is None else cols))
     if not shape[0] or not shape[1]:
         raise ItoError(ITO_ERR_SHAPE, "%s: no elements" % name)
-    if not t.is_cuda:
-        raise ItoError(ITO_ERR_ARG, "%s: not on the GPU" % name)
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
     if dtype is not None and t.dtype is not dtype:
         raise ItoError(ITO_ERR_ARG, "%s: type %s, expected %s" % (name, t.dtype, dtype))
     s0, s1 = t.stride()
@@ -858,15 +876,17 @@ def _matrix(t, name, rows, cols, dtype):
     return s0
 
 
-def _vector(t, name, n, dtype, other=None):
-    """Checks a dense 1-D device tensor of one of two types (None passes); -> its address."""
+def _vector(t, name, n, index, dtype, other=None):
+    """Checks a dense 1-D tensor on the device `index` of one of two types (None passes); -> its address."""
     if t is None:
         return None
     shape = t.shape
     if len(shape) != 1 or shape[0] != n:
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%d]" % (name, list(shape), n))
-    if not t.is_cuda or (t.dtype is not dtype and t.dtype is not other):
-        raise ItoError(ITO_ERR_ARG, "%s: %s on %s" % (name, t.dtype, t.device))
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    if t.dtype is not dtype and t.dtype is not other:
+        raise ItoError(ITO_ERR_ARG, "%s: type %s" % (name, t.dtype))
     if n > 1 and t.stride(0) != 1:
         raise ItoError(ITO_ERR_ARG, "%s: not contiguous" % name)
     return t.data_ptr()
@@ -912,18 +932,18 @@ def ito_fp_linear_fwd(x, W, bias=None, act="none", residual=None, save_z=False, 
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_fp_linear_fwd(x, W, bias, act, residual, save_z, out_dtype), stream)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", None, None, None)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
     B, IC = x.shape
-    ldw = _matrix(W, "W", None, IC, dtype)
+    ldw = _matrix(W, "W", None, IC, dtype, index)
     OC = W.shape[0]
     ty = _type_id(dtype, "x")
     out = dtype if out_dtype is None else out_dtype
-    pb = _vector(bias, "bias", OC, dtype, _F32)
-    pr, ldr = (None, 0) if residual is None else (residual.data_ptr(), _matrix(residual, "residual", B, OC, out))
+    pb = _vector(bias, "bias", OC, index, dtype, _F32)
+    pr, ldr = (None, 0) if residual is None else (residual.data_ptr(), _matrix(residual, "residual", B, OC, out, index))
     y = torch.empty((B, OC), dtype=out, device=dev)
     z = torch.empty((B, OC), dtype=dtype, device=dev) if save_z else None
-    s = _raw_stream_of(dev.index)
+    s = _raw_stream_of(index)
     px, pw = x.data_ptr(), W.data_ptr()
     ws, hold = None, None
     n = _lib.ito_fp_linear_fwd_workspace_size(px, ldx, pw, ldw, B, IC, OC)
@@ -944,20 +964,20 @@ def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, 
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_fp_linear_bwd(dy, x, W, z, act, need_dx, need_dw, need_dbias, dw_dtype), stream)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", None, None, None)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
     B, IC = x.shape
-    ldw = _matrix(W, "W", None, IC, dtype)
+    ldw = _matrix(W, "W", None, IC, dtype, index)
     OC = W.shape[0]
-    lddy = _matrix(dy, "dy", B, OC, dtype)
-    pz, ldz = (None, 0) if z is None else (z.data_ptr(), _matrix(z, "z", B, OC, dtype))
+    lddy = _matrix(dy, "dy", B, OC, dtype, index)
+    pz, ldz = (None, 0) if z is None else (z.data_ptr(), _matrix(z, "z", B, OC, dtype, index))
     ty = _type_id(dtype, "x")
     a = _act_id(act)
     dwt = dtype if dw_dtype is None else dw_dtype
     dx = torch.empty((B, IC), dtype=dtype, device=dev) if need_dx else None
     dw = torch.empty((OC, IC), dtype=dwt, device=dev) if need_dw else None
     db = torch.empty(OC, dtype=_F32, device=dev) if need_dbias else None
-    s = _raw_stream_of(dev.index)
+    s = _raw_stream_of(index)
     pd, px, pw = dy.data_ptr(), x.data_ptr(), W.data_ptr()
     ws, hold = None, None
     n = _lib.ito_fp_linear_bwd_workspace_size(pd, lddy, px, ldx, pw, ldw, a, B, IC, OC)
@@ -976,10 +996,10 @@ def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", None, None, None)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
     rows, cols = x.shape
-    pg, pb = _vector(gamma, "gamma", cols, dtype, _F32), _vector(beta, "beta", cols, dtype, _F32)
+    pg, pb = _vector(gamma, "gamma", cols, index, dtype, _F32), _vector(beta, "beta", cols, index, dtype, _F32)
     if pg is not None and pb is not None and gamma.dtype is not beta.dtype:
         raise ItoError(ITO_ERR_ARG, "gamma and beta of one type")
     w = gamma if gamma is not None else beta
@@ -988,7 +1008,7 @@ def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     mean = torch.empty(rows, dtype=_F32, device=dev)
     rstd = torch.empty_like(mean)
     r = _lib.ito_layer_norm_fwd(x.data_ptr(), ldx, ty, pg, pb, ITO_F32 if w is None else _TYPE_IDS[w.dtype], rows, cols,
-                                eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), _raw_stream_of(dev.index))
+                                eps, y.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(), _raw_stream_of(index))
     if r:
         _check(r)
     return y, mean, rstd
@@ -999,15 +1019,15 @@ def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, str
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream)
-    dtype, dev = x.dtype, x.device
-    ldx = _matrix(x, "x", None, None, None)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
     rows, cols = x.shape
-    lddy = _matrix(dy, "dy", rows, cols, dtype)
-    pg = _vector(gamma, "gamma", cols, dtype, _F32)
-    pm, ps = _vector(mean, "mean", rows, _F32), _vector(rstd, "rstd", rows, _F32)
+    lddy = _matrix(dy, "dy", rows, cols, dtype, index)
+    pg = _vector(gamma, "gamma", cols, index, dtype, _F32)
+    pm, ps = _vector(mean, "mean", rows, index, _F32), _vector(rstd, "rstd", rows, index, _F32)
     ty = _type_id(dtype, "x")
     dx = torch.empty((rows, cols), dtype=dtype, device=dev) if need_dx else None
-    s = _raw_stream_of(dev.index)
+    s = _raw_stream_of(index)
     dg = db = ws = hold = None
     n = 0
     if need_dw:
@@ -1030,10 +1050,10 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream)
-    dev = logits.device
-    ld = _matrix(logits, "logits", None, None, None)
+    dev, index = logits.device, _device_index(logits, "logits")
+    ld = _matrix(logits, "logits", None, None, None, index)
     rows, classes = logits.shape
-    pt = _vector(targets, "targets", rows, torch.int32)
+    pt = _vector(targets, "targets", rows, index, torch.int32)
     ty = _type_id(logits.dtype, "logits")
     entropy = torch.empty(rows, dtype=_F32, device=dev)
     lse = torch.empty_like(entropy)
@@ -1042,7 +1062,7 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     ids = torch.empty((rows, k), dtype=torch.int32, device=dev)
     r = _lib.ito_token_logprobs_fwd(logits.data_ptr(), ld, ty, pt, rows, classes, k,
                                     None if pt is None else logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
-                                    ids.data_ptr(), top.data_ptr(), _raw_stream_of(dev.index))
+                                    ids.data_ptr(), top.data_ptr(), _raw_stream_of(index))
     if r:
         _check(r)
     return logp, entropy, lse, ids, top
@@ -1053,17 +1073,17 @@ def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream)
-    dtype, dev = logits.dtype, logits.device
-    ld = _matrix(logits, "logits", None, None, None)
+    dtype, dev, index = logits.dtype, logits.device, _device_index(logits, "logits")
+    ld = _matrix(logits, "logits", None, None, None, index)
     rows, classes = logits.shape
-    pt = _vector(targets, "targets", rows, torch.int32)
-    pl, pe = _vector(lse, "lse", rows, _F32), _vector(entropy, "entropy", rows, _F32)
-    pg, ph = _vector(g_logp, "g_logp", rows, _F32), _vector(g_entropy, "g_entropy", rows, _F32)
+    pt = _vector(targets, "targets", rows, index, torch.int32)
+    pl, pe = _vector(lse, "lse", rows, index, _F32), _vector(entropy, "entropy", rows, index, _F32)
+    pg, ph = _vector(g_logp, "g_logp", rows, index, _F32), _vector(g_entropy, "g_entropy", rows, index, _F32)
     ty = _type_id(dtype, "logits")
     d = torch.empty((rows, classes), dtype=dtype, device=dev) if out is None else out
-    ldd = classes if out is None else _matrix(d, "out", rows, classes, dtype)
+    ldd = classes if out is None else _matrix(d, "out", rows, classes, dtype, index)
     r = _lib.ito_token_logprobs_bwd(logits.data_ptr(), ld, ty, pt, pl, pe, rows, classes, pg, ph, d.data_ptr(), ldd,
-                                    _raw_stream_of(dev.index))
+                                    _raw_stream_of(index))
     if r:
         _check(r)
     return d
@@ -1092,6 +1112,7 @@ class AdamW:
         sizes = [w.numel() for w in self.weights]
         blocks = [(n + 127) // 128 for n in sizes]
         dev = self.weights[0].device
+        index = _device_index(self.weights[0], "weights[0]")
         if states is None:
             if bits == 32:
                 states = [[torch.zeros(n, dtype=torch.float32, device=dev) for n in sizes] for _ in range(2)]
@@ -1113,7 +1134,7 @@ class AdamW:
         for ts, dtype, lengths, name in groups:
             if len(ts) != len(sizes):
                 raise ItoError(ITO_ERR_SHAPE, "%s: %d tensors, expected %d" % (name, len(ts), len(sizes)))
-            self._dense(ts, dtype, lengths, name)
+            self._dense(ts, dtype, lengths, name, index)
         if len(decays) != len(sizes):
             raise ItoError(ITO_ERR_SHAPE, "weight_decay: %d values, expected %d" % (len(decays), len(sizes)))
         self._copy_type = ITO_BF16 if self.copies is None else _type_id(self.copies[0].dtype, "copies")
@@ -1130,25 +1151,26 @@ class AdamW:
         tab["weight_decay"] = decays
 
     @staticmethod
-    def _dense(ts, dtype, lengths, name):
+    def _dense(ts, dtype, lengths, name, index):
         for i, (t, n) in enumerate(zip(ts, lengths)):
             if t.numel() != n:
                 raise ItoError(ITO_ERR_SHAPE, "%s[%d]: %d elements, expected %d" % (name, i, t.numel(), n))
-            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-                raise ItoError(ITO_ERR_ARG, "%s[%d]: a dense %s tensor on the GPU is expected" % (name, i, dtype))
+            if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+                raise ItoError(ITO_ERR_ARG, "%s[%d]: a dense %s tensor on cuda:%d is expected" % (name, i, dtype, index))
 
     def step(self, grads, lr, grad_scale=1.0, stream=None):
         """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16)."""
         if len(grads) != self._n:
             raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
+        index = _device_index(self.weights[0], "weights[0]")
         dtype = grads[0].dtype
         for g, n in zip(grads, self._sizes):
-            if g.numel() != n or g.dtype != dtype or not g.is_cuda or not g.is_contiguous():
-                self._dense(grads, dtype, self._sizes, "grads")     # says which and why
+            if g.numel() != n or g.dtype != dtype or g.get_device() != index or not g.is_contiguous():
+                self._dense(grads, dtype, self._sizes, "grads", index)     # says which and why
         self._fields["g"] = [g.data_ptr() for g in grads]
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
                         _type_id(dtype, "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
-        s = _raw_stream_of(self.weights[0].device.index) if stream is None else stream.cuda_stream
+        s = _raw_stream_of(index) if stream is None else stream.cuda_stream
         _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), s))
         self.steps += 1
 
@@ -1161,9 +1183,9 @@ class AdamW:
         if self.bits == 32:
             return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)
         dtype = dtype or torch.bfloat16
-        dev = self.weights[0].device
+        dev, index = self.weights[0].device, _device_index(self.weights[0], "weights[0]")
         m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
         if self.total:
             _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(dtype, "dtype"), m.data_ptr(), v.data_ptr(),
-                                          _raw_stream_of(dev.index)))
+                                          _raw_stream_of(index)))
         return m, v

@@ -1,0 +1,112 @@
+"""The float operators' wrappers refuse tensors that are not on the current device, or not all on one
+(stand-ins for tensors: no GPU needed)."""
+import pytest
+from test_abi import _lib_path
+
+
+class Stand:
+    """What the wrappers look at before a launch."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index=0):
+        self.shape, self.dtype, self.index = shape, dtype, index
+        self.device = "cuda:%d" % index
+
+    def get_device(self):
+        return self.index
+
+    def stride(self, dim=None):
+        s = [1] * len(self.shape)
+        for i in range(len(s) - 2, -1, -1):
+            s[i] = s[i + 1] * self.shape[i + 1]
+        return tuple(s) if dim is None else s[dim]
+
+    def numel(self):
+        n = 1
+        for k in self.shape:
+            n *= k
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.fixture
+def ito(monkeypatch):
+    torch = pytest.importorskip("torch")
+    _lib_path()
+    import integer_only_nn_gb300 as m
+    m._float_setup()
+    monkeypatch.setattr(m, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(m, "_float_setup", lambda: torch)
+
+    def no_more(*a, **kw):
+        raise AssertionError("the call went past its checks")
+
+    monkeypatch.setattr(torch, "empty", no_more)
+    return m
+
+
+def calls(ito):
+    """Each wrapper with the names of its tensors, and a call with any of them on another device."""
+    import torch
+    h, f, i32 = torch.bfloat16, torch.float32, torch.int32
+    spec = {
+        "linear_fwd": (dict(x=((4, 16), h), W=((8, 16), h), bias=((8,), h), residual=((4, 8), h)),
+                       lambda t: ito.ito_fp_linear_fwd(t["x"], t["W"], bias=t["bias"], residual=t["residual"])),
+        "linear_bwd": (dict(x=((4, 16), h), dy=((4, 8), h), W=((8, 16), h), z=((4, 8), h)),
+                       lambda t: ito.ito_fp_linear_bwd(t["dy"], t["x"], t["W"], z=t["z"], act="gelu")),
+        "layer_norm_fwd": (dict(x=((4, 16), h), gamma=((16,), f), beta=((16,), f)),
+                           lambda t: ito.ito_layer_norm_fwd(t["x"], t["gamma"], t["beta"])),
+        "layer_norm_bwd": (dict(x=((4, 16), h), dy=((4, 16), h), gamma=((16,), f), mean=((4,), f), rstd=((4,), f)),
+                           lambda t: ito.ito_layer_norm_bwd(t["dy"], t["x"], t["gamma"], t["mean"], t["rstd"])),
+        "logprobs_fwd": (dict(logits=((4, 16), h), targets=((4,), i32)),
+                         lambda t: ito.ito_token_logprobs_fwd(t["logits"], t["targets"])),
+        "logprobs_bwd": (dict(logits=((4, 16), h), targets=((4,), i32), lse=((4,), f), entropy=((4,), f), g_logp=((4,), f),
+                              g_entropy=((4,), f), out=((4, 16), h)),
+                         lambda t: ito.ito_token_logprobs_bwd(t["logits"], t["targets"], t["lse"], t["entropy"], t["g_logp"],
+                                                              t["g_entropy"], out=t["out"])),
+        "adamw": (dict(w=((10,), f), copy=((10,), h), m=((10,), f), v=((10,), f)),
+                  lambda t: ito.AdamW([t["w"]], copies=[t["copy"]], states=[[t["m"]], [t["v"]]])),
+    }
+    return spec
+
+
+NAMES = ["linear_fwd", "linear_bwd", "layer_norm_fwd", "layer_norm_bwd", "logprobs_fwd", "logprobs_bwd", "adamw"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_every_tensor_on_one_device(ito, name):
+    tensors, call = calls(ito)[name]
+    for other in tensors:
+        for index in (1, -1):
+            t = {k: Stand(shape, dtype, index if k == other else 0) for k, (shape, dtype) in tensors.items()}
+            with pytest.raises(ito.ItoError) as e:
+                call(t)
+            assert e.value.code == ito.ITO_ERR_ARG, other
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_current_device(ito, name):
+    """All tensors on one device which is not the current one."""
+    tensors, call = calls(ito)[name]
+    with pytest.raises(ito.ItoError) as e:
+        call({k: Stand(shape, dtype, 1) for k, (shape, dtype) in tensors.items()})
+    assert e.value.code == ito.ITO_ERR_ARG and "current" in str(e.value)
+
+
+def test_a_step_on_one_device(ito):
+    import torch
+    opt = ito.AdamW([Stand((10,), torch.float32) for _ in range(2)],
+                    states=[[Stand((10,), torch.float32) for _ in range(2)] for _ in range(2)])
+    with pytest.raises(ito.ItoError) as e:
+        opt.step([Stand((10,), torch.bfloat16), Stand((10,), torch.bfloat16, 1)], lr=0.1)
+    assert e.value.code == ito.ITO_ERR_ARG
+    opt.weights[0].index = 1
+    with pytest.raises(ito.ItoError) as e:
+        opt.step([Stand((10,), torch.bfloat16) for _ in range(2)], lr=0.1)
+    assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
