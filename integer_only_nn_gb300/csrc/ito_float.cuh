@@ -2,6 +2,7 @@
 // beside the integer layers): element types, conversions, vector loads and block sums.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include <cuda_fp16.h>
@@ -227,6 +228,22 @@ inline __device__ __noinline__ void ring_landed(uint64_t* full, int stages, Ring
         while (!mbar_try_wait(&full[at.stage], at.phase))
             if (globaltimer_ns() - t0 > kWaitTimeoutNs) return;
 }
+
+// What has to be done once on each device (a kernel's attributes belong to the function on one device).
+// Host threads that meet here may both do it. `call` returns a cudaError_t.
+struct OnEachDevice {
+    std::atomic<uint64_t> done{0};
+
+    template <typename Call>
+    cudaError_t run(int device, Call call)
+    {
+        const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;     // (0: every time)
+        if (done.load() & bit) return cudaSuccess;
+        const cudaError_t e = call();
+        if (e == cudaSuccess) done.fetch_or(bit);
+        return e;
+    }
+};
 
 inline int launch_status(const char* what)
 {

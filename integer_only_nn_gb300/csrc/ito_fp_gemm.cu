@@ -869,23 +869,25 @@ static bool rows_aligned(const void* p, int64_t ld, int size, int64_t rows)
     return aligned_to(p, 16) && (ld * size) % 16 == 0 && ld > 0 && (rows == 1 || ld * size < (int64_t(1) << 40));
 }
 
+// `kern` may have `bytes` of shared memory on the current device.
 template <typename K>
-static cudaError_t allow_smem(K kern, int bytes, bool* done)
+static cudaError_t allow_smem(K kern, int bytes, OnEachDevice* set)
 {
-    if (*done) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    *done = e == cudaSuccess;
-    return e;
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return set->run(device, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
+// Pairs that run at the same time: a figure of the kernel and this part, the same on each device of it.
 template <int PROBLEMS>
 static int max_pairs()
 {
-    static int n = 0;
-    static bool ready = false;
-    if (n) return n;
+    static std::atomic<int> most{0};
+    static OnEachDevice ready;
     const auto kern = k_fp_gemm_pair<PROBLEMS>;
     if (allow_smem(kern, FpPairCfg::SMEM_BYTES, &ready) != cudaSuccess) return 0;
+    if (most) return most;
     cudaLaunchConfig_t q = {};
     q.gridDim = dim3(2 * num_sms());
     q.blockDim = dim3(FpPairCfg::THREADS);
@@ -898,15 +900,15 @@ static int max_pairs()
     q.attrs = at;
     q.numAttrs = 1;
     int got = 0;
-    if (cudaOccupancyMaxActiveClusters(&got, kern, &q) == cudaSuccess && got > 0) n = got;
-    return n;
+    if (cudaOccupancyMaxActiveClusters(&got, kern, &q) == cudaSuccess && got > 0) most = got;
+    return most;
 }
 
 template <int BN>
 static int launch_single(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& Y, const CUtensorMap& Z,
                          const CUtensorMap& S, const FpGemmArgs& a, cudaStream_t s)
 {
-    static bool ready = false;
+    static OnEachDevice ready;
     if (allow_smem(k_fp_gemm<BN>, FpCfg<BN>::SMEM_BYTES, &ready) != cudaSuccess)
         return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
     const int64_t items = (int64_t)((a.M + 127) / 128) * ((a.N + BN - 1) / BN) * a.splits;
