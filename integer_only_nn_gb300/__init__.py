@@ -892,11 +892,17 @@ def _vector(t, name, n, index, dtype, other=None):
     return t.data_ptr()
 
 
-def _on_stream(call, stream):
+def _on_stream(call, stream, *tensors):
     """Runs a call with `stream` as torch's current stream, so that what it allocates belongs to
-    the stream that it launches on."""
+    the stream that it launches on. The call's tensors (None passes) may be dropped after it: their
+    memory is not given away before the stream has passed the call. What the stream has to wait for
+    (the work that makes the tensors, the use of the results) is the caller's to order."""
     with _torch().cuda.stream(stream):
-        return call()
+        r = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return r
 
 
 class _Scratch(threading.local):
@@ -931,7 +937,8 @@ def ito_fp_linear_fwd(x, W, bias=None, act="none", residual=None, save_z=False, 
     or float32. bias: x's type or float32."""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_fp_linear_fwd(x, W, bias, act, residual, save_z, out_dtype), stream)
+        return _on_stream(lambda: ito_fp_linear_fwd(x, W, bias, act, residual, save_z, out_dtype), stream, x, W, bias,
+                          residual)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
     ldx = _matrix(x, "x", None, None, None, index)
     B, IC = x.shape
@@ -963,7 +970,8 @@ def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, 
     type or float32), dbias float32 [OC]); None for those not needed."""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_fp_linear_bwd(dy, x, W, z, act, need_dx, need_dw, need_dbias, dw_dtype), stream)
+        return _on_stream(lambda: ito_fp_linear_bwd(dy, x, W, z, act, need_dx, need_dw, need_dbias, dw_dtype), stream, dy, x,
+                          W, z)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
     ldx = _matrix(x, "x", None, None, None, index)
     B, IC = x.shape
@@ -995,7 +1003,7 @@ def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """x [rows][cols] of float32, bfloat16 or float16 -> (y, mean float32 [rows], rstd float32 [rows])"""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream)
+        return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream, x, gamma, beta)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
     ldx = _matrix(x, "x", None, None, None, index)
     rows, cols = x.shape
@@ -1018,7 +1026,8 @@ def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, str
     """-> (dx in x's type, dgamma float32 [cols], dbeta float32 [cols]); None for those not needed."""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream)
+        return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream, dy, x, gamma, mean,
+                          rstd)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
     ldx = _matrix(x, "x", None, None, None, index)
     rows, cols = x.shape
@@ -1049,7 +1058,7 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     (logp (None without targets), entropy, lse float32 [rows], top_ids int32 [rows][k], top_logp float32 [rows][k])"""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream)
+        return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream, logits, targets)
     dev, index = logits.device, _device_index(logits, "logits")
     ld = _matrix(logits, "logits", None, None, None, index)
     rows, classes = logits.shape
@@ -1072,7 +1081,8 @@ def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy
     """-> dlogits in the logits' type (out: a tensor to write it to, which may be the logits)."""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
-        return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream)
+        return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream, logits,
+                          targets, lse, entropy, g_logp, g_entropy, out)
     dtype, dev, index = logits.dtype, logits.device, _device_index(logits, "logits")
     ld = _matrix(logits, "logits", None, None, None, index)
     rows, classes = logits.shape
@@ -1149,6 +1159,7 @@ class AdamW:
             tab[f] = [t.data_ptr() for t in s]
         tab["n"] = sizes
         tab["weight_decay"] = decays
+        self._streams = set()
 
     @staticmethod
     def _dense(ts, dtype, lengths, name, index):
@@ -1160,6 +1171,8 @@ class AdamW:
 
     def step(self, grads, lr, grad_scale=1.0, stream=None):
         """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16)."""
+        if stream is not None:
+            return _on_stream(lambda: self.step(grads, lr, grad_scale), stream, *grads, *self._new_to(stream))
         if len(grads) != self._n:
             raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
         index = _device_index(self.weights[0], "weights[0]")
@@ -1170,15 +1183,22 @@ class AdamW:
         self._fields["g"] = [g.data_ptr() for g in grads]
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
                         _type_id(dtype, "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
-        s = _raw_stream_of(index) if stream is None else stream.cuda_stream
-        _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), s))
+        _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), _raw_stream_of(index)))
         self.steps += 1
+
+    def _new_to(self, stream):
+        """The object's own tensors at its first call on a stream, which has to be recorded once for each
+        of them; then none."""
+        if stream.cuda_stream in self._streams:
+            return []
+        self._streams.add(stream.cuda_stream)
+        return [t for ts in (self.weights, self.copies or [], *self.states) for t in ts]
 
     def moments(self, dtype=None, stream=None):
         """The moments' values (m, v), the tensors' one after another: bfloat16 (exact; default)
         or float32 for 8-bit states, float32 for 32-bit ones."""
         if stream is not None:
-            return _on_stream(lambda: self.moments(dtype), stream)
+            return _on_stream(lambda: self.moments(dtype), stream, *self._new_to(stream))
         torch = _torch()
         if self.bits == 32:
             return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)

@@ -110,3 +110,48 @@ def test_a_step_on_one_device(ito):
     with pytest.raises(ito.ItoError) as e:
         opt.step([Stand((10,), torch.bfloat16) for _ in range(2)], lr=0.1)
     assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
+
+
+class Stream:
+    cuda_stream = 77
+
+
+def test_calls_on_a_stream_keep_their_tensors(ito, monkeypatch):
+    """Each wrapper names all its tensors to the stream it is given, whether or not they outlive the call."""
+    given = []
+    monkeypatch.setattr(ito, "_on_stream", lambda call, stream, *tensors: given.append((stream, tensors)))
+    import torch
+    h, f, i32 = torch.bfloat16, torch.float32, torch.int32
+    x, W, dy, b = Stand((4, 16), h), Stand((8, 16), h), Stand((4, 8), h), Stand((8,), h)
+    v, t, r = [Stand((4,), f) for _ in range(4)], Stand((4,), i32), Stand((4, 8), h)
+    s = Stream()
+    calls = [(lambda: ito.ito_fp_linear_fwd(x, W, bias=b, residual=r, stream=s), [x, W, b, r]),
+             (lambda: ito.ito_fp_linear_bwd(dy, x, W, z=r, act="gelu", stream=s), [dy, x, W, r]),
+             (lambda: ito.ito_layer_norm_fwd(x, b, dy, stream=s), [x, b, dy]),
+             (lambda: ito.ito_layer_norm_bwd(dy, x, b, v[0], v[1], stream=s), [dy, x, b, v[0], v[1]]),
+             (lambda: ito.ito_token_logprobs_fwd(x, t, stream=s), [x, t]),
+             (lambda: ito.ito_token_logprobs_bwd(x, t, v[0], v[1], v[2], v[3], out=W, stream=s), [x, t, *v, W])]
+    w, c, m, n, g = [Stand((10,), k) for k in (f, h, f, f, h)]
+    opt = ito.AdamW([w], copies=[c], states=[[m], [n]])
+    calls += [(lambda: opt.step([g], lr=0.1, stream=s), [g, w, c, m, n]), (lambda: opt.step([g], lr=0.1, stream=s), [g])]
+    for call, tensors in calls:
+        call()
+        stream, got = given.pop()
+        assert stream is s and not given
+        assert sorted(map(id, got)) == sorted(map(id, tensors))
+
+
+def test_a_stream_is_recorded_for_each_tensor(ito, monkeypatch):
+    import contextlib
+    import types
+    seen = []
+
+    class Recorded:
+        def record_stream(self, stream):
+            seen.append((self, stream))
+
+    monkeypatch.setattr(ito, "_torch", lambda: types.SimpleNamespace(
+        cuda=types.SimpleNamespace(stream=lambda s: contextlib.nullcontext())))
+    a, b, s = Recorded(), Recorded(), Stream()
+    assert ito._on_stream(lambda: 5, s, a, None, b) == 5
+    assert seen == [(a, s), (b, s)]

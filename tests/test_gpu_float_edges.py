@@ -130,3 +130,46 @@ def test_activations_of_large_finite_values(torch, ito, act, dtype, B):
         want = np.array([max(v, 0.0) if abs(v) > 60 else v * cdf(v) for v in Z])
     tol = 8 * U * (1 + np.where(Z > 0, Z, near))
     within(y, np.broadcast_to(want, (B, n)), np.broadcast_to(tol, (B, n)), "activation")
+
+
+# ----------------------------------------------------------------- streams
+
+def test_tensors_may_be_dropped_after_a_call_on_another_stream(torch, ito):
+    """A call on a stream that is still busy, its inputs dropped at once and others allocated and
+    filled in their place: the results are those of the inputs that were given."""
+    side = torch.cuda.Stream()
+    x0, W0 = normal(torch, (300, 256), 1, 1.0, "bfloat16"), normal(torch, (512, 256), 2, 0.1, "bfloat16")
+    logits0 = normal(torch, (300, 512), 3, 2.0)
+    tgt = torch.arange(300, device="cuda", dtype=torch.int32)
+    w0, g0 = normal(torch, (5000,), 4), normal(torch, (5000,), 5)
+    want_w = w0.clone()
+    ito.AdamW([want_w]).step([g0], lr=0.1)
+    cases = [(lambda t, s: ito.ito_fp_linear_fwd(t[0], t[1], residual=t[2], stream=s),
+              [x0, W0, normal(torch, (300, 512), 6, 1.0, "bfloat16")]),
+             (lambda t, s: ito.ito_fp_linear_bwd(t[2], t[0], t[1], stream=s)[0],
+              [x0, W0, normal(torch, (300, 512), 6, 1.0, "bfloat16")]),
+             (lambda t, s: ito.ito_layer_norm_fwd(t[0], stream=s)[0], [logits0]),
+             (lambda t, s: ito.ito_token_logprobs_fwd(t[0], t[1], stream=s)[0], [logits0, tgt])]
+    for call, inputs in cases:
+        want = call(inputs, None)
+        t = [i.clone() for i in inputs]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20000000)
+        got = call(t, side)
+        del t
+        others = [torch.zeros_like(i) for i in inputs for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del others
+    w, g = w0.clone(), [g0.clone()]
+    opt = ito.AdamW([w])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20000000)
+    opt.step(g, lr=0.1, stream=side)
+    del g, opt
+    others = [torch.full_like(w0, 7.0) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(w, want_w)
+    del others
