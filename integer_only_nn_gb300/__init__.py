@@ -10,6 +10,7 @@ there is no other implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import threading
 
@@ -812,17 +813,19 @@ _TYPE_IDS = {}          # torch dtype -> ito_type
 _F32 = None             # torch.float32, once torch is there
 _raw_stream_of = None   # device index -> the current stream's handle
 _current_device = None  # -> the current device's index
+_address = None         # Tensor.data_ptr
 
 
 def _float_setup():
     """torch, and what this part needs of it."""
-    global _F32, _raw_stream_of, _current_device
+    global _F32, _raw_stream_of, _current_device, _address
     import torch
     _TYPE_IDS.update({torch.float32: ITO_F32, torch.bfloat16: ITO_BF16, torch.float16: ITO_F16})
     # (torch.cuda.current_stream() makes an object, which takes as long as a small kernel's launch)
     _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _address = torch.Tensor.data_ptr
     _F32 = torch.float32
     return torch
 
@@ -1106,8 +1109,10 @@ class AdamW:
     copies: bfloat16 or float16 tensors that receive the updated weights (None: none).
     weight_decay: a number, or one for each tensor. states: [m, v] lists (bits=32: float32) or
     [m, v, m_exp, v_exp] lists (bits=8: uint8 codes and int8 exponents); None starts from zero.
-    step: steps taken so far. The object keeps the tensors and their addresses: they must not
-    be reallocated (Tensor.set_ or resize_) while it lives."""
+    step: steps taken so far. The object keeps the tensors and a table of their addresses. Weights and
+    copies that have been given other memory since (w.data = .., module.to(), resize_) are found by
+    their addresses, checked as in the constructor, and stepped where they are now. The states' memory is the
+    object's: it stays in use whatever a state tensor is given, and must not be resized."""
 
     def __init__(self, weights, bits=32, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, copies=None, states=None,
                  step=0, seed=0):
@@ -1122,7 +1127,7 @@ class AdamW:
         sizes = [w.numel() for w in self.weights]
         blocks = [(n + 127) // 128 for n in sizes]
         dev = self.weights[0].device
-        index = _device_index(self.weights[0], "weights[0]")
+        _device_index(self.weights[0], "weights[0]")
         if states is None:
             if bits == 32:
                 states = [[torch.zeros(n, dtype=torch.float32, device=dev) for n in sizes] for _ in range(2)]
@@ -1135,31 +1140,48 @@ class AdamW:
         self.states = [list(s) for s in states]
         self.copies = None if copies is None else list(copies)
         decays = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * len(sizes)
-        groups = [(self.weights, torch.float32, sizes, "weights")]
-        groups += [(s, d, n, "states") for s, (d, n) in zip(self.states, kinds)]
+        if self.copies is not None and (not self.copies or self.copies[0].dtype not in (torch.bfloat16, torch.float16)):
+            raise ItoError(ITO_ERR_ARG, "copies must be bfloat16 or float16")
+        # the table's fields, their tensors, and what those have to be
+        groups = [("w", self.weights, torch.float32, sizes, "weights")]
         if self.copies is not None:
-            if not self.copies or self.copies[0].dtype not in (torch.bfloat16, torch.float16):
-                raise ItoError(ITO_ERR_ARG, "copies must be bfloat16 or float16")
-            groups.append((self.copies, self.copies[0].dtype, sizes, "copies"))
-        for ts, dtype, lengths, name in groups:
-            if len(ts) != len(sizes):
-                raise ItoError(ITO_ERR_SHAPE, "%s: %d tensors, expected %d" % (name, len(ts), len(sizes)))
-            self._dense(ts, dtype, lengths, name, index)
+            groups.append(("copy", self.copies, self.copies[0].dtype, sizes, "copies"))
+        held = [(f, s, d, n, "states") for f, s, (d, n) in zip(("m", "v", "m_exp", "v_exp"), self.states, kinds)]
         if len(decays) != len(sizes):
             raise ItoError(ITO_ERR_SHAPE, "weight_decay: %d values, expected %d" % (len(decays), len(sizes)))
         self._copy_type = ITO_BF16 if self.copies is None else _type_id(self.copies[0].dtype, "copies")
-        self._n, self._sizes, self.total = len(sizes), sizes, sum(sizes)
+        self._n, self._sizes, self.total, self._groups = len(sizes), sizes, sum(sizes), groups
         self._table = (AdamwTensor * self._n)()
         tab = self._fields = np.frombuffer(self._table, dtype=np.dtype(
             [(f, np.float64 if f == "weight_decay" else np.int64) for f, _ in AdamwTensor._fields_]))
-        tab["w"] = [w.data_ptr() for w in self.weights]
-        if self.copies is not None:
-            tab["copy"] = [c.data_ptr() for c in self.copies]
-        for f, s in zip(("m", "v", "m_exp", "v_exp"), self.states):
-            tab[f] = [t.data_ptr() for t in s]
         tab["n"] = sizes
         tab["weight_decay"] = decays
-        self._streams = set()
+        index = _device_index(self.weights[0], "weights[0]")
+        self._fill(held, index)
+        self._held = [[t.detach() for t in ts] for ts in self.states]     # (they hold the memory)
+        self._lists = [ts for _, ts, _, _, _ in groups]
+        self._at, self._streams = None, {}
+        self._bind()
+
+    def _fill(self, groups, index):
+        """Checks tensors and puts their addresses in the table."""
+        for _, ts, dtype, lengths, name in groups:
+            if len(ts) != self._n:
+                raise ItoError(ITO_ERR_SHAPE, "%s: %d tensors, expected %d" % (name, len(ts), self._n))
+            self._dense(ts, dtype, lengths, name, index)
+        for field, ts, _, _, _ in groups:
+            self._fields[field] = [t.data_ptr() for t in ts]
+
+    def _bind(self):
+        """Weights and copies where they are now, in the table. -> their device"""
+        index = _device_index(self.weights[0], "weights[0]")
+        # (a small model's 28 addresses take 1.7 us of its step's 12)
+        at = list(map(_address, itertools.chain.from_iterable(self._lists)))
+        if at != self._at:
+            self._at = None
+            self._fill(self._groups, index)
+            self._at = at
+        return index
 
     @staticmethod
     def _dense(ts, dtype, lengths, name, index):
@@ -1175,12 +1197,12 @@ class AdamW:
             return _on_stream(lambda: self.step(grads, lr, grad_scale), stream, *grads, *self._new_to(stream))
         if len(grads) != self._n:
             raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
-        index = _device_index(self.weights[0], "weights[0]")
+        index = self._bind()
         dtype = grads[0].dtype
         for g, n in zip(grads, self._sizes):
-            if g.numel() != n or g.dtype != dtype or g.get_device() != index or not g.is_contiguous():
+            if g.numel() != n or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous():
                 self._dense(grads, dtype, self._sizes, "grads", index)     # says which and why
-        self._fields["g"] = [g.data_ptr() for g in grads]
+        self._fields["g"] = list(map(_address, grads))
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
                         _type_id(dtype, "grads"), self._copy_type, self.seed & 0xFFFFFFFF)
         _check(_lib.ito_adamw_step(self._table, self._n, ctypes.byref(p), _raw_stream_of(index)))
@@ -1188,11 +1210,12 @@ class AdamW:
 
     def _new_to(self, stream):
         """The object's own tensors at its first call on a stream, which has to be recorded once for each
-        of them; then none."""
-        if stream.cuda_stream in self._streams:
+        of them and their memory; then none."""
+        at = list(map(_address, itertools.chain.from_iterable(self._lists)))
+        if self._streams.get(stream.cuda_stream) == at:
             return []
-        self._streams.add(stream.cuda_stream)
-        return [t for ts in (self.weights, self.copies or [], *self.states) for t in ts]
+        self._streams[stream.cuda_stream] = at
+        return [t for ts in self._lists + self._held for t in ts]
 
     def moments(self, dtype=None, stream=None):
         """The moments' values (m, v), the tensors' one after another: bfloat16 (exact; default)
@@ -1201,9 +1224,9 @@ class AdamW:
             return _on_stream(lambda: self.moments(dtype), stream, *self._new_to(stream))
         torch = _torch()
         if self.bits == 32:
-            return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self.states)
+            return tuple(torch.cat([t.reshape(-1) for t in s]) for s in self._held)
         dtype = dtype or torch.bfloat16
-        dev, index = self.weights[0].device, _device_index(self.weights[0], "weights[0]")
+        dev, index = self.weights[0].device, self._bind()
         m, v = (torch.empty(self.total, dtype=dtype, device=dev) for _ in range(2))
         if self.total:
             _check(_lib.ito_adamw_moments(self._table, self._n, _type_id(dtype, "dtype"), m.data_ptr(), v.data_ptr(),

@@ -31,8 +31,15 @@ class Stand:
     def is_contiguous(self):
         return True
 
+    at = 4096
+
     def data_ptr(self):
-        return 4096
+        return self.at
+
+    def detach(self):
+        t = Stand(self.shape, self.dtype, self.index)
+        t.at = self.at
+        return t
 
 
 @pytest.fixture
@@ -42,6 +49,7 @@ def ito(monkeypatch):
     import integer_only_nn_gb300 as m
     m._float_setup()
     monkeypatch.setattr(m, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(m, "_address", lambda t: t.data_ptr(), raising=False)
     monkeypatch.setattr(m, "_float_setup", lambda: torch)
 
     def no_more(*a, **kw):
@@ -132,13 +140,15 @@ def test_calls_on_a_stream_keep_their_tensors(ito, monkeypatch):
              (lambda: ito.ito_token_logprobs_fwd(x, t, stream=s), [x, t]),
              (lambda: ito.ito_token_logprobs_bwd(x, t, v[0], v[1], v[2], v[3], out=W, stream=s), [x, t, *v, W])]
     w, c, m, n, g = [Stand((10,), k) for k in (f, h, f, f, h)]
-    opt = ito.AdamW([w], copies=[c], states=[[m], [n]])
     calls += [(lambda: opt.step([g], lr=0.1, stream=s), [g, w, c, m, n]), (lambda: opt.step([g], lr=0.1, stream=s), [g])]
+    for i, each in enumerate([x, W, dy, b, t, r, w, c, m, n, g] + v):
+        each.at = 4096 * (i + 1)
+    opt = ito.AdamW([w], copies=[c], states=[[m], [n]])
     for call, tensors in calls:
         call()
         stream, got = given.pop()
         assert stream is s and not given
-        assert sorted(map(id, got)) == sorted(map(id, tensors))
+        assert sorted(a.at for a in got) == sorted(a.at for a in tensors)
 
 
 def test_a_stream_is_recorded_for_each_tensor(ito, monkeypatch):
@@ -155,3 +165,42 @@ def test_a_stream_is_recorded_for_each_tensor(ito, monkeypatch):
     a, b, s = Recorded(), Recorded(), Stream()
     assert ito._on_stream(lambda: 5, s, a, None, b) == 5
     assert seen == [(a, s), (b, s)]
+
+
+def test_a_step_goes_to_where_the_tensors_are(ito, monkeypatch):
+    """Weights and copies that have been given other memory since the constructor: the step's table
+    holds their addresses of now; what they may be is checked again. The states' memory stays."""
+    import types
+    import torch
+    seen = []
+
+    def step(table, n, params, stream):
+        seen.append([(t.w, t.g, t.copy, t.m, t.v, t.n) for t in table])
+        return 0
+
+    monkeypatch.setattr(ito, "_lib", types.SimpleNamespace(ito_adamw_step=step))
+    monkeypatch.setattr(ito, "_raw_stream_of", lambda index: 0)
+
+    def stand(dtype, at, n=10):
+        t = Stand((n,), dtype)
+        t.at = at
+        return t
+
+    f, h = torch.float32, torch.bfloat16
+    w, c, m, v = ([stand(k, base + 256 * i) for i in range(2)] for k, base in ((f, 4096), (h, 8192), (f, 12288), (f, 16384)))
+    g = [stand(h, 65536 + 256 * i) for i in range(2)]
+    opt = ito.AdamW(w, copies=c, states=[m, v])
+    opt.step(g, lr=0.1)
+    w[1].at, c[0].at, m[1].at, v[0].at = 20480, 24576, 28672, 32768
+    opt.step(g, lr=0.1)
+    assert seen[0] == [(4096, 65536, 8192, 12288, 16384, 10), (4352, 65792, 8448, 12544, 16640, 10)]
+    assert seen[1] == [(4096, 65536, 24576, 12288, 16384, 10), (20480, 65792, 8448, 12544, 16640, 10)]
+    w[0].at, w[0].dtype = 36864, h
+    with pytest.raises(ito.ItoError):
+        opt.step(g, lr=0.1)
+    w[0].dtype, w[0].shape = f, (9,)
+    with pytest.raises(ito.ItoError):
+        opt.step(g, lr=0.1)
+    w[0].shape = (10,)
+    opt.step(g, lr=0.1)
+    assert len(seen) == 3 and seen[2][0][0] == 36864 and opt.steps == 3

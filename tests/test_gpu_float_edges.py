@@ -173,3 +173,32 @@ def test_tensors_may_be_dropped_after_a_call_on_another_stream(torch, ito):
     torch.cuda.synchronize()
     assert torch.equal(w, want_w)
     del others
+
+
+# ------------------------------------------------------------------- AdamW
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_steps_tensors_where_they_are(torch, ito, bits):
+    """Weights and copies given other memory between two steps: both steps reach them."""
+    sizes = [70000, 129, 1]
+    start, g = [normal(torch, (n,), n) for n in sizes], [normal(torch, (n,), n + 1) for n in sizes]
+
+    def train(move):
+        w = [t.clone() for t in start]
+        c = [t.bfloat16() for t in start]
+        opt = ito.AdamW(w, bits=bits, copies=c, seed=3)
+        for i in range(3):
+            opt.step(g, lr=0.01)
+            if move:
+                for ts in (w, c):
+                    for t in ts:
+                        t.data = t.data.clone()
+        return w + c + [t for ts in opt.states for t in ts] + list(opt.moments())
+
+    assert all(torch.equal(a, b) for a, b in zip(train(False), train(True)))
+    w = [t.clone() for t in start]
+    opt = ito.AdamW(w, bits=bits)
+    w[1].data = w[1].data.half()
+    with pytest.raises(ito.ItoError) as e:
+        opt.step(g, lr=0.01)
+    assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
