@@ -1192,16 +1192,20 @@ class AdamW:
                 raise ItoError(ITO_ERR_ARG, "%s[%d]: a dense %s tensor on cuda:%d is expected" % (name, i, dtype, index))
 
     def step(self, grads, lr, grad_scale=1.0, stream=None):
-        """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16)."""
+        """One step with a gradient for each tensor (all of one type: float32, bfloat16 or float16; a
+        tensor without one has to be left out of the object, or given zeros)."""
         if stream is not None:
             return _on_stream(lambda: self.step(grads, lr, grad_scale), stream, *grads, *self._new_to(stream))
         if len(grads) != self._n:
             raise ItoError(ITO_ERR_SHAPE, "%d gradients, expected %d" % (len(grads), self._n))
         index = self._bind()
-        dtype = grads[0].dtype
-        for g, n in zip(grads, self._sizes):
-            if g.numel() != n or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous():
-                self._dense(grads, dtype, self._sizes, "grads", index)     # says which and why
+        try:
+            dtype = grads[0].dtype
+            for g, n in zip(grads, self._sizes):
+                if g.numel() != n or g.dtype is not dtype or g.get_device() != index or not g.is_contiguous():
+                    self._dense(grads, dtype, self._sizes, "grads", index)     # says which and why
+        except AttributeError:
+            raise ItoError(ITO_ERR_ARG, "grads: %s, expected tensors" % sorted({type(g).__name__ for g in grads})) from None
         self._fields["g"] = list(map(_address, grads))
         p = AdamwParams(lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.steps + 1, self.bits,
                         _type_id(dtype, "grads"), self._copy_type, self.seed & 0xFFFFFFFF)

@@ -204,3 +204,14 @@ def test_a_step_goes_to_where_the_tensors_are(ito, monkeypatch):
     w[0].shape = (10,)
     opt.step(g, lr=0.1)
     assert len(seen) == 3 and seen[2][0][0] == 36864 and opt.steps == 3
+
+
+def test_a_step_without_a_gradient_is_refused(ito):
+    import torch
+    opt = ito.AdamW([Stand((10,), torch.float32) for _ in range(2)],
+                    states=[[Stand((10,), torch.float32) for _ in range(2)] for _ in range(2)])
+    g = Stand((10,), torch.bfloat16)
+    for grads in ([g, None], [None, g], [None, None]):
+        with pytest.raises(ito.ItoError) as e:
+            opt.step(grads, lr=0.1)
+        assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
