@@ -1066,6 +1066,10 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     ld = _matrix(logits, "logits", None, None, None, index)
     rows, classes = logits.shape
     pt = _vector(targets, "targets", rows, index, torch.int32)
+    if not 0 <= k <= 32:
+        raise ItoError(ITO_ERR_ARG, "k must be in 0 .. 32")
+    if k > classes:
+        raise ItoError(ITO_ERR_SHAPE, "k above classes")
     ty = _type_id(logits.dtype, "logits")
     entropy = torch.empty(rows, dtype=_F32, device=dev)
     lse = torch.empty_like(entropy)

@@ -215,3 +215,12 @@ def test_a_step_without_a_gradient_is_refused(ito):
         with pytest.raises(ito.ItoError) as e:
             opt.step(grads, lr=0.1)
         assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
+
+
+def test_alternatives_are_refused_before_their_results_are_allocated(ito):
+    import torch
+    x = Stand((4, 16), torch.bfloat16)
+    for k, code in ((-1, ito.ITO_ERR_ARG), (33, ito.ITO_ERR_ARG), (1 << 40, ito.ITO_ERR_ARG), (17, ito.ITO_ERR_SHAPE)):
+        with pytest.raises(ito.ItoError) as e:
+            ito.ito_token_logprobs_fwd(x, None, k=k)
+        assert e.value.code == code
