@@ -175,6 +175,47 @@ def test_tensors_may_be_dropped_after_a_call_on_another_stream(torch, ito):
     del others
 
 
+def test_threads_on_one_stream(torch, ito):
+    """Host threads that call on the same stream share no workspace: each gets the bits of a call alone."""
+    import threading
+    stream = torch.cuda.Stream()
+    sets = []
+    for i in range(4):
+        B, IC, OC = [(40, 251, 264), (333, 787, 1000), (300, 1000, 136), (64, 2048, 72)][i]
+        x, W = normal(torch, (B, IC), i, 1.0, "bfloat16"), normal(torch, (OC, IC), i + 10, 0.1, "bfloat16")
+        dy, z = normal(torch, (B, OC), i + 20, 1.0, "bfloat16"), normal(torch, (B, OC), i + 30, 1.0, "bfloat16")
+        v = normal(torch, (B, OC), i + 40)
+        _, mean, rstd = ito.ito_layer_norm_fwd(v)
+        sets.append((x, W, dy, z, v, mean, rstd))
+
+    def calls(s):
+        x, W, dy, z, v, mean, rstd = s
+        return [ito.ito_fp_linear_fwd(x, W, act="silu"), *ito.ito_fp_linear_bwd(dy, x, W, z=z, act="gelu"),
+                *ito.ito_layer_norm_bwd(v, v, None, mean, rstd)]
+
+    want = [calls(s) for s in sets]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(len(sets))
+
+    def work(i):
+        try:
+            start.wait()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = calls(sets[i])
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(i)
+        except Exception as e:      # (an assertion of a thread would be lost)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 # ------------------------------------------------------------------- AdamW
 
 @pytest.mark.parametrize("bits", [32, 8])
