@@ -223,10 +223,13 @@ struct RingPlace {
 // within the limit of one wait; nothing more can be done for what has not come by then.
 inline __device__ __noinline__ void ring_landed(uint64_t* full, int stages, RingPlace at, int copies)
 {
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = 0;                 // (the timer takes a microsecond: not where copies have landed)
     for (int i = 0; i < copies; ++i, at.next(stages))
-        while (!mbar_try_wait(&full[at.stage], at.phase))
-            if (globaltimer_ns() - t0 > kWaitTimeoutNs) return;
+        while (!mbar_try_wait(&full[at.stage], at.phase)) {
+            const uint64_t t = globaltimer_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > kWaitTimeoutNs) return;
+        }
 }
 
 // What has to be done once on each device (a kernel's attributes belong to the function on one device).
