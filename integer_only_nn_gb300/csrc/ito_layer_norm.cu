@@ -992,13 +992,18 @@ static int run_bwd(const void* dyp, int64_t lddy, const void* xp, int64_t ldx, c
     else if (sh.vpt == 2) ITO_LN(2, 2);
     else if (sh.vpt == 4) ITO_LN(4, 1);
     else {
-        // the shares first: they read dy, which dx may replace
-        if (wgrad)
-            launch_pdl(k_layer_norm_shares_long<T>, dim3((cols + 255) / 256, parts), 256, 0,
-                       s, dy, lddy, x, ldx, mean, rstd, rows, cols, share);
+        // The shares read dy, so they come first where dx replaces it; else dx, after whose two passes the
+        // shares find more of both tensors in L2 (3000 x 10000 float32: 195 us, 208 with the shares first).
+        const auto shares = [&] {
+            if (wgrad)
+                launch_pdl(k_layer_norm_shares_long<T>, dim3((cols + 255) / 256, parts), 256, 0, s, dy, lddy, x, ldx,
+                           mean, rstd, rows, cols, share);
+        };
+        if (dx == dy) shares();
         if (dx)
             launch_pdl(k_layer_norm_dx_long<T>, grid, sh.block, 0, s, dy, lddy, dyv, x, ldx, xv, gamma, w_type, mean,
                        rstd, rows, cols, dx, lddx, dxv);
+        if (dx != dy) shares();
     }
 #undef ITO_LN
 #undef ITO_LN_AS
