@@ -770,8 +770,8 @@ size_t ito_fp_linear_fwd_workspace_size(const void *x, int64_t ldx, const void *
  * type: ITO_BF16 or ITO_F16, of x [B][IC], W [OC][IC] and z [B][OC]; out_type:
  * type or ITO_F32, of y [B][OC] and residual [B][OC] (NULL: none; it may be y
  * itself with the same stride); bias_type: type or ITO_F32, of bias [OC] (NULL:
- * none); act: ito_act. A few rows (B up to 16 to 32) stream W once at the memory's
- * rate. workspace: 256-byte aligned, at least
+ * none); act: ito_act. A few rows (B up to 16 to 32) stream W once past them.
+ * workspace: 256-byte aligned, at least
  * ito_fp_linear_fwd_workspace_size() bytes (may be NULL where that is 0).
  * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type or act,
  * workspace), ITO_ERR_SHAPE (a size outside 1 .. 2^20, a row stride below the

@@ -1108,7 +1108,8 @@ def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy
 
 class AdamW:
     """AdamW over many weight tensors (float32, dense, updated in place), one launch a step
-    for up to a few dozen of them, with moments in 32 bits or in 8 (see include/ito.h).
+    for up to a few dozen of them (two with 8-bit moments and large tensors), with moments in 32 bits or
+    in 8 (see include/ito.h).
 
     copies: bfloat16 or float16 tensors that receive the updated weights (None: none).
     weight_decay: a number, or one for each tensor. states: [m, v] lists (bits=32: float32) or

@@ -1,4 +1,5 @@
-// The AdamW step over many tensors in one launch, its moments held in 32 bits or in 8.
+// The AdamW step over many tensors, its moments held in 32 bits or in 8, in one launch for up to
+// kAdamEntries tensors; with 8-bit moments and tensors of many chunks in two, their whole chunks and the rest.
 //
 //   m = b1 m + (1 - b1) g           v = b2 v + (1 - b2) g^2
 //   w = w (1 - lr wd) - (m lr / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps)
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
 // ------------------------------------------------------ whole chunks, 8-bit moments
 //
 // The step reads 8 and writes 8 bytes an element (bf16 gradients and copies), with about 105
-// instructions between, and their issue bounds it (138M weights: 477 us, 290 at the memory's rate;
+// instructions between, and their issue bounds it (138M weights: 480 us, 332 at the memory's rate;
 // roots and quotients take 7 % of it, the rounding's hash 9 %), so loads may not wait for
 // arithmetic. A producer thread keeps a ring of chunks of 2048 elements coming into shared
 // memory by bulk copies, and three teams of eight warps take them in turn, half a warp to a

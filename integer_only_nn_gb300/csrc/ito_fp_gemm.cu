@@ -99,8 +99,8 @@ struct FpSteps {
 // the 64-byte swizzle), and leave by TMA, which clips them at the tensor's edges, or, where rows
 // do not start on 16-byte boundaries, by coalesced plain stores. Two buffers to a warp (four
 // measured the same), because the operands' ring needs the room: its loads take about as long
-// as four stages' products, and 8192 x 4096 x 4096 took 220 us with four stages, 156 with five,
-// 144 with six.
+// as four stages' products, and 8192 x 4096 x 4096 takes 160 us with four stages, 144 with five,
+// 142 with six (with bias, GELU, z and residual 190, 177, 160).
 constexpr int kFpBox = 2048, kFpBoxes = 2;
 
 struct FpStage {
@@ -557,7 +557,8 @@ struct FpProblem {
 // one, go round the pairs; of its last round `rest` pairs have one, and the others meanwhile take
 // `gap` items each of problem 1, whose remaining items go round all pairs. At 2048 x 4096 x 4096 the two products
 // are 2 + 4 waves one by one, 7/8 of that together. A launch of one product has a kernel of its
-// own: with the second one's branches 8192 x 4096 x 4096 took 156 us instead of 144.
+// own: with the second one's branches 8192 x 4096 x 4096 takes 145 us instead of 142, and 171 instead of
+// 160 with bias, GELU, z and residual.
 template <int PROBLEMS>
 struct FpPairWork {
     FpProblem p[PROBLEMS];
@@ -797,9 +798,9 @@ struct FpPlan {
 // operands from L2 at about 100 KB a us (8192 x 4096 x 4096: a K block of a 256-column pair's tile is
 // 32 KB an SM and took 0.32 us), a K block of products takes at least 0.27 us for 256 columns,
 // and a block's loads and their waits about 0.12; a join takes 2.5 us and the slices' sums pass
-// through memory at 4 TB/s. It orders the measured choices (us): 8192 x 4096 x 4096 144 with
-// 256 columns, 199 with 160; 2048 x 4096 x 4096 39.5 with 224, 47 with 256; 512 x 4096 x 4096 20 in
-// 128 x 128 tiles, 18 in pairs of 128 columns; 33 x 6080 x 5824 27 whole, 20 in three slices.
+// through memory at 4 TB/s. It orders the measured choices (us): 8192 x 4096 x 4096 142 with
+// 256 columns, 185 with 160; 2048 x 4096 x 4096 40 with 224, 53 with 256; 512 x 4096 x 4096 23 in
+// 128 x 128 tiles, 22 in pairs of 128 columns; 33 x 6080 x 5824 27 whole, 15 in three slices.
 static FpPlan fp_plan(int M, int N, int K, bool b_mn)
 {
     const int num_kb = (K + 63) / 64, sms = num_sms(), pairs = sms / 2;
