@@ -243,3 +243,57 @@ def test_adamw_steps_tensors_where_they_are(torch, ito, bits):
     with pytest.raises(ito.ItoError) as e:
         opt.step(g, lr=0.01)
     assert e.value.code == ito.ITO_ERR_ARG and opt.steps == 0
+
+
+# -------------------------------------------------- beyond 2^31 elements
+
+def _filled(torch, shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, scale, generator=g)
+
+
+@pytest.mark.parametrize("OC", [4104, 4101])      # rows that TMA stores take, and plain stores
+def test_linear_rows_beyond_32_bits(torch, ito, OC):
+    """The last rows of more than 2^31 elements, against 64-bit products of those rows."""
+    B, IC = (1 << 19) + 5, 72
+    x, W, r = _filled(torch, (B, IC), 1), _filled(torch, (OC, IC), 2, IC ** -0.5), _filled(torch, (B, OC), 3)
+    y = ito.ito_fp_linear_fwd(x, W, residual=r)
+    dx, _, db = ito.ito_fp_linear_bwd(r, x, W, need_dw=False)
+    for rows in (slice(0, 130), slice(B - 130, B)):
+        X, V, R = f64(x[rows]), f64(W), f64(r[rows])
+        within_rounded(y[rows], X @ V.T + R, 2 * (IC + 2) * U * (np.abs(X) @ np.abs(V).T + np.abs(R)), "bfloat16", "y")
+        within_rounded(dx[rows], R @ V, 2 * OC * U * (np.abs(R) @ np.abs(V)), "bfloat16", "dx")
+    total, size = (sum(f(r[i:i + 65536].double()).sum(0) for i in range(0, B, 65536)) for f in (lambda t: t, torch.abs))
+    # a thread adds at most B / (8 * 32) rows of its share, then 32 threads' and 8 blocks' sums are added
+    within(db, f64(total), (B / 256 + 48) * U * f64(size), "dbias")
+
+
+@pytest.mark.parametrize("cols", [4104, 4101])
+def test_layer_norm_rows_beyond_32_bits(torch, ito, cols):
+    """The last rows of more than 2^31 elements have the bits that a call on them alone gives."""
+    rows = (1 << 19) + 5
+    x, dy = _filled(torch, (rows, cols), 1, 1.5), _filled(torch, (rows, cols), 2)
+    gamma, beta = 1 + normal(torch, (cols,), 3, 0.2), normal(torch, (cols,), 4, 0.5)
+    y, mean, rstd = ito.ito_layer_norm_fwd(x, gamma, beta)
+    dx, _, _ = ito.ito_layer_norm_bwd(dy, x, gamma, mean, rstd)
+    many = 4 * torch.cuda.get_device_properties(0).multi_processor_count + 8       # rows enough for the same kernels
+    end = slice(rows - many, rows)
+    y2, mean2, rstd2 = ito.ito_layer_norm_fwd(x[end], gamma, beta)
+    dx2, _, _ = ito.ito_layer_norm_bwd(dy[end], x[end], gamma, mean2, rstd2)
+    assert torch.equal(y[end], y2) and torch.equal(mean[end], mean2) and torch.equal(rstd[end], rstd2)
+    assert torch.equal(dx[end], dx2)
+
+
+@pytest.mark.parametrize("n", [65536, 65533])
+def test_logprobs_rows_beyond_32_bits(torch, ito, n):
+    """The last rows of more than 2^31 elements have the bits that a call on enough of them alone gives."""
+    rows = 33000
+    x = _filled(torch, (rows, n), 1, 2.0)
+    tgt = torch.arange(rows, device="cuda", dtype=torch.int32)
+    gl, gh = normal(torch, (rows,), 2), normal(torch, (rows,), 3)
+    got = ito.ito_token_logprobs_fwd(x, tgt, k=3)
+    d = ito.ito_token_logprobs_bwd(x, tgt, got[2], got[1], gl, gh)
+    end = slice(rows - 8 * torch.cuda.get_device_properties(0).multi_processor_count - 8, rows)
+    alone = ito.ito_token_logprobs_fwd(x[end], tgt[end], k=3)
+    assert all(torch.equal(a[end], b) for a, b in zip(got, alone))
+    assert torch.equal(d[end], ito.ito_token_logprobs_bwd(x[end], tgt[end], alone[2], alone[1], gl[end], gh[end]))
