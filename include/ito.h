@@ -801,6 +801,47 @@ int ito_fp_linear_bwd(const void *dy, int64_t lddy, const void *z, int64_t ldz, 
                       void *workspace, size_t workspace_bytes, void *dx, int64_t lddx, void *dW, int64_t lddw,
                       float *dbias, void *stream);
 
+/* Bytes of device workspace ito_fp_gated_linear_fwd needs (0 on invalid sizes,
+ * and where none is needed), as ito_fp_linear_fwd_workspace_size. */
+size_t ito_fp_gated_linear_fwd_workspace_size(const void *x, int64_t ldx, const void *Wg, int64_t ldwg,
+                                              const void *Wu, int64_t ldwu, int B, int IC, int OC);
+
+/* Gated layer on 16-bit floats: both projections, the activation and the product
+ * in one kernel:
+ *   g[b][oc] = sum_ic x[b][ic] * Wg[oc][ic] + bias_g[oc]     (32-bit sums)
+ *   u[b][oc] = sum_ic x[b][ic] * Wu[oc][ic] + bias_u[oc]
+ *   h = act(g) * u,  zg = g,  zu = u, each rounded once to `type`
+ * type: ITO_BF16 or ITO_F16, of all tensors but the biases; zg, zu: both for the
+ * backward pass, or both NULL; bias_type: type or ITO_F32, of bias_g and bias_u
+ * [OC] (each may be NULL: none); act: ito_act. A few rows (B up to 16 to 32)
+ * stream both weights once past them. workspace: 256-byte aligned, at least
+ * ito_fp_gated_linear_fwd_workspace_size() bytes (may be NULL where that is 0).
+ * Errors as ito_fp_linear_fwd. */
+int ito_fp_gated_linear_fwd(const void *x, int64_t ldx, const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu,
+                            const void *bias_g, const void *bias_u, int type, int bias_type, int act, int B, int IC,
+                            int OC, void *workspace, size_t workspace_bytes, void *zg, int64_t ldzg, void *zu,
+                            int64_t ldzu, void *h, int64_t ldh, void *stream);
+
+/* Bytes of device workspace ito_fp_gated_linear_bwd needs (0 on invalid sizes): dzg
+ * and dzu, aligned copies, and partial sums. */
+size_t ito_fp_gated_linear_bwd_workspace_size(const void *x, int64_t ldx, const void *Wg, int64_t ldwg,
+                                              const void *Wu, int64_t ldwu, int B, int IC, int OC);
+
+/* Backward pass of ito_fp_gated_linear_fwd:
+ *   dzg = dh * zu * act'(zg),  dzu = dh * act(zg), rounded once to `type` (they
+ *         are operands of the products below)
+ *   dx[b][ic] = sum_oc dzg[b][oc] * Wg[oc][ic] + dzu[b][oc] * Wu[oc][ic]  in `type`
+ *   dWg = dzg^T x, dWu = dzu^T x                                     in `out_type`
+ *   dbias_g[oc] = sum_b dzg[b][oc], dbias_u of dzu (before the rounding) in 32 bits
+ * zg, zu: as the forward pass wrote them. Any of dx, dbias_g, dbias_u may be NULL
+ * (not computed), dWg and dWu both; x is read for them only, Wg and Wu for dx
+ * only. out_type: type or ITO_F32. Errors as ito_fp_linear_fwd. */
+int ito_fp_gated_linear_bwd(const void *dh, int64_t lddh, const void *zg, int64_t ldzg, const void *zu, int64_t ldzu,
+                            const void *x, int64_t ldx, const void *Wg, int64_t ldwg, const void *Wu, int64_t ldwu,
+                            int type, int out_type, int act, int B, int IC, int OC, void *workspace,
+                            size_t workspace_bytes, void *dx, int64_t lddx, void *dWg, int64_t lddwg, void *dWu,
+                            int64_t lddwu, float *dbias_g, float *dbias_u, void *stream);
+
 /* Layer norm over a row of `cols` elements:
  *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   y = (x - mean) * rstd * gamma + beta
@@ -861,6 +902,78 @@ int ito_token_logprobs_fwd(const void *logits, int64_t ld, int type, const int32
 int ito_token_logprobs_bwd(const void *logits, int64_t ld, int type, const int32_t *targets, const float *lse,
                            const float *entropy, int64_t rows, int classes, const float *g_logp,
                            const float *g_entropy, void *dlogits, int64_t ldd, void *stream);
+
+/* Bytes of device workspace ito_linear_cross_entropy_fwd needs (0 on invalid
+ * sizes): 8 bytes for each row and 16 to 128 classes, and what
+ * ito_fp_linear_fwd_workspace_size names. */
+size_t ito_linear_cross_entropy_fwd_workspace_size(const void *x, int64_t ldx, const void *W, int64_t ldw, int rows,
+                                                   int d, int classes);
+
+/* Cross entropy of a linear layer's classes, without its logits in memory:
+ *   l_j = sum_k x[row][k] * W[j][k]    (32 bits, not rounded)
+ *   lse = log sum_j exp(l_j),  loss = lse - l_target
+ * type: ITO_BF16 or ITO_F16, of x [rows][d] and W [classes][d]. targets: int32
+ * [rows]; -1 stands for no token (loss 0); any other value outside [0, classes) is
+ * treated the same and records ITO_ERR_ARG in the device error word
+ * (ito_get_error), as in ito_token_logprobs_fwd. A logit of -inf has p = 0; a row
+ * of them only has lse -inf and loss +inf; a row with a NaN or +inf has NaN
+ * results. loss, lse: float [rows] (either may be NULL). workspace: 256-byte
+ * aligned, at least ito_linear_cross_entropy_fwd_workspace_size() bytes.
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type, workspace),
+ * ITO_ERR_SHAPE (a size outside 1 .. 2^20, a row stride below the row's length),
+ * ITO_ERR_CUDA. */
+int ito_linear_cross_entropy_fwd(const void *x, int64_t ldx, const void *W, int64_t ldw, int type,
+                                 const int32_t *targets, int rows, int d, int classes, void *workspace,
+                                 size_t workspace_bytes, float *loss, float *lse, void *stream);
+
+/* Bytes of device workspace ito_linear_cross_entropy_bwd needs (0 on invalid
+ * sizes): the gradient of a piece of the logits (up to 256 MB, or 256 classes),
+ * dx in 32 bits where there are several pieces, aligned copies and partial sums. */
+size_t ito_linear_cross_entropy_bwd_workspace_size(const void *x, int64_t ldx, const void *W, int64_t ldw, int rows,
+                                                   int d, int classes);
+
+/* Gradient of sum_r (g_loss[r] * loss[r] + g_lse[r] * lse[r]), piece of the
+ * vocabulary by piece, with p_j = exp(l_j - lse):
+ *   dl_j = g_loss * (p_j - [j == target]) + g_lse * p_j, rounded once to `type` (it
+ *          is an operand of the products below; in ITO_F16 after multiplication by a
+ *          power of two that brings the largest |g_loss| + |g_lse| to 2^12 .. 2^13)
+ *   dx[row][k] = sum_j dl_j * W[j][k]             in `type` (summed in 32 bits)
+ *   dW[j][k] = sum over rows of dl_j * x[row][k]  in `out_type` (type or ITO_F32)
+ * lse: as the forward pass wrote it; g_loss: float [rows]; g_lse: float [rows] or
+ * NULL (none). Targets outside [0, classes) as in the forward pass: no term from
+ * g_loss. A row whose lse is -inf, or whose factors are 0, has a gradient of 0.
+ * dx or dW may be NULL (not computed). Errors as ito_linear_cross_entropy_fwd. */
+int ito_linear_cross_entropy_bwd(const void *x, int64_t ldx, const void *W, int64_t ldw, int type,
+                                 const int32_t *targets, const float *lse, const float *g_loss, const float *g_lse,
+                                 int out_type, int rows, int d, int classes, void *workspace, size_t workspace_bytes,
+                                 void *dx, int64_t lddx, void *dW, int64_t lddw, void *stream);
+
+/* Embedding lookup: y[i] = scale * table[ids[i]], rounded once to out_type.
+ * ids: int32 [n]; -1 stands for no token (y is 0); any other value outside
+ * [0, classes) is treated the same and records ITO_ERR_ARG in the device error
+ * word (ito_get_error). table [classes][d] of `type`, y [n][d] of out_type (any
+ * ito_type each).
+ * Errors: ITO_ERR_ARG (NULL or misaligned pointer, unknown type), ITO_ERR_SHAPE (a
+ * size < 1, n or classes above 2^30, d above 2^24, a row stride below d),
+ * ITO_ERR_CUDA. */
+int ito_embedding_fwd(const int32_t *ids, int64_t n, const void *table, int64_t ldt, int type, int classes, int d,
+                      float scale, int out_type, void *y, int64_t ldy, void *stream);
+
+/* Bytes of device workspace for the sorted places and the pieces of sums (0 on
+ * invalid sizes). */
+size_t ito_embedding_bwd_workspace_size(int64_t n, int classes, int d);
+
+/* Gradient of ito_embedding_fwd for the table, in the order of the places (no
+ * atomics on sums):
+ *   dtable[v] = scale * sum over i with ids[i] == v of dy[i]   (32-bit sums), 0 for
+ *               tokens that do not occur; with add != 0 that is added to dtable
+ *               [v] instead, and the rows of absent tokens are not touched
+ * dy [n][d] of `type`, dtable [classes][d] of out_type (type or ITO_F32). ids as in
+ * the forward pass. workspace: 256-byte aligned. Errors as ito_embedding_fwd, and
+ * ITO_ERR_ARG for a workspace that is NULL, misaligned or too small. */
+int ito_embedding_bwd(const void *dy, int64_t lddy, int type, const int32_t *ids, int64_t n, int classes, int d,
+                      float scale, int add, int out_type, void *workspace, size_t workspace_bytes, void *dtable,
+                      int64_t ldt, void *stream);
 
 /* One tensor of an AdamW step. States in 32 bits: m, v are float [n]. In 8 bits
  * they are bytes [n] under a shared exponent E for each 128 consecutive elements

@@ -148,11 +148,25 @@ _SIGS = {
     "ito_fp_linear_bwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I]),
     "ito_fp_linear_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P,
                                _I64, _P, _P]),
+    "ito_fp_gated_linear_fwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I]),
+    "ito_fp_gated_linear_fwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P,
+                                     _I64, _P, _I64, _P]),
+    "ito_fp_gated_linear_bwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I]),
+    "ito_fp_gated_linear_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _I, _I,
+                                     _P, _SZ, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
     "ito_layer_norm_fwd": (_I, [_P, _I64, _I, _P, _P, _I, _I64, _I, ctypes.c_float, _P, _I64, _P, _P, _P]),
     "ito_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I]),
     "ito_layer_norm_bwd": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _I, _P, _SZ, _P, _I64, _P, _P, _P]),
     "ito_token_logprobs_fwd": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _P, _P, _P, _P, _P, _P]),
     "ito_token_logprobs_bwd": (_I, [_P, _I64, _I, _P, _P, _P, _I64, _I, _P, _P, _P, _I64, _P]),
+    "ito_linear_cross_entropy_fwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _I, _I, _I]),
+    "ito_linear_cross_entropy_fwd": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _I, _I, _P, _SZ, _P, _P, _P]),
+    "ito_linear_cross_entropy_bwd_workspace_size": (_SZ, [_P, _I64, _P, _I64, _I, _I, _I]),
+    "ito_linear_cross_entropy_bwd": (_I, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P,
+                                          _I64, _P]),
+    "ito_embedding_fwd": (_I, [_P, _I64, _P, _I64, _I, _I, _I, ctypes.c_float, _I, _P, _I64, _P]),
+    "ito_embedding_bwd_workspace_size": (_SZ, [_I64, _I, _I]),
+    "ito_embedding_bwd": (_I, [_P, _I64, _I, _P, _I64, _I, _I, ctypes.c_float, _I, _I, _P, _SZ, _P, _I64, _P]),
     "ito_adamw_step": (_I, [_P, _I, ctypes.POINTER(AdamwParams), _P]),
     "ito_adamw_moments": (_I, [_P, _I, _I, _P, _P, _P]),
 }
@@ -895,6 +909,14 @@ def _vector(t, name, n, index, dtype, other=None):
     return t.data_ptr()
 
 
+def _length(t, name):
+    """The length of a 1-D tensor with elements."""
+    shape = t.shape
+    if len(shape) != 1 or not shape[0]:
+        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [n] with n >= 1" % (name, list(shape)))
+    return shape[0]
+
+
 def _on_stream(call, stream, *tensors):
     """Runs a call with `stream` as torch's current stream, so that what it allocates belongs to
     the stream that it launches on. The call's tensors (None passes) may be dropped after it: their
@@ -1002,6 +1024,79 @@ def ito_fp_linear_bwd(dy, x, W, z=None, act="none", need_dx=True, need_dw=True, 
     return dx, dw, db
 
 
+def ito_fp_gated_linear_fwd(x, Wg, Wu, bias_g=None, bias_u=None, act="silu", save_z=False, stream=None):
+    """h = act(zg) zu with zg = x Wg^T + bias_g, zu = x Wu^T + bias_u for bf16 or f16 x [B][IC], Wg and Wu
+    [OC][IC]; -> h, or (h, zg, zu) where save_z, all in x's type. Biases: x's type or float32, both alike."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_fp_gated_linear_fwd(x, Wg, Wu, bias_g, bias_u, act, save_z), stream, x, Wg, Wu,
+                          bias_g, bias_u)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
+    B, IC = x.shape
+    ldg = _matrix(Wg, "Wg", None, IC, dtype, index)
+    OC = Wg.shape[0]
+    ldu = _matrix(Wu, "Wu", OC, IC, dtype, index)
+    pbg, pbu = _vector(bias_g, "bias_g", OC, index, dtype, _F32), _vector(bias_u, "bias_u", OC, index, dtype, _F32)
+    if pbg is not None and pbu is not None and bias_g.dtype is not bias_u.dtype:
+        raise ItoError(ITO_ERR_ARG, "bias_g and bias_u of one type")
+    b = bias_g if bias_g is not None else bias_u
+    ty, a = _type_id(dtype, "x"), _act_id(act)
+    px, pg, pu = x.data_ptr(), Wg.data_ptr(), Wu.data_ptr()
+    h = torch.empty((B, OC), dtype=dtype, device=dev)
+    zg, zu = (torch.empty_like(h), torch.empty_like(h)) if save_z else (None, None)
+    s = _raw_stream_of(index)
+    ws, hold = None, None
+    n = _lib.ito_fp_gated_linear_fwd_workspace_size(px, ldx, pg, ldg, pu, ldu, B, IC, OC)
+    if n:
+        ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_fp_gated_linear_fwd(px, ldx, pg, ldg, pu, ldu, pbg, pbu, ty, ITO_F32 if b is None else _TYPE_IDS[b.dtype],
+                                     a, B, IC, OC, ws, n, zg.data_ptr() if save_z else None, OC,
+                                     zu.data_ptr() if save_z else None, OC, h.data_ptr(), OC, s)
+    if r:
+        _check(r)
+    return (h, zg, zu) if save_z else h
+
+
+def ito_fp_gated_linear_bwd(dh, x, Wg, Wu, zg, zu, act="silu", need_dx=True, need_dw=True, need_dbias=False,
+                            dw_dtype=None, stream=None):
+    """Gradients of ito_fp_gated_linear_fwd -> (dx [B][IC] in x's type, dWg and dWu [OC][IC] in dw_dtype (x's
+    type or float32), dbias_g and dbias_u float32 [OC]); None for those not needed."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_fp_gated_linear_bwd(dh, x, Wg, Wu, zg, zu, act, need_dx, need_dw, need_dbias,
+                                                          dw_dtype), stream, dh, x, Wg, Wu, zg, zu)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
+    B, IC = x.shape
+    ldg = _matrix(Wg, "Wg", None, IC, dtype, index)
+    OC = Wg.shape[0]
+    ldu = _matrix(Wu, "Wu", OC, IC, dtype, index)
+    lddh, ldzg, ldzu = (_matrix(t, name, B, OC, dtype, index) for t, name in ((dh, "dh"), (zg, "zg"), (zu, "zu")))
+    ty, a = _type_id(dtype, "x"), _act_id(act)
+    dwt = dtype if dw_dtype is None else dw_dtype
+    out = _type_id(dwt, "dw_dtype")
+    px, pg, pu = x.data_ptr(), Wg.data_ptr(), Wu.data_ptr()
+    dx = torch.empty((B, IC), dtype=dtype, device=dev) if need_dx else None
+    dwg = dwu = dbg = dbu = None
+    if need_dw:
+        dwg = torch.empty((OC, IC), dtype=dwt, device=dev)
+        dwu = torch.empty_like(dwg)
+    if need_dbias:
+        dbg = torch.empty(OC, dtype=_F32, device=dev)
+        dbu = torch.empty_like(dbg)
+    s = _raw_stream_of(index)
+    n = _lib.ito_fp_gated_linear_bwd_workspace_size(px, ldx, pg, ldg, pu, ldu, B, IC, OC)
+    ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_fp_gated_linear_bwd(dh.data_ptr(), lddh, zg.data_ptr(), ldzg, zu.data_ptr(), ldzu, px, ldx, pg, ldg, pu,
+                                     ldu, ty, out, a, B, IC, OC, ws, n, dx.data_ptr() if need_dx else None, IC,
+                                     dwg.data_ptr() if need_dw else None, IC, dwu.data_ptr() if need_dw else None, IC,
+                                     dbg.data_ptr() if need_dbias else None, dbu.data_ptr() if need_dbias else None, s)
+    if r:
+        _check(r)
+    return dx, dwg, dwu, dbg, dbu
+
+
 def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     """x [rows][cols] of float32, bfloat16 or float16 -> (y, mean float32 [rows], rstd float32 [rows])"""
     torch = _torch() if _F32 is not None else _float_setup()
@@ -1104,6 +1199,119 @@ def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy
     if r:
         _check(r)
     return d
+
+
+def ito_linear_cross_entropy_fwd(x, W, targets, stream=None):
+    """bf16 or f16 x [rows][d], W [classes][d], targets int32 [rows] (-1: no token) -> (loss, lse float32 [rows]):
+    lse of the logits x W^T and loss = lse - the target's logit (0 without one). The logits are not stored."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_linear_cross_entropy_fwd(x, W, targets), stream, x, W, targets)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
+    rows, d = x.shape
+    ldw = _matrix(W, "W", None, d, dtype, index)
+    classes = W.shape[0]
+    pt = _vector(targets, "targets", rows, index, torch.int32)
+    ty = _type_id(dtype, "x")
+    loss = torch.empty(rows, dtype=_F32, device=dev)
+    lse = torch.empty_like(loss)
+    s = _raw_stream_of(index)
+    px, pw = x.data_ptr(), W.data_ptr()
+    n = _lib.ito_linear_cross_entropy_fwd_workspace_size(px, ldx, pw, ldw, rows, d, classes)
+    ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_linear_cross_entropy_fwd(px, ldx, pw, ldw, ty, pt, rows, d, classes, ws, n, loss.data_ptr(),
+                                          lse.data_ptr(), s)
+    if r:
+        _check(r)
+    return loss, lse
+
+
+def ito_linear_cross_entropy_bwd(x, W, targets, lse, g_loss, g_lse=None, need_dx=True, need_dw=True, dw_dtype=None,
+                                 stream=None):
+    """Gradients of sum(g_loss loss + g_lse lse) -> (dx [rows][d] in x's type, dW [classes][d] in dw_dtype (x's type or
+    float32)); None for those not needed. g_loss, g_lse: float32 [rows]."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_linear_cross_entropy_bwd(x, W, targets, lse, g_loss, g_lse, need_dx, need_dw,
+                                                               dw_dtype), stream, x, W, targets, lse, g_loss, g_lse)
+    dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
+    ldx = _matrix(x, "x", None, None, None, index)
+    rows, d = x.shape
+    ldw = _matrix(W, "W", None, d, dtype, index)
+    classes = W.shape[0]
+    pt = _vector(targets, "targets", rows, index, torch.int32)
+    pl = _vector(lse, "lse", rows, index, _F32)
+    pg, pe = _vector(g_loss, "g_loss", rows, index, _F32), _vector(g_lse, "g_lse", rows, index, _F32)
+    ty = _type_id(dtype, "x")
+    dwt = dtype if dw_dtype is None else dw_dtype
+    out = _type_id(dwt, "dw_dtype")
+    dx = torch.empty((rows, d), dtype=dtype, device=dev) if need_dx else None
+    dw = torch.empty((classes, d), dtype=dwt, device=dev) if need_dw else None
+    s = _raw_stream_of(index)
+    px, pw = x.data_ptr(), W.data_ptr()
+    n = _lib.ito_linear_cross_entropy_bwd_workspace_size(px, ldx, pw, ldw, rows, d, classes)
+    ws, hold = _scratch.get(n, dev, s, torch)
+    r = _lib.ito_linear_cross_entropy_bwd(px, ldx, pw, ldw, ty, pt, pl, pg, pe, out, rows, d, classes, ws, n,
+                                          dx.data_ptr() if need_dx else None, d, dw.data_ptr() if need_dw else None, d, s)
+    if r:
+        _check(r)
+    return dx, dw
+
+
+def ito_embedding_fwd(ids, table, scale=1.0, out_dtype=None, stream=None):
+    """y [n][d] = scale table[ids] in out_dtype (the table's type by default; float32, bfloat16, float16 each);
+    ids int32 [n], -1: no token (zeros)."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_embedding_fwd(ids, table, scale, out_dtype), stream, ids, table)
+    dtype, dev, index = table.dtype, table.device, _device_index(table, "table")
+    ldt = _matrix(table, "table", None, None, None, index)
+    classes, d = table.shape
+    n = _length(ids, "ids")
+    pi = _vector(ids, "ids", n, index, torch.int32)
+    out = dtype if out_dtype is None else out_dtype
+    ty, oty = _type_id(dtype, "table"), _type_id(out, "out_dtype")
+    y = torch.empty((n, d), dtype=out, device=dev)
+    r = _lib.ito_embedding_fwd(pi, n, table.data_ptr(), ldt, ty, classes, d, scale, oty, y.data_ptr(), d,
+                               _raw_stream_of(index))
+    if r:
+        _check(r)
+    return y
+
+
+def ito_embedding_bwd(dy, ids, classes, scale=1.0, dtype=None, add_to=None, stream=None):
+    """The table's gradient [classes][d] in dtype (float32 by default, or dy's type): scale times the sums of dy's
+    rows by token, zeros for tokens that do not occur. add_to: a gradient to which the sums are added instead (rows of
+    absent tokens are not touched); it is returned."""
+    torch = _torch() if _F32 is not None else _float_setup()
+    if stream is not None:
+        return _on_stream(lambda: ito_embedding_bwd(dy, ids, classes, scale, dtype, add_to), stream, dy, ids, add_to)
+    dev, index = dy.device, _device_index(dy, "dy")
+    n = _length(ids, "ids")
+    lddy = _matrix(dy, "dy", n, None, None, index)
+    d = dy.shape[1]
+    pi = _vector(ids, "ids", n, index, torch.int32)
+    if add_to is not None:
+        if dtype is not None and add_to.dtype is not dtype:
+            raise ItoError(ITO_ERR_ARG, "add_to: type %s, expected %s" % (add_to.dtype, dtype))
+        ldt, out = _matrix(add_to, "add_to", classes, d, None, index), add_to
+    else:
+        ldt, out = d, None
+    oty = _type_id(add_to.dtype if out is not None else _F32 if dtype is None else dtype, "dtype")
+    ty = _type_id(dy.dtype, "dy")
+    if classes < 1:
+        raise ItoError(ITO_ERR_SHAPE, "classes must be >= 1")
+    if out is None:
+        out = torch.empty((classes, d), dtype=_F32 if dtype is None else dtype, device=dev)
+    s = _raw_stream_of(index)
+    m = _lib.ito_embedding_bwd_workspace_size(n, classes, d)
+    ws, hold = _scratch.get(m, dev, s, torch)
+    r = _lib.ito_embedding_bwd(dy.data_ptr(), lddy, ty, pi, n, classes, d, scale, int(add_to is not None), oty, ws, m,
+                               out.data_ptr(), ldt, s)
+    if r:
+        _check(r)
+    return out
 
 
 class AdamW:

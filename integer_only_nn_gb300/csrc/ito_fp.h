@@ -1,4 +1,4 @@
-// The 16-bit float products of the linear layer: what their epilogue does, and how they are run.
+// The 16-bit float products of the float layers: what their epilogue does, and how they are run.
 #pragma once
 
 #include "ito_internal.h"
@@ -18,6 +18,34 @@ struct FpEpilogue {
     int64_t ldz;
 };
 
+// What happens to a product's sums:
+//   Linear    FpEpilogue as above
+//   Gated     two products of one A: y = act(zg) zu with zg = sum + bias, zu = sum2 + bias2, which go to z and z2
+//   Loss      each tile's part of a row's softmax sums, and the row's target among the sums: nothing else is written
+//   DLogits   y = (g_loss + g_lse) exp(sum - lse) - g_loss [column is the target], times *scale
+//   Grad      y = *alpha sum + acc; the operands may come in two halves (below)
+enum class FpEnd { Linear, Gated, Loss, DLogits, Grad };
+
+// the other ends' arguments
+struct FpMore {
+    const void* bias2;       // Gated
+    void* z2;
+    int64_t ldz2;
+    const int32_t* targets;  // Loss, DLogits: [M], classes; a product's column 0 is class `first` of `classes`
+    int first, classes;
+    float2* part;            // Loss: [fp_loss_parts()][M] (largest sum, sum of exp(sum - largest))
+    float* hit;              // Loss: [M] the target's sum
+    const float* lse;        // DLogits: [M]; g_lse and scale may be null
+    const float* g_loss;
+    const float* g_lse;
+    const float* scale;
+    const float* alpha;      // Grad: may be null (1)
+    const float* acc;        // Grad: [M][ldacc], may be null (0); may be y
+    int64_t ldacc;
+    void* y2;                // Grad with two halves of rows
+    int64_t ldy2;
+};
+
 // A 16-bit operand: [rows][K] with K contiguous (mn false) or [K][rows] (mn true). Its base is
 // 16-byte aligned and ld a multiple of 8 elements.
 struct FpOperand {
@@ -31,12 +59,51 @@ struct FpProduct {
     FpOperand A, B;
     int M, N, K;
     FpEpilogue e;
+    FpEnd end;
+    FpMore x;
+    // Gated: the second product's B. Grad: with k_half, B(n, k) = B2(n, k - k_half) from k = k_half on (a
+    // multiple of 64; A has 2 k_half columns; each half of B has k_rows rows, and A's columns beyond are 0).
+    FpOperand B2;
+    int k_half, k_rows;
+    // Grad: with a_half, a second result y2 [M][N] from the rows a_half + m of A (an MN-major one; a
+    // multiple of 8)
+    int a_half;
 };
 
-// One or two products that do not depend on one another, on the tensor cores; ws: the sum of the
-// bytes that fp_gemm_ws_bytes names for each (sums of a product cut into slices of K; b_mn: B.mn),
-// 256-byte aligned.
-size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn);
+// One or two products that do not depend on one another and have the same end (two: Linear or Grad), on the
+// tensor cores; ws: the sum of the bytes that fp_gemm_ws_bytes names for each (sums of a product cut into
+// slices of K; b_mn: B.mn; halves: 2 for Grad with a_half), 256-byte aligned.
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end = FpEnd::Linear, int halves = 1);
 int fp_gemm(const FpProduct* products, int n, void* ws, cudaStream_t s);
+// Parts of each row's sums that a Loss product leaves; 0: none, the workspace's slices are summed and (hit, part[0])
+// are the row's own
+int fp_loss_parts(int M, int N, int K);
+
+// ---- shared by the layers' entry points (ito_fp_linear.cu)
+
+// Rows whose starts TMA cannot address, copied to rows padded to 8 elements; up to three tensors
+// (blockIdx.z).
+constexpr int kFpCopies = 3;
+struct FpCopy {
+    const uint16_t* src[kFpCopies];
+    uint16_t* dst[kFpCopies];
+    int64_t ld[kFpCopies], ldd[kFpCopies];
+    int rows[kFpCopies], cols[kFpCopies];
+    int n;
+};
+int64_t fp_row_stride(int64_t ld, int rows, int cols);           // (a row's stride says nothing about a single row)
+bool fp_tma_rows(const void* p, int64_t ld, int rows, int cols);
+size_t fp_copy_bytes(const void* p, int64_t ld, int rows, int cols);
+// The operand itself, or where its aligned copy will be (at *ws, which moves on), noted in `c`.
+const void* fp_aligned_operand(const void* p, int64_t* ld, int rows, int cols, char** ws, FpCopy* c);
+int fp_run_copies(const FpCopy& c, cudaStream_t s);
+int fp_check_sizes(int B, int IC, int OC);
+int fp_check_tensor(const void* p, int type, int64_t ld, int rows, int cols, const char* name);
+int fp_check_types(int type, int out_type, int act);
+int fp_check_ws(const void* ws, size_t bytes, size_t need);
+inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Whether a few rows of x stream W (see ito_fp_rows.cuh) instead of taking tensor-core tiles.
+bool fp_rows_kernel(int B, int IC, int OC);
 
 }  // namespace ito

@@ -127,6 +127,36 @@ __device__ __forceinline__ void fp_finish(const FpEpilogue& e, int64_t r, int64_
     store_typed(e.y, e.out_type, r * e.ldy + c, v);
 }
 
+// one element of a gated layer
+__device__ __forceinline__ void fp_finish_gated(const FpEpilogue& e, const FpMore& x, int64_t r, int64_t c, float g, float u)
+{
+    if (e.bias) g += load_typed(e.bias, e.bias_type, c);
+    if (x.bias2) u += load_typed(x.bias2, e.bias_type, c);
+    if (e.z) {
+        store_typed(e.z, e.type, r * e.ldz + c, g);
+        store_typed(x.z2, e.type, r * x.ldz2 + c, u);
+    }
+    store_typed(e.y, e.type, r * e.ldy + c, act_value(e.act, g) * u);
+}
+
+// (m, s) of a set of numbers, s = sum of exp(v - m) with m the largest, joined with another's. Where both
+// hold nothing but -inf, s stays 0; a NaN or an infinity makes s a NaN.
+constexpr float kFpLog2e = 1.4426950408889634f;
+__device__ __forceinline__ void fp_softmax_add(float& m, float& s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_approx((m - ref) * kFpLog2e) + s2 * exp2_approx((m2 - ref) * kFpLog2e);
+    m = top;
+}
+// joined over a group of `lanes` consecutive lanes, in the same order for each of them
+__device__ __forceinline__ void fp_softmax_warp(float& m, float& s, int lanes = 32)
+{
+    for (int o = 1; o < lanes; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+        fp_softmax_add(m, s, m2, s2);
+    }
+}
+
 // two floats as one word of two 16-bit floats, lo in the low half
 __device__ __forceinline__ uint32_t pack16(int type, float lo, float hi)
 {

@@ -12,6 +12,9 @@
 // 128 x 64 tiles of one CTA, with K cut into slices where there are few tiles, for the rest.
 // Slices write their sums in 32 bits to the workspace, and a second kernel adds them in a fixed
 // order and does the epilogue. A weight gradient over a long batch is such a product too.
+//
+// Each kernel is compiled once for each end (FpEnd): the gated layer's two products on one A, the
+// parts of a softmax over the columns, the gradient that such a softmax sends back, and gradients in halves.
 #include <algorithm>
 #include <cstring>
 
@@ -43,6 +46,7 @@ __host__ __device__ constexpr uint32_t fp_idesc(int M, int N, bool a_mn, bool b_
 
 struct FpGemmArgs {
     FpEpilogue e;
+    FpMore x;
     int M, N, K;
     int a_mn, b_mn;
     uint32_t idesc;
@@ -51,6 +55,17 @@ struct FpGemmArgs {
     int y_tma, z_tma;           // rows of y and z that TMA stores can take
     int r_vec, b_vec;           // rows of the residual, and a bias, that 16-byte loads can take
     int* err;
+    // the other ends'
+    int y2_tma, z2_tma, b2_vec;
+    int cols;                   // result columns of a tile: bn, half of it in the gated layer
+    int kb_half;                // K blocks in the first half of B (0: no halves)
+    int halves, a_half;         // results from one A
+};
+
+// A product's tensor maps and arguments. B2, Y2: a second B, a second result (z2 or y2)
+struct FpProblem {
+    CUtensorMap A, B, Y, Z, S, B2, Y2;
+    FpGemmArgs a;
 };
 
 // The producer's and the issuer's warps run their loops whole, so that what they count is uniform
@@ -213,6 +228,17 @@ __device__ __forceinline__ void activate(float (&v)[32])
     }
 }
 
+__device__ __forceinline__ void activate(int act, float (&v)[32])
+{
+    switch (act) {
+    case ITO_ACT_RELU: activate<ITO_ACT_RELU>(v); break;
+    case ITO_ACT_GELU: activate<ITO_ACT_GELU>(v); break;
+    case ITO_ACT_GELU_TANH: activate<ITO_ACT_GELU_TANH>(v); break;
+    case ITO_ACT_SILU: activate<ITO_ACT_SILU>(v); break;
+    default: break;
+    }
+}
+
 // this lane's row of a 16-bit residual, 32 columns (0 beyond the edges); asked for before the
 // sums are there
 __device__ __forceinline__ void load_residual16(const FpGemmArgs& a, int col, int row, uint32_t (&w)[16])
@@ -237,25 +263,24 @@ __device__ __forceinline__ void load_residual16(const FpGemmArgs& a, int col, in
     }
 }
 
-// the columns' biases, the same for every lane
-__device__ __forceinline__ void add_bias(const FpGemmArgs& a, float (&v)[32], int col)
+// the columns' biases, the same for every lane; vec: 16-byte loads can take them
+__device__ __forceinline__ void add_bias(const void* bias, int type, int vec, int N, float (&v)[32], int col)
 {
-    const FpEpilogue& e = a.e;
-    if (a.b_vec && col + 32 <= a.N && e.bias_type != ITO_F32) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + col);
+    if (vec && col + 32 <= N && type != ITO_F32) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(bias) + col);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint4 q = __ldg(p + j);
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack16(e.bias_type, w[i]);
+                const float2 f = unpack16(type, w[i]);
                 v[8 * j + 2 * i] += f.x;
                 v[8 * j + 2 * i + 1] += f.y;
             }
         }
-    } else if (a.b_vec && col + 32 <= a.N) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + col);
+    } else if (vec && col + 32 <= N) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(bias) + col);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float4 q = __ldg(p + j);
@@ -266,9 +291,28 @@ __device__ __forceinline__ void add_bias(const FpGemmArgs& a, float (&v)[32], in
         }
     } else {
         const int c = col + (threadIdx.x & 31);
-        const float mine = c < a.N ? load_typed(e.bias, e.bias_type, c) : 0.0f;
+        const float mine = c < N ? load_typed(bias, type, c) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, mine, i);
+    }
+}
+
+// `left` elements of a row of 32-bit floats added (32 at most)
+__device__ __forceinline__ void add_row32(const float* r, int vec, int left, float (&v)[32])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (vec && 4 * j + 4 <= left) {
+            const float4 q = *reinterpret_cast<const float4*>(r + 4 * j);
+            v[4 * j] += q.x;
+            v[4 * j + 1] += q.y;
+            v[4 * j + 2] += q.z;
+            v[4 * j + 3] += q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * j + i < left) v[4 * j + i] += r[4 * j + i];
+        }
     }
 }
 
@@ -278,15 +322,9 @@ __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensor
 {
     const FpEpilogue& e = a.e;
     const int lane = st.lane;
-    if (e.bias) add_bias(a, v, col);
+    if (e.bias) add_bias(e.bias, e.bias_type, a.b_vec, a.N, v, col);
     if (e.z) store16(v, e.type, mapZ, a.z_tma, e.z, e.ldz, st, col, row, a.M, a.N);
-    switch (e.act) {
-    case ITO_ACT_RELU: activate<ITO_ACT_RELU>(v); break;
-    case ITO_ACT_GELU: activate<ITO_ACT_GELU>(v); break;
-    case ITO_ACT_GELU_TANH: activate<ITO_ACT_GELU_TANH>(v); break;
-    case ITO_ACT_SILU: activate<ITO_ACT_SILU>(v); break;
-    default: break;
-    }
+    activate(e.act, v);
     if (e.out_type != ITO_F32) {
         if (e.residual) {
 #pragma unroll
@@ -299,24 +337,46 @@ __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensor
         store16(v, e.out_type, mapY, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
         return;
     }
-    if (e.residual && row + lane < a.M) {
-        const float* r = static_cast<const float*>(e.residual) + (row + lane) * e.ldr + col;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (a.r_vec && col + 4 * j + 4 <= a.N) {
-                const float4 q = *reinterpret_cast<const float4*>(r + 4 * j);
-                v[4 * j] += q.x;
-                v[4 * j + 1] += q.y;
-                v[4 * j + 2] += q.z;
-                v[4 * j + 3] += q.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (col + 4 * j + i < a.N) v[4 * j + i] += r[4 * j + i];
-            }
-        }
-    }
+    if (e.residual && row + lane < a.M)
+        add_row32(static_cast<const float*>(e.residual) + (row + lane) * e.ldr + col, a.r_vec, a.N - col, v);
     store32(v, mapY, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
+}
+
+// zg and zu of a gated layer: both biases, both saved, h = act(zg) zu
+__device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32], float (&u)[32], FpStage& st, int col,
+                                             int row)
+{
+    const FpGemmArgs& a = p.a;
+    const FpEpilogue& e = a.e;
+    if (e.bias) add_bias(e.bias, e.bias_type, a.b_vec, a.N, g, col);
+    if (a.x.bias2) add_bias(a.x.bias2, e.bias_type, a.b2_vec, a.N, u, col);
+    if (e.z) {
+        store16(g, e.type, &p.Z, a.z_tma, e.z, e.ldz, st, col, row, a.M, a.N);
+        store16(u, e.type, &p.Y2, a.z2_tma, a.x.z2, a.x.ldz2, st, col, row, a.M, a.N);
+    }
+    activate(e.act, g);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] *= u[i];
+    store16(g, e.type, &p.Y, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
+}
+
+// a gradient's sums: *alpha sum + acc
+__device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int col, int row)
+{
+    const FpGemmArgs& a = p.a;
+    const FpEpilogue& e = a.e;
+    if (a.x.alpha) {
+        const float alpha = __ldg(a.x.alpha);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= alpha;
+    }
+    if (a.x.acc && row + st.lane < a.M) add_row32(a.x.acc + (row + st.lane) * a.x.ldacc + col, a.r_vec, a.N - col, v);
+    const CUtensorMap* map = half ? &p.Y2 : &p.Y;
+    const bool tma = half ? a.y2_tma : a.y_tma;
+    void* y = half ? a.x.y2 : e.y;
+    const int64_t ld = half ? a.x.ldy2 : e.ldy;
+    if (e.out_type == ITO_F32) store32(v, map, tma, y, ld, st, col, row, a.M, a.N);
+    else store16(v, e.out_type, map, tma, y, ld, st, col, row, a.M, a.N);
 }
 
 // a warp's wait: one lane asks
@@ -336,19 +396,114 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// ------------------------------------------------------- a softmax's parts and its gradient
+
+// One lane's row of a tile: its class, and the running largest sum m and s = sum of exp(sum - m).
+// A sum of -inf adds 0; a NaN or an infinity makes s a NaN.
+struct LossRow {
+    int target;
+    float m, s;
+
+    // 32 columns from col on, of which `left` exist; -> the target's sum to *hit, where it is among them
+    __device__ __forceinline__ void add(float (&v)[32], int col, int left, float* hit)
+    {
+        if (left < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i >= left) v[i] = -INFINITY;
+        }
+        const int at = target - col;
+        if (at >= 0 && at < 32) {
+            float x = v[0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i)
+                if (i == at) x = v[i];
+            *hit = x;
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        s *= exp2_approx((m - ref) * kFpLog2e);
+        float t[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            t[0] += exp2_approx((v[i] - ref) * kFpLog2e);
+            t[1] += exp2_approx((v[i + 1] - ref) * kFpLog2e);
+        }
+        s += t[0] + t[1];
+        m = top;
+    }
+};
+
+// What a row of logits sends back: (a exp(v - lse) - hot [column is the target]). A row without a
+// token or whose lse is -inf sends 0.
+struct SlopeRow {
+    int target;
+    float a, hot, lse;
+    bool none;
+
+    __device__ __forceinline__ void load(const FpGemmArgs& g, int row, bool first)
+    {
+        target = -1;
+        a = hot = 0.0f;
+        lse = 0.0f;
+        if (row < g.M) {
+            const int t = g.x.targets[row];
+            const bool in = t >= 0 && t < g.x.classes;
+            if (first && !in && t != -1) raise_device_error(g.err, ITO_ERR_ARG);
+            const float scale = g.x.scale ? *g.x.scale : 1.0f;
+            lse = g.x.lse[row];
+            if (in) {
+                target = t - g.x.first;
+                hot = a = g.x.g_loss[row];
+            }
+            if (g.x.g_lse) a += g.x.g_lse[row];
+            a *= scale;
+            hot *= scale;
+        }
+        none = (a == 0.0f && hot == 0.0f) || lse == -INFINITY;
+    }
+    __device__ __forceinline__ float at(float v, int col) const
+    {
+        if (none) return 0.0f;
+        const float p = a * exp2_approx((v - lse) * kFpLog2e);
+        return col == target ? p - hot : p;
+    }
+    __device__ __forceinline__ void apply(float (&v)[32], int col) const
+    {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = a * exp2_approx((v[i] - lse) * kFpLog2e);
+        const int at = target - col;
+        if (at >= 0 && at < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i == at) v[i] -= hot;
+        }
+        if (none) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+    }
+};
+
 // The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
 // (row, col0), sums at `taddr`; `done` tells the issuing warp that the accumulator is drained. A
-// slice of K (slice >= 0) leaves its sums as they are, in mapS.
-template <typename Wait, typename Done>
-__device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
-                                           const CUtensorMap* mapS, int slice, FpStage& st, int first, int step,
+// slice of K (slice >= 0) leaves its sums as they are, in the workspace. `half`: of a result in halves.
+template <FpEnd END, typename Wait, typename Done>
+__device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int half, FpStage& st, int first, int step,
                                            int columns, int col0, int row, uint32_t taddr, Wait wait, Done done,
                                            bool& ok)
 {
+    const FpGemmArgs& a = p.a;
     // a 16-bit residual comes while the sums are still being made
-    const bool res16 = slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
+    const bool res16 = END == FpEnd::Linear && slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
     uint32_t res[16];
     if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
+    LossRow loss{-1, -INFINITY, 0.0f};
+    SlopeRow slope;
+    if (END == FpEnd::Loss && row + st.lane < a.M) loss.target = a.x.targets[row + st.lane];
+    if (END == FpEnd::DLogits) slope.load(a, row + st.lane, first == 0 && col0 == 0 && a.x.first == 0);
     if (!wait()) {
         ok = false;
         return;
@@ -356,8 +511,9 @@ __device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMa
     tc_fence_after();
 #pragma unroll 1
     for (int c = first * 32; c < columns; c += step * 32) {
-        float v[32];
+        float v[32], u[32];
         load_sums(taddr + c, v);
+        if (END == FpEnd::Gated) load_sums(taddr + columns + c, u);
         if (c + step * 32 >= columns) {
             tc_fence_before();
             __syncwarp();
@@ -365,22 +521,37 @@ __device__ __forceinline__ void drain_tile(const FpGemmArgs& a, const CUtensorMa
         }
         if (row >= a.M || col0 + c >= a.N) continue;
         if (slice >= 0) {
+            constexpr int PLANES = END == FpEnd::Gated ? 2 : 1;
+            const int plane = END == FpEnd::Gated ? 2 * slice : END == FpEnd::Grad ? a.halves * slice + half : slice;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (col0 + c + 16 * h >= a.N) break;
-                uint8_t* stg = stage32(v, h, st);
+            for (int h = 0; h < 2 * PLANES; ++h) {
+                if (col0 + c + 16 * (h & 1) >= a.N) continue;
+                uint8_t* stg = stage32(h < 2 ? v : u, h & 1, st);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (st.lane == 0) {
-                    tma_store_3d(mapS, stg, col0 + c + 16 * h, row, slice);
+                    tma_store_3d(&p.S, stg, col0 + c + 16 * (h & 1), row, plane + (h >> 1));
                     bulk_commit();
                 }
             }
             continue;
         }
-        if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
-        finish_group(a, mapY, mapZ, v, res, st, col0 + c, row);
+        if (END == FpEnd::Linear) {
+            if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
+            finish_group(a, &p.Y, &p.Z, v, res, st, col0 + c, row);
+        } else if (END == FpEnd::Gated) {
+            finish_gated(p, v, u, st, col0 + c, row);
+        } else if (END == FpEnd::Loss) {
+            loss.add(v, col0 + c, a.N - col0 - c, a.x.hit + row + st.lane);
+        } else if (END == FpEnd::DLogits) {
+            slope.apply(v, col0 + c);
+            store16(v, a.e.type, &p.Y, true, a.e.y, a.e.ldy, st, col0 + c, row, a.M, a.N);
+        } else {
+            finish_grad(p, half, v, st, col0 + c, row);
+        }
     }
+    if (END == FpEnd::Loss && slice < 0 && row + st.lane < a.M)
+        a.x.part[(int64_t)(col0 / columns * step + first) * a.M + row + st.lane] = make_float2(loss.m, loss.s);
 }
 
 // ----------------------------------------------------------------- one CTA
@@ -397,13 +568,12 @@ struct FpCfg {
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
 };
 
-template <int BN>
-__global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
-    k_fp_gemm(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-              const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapZ,
-              const __grid_constant__ CUtensorMap mapS, const __grid_constant__ FpGemmArgs a)
+template <int BN, FpEnd END>
+__global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1) k_fp_gemm(const __grid_constant__ FpProblem p)
 {
     using Cfg = FpCfg<BN>;
+    constexpr int COLS = END == FpEnd::Gated ? BN / 2 : BN;      // result columns of a tile
+    const FpGemmArgs& a = p.a;
     constexpr int BM = Cfg::BM, BK = Cfg::BK, STAGES = Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -415,7 +585,8 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce_bar + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const FpTiles tiles{(a.M + BM - 1) / BM, (a.N + BN - 1) / BN, a.group};
+    const int num_m = (a.M + BM - 1) / BM;                       // row tiles of a result
+    const FpTiles tiles{END == FpEnd::Grad ? num_m * a.halves : num_m, (a.N + COLS - 1) / COLS, a.group};
     const int num_items = tiles.num_m * tiles.num_n * a.splits;
     const int num_kb = (a.K + BK - 1) / BK;
 
@@ -430,8 +601,8 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
         }
         *abort_flag = 0;
         fence_mbar_init();
-        prefetch_tensormap(&mapA);
-        prefetch_tensormap(&mapB);
+        prefetch_tensormap(&p.A);
+        prefetch_tensormap(&p.B);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
@@ -452,6 +623,8 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
             const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
+            int rowA = tm * BM;
+            if (END == FpEnd::Grad && tm >= num_m) rowA = a.a_half + (tm - num_m) * BM;
             for (int kb = lo; kb < hi; ++kb) {
                 if (!ring_wait(&empty_bar[stage], phase ^ 1, abort_flag, a.err)) { ok = false; break; }
                 if (elect_one()) {
@@ -459,17 +632,23 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
                     uint8_t* sA = smem + stage * Cfg::STAGE_BYTES;
                     uint8_t* sB = sA + Cfg::A_BYTES;
                     if (!a.a_mn) {
-                        tma_load_2d(&mapA, &full_bar[stage], sA, kb * BK, tm * BM);
+                        tma_load_2d(&p.A, &full_bar[stage], sA, kb * BK, rowA);
                     } else {
-                        tma_load_2d(&mapA, &full_bar[stage], sA, tm * BM, kb * BK);
-                        tma_load_2d(&mapA, &full_bar[stage], sA + 8192, tm * BM + 64, kb * BK);
+                        tma_load_2d(&p.A, &full_bar[stage], sA, rowA, kb * BK);
+                        tma_load_2d(&p.A, &full_bar[stage], sA + 8192, rowA + 64, kb * BK);
                     }
-                    if (!a.b_mn) {
-                        tma_load_2d(&mapB, &full_bar[stage], sB, kb * BK, tn * BN);
+                    if (END == FpEnd::Gated) {           // (both K-major; boxes of COLS rows)
+                        tma_load_2d(&p.B, &full_bar[stage], sB, kb * BK, tn * COLS);
+                        tma_load_2d(&p.B2, &full_bar[stage], sB + Cfg::B_BYTES / 2, kb * BK, tn * COLS);
+                    } else if (!a.b_mn) {
+                        tma_load_2d(&p.B, &full_bar[stage], sB, kb * BK, tn * BN);
                     } else {
+                        const bool second = END == FpEnd::Grad && a.kb_half && kb >= a.kb_half;
+                        const CUtensorMap* map = second ? &p.B2 : &p.B;
+                        const int k = second ? kb - a.kb_half : kb;
 #pragma unroll
                         for (int j = 0; j < BN / 64; ++j)
-                            tma_load_2d(&mapB, &full_bar[stage], sB + j * 8192, tn * BN + j * 64, kb * BK);
+                            tma_load_2d(map, &full_bar[stage], sB + j * 8192, tn * BN + j * 64, k * BK);
                     }
                 }
                 __syncwarp();
@@ -514,8 +693,10 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1)
         for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
-            drain_tile(
-                a, &mapY, &mapZ, &mapS, a.splits > 1 ? w % a.splits : -1, st, part, 2, BN, tn * BN, tm * BM + quad * 32,
+            const int half = END == FpEnd::Grad && tm >= num_m;
+            drain_tile<END>(
+                p, a.splits > 1 ? w % a.splits : -1, half, st, part, 2, COLS, tn * COLS,
+                (half ? tm - num_m : tm) * BM + quad * 32,
                 tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN),
                 [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err); },
                 [&] { if (lane == 0) mbar_arrive(&acce_bar[buf]); }, ok);
@@ -545,11 +726,6 @@ struct FpPairCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int STAGING_BYTES = EPI_WARPS * kFpBoxes * kFpBox;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 256;
-};
-
-struct FpProblem {
-    CUtensorMap A, B, Y, Z, S;
-    FpGemmArgs a;
 };
 
 // One product, or two in one launch (the backward pass's), so that the second's items (tiles, or
@@ -589,7 +765,7 @@ struct FpPairWork {
     }
 };
 
-template <int PROBLEMS>
+template <int PROBLEMS, FpEnd END>
 __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     k_fp_gemm_pair(const __grid_constant__ FpPairWork<PROBLEMS> work)
 {
@@ -639,13 +815,16 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // an item's place in its result, and its K blocks
-    auto place = [&](const FpGemmArgs& a, int item, int& row, int& col) {
-        const FpTiles tiles{(a.M + 2 * BM - 1) / (2 * BM), (a.N + a.bn - 1) / a.bn, a.group};
+    // an item's place in its result (and which, of two halves), and its K blocks
+    auto place = [&](const FpGemmArgs& a, int item, int& row, int& col, int& half) {
+        const int cols = END == FpEnd::Gated ? a.cols : a.bn, num_m = (a.M + 2 * BM - 1) / (2 * BM);
+        const FpTiles tiles{END == FpEnd::Grad ? num_m * a.halves : num_m, (a.N + cols - 1) / cols, a.group};
         int tm, tn;
         tiles.coords(item / a.splits, tm, tn);
+        half = END == FpEnd::Grad && tm >= num_m;
+        if (half) tm -= num_m;
         row = tm * 2 * BM + (int)rank * BM;
-        col = tn * a.bn;
+        col = tn * cols;
     };
     auto k_range = [&](const FpGemmArgs& a, int item, int& lo, int& hi) {
         lo = item % a.splits * a.kb_per_split;
@@ -664,10 +843,13 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                 const FpGemmArgs& a = p.a;
                 const bool a_mn = a.a_mn, b_mn = a.b_mn;
                 const uint32_t stage_bytes = 2 * (Cfg::A_BYTES + (b_mn ? Cfg::B_BYTES : (a.bn / 2) * BK * 2));
-                int rowA, rowB, lo, hi;
-                place(a, item, rowA, rowB);
+                int rowA, rowB, half, lo, hi;
+                place(a, item, rowA, rowB, half);
                 k_range(a, item, lo, hi);
-                rowB += (int)rank * (a.bn / 2);
+                if (half) rowA += a.a_half;
+                // of the gated layer's two products each CTA stages its own one's B
+                const CUtensorMap* mapB = END == FpEnd::Gated && !leader ? &p.B2 : &p.B;
+                if (END != FpEnd::Gated) rowB += (int)rank * (a.bn / 2);
                 for (int kb = lo; kb < hi; ++kb) {
                     if (!ring_wait(&empty_bar[stage], phase ^ 1, abort_flag, err)) { ok = false; break; }
                     if (elect_one()) {
@@ -682,10 +864,13 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                             tma_load_2d_pair(&p.A, fb, sA + 8192, rowA + 64, kb * BK);
                         }
                         if (!b_mn) {
-                            tma_load_2d_pair(&p.B, fb, sB, kb * BK, rowB);
+                            tma_load_2d_pair(mapB, fb, sB, kb * BK, rowB);
                         } else {
-                            tma_load_2d_pair(&p.B, fb, sB, rowB, kb * BK);
-                            tma_load_2d_pair(&p.B, fb, sB + 8192, rowB + 64, kb * BK);
+                            const bool second = END == FpEnd::Grad && a.kb_half && kb >= a.kb_half;
+                            const CUtensorMap* map = second ? &p.B2 : mapB;
+                            const int k = second ? kb - a.kb_half : kb;
+                            tma_load_2d_pair(map, fb, sB, rowB, k * BK);
+                            tma_load_2d_pair(map, fb, sB + 8192, rowB + 64, k * BK);
                         }
                     }
                     __syncwarp();
@@ -739,10 +924,11 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
         bool ok = true;
         for (int k = 0; ok && work.item(k, cluster, nclusters, problem, item); ++k) {
             const FpProblem& p = PROBLEMS == 1 || problem == 0 ? work.p[0] : work.p[LAST];
-            int row, col;
-            place(p.a, item, row, col);
-            drain_tile(
-                p.a, &p.Y, &p.Z, &p.S, p.a.splits > 1 ? item % p.a.splits : -1, st, part, Cfg::EPI_WARPS / 4, p.a.bn, col, row + quad * 32,
+            int row, col, half;
+            place(p.a, item, row, col, half);
+            drain_tile<END>(
+                p, p.a.splits > 1 ? item % p.a.splits : -1, half, st, part, Cfg::EPI_WARPS / 4,
+                END == FpEnd::Gated ? p.a.cols : p.a.bn, col, row + quad * 32,
                 tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN),
                 [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err); },
                 [&] { if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
@@ -760,30 +946,93 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
 
 // ------------------------------------------------------- the slices' sum and epilogue
 
-// P [splits][M][pitch]: four columns to a thread, the slices added in their order
+// P [splits][M][pitch], or [splits][2][M][pitch] with a second sum of each element or for each half:
+// four columns to a thread, the slices added in their order. `stride`: from slice to slice
+__device__ __forceinline__ float4 add_slices(const float* src, int splits, int64_t stride)
+{
+    float4 s = __ldcs(reinterpret_cast<const float4*>(src));
+    for (int q = 1; q < splits; ++q) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(src + q * stride));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    return s;
+}
+
+template <FpEnd END>
 __global__ void __launch_bounds__(256)
-    k_fp_join(const float* __restrict__ P, int splits, int64_t stride, int pitch, int M, int N, const FpEpilogue e)
+    k_fp_join(const float* __restrict__ P, int splits, int64_t stride, int pitch, const __grid_constant__ FpGemmArgs a)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int quads = pitch / 4;
+    const int quads = pitch / 4, M = a.M, N = a.N;
+    const FpEpilogue& e = a.e;
     const int64_t n = (int64_t)M * quads;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = i / quads;
         const int c = (int)(i - r * quads) * 4;
-        const float* src = P + r * pitch + c;
-        float4 s = __ldcs(reinterpret_cast<const float4*>(src));
-        for (int q = 1; q < splits; ++q) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(src + q * stride));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
+        const float4 s = add_slices(P + r * pitch + c, splits, stride);
         const float v[4] = {s.x, s.y, s.z, s.w};
+        if (END == FpEnd::Linear) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < N) fp_finish(e, r, c + j, v[j]);
+            for (int j = 0; j < 4; ++j)
+                if (c + j < N) fp_finish(e, r, c + j, v[j]);
+        } else if (END == FpEnd::Gated) {
+            const float4 t = add_slices(P + (int64_t)M * pitch + r * pitch + c, splits, stride);
+            const float u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < N) fp_finish_gated(e, a.x, r, c + j, v[j], u[j]);
+        } else if (END == FpEnd::DLogits) {
+            SlopeRow row;
+            row.load(a, (int)r, c == 0 && a.x.first == 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < N) store_typed(e.y, e.type, r * e.ldy + c + j, row.at(v[j], c + j));
+        } else {
+            const float alpha = a.x.alpha ? *a.x.alpha : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < N) {
+                    float y = v[j] * alpha;
+                    if (a.x.acc) y += a.x.acc[r * a.x.ldacc + c + j];
+                    store_typed(e.y, e.out_type, r * e.ldy + c + j, y);
+                }
+        }
+    }
+}
+
+// A block to a row: its sums' largest, sum of exponentials and target's
+__global__ void __launch_bounds__(256)
+    k_fp_join_loss(const float* __restrict__ P, int splits, int64_t stride, int pitch, const __grid_constant__ FpGemmArgs a)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    __shared__ float ms[8], ss[8];
+    const int64_t r = blockIdx.x;
+    const int target = a.x.targets[r];
+    float m = -INFINITY, s = 0.0f;
+    for (int c = threadIdx.x * 4; c < a.N; c += blockDim.x * 4) {
+        const float4 q = add_slices(P + r * pitch + c, splits, stride);
+        const float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (c + j >= a.N) break;
+            if (c + j == target) a.x.hit[r] = v[j];
+            fp_softmax_add(m, s, v[j], 1.0f);
+        }
+    }
+    fp_softmax_warp(m, s);
+    if ((threadIdx.x & 31) == 0) {
+        ms[threadIdx.x >> 5] = m;
+        ss[threadIdx.x >> 5] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) fp_softmax_add(m, s, ms[w], ss[w]);
+        a.x.part[r] = make_float2(m, s);
     }
 }
 
@@ -801,8 +1050,12 @@ struct FpPlan {
 // through memory at 4 TB/s. It orders the measured choices (us): 8192 x 4096 x 4096 142 with
 // 256 columns, 185 with 160; 2048 x 4096 x 4096 40 with 224, 53 with 256; 512 x 4096 x 4096 23 in
 // 128 x 128 tiles, 22 in pairs of 128 columns; 33 x 6080 x 5824 27 whole, 15 in three slices.
-static FpPlan fp_plan(int M, int N, int K, bool b_mn)
+// The gated layer's tiles have two sums to a result column (their widths are multiples of 64, so that
+// both of a row quarter's epilogue warps have columns); a result in halves has its row tiles twice.
+static FpPlan fp_plan(int M, int N, int K, bool b_mn, FpEnd end = FpEnd::Linear, int halves = 1)
 {
+    const bool gated = end == FpEnd::Gated;
+    const int sums = gated ? 2 : 1;              // of a result column
     const int num_kb = (K + 63) / 64, sms = num_sms(), pairs = sms / 2;
     FpPlan best{};
     double best_us = 1e30;
@@ -811,7 +1064,7 @@ static FpPlan fp_plan(int M, int N, int K, bool b_mn)
         for (int s = 1; s <= 16 && (s == 1 || num_kb / s >= 4); ++s) {
             const int per = (num_kb + s - 1) / s;
             if ((num_kb + per - 1) / per != s) continue;
-            const double join = s > 1 ? 2.5 + 2.0 * s * M * N * 4 / 4e6 : 0;
+            const double join = s > 1 ? 2.5 + 2.0 * s * M * N * 4 * sums * halves / 4e6 : 0;
             const double us = fixed + (double)((tiles * s + workers - 1) / workers) * per * kb_us + join;
             if (us < best_us) {
                 best_us = us;
@@ -819,17 +1072,19 @@ static FpPlan fp_plan(int M, int N, int K, bool b_mn)
             }
         }
     };
-    if (M > 128 && N > 64)
-        for (int bn = 256; bn >= 128; bn -= 32) {
-            const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + bn - 1) / bn);
+    if (M > 128 && N * sums > 64)
+        for (int bn = 256; bn >= 128; bn -= 32 * sums) {
+            const int cols = bn / sums;
+            const int64_t tiles = (int64_t)((M + 255) / 256) * halves * ((N + cols - 1) / cols);
             const int loaded = b_mn ? (bn + 127) / 128 * 128 : bn;
             const double kb_us = std::max(0.27 * bn / 256, (16.0 + loaded / 16.0) / 100);
             consider(true, bn, tiles, pairs, kb_us, 3);
         }
-    const int64_t row_tiles = (M + 127) / 128;
+    const int64_t row_tiles = (int64_t)((M + 127) / 128) * halves;
     const double a_kb = 16.0 * std::min(M, 128) / 128;
-    for (int bn = 128; bn >= 64; bn -= 64) {
-        const int64_t tiles = row_tiles * ((N + bn - 1) / bn);
+    for (int bn = 128; bn >= 64 * sums; bn -= 64) {
+        const int cols = bn / sums;
+        const int64_t tiles = row_tiles * ((N + cols - 1) / cols);
         const double kb_us = std::max(0.12, (a_kb + bn / 8.0) / 100);
         consider(false, bn, tiles, sms, kb_us, 4);
     }
@@ -838,12 +1093,24 @@ static FpPlan fp_plan(int M, int N, int K, bool b_mn)
 
 static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
-static size_t plan_bytes(const FpPlan& p, int M, int N)
+// planes of sums that a slice leaves
+static int planes(FpEnd end, int halves) { return end == FpEnd::Gated ? 2 : halves; }
+
+static size_t plan_bytes(const FpPlan& p, int M, int N, FpEnd end, int halves)
 {
-    return p.splits > 1 ? ((size_t)p.splits * M * pad4(N) * sizeof(float) + 255) & ~size_t(255) : 0;
+    return p.splits > 1 ? align256((size_t)p.splits * planes(end, halves) * M * pad4(N) * sizeof(float)) : 0;
 }
 
-size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn) { return plan_bytes(fp_plan(M, N, K, b_mn), M, N); }
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end, int halves)
+{
+    return plan_bytes(fp_plan(M, N, K, b_mn, end, halves), M, N, end, halves);
+}
+
+int fp_loss_parts(int M, int N, int K)
+{
+    const FpPlan p = fp_plan(M, N, K, false, FpEnd::Loss);
+    return p.splits > 1 ? 0 : 2 * ((N + p.bn - 1) / p.bn);     // (two warps to a tile's row)
+}
 
 // 2-D box map over a row-major tensor of 16-bit or 32-bit elements: rows of 128 bytes with the
 // 128-byte swizzle, or of 64 bytes with the 64-byte one
@@ -881,12 +1148,12 @@ static cudaError_t allow_smem(K kern, int bytes, OnEachDevice* set)
 }
 
 // Pairs that run at the same time: a figure of the kernel and this part, the same on each device of it.
-template <int PROBLEMS>
+template <int PROBLEMS, FpEnd END>
 static int max_pairs()
 {
     static std::atomic<int> most{0};
     static OnEachDevice ready;
-    const auto kern = k_fp_gemm_pair<PROBLEMS>;
+    const auto kern = k_fp_gemm_pair<PROBLEMS, END>;
     if (allow_smem(kern, FpPairCfg::SMEM_BYTES, &ready) != cudaSuccess) return 0;
     if (most) return most;
     cudaLaunchConfig_t q = {};
@@ -905,16 +1172,18 @@ static int max_pairs()
     return most;
 }
 
-template <int BN>
-static int launch_single(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& Y, const CUtensorMap& Z,
-                         const CUtensorMap& S, const FpGemmArgs& a, cudaStream_t s)
+static int halves_of(const FpProduct& c) { return c.a_half ? 2 : 1; }
+
+template <int BN, FpEnd END>
+static int launch_single(const FpProblem& q, cudaStream_t s)
 {
     static OnEachDevice ready;
-    if (allow_smem(k_fp_gemm<BN>, FpCfg<BN>::SMEM_BYTES, &ready) != cudaSuccess)
+    if (allow_smem(k_fp_gemm<BN, END>, FpCfg<BN>::SMEM_BYTES, &ready) != cudaSuccess)
         return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
-    const int64_t items = (int64_t)((a.M + 127) / 128) * ((a.N + BN - 1) / BN) * a.splits;
+    const FpGemmArgs& a = q.a;
+    const int64_t items = (int64_t)((a.M + 127) / 128) * a.halves * ((a.N + a.cols - 1) / a.cols) * a.splits;
     const int grid = items < num_sms() ? (int)items : num_sms();
-    launch_pdl(k_fp_gemm<BN>, grid, FpCfg<BN>::THREADS, FpCfg<BN>::SMEM_BYTES, s, A, B, Y, Z, S, a);
+    launch_pdl(k_fp_gemm<BN, END>, grid, FpCfg<BN>::THREADS, FpCfg<BN>::SMEM_BYTES, s, q);
     return launch_status("linear product");
 }
 
@@ -922,8 +1191,10 @@ static int launch_single(const CUtensorMap& A, const CUtensorMap& B, const CUten
 static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p, void* ws)
 {
     const FpEpilogue& e = c.e;
+    const bool gated = c.end == FpEnd::Gated;
     FpGemmArgs& a = q->a;
     a.e = e;
+    a.x = c.x;
     a.M = c.M;
     a.N = c.N;
     a.K = c.K;
@@ -931,32 +1202,48 @@ static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p, void*
     a.b_mn = c.B.mn;
     a.group = 16;
     a.bn = p.bn;
+    a.cols = gated ? p.bn / 2 : p.bn;
     a.splits = p.splits;
     a.kb_per_split = p.kb_per_split;
+    a.halves = halves_of(c);
+    a.a_half = c.a_half;
+    a.kb_half = c.k_half / 64;
     a.err = device_error_word();
     if (!a.err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const bool wide = e.out_type == ITO_F32;
-    a.y_tma = rows_aligned(e.y, e.ldy, wide ? 4 : 2, c.M);
+    const int out = wide ? 4 : 2;
+    a.y_tma = e.y && rows_aligned(e.y, e.ldy, out, c.M);
     a.z_tma = e.z && rows_aligned(e.z, e.ldz, 2, c.M);
+    void* const y2 = gated ? c.x.z2 : c.x.y2;
+    const int64_t ldy2 = gated ? c.x.ldz2 : c.x.ldy2;
+    a.y2_tma = a.z2_tma = y2 && rows_aligned(y2, ldy2, out, c.M);
     a.b_vec = aligned_to(e.bias, 16);
-    a.r_vec = e.residual && rows_aligned(e.residual, e.ldr, wide ? 4 : 2, c.M);
+    a.b2_vec = aligned_to(c.x.bias2, 16);
+    a.r_vec = c.x.acc ? rows_aligned(c.x.acc, c.x.ldacc, 4, c.M)
+                      : e.residual && rows_aligned(e.residual, e.ldr, out, c.M);
     a.idesc = fp_idesc(p.pair ? 256 : 128, p.bn, c.A.mn, c.B.mn, e.type == ITO_BF16);
-    int r = box_map(&q->A, const_cast<void*>(c.A.p), false, c.A.mn ? c.K : c.M, c.A.mn ? c.M : c.K, c.A.ld,
+    const int64_t rows = c.a_half ? (int64_t)c.a_half + c.M : c.M;
+    int r = box_map(&q->A, const_cast<void*>(c.A.p), false, c.A.mn ? c.K : rows, c.A.mn ? rows : c.K, c.A.ld,
                     c.A.mn ? 64 : 128);
+    // (rows of a B in two halves end before its last K block does: those beyond come as 0)
+    const int64_t k_rows = c.k_half ? c.k_rows : c.K;
+    const int box = c.B.mn ? 64 : p.pair || gated ? p.bn / 2 : p.bn;
     if (!r)
-        r = box_map(&q->B, const_cast<void*>(c.B.p), false, c.B.mn ? c.K : c.N, c.B.mn ? c.N : c.K, c.B.ld,
-                    c.B.mn ? 64 : p.pair ? p.bn / 2 : p.bn);
+        r = box_map(&q->B, const_cast<void*>(c.B.p), false, c.B.mn ? k_rows : c.N, c.B.mn ? c.N : c.K, c.B.ld, box);
+    if (!r && c.B2.p)
+        r = box_map(&q->B2, const_cast<void*>(c.B2.p), false, c.B.mn ? k_rows : c.N, c.B.mn ? c.N : c.K, c.B2.ld, box);
     if (!r && a.y_tma) r = box_map(&q->Y, e.y, wide, c.M, c.N, e.ldy, 32, 64);
     if (!r && a.z_tma) r = box_map(&q->Z, e.z, false, c.M, c.N, e.ldz, 32, 64);
+    if (!r && a.y2_tma) r = box_map(&q->Y2, y2, wide, c.M, c.N, ldy2, 32, 64);
     if (!r && p.splits > 1) {
-        // the slices' sums [splits][M][pitch]
+        // the slices' sums [splits][planes][M][pitch]
         const int64_t pitch = pad4(c.N);
         auto enc = get_encode();
-        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)c.M, (cuuint64_t)p.splits};
+        cuuint64_t dims[3] = {(cuuint64_t)pitch, (cuuint64_t)c.M, (cuuint64_t)p.splits * planes(c.end, a.halves)};
         cuuint64_t strides[2] = {(cuuint64_t)pitch * 4, (cuuint64_t)pitch * c.M * 4};
-        cuuint32_t box[3] = {16, 32, 1};
+        cuuint32_t box3[3] = {16, 32, 1};
         cuuint32_t estr[3] = {1, 1, 1};
-        const CUresult cr = enc(&q->S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box, estr,
+        const CUresult cr = enc(&q->S, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ws, dims, strides, box3, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (cr != CUDA_SUCCESS) r = set_error(ITO_ERR_CUDA, "cuTensorMapEncodeTiled (partials) failed (%d)", (int)cr);
@@ -964,23 +1251,35 @@ static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p, void*
     return r;
 }
 
-static int run_join(const FpProduct& c, const FpPlan& p, const void* ws, cudaStream_t s)
+template <FpEnd END>
+static int run_join(const FpGemmArgs& given, const void* ws, cudaStream_t s)
 {
-    const int64_t pitch = pad4(c.N);
-    launch_pdl(k_fp_join, launch_grid_blocks((int64_t)c.M * (pitch / 4), 256), 256, 0, s, static_cast<const float*>(ws),
-               p.splits, pitch * c.M, (int)pitch, c.M, c.N, c.e);
-    return launch_status("linear join");
+    FpGemmArgs a = given;
+    const int64_t pitch = pad4(a.N), plane = pitch * a.M, stride = plane * planes(END, a.halves);
+    const float* P = static_cast<const float*>(ws);
+    if constexpr (END == FpEnd::Loss) {
+        launch_pdl(k_fp_join_loss, a.M, 256, 0, s, P, a.splits, stride, (int)pitch, a);
+        return launch_status("linear join");
+    } else {
+        for (int h = 0; h < a.halves; ++h) {
+            launch_pdl(k_fp_join<END>, launch_grid_blocks((int64_t)a.M * (pitch / 4), 256), 256, 0, s, P + h * plane,
+                       a.splits, stride, (int)pitch, a);
+            a.e.y = a.x.y2;
+            a.e.ldy = a.x.ldy2;
+        }
+        return launch_status("linear join");
+    }
 }
 
 static int pair_items(const FpProblem& q)
 {
-    return ((q.a.M + 255) / 256) * ((q.a.N + q.a.bn - 1) / q.a.bn) * q.a.splits;
+    return ((q.a.M + 255) / 256) * q.a.halves * ((q.a.N + q.a.cols - 1) / q.a.cols) * q.a.splits;
 }
 
-template <int PROBLEMS>
+template <int PROBLEMS, FpEnd END>
 static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
 {
-    const int most = max_pairs<PROBLEMS>();
+    const int most = max_pairs<PROBLEMS, END>();
     if (!most) return set_error(ITO_ERR_CUDA, "no CTA pair fits on this device");
     const int items = w.items[0] + w.items[1], pairs = items < most ? items : most;
     w.rest = w.gap = 0;
@@ -1003,51 +1302,65 @@ static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp_gemm_pair<PROBLEMS>, w);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_fp_gemm_pair<PROBLEMS, END>, w);
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "linear product launch: %s", cudaGetErrorString(e));
 }
 
-int fp_gemm(const FpProduct* c, int n, void* ws, cudaStream_t s)
+template <FpEnd END>
+static int run_products(const FpProduct* c, int n, void* ws, cudaStream_t s)
 {
     FpPlan p[2];
+    FpProblem q[2];
     void* at[2];
     for (int i = 0; i < n; ++i) {
-        p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn);
+        p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn, END, halves_of(c[i]));
         at[i] = ws;
-        ws = static_cast<char*>(ws) + plan_bytes(p[i], c[i].M, c[i].N);
-    }
-    const bool both = n == 2 && p[0].pair && p[1].pair;
-    if (both) {
-        FpPairWork<2> w;
-        memset(&w, 0, sizeof(w));
-        const int first = p[0].kb_per_split >= p[1].kb_per_split ? 0 : 1;
-        for (int i = 0; i < 2; ++i) {
-            const int r = fill_problem(&w.p[i], c[first ^ i], p[first ^ i], at[first ^ i]);
-            if (r) return r;
-            w.items[i] = pair_items(w.p[i]);
-        }
-        const int r = launch_pairs(w, s);
+        ws = static_cast<char*>(ws) + plan_bytes(p[i], c[i].M, c[i].N, END, halves_of(c[i]));
+        memset(&q[i], 0, sizeof(q[i]));
+        const int r = fill_problem(&q[i], c[i], p[i], at[i]);
         if (r) return r;
+    }
+    constexpr bool TWO = END == FpEnd::Linear || END == FpEnd::Grad;
+    const bool both = TWO && n == 2 && p[0].pair && p[1].pair;
+    if constexpr (TWO) {
+        if (both) {
+            FpPairWork<2> w;
+            const int first = p[0].kb_per_split >= p[1].kb_per_split ? 0 : 1;
+            for (int i = 0; i < 2; ++i) {
+                w.p[i] = q[first ^ i];
+                w.items[i] = pair_items(w.p[i]);
+            }
+            const int r = launch_pairs<2, END>(w, s);
+            if (r) return r;
+        }
     }
     for (int i = 0; i < n; ++i) {
         int r = ITO_OK;
         if (!both && p[i].pair) {
             FpPairWork<1> w;
-            memset(&w, 0, sizeof(w));
-            r = fill_problem(&w.p[0], c[i], p[i], at[i]);
-            w.items[0] = pair_items(w.p[0]);
-            if (!r) r = launch_pairs(w, s);
+            w.p[0] = q[i];
+            w.items[0] = pair_items(q[i]);
+            w.items[1] = 0;
+            r = launch_pairs<1, END>(w, s);
         } else if (!both) {
-            FpProblem q;
-            memset(&q, 0, sizeof(q));
-            r = fill_problem(&q, c[i], p[i], at[i]);
-            if (!r && p[i].bn == 128) r = launch_single<128>(q.A, q.B, q.Y, q.Z, q.S, q.a, s);
-            else if (!r) r = launch_single<64>(q.A, q.B, q.Y, q.Z, q.S, q.a, s);
+            if (END == FpEnd::Gated || p[i].bn == 128) r = launch_single<128, END>(q[i], s);
+            else if constexpr (END != FpEnd::Gated) r = launch_single<64, END>(q[i], s);
         }
-        if (!r && p[i].splits > 1) r = run_join(c[i], p[i], at[i], s);
+        if (!r && p[i].splits > 1) r = run_join<END>(q[i].a, at[i], s);
         if (r) return r;
     }
     return ITO_OK;
+}
+
+int fp_gemm(const FpProduct* c, int n, void* ws, cudaStream_t s)
+{
+    switch (c[0].end) {
+    case FpEnd::Gated: return run_products<FpEnd::Gated>(c, n, ws, s);
+    case FpEnd::Loss: return run_products<FpEnd::Loss>(c, n, ws, s);
+    case FpEnd::DLogits: return run_products<FpEnd::DLogits>(c, n, ws, s);
+    case FpEnd::Grad: return run_products<FpEnd::Grad>(c, n, ws, s);
+    default: return run_products<FpEnd::Linear>(c, n, ws, s);
+    }
 }
 
 }  // namespace ito
