@@ -9,12 +9,13 @@
 //
 // The gradient sums rows of dy that are far apart. Places are sorted by token first (stably, so the
 // order of every sum is the places' own and equal calls give equal bits; no atomics on the sums), then
-// a warp adds up the rows of a chunk of sorted places, column strip by column strip, and writes each
-// token's sum where the token changes. A token whose places go on beyond its chunk leaves pieces, which
-// a third kernel joins: a frequent token's thousands of rows are the work of many warps. While one
-// cluster of blocks sorts (in the order of 10 us, by latency), the rest of the device writes the zeros of
-// the tokens that do not occur.
+// warps add up the rows of chunks of sorted places, a strip of columns each, and write a token's sum where
+// the token changes. A token whose places go on into the next chunk leaves pieces, which are joined in
+// the block, and over blocks by a third kernel: a frequent token's thousands of rows are the work of many warps. The rows of
+// tokens that do not occur get zeros: some while the places are sorted, which leaves most of the device
+// idle, the rest beside the sums.
 #include <algorithm>
+#include <climits>
 
 #include "ito_float.cuh"
 
@@ -157,81 +158,166 @@ __global__ void __launch_bounds__(kEmbThreads)
 // `classes`, behind all others.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 8;
 constexpr int kZeroRows = 16384;     // rows of the table whose presence a block notes at a time
+// A few places are sorted by counting, for each, those that go before it: a comparison for each pair, on all
+// SMs, without a barrier between blocks (n = 2047: RANK_2047 us; the digits' passes SORT_2047).
+constexpr int kRankMost = 4096, kRankThreads = 256, kRankParts = 8, kRankPlaces = kRankThreads / kRankParts;
 
 struct EmbSort {
     const int32_t* ids;
     int n, classes, passes, blocks;  // blocks that sort
     int32_t* keys[2];                // [n] each: the last pass writes keys[0], places[0]
     int32_t* places[2];
-    void* table;                     // rows of absent tokens get zeros (null: they stay)
+    void* table;                     // its first zero_rows rows get zeros where the token is absent
+    int zero_rows;
     int64_t row_bytes, pitch_bytes;
     int wide;                        // 16-byte stores
     int* err;
 };
 
-__device__ __forceinline__ void emb_sort(const EmbSort& a)
+struct SortSums {
+    unsigned counts[kSortWarps][256];    // of a warp's digits, then where the warp's places of a digit begin
+    unsigned quarter[4][256], total[256], base[256], scan[8];
+};
+
+// From the warps' counts to where each warp's places of each digit begin: counts becomes the block's
+// exclusive sums over its warps, base[digit] the cluster's place of the block's first.
+__device__ __forceinline__ void sort_offsets(SortSums& q, int blocks, int block)
 {
-    __shared__ unsigned counts[kSortWarps][256];
-    __shared__ unsigned total[256], base[256], scan[8];
+    const int t = threadIdx.x, d = t & 255, lane = t & 31, warp = t >> 5;
+    constexpr int W = kSortWarps / 4;    // four threads to a digit
+    const int w0 = (t >> 8) * W;
+    unsigned c[W], sum = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) c[w] = q.counts[w0 + w][d];
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += c[w];
+    q.quarter[t >> 8][d] = sum;
+    __syncthreads();
+    unsigned first = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) first += i < t >> 8 ? q.quarter[i][d] : 0;
+    if (t >> 8 == 3) q.total[d] = first + sum;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        q.counts[w0 + w][d] = first;
+        first += c[w];
+    }
+    cluster_sync();
+    if (t < 256) {
+        unsigned of[kSortCluster], before = 0, all = 0;
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) {
+            of[b] = 0;
+            if (b < blocks)
+                asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                             : "=r"(of[b])
+                             : "r"(mapa_shared(smem_u32(&q.total[t]), b))
+                             : "memory");
+        }
+#pragma unroll
+        for (int b = 0; b < kSortCluster; ++b) {
+            if (b < block) before += of[b];
+            all += of[b];
+        }
+        unsigned inc = all;              // inclusive sums over the digits
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) q.scan[warp] = inc;
+        q.base[t] = before + inc - all;
+    }
+    __syncthreads();
+    if (t < 256) {
+        unsigned lower = 0;
+        for (int w = 0; w < warp; ++w) lower += q.scan[w];
+        q.base[t] += lower;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int emb_key(const EmbSort& a, int id) { return id >= 0 && id < a.classes ? id : a.classes; }
+
+// Up to 8192 R places (with a cluster of eight): R to a lane, kept in registers between the passes and
+// exchanged through the blocks' shared memory. Places beyond n have a key above all and stay the last.
+template <int R>
+__device__ __forceinline__ void emb_sort_held(const EmbSort& a, SortSums& q, int* exchange)
+{
+    constexpr int HOLD = R * kSortThreads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = (int)cluster_ctarank();
+    int* const xkeys = exchange;
+    int* const xplaces = exchange + HOLD;
+    int key[R], place[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        place[r] = block * HOLD + (warp * R + r) * 32 + lane;
+        key[r] = place[r] < a.n ? emb_key(a, __ldg(a.ids + place[r])) : INT_MAX;
+    }
+    for (int pass = 0; pass < a.passes; ++pass) {
+        unsigned rank[R];
+        for (int i = lane; i < 256; i += 32) q.counts[warp][i] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const unsigned digit = (unsigned)key[r] >> (8 * pass) & 255;
+            const unsigned same = __match_any_sync(0xffffffffu, digit);
+            const unsigned so_far = q.counts[warp][digit];
+            __syncwarp();
+            if (lane == __ffs(same) - 1) q.counts[warp][digit] = so_far + __popc(same);
+            __syncwarp();
+            rank[r] = so_far + __popc(same & ((1u << lane) - 1));
+        }
+        __syncthreads();
+        sort_offsets(q, a.blocks, block);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const unsigned digit = (unsigned)key[r] >> (8 * pass) & 255;
+            const int at = (int)(q.base[digit] + q.counts[warp][digit] + rank[r]);
+            if (pass + 1 < a.passes) {
+                const int to = at / HOLD, i = at % HOLD;
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(xkeys + i), to)), "r"(key[r])
+                             : "memory");
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(xplaces + i), to)), "r"(place[r])
+                             : "memory");
+            } else if (at < a.n) {
+                a.keys[0][at] = key[r];
+                a.places[0][at] = place[r];
+            }
+        }
+        cluster_sync();                  // the exchange is written, and the blocks' totals are read
+        if (pass + 1 < a.passes) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                key[r] = xkeys[(warp * R + r) * 32 + lane];
+                place[r] = xplaces[(warp * R + r) * 32 + lane];
+            }
+        }
+    }
+}
+
+// Any number of places, which go through memory from pass to pass.
+__device__ __forceinline__ void emb_sort(const EmbSort& a, SortSums& q)
+{
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = (int)cluster_ctarank();
     const int per = (a.n + a.blocks * kSortWarps - 1) / (a.blocks * kSortWarps);     // places of a warp
     const int64_t lo = (int64_t)(block * kSortWarps + warp) * per;
     const int64_t hi = min((int64_t)a.n, lo + per);
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 8 * pass, to = (a.passes - 1 - pass) & 1;
-        auto key_at = [&](int64_t i) -> int {
-            if (pass) return __ldcg(a.keys[to ^ 1] + i);
-            const int id = a.ids[i];
-            return id >= 0 && id < a.classes ? id : a.classes;
-        };
-        for (int i = threadIdx.x; i < kSortWarps * 256; i += kSortThreads) (&counts[0][0])[i] = 0;
-        __syncthreads();
+        auto key_at = [&](int64_t i) -> int { return pass ? __ldcg(a.keys[to ^ 1] + i) : emb_key(a, a.ids[i]); };
+        for (int i = lane; i < 256; i += 32) q.counts[warp][i] = 0;
+        __syncwarp();
         for (int64_t i = lo; i < hi; i += 32) {
             const bool in = i + lane < hi;
             const int key = in ? key_at(i + lane) : 0;
             const unsigned digit = in ? (unsigned)key >> shift & 255 : 256;
             const unsigned same = __match_any_sync(0xffffffffu, digit);
-            if (in && lane == __ffs(same) - 1) counts[warp][digit] += __popc(same);
+            if (in && lane == __ffs(same) - 1) q.counts[warp][digit] += __popc(same);
             __syncwarp();
         }
         __syncthreads();
-        if (threadIdx.x < 256) {
-            unsigned sum = 0;
-            for (int w = 0; w < kSortWarps; ++w) {
-                const unsigned c = counts[w][threadIdx.x];
-                counts[w][threadIdx.x] = sum;
-                sum += c;
-            }
-            total[threadIdx.x] = sum;
-        }
-        cluster_sync();
-        if (threadIdx.x < 256) {
-            unsigned before = 0, all = 0;
-            for (int b = 0; b < a.blocks; ++b) {
-                unsigned c;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                             : "=r"(c)
-                             : "r"(mapa_shared(smem_u32(&total[threadIdx.x]), b))
-                             : "memory");
-                if (b < block) before += c;
-                all += c;
-            }
-            unsigned inc = all;              // inclusive sums over the digits
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned c = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += c;
-            }
-            if (lane == 31) scan[warp] = inc;
-            base[threadIdx.x] = before + inc - all;
-        }
-        __syncthreads();
-        if (threadIdx.x < 256) {
-            unsigned lower = 0;
-            for (int w = 0; w < warp; ++w) lower += scan[w];
-            base[threadIdx.x] += lower;
-        }
-        __syncthreads();
+        sort_offsets(q, a.blocks, block);
         for (int64_t i = lo; i < hi; i += 32) {
             const bool in = i + lane < hi;
             const int key = in ? key_at(i + lane) : 0;
@@ -239,15 +325,24 @@ __device__ __forceinline__ void emb_sort(const EmbSort& a)
             const unsigned digit = in ? (unsigned)key >> shift & 255 : 256;
             const unsigned same = __match_any_sync(0xffffffffu, digit);
             if (in) {
-                const unsigned at = base[digit] + counts[warp][digit] + __popc(same & ((1u << lane) - 1));
+                const unsigned at = q.base[digit] + q.counts[warp][digit] + __popc(same & ((1u << lane) - 1));
                 a.keys[to][at] = key;
                 a.places[to][at] = place;
             }
             __syncwarp();
-            if (in && lane == __ffs(same) - 1) counts[warp][digit] += __popc(same);
+            if (in && lane == __ffs(same) - 1) q.counts[warp][digit] += __popc(same);
             __syncwarp();
         }
         cluster_sync();                      // the pass is written, and the blocks' totals are read
+    }
+}
+
+__device__ __forceinline__ void zero_row(char* row, int64_t bytes, bool wide, int lane)
+{
+    if (wide) {
+        for (int64_t i = lane * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(row + i) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        for (int64_t i = lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
     }
 }
 
@@ -256,66 +351,149 @@ __device__ __forceinline__ void emb_zero(const EmbSort& a, int b, int blocks)
 {
     __shared__ unsigned there[kZeroRows / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (a.classes + blocks - 1) / blocks;
-    const int64_t end = min((int64_t)a.classes, (int64_t)(b + 1) * per);
+    const int per = (a.zero_rows + blocks - 1) / blocks, threads = blockDim.x;
+    const int64_t end = min((int64_t)a.zero_rows, (int64_t)(b + 1) * per);
     for (int64_t r0 = (int64_t)b * per; r0 < end; r0 += kZeroRows) {
         const int rows = (int)min((int64_t)kZeroRows, end - r0);
         __syncthreads();
-        for (int i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) there[i] = 0;
+        for (int i = threadIdx.x; i < (rows + 31) / 32; i += threads) there[i] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < a.n; i += kSortThreads) {
-            const int64_t r = a.ids[i] - r0;
-            if (r >= 0 && r < rows) atomicOr(&there[r >> 5], 1u << (r & 31));
+        for (int64_t i0 = threadIdx.x; i0 < a.n; i0 += 8 * threads) {
+            int id[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) id[u] = i0 + u * threads < a.n ? __ldg(a.ids + i0 + u * threads) : -1;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int64_t r = id[u] - r0;
+                if (id[u] >= 0 && r >= 0 && r < rows) atomicOr(&there[r >> 5], 1u << (r & 31));
+            }
         }
         __syncthreads();
-        for (int r = warp; r < rows; r += kSortWarps) {
+        for (int r = warp; r < rows; r += threads / 32) {
             if (there[r >> 5] >> (r & 31) & 1) continue;
-            char* row = static_cast<char*>(a.table) + (r0 + r) * a.pitch_bytes;
-            if (a.wide) {
-                for (int64_t i = lane * 16; i < a.row_bytes; i += 512)
-                    *reinterpret_cast<uint4*>(row + i) = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                for (int64_t i = lane * 2; i < a.row_bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
-            }
+            zero_row(static_cast<char*>(a.table) + (r0 + r) * a.pitch_bytes, a.row_bytes, a.wide, lane);
         }
     }
 }
 
+__device__ __forceinline__ void check_ids(const EmbSort& a, int first, int step)
+{
+    for (int i = first; i < a.n; i += step) {
+        const int id = a.ids[i];
+        if (id < -1 || id >= a.classes) raise_device_error(a.err, ITO_ERR_ARG);
+    }
+}
+
+// R: places a lane holds (0: they go through memory)
+template <int R>
 __global__ void __launch_bounds__(kSortThreads) k_emb_sort(const __grid_constant__ EmbSort a)
 {
+    extern __shared__ int exchange[];
+    __shared__ SortSums sums;
     griddep_wait();
     griddep_launch_dependents();
     if ((int)blockIdx.x < a.blocks) {
-        for (int i = blockIdx.x * kSortThreads + threadIdx.x; i < a.n; i += a.blocks * kSortThreads) {
-            const int id = a.ids[i];
-            if (id < -1 || id >= a.classes) raise_device_error(a.err, ITO_ERR_ARG);
-        }
-        emb_sort(a);
+        if constexpr (R > 0) emb_sort_held<R>(a, sums, exchange);
+        else emb_sort(a, sums);
+        check_ids(a, blockIdx.x * kSortThreads + threadIdx.x, a.blocks * kSortThreads);
     } else {
         emb_zero(a, (int)blockIdx.x - a.blocks, (int)gridDim.x - a.blocks);
     }
 }
 
+// Eight threads to a place, each of which compares a share of the keys: those that are smaller, or equal and
+// earlier, go before it.
+__global__ void __launch_bounds__(kRankThreads) k_emb_rank(const __grid_constant__ EmbSort a)
+{
+    __shared__ int4 keys[kRankMost / 4];
+    griddep_wait();
+    griddep_launch_dependents();
+    if ((int)blockIdx.x >= a.blocks) {
+        emb_zero(a, (int)blockIdx.x - a.blocks, (int)gridDim.x - a.blocks);
+        return;
+    }
+    if (blockIdx.x == 0) check_ids(a, threadIdx.x, kRankThreads);
+    const int vecs = (a.n + 4 * kRankParts - 1) / (4 * kRankParts) * kRankParts;     // padded with keys above all
+    for (int i0 = threadIdx.x; i0 < 4 * vecs; i0 += 8 * kRankThreads) {
+        int id[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) id[u] = i0 + u * kRankThreads < a.n ? __ldg(a.ids + i0 + u * kRankThreads) : -1;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kRankThreads, key = id[u] >= 0 && id[u] < a.classes ? id[u] : a.classes;
+            if (i < 4 * vecs) reinterpret_cast<int*>(keys)[i] = i < a.n ? key : INT_MAX;
+        }
+    }
+    __syncthreads();
+    const int place = blockIdx.x * kRankPlaces + threadIdx.x / kRankParts, part = threadIdx.x % kRankParts;
+    const int mine = place < a.n ? reinterpret_cast<const int*>(keys)[place] : 0;
+    int before = 0;
+#pragma unroll 4
+    for (int v = part; v < vecs; v += kRankParts) {
+        const int4 k = keys[v];
+        // keys of earlier places go before an equal one (those behind it in its own vector are taken out below)
+        const int limit = 4 * v < place ? mine + 1 : mine;
+        before += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+    }
+    if (place < a.n && place / 4 % kRankParts == part)
+        for (int i = place; i < (place | 3) + 1; ++i)
+            before -= place % 4 != 0 && reinterpret_cast<const int*>(keys)[i] == mine;
+#pragma unroll
+    for (int o = 1; o < kRankParts; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (place < a.n && part == 0) {
+        a.keys[0][before] = mine;
+        a.places[0][before] = place;
+    }
+}
+
 // ----------------------------------------------------------- sums of sorted places
 
-// A warp's chunk of sorted places holds runs of equal tokens. A run that began before the chunk leaves
-// its sum in head[chunk]; one that begins in the chunk and goes on behind it in tail[chunk]; others
-// are whole and go to the table.
+// A block adds the rows of a span of sorted places, a chunk to each warp. A run of equal tokens that begins
+// and ends in a chunk is whole and goes to the table; the pieces of one that goes on into the next chunks
+// meet in shared memory, in their order. What began before the span leaves its sum in head[span], what
+// goes on behind it in tail[span], for k_emb_join.
 constexpr int kSumThreads = 256;
+constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kSumAhead = 4;         // rows of dy whose loads are in flight together
 
 struct EmbSum {
     const int32_t *keys, *places;
-    int n, classes, d, chunk, chunks, strips;
+    int n, classes, d, strips;
+    int chunk, span, spans;          // places of a warp, of a block; blocks' worth of places
     const void* dy;
     int64_t lddy;
     float scale;
     int add;
     void* table;
     int64_t ldt;
-    float *head, *tail;              // [chunks][pitch]
+    float *head, *tail;              // [spans][pitch]
     int pitch;
+    int sum_blocks;                  // the others write zeros to the rows from zero_from on
+    int zero_from, wide;
+    int64_t row_bytes, pitch_bytes;
 };
+
+// The rows of absent tokens, kZeroWarpRows to a warp (32: 190 us instead of SUM_ZERO for 16384 x 4096 and
+// 32768 tokens, too few warps to keep the memory busy): each lane looks its row up among the sorted keys
+constexpr int kZeroWarpRows = 4;
+
+__device__ __forceinline__ void emb_zero_rest(const EmbSum& a, int64_t warp, int lane)
+{
+    const int64_t r0 = a.zero_from + warp * kZeroWarpRows, row = r0 + lane;
+    bool absent = false;
+    if (lane < kZeroWarpRows && row < a.classes) {
+        int lo = 0, hi = a.n;                        // the first key that is not below `row` is in lo .. hi
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (__ldg(a.keys + mid) < row) lo = mid + 1;
+            else hi = mid;
+        }
+        absent = lo == a.n || __ldg(a.keys + lo) != row;
+    }
+    const unsigned rows = __ballot_sync(0xffffffffu, absent);
+    for (int i = 0; i < kZeroWarpRows; ++i)
+        if (rows >> i & 1) zero_row(static_cast<char*>(a.table) + (r0 + i) * a.pitch_bytes, a.row_bytes, a.wide, lane);
+}
 
 template <typename O, bool VEC>
 __device__ __forceinline__ void emb_put(const EmbSum& a, int key, int strip, int lane, const float (&s)[8])
@@ -343,28 +521,41 @@ __device__ __forceinline__ void piece_store(float* p, const float (&s)[8])
     reinterpret_cast<float4*>(p)[1] = make_float4(s[4], s[5], s[6], s[7]);
 }
 
+__device__ __forceinline__ void add_piece(float (&s)[8], const float* p)
+{
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+    s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+}
+
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(kSumThreads) k_emb_sum(const __grid_constant__ EmbSum a)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t unit = (int64_t)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (unit >= (int64_t)a.chunks * a.strips) return;
-    const int chunk = (int)(unit / a.strips), strip = (int)(unit % a.strips);
-    const int lo = chunk * a.chunk, len = min(a.chunk, a.n - lo);
+    __shared__ float heads[kSumWarps][256], tails[kSumWarps][256];
+    __shared__ int state[kSumWarps];                 // of a warp's chunk: it has a head, that goes on; it has a tail
+    constexpr int HEAD = 1, ON = 2, TAIL = 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= a.sum_blocks) {
+        emb_zero_rest(a, (int64_t)(blockIdx.x - a.sum_blocks) * kSumWarps + warp, lane);
+        return;
+    }
+    const int span = (int)(blockIdx.x / a.strips), strip = (int)(blockIdx.x % a.strips);
+    const int64_t lo = (int64_t)span * a.span + warp * a.chunk;
+    const int len = (int)max((int64_t)0, min((int64_t)a.chunk, a.n - lo));
     // (a chunk has 32 places at most: one to a lane)
     const int mine = lane < len ? __ldg(a.keys + lo + lane) : a.classes;
     const int place = lane < len ? __ldg(a.places + lo + lane) : 0;
     int before = -1, after = -1;
-    if (lo > 0) before = __ldg(a.keys + lo - 1);
+    if (lo > 0 && len) before = __ldg(a.keys + lo - 1);
     if (lo + len < a.n) after = __ldg(a.keys + lo + len);
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    bool from_before = before == __shfl_sync(0xffffffffu, mine, 0);
-    const int64_t at = (int64_t)chunk * a.pitch + strip * 256 + lane * 8;
-    for (int i0 = 0; i0 < len; i0 += kSumAhead) {
+    bool from_before = before == __shfl_sync(0xffffffffu, mine, 0), none = false;
+    int st = 0, tail_key = 0;
+    for (int i0 = 0; i0 < len && !none; i0 += kSumAhead) {
         Eight<T> e[kSumAhead];
 #pragma unroll
         for (int u = 0; u < kSumAhead; ++u) {
@@ -378,77 +569,108 @@ __global__ void __launch_bounds__(kSumThreads) k_emb_sum(const __grid_constant__
             const int i = i0 + u;
             if (i >= len) break;
             const int key = __shfl_sync(0xffffffffu, mine, i);
-            if (key >= a.classes) return;            // places without a token are the last
+            none = key >= a.classes;                 // places without a token are the last
+            if (none) break;
             float f[8];
             e[u].get(f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] += f[j];
             const int next = i + 1 < len ? __shfl_sync(0xffffffffu, mine, i + 1 & 31) : after;
             if (next == key && i + 1 < len) continue;
-            if (from_before) piece_store(a.head + at, s);
-            else if (next == key) piece_store(a.tail + at, s);
-            else emb_put<O, VEC>(a, key, strip, lane, s);
+            if (from_before) {
+                piece_store(&heads[warp][lane * 8], s);
+                st |= next == key ? HEAD | ON : HEAD;
+            } else if (next == key) {
+                piece_store(&tails[warp][lane * 8], s);
+                st |= TAIL;
+                tail_key = key;
+            } else {
+                emb_put<O, VEC>(a, key, strip, lane, s);
+            }
             from_before = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = 0.0f;
         }
     }
+    if (lane == 0) state[warp] = st;
+    __syncthreads();
+    const int64_t at = (int64_t)span * a.pitch + strip * 256 + lane * 8;
+    // a run from this warp's tail on, and (warp 0) the one from before the span
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (which ? warp || !(st & HEAD) : !(st & TAIL)) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+        add_piece(s, which ? &heads[0][lane * 8] : &tails[warp][lane * 8]);
+        bool on = which ? st & ON : true;
+        for (int w = warp + 1; on && w < kSumWarps; ++w) {
+            add_piece(s, &heads[w][lane * 8]);
+            on = state[w] & ON;
+        }
+        if (which) piece_store(a.head + at, s);
+        else if (on) piece_store(a.tail + at, s);
+        else emb_put<O, VEC>(a, tail_key, strip, lane, s);
+    }
 }
 
-// A block to a chunk's strip: where a token's run begins in the chunk and goes on, its pieces are
-// added, a share of the chunks that it goes on through to each warp, and the shares in their order.
+// A block to eight strips of a span: where a token's run begins in the span and goes on, its pieces are
+// added. Of a few pieces each warp adds its strip's; of many (a run through kJoinAlone spans and more)
+// every strip's are shared among the warps, and the shares added in their order.
+constexpr int kJoinWarps = kSumThreads / 32, kJoinAlone = 64;
+
 template <typename O, bool VEC>
 __global__ void __launch_bounds__(kSumThreads) k_emb_join(const __grid_constant__ EmbSum a)
 {
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int WARPS = kSumThreads / 32;
-    __shared__ float part[WARPS][256];
-    const int chunk = (int)(blockIdx.x / a.strips), strip = (int)(blockIdx.x % a.strips);
+    __shared__ float part[kJoinWarps][256];
+    const int groups = (a.strips + kJoinWarps - 1) / kJoinWarps;
+    const int span = (int)(blockIdx.x / groups), strip0 = (int)(blockIdx.x % groups) * kJoinWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int end = (chunk + 1) * a.chunk;           // the chunk's last place is end - 1; (end <= n - 1 here)
-    const int key = __ldg(a.keys + end - 1);
+    const int end = (span + 1) * a.span;             // the span's last place is end - 1 (and end < n here)
+    const int key = __ldg(a.keys + end - 1), first = __ldg(a.keys + span * a.span);
+    const int before = span > 0 ? __ldg(a.keys + span * a.span - 1) : -1;
     if (key >= a.classes || __ldg(a.keys + end) != key) return;
-    if (chunk > 0 && __ldg(a.keys + chunk * a.chunk) == key && __ldg(a.keys + chunk * a.chunk - 1) == key) return;
-    // the run's end: the first place from `end` on with another key, 32 guesses at a time
-    int lo = end, hi = a.n;                          // keys[lo] == key; the end is in lo + 1 .. hi
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int64_t guess = lo + (int64_t)step * (lane + 1);
-        const unsigned same = __ballot_sync(0xffffffffu, guess < hi && __ldg(a.keys + guess) == key);
-        const int got = __popc(same);                // (the keys are sorted: a prefix of the guesses)
-        const int64_t up = lo + (int64_t)step * (got + 1);
-        lo += step * got;
-        hi = (int)min((int64_t)hi, up);
+    if (first == key && before == key) return;
+    // the span that the run ends in: 32 spans at a time, those at whose ends it goes on (a prefix of them)
+    int last = span + 1;
+    for (;;) {
+        const int64_t next = (int64_t)(last + lane + 1) * a.span;
+        const int on = __popc(__ballot_sync(0xffffffffu, next < a.n && __ldg(a.keys + next) == key));
+        last += on;
+        if (on < 32) break;
     }
-    const int last = (hi - 1) / a.chunk;             // the chunk that the run ends in
-    const int more = last - chunk, per = (more + WARPS - 1) / WARPS;
-    const int64_t at = strip * 256 + lane * 8;
-    const int c0 = chunk + 1 + warp * per, c1 = min(last + 1, c0 + per);
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-    if (warp == 0) {
-        const float4* p = reinterpret_cast<const float4*>(a.tail + (int64_t)chunk * a.pitch + at);
-        const float4 x = p[0], y = p[1];
-        s[0] = x.x; s[1] = x.y; s[2] = x.z; s[3] = x.w;
-        s[4] = y.x; s[5] = y.y; s[6] = y.z; s[7] = y.w;
+    const int more = last - span;
+    if (more < kJoinAlone) {
+        const int strip = strip0 + warp;
+        if (strip >= a.strips) return;
+        const int64_t at = strip * 256 + lane * 8;
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        add_piece(s, a.tail + (int64_t)span * a.pitch + at);
+#pragma unroll 16
+        for (int c = span + 1; c <= last; ++c) add_piece(s, a.head + (int64_t)c * a.pitch + at);
+        emb_put<O, VEC>(a, key, strip, lane, s);
+        return;
     }
-#pragma unroll 4
-    for (int c = c0; c < c1; ++c) {
-        const float4* p = reinterpret_cast<const float4*>(a.head + (int64_t)c * a.pitch + at);
-        const float4 x = p[0], y = p[1];
-        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
-        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+    const int per = (more + kJoinWarps - 1) / kJoinWarps;
+    const int c0 = span + 1 + warp * per, c1 = min(last + 1, c0 + per);
+    for (int strip = strip0; strip < min(a.strips, strip0 + kJoinWarps); ++strip) {
+        const int64_t at = strip * 256 + lane * 8;
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (warp == 0) add_piece(s, a.tail + (int64_t)span * a.pitch + at);
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) add_piece(s, a.head + (int64_t)c * a.pitch + at);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[warp][lane * 8 + i] = s[i];
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += part[w][lane * 8 + i];
+            emb_put<O, VEC>(a, key, strip, lane, s);
+        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][lane * 8 + i] = s[i];
-    __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < WARPS; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += part[w][lane * 8 + i];
-    emb_put<O, VEC>(a, key, strip, lane, s);
 }
 
 // ------------------------------------------------------------------------ host
@@ -499,11 +721,49 @@ static int run_emb_fwd_to(int out_type, const int32_t* ids, int64_t n, const voi
 
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Places of a chunk: 32, or 8 where 32 would leave SMs without a warp's work.
-static int sum_chunk(int64_t n, int strips) { return n / 32 * strips >= 8 * kNumSMsHint ? 32 : 8; }
+// Bytes of zeros written while the places are sorted.
+constexpr int64_t kZeroBesideRank = 16 << 20, kZeroBesideSort = 112 << 20;
+
+// Places of a chunk: 32, or fewer down to 4 where that many would leave an SM fewer than 32 warps' work.
+static int sum_chunk(int64_t n, int strips)
+{
+    int chunk = 32;
+    while (chunk > 4 && n / chunk * strips < 32 * kNumSMsHint) chunk /= 2;
+    return chunk;
+}
+
+template <int R>
+static int run_emb_sort(EmbSort q, cudaStream_t s)
+{
+    constexpr int BYTES = R * kSortThreads * 8;
+    static OnEachDevice ready;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess)
+        e = ready.run(device, [&] { return cudaFuncSetAttribute(k_emb_sort<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES); });
+    if (e != cudaSuccess) return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    q.blocks = kSortCluster;
+    const int zero = (std::min(2 * num_sms(), q.zero_rows) + q.blocks - 1) / q.blocks * q.blocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(q.blocks + zero));
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = q.blocks;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, k_emb_sort<R>, q);
+    return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "embedding backward launch: %s", cudaGetErrorString(e));
+}
 
 struct EmbLayout {
-    int strips, chunk, chunks, pitch;
+    int strips, chunk, span, spans, pitch;
     size_t keys, pieces, bytes;      // of one array of keys or places; of heads or tails; of all
 };
 
@@ -512,21 +772,24 @@ static EmbLayout emb_layout(int64_t n, int d)
     EmbLayout l;
     l.strips = (d + 255) / 256;
     l.chunk = sum_chunk(n, l.strips);
-    l.chunks = (int)((n + l.chunk - 1) / l.chunk);
+    l.span = kSumWarps * l.chunk;
+    l.spans = (int)((n + l.span - 1) / l.span);
     l.pitch = l.strips * 256;
     l.keys = align256((size_t)n * 4);
-    l.pieces = align256((size_t)l.chunks * l.pitch * 4);
+    l.pieces = align256((size_t)l.spans * l.pitch * 4);
     l.bytes = 4 * l.keys + 2 * l.pieces;
     return l;
 }
 
 template <typename T, typename O>
-static int run_emb_sum(const EmbSum& a, bool vec, cudaStream_t s)
+static int run_emb_sum(EmbSum a, bool vec, cudaStream_t s)
 {
-    const int64_t units = (int64_t)a.chunks * a.strips, blocks = (units + kSumThreads / 32 - 1) / (kSumThreads / 32);
-    launch_pdl(vec ? k_emb_sum<T, O, true> : k_emb_sum<T, O, false>, (unsigned)blocks, kSumThreads, 0, s, a);
-    if (a.chunks > 1)
-        launch_pdl(vec ? k_emb_join<O, true> : k_emb_join<O, false>, (unsigned)((int64_t)(a.chunks - 1) * a.strips),
+    a.sum_blocks = a.spans * a.strips;
+    const int zero = (a.classes - a.zero_from + kZeroWarpRows * kSumWarps - 1) / (kZeroWarpRows * kSumWarps);
+    launch_pdl(vec ? k_emb_sum<T, O, true> : k_emb_sum<T, O, false>, (unsigned)(a.sum_blocks + zero), kSumThreads, 0, s, a);
+    const int groups = (a.strips + kJoinWarps - 1) / kJoinWarps;
+    if (a.spans > 1)
+        launch_pdl(vec ? k_emb_join<O, true> : k_emb_join<O, false>, (unsigned)((int64_t)(a.spans - 1) * groups),
                    kSumThreads, 0, s, a);
     return launch_status("embedding backward");
 }
@@ -573,7 +836,7 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     if (r) return r;
     if (out_type != type && out_type != ITO_F32) return set_error(ITO_ERR_ARG, "out_type must be type or ITO_F32");
     const EmbLayout l = emb_layout(n, d);
-    if ((int64_t)l.chunks * l.strips > INT32_MAX) return set_error(ITO_ERR_SHAPE, "too many elements");
+    if ((int64_t)l.spans * l.strips > INT32_MAX) return set_error(ITO_ERR_SHAPE, "too many elements");
     if (!workspace) return set_error(ITO_ERR_ARG, "workspace is NULL");
     if (!aligned_to(workspace, 256)) return set_error(ITO_ERR_ARG, "workspace not 256-byte aligned");
     if (workspace_bytes < l.bytes) return set_error(ITO_ERR_ARG, "workspace too small");
@@ -587,35 +850,29 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     q.n = (int)n;
     q.classes = classes;
     for (q.passes = 1; q.passes < 4 && (classes >> (8 * q.passes)); ++q.passes) {}
-    // 2048 places a block and more: fewer take the cluster's barriers longer than the places
-    for (q.blocks = 1; q.blocks < kSortCluster && q.blocks * 2048 < n; q.blocks *= 2) {}
     for (int i = 0; i < 2; ++i) {
         q.keys[i] = reinterpret_cast<int32_t*>(ws + i * l.keys);
         q.places[i] = reinterpret_cast<int32_t*>(ws + (2 + i) * l.keys);
     }
-    q.table = add ? nullptr : dtable;
+    const bool rank = n <= kRankMost;
+    q.table = dtable;
     q.row_bytes = (int64_t)d * type_bytes(out_type);
     q.pitch_bytes = ldt * (int64_t)type_bytes(out_type);
     q.wide = aligned_to(dtable, 16) && q.row_bytes % 16 == 0 && (classes == 1 || q.pitch_bytes % 16 == 0);
     q.err = err;
-    // zeros: a block to an SM beside the sorting cluster, and no more than there are rows
-    int zero = 0;
-    if (!add) zero = (std::min(2 * num_sms(), classes) + q.blocks - 1) / q.blocks * q.blocks;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(q.blocks + zero));
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = q.blocks;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_emb_sort, q);
-    if (e != cudaSuccess) return set_error(ITO_ERR_CUDA, "embedding backward launch: %s", cudaGetErrorString(e));
+    // zeros that take about as long as the sort
+    q.zero_rows = add ? 0 : (int)std::min<int64_t>(classes, (rank ? kZeroBesideRank : kZeroBesideSort) / q.row_bytes);
+    if (rank) {
+        q.blocks = (int)((n + kRankPlaces - 1) / kRankPlaces);
+        const int zero = std::min(4 * num_sms(), q.zero_rows);
+        launch_pdl(k_emb_rank, (unsigned)(q.blocks + zero), kRankThreads, 0, s, q);
+        r = launch_status("embedding backward");
+        if (r) return r;
+    } else {
+        r = n <= 8192 ? run_emb_sort<1>(q, s) : n <= 16384 ? run_emb_sort<2>(q, s) : n <= 32768 ? run_emb_sort<4>(q, s)
+            : n <= 65536 ? run_emb_sort<8>(q, s) : run_emb_sort<0>(q, s);
+        if (r) return r;
+    }
 
     EmbSum a{};
     a.keys = q.keys[0];
@@ -624,7 +881,8 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     a.classes = classes;
     a.d = d;
     a.chunk = l.chunk;
-    a.chunks = l.chunks;
+    a.span = l.span;
+    a.spans = l.spans;
     a.strips = l.strips;
     a.dy = dy;
     a.lddy = lddy;
@@ -635,6 +893,10 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     a.head = reinterpret_cast<float*>(ws + 4 * l.keys);
     a.tail = reinterpret_cast<float*>(ws + 4 * l.keys + l.pieces);
     a.pitch = l.pitch;
+    a.zero_from = add ? classes : q.zero_rows;
+    a.wide = q.wide;
+    a.row_bytes = q.row_bytes;
+    a.pitch_bytes = q.pitch_bytes;
     const bool vec = rows_in_eights(dy, type, lddy, n, d) && rows_in_eights(dtable, out_type, ldt, classes, d);
     if (type == ITO_F32) return run_emb_sum<float, float>(a, vec, s);
     if (type == ITO_BF16)

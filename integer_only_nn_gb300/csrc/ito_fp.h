@@ -81,7 +81,7 @@ int fp_loss_parts(int M, int N, int K);
 
 // ---- shared by the layers' entry points (ito_fp_linear.cu)
 
-// Rows whose starts TMA cannot address, copied to rows padded to 8 elements; up to three tensors
+// Rows whose starts TMA cannot address, copied to rows padded to 32 elements; up to three tensors
 // (blockIdx.z).
 constexpr int kFpCopies = 3;
 struct FpCopy {

@@ -167,16 +167,73 @@ __device__ __forceinline__ void store16(const float (&v)[32], int type, const CU
         return;
     }
     __syncwarp();
-    // half a warp to a row, a word of two columns to a lane
-    const int w = lane & 15;
-    for (int r = lane >> 4; r < 32 && row + r < M; r += 2) {
-        const uint32_t x = box_word(stg, r, w);
-        uint16_t* dst = static_cast<uint16_t*>(out) + (row + r) * ld + col + 2 * w;
-        if (col + 2 * w < N) dst[0] = (uint16_t)x;
-        if (col + 2 * w + 1 < N) dst[1] = (uint16_t)(x >> 16);
+    // half a warp to a row, a word of two columns to a lane; in a row that starts on an odd element the
+    // words are shifted by one, and its first element is stored alone
+    const int w = lane & 15, cols = min(32, N - col);
+    uint16_t* dst = static_cast<uint16_t*>(out) + (int64_t)(row + (lane >> 4)) * ld + col;
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+        uint32_t x[8], next[8];                  // eight rows' words before their stores
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = box_word(stg, r0 + 2 * k + (lane >> 4), w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) next[k] = __shfl_down_sync(0xffffffffu, x[k], 1, 16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k, dst += 2 * ld) {
+            const bool in = row + r0 + 2 * k + (lane >> 4) < M;
+            const bool odd = reinterpret_cast<uintptr_t>(dst) & 2;
+            const int at = 2 * w + odd;          // columns at and at + 1 of the box
+            const uint32_t y = odd ? __funnelshift_r(x[k], next[k], 16) : x[k];
+            if (in && at + 1 < cols) *reinterpret_cast<uint32_t*>(dst + at) = y;
+            if (in && at + 1 == cols) dst[at] = (uint16_t)y;
+            if (in && odd && w == 0) dst[0] = (uint16_t)x[k];
+        }
     }
     __syncwarp();
     if (lane == 0) bulk_commit();
+}
+
+// Two boxes side by side (64 columns, or 32 where there is one) by plain stores: a warp to a row, so a row's
+// store takes half as many accesses for its bytes as box by box (50001 x 787 sums of 333 products, us:
+// PLAIN_ONE by boxes, PLAIN_TWO by two). `which`: the box that v goes to; `flush`: it is the last.
+__device__ __forceinline__ void store16_plain(const float (&v)[32], int type, void* out, int64_t ld, FpStage& st, int which,
+                                              bool flush, int col, int row, int M, int N)
+{
+    const int lane = st.lane;
+    if (!which) {                                // (the boxes may still leave by TMA for another result)
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+    }
+    const uint32_t at = smem_u32(st.p + which * kFpBox) + lane * 64;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        st_shared_v4(at + ((j ^ (lane >> 1 & 3)) << 4), (int)pack16(type, v[8 * j], v[8 * j + 1]),
+                     (int)pack16(type, v[8 * j + 2], v[8 * j + 3]), (int)pack16(type, v[8 * j + 4], v[8 * j + 5]),
+                     (int)pack16(type, v[8 * j + 6], v[8 * j + 7]));
+    if (!flush) return;
+    __syncwarp();
+    const int cols = min(32 + 32 * which, N - col);
+    const uint8_t* box = st.p + (lane >> 4) * kFpBox;
+    uint16_t* dst = static_cast<uint16_t*>(out) + (int64_t)row * ld + col;
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 8) {
+        uint32_t x[8], next[8];                  // eight rows' words before their stores
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = box_word(box, r0 + k, lane & 15);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) next[k] = __shfl_down_sync(0xffffffffu, x[k], 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k, dst += ld) {
+            if (row + r0 + k >= M) break;
+            const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1 & 1);
+            const int c = 2 * lane + odd;        // columns c and c + 1
+            const uint32_t y = odd ? __funnelshift_r(x[k], next[k], 16) : x[k];
+            if (c + 1 < cols) *reinterpret_cast<uint32_t*>(dst + c) = y;
+            if (c + 1 == cols) dst[c] = (uint16_t)y;
+            if (odd && lane == 0) dst[0] = (uint16_t)x[k];
+        }
+    }
+    __syncwarp();
 }
 
 // 16 of the columns (half h) as 32-bit floats, staged
@@ -361,7 +418,9 @@ __device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32],
 }
 
 // a gradient's sums: *alpha sum + acc
-__device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int col, int row)
+// (the group is the `which`-th of two side by side, `last` of them)
+__device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int which, bool last,
+                                            int col, int row)
 {
     const FpGemmArgs& a = p.a;
     const FpEpilogue& e = a.e;
@@ -376,7 +435,8 @@ __device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float 
     void* y = half ? a.x.y2 : e.y;
     const int64_t ld = half ? a.x.ldy2 : e.ldy;
     if (e.out_type == ITO_F32) store32(v, map, tma, y, ld, st, col, row, a.M, a.N);
-    else store16(v, e.out_type, map, tma, y, ld, st, col, row, a.M, a.N);
+    else if (tma) store16(v, e.out_type, map, true, y, ld, st, col, row, a.M, a.N);
+    else store16_plain(v, e.out_type, y, ld, st, which, last, col - 32 * which, row, a.M, a.N);
 }
 
 // a warp's wait: one lane asks
@@ -487,6 +547,84 @@ struct SlopeRow {
     }
 };
 
+// The tensor cores cut off what a sum's 24 bits cannot hold, at each step of 16 k: a chain of 256 steps
+// leaves logits short by 2^-17 of their size, and lse by 1.5e-6 of its own (4096 x 4096 -> 32768). So a
+// Loss product's sums are taken out of tensor memory every kLossChunk K blocks and added up in registers,
+// rounded: one accumulator is added while the other fills.
+constexpr int kLossChunk = 16;
+
+// K blocks from one drain of the accumulator to the next
+template <FpEnd END>
+__device__ __forceinline__ int chunk_end(int kb, int hi)
+{
+    return END == FpEnd::Loss ? min(hi, kb + kLossChunk) : hi;
+}
+
+// A Loss tile's epilogue: as drain_tile, over all `chunks` of the tile's K range. ready() waits for a chunk's
+// sums and gives their place in tensor memory, done() tells that they are read.
+template <int MAX_COLS, typename Ready, typename Done>
+__device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStage& st, int first, int columns, int col0,
+                                           int row, int chunks, Ready ready, Done done, bool& ok)
+{
+    constexpr int GROUPS = MAX_COLS / 64;            // (two warps to a row quarter)
+    const FpGemmArgs& a = p.a;
+    const int lane = st.lane;
+    LossRow loss{row + lane < a.M ? a.x.targets[row + lane] : -1, -INFINITY, 0.0f};
+    float sum[GROUPS][32];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[g][i] = 0.0f;
+#pragma unroll 1
+    for (int q = 0; q < chunks; ++q) {
+        uint32_t taddr;
+        if (!ready(taddr)) {
+            ok = false;
+            return;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int c = (first + 2 * g) * 32;
+            if (c < columns) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {        // (16 at a time: the sums leave few registers)
+                    uint32_t v[16];
+                    tmem_ld16(taddr + c + 16 * h, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[g][16 * h + i] += __uint_as_float(v[i]);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        done();
+    }
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        const int c = (first + 2 * g) * 32;
+        if (c >= columns || row >= a.M || col0 + c >= a.N) continue;
+        if (slice < 0) {
+            loss.add(sum[g], col0 + c, a.N - col0 - c, a.x.hit + row + lane);
+            continue;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (col0 + c + 16 * h >= a.N) break;
+            uint8_t* stg = stage32(sum[g], h, st);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&p.S, stg, col0 + c + 16 * h, row, slice);
+                bulk_commit();
+            }
+        }
+    }
+    if (slice < 0 && row + lane < a.M)
+        a.x.part[(int64_t)(col0 / columns * 2 + first) * a.M + row + lane] = make_float2(loss.m, loss.s);
+}
+
 // The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
 // (row, col0), sums at `taddr`; `done` tells the issuing warp that the accumulator is drained. A
 // slice of K (slice >= 0) leaves its sums as they are, in the workspace. `half`: of a result in halves.
@@ -500,21 +638,24 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
     const bool res16 = END == FpEnd::Linear && slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
     uint32_t res[16];
     if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
-    LossRow loss{-1, -INFINITY, 0.0f};
     SlopeRow slope;
-    if (END == FpEnd::Loss && row + st.lane < a.M) loss.target = a.x.targets[row + st.lane];
     if (END == FpEnd::DLogits) slope.load(a, row + st.lane, first == 0 && col0 == 0 && a.x.first == 0);
     if (!wait()) {
         ok = false;
         return;
     }
     tc_fence_after();
+    // groups in turns, or (Grad) a run of consecutive ones for each of the `step` warps, two of which share their stores
+    const int each = (columns / 32 + step - 1) / step * 32;
+    const int from = END == FpEnd::Grad ? first * each : first * 32;
+    const int end = END == FpEnd::Grad ? min(columns, from + each) : columns;
+    const int by = END == FpEnd::Grad ? 32 : step * 32;
 #pragma unroll 1
-    for (int c = first * 32; c < columns; c += step * 32) {
+    for (int c = from; c < end; c += by) {
         float v[32], u[32];
         load_sums(taddr + c, v);
         if (END == FpEnd::Gated) load_sums(taddr + columns + c, u);
-        if (c + step * 32 >= columns) {
+        if (c + by >= end) {
             tc_fence_before();
             __syncwarp();
             done();
@@ -541,17 +682,22 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
             finish_group(a, &p.Y, &p.Z, v, res, st, col0 + c, row);
         } else if (END == FpEnd::Gated) {
             finish_gated(p, v, u, st, col0 + c, row);
-        } else if (END == FpEnd::Loss) {
-            loss.add(v, col0 + c, a.N - col0 - c, a.x.hit + row + st.lane);
         } else if (END == FpEnd::DLogits) {
             slope.apply(v, col0 + c);
             store16(v, a.e.type, &p.Y, true, a.e.y, a.e.ldy, st, col0 + c, row, a.M, a.N);
         } else {
-            finish_grad(p, half, v, st, col0 + c, row);
+            const int which = (c - from) >> 5 & 1;
+            finish_grad(p, half, v, st, which, which || c + 32 >= end || col0 + c + 32 >= a.N, col0 + c, row);
         }
     }
-    if (END == FpEnd::Loss && slice < 0 && row + st.lane < a.M)
-        a.x.part[(int64_t)(col0 / columns * step + first) * a.M + row + st.lane] = make_float2(loss.m, loss.s);
+}
+
+// Tells the pair's leader that this warp has read its part of an accumulator. What the arrival orders are reads of
+// tensor memory, complete since tcgen05.wait::ld; a release at the cluster's scope would wait for the warp's
+// stores to global memory as well: 2000 to 3000 cycles a tile, which bounds products of a short K.
+__device__ __forceinline__ void mbar_arrive_drained(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // ----------------------------------------------------------------- one CTA
@@ -663,25 +809,28 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1) k_fp_gemm(const __grid_
         const FpSteps step(a, smem_u32(smem), Cfg::A_BYTES);
         const uint32_t idesc = a.idesc;
         for (int w = blockIdx.x; ok && w < num_items; w += gridDim.x) {
-            const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
-            if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) break;
-            tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(buf * BN);
-            for (int kb = lo; kb < hi; ++kb) {
-                if (!ring_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
+            const int first = (w % a.splits) * a.kb_per_split, end = min(num_kb, first + a.kb_per_split);
+            for (int lo = first, hi; ok && lo < end; lo = hi) {
+                hi = chunk_end<END>(lo, end);
+                if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
-                if (elect_one()) {
+                const uint32_t d = tmem_base + (uint32_t)(buf * BN);
+                for (int kb = lo; kb < hi; ++kb) {
+                    if (!ring_wait(&full_bar[stage], phase, abort_flag, a.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        tc_mma_bf16(d, step.a(at, k), step.b(at, k), idesc, (kb > lo || k > 0) ? 1u : 0u);
-                    tc_commit(&empty_bar[stage]);
-                    if (kb + 1 == hi) tc_commit(&accf_bar[buf]);
+                        for (int k = 0; k < BK / 16; ++k)
+                            tc_mma_bf16(d, step.a(at, k), step.b(at, k), idesc, (kb > lo || k > 0) ? 1u : 0u);
+                        tc_commit(&empty_bar[stage]);
+                        if (kb + 1 == hi) tc_commit(&accf_bar[buf]);
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                if (++buf == 2) { buf = 0; buf_phase ^= 1; }
             }
-            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
         if (lane == 0) ring_landed(empty_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
     } else {
@@ -694,6 +843,22 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1) k_fp_gemm(const __grid_
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
             const int half = END == FpEnd::Grad && tm >= num_m;
+            if constexpr (END == FpEnd::Loss) {
+                const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
+                drain_loss<BN>(
+                    p, a.splits > 1 ? w % a.splits : -1, st, part, COLS, tn * COLS, tm * BM + quad * 32,
+                    (hi - lo + kLossChunk - 1) / kLossChunk,
+                    [&](uint32_t& taddr) {
+                        taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
+                        return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err);
+                    },
+                    [&] {
+                        if (lane == 0) mbar_arrive(&acce_bar[buf]);
+                        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+                    },
+                    ok);
+                continue;
+            }
             drain_tile<END>(
                 p, a.splits > 1 ? w % a.splits : -1, half, st, part, 2, COLS, tn * COLS,
                 (half ? tm - num_m : tm) * BM + quad * 32,
@@ -892,26 +1057,29 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
                 const FpGemmArgs& a = PROBLEMS == 1 || problem == 0 ? work.p[0].a : work.p[LAST].a;
                 const FpSteps step(a, smem_u32(smem), Cfg::A_BYTES);
                 const uint32_t idesc = a.idesc;
-                int lo, hi;
-                k_range(a, item, lo, hi);
-                if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, err)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * Cfg::MAX_BN);
-                for (int kb = lo; kb < hi; ++kb) {
-                    if (!ring_wait(&full_bar[stage], phase, abort_flag, err)) { ok = false; break; }
+                int first, end;
+                k_range(a, item, first, end);
+                for (int lo = first, hi; ok && lo < end; lo = hi) {
+                    hi = chunk_end<END>(lo, end);
+                    if (!ring_wait(&acce_bar[buf], buf_phase ^ 1, abort_flag, err)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
-                    if (elect_one()) {
+                    const uint32_t d = tmem_base + (uint32_t)(buf * Cfg::MAX_BN);
+                    for (int kb = lo; kb < hi; ++kb) {
+                        if (!ring_wait(&full_bar[stage], phase, abort_flag, err)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t at = (uint32_t)stage * (Cfg::STAGE_BYTES >> 4);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < BK / 16; ++q)
-                            tc_mma_bf16_pair(d, step.a(at, q), step.b(at, q), idesc, (kb > lo || q > 0) ? 1u : 0u);
-                        tc_commit_pair_mc(&empty_bar[stage], 0x3);
-                        if (kb + 1 == hi) tc_commit_pair_mc(&accf_bar[buf], 0x3);
+                            for (int q = 0; q < BK / 16; ++q)
+                                tc_mma_bf16_pair(d, step.a(at, q), step.b(at, q), idesc, (kb > lo || q > 0) ? 1u : 0u);
+                            tc_commit_pair_mc(&empty_bar[stage], 0x3);
+                            if (kb + 1 == hi) tc_commit_pair_mc(&accf_bar[buf], 0x3);
+                        }
+                        __syncwarp();
+                        if (++stage == STAGES) { stage = 0; phase ^= 1; }
                     }
-                    __syncwarp();
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                    if (++buf == 2) { buf = 0; buf_phase ^= 1; }
                 }
-                if (++buf == 2) { buf = 0; buf_phase ^= 1; }
             }
             if (lane == 0) ring_landed(empty_bar, STAGES, RingPlace{stage, phase}.lap_before(), STAGES);
         }
@@ -926,12 +1094,29 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
             const FpProblem& p = PROBLEMS == 1 || problem == 0 ? work.p[0] : work.p[LAST];
             int row, col, half;
             place(p.a, item, row, col, half);
+            if constexpr (END == FpEnd::Loss) {
+                int lo, hi;
+                k_range(p.a, item, lo, hi);
+                drain_loss<Cfg::MAX_BN>(
+                    p, p.a.splits > 1 ? item % p.a.splits : -1, st, part, p.a.bn, col, row + quad * 32,
+                    (hi - lo + kLossChunk - 1) / kLossChunk,
+                    [&](uint32_t& taddr) {
+                        taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN);
+                        return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err);
+                    },
+                    [&] {
+                        if (lane == 0) mbar_arrive_drained(mapa_shared(smem_u32(&acce_bar[buf]), 0));
+                        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+                    },
+                    ok);
+                continue;
+            }
             drain_tile<END>(
                 p, p.a.splits > 1 ? item % p.a.splits : -1, half, st, part, Cfg::EPI_WARPS / 4,
                 END == FpEnd::Gated ? p.a.cols : p.a.bn, col, row + quad * 32,
                 tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN),
                 [&] { return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err); },
-                [&] { if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
+                [&] { if (lane == 0) mbar_arrive_drained(mapa_shared(smem_u32(&acce_bar[buf]), 0)); }, ok);
             if (++buf == 2) { buf = 0; buf_phase ^= 1; }
         }
         if (lane == 0) bulk_wait_all();
@@ -1285,8 +1470,10 @@ static int launch_pairs(FpPairWork<PROBLEMS>& w, cudaStream_t s)
     w.rest = w.gap = 0;
     if (PROBLEMS == 2) {
         w.rest = w.items[0] % pairs;
-        // (K blocks tell an item's time: both problems' tiles have the same width or nearly)
-        if (w.rest) w.gap = w.p[0].a.kb_per_split / w.p[PROBLEMS - 1].a.kb_per_split;
+        // K blocks tell an item's time (both problems' tiles have the same width or nearly), where it is above its
+        // epilogue's, about that of 10 K blocks (a weight gradient of 333 rows has 6; Linear keeps its order)
+        const int least = END == FpEnd::Grad ? 10 : 1;
+        if (w.rest) w.gap = std::max(w.p[0].a.kb_per_split, least) / std::max(w.p[PROBLEMS - 1].a.kb_per_split, least);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);

@@ -29,17 +29,93 @@ bool fp_rows_kernel(int B, int IC, int OC)
 
 // --------------------------------------------------------- element-wise passes
 
+// A warp copies strips of 256 elements, eight to a lane. A row starts at any element, so a lane loads the
+// 16 aligned bytes in which its eight begin, has those that follow from its neighbour, and shifts. Such a
+// load may take in elements of the row before or after; the first and the last row, where there may be
+// none, go element by element.
+constexpr int kCopyStrips = 4;       // strips of a warp whose loads are in flight together
+
 __global__ void __launch_bounds__(256) k_fp_align(const __grid_constant__ FpCopy c)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int z = blockIdx.z;
-    const uint16_t* src = c.src[z];
-    uint16_t* dst = c.dst[z];
-    const int end = min(c.cols[z], ((int)blockIdx.x + 1) * 1024);
-    for (int64_t r = blockIdx.y; r < c.rows[z]; r += gridDim.y)
-#pragma unroll 4
-        for (int i = blockIdx.x * 1024 + threadIdx.x; i < end; i += 256) dst[r * c.ldd[z] + i] = src[r * c.ld[z] + i];
+    const int z = blockIdx.z, lane = threadIdx.x & 31, rows = c.rows[z], cols = c.cols[z];
+    const int strips = (cols + 255) / 256;
+    const int64_t units = (int64_t)rows * strips;
+    const int64_t stride = (int64_t)gridDim.x * 8 * kCopyStrips;
+    for (int64_t u0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kCopyStrips; u0 < units; u0 += stride) {
+        uint4 a[kCopyStrips], b[kCopyStrips];
+        int64_t row = units >> 32 ? u0 / strips : (int64_t)((uint32_t)u0 / (uint32_t)strips);
+        int strip = (int)(u0 - row * strips);
+        const int64_t row0 = row;
+        const int strip0 = strip;
+#pragma unroll
+        for (int u = 0; u < kCopyStrips; ++u) {
+            a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (u0 + u < units && row > 0 && row + 1 < rows) {
+                const int i = strip * 256 + lane * 8;
+                const char* at = reinterpret_cast<const char*>(c.src[z] + row * c.ld[z] + i);
+                const int off = (int)(reinterpret_cast<uintptr_t>(at) & 15);
+                if (i - off / 2 < cols) a[u] = __ldg(reinterpret_cast<const uint4*>(at - off));
+                if (lane == 31 && off && i + 8 - off / 2 < cols) b[u] = __ldg(reinterpret_cast<const uint4*>(at - off) + 1);
+            }
+            if (++strip == strips) {
+                strip = 0;
+                ++row;
+            }
+        }
+        row = row0;
+        strip = strip0;
+#pragma unroll
+        for (int u = 0; u < kCopyStrips; ++u) {
+            if (u0 + u >= units) break;
+            const int i = strip * 256 + lane * 8;
+            const uint16_t* src = c.src[z] + row * c.ld[z];
+            uint16_t* dst = c.dst[z] + row * c.ldd[z];
+            if (row > 0 && row + 1 < rows) {
+                uint32_t w[9] = {a[u].x, a[u].y, a[u].z, a[u].w, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[4 + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+                if (lane == 31) {
+                    w[4] = b[u].x;
+                    w[5] = b[u].y;
+                    w[6] = b[u].z;
+                    w[7] = b[u].w;
+                }
+                const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);     // (a strip is 512 bytes)
+                if (off & 8) {
+#pragma unroll
+                    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+                }
+                if (off & 4) {
+#pragma unroll
+                    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+                }
+                if (off & 2) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+                }
+                // (rows of the copy are padded to 8 elements)
+                if (i < cols) *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                uint16_t e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int j = strip * 256 + lane + 32 * k;
+                    if (j < cols) e[k] = src[j];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int j = strip * 256 + lane + 32 * k;
+                    if (j < cols) dst[j] = e[k];
+                }
+            }
+            if (++strip == strips) {
+                strip = 0;
+                ++row;
+            }
+        }
+    }
 }
 
 // dz = dy act'(z), rounded to the operands' type (dz may be null), and the columns' sums before
@@ -168,9 +244,13 @@ bool fp_tma_rows(const void* p, int64_t ld, int rows, int cols)
     return aligned_to(p, 16) && fp_row_stride(ld, rows, cols) % 8 == 0;
 }
 
+// A copy's rows are padded to 64 bytes: rows of 16-byte multiples have TMA read, and the copy write, a sector
+// of each 128 bytes more.
+static int64_t copy_ld(int64_t cols) { return (cols + 31) & ~int64_t(31); }
+
 size_t fp_copy_bytes(const void* p, int64_t ld, int rows, int cols)
 {
-    return fp_tma_rows(p, ld, rows, cols) ? 0 : align256((size_t)rows * pad8(cols) * 2);
+    return fp_tma_rows(p, ld, rows, cols) ? 0 : align256((size_t)rows * copy_ld(cols) * 2);
 }
 
 const void* fp_aligned_operand(const void* p, int64_t* ld, int rows, int cols, char** ws, FpCopy* c)
@@ -184,23 +264,21 @@ const void* fp_aligned_operand(const void* p, int64_t* ld, int rows, int cols, c
     c->src[c->n] = static_cast<const uint16_t*>(p);
     c->dst[c->n] = dst;
     c->ld[c->n] = *ld;
-    c->ldd[c->n] = pad8(cols);
+    c->ldd[c->n] = copy_ld(cols);
     c->rows[c->n] = rows;
     c->cols[c->n] = cols;
     ++c->n;
-    *ld = pad8(cols);
+    *ld = copy_ld(cols);
     return dst;
 }
 
 int fp_run_copies(const FpCopy& c, cudaStream_t s)
 {
     if (!c.n) return ITO_OK;
-    int rows = 0, cols = 0;
-    for (int i = 0; i < c.n; ++i) {
-        rows = std::max(rows, c.rows[i]);
-        cols = std::max(cols, c.cols[i]);
-    }
-    launch_pdl(k_fp_align, dim3((cols + 1023) / 1024, std::min(rows, 16384), c.n), 256, 0, s, c);
+    int64_t units = 0;
+    for (int i = 0; i < c.n; ++i) units = std::max(units, (int64_t)c.rows[i] * ((c.cols[i] + 255) / 256));
+    const int64_t blocks = (units + 8 * kCopyStrips - 1) / (8 * kCopyStrips);
+    launch_pdl(k_fp_align, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16), 1, c.n), 256, 0, s, c);
     return launch_status("linear operand copy");
 }
 

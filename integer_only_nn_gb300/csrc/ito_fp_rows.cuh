@@ -173,7 +173,9 @@ static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw
                           int IC, int OC, const FpEpilogue& e, const FpMore& more, cudaStream_t s)
 {
     constexpr int STEP = 32 * kRowsSteps<END>;
-    const int warps = std::min(kRowsWarps, std::max(1, (IC + STEP - 1) / STEP));
+    // (the number of warps is part of the sums' order: the plain linear layer keeps its)
+    const int most = END == FpEnd::Linear ? kRowsWarps : kRowsWarps / 2;
+    const int warps = std::min(most, std::max(1, (IC + STEP - 1) / STEP));
     const bool vec = IC % 8 == 0 && fp_tma_rows(x, ldx, B, IC) && fp_tma_rows(W, ldw, OC, IC) &&
                      (!W2 || fp_tma_rows(W2, ldw2, OC, IC));
     launch_pdl(vec ? k_fp_rows<END, NT, true> : k_fp_rows<END, NT, false>, (OC + 15) / 16, warps * 32, 0, s,

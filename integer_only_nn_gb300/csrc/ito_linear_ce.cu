@@ -104,6 +104,9 @@ static int ce_piece(int rows, int classes)
     return (int)std::min<int64_t>(classes, std::max<int64_t>(n, 256));
 }
 
+// a row of dl: whole lines of 128 bytes, which is what the products' loads take of it at a time
+static int64_t ce_ldl(int64_t piece) { return (piece + 63) & ~int64_t(63); }
+
 static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
 static int ce_parts(int rows, int d, int classes)
@@ -196,7 +199,7 @@ size_t ito_linear_cross_entropy_bwd_workspace_size(const void* x, int64_t ldx, c
     if (fp_check_sizes(rows, d, classes)) return 0;
     const int piece = ce_piece(rows, classes), last = (classes - 1) % piece + 1;
     size_t n = 256 + fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d) +
-               align256((size_t)rows * pad8(piece) * 2);
+               align256((size_t)rows * ce_ldl(piece) * 2);
     if (piece < classes) n += align256((size_t)rows * pad4(d) * 4);
     return n + std::max(ce_products_bytes(rows, d, piece), ce_products_bytes(rows, d, last));
 }
@@ -235,7 +238,7 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
     r = fp_run_copies(copies, s);
     if (r) return r;
     void* dl = ws;
-    const int64_t ldl = pad8(piece);
+    const int64_t ldl = ce_ldl(piece);
     ws += align256((size_t)rows * ldl * 2);
     float* acc = nullptr;
     if (piece < classes) {

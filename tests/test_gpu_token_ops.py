@@ -49,7 +49,8 @@ def tokens(torch, kind, n, classes, seed):
 
 EMB_SIZES = [(1, 1, 1), (1, 5, 787), (2, 2, 3), (7, 50001, 787), (31, 100, 8), (32, 3, 16), (33, 255, 256), (65, 256, 250),
              (300, 257, 264), (1000, 17, 1), (2047, 65535, 40), (2049, 65536, 24), (5000, 70000, 8), (4096, 300, 1024),
-             (20000, 1000, 72), (9000, 40, 520)]
+             (20000, 1000, 72), (9000, 40, 520), (4097, 257, 16), (8192, 70000, 8), (8193, 300, 24), (50000, 3000, 40),
+             (65537, 66000, 8)]
 KINDS = ("text", "one", "even", "up", "down", "none")
 TYPES = ("float32", "bfloat16", "float16")
 
