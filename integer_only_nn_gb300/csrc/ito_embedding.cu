@@ -149,14 +149,94 @@ __global__ void __launch_bounds__(kEmbThreads)
     }
 }
 
+// 16-bit rows at any alignment, of the table and of y: a thread writes the eight elements of y in one aligned
+// 16 bytes, which begin anywhere in the table's row (Eight16); one by one at a row's two ends. `eights`
+// aligned eights touch a row at most. (30000 x 1001 of 32768 rows: SHIFT_US us; elements one by one 38.)
+constexpr int kEmbShifted = 2;       // eights of a thread whose loads are in flight together
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kEmbThreads, 5)
+    k_emb_fwd_shifted(const int32_t* __restrict__ ids, int64_t n, const T* __restrict__ table, int64_t ldt, int classes,
+                      int d, Divider eights, float scale, O* __restrict__ y, int64_t ldy, int* err)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int PER = kEmbThreads * kEmbShifted;
+    const uint16_t* const lo = reinterpret_cast<const uint16_t*>(table);
+    const uint16_t* const hi = lo + (classes - 1) * ldt + d;
+    const int64_t first = (int64_t)blockIdx.x * PER, total = n * eights.d;
+    const int64_t row0 = first / eights.d;
+    const unsigned rest = (unsigned)(first - row0 * eights.d), left = (unsigned)min((int64_t)PER, total - first);
+    int id[kEmbShifted], col[kEmbShifted];
+    uint16_t* to[kEmbShifted];
+#pragma unroll
+    for (int u = 0; u < kEmbShifted; ++u) {
+        const unsigned j = u * kEmbThreads + threadIdx.x, r = eights(rest + j);
+        id[u] = j < left ? __ldg(ids + row0 + r) : -1;
+        to[u] = reinterpret_cast<uint16_t*>(y) + (row0 + r) * ldy;
+        // the row's first aligned eight begins up to seven elements before it
+        col[u] = (int)(rest + j - r * eights.d) * 8 - (int)(reinterpret_cast<uintptr_t>(to[u]) >> 1 & 7);
+        if (j >= left) col[u] = d;
+        if (id[u] >= classes || id[u] < 0) {
+            if (id[u] != -1 && col[u] <= 0) raise_device_error(err, ITO_ERR_ARG);
+            id[u] = -1;
+        }
+    }
+    Eight16 e[kEmbShifted];
+#pragma unroll
+    for (int u = 0; u < kEmbShifted; ++u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) e[u].w[i] = 0u;
+        if (id[u] < 0) continue;
+        const uint16_t* row = lo + id[u] * ldt;
+        if (col[u] >= 0 && col[u] + 8 <= d && Eight16::whole(row + col[u], lo, hi)) {
+            e[u].load(row + col[u]);
+        } else {                                     // as `load` leaves them for these eight
+            uint16_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = col[u] + i >= 0 && col[u] + i < d ? __ldg(row + col[u] + i) : 0;
+            const bool half = reinterpret_cast<uintptr_t>(row + col[u]) & 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[u].w[i] = half ? (uint32_t)x[2 * i] << 16 | (i ? x[2 * i - 1] : 0) : x[2 * i] | (uint32_t)x[2 * i + 1] << 16;
+            }
+            e[u].w[4] = half ? x[7] : 0;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kEmbShifted; ++u) {
+        if (col[u] >= d) continue;
+        Vec<T> v;
+        v.raw = e[u].get(lo + (id[u] < 0 ? 0 : id[u] * ldt) + col[u]);
+        Vec<O> o;
+        if (std::is_same<T, O>::value && scale == 1.0f) {
+            o.raw = v.raw;
+        } else {
+            float f[8];
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= scale;
+            o.set(f);
+        }
+        if (col[u] >= 0 && col[u] + 8 <= d) {
+            *reinterpret_cast<uint4*>(to[u] + col[u]) = o.raw;
+        } else {
+            const uint32_t w[4] = {o.raw.x, o.raw.y, o.raw.z, o.raw.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col[u] + i >= 0 && col[u] + i < d) to[u][col[u] + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
 // ------------------------------------------------------- sorting places by token
 
-// A stable sort by digits of 8 bits, lowest first, by one cluster of blocks: each warp counts the
+// A stable sort by digits of 8 bits, lowest first, by one cluster of 16 blocks or 8: each warp counts the
 // digits of its own run of places, the counts of a block's warps and of the cluster's blocks are
 // summed up to where each warp's places of each digit go, and the warps write them there. Runs are
 // consecutive, so places of equal digits keep their order. A place without a token has the key
 // `classes`, behind all others.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 8;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 16;
 constexpr int kZeroRows = 16384;     // rows of the table whose presence a block notes at a time
 // A few places are sorted by counting, for each, those that go before it: a comparison for each pair, on all
 // SMs, without a barrier between blocks (n = 2047: RANK_2047 us; the digits' passes SORT_2047).
@@ -170,7 +250,6 @@ struct EmbSort {
     void* table;                     // its first zero_rows rows get zeros where the token is absent
     int zero_rows;
     int64_t row_bytes, pitch_bytes;
-    int wide;                        // 16-byte stores
     int* err;
 };
 
@@ -237,9 +316,23 @@ __device__ __forceinline__ void sort_offsets(SortSums& q, int blocks, int block)
     __syncthreads();
 }
 
+// The lanes whose digit (of 8 bits) is this lane's, by a vote on each bit: a match over the warp in one
+// instruction takes longer (34586 places: VOTE_US us in all, MATCH_US with it).
+__device__ __forceinline__ unsigned same_digit(unsigned digit)
+{
+    unsigned same = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const bool bit = digit >> b & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, bit);
+        same &= bit ? with : ~with;
+    }
+    return same;
+}
+
 __device__ __forceinline__ int emb_key(const EmbSort& a, int id) { return id >= 0 && id < a.classes ? id : a.classes; }
 
-// Up to 8192 R places (with a cluster of eight): R to a lane, kept in registers between the passes and
+// Up to 1024 R places a block: R to a lane, kept in registers between the passes and
 // exchanged through the blocks' shared memory. Places beyond n have a key above all and stay the last.
 template <int R>
 __device__ __forceinline__ void emb_sort_held(const EmbSort& a, SortSums& q, int* exchange)
@@ -261,7 +354,7 @@ __device__ __forceinline__ void emb_sort_held(const EmbSort& a, SortSums& q, int
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const unsigned digit = (unsigned)key[r] >> (8 * pass) & 255;
-            const unsigned same = __match_any_sync(0xffffffffu, digit);
+            const unsigned same = same_digit(digit);
             const unsigned so_far = q.counts[warp][digit];
             __syncwarp();
             if (lane == __ffs(same) - 1) q.counts[warp][digit] = so_far + __popc(same);
@@ -311,8 +404,8 @@ __device__ __forceinline__ void emb_sort(const EmbSort& a, SortSums& q)
         for (int64_t i = lo; i < hi; i += 32) {
             const bool in = i + lane < hi;
             const int key = in ? key_at(i + lane) : 0;
-            const unsigned digit = in ? (unsigned)key >> shift & 255 : 256;
-            const unsigned same = __match_any_sync(0xffffffffu, digit);
+            const unsigned digit = (unsigned)key >> shift & 255;
+            const unsigned same = same_digit(digit) & __ballot_sync(0xffffffffu, in);
             if (in && lane == __ffs(same) - 1) q.counts[warp][digit] += __popc(same);
             __syncwarp();
         }
@@ -322,8 +415,8 @@ __device__ __forceinline__ void emb_sort(const EmbSort& a, SortSums& q)
             const bool in = i + lane < hi;
             const int key = in ? key_at(i + lane) : 0;
             const int place = !in ? 0 : pass ? __ldcg(a.places[to ^ 1] + i + lane) : (int)(i + lane);
-            const unsigned digit = in ? (unsigned)key >> shift & 255 : 256;
-            const unsigned same = __match_any_sync(0xffffffffu, digit);
+            const unsigned digit = (unsigned)key >> shift & 255;
+            const unsigned same = same_digit(digit) & __ballot_sync(0xffffffffu, in);
             if (in) {
                 const unsigned at = q.base[digit] + q.counts[warp][digit] + __popc(same & ((1u << lane) - 1));
                 a.keys[to][at] = key;
@@ -337,13 +430,16 @@ __device__ __forceinline__ void emb_sort(const EmbSort& a, SortSums& q)
     }
 }
 
-__device__ __forceinline__ void zero_row(char* row, int64_t bytes, bool wide, int lane)
+// a row of zeros by a warp: 16 bytes at a time, its ends up to the next 16-byte boundary by elements of 2
+__device__ __forceinline__ void zero_row(char* row, int64_t bytes, int lane)
 {
-    if (wide) {
-        for (int64_t i = lane * 16; i < bytes; i += 512) *reinterpret_cast<uint4*>(row + i) = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        for (int64_t i = lane * 2; i < bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
-    }
+    char* const end = row + bytes;
+    char* const a = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(row) + 15) & ~uintptr_t(15));
+    char* const b = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+    for (char* p = a + lane * 16; p < b; p += 512) *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+    char* const head = a < b ? a : end;              // (a row may lie within 32 bytes)
+    if (row + lane * 2 < head) *reinterpret_cast<uint16_t*>(row + lane * 2) = 0;
+    if (a < b && b + lane * 2 < end) *reinterpret_cast<uint16_t*>(b + lane * 2) = 0;
 }
 
 // zeros for the rows of tokens that do not occur, block `b` of `blocks`
@@ -371,7 +467,7 @@ __device__ __forceinline__ void emb_zero(const EmbSort& a, int b, int blocks)
         __syncthreads();
         for (int r = warp; r < rows; r += threads / 32) {
             if (there[r >> 5] >> (r & 31) & 1) continue;
-            zero_row(static_cast<char*>(a.table) + (r0 + r) * a.pitch_bytes, a.row_bytes, a.wide, lane);
+            zero_row(static_cast<char*>(a.table) + (r0 + r) * a.pitch_bytes, a.row_bytes, lane);
         }
     }
 }
@@ -469,7 +565,7 @@ struct EmbSum {
     float *head, *tail;              // [spans][pitch]
     int pitch;
     int sum_blocks;                  // the others write zeros to the rows from zero_from on
-    int zero_from, wide;
+    int zero_from;
     int64_t row_bytes, pitch_bytes;
 };
 
@@ -492,7 +588,7 @@ __device__ __forceinline__ void emb_zero_rest(const EmbSum& a, int64_t warp, int
     }
     const unsigned rows = __ballot_sync(0xffffffffu, absent);
     for (int i = 0; i < kZeroWarpRows; ++i)
-        if (rows >> i & 1) zero_row(static_cast<char*>(a.table) + (r0 + i) * a.pitch_bytes, a.row_bytes, a.wide, lane);
+        if (rows >> i & 1) zero_row(static_cast<char*>(a.table) + (r0 + i) * a.pitch_bytes, a.row_bytes, lane);
 }
 
 template <typename O, bool VEC>
@@ -701,6 +797,16 @@ template <typename T, typename O>
 static int run_emb_fwd(const int32_t* ids, int64_t n, const void* table, int64_t ldt, int classes, int d, bool vec,
                        float scale, void* y, int64_t ldy, int* err, cudaStream_t s)
 {
+    if constexpr (sizeof(T) == 2 && sizeof(O) == 2) {
+        if (!vec && d >= 16) {
+            const Divider eights(d / 8 + 2);         // (d elements that begin at any of an eight's)
+            const int64_t blocks = (n * eights.d + kEmbThreads * kEmbShifted - 1) / (kEmbThreads * kEmbShifted);
+            if (blocks > INT32_MAX) return set_error(ITO_ERR_SHAPE, "too many elements");
+            launch_pdl(k_emb_fwd_shifted<T, O>, (unsigned)blocks, kEmbThreads, 0, s, ids, n, static_cast<const T*>(table),
+                       ldt, classes, d, eights, scale, static_cast<O*>(y), ldy, err);
+            return launch_status("embedding");
+        }
+    }
     const int lanes = row_lanes(d), strips = (d + 8 * lanes - 1) / (8 * lanes);
     const int64_t per = (int64_t)kEmbThreads / lanes * kEmbUnits, blocks = (n * strips + per - 1) / per;
     if (blocks > INT32_MAX) return set_error(ITO_ERR_SHAPE, "too many elements");
@@ -732,34 +838,61 @@ static int sum_chunk(int64_t n, int strips)
     return chunk;
 }
 
+static void sort_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&at)[2], int cluster, int blocks, size_t bytes,
+                        cudaStream_t s)
+{
+    cfg->gridDim = dim3((unsigned)blocks);
+    cfg->blockDim = dim3(kSortThreads);
+    cfg->dynamicSmemBytes = bytes;
+    cfg->stream = s;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = at;
+    cfg->numAttrs = 2;
+}
+
 template <int R>
-static int run_emb_sort(EmbSort q, cudaStream_t s)
+static int run_emb_sort(const EmbSort& q, cudaStream_t s)
 {
     constexpr int BYTES = R * kSortThreads * 8;
     static OnEachDevice ready;
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e == cudaSuccess)
-        e = ready.run(device, [&] { return cudaFuncSetAttribute(k_emb_sort<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES); });
+        e = ready.run(device, [&] {
+            const cudaError_t f = cudaFuncSetAttribute(k_emb_sort<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+            return f == cudaSuccess ? cudaFuncSetAttribute(k_emb_sort<R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : f;
+        });
     if (e != cudaSuccess) return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    q.blocks = kSortCluster;
     const int zero = (std::min(2 * num_sms(), q.zero_rows) + q.blocks - 1) / q.blocks * q.blocks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(q.blocks + zero));
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = BYTES;
-    cfg.stream = s;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = q.blocks;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
+    sort_launch(&cfg, at, q.blocks, q.blocks + zero, BYTES, s);
     e = cudaLaunchKernelEx(&cfg, k_emb_sort<R>, q);
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "embedding backward launch: %s", cudaGetErrorString(e));
+}
+
+// Whether a cluster of 16 blocks that sort fits on this device (8 always do).
+static bool sort_in_sixteen()
+{
+    static std::atomic<int> known{0};                // (the same on each device of this part)
+    if (!known) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[2];
+        sort_launch(&cfg, at, 16, 16, 4 * kSortThreads * 8, nullptr);
+        cfg.numAttrs = 1;
+        int got = 0;
+        const bool fits = cudaFuncSetAttribute(k_emb_sort<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSortThreads * 8) == cudaSuccess &&
+                          cudaFuncSetAttribute(k_emb_sort<4>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                          cudaOccupancyMaxActiveClusters(&got, k_emb_sort<4>, &cfg) == cudaSuccess && got > 0;
+        if (!fits) cudaGetLastError();
+        known = fits ? 16 : 8;
+    }
+    return known == 16;
 }
 
 struct EmbLayout {
@@ -858,7 +991,6 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     q.table = dtable;
     q.row_bytes = (int64_t)d * type_bytes(out_type);
     q.pitch_bytes = ldt * (int64_t)type_bytes(out_type);
-    q.wide = aligned_to(dtable, 16) && q.row_bytes % 16 == 0 && (classes == 1 || q.pitch_bytes % 16 == 0);
     q.err = err;
     // zeros that take about as long as the sort
     q.zero_rows = add ? 0 : (int)std::min<int64_t>(classes, (rank ? kZeroBesideRank : kZeroBesideSort) / q.row_bytes);
@@ -869,8 +1001,11 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
         r = launch_status("embedding backward");
         if (r) return r;
     } else {
-        r = n <= 8192 ? run_emb_sort<1>(q, s) : n <= 16384 ? run_emb_sort<2>(q, s) : n <= 32768 ? run_emb_sort<4>(q, s)
-            : n <= 65536 ? run_emb_sort<8>(q, s) : run_emb_sort<0>(q, s);
+        // (34586 places: SORT_16 us in 16 blocks, SORT_8 in 8)
+        q.blocks = n > 8192 && sort_in_sixteen() ? 16 : 8;
+        const int64_t each = (n + q.blocks * kSortThreads - 1) / (q.blocks * kSortThreads);
+        r = each <= 1 ? run_emb_sort<1>(q, s) : each <= 2 ? run_emb_sort<2>(q, s) : each <= 4 ? run_emb_sort<4>(q, s)
+            : run_emb_sort<0>(q, s);
         if (r) return r;
     }
 
@@ -894,7 +1029,6 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     a.tail = reinterpret_cast<float*>(ws + 4 * l.keys + l.pieces);
     a.pitch = l.pitch;
     a.zero_from = add ? classes : q.zero_rows;
-    a.wide = q.wide;
     a.row_bytes = q.row_bytes;
     a.pitch_bytes = q.pitch_bytes;
     const bool vec = rows_in_eights(dy, type, lddy, n, d) && rows_in_eights(dtable, out_type, ldt, classes, d);

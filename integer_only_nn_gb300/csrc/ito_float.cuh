@@ -170,6 +170,55 @@ struct Vec {
     }
 };
 
+// Eight consecutive 16-bit elements at any of their addresses: the four aligned words that hold them, or
+// five and a shift by half a word where they begin in a word's middle. (Two aligned loads of 16 bytes have
+// fewer accesses, but words then have to be selected by the address: 105 instructions a copied eight instead
+// of INSTR_WORDS.) The words beyond the first and the last element may lie outside the tensor at its two ends:
+// whole() tells whether they are in its span of memory lo .. hi.
+struct Eight16 {
+    uint32_t w[5];
+    static __device__ __forceinline__ bool whole(const uint16_t* p, const uint16_t* lo, const uint16_t* hi)
+    {
+        const bool half = reinterpret_cast<uintptr_t>(p) & 2;
+        return half ? p > lo && p + 8 < hi : p + 8 <= hi;
+    }
+    __device__ __forceinline__ void load(const uint16_t* p)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(q + i);
+        w[4] = 0;
+        if (at & 2) w[4] = __ldg(q + 4);
+    }
+    // the eight at p, once loaded
+    __device__ __forceinline__ uint4 get(const uint16_t* p) const
+    {
+        const int by = (int)(reinterpret_cast<uintptr_t>(p) & 2) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by),
+                          __funnelshift_r(w[2], w[3], by), __funnelshift_r(w[3], w[4], by));
+    }
+};
+
+// n / d for n below 2^31 by a multiplication (Granlund and Montgomery, Division by Invariant Integers using
+// Multiplication, with one bit less of n)
+struct Divider {
+    uint32_t d, m, s;
+    Divider(uint32_t by = 1) : d(by), s(0)
+    {
+        while (s < 31 && (1u << s) < by) ++s;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - by)) / by + 1);
+    }
+    __host__ __device__ __forceinline__ uint32_t operator()(uint32_t n) const
+    {
+#ifdef __CUDA_ARCH__
+        return (__umulhi(m, n) + n) >> s;
+#else
+        return (uint32_t)((((uint64_t)m * n >> 32) + n) >> s);
+#endif
+    }
+};
+
 // rows that 16-byte accesses can take: every row starts on a 16-byte boundary
 inline bool rows_vec(const void* p, int64_t ld, size_t size, int64_t rows)
 {

@@ -1,7 +1,7 @@
 // The 16-bit float products of the float layers: what their epilogue does, and how they are run.
 #pragma once
 
-#include "ito_internal.h"
+#include "ito_float.cuh"
 
 namespace ito {
 
@@ -89,6 +89,7 @@ struct FpCopy {
     uint16_t* dst[kFpCopies];
     int64_t ld[kFpCopies], ldd[kFpCopies];
     int rows[kFpCopies], cols[kFpCopies];
+    Divider by[kFpCopies];                   // by eights of a row
     int n;
 };
 int64_t fp_row_stride(int64_t ld, int rows, int cols);           // (a row's stride says nothing about a single row)
@@ -103,7 +104,9 @@ int fp_check_types(int type, int out_type, int act);
 int fp_check_ws(const void* ws, size_t bytes, size_t need);
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Whether a few rows of x stream W (see ito_fp_rows.cuh) instead of taking tensor-core tiles.
+// Whether a few rows of x stream W (see ito_fp_rows.cuh) instead of taking tensor-core tiles: the plain linear
+// layer's rule, and the other ends' (W: one of the gated layer's two).
 bool fp_rows_kernel(int B, int IC, int OC);
+bool fp_few_rows(int B, int IC, int OC);
 
 }  // namespace ito

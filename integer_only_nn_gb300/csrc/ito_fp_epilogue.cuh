@@ -157,6 +157,58 @@ __device__ __forceinline__ void fp_softmax_warp(float& m, float& s, int lanes = 
     }
 }
 
+// What a row of logits sends back: (a exp(v - lse) - hot [column is the target]). A row without a
+// token or whose lse is -inf sends 0.
+struct SlopeRow {
+    int target;
+    float a, hot, lse;
+    bool none;
+
+    // first: this is where targets out of range are told of
+    __device__ __forceinline__ void load(const FpMore& x, int M, int row, bool first, int* err)
+    {
+        target = -1;
+        a = hot = 0.0f;
+        lse = 0.0f;
+        if (row < M) {
+            const int t = x.targets[row];
+            const bool in = t >= 0 && t < x.classes;
+            if (first && !in && t != -1) raise_device_error(err, ITO_ERR_ARG);
+            const float scale = x.scale ? *x.scale : 1.0f;
+            lse = x.lse[row];
+            if (in) {
+                target = t - x.first;
+                hot = a = x.g_loss[row];
+            }
+            if (x.g_lse) a += x.g_lse[row];
+            a *= scale;
+            hot *= scale;
+        }
+        none = (a == 0.0f && hot == 0.0f) || lse == -INFINITY;
+    }
+    __device__ __forceinline__ float at(float v, int col) const
+    {
+        if (none) return 0.0f;
+        const float p = a * exp2_approx((v - lse) * kFpLog2e);
+        return col == target ? p - hot : p;
+    }
+    __device__ __forceinline__ void apply(float (&v)[32], int col) const
+    {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = a * exp2_approx((v[i] - lse) * kFpLog2e);
+        const int at = target - col;
+        if (at >= 0 && at < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i == at) v[i] -= hot;
+        }
+        if (none) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+    }
+};
+
 // two floats as one word of two 16-bit floats, lo in the low half
 __device__ __forceinline__ uint32_t pack16(int type, float lo, float hi)
 {

@@ -167,7 +167,7 @@ extern "C" {
 size_t ito_fp_gated_linear_fwd_workspace_size(const void* x, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
                                               int64_t ldwu, int B, int IC, int OC)
 {
-    if (fp_check_sizes(B, IC, OC) || fp_rows_kernel(B, IC, OC)) return 0;
+    if (fp_check_sizes(B, IC, OC) || fp_few_rows(B, IC, OC)) return 0;
     return fp_copy_bytes(x, ldx, B, IC) + fp_copy_bytes(Wg, ldwg, OC, IC) + fp_copy_bytes(Wu, ldwu, OC, IC) +
            fp_gemm_ws_bytes(B, OC, IC, false, FpEnd::Gated);
 }
@@ -201,7 +201,7 @@ int ito_fp_gated_linear_fwd(const void* x, int64_t ldx, const void* Wg, int64_t 
     more.z2 = zu;
     more.ldz2 = ldzu;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp_rows_kernel(B, IC, OC))
+    if (fp_few_rows(B, IC, OC))
         return fp_run_rows<FpEnd::Gated>(x, ldx, Wg, ldwg, Wu, ldwu, B, IC, OC, e, more, s);
     char* ws = static_cast<char*>(workspace);
     FpCopy copies{};

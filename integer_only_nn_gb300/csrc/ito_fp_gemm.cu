@@ -373,9 +373,18 @@ __device__ __forceinline__ void add_row32(const float* r, int vec, int left, flo
     }
 }
 
+// a 16-bit result's group by TMA, or by plain stores: the group is the `which`-th of two side by side, `last` of them.
+// (With a second result, whose boxes go between, each group goes alone.)
+__device__ __forceinline__ void store16_group(const float (&v)[32], int type, const CUtensorMap* map, bool tma, bool alone,
+                                              void* out, int64_t ld, FpStage& st, int which, bool last, int col, int row, int M,
+                                              int N)
+{
+    if (tma || alone) store16(v, type, map, tma, out, ld, st, col, row, M, N);
+    else store16_plain(v, type, out, ld, st, which, last, col - 32 * which, row, M, N);
+}
+
 __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
-                                             float (&v)[32], const uint32_t (&res)[16], FpStage& st, int col,
-                                             int row)
+                                             float (&v)[32], const uint32_t (&res)[16], FpStage& st, int col, int row)
 {
     const FpEpilogue& e = a.e;
     const int lane = st.lane;
@@ -400,8 +409,8 @@ __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensor
 }
 
 // zg and zu of a gated layer: both biases, both saved, h = act(zg) zu
-__device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32], float (&u)[32], FpStage& st, int col,
-                                             int row)
+__device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32], float (&u)[32], FpStage& st, int which,
+                                             bool last, int col, int row)
 {
     const FpGemmArgs& a = p.a;
     const FpEpilogue& e = a.e;
@@ -414,11 +423,10 @@ __device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32],
     activate(e.act, g);
 #pragma unroll
     for (int i = 0; i < 32; ++i) g[i] *= u[i];
-    store16(g, e.type, &p.Y, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
+    store16_group(g, e.type, &p.Y, a.y_tma, e.z, e.y, e.ldy, st, which, last, col, row, a.M, a.N);
 }
 
 // a gradient's sums: *alpha sum + acc
-// (the group is the `which`-th of two side by side, `last` of them)
 __device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int which, bool last,
                                             int col, int row)
 {
@@ -435,8 +443,7 @@ __device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float 
     void* y = half ? a.x.y2 : e.y;
     const int64_t ld = half ? a.x.ldy2 : e.ldy;
     if (e.out_type == ITO_F32) store32(v, map, tma, y, ld, st, col, row, a.M, a.N);
-    else if (tma) store16(v, e.out_type, map, true, y, ld, st, col, row, a.M, a.N);
-    else store16_plain(v, e.out_type, y, ld, st, which, last, col - 32 * which, row, a.M, a.N);
+    else store16_group(v, e.out_type, map, tma, false, y, ld, st, which, last, col, row, a.M, a.N);
 }
 
 // a warp's wait: one lane asks
@@ -454,6 +461,19 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[32])
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void load_sums(uint32_t first, uint32_t second, float (&v)[32], float (&u)[32])
+{
+    uint32_t r[32], q[32];
+    tmem_ld32(first, r);
+    tmem_ld32(second, q);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] = __uint_as_float(r[i]);
+        u[i] = __uint_as_float(q[i]);
+    }
 }
 
 // ------------------------------------------------------- a softmax's parts and its gradient
@@ -493,57 +513,6 @@ struct LossRow {
         }
         s += t[0] + t[1];
         m = top;
-    }
-};
-
-// What a row of logits sends back: (a exp(v - lse) - hot [column is the target]). A row without a
-// token or whose lse is -inf sends 0.
-struct SlopeRow {
-    int target;
-    float a, hot, lse;
-    bool none;
-
-    __device__ __forceinline__ void load(const FpGemmArgs& g, int row, bool first)
-    {
-        target = -1;
-        a = hot = 0.0f;
-        lse = 0.0f;
-        if (row < g.M) {
-            const int t = g.x.targets[row];
-            const bool in = t >= 0 && t < g.x.classes;
-            if (first && !in && t != -1) raise_device_error(g.err, ITO_ERR_ARG);
-            const float scale = g.x.scale ? *g.x.scale : 1.0f;
-            lse = g.x.lse[row];
-            if (in) {
-                target = t - g.x.first;
-                hot = a = g.x.g_loss[row];
-            }
-            if (g.x.g_lse) a += g.x.g_lse[row];
-            a *= scale;
-            hot *= scale;
-        }
-        none = (a == 0.0f && hot == 0.0f) || lse == -INFINITY;
-    }
-    __device__ __forceinline__ float at(float v, int col) const
-    {
-        if (none) return 0.0f;
-        const float p = a * exp2_approx((v - lse) * kFpLog2e);
-        return col == target ? p - hot : p;
-    }
-    __device__ __forceinline__ void apply(float (&v)[32], int col) const
-    {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = a * exp2_approx((v[i] - lse) * kFpLog2e);
-        const int at = target - col;
-        if (at >= 0 && at < 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i == at) v[i] -= hot;
-        }
-        if (none) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-        }
     }
 };
 
@@ -625,7 +594,7 @@ __device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStag
         a.x.part[(int64_t)(col0 / columns * 2 + first) * a.M + row + lane] = make_float2(loss.m, loss.s);
 }
 
-// The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
+// The epilogue of one of `step` warps' groups of 32 of the `columns` columns of a tile at
 // (row, col0), sums at `taddr`; `done` tells the issuing warp that the accumulator is drained. A
 // slice of K (slice >= 0) leaves its sums as they are, in the workspace. `half`: of a result in halves.
 template <FpEnd END, typename Wait, typename Done>
@@ -637,25 +606,22 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
     // a 16-bit residual comes while the sums are still being made
     const bool res16 = END == FpEnd::Linear && slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
     uint32_t res[16];
-    if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
+    // a run of consecutive groups for each of the `step` warps, two of which share their plain stores
+    const int each = (columns / 32 + step - 1) / step * 32, from = first * each, end = min(columns, from + each);
+    if (res16) load_residual16(a, col0 + from, row + st.lane, res);
     SlopeRow slope;
-    if (END == FpEnd::DLogits) slope.load(a, row + st.lane, first == 0 && col0 == 0 && a.x.first == 0);
+    if (END == FpEnd::DLogits) slope.load(a.x, a.M, row + st.lane, first == 0 && col0 == 0 && a.x.first == 0, a.err);
     if (!wait()) {
         ok = false;
         return;
     }
     tc_fence_after();
-    // groups in turns, or (Grad) a run of consecutive ones for each of the `step` warps, two of which share their stores
-    const int each = (columns / 32 + step - 1) / step * 32;
-    const int from = END == FpEnd::Grad ? first * each : first * 32;
-    const int end = END == FpEnd::Grad ? min(columns, from + each) : columns;
-    const int by = END == FpEnd::Grad ? 32 : step * 32;
 #pragma unroll 1
-    for (int c = from; c < end; c += by) {
+    for (int c = from; c < end; c += 32) {
         float v[32], u[32];
-        load_sums(taddr + c, v);
-        if (END == FpEnd::Gated) load_sums(taddr + columns + c, u);
-        if (c + by >= end) {
+        if (END == FpEnd::Gated) load_sums(taddr + c, taddr + columns + c, v, u);
+        else load_sums(taddr + c, v);
+        if (c + 32 >= end) {
             tc_fence_before();
             __syncwarp();
             done();
@@ -677,17 +643,18 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
             }
             continue;
         }
+        const int which = (c - from) >> 5 & 1;
+        const bool last = which || c + 32 >= end || col0 + c + 32 >= a.N;
         if (END == FpEnd::Linear) {
-            if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
+            if (res16 && c > from) load_residual16(a, col0 + c, row + st.lane, res);
             finish_group(a, &p.Y, &p.Z, v, res, st, col0 + c, row);
         } else if (END == FpEnd::Gated) {
-            finish_gated(p, v, u, st, col0 + c, row);
+            finish_gated(p, v, u, st, which, last, col0 + c, row);
         } else if (END == FpEnd::DLogits) {
             slope.apply(v, col0 + c);
             store16(v, a.e.type, &p.Y, true, a.e.y, a.e.ldy, st, col0 + c, row, a.M, a.N);
         } else {
-            const int which = (c - from) >> 5 & 1;
-            finish_grad(p, half, v, st, which, which || c + 32 >= end || col0 + c + 32 >= a.N, col0 + c, row);
+            finish_grad(p, half, v, st, which, last, col0 + c, row);
         }
     }
 }
@@ -1172,7 +1139,7 @@ __global__ void __launch_bounds__(256)
                 if (c + j < N) fp_finish_gated(e, a.x, r, c + j, v[j], u[j]);
         } else if (END == FpEnd::DLogits) {
             SlopeRow row;
-            row.load(a, (int)r, c == 0 && a.x.first == 0);
+            row.load(a.x, M, (int)r, c == 0 && a.x.first == 0, a.err);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (c + j < N) store_typed(e.y, e.type, r * e.ldy + c + j, row.at(v[j], c + j));

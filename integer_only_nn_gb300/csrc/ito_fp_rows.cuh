@@ -51,22 +51,29 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p)      // (read by o
     return v;
 }
 
-constexpr int kRowsWarps = 8;        // of a block, at most
+// warps of a block, at most
+template <FpEnd END, int NT>
+constexpr int kRowsWarps = END == FpEnd::Linear || NT > 2 ? 8 : 16;
 // steps of 32 k whose loads of W are in flight together
-template <FpEnd END>
-constexpr int kRowsSteps = END == FpEnd::Gated ? 2 : 4;
+template <FpEnd END, bool VEC>
+constexpr int kRowsSteps = END == FpEnd::Linear ? 4 : 2;
 
-// VEC: both operands' rows start on 16-byte boundaries and IC is a multiple of 8. The gated layer
+// VEC: both operands' rows start on 16-byte boundaries and IC is a multiple of 8. Of other rows each eight
+// elements come in words and a shift (Eight16; the plain linear layer, whose sums keep their
+// order and so their four steps, loads them one by one). The gated layer
 // streams two weights, 16 rows of each to a block, half as many steps of each ahead (the same bytes
-// in flight and registers). A Loss leaves each row's parts of 16 columns.
+// in flight and registers). A Loss leaves each row's parts of 16 columns; DLogits are as from the tensor cores' kernels.
 template <FpEnd END, int NT, bool VEC>
-__global__ void __launch_bounds__(kRowsWarps * 32)
+__global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
     k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ W, int64_t ldw,
               const uint16_t* __restrict__ W2, int64_t ldw2, int B, int IC, int OC, const __grid_constant__ FpEpilogue e,
-              const __grid_constant__ FpMore more)
+              const __grid_constant__ FpMore more, int* err)
 {
-    constexpr int U = kRowsSteps<END>, WS = END == FpEnd::Gated ? 2 : 1;
-    __shared__ float part[kRowsWarps][WS][16 * 8 * NT];
+    constexpr int U = kRowsSteps<END, VEC>, WS = END == FpEnd::Gated ? 2 : 1;
+    constexpr bool SHIFT = !VEC && END != FpEnd::Linear;
+    using Raw = typename std::conditional<SHIFT, Eight16, uint4>::type;
+    extern __shared__ float rows_part[];
+    float(*const part)[WS][16 * 8 * NT] = reinterpret_cast<float(*)[WS][16 * 8 * NT]>(rows_part);
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -81,9 +88,42 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
         w1[WS - 1] = W2 + (int64_t)(in1 ? oc0 + g + 8 : 0) * ldw2;
     }
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    auto load = [&](const uint16_t* row, int k, bool in) {
-        if (VEC) return in && k < IC ? load_once(row + k) : zero;
-        return in && k < IC ? load_eight(row, k, IC, false) : zero;
+    const uint16_t* const w_end[2] = {W + (OC - 1) * ldw + IC, WS == 2 ? W2 + (OC - 1) * ldw2 + IC : nullptr};
+    // only a weight's first and last row have words that reach beyond it
+    const bool inner0 = oc0 + g > 0 && oc0 + g + 1 < OC, inner1 = oc0 + g + 9 < OC;
+    auto load = [&](const uint16_t* row, int k, bool in, bool inner, int h) -> Raw {
+        if constexpr (SHIFT) {
+            Raw e;
+            e.w[0] = e.w[1] = e.w[2] = e.w[3] = e.w[4] = 0u;
+            if (in && k + 8 <= IC && (inner || Eight16::whole(row + k, h ? W2 : W, w_end[h]))) e.load(row + k);
+            return e;
+        } else if constexpr (VEC) {
+            return in && k < IC ? load_once(row + k) : zero;
+        } else {
+            return in && k < IC ? load_eight(row, k, IC, false) : zero;
+        }
+    };
+    // what was loaded, as the eight elements (those at a row's or the weight's end are loaded here)
+    auto eight = [&](const Raw& e, const uint16_t* row, int k, bool in, bool inner, int h) -> uint4 {
+        if constexpr (SHIFT) {
+            if (!in || k >= IC) return zero;
+            if (k + 8 <= IC && (inner || Eight16::whole(row + k, h ? W2 : W, w_end[h]))) return e.get(row + k);
+            return load_eight(row, k, IC, false);
+        } else {
+            return e;
+        }
+    };
+    const uint16_t* const x_end = x + (B - 1) * ldx + IC;
+    auto load_x = [&](const uint16_t* row, int k, bool in) -> uint4 {
+        if (!in || k >= IC) return zero;
+        if constexpr (SHIFT) {
+            if (k + 8 <= IC && Eight16::whole(row + k, x, x_end)) {
+                Eight16 e;
+                e.load(row + k);
+                return e.get(row + k);
+            }
+        }
+        return load_eight(row, k, IC, VEC);
     };
     float c[WS][NT][4];
 #pragma unroll
@@ -92,25 +132,33 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[h][n][i] = 0.0f;
-    uint4 a[WS][U], b[WS][U];
+    Raw a[WS][U], b[WS][U];
     const int stride = warps * U * 32;
     int k0 = warp * U * 32;
 #pragma unroll
     for (int h = 0; h < WS; ++h)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            a[h][u] = load(w0[h], k0 + u * 32 + t * 8, in0);
-            b[h][u] = load(w1[h], k0 + u * 32 + t * 8, in1);
+            a[h][u] = load(w0[h], k0 + u * 32 + t * 8, in0, inner0, h);
+            b[h][u] = load(w1[h], k0 + u * 32 + t * 8, in1, inner1, h);
         }
     for (; k0 < IC; k0 += stride) {
         // the next steps' rows of W are on their way while these are multiplied
-        uint4 an[WS][U], bn[WS][U];
+        Raw an[WS][U], bn[WS][U];
 #pragma unroll
         for (int h = 0; h < WS; ++h)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                an[h][u] = load(w0[h], k0 + stride + u * 32 + t * 8, in0);
-                bn[h][u] = load(w1[h], k0 + stride + u * 32 + t * 8, in1);
+                an[h][u] = load(w0[h], k0 + stride + u * 32 + t * 8, in0, inner0, h);
+                bn[h][u] = load(w1[h], k0 + stride + u * 32 + t * 8, in1, inner1, h);
+            }
+        uint4 wa[WS][U], wb[WS][U];
+#pragma unroll
+        for (int h = 0; h < WS; ++h)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                wa[h][u] = eight(a[h][u], w0[h], k0 + u * 32 + t * 8, in0, inner0, h);
+                wb[h][u] = eight(b[h][u], w1[h], k0 + u * 32 + t * 8, in1, inner1, h);
             }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -120,14 +168,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = k0 + u * 32 + t * 8;
-                v[u] = in && k < IC ? load_eight(xr, k, IC, VEC) : zero;
+                v[u] = load_x(xr, k, in);
             }
 #pragma unroll
             for (int h = 0; h < WS; ++h)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    mma_16816(e.type, c[h][n], a[h][u].x, b[h][u].x, a[h][u].y, b[h][u].y, v[u].x, v[u].y);
-                    mma_16816(e.type, c[h][n], a[h][u].z, b[h][u].z, a[h][u].w, b[h][u].w, v[u].z, v[u].w);
+                    mma_16816(e.type, c[h][n], wa[h][u].x, wb[h][u].x, wa[h][u].y, wb[h][u].y, v[u].x, v[u].y);
+                    mma_16816(e.type, c[h][n], wa[h][u].z, wb[h][u].z, wa[h][u].w, wb[h][u].w, v[u].z, v[u].w);
                 }
         }
 #pragma unroll
@@ -162,7 +210,11 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
             fp_softmax_warp(m, sum, 16);
             if (row < B && (i & 15) == 0) more.part[(int64_t)blockIdx.x * B + row] = make_float2(m, sum);
         } else if (in) {
-            if (END == FpEnd::Gated) fp_finish_gated(e, more, row, oc, s[0], s[WS - 1]);
+            if (END == FpEnd::DLogits) {
+                SlopeRow slope;
+                slope.load(more, B, row, oc == 0 && more.first == 0, err);
+                store_typed(e.y, e.type, row * e.ldy + oc, slope.at(s[0], oc));
+            } else if (END == FpEnd::Gated) fp_finish_gated(e, more, row, oc, s[0], s[WS - 1]);
             else fp_finish(e, row, oc, s[0]);
         }
     }
@@ -172,15 +224,21 @@ template <FpEnd END, int NT>
 static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw, const void* W2, int64_t ldw2, int B,
                           int IC, int OC, const FpEpilogue& e, const FpMore& more, cudaStream_t s)
 {
-    constexpr int STEP = 32 * kRowsSteps<END>;
-    // (the number of warps is part of the sums' order: the plain linear layer keeps its)
-    const int most = END == FpEnd::Linear ? kRowsWarps : kRowsWarps / 2;
-    const int warps = std::min(most, std::max(1, (IC + STEP - 1) / STEP));
+    int* const err = END == FpEnd::DLogits ? device_error_word() : nullptr;
+    if (END == FpEnd::DLogits && !err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const bool vec = IC % 8 == 0 && fp_tma_rows(x, ldx, B, IC) && fp_tma_rows(W, ldw, OC, IC) &&
                      (!W2 || fp_tma_rows(W2, ldw2, OC, IC));
-    launch_pdl(vec ? k_fp_rows<END, NT, true> : k_fp_rows<END, NT, false>, (OC + 15) / 16, warps * 32, 0, s,
+    // With blocks for two to an SM and more, 4 warps each let all of them run at the same time (one row of 4096 ->
+    // 8192: 22 us instead of 25, of 4096 -> 131072 classes 162 instead of 173); fewer blocks have more warps. (The
+    // number of warps is part of the sums' order: the plain linear layer keeps its.)
+    const int blocks = (OC + 15) / 16;
+    const int most = END == FpEnd::Linear ? 8 : std::min(kRowsWarps<END, NT>, blocks < num_sms() ? 16 : blocks < 2 * num_sms() ? 8 : 4);
+    const int step = 32 * (vec ? kRowsSteps<END, true> : kRowsSteps<END, false>);
+    const int warps = std::min(most, std::max(1, (IC + step - 1) / step));
+    launch_pdl(vec ? k_fp_rows<END, NT, true> : k_fp_rows<END, NT, false>, (OC + 15) / 16, warps * 32,
+               (size_t)warps * (END == FpEnd::Gated ? 2 : 1) * 16 * 8 * NT * sizeof(float), s,
                static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(W), ldw,
-               static_cast<const uint16_t*>(W2), ldw2, B, IC, OC, e, more);
+               static_cast<const uint16_t*>(W2), ldw2, B, IC, OC, e, more, err);
     return launch_status("linear");
 }
 

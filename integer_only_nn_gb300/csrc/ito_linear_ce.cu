@@ -111,7 +111,7 @@ static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
 static int ce_parts(int rows, int d, int classes)
 {
-    if (fp_rows_kernel(rows, d, classes)) return (classes + 15) / 16;
+    if (fp_few_rows(rows, d, classes)) return (classes + 15) / 16;
     return std::max(1, fp_loss_parts(rows, classes, d));
 }
 
@@ -144,7 +144,7 @@ size_t ito_linear_cross_entropy_fwd_workspace_size(const void* x, int64_t ldx, c
 {
     if (fp_check_sizes(rows, d, classes)) return 0;
     const size_t own = align256((size_t)ce_parts(rows, d, classes) * rows * 8) + align256((size_t)rows * 4);
-    if (fp_rows_kernel(rows, d, classes)) return own;
+    if (fp_few_rows(rows, d, classes)) return own;
     return own + fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d) +
            fp_gemm_ws_bytes(rows, classes, d, false, FpEnd::Loss);
 }
@@ -174,7 +174,7 @@ int ito_linear_cross_entropy_fwd(const void* x, int64_t ldx, const void* W, int6
     ws += align256((size_t)rows * 4);
     FpEpilogue e{};
     e.type = e.out_type = type;
-    if (fp_rows_kernel(rows, d, classes)) {
+    if (fp_few_rows(rows, d, classes)) {
         r = fp_run_rows<FpEnd::Loss>(x, ldx, W, ldw, nullptr, 0, rows, d, classes, e, more, s);
     } else {
         FpCopy copies{};
@@ -262,7 +262,8 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
         logits.x.g_loss = g_loss;
         logits.x.g_lse = g_lse;
         logits.x.scale = scale;
-        r = fp_gemm(&logits, 1, ws, s);
+        r = fp_few_rows(rows, d, n) ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
+                                       : fp_gemm(&logits, 1, ws, s);
         if (r) return r;
         FpProduct products[2];
         int k = 0;
