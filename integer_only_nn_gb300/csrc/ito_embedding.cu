@@ -12,8 +12,9 @@
 // warps add up the rows of chunks of sorted places, a strip of columns each, and write a token's sum where
 // the token changes. A token whose places go on into the next chunk leaves pieces, which are joined in
 // the block, and over blocks by a third kernel: a frequent token's thousands of rows are the work of many warps. The rows of
-// tokens that do not occur get zeros: some while the places are sorted, which leaves most of the device
-// idle, the rest beside the sums.
+// tokens that do not occur get zeros while pieces are joined, which leaves most of the device idle (some of
+// them while the places are sorted: 47 us instead of 41 for 34586 x 304 of 15292, 126 instead of 123 for
+// 16384 x 4096 of 32768, because the presence of a token is then not known from the sorted ones).
 #include <algorithm>
 #include <climits>
 
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kEmbThreads)
 
 // 16-bit rows at any alignment, of the table and of y: a thread writes the eight elements of y in one aligned
 // 16 bytes, which begin anywhere in the table's row (Eight16); one by one at a row's two ends. `eights`
-// aligned eights touch a row at most. (30000 x 1001 of 32768 rows: SHIFT_US us; elements one by one 38.)
+// aligned eights touch a row at most. (30000 x 1001 of 32768 rows: 24 us; elements one by one 38.)
 constexpr int kEmbShifted = 2;       // eights of a thread whose loads are in flight together
 
 template <typename T, typename O>
@@ -237,19 +238,16 @@ __global__ void __launch_bounds__(kEmbThreads, 5)
 // consecutive, so places of equal digits keep their order. A place without a token has the key
 // `classes`, behind all others.
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 16;
-constexpr int kZeroRows = 16384;     // rows of the table whose presence a block notes at a time
 // A few places are sorted by counting, for each, those that go before it: a comparison for each pair, on all
-// SMs, without a barrier between blocks (n = 2047: RANK_2047 us; the digits' passes SORT_2047).
-constexpr int kRankMost = 4096, kRankThreads = 256, kRankParts = 8, kRankPlaces = kRankThreads / kRankParts;
+// SMs, without a barrier between blocks (the whole gradient of 2047 x 787, added: 13.4 us, and 15.7 with the
+// digits' passes; of 4000: 19.9 and 17.6).
+constexpr int kRankMost = 2048, kRankThreads = 256, kRankParts = 8, kRankPlaces = kRankThreads / kRankParts;
 
 struct EmbSort {
     const int32_t* ids;
     int n, classes, passes, blocks;  // blocks that sort
     int32_t* keys[2];                // [n] each: the last pass writes keys[0], places[0]
     int32_t* places[2];
-    void* table;                     // its first zero_rows rows get zeros where the token is absent
-    int zero_rows;
-    int64_t row_bytes, pitch_bytes;
     int* err;
 };
 
@@ -317,7 +315,7 @@ __device__ __forceinline__ void sort_offsets(SortSums& q, int blocks, int block)
 }
 
 // The lanes whose digit (of 8 bits) is this lane's, by a vote on each bit: a match over the warp in one
-// instruction takes longer (34586 places: VOTE_US us in all, MATCH_US with it).
+// instruction takes longer (34586 places in 8 blocks: 30 us, 34 with it).
 __device__ __forceinline__ unsigned same_digit(unsigned digit)
 {
     unsigned same = 0xffffffffu;
@@ -442,36 +440,6 @@ __device__ __forceinline__ void zero_row(char* row, int64_t bytes, int lane)
     if (a < b && b + lane * 2 < end) *reinterpret_cast<uint16_t*>(b + lane * 2) = 0;
 }
 
-// zeros for the rows of tokens that do not occur, block `b` of `blocks`
-__device__ __forceinline__ void emb_zero(const EmbSort& a, int b, int blocks)
-{
-    __shared__ unsigned there[kZeroRows / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (a.zero_rows + blocks - 1) / blocks, threads = blockDim.x;
-    const int64_t end = min((int64_t)a.zero_rows, (int64_t)(b + 1) * per);
-    for (int64_t r0 = (int64_t)b * per; r0 < end; r0 += kZeroRows) {
-        const int rows = (int)min((int64_t)kZeroRows, end - r0);
-        __syncthreads();
-        for (int i = threadIdx.x; i < (rows + 31) / 32; i += threads) there[i] = 0;
-        __syncthreads();
-        for (int64_t i0 = threadIdx.x; i0 < a.n; i0 += 8 * threads) {
-            int id[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) id[u] = i0 + u * threads < a.n ? __ldg(a.ids + i0 + u * threads) : -1;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int64_t r = id[u] - r0;
-                if (id[u] >= 0 && r >= 0 && r < rows) atomicOr(&there[r >> 5], 1u << (r & 31));
-            }
-        }
-        __syncthreads();
-        for (int r = warp; r < rows; r += threads / 32) {
-            if (there[r >> 5] >> (r & 31) & 1) continue;
-            zero_row(static_cast<char*>(a.table) + (r0 + r) * a.pitch_bytes, a.row_bytes, lane);
-        }
-    }
-}
-
 __device__ __forceinline__ void check_ids(const EmbSort& a, int first, int step)
 {
     for (int i = first; i < a.n; i += step) {
@@ -488,13 +456,9 @@ __global__ void __launch_bounds__(kSortThreads) k_emb_sort(const __grid_constant
     __shared__ SortSums sums;
     griddep_wait();
     griddep_launch_dependents();
-    if ((int)blockIdx.x < a.blocks) {
-        if constexpr (R > 0) emb_sort_held<R>(a, sums, exchange);
-        else emb_sort(a, sums);
-        check_ids(a, blockIdx.x * kSortThreads + threadIdx.x, a.blocks * kSortThreads);
-    } else {
-        emb_zero(a, (int)blockIdx.x - a.blocks, (int)gridDim.x - a.blocks);
-    }
+    if constexpr (R > 0) emb_sort_held<R>(a, sums, exchange);
+    else emb_sort(a, sums);
+    check_ids(a, blockIdx.x * kSortThreads + threadIdx.x, a.blocks * kSortThreads);
 }
 
 // Eight threads to a place, each of which compares a share of the keys: those that are smaller, or equal and
@@ -504,10 +468,6 @@ __global__ void __launch_bounds__(kRankThreads) k_emb_rank(const __grid_constant
     __shared__ int4 keys[kRankMost / 4];
     griddep_wait();
     griddep_launch_dependents();
-    if ((int)blockIdx.x >= a.blocks) {
-        emb_zero(a, (int)blockIdx.x - a.blocks, (int)gridDim.x - a.blocks);
-        return;
-    }
     if (blockIdx.x == 0) check_ids(a, threadIdx.x, kRankThreads);
     const int vecs = (a.n + 4 * kRankParts - 1) / (4 * kRankParts) * kRankParts;     // padded with keys above all
     for (int i0 = threadIdx.x; i0 < 4 * vecs; i0 += 8 * kRankThreads) {
@@ -564,20 +524,20 @@ struct EmbSum {
     int64_t ldt;
     float *head, *tail;              // [spans][pitch]
     int pitch;
-    int sum_blocks;                  // the others write zeros to the rows from zero_from on
-    int zero_from;
+    int join_blocks;                 // the others of the joining kernel write zeros to the rows of absent tokens
+    int zero_rows;                   // of a warp
     int64_t row_bytes, pitch_bytes;
 };
 
-// The rows of absent tokens, kZeroWarpRows to a warp (32: 190 us instead of SUM_ZERO for 16384 x 4096 and
-// 32768 tokens, too few warps to keep the memory busy): each lane looks its row up among the sorted keys
-constexpr int kZeroWarpRows = 4;
-
+// The rows of absent tokens, zero_rows to a warp (32 KB, 32 rows at most): each lane looks its row up among
+// the sorted keys, and runs of absent rows are zeroed at once where nothing lies between rows. (512 KB to a
+// warp: the sums' kernel, which these were part of, took 190 us instead of 100 for 16384 x 4096 and 32768
+// tokens, because too few warps were left to keep the memory busy.)
 __device__ __forceinline__ void emb_zero_rest(const EmbSum& a, int64_t warp, int lane)
 {
-    const int64_t r0 = a.zero_from + warp * kZeroWarpRows, row = r0 + lane;
+    const int64_t r0 = warp * a.zero_rows, row = r0 + lane;
     bool absent = false;
-    if (lane < kZeroWarpRows && row < a.classes) {
+    if (lane < a.zero_rows && row < a.classes) {
         int lo = 0, hi = a.n;                        // the first key that is not below `row` is in lo .. hi
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
@@ -586,9 +546,14 @@ __device__ __forceinline__ void emb_zero_rest(const EmbSum& a, int64_t warp, int
         }
         absent = lo == a.n || __ldg(a.keys + lo) != row;
     }
-    const unsigned rows = __ballot_sync(0xffffffffu, absent);
-    for (int i = 0; i < kZeroWarpRows; ++i)
-        if (rows >> i & 1) zero_row(static_cast<char*>(a.table) + (r0 + i) * a.pitch_bytes, a.row_bytes, lane);
+    const bool dense = a.pitch_bytes == a.row_bytes;
+    for (unsigned rows = __ballot_sync(0xffffffffu, absent); rows;) {
+        const int first = __ffs(rows) - 1;
+        const unsigned gap = ~(rows >> first);       // its lowest bit: the length of the run of rows
+        const int run = dense ? (gap ? __ffs(gap) - 1 : 32) : 1;
+        zero_row(static_cast<char*>(a.table) + (r0 + first) * a.pitch_bytes, run * a.row_bytes, lane);
+        rows &= run + first >= 32 ? 0u : ~0u << (run + first);
+    }
 }
 
 template <typename O, bool VEC>
@@ -633,10 +598,6 @@ __global__ void __launch_bounds__(kSumThreads) k_emb_sum(const __grid_constant__
     __shared__ int state[kSumWarps];                 // of a warp's chunk: it has a head, that goes on; it has a tail
     constexpr int HEAD = 1, ON = 2, TAIL = 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x >= a.sum_blocks) {
-        emb_zero_rest(a, (int64_t)(blockIdx.x - a.sum_blocks) * kSumWarps + warp, lane);
-        return;
-    }
     const int span = (int)(blockIdx.x / a.strips), strip = (int)(blockIdx.x % a.strips);
     const int64_t lo = (int64_t)span * a.span + warp * a.chunk;
     const int len = (int)max((int64_t)0, min((int64_t)a.chunk, a.n - lo));
@@ -723,6 +684,10 @@ __global__ void __launch_bounds__(kSumThreads) k_emb_join(const __grid_constant_
     const int groups = (a.strips + kJoinWarps - 1) / kJoinWarps;
     const int span = (int)(blockIdx.x / groups), strip0 = (int)(blockIdx.x % groups) * kJoinWarps;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= a.join_blocks) {
+        emb_zero_rest(a, (int64_t)(blockIdx.x - a.join_blocks) * kJoinWarps + warp, lane);
+        return;
+    }
     const int end = (span + 1) * a.span;             // the span's last place is end - 1 (and end < n here)
     const int key = __ldg(a.keys + end - 1), first = __ldg(a.keys + span * a.span);
     const int before = span > 0 ? __ldg(a.keys + span * a.span - 1) : -1;
@@ -827,9 +792,6 @@ static int run_emb_fwd_to(int out_type, const int32_t* ids, int64_t n, const voi
 
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Bytes of zeros written while the places are sorted.
-constexpr int64_t kZeroBesideRank = 16 << 20, kZeroBesideSort = 112 << 20;
-
 // Places of a chunk: 32, or fewer down to 4 where that many would leave an SM fewer than 32 warps' work.
 static int sum_chunk(int64_t n, int strips)
 {
@@ -838,15 +800,14 @@ static int sum_chunk(int64_t n, int strips)
     return chunk;
 }
 
-static void sort_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&at)[2], int cluster, int blocks, size_t bytes,
-                        cudaStream_t s)
+static void sort_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&at)[2], int blocks, size_t bytes, cudaStream_t s)
 {
     cfg->gridDim = dim3((unsigned)blocks);
     cfg->blockDim = dim3(kSortThreads);
     cfg->dynamicSmemBytes = bytes;
     cfg->stream = s;
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.x = blocks;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -868,10 +829,9 @@ static int run_emb_sort(const EmbSort& q, cudaStream_t s)
             return f == cudaSuccess ? cudaFuncSetAttribute(k_emb_sort<R>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : f;
         });
     if (e != cudaSuccess) return set_error(ITO_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    const int zero = (std::min(2 * num_sms(), q.zero_rows) + q.blocks - 1) / q.blocks * q.blocks;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
-    sort_launch(&cfg, at, q.blocks, q.blocks + zero, BYTES, s);
+    sort_launch(&cfg, at, q.blocks, BYTES, s);
     e = cudaLaunchKernelEx(&cfg, k_emb_sort<R>, q);
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "embedding backward launch: %s", cudaGetErrorString(e));
 }
@@ -883,7 +843,7 @@ static bool sort_in_sixteen()
     if (!known) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute at[2];
-        sort_launch(&cfg, at, 16, 16, 4 * kSortThreads * 8, nullptr);
+        sort_launch(&cfg, at, 16, 4 * kSortThreads * 8, nullptr);
         cfg.numAttrs = 1;
         int got = 0;
         const bool fits = cudaFuncSetAttribute(k_emb_sort<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSortThreads * 8) == cudaSuccess &&
@@ -917,13 +877,13 @@ static EmbLayout emb_layout(int64_t n, int d)
 template <typename T, typename O>
 static int run_emb_sum(EmbSum a, bool vec, cudaStream_t s)
 {
-    a.sum_blocks = a.spans * a.strips;
-    const int zero = (a.classes - a.zero_from + kZeroWarpRows * kSumWarps - 1) / (kZeroWarpRows * kSumWarps);
-    launch_pdl(vec ? k_emb_sum<T, O, true> : k_emb_sum<T, O, false>, (unsigned)(a.sum_blocks + zero), kSumThreads, 0, s, a);
+    launch_pdl(vec ? k_emb_sum<T, O, true> : k_emb_sum<T, O, false>, (unsigned)(a.spans * a.strips), kSumThreads, 0, s, a);
     const int groups = (a.strips + kJoinWarps - 1) / kJoinWarps;
-    if (a.spans > 1)
-        launch_pdl(vec ? k_emb_join<O, true> : k_emb_join<O, false>, (unsigned)((int64_t)(a.spans - 1) * groups),
-                   kSumThreads, 0, s, a);
+    a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, 32768 / a.row_bytes));
+    const int zero = a.add ? 0 : (a.classes + a.zero_rows * kJoinWarps - 1) / (a.zero_rows * kJoinWarps);
+    a.join_blocks = (a.spans - 1) * groups;
+    if (a.join_blocks + zero)
+        launch_pdl(vec ? k_emb_join<O, true> : k_emb_join<O, false>, (unsigned)(a.join_blocks + zero), kSumThreads, 0, s, a);
     return launch_status("embedding backward");
 }
 
@@ -988,20 +948,14 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
         q.places[i] = reinterpret_cast<int32_t*>(ws + (2 + i) * l.keys);
     }
     const bool rank = n <= kRankMost;
-    q.table = dtable;
-    q.row_bytes = (int64_t)d * type_bytes(out_type);
-    q.pitch_bytes = ldt * (int64_t)type_bytes(out_type);
     q.err = err;
-    // zeros that take about as long as the sort
-    q.zero_rows = add ? 0 : (int)std::min<int64_t>(classes, (rank ? kZeroBesideRank : kZeroBesideSort) / q.row_bytes);
     if (rank) {
         q.blocks = (int)((n + kRankPlaces - 1) / kRankPlaces);
-        const int zero = std::min(4 * num_sms(), q.zero_rows);
-        launch_pdl(k_emb_rank, (unsigned)(q.blocks + zero), kRankThreads, 0, s, q);
+        launch_pdl(k_emb_rank, (unsigned)q.blocks, kRankThreads, 0, s, q);
         r = launch_status("embedding backward");
         if (r) return r;
     } else {
-        // (34586 places: SORT_16 us in 16 blocks, SORT_8 in 8)
+        // (34586 places: 20 us in 16 blocks, 29 in 8)
         q.blocks = n > 8192 && sort_in_sixteen() ? 16 : 8;
         const int64_t each = (n + q.blocks * kSortThreads - 1) / (q.blocks * kSortThreads);
         r = each <= 1 ? run_emb_sort<1>(q, s) : each <= 2 ? run_emb_sort<2>(q, s) : each <= 4 ? run_emb_sort<4>(q, s)
@@ -1028,9 +982,8 @@ int ito_embedding_bwd(const void* dy, int64_t lddy, int type, const int32_t* ids
     a.head = reinterpret_cast<float*>(ws + 4 * l.keys);
     a.tail = reinterpret_cast<float*>(ws + 4 * l.keys + l.pieces);
     a.pitch = l.pitch;
-    a.zero_from = add ? classes : q.zero_rows;
-    a.row_bytes = q.row_bytes;
-    a.pitch_bytes = q.pitch_bytes;
+    a.row_bytes = (int64_t)d * type_bytes(out_type);
+    a.pitch_bytes = ldt * (int64_t)type_bytes(out_type);
     const bool vec = rows_in_eights(dy, type, lddy, n, d) && rows_in_eights(dtable, out_type, ldt, classes, d);
     if (type == ITO_F32) return run_emb_sum<float, float>(a, vec, s);
     if (type == ITO_BF16)

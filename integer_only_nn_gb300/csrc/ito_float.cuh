@@ -171,9 +171,9 @@ struct Vec {
 };
 
 // Eight consecutive 16-bit elements at any of their addresses: the four aligned words that hold them, or
-// five and a shift by half a word where they begin in a word's middle. (Two aligned loads of 16 bytes have
-// fewer accesses, but words then have to be selected by the address: 105 instructions a copied eight instead
-// of INSTR_WORDS.) The words beyond the first and the last element may lie outside the tensor at its two ends:
+// five and a shift by half a word where they begin in a word's middle. (Two aligned loads of 16 bytes are
+// fewer accesses, but words then have to be selected by the address: a copy of 50001 x 787 takes 46 us
+// that way, 35 this way; a lookup of 30000 x 1001 44 and 24.) The words beyond the first and the last element may lie outside the tensor at its two ends:
 // whole() tells whether they are in its span of memory lo .. hi.
 struct Eight16 {
     uint32_t w[5];

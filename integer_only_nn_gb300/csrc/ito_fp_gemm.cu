@@ -193,49 +193,6 @@ __device__ __forceinline__ void store16(const float (&v)[32], int type, const CU
     if (lane == 0) bulk_commit();
 }
 
-// Two boxes side by side (64 columns, or 32 where there is one) by plain stores: a warp to a row, so a row's
-// store takes half as many accesses for its bytes as box by box (50001 x 787 sums of 333 products, us:
-// PLAIN_ONE by boxes, PLAIN_TWO by two). `which`: the box that v goes to; `flush`: it is the last.
-__device__ __forceinline__ void store16_plain(const float (&v)[32], int type, void* out, int64_t ld, FpStage& st, int which,
-                                              bool flush, int col, int row, int M, int N)
-{
-    const int lane = st.lane;
-    if (!which) {                                // (the boxes may still leave by TMA for another result)
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
-    }
-    const uint32_t at = smem_u32(st.p + which * kFpBox) + lane * 64;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        st_shared_v4(at + ((j ^ (lane >> 1 & 3)) << 4), (int)pack16(type, v[8 * j], v[8 * j + 1]),
-                     (int)pack16(type, v[8 * j + 2], v[8 * j + 3]), (int)pack16(type, v[8 * j + 4], v[8 * j + 5]),
-                     (int)pack16(type, v[8 * j + 6], v[8 * j + 7]));
-    if (!flush) return;
-    __syncwarp();
-    const int cols = min(32 + 32 * which, N - col);
-    const uint8_t* box = st.p + (lane >> 4) * kFpBox;
-    uint16_t* dst = static_cast<uint16_t*>(out) + (int64_t)row * ld + col;
-#pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 8) {
-        uint32_t x[8], next[8];                  // eight rows' words before their stores
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = box_word(box, r0 + k, lane & 15);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) next[k] = __shfl_down_sync(0xffffffffu, x[k], 1);
-#pragma unroll
-        for (int k = 0; k < 8; ++k, dst += ld) {
-            if (row + r0 + k >= M) break;
-            const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1 & 1);
-            const int c = 2 * lane + odd;        // columns c and c + 1
-            const uint32_t y = odd ? __funnelshift_r(x[k], next[k], 16) : x[k];
-            if (c + 1 < cols) *reinterpret_cast<uint32_t*>(dst + c) = y;
-            if (c + 1 == cols) dst[c] = (uint16_t)y;
-            if (odd && lane == 0) dst[0] = (uint16_t)x[k];
-        }
-    }
-    __syncwarp();
-}
-
 // 16 of the columns (half h) as 32-bit floats, staged
 __device__ __forceinline__ uint8_t* stage32(const float (&v)[32], int h, FpStage& st)
 {
@@ -373,16 +330,6 @@ __device__ __forceinline__ void add_row32(const float* r, int vec, int left, flo
     }
 }
 
-// a 16-bit result's group by TMA, or by plain stores: the group is the `which`-th of two side by side, `last` of them.
-// (With a second result, whose boxes go between, each group goes alone.)
-__device__ __forceinline__ void store16_group(const float (&v)[32], int type, const CUtensorMap* map, bool tma, bool alone,
-                                              void* out, int64_t ld, FpStage& st, int which, bool last, int col, int row, int M,
-                                              int N)
-{
-    if (tma || alone) store16(v, type, map, tma, out, ld, st, col, row, M, N);
-    else store16_plain(v, type, out, ld, st, which, last, col - 32 * which, row, M, N);
-}
-
 __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensorMap* mapY, const CUtensorMap* mapZ,
                                              float (&v)[32], const uint32_t (&res)[16], FpStage& st, int col, int row)
 {
@@ -409,8 +356,8 @@ __device__ __forceinline__ void finish_group(const FpGemmArgs& a, const CUtensor
 }
 
 // zg and zu of a gated layer: both biases, both saved, h = act(zg) zu
-__device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32], float (&u)[32], FpStage& st, int which,
-                                             bool last, int col, int row)
+__device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32], float (&u)[32], FpStage& st, int col,
+                                             int row)
 {
     const FpGemmArgs& a = p.a;
     const FpEpilogue& e = a.e;
@@ -423,12 +370,11 @@ __device__ __forceinline__ void finish_gated(const FpProblem& p, float (&g)[32],
     activate(e.act, g);
 #pragma unroll
     for (int i = 0; i < 32; ++i) g[i] *= u[i];
-    store16_group(g, e.type, &p.Y, a.y_tma, e.z, e.y, e.ldy, st, which, last, col, row, a.M, a.N);
+    store16(g, e.type, &p.Y, a.y_tma, e.y, e.ldy, st, col, row, a.M, a.N);
 }
 
 // a gradient's sums: *alpha sum + acc
-__device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int which, bool last,
-                                            int col, int row)
+__device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float (&v)[32], FpStage& st, int col, int row)
 {
     const FpGemmArgs& a = p.a;
     const FpEpilogue& e = a.e;
@@ -443,7 +389,7 @@ __device__ __forceinline__ void finish_grad(const FpProblem& p, int half, float 
     void* y = half ? a.x.y2 : e.y;
     const int64_t ld = half ? a.x.ldy2 : e.ldy;
     if (e.out_type == ITO_F32) store32(v, map, tma, y, ld, st, col, row, a.M, a.N);
-    else store16_group(v, e.out_type, map, tma, false, y, ld, st, which, last, col, row, a.M, a.N);
+    else store16(v, e.out_type, map, tma, y, ld, st, col, row, a.M, a.N);
 }
 
 // a warp's wait: one lane asks
@@ -594,7 +540,7 @@ __device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStag
         a.x.part[(int64_t)(col0 / columns * 2 + first) * a.M + row + lane] = make_float2(loss.m, loss.s);
 }
 
-// The epilogue of one of `step` warps' groups of 32 of the `columns` columns of a tile at
+// The epilogue of the groups of 32 columns first, first + step, .. below `columns` of a tile at
 // (row, col0), sums at `taddr`; `done` tells the issuing warp that the accumulator is drained. A
 // slice of K (slice >= 0) leaves its sums as they are, in the workspace. `half`: of a result in halves.
 template <FpEnd END, typename Wait, typename Done>
@@ -606,9 +552,7 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
     // a 16-bit residual comes while the sums are still being made
     const bool res16 = END == FpEnd::Linear && slice < 0 && a.e.residual && a.e.out_type != ITO_F32;
     uint32_t res[16];
-    // a run of consecutive groups for each of the `step` warps, two of which share their plain stores
-    const int each = (columns / 32 + step - 1) / step * 32, from = first * each, end = min(columns, from + each);
-    if (res16) load_residual16(a, col0 + from, row + st.lane, res);
+    if (res16) load_residual16(a, col0 + first * 32, row + st.lane, res);
     SlopeRow slope;
     if (END == FpEnd::DLogits) slope.load(a.x, a.M, row + st.lane, first == 0 && col0 == 0 && a.x.first == 0, a.err);
     if (!wait()) {
@@ -617,11 +561,11 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
     }
     tc_fence_after();
 #pragma unroll 1
-    for (int c = from; c < end; c += 32) {
+    for (int c = first * 32; c < columns; c += step * 32) {
         float v[32], u[32];
         if (END == FpEnd::Gated) load_sums(taddr + c, taddr + columns + c, v, u);
         else load_sums(taddr + c, v);
-        if (c + 32 >= end) {
+        if (c + step * 32 >= columns) {
             tc_fence_before();
             __syncwarp();
             done();
@@ -643,18 +587,16 @@ __device__ __forceinline__ void drain_tile(const FpProblem& p, int slice, int ha
             }
             continue;
         }
-        const int which = (c - from) >> 5 & 1;
-        const bool last = which || c + 32 >= end || col0 + c + 32 >= a.N;
         if (END == FpEnd::Linear) {
-            if (res16 && c > from) load_residual16(a, col0 + c, row + st.lane, res);
+            if (res16 && c > first * 32) load_residual16(a, col0 + c, row + st.lane, res);
             finish_group(a, &p.Y, &p.Z, v, res, st, col0 + c, row);
         } else if (END == FpEnd::Gated) {
-            finish_gated(p, v, u, st, which, last, col0 + c, row);
+            finish_gated(p, v, u, st, col0 + c, row);
         } else if (END == FpEnd::DLogits) {
             slope.apply(v, col0 + c);
             store16(v, a.e.type, &p.Y, true, a.e.y, a.e.ldy, st, col0 + c, row, a.M, a.N);
         } else {
-            finish_grad(p, half, v, st, which, last, col0 + c, row);
+            finish_grad(p, half, v, st, col0 + c, row);
         }
     }
 }
