@@ -92,6 +92,12 @@ struct FpCopy {
     Divider by[kFpCopies];                   // by eights of a row
     int n;
 };
+// Whether the words of all eights of the rows first .. last (Eight16: an element before the eight and one behind
+// it at most) lie in the tensor's span of memory.
+__host__ __device__ inline bool fp_copy_inner(int64_t first, int64_t last, int rows, int cols, int64_t ld)
+{
+    return first > 0 && last * ld + (cols + 7) / 8 * 8 < (int64_t)(rows - 1) * ld + cols;
+}
 int64_t fp_row_stride(int64_t ld, int rows, int cols);           // (a row's stride says nothing about a single row)
 bool fp_tma_rows(const void* p, int64_t ld, int rows, int cols);
 size_t fp_copy_bytes(const void* p, int64_t ld, int rows, int cols);

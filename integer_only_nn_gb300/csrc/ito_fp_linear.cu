@@ -54,9 +54,7 @@ __global__ void __launch_bounds__(kCopyThreads, 6) k_fp_align(const __grid_const
         const uint32_t rest = (uint32_t)(first - row0 * by.d), left = (uint32_t)min((int64_t)PER, total - first);
         const uint16_t* const src = c.src[z] + row0 * ld;
         uint16_t* const dst = c.dst[z] + row0 * ldd;
-        // only the tensor's first and last row have words that reach beyond it
-        const bool inner = row0 > 0 && row0 + by(rest + PER - 1) + 1 < rows;
-        if (inner) {
+        if (fp_copy_inner(row0, row0 + by(rest + PER - 1), rows, cols, ld)) {
             Eight16 e[kCopyAhead];
             const uint16_t* at[kCopyAhead];
             uint16_t* to[kCopyAhead];

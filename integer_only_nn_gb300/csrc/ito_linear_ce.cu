@@ -67,17 +67,23 @@ __global__ void __launch_bounds__(kCeJoinThreads)
 // ---------------------------------------------------------- backward's scale
 
 // float16 has no room below 6e-8 for the gradients of rare classes: dl carries a power of two that
-// brings the largest |g| to 2^12 .. 2^13, and the products' sums are multiplied by its inverse.
+// brings the largest |g| to 2^12 .. 2^13, and the products' sums are multiplied by its inverse. What rows without
+// a token hold in g_loss does not count.
 // out: [2] that factor and its inverse
 __global__ void __launch_bounds__(1024)
-    k_ce_scale(const float* __restrict__ g_loss, const float* __restrict__ g_lse, int rows, float* __restrict__ out)
+    k_ce_scale(const float* __restrict__ g_loss, const float* __restrict__ g_lse, const int32_t* __restrict__ targets,
+               int classes, int rows, float* __restrict__ out)
 {
     griddep_wait();
     griddep_launch_dependents();
     __shared__ float most[32];
     float m = 0.0f;
-    for (int r = threadIdx.x; r < rows; r += blockDim.x)
-        m = fmaxf(m, fabsf(g_loss[r]) + (g_lse ? fabsf(g_lse[r]) : 0.0f));
+#pragma unroll 4
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        const int t = targets[r];
+        const float g = fabsf(g_loss[r]);
+        m = fmaxf(m, (t >= 0 && t < classes ? g : 0.0f) + (g_lse ? fabsf(g_lse[r]) : 0.0f));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
@@ -227,7 +233,7 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
     float* scale = nullptr;
     if (type == ITO_F16) {
         scale = reinterpret_cast<float*>(ws);
-        launch_pdl(k_ce_scale, 1, 1024, 0, s, g_loss, g_lse, rows, scale);
+        launch_pdl(k_ce_scale, 1, 1024, 0, s, g_loss, g_lse, targets, classes, rows, scale);
         r = launch_status("linear cross entropy backward");
         if (r) return r;
     }

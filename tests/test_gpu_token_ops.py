@@ -609,6 +609,19 @@ def test_cross_entropy_small_factors_in_float16(torch, ito):
     assert all(bool((z == 0).all()) for z in zero)
 
 
+@pytest.mark.parametrize("junk", [1e30, -1e30, math.inf, math.nan])
+@pytest.mark.parametrize("rows", [5, 90])
+def test_cross_entropy_factors_of_rows_without_a_token(torch, ito, junk, rows):
+    """What they hold is not looked at: not for the gradient, and not for float16's factor."""
+    x, W, t = make_ce(torch, rows, 64, 300, "float16", 14)
+    t[::3] = -1
+    _, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    g = normal(torch, (rows,), 5).abs() * 2.0 ** -20
+    want = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, torch.where(t < 0, torch.zeros_like(g), g), dw_dtype=torch.float32)
+    got = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, torch.where(t < 0, torch.full_like(g, junk), g), dw_dtype=torch.float32)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((want[1] != 0).any())
+
+
 def test_cross_entropy_parts(torch, ito):
     for rows, d, classes in ((300, 136, 1000), (7, 64, 333)):
         x, W, t = make_ce(torch, rows, d, classes, "bfloat16", 4)
@@ -814,7 +827,7 @@ def test_a_token_model_step(torch, ito, n):
     L = Y @ e.T
     each = torch.logsumexp(L, 1) - L.gather(1, tgt.long()[:, None])[:, 0]
     each.mean().backward()
-    assert float((loss.double() - each).norm() / each.norm()) <= 4 * 2.0 ** -8
+    assert float((loss.double() - each.detach()).norm() / each.detach().norm()) <= 4 * 2.0 ** -8
     for got, leaf in zip((dE, dWg, dWu, dWd), leaves):
         assert float((got.double() - leaf.grad).norm() / leaf.grad.norm()) <= 20 * 2.0 ** -8
     assert ito._lib.ito_get_error() == 0
