@@ -39,8 +39,27 @@ struct Eight {
             for (int i = 0; i < kVecs; ++i) v[i].raw = make_uint4(0u, 0u, 0u, 0u);
         }
     }
+    // KEPT: nothing is written there while the kernel runs
+    template <bool KEPT>
     __device__ __forceinline__ void load_apart(const T* row, int c, int step, int n)
     {
+        if (c + 7 * step < n) {              // all of them: no look at each
+            const T* p = row + c;
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i, p += step) {
+                using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+                const Bits* q = reinterpret_cast<const Bits*>(p);
+                w[i] = KEPT ? __ldg(q) : *q;
+            }
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) v[i].raw = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            } else {
+                v[0].raw = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i].load_apart(row, c + i * Vec<T>::kPer * step, step, n);
     }
@@ -72,6 +91,17 @@ struct Eight {
     }
     __device__ __forceinline__ void store_apart(T* row, int c, int step, int n) const
     {
+        if (c + 7 * step < n) {
+            T* p = row + c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i, p += step) {
+                const uint4 r = v[i / Vec<T>::kPer].raw;
+                const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+                if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(p) = w[i & 3];
+                else *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i].store_apart(row, c + i * Vec<T>::kPer * step, step, n);
     }
@@ -80,11 +110,11 @@ struct Eight {
 // Lanes that share a row's strip of 8 lanes elements. VEC: lane l holds elements 8 l .. 8 l + 7 of
 // the strip (rows on 16-byte boundaries, d a multiple of 8); otherwise l, l + lanes, ..: consecutive
 // lanes touch consecutive elements either way.
-template <bool VEC, typename T>
+template <bool VEC, bool KEPT = true, typename T>
 __device__ __forceinline__ void load_strip(Eight<T>& e, const T* row, int strip, int lane, int lanes, int d)
 {
     if (VEC) e.load(row, strip * 8 * lanes + lane * 8, d);
-    else e.load_apart(row, strip * 8 * lanes + lane, lanes, d);
+    else e.template load_apart<KEPT>(row, strip * 8 * lanes + lane, lanes, d);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_strip(const Eight<T>& e, T* row, int strip, int lane, int lanes, int d)
@@ -93,11 +123,11 @@ __device__ __forceinline__ void store_strip(const Eight<T>& e, T* row, int strip
     else e.store_apart(row, strip * 8 * lanes + lane, lanes, d);
 }
 
-// lanes of a group: as many as a row has vectors, a power of two up to 32
+// lanes of a group: as many as a row has vectors, a power of two up to 32; -> its logarithm
 static int row_lanes(int d)
 {
-    int n = 1;
-    while (n < 32 && n * 8 < d) n *= 2;
+    int n = 0;
+    while (n < 5 && 8 << n < d) ++n;
     return n;
 }
 
@@ -109,44 +139,49 @@ constexpr int kEmbUnits = 4;         // strips of a group whose loads are in fli
 template <typename T, typename O, bool VEC>
 __global__ void __launch_bounds__(kEmbThreads)
     k_emb_fwd(const int32_t* __restrict__ ids, int64_t n, const T* __restrict__ table, int64_t ldt, int classes, int d,
-              int lanes, int strips, float scale, O* __restrict__ y, int64_t ldy, int* err)
+              int log_lanes, Divider strips, float scale, O* __restrict__ y, int64_t ldy, int* err)
 {
     griddep_wait();
     griddep_launch_dependents();
-    const int groups = kEmbThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t units = n * strips;
+    const int lanes = 1 << log_lanes, groups = kEmbThreads >> log_lanes, group = threadIdx.x >> log_lanes;
+    const int lane = threadIdx.x & (lanes - 1);
     const int64_t first = (int64_t)blockIdx.x * groups * kEmbUnits;
     // (one long division a block; what is left fits 32 bits)
-    const int64_t row0 = first / strips;
-    const unsigned rest = (unsigned)(first - row0 * strips);
-    Eight<T> e[kEmbUnits];
+    const int64_t row0 = first / strips.d;
+    const unsigned rest = (unsigned)(first - row0 * strips.d);
+    const unsigned units = (unsigned)min((int64_t)groups * kEmbUnits, n * strips.d - first);
+    unsigned row[kEmbUnits];
     int id[kEmbUnits];
 #pragma unroll
     for (int u = 0; u < kEmbUnits; ++u) {
-        const unsigned at = rest + u * groups + group;
-        const int64_t row = row0 + at / (unsigned)strips;
-        id[u] = first + u * groups + group < units ? ids[row] : -1;
+        const unsigned k = u * groups + group;
+        row[u] = strips(rest + k);
+        id[u] = k < units ? __ldg(ids + row0 + row[u]) : -1;
     }
+    Eight<T> e[kEmbUnits];
 #pragma unroll
     for (int u = 0; u < kEmbUnits; ++u) {
-        const unsigned at = rest + u * groups + group;
-        const int strip = (int)(at % (unsigned)strips);
-        const bool in = id[u] >= 0 && id[u] < classes;
+        const int strip = (int)(rest + u * groups + group - row[u] * strips.d);
+        const bool in = (unsigned)id[u] < (unsigned)classes;
         if (!in && id[u] != -1 && strip == 0 && lane == 0) raise_device_error(err, ITO_ERR_ARG);
         load_strip<VEC>(e[u], table + (in ? id[u] * ldt : 0), strip, lane, lanes, in ? d : 0);
     }
+    O* const out = y + row0 * ldy;
 #pragma unroll
     for (int u = 0; u < kEmbUnits; ++u) {
-        if (first + u * groups + group >= units) break;
-        const unsigned at = rest + u * groups + group;
-        const int64_t row = row0 + at / (unsigned)strips;
-        float f[8];
-        e[u].get(f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= scale;
+        const unsigned k = u * groups + group;
+        if (k >= units) break;
         Eight<O> o;
-        o.set(f);
-        store_strip<VEC>(o, y + row * ldy, (int)(at % (unsigned)strips), lane, lanes, d);
+        if (std::is_same<T, O>::value && scale == 1.0f) {
+            o = reinterpret_cast<const Eight<O>&>(e[u]);
+        } else {
+            float f[8];
+            e[u].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= scale;
+            o.set(f);
+        }
+        store_strip<VEC>(o, out + row[u] * ldy, (int)(rest + k - row[u] * strips.d), lane, lanes, d);
     }
 }
 
@@ -563,7 +598,7 @@ __device__ __forceinline__ void emb_put(const EmbSum& a, int key, int strip, int
     Eight<O> o;
     float f[8];
     if (a.add) {
-        load_strip<VEC>(o, static_cast<const O*>(row), strip, lane, 32, a.d);
+        load_strip<VEC, false>(o, static_cast<const O*>(row), strip, lane, 32, a.d);
         o.get(f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] += a.scale * s[i];
@@ -772,11 +807,11 @@ static int run_emb_fwd(const int32_t* ids, int64_t n, const void* table, int64_t
             return launch_status("embedding");
         }
     }
-    const int lanes = row_lanes(d), strips = (d + 8 * lanes - 1) / (8 * lanes);
+    const int log_lanes = row_lanes(d), lanes = 1 << log_lanes, strips = (d + 8 * lanes - 1) / (8 * lanes);
     const int64_t per = (int64_t)kEmbThreads / lanes * kEmbUnits, blocks = (n * strips + per - 1) / per;
     if (blocks > INT32_MAX) return set_error(ITO_ERR_SHAPE, "too many elements");
     launch_pdl(vec ? k_emb_fwd<T, O, true> : k_emb_fwd<T, O, false>, (unsigned)blocks, kEmbThreads, 0, s, ids, n,
-               static_cast<const T*>(table), ldt, classes, d, lanes, strips, scale, static_cast<O*>(y), ldy, err);
+               static_cast<const T*>(table), ldt, classes, d, log_lanes, Divider(strips), scale, static_cast<O*>(y), ldy, err);
     return launch_status("embedding");
 }
 
