@@ -564,7 +564,7 @@ struct EmbSum {
     int64_t row_bytes, pitch_bytes;
 };
 
-// The rows of absent tokens, zero_rows to a warp (32 KB, 32 rows at most): each lane looks its row up among
+// The rows of absent tokens, zero_rows to a warp (32 KB, 32 rows at most, 16 warps to an SM at least): each lane looks its row up among
 // the sorted keys, and runs of absent rows are zeroed at once where nothing lies between rows. (512 KB to a
 // warp: the sums' kernel, which these were part of, took 190 us instead of 100 for 16384 x 4096 and 32768
 // tokens, because too few warps were left to keep the memory busy.)
@@ -914,7 +914,7 @@ static int run_emb_sum(EmbSum a, bool vec, cudaStream_t s)
 {
     launch_pdl(vec ? k_emb_sum<T, O, true> : k_emb_sum<T, O, false>, (unsigned)(a.spans * a.strips), kSumThreads, 0, s, a);
     const int groups = (a.strips + kJoinWarps - 1) / kJoinWarps;
-    a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, 32768 / a.row_bytes));
+    a.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, 32768 / a.row_bytes), a.classes / (16 * num_sms())));
     const int zero = a.add ? 0 : (a.classes + a.zero_rows * kJoinWarps - 1) / (a.zero_rows * kJoinWarps);
     a.join_blocks = (a.spans - 1) * groups;
     if (a.join_blocks + zero)

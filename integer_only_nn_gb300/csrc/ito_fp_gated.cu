@@ -32,7 +32,7 @@ struct GatedDz {
 };
 
 template <int ACT>
-__global__ void __launch_bounds__(kGdThreads) k_fp_gated_dz(const __grid_constant__ GatedDz a)
+__global__ void __launch_bounds__(kGdThreads, 4) k_fp_gated_dz(const __grid_constant__ GatedDz a)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -122,11 +122,13 @@ __global__ void __launch_bounds__(kGdThreads) k_fp_gated_dz(const __grid_constan
 
 static int gated_half(int OC) { return (OC + 63) / 64 * 64; }
 
-static int gated_shares(int B, bool sums)
+// Shares of the batch. With sums they cost a block its barriers: as many as give an SM four blocks, of 64 rows at
+// least, and as a cluster has blocks (1262 x 16128, us: 8 shares 47, as many as this 38).
+static int gated_shares(int B, int half, bool sums)
 {
     if (!sums) return (B + 63) / 64;
     int n = 1;
-    while (n < kGdCluster && B >= 128 * n) n *= 2;
+    while (n < kGdCluster && B >= 128 * n && half / kGdColumns * n < 4 * num_sms()) n *= 2;
     return n;
 }
 
@@ -134,7 +136,7 @@ template <int ACT>
 static int run_gated_dz(GatedDz a, cudaStream_t s)
 {
     const bool sums = a.dbg || a.dbu;
-    a.shares = gated_shares(a.B, sums);
+    a.shares = gated_shares(a.B, a.half, sums);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.half / kGdColumns) * a.shares);
     cfg.blockDim = dim3(kGdThreads);
@@ -152,6 +154,12 @@ static int run_gated_dz(GatedDz a, cudaStream_t s)
     return e == cudaSuccess ? ITO_OK : set_error(ITO_ERR_CUDA, "gated layer backward launch: %s", cudaGetErrorString(e));
 }
 
+static bool gated_few(const void* x, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu, int B, int IC,
+                      int OC)
+{
+    return fp_few_rows(B, IC, OC, fp_rows_vec(x, ldx, Wg, ldwg, B, IC, OC) && fp_tma_rows(Wu, ldwu, OC, IC));
+}
+
 static int check_gated(int type, int act, int B, int IC, int OC)
 {
     const int r = fp_check_types(type, type, act);
@@ -167,7 +175,7 @@ extern "C" {
 size_t ito_fp_gated_linear_fwd_workspace_size(const void* x, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
                                               int64_t ldwu, int B, int IC, int OC)
 {
-    if (fp_check_sizes(B, IC, OC) || fp_few_rows(B, IC, OC)) return 0;
+    if (fp_check_sizes(B, IC, OC) || gated_few(x, ldx, Wg, ldwg, Wu, ldwu, B, IC, OC)) return 0;
     return fp_copy_bytes(x, ldx, B, IC) + fp_copy_bytes(Wg, ldwg, OC, IC) + fp_copy_bytes(Wu, ldwu, OC, IC) +
            fp_gemm_ws_bytes(B, OC, IC, false, FpEnd::Gated);
 }
@@ -201,7 +209,7 @@ int ito_fp_gated_linear_fwd(const void* x, int64_t ldx, const void* Wg, int64_t 
     more.z2 = zu;
     more.ldz2 = ldzu;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp_few_rows(B, IC, OC))
+    if (gated_few(x, ldx, Wg, ldwg, Wu, ldwu, B, IC, OC))
         return fp_run_rows<FpEnd::Gated>(x, ldx, Wg, ldwg, Wu, ldwu, B, IC, OC, e, more, s);
     char* ws = static_cast<char*>(workspace);
     FpCopy copies{};

@@ -1063,6 +1063,10 @@ __global__ void __launch_bounds__(256)
     griddep_launch_dependents();
     const int quads = pitch / 4, M = a.M, N = a.N;
     const FpEpilogue& e = a.e;
+    const bool half = END == FpEnd::Grad && blockIdx.y;
+    if (half) P += (int64_t)M * pitch;
+    void* const y = half ? a.x.y2 : e.y;
+    const int64_t ldy = half ? a.x.ldy2 : e.ldy;
     const int64_t n = (int64_t)M * quads;
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = i / quads;
@@ -1090,9 +1094,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (c + j < N) {
-                    float y = v[j] * alpha;
-                    if (a.x.acc) y += a.x.acc[r * a.x.ldacc + c + j];
-                    store_typed(e.y, e.out_type, r * e.ldy + c + j, y);
+                    float sum = v[j] * alpha;
+                    if (a.x.acc) sum += a.x.acc[r * a.x.ldacc + c + j];
+                    store_typed(y, e.out_type, r * ldy + c + j, sum);
                 }
         }
     }
@@ -1346,21 +1350,16 @@ static int fill_problem(FpProblem* q, const FpProduct& c, const FpPlan& p, void*
 }
 
 template <FpEnd END>
-static int run_join(const FpGemmArgs& given, const void* ws, cudaStream_t s)
+static int run_join(const FpGemmArgs& a, const void* ws, cudaStream_t s)
 {
-    FpGemmArgs a = given;
     const int64_t pitch = pad4(a.N), plane = pitch * a.M, stride = plane * planes(END, a.halves);
     const float* P = static_cast<const float*>(ws);
     if constexpr (END == FpEnd::Loss) {
         launch_pdl(k_fp_join_loss, a.M, 256, 0, s, P, a.splits, stride, (int)pitch, a);
         return launch_status("linear join");
     } else {
-        for (int h = 0; h < a.halves; ++h) {
-            launch_pdl(k_fp_join<END>, launch_grid_blocks((int64_t)a.M * (pitch / 4), 256), 256, 0, s, P + h * plane,
-                       a.splits, stride, (int)pitch, a);
-            a.e.y = a.x.y2;
-            a.e.ldy = a.x.ldy2;
-        }
+        launch_pdl(k_fp_join<END>, dim3(launch_grid_blocks((int64_t)a.M * (pitch / 4), 256), a.halves), 256, 0, s, P,
+                   a.splits, stride, (int)pitch, a);
         return launch_status("linear join");
     }
 }

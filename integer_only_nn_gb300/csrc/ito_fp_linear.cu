@@ -29,10 +29,11 @@ bool fp_rows_kernel(int B, int IC, int OC)
 
 // us of this kernel : the tensor cores'. Classes (Loss) 4096 -> 131072 with 8 rows 162 : 270, 9 207 : 248, 16
 // 239 : 174, 32 366 : 175; 1024 -> 50000 with 9 rows 31 : 33, 16 34 : 34, 32 48 : 34. Gated 4096 -> 8192 with 8
-// rows 23 : 39, 9 28 : 37, 16 30 : 26; 1024 -> 2048 with 16 rows 4.2 : 7.7, 32 6.8 : 7.8.
-bool fp_few_rows(int B, int IC, int OC)
+// rows 23 : 39, 9 28 : 37, 16 30 : 26; 1024 -> 2048 with 16 rows 4.2 : 7.7, 32 6.8 : 7.8. Of unaligned rows 31,
+// 2530 -> 1440, 24 : 11 and a copy of 5.
+bool fp_few_rows(int B, int IC, int OC, bool vec)
 {
-    return B < 16 || (B <= 32 && (int64_t)IC * OC <= (1 << 22));
+    return B < 16 || (vec && B <= 32 && (int64_t)IC * OC <= (1 << 22));
 }
 
 // --------------------------------------------------------- element-wise passes
@@ -212,6 +213,11 @@ bool fp_tma_rows(const void* p, int64_t ld, int rows, int cols)
 // A copy's rows are padded to 64 bytes: rows of 16-byte multiples have TMA read, and the copy write, a sector
 // of each 128 bytes more.
 static int64_t copy_ld(int64_t cols) { return (cols + 31) & ~int64_t(31); }
+
+bool fp_rows_vec(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC)
+{
+    return IC % 8 == 0 && fp_tma_rows(x, ldx, B, IC) && fp_tma_rows(W, ldw, OC, IC);
+}
 
 size_t fp_copy_bytes(const void* p, int64_t ld, int rows, int cols)
 {

@@ -226,8 +226,7 @@ static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw
 {
     int* const err = END == FpEnd::DLogits ? device_error_word() : nullptr;
     if (END == FpEnd::DLogits && !err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
-    const bool vec = IC % 8 == 0 && fp_tma_rows(x, ldx, B, IC) && fp_tma_rows(W, ldw, OC, IC) &&
-                     (!W2 || fp_tma_rows(W2, ldw2, OC, IC));
+    const bool vec = fp_rows_vec(x, ldx, W, ldw, B, IC, OC) && (!W2 || fp_tma_rows(W2, ldw2, OC, IC));
     // With blocks for two to an SM and more, 4 warps each let all of them run at the same time (one row of 4096 ->
     // 8192: 22 us instead of 25, of 4096 -> 131072 classes 162 instead of 173); fewer blocks have more warps. (The
     // number of warps is part of the sums' order: the plain linear layer keeps its.)

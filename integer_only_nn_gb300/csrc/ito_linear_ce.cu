@@ -115,9 +115,9 @@ static int64_t ce_ldl(int64_t piece) { return (piece + 63) & ~int64_t(63); }
 
 static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
-static int ce_parts(int rows, int d, int classes)
+static int ce_parts(int rows, int d, int classes, bool few)
 {
-    if (fp_few_rows(rows, d, classes)) return (classes + 15) / 16;
+    if (few) return (classes + 15) / 16;
     return std::max(1, fp_loss_parts(rows, classes, d));
 }
 
@@ -149,8 +149,9 @@ size_t ito_linear_cross_entropy_fwd_workspace_size(const void* x, int64_t ldx, c
                                                    int d, int classes)
 {
     if (fp_check_sizes(rows, d, classes)) return 0;
-    const size_t own = align256((size_t)ce_parts(rows, d, classes) * rows * 8) + align256((size_t)rows * 4);
-    if (fp_few_rows(rows, d, classes)) return own;
+    const bool few = fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
+    const size_t own = align256((size_t)ce_parts(rows, d, classes, few) * rows * 8) + align256((size_t)rows * 4);
+    if (few) return own;
     return own + fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d) +
            fp_gemm_ws_bytes(rows, classes, d, false, FpEnd::Loss);
 }
@@ -169,7 +170,8 @@ int ito_linear_cross_entropy_fwd(const void* x, int64_t ldx, const void* W, int6
     int* err = device_error_word();
     if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int parts = ce_parts(rows, d, classes);
+    const bool few = fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
+    const int parts = ce_parts(rows, d, classes, few);
     char* ws = static_cast<char*>(workspace);
     FpMore more{};
     more.targets = targets;
@@ -180,7 +182,7 @@ int ito_linear_cross_entropy_fwd(const void* x, int64_t ldx, const void* W, int6
     ws += align256((size_t)rows * 4);
     FpEpilogue e{};
     e.type = e.out_type = type;
-    if (fp_few_rows(rows, d, classes)) {
+    if (few) {
         r = fp_run_rows<FpEnd::Loss>(x, ldx, W, ldw, nullptr, 0, rows, d, classes, e, more, s);
     } else {
         FpCopy copies{};
@@ -268,8 +270,11 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
         logits.x.g_loss = g_loss;
         logits.x.g_lse = g_lse;
         logits.x.scale = scale;
-        r = fp_few_rows(rows, d, n) ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
-                                       : fp_gemm(&logits, 1, ws, s);
+        // (the products' copies serve the tensor cores' kernel where rows are not 16-byte ones)
+        const bool vec = fp_rows_vec(xa, ldx, w, ldw, rows, d, n);
+        r = vec && fp_few_rows(rows, d, n, vec)
+                ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
+                : fp_gemm(&logits, 1, ws, s);
         if (r) return r;
         FpProduct products[2];
         int k = 0;
