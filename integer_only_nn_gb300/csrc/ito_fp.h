@@ -79,6 +79,26 @@ int fp_gemm(const FpProduct* products, int n, void* ws, cudaStream_t s);
 // are the row's own
 int fp_loss_parts(int M, int N, int K);
 
+// Gradients of a product of a few rows (fp_few_grad_rows) with one weight or two of [V][D]; g: [B][V], rows on
+// 16-byte boundaries and padded to 64 elements, of which those from V on may hold anything.
+struct FpFewGrad {
+    const uint16_t* g[2];                    // (g[1] null: one weight)
+    int64_t ldg;
+    const uint16_t* W[2];
+    int64_t ldw[2];
+    const uint16_t* x;                       // [B][D]
+    int64_t ldx;
+    int type, out_type, B, V, D;
+    const float* alpha;                      // factor of all results; may be null (1)
+    void* dx;                                // [B][D] in type: sum over the weights of g W; may be null
+    int64_t lddx;
+    void* dW[2];                             // [V][D] in out_type: g^T x; both may be null
+    int64_t lddw[2];
+};
+bool fp_few_grad_rows(int B);
+size_t fp_few_grad_ws_bytes(int B, int V, int D, int weights);
+int fp_few_grad(const FpFewGrad& p, void* ws, cudaStream_t s);
+
 // ---- shared by the layers' entry points (ito_fp_linear.cu)
 
 // Rows whose starts TMA cannot address, copied to rows padded to 32 elements; up to three tensors

@@ -10,7 +10,8 @@
 //
 // Backward dzg and dzu stand side by side in the workspace, [B][2][OC padded to K blocks], rounded
 // once to the operands' type: dx is one product over both halves of K, dWg and dWu one of both
-// halves of rows, and the two share a launch (ito_fp_gemm.cu, FpEnd::Grad).
+// halves of rows, and the two share a launch (ito_fp_gemm.cu, FpEnd::Grad). Of a few rows both stream
+// the weights (ito_fp_few_grad.cu).
 #include "ito_fp_rows.cuh"
 
 namespace ito {
@@ -228,6 +229,7 @@ size_t ito_fp_gated_linear_bwd_workspace_size(const void* x, int64_t ldx, const 
 {
     if (fp_check_sizes(B, IC, OC)) return 0;
     const int half = gated_half(OC);
+    if (fp_few_grad_rows(B)) return align256((size_t)B * 2 * half * 2) + fp_few_grad_ws_bytes(B, OC, IC, 2);
     return align256((size_t)B * 2 * half * 2) + fp_copy_bytes(x, ldx, B, IC) + fp_copy_bytes(Wg, ldwg, OC, IC) +
            fp_copy_bytes(Wu, ldwu, OC, IC) + fp_gemm_ws_bytes(B, IC, 2 * half, true, FpEnd::Grad) +
            fp_gemm_ws_bytes(OC, IC, B, true, FpEnd::Grad, 2);
@@ -285,6 +287,14 @@ int ito_fp_gated_linear_bwd(const void* dh, int64_t lddh, const void* zg, int64_
     default: r = run_gated_dz<ITO_ACT_NONE>(a, s); break;
     }
     if (r) return r;
+    if (fp_few_grad_rows(B)) {
+        if (!a.dz) return ITO_OK;
+        FpFewGrad p{{a.dz, a.dz + half}, 2 * half,
+                    {static_cast<const uint16_t*>(Wg), static_cast<const uint16_t*>(Wu)}, {ldwg, ldwu},
+                    static_cast<const uint16_t*>(x), ldx, type, out_type, B, OC, IC, nullptr, dx, lddx, {dWg, dWu},
+                    {lddwg, lddwu}};
+        return fp_few_grad(p, ws + align256((size_t)B * 2 * half * 2), s);
+    }
     // the copies keep their places in the workspace whether or not all are made
     char* wx = ws + align256((size_t)B * 2 * half * 2);
     char* wg = wx + fp_copy_bytes(x, ldx, B, IC);

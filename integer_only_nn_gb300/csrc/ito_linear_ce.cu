@@ -11,7 +11,7 @@
 // Backward goes through the vocabulary in pieces: a piece's logits are computed again, their
 // epilogue leaves dl in the operands' type (rounded once; it is an operand of the two products
 // that follow), then dx's and dW's products of the piece share a launch. dx is added up over the
-// pieces in 32 bits and rounded at the last one.
+// pieces in 32 bits and rounded at the last one. Of a few rows the products stream W (ito_fp_few_grad.cu).
 #include "ito_fp_rows.cuh"
 
 namespace ito {
@@ -121,6 +121,17 @@ static int ce_parts(int rows, int d, int classes, bool few)
     return std::max(1, fp_loss_parts(rows, classes, d));
 }
 
+// Backward of a few rows, in one piece: the products stream W (fp_few_grad), and where the logits do so too, W and x are
+// read as they are (5 x 787 x 50001 f16, us: 101; with copies and all in tiles 142).
+struct CeFew {
+    bool grad, logits;
+};
+static CeFew ce_few(const void* x, int64_t ldx, const void* W, int64_t ldw, int rows, int d, int classes)
+{
+    const bool grad = fp_few_grad_rows(rows) && ce_piece(rows, classes) == classes;
+    return CeFew{grad, grad && fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes))};
+}
+
 static size_t ce_products_bytes(int rows, int d, int n)
 {
     return std::max(fp_gemm_ws_bytes(rows, n, d, false, FpEnd::DLogits),
@@ -206,8 +217,12 @@ size_t ito_linear_cross_entropy_bwd_workspace_size(const void* x, int64_t ldx, c
 {
     if (fp_check_sizes(rows, d, classes)) return 0;
     const int piece = ce_piece(rows, classes), last = (classes - 1) % piece + 1;
-    size_t n = 256 + fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d) +
-               align256((size_t)rows * ce_ldl(piece) * 2);
+    const CeFew few = ce_few(x, ldx, W, ldw, rows, d, classes);
+    size_t n = 256 + align256((size_t)rows * ce_ldl(piece) * 2);
+    if (!few.logits) n += fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d);
+    if (few.grad)
+        return n + std::max(few.logits ? 0 : fp_gemm_ws_bytes(rows, classes, d, false, FpEnd::DLogits),
+                            fp_few_grad_ws_bytes(rows, classes, d, 1));
     if (piece < classes) n += align256((size_t)rows * pad4(d) * 4);
     return n + std::max(ce_products_bytes(rows, d, piece), ce_products_bytes(rows, d, last));
 }
@@ -240,11 +255,16 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
         if (r) return r;
     }
     ws += 256;
-    FpCopy copies{};
-    const void* xa = fp_aligned_operand(x, &ldx, rows, d, &ws, &copies);
-    const uint16_t* wa = static_cast<const uint16_t*>(fp_aligned_operand(W, &ldw, classes, d, &ws, &copies));
-    r = fp_run_copies(copies, s);
-    if (r) return r;
+    const CeFew few = ce_few(x, ldx, W, ldw, rows, d, classes);
+    const void* xa = x;
+    const uint16_t* wa = static_cast<const uint16_t*>(W);
+    if (!few.logits) {
+        FpCopy copies{};
+        xa = fp_aligned_operand(x, &ldx, rows, d, &ws, &copies);
+        wa = static_cast<const uint16_t*>(fp_aligned_operand(W, &ldw, classes, d, &ws, &copies));
+        r = fp_run_copies(copies, s);
+        if (r) return r;
+    }
     void* dl = ws;
     const int64_t ldl = ce_ldl(piece);
     ws += align256((size_t)rows * ldl * 2);
@@ -270,12 +290,14 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
         logits.x.g_loss = g_loss;
         logits.x.g_lse = g_lse;
         logits.x.scale = scale;
-        // (the products' copies serve the tensor cores' kernel where rows are not 16-byte ones)
-        const bool vec = fp_rows_vec(xa, ldx, w, ldw, rows, d, n);
-        r = vec && fp_few_rows(rows, d, n, vec)
-                ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
-                : fp_gemm(&logits, 1, ws, s);
+        r = few.logits ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
+                       : fp_gemm(&logits, 1, ws, s);
         if (r) return r;
+        if (few.grad) {
+            const FpFewGrad p{{static_cast<const uint16_t*>(dl)}, ldl, {w}, {ldw}, static_cast<const uint16_t*>(xa), ldx,
+                              type, out_type, rows, n, d, scale ? scale + 1 : nullptr, dx, lddx, {dW}, {lddw}};
+            return fp_few_grad(p, ws, s);
+        }
         FpProduct products[2];
         int k = 0;
         if (dx) {

@@ -302,6 +302,78 @@ def test_gated_bwd_parts(torch, ito):
                 assert torch.equal(part[j], full[j])
 
 
+# (columns, rows of a weight): fewer than a tile's, one more, ragged ends; the last two give each warp many chunks
+FEW_SIZES = [(1, 1), (2, 16), (3, 40), (7, 17), (8, 15), (63, 33), (64, 16), (65, 1000), (130, 257), (264, 5000), (520, 70),
+             (4096, 4000), (2051, 7511)]
+
+
+@pytest.mark.parametrize("B", [1, 7, 8, 9, 16, 17])
+@pytest.mark.parametrize("i,size", list(enumerate(FEW_SIZES)))
+def test_gradients_of_few_rows(torch, ito, i, size, B):
+    n = i + B
+    dtype = ("bfloat16", "float16")[n % 2]
+    check_gated_bwd(torch, ito, B, *size, dtype, ACTS[n % 5], "float32" if n % 3 else dtype, seed=n)
+    x, W, t = make_ce(torch, B, *size, dtype, n, masked=n % 4 > 0)
+    _, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    g = normal(torch, (B,), n + 3).abs() + 0.1
+    check_ce_bwd(torch, ito, x, W, t, lse, g, None, dtype, dtype if n % 3 else "float32")
+
+
+@pytest.mark.parametrize("offset,pad", [(0, 0), (0, 8), (1, 0), (2, 3), (5, 2), (7, 1)])
+@pytest.mark.parametrize("size", [(1, 1, 3), (3, 5, 40), (9, 65, 33), (16, 130, 257), (8, 72, 1000)])
+def test_gradients_of_few_rows_amid_nan(torch, ito, offset, pad, size):
+    """Neither what lies between and around the rows of x and the weights nor the workspace's old contents come into the
+    results, and what lies between the results' rows is left as it was."""
+    B, IC, OC = size
+    lib = ito._lib
+
+    def amid(rows, cols, seed, scale):
+        t = normal(torch, (rows, cols), seed, scale, "bfloat16")
+        wide = torch.full((rows * (cols + offset + pad) + 16,), math.nan, dtype=torch.bfloat16, device="cuda")
+        v = torch.as_strided(wide, (rows, cols), (cols + offset + pad, 1), offset)
+        v.copy_(t)
+        return t, v
+
+    (x, xv), (Wg, gv), (Wu, uv) = (amid(r, IC, s, sc) for r, s, sc in ((B, 1, 1.0), (OC, 2, 0.2), (OC, 3, 0.2)))
+    dh, zg, zu = (normal(torch, (B, OC), s, 1.0, "bfloat16") for s in (4, 5, 6))
+    t = torch.randint(0, OC, (B,), device="cuda", dtype=torch.int32)
+    _, lse = ito.ito_linear_cross_entropy_fwd(x, Wg, t)
+    g = torch.ones(B, device="cuda")
+    # Logits of rows at other alignments are added in another order: dl may be rounded to the other side, half a step or
+    # 2^-8 of it each, and so the results (the 32-bit sums' own errors: the last factor).
+    dl = torch.exp(x.double() @ Wg.double().T - lse.double()[:, None])
+    dl[torch.arange(B, device="cuda"), t.long()] -= 1.0
+    apart = [4 * 2.0 ** -8 * 1.01 * m for m in (dl.abs() @ Wg.double().abs(), dl.abs().T @ x.double().abs())]
+    ld = IC + offset + pad
+    xs, gs, us = (xv.data_ptr(), ld), (gv.data_ptr(), ld), (uv.data_ptr(), ld)
+    for dw in (torch.bfloat16, torch.float32):
+        ty = ito.ITO_BF16 if dw is torch.bfloat16 else ito.ITO_F32
+        wants = (ito.ito_fp_gated_linear_bwd(dh, x, Wg, Wu, zg, zu, dw_dtype=dw)[:3],
+                 ito.ito_linear_cross_entropy_bwd(x, Wg, t, lse, g, dw_dtype=dw))
+        for k, want in enumerate(wants):
+            bufs = [torch.full((w.shape[0] * ld + 16,), 7.0, dtype=w.dtype, device="cuda") for w in want]
+            out = [v for b in bufs for v in (b.data_ptr() + offset * b.element_size(), ld)]
+            n = (lib.ito_linear_cross_entropy_bwd_workspace_size(*xs, *gs, B, IC, OC) if k else
+                 lib.ito_fp_gated_linear_bwd_workspace_size(*xs, *gs, *us, B, IC, OC))
+            ws = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")
+            if k:
+                r = lib.ito_linear_cross_entropy_bwd(*xs, *gs, ito.ITO_BF16, t.data_ptr(), lse.data_ptr(), g.data_ptr(), None,
+                                                     ty, B, IC, OC, ito._aligned256(ws), n, *out, ito._stream())
+            else:
+                r = lib.ito_fp_gated_linear_bwd(dh.data_ptr(), OC, zg.data_ptr(), OC, zu.data_ptr(), OC, *xs, *gs, *us,
+                                                ito.ITO_BF16, ty, ito.ITO_ACT_SILU, B, IC, OC, ito._aligned256(ws), n, *out,
+                                                None, None, ito._stream())
+            assert r == 0
+            for b, w, e in zip(bufs, want, apart if k else want):
+                cells = torch.as_strided(b, tuple(w.shape), (ld, 1), offset)
+                if k:
+                    assert bool(((cells.double() - w.double()).abs() <= e).all())
+                else:                    # the same products in the same order
+                    assert torch.equal(cells, w)
+                cells.fill_(7.0)
+                assert bool((b == 7.0).all())
+
+
 def test_gated_one_bias(torch, ito):
     x = normal(torch, (150, 72), 1, 1.0, "bfloat16")
     Wg, Wu = (normal(torch, (136, 72), s, 0.1, "bfloat16") for s in (2, 3))
