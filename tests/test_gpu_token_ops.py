@@ -374,6 +374,27 @@ def test_gradients_of_few_rows_amid_nan(torch, ito, offset, pad, size):
                 assert bool((b == 7.0).all())
 
 
+@pytest.mark.parametrize("B", [4, 13, 40])
+def test_gated_bwd_without_what_it_does_not_read(torch, ito, B):
+    """x may be missing where no dW is asked for, the weights where no dx is."""
+    IC, OC = 133, 77
+    x, dh = normal(torch, (B, IC), 1, 1.0, "float16"), normal(torch, (B, OC), 2, 1.0, "float16")
+    Wg, Wu = (normal(torch, (OC, IC), s, 0.1, "float16") for s in (3, 4))
+    zg, zu = (normal(torch, (B, OC), s, 1.0, "float16") for s in (5, 6))
+    want = ito.ito_fp_gated_linear_bwd(dh, x, Wg, Wu, zg, zu)
+    got = [torch.full_like(w, 7.0) for w in want[:3]]
+    dz = [v for t in (dh, zg, zu) for v in (t.data_ptr(), OC)]
+    for dx in (True, False):
+        xs = (None, IC) if dx else (x.data_ptr(), IC)
+        ws = (Wg.data_ptr(), IC, Wu.data_ptr(), IC) if dx else (None, IC, None, IC)
+        outs = [v for k, t in enumerate(got) for v in (t.data_ptr() if (k == 0) == dx else None, IC)]
+        n = ito._lib.ito_fp_gated_linear_bwd_workspace_size(*xs, *ws, B, IC, OC)
+        buf = torch.empty(n + 512, dtype=torch.uint8, device="cuda")
+        assert ito._lib.ito_fp_gated_linear_bwd(*dz, *xs, *ws, ito.ITO_F16, ito.ITO_F16, ito.ITO_ACT_SILU, B, IC, OC,
+                                                ito._aligned256(buf), n, *outs, None, None, ito._stream()) == 0
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_gated_one_bias(torch, ito):
     x = normal(torch, (150, 72), 1, 1.0, "bfloat16")
     Wg, Wu = (normal(torch, (136, 72), s, 0.1, "bfloat16") for s in (2, 3))
