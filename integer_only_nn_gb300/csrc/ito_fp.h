@@ -68,12 +68,16 @@ struct FpProduct {
     // Grad: with a_half, a second result y2 [M][N] from the rows a_half + m of A (an MN-major one; a
     // multiple of 8)
     int a_half;
+    // DLogits of a piece of the columns: how many there are in all (0: N). The plan is that of the whole, which
+    // the Loss had, so that the sums are the same in every bit.
+    int plan_n;
 };
 
 // One or two products that do not depend on one another and have the same end (two: Linear or Grad), on the
 // tensor cores; ws: the sum of the bytes that fp_gemm_ws_bytes names for each (sums of a product cut into
-// slices of K; b_mn: B.mn; halves: 2 for Grad with a_half), 256-byte aligned.
-size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end = FpEnd::Linear, int halves = 1);
+// slices of K; b_mn: B.mn; halves: 2 for Grad with a_half; plan_n as a product's), 256-byte aligned.
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end = FpEnd::Linear, int halves = 1,
+                        int plan_n = 0);
 int fp_gemm(const FpProduct* products, int n, void* ws, cudaStream_t s);
 // Parts of each row's sums that a Loss product leaves; 0: none, the workspace's slices are summed and (hit, part[0])
 // are the row's own

@@ -464,27 +464,42 @@ struct LossRow {
 
 // The tensor cores cut off what a sum's 24 bits cannot hold, at each step of 16 k: a chain of 256 steps
 // leaves logits short by 2^-17 of their size, and lse by 1.5e-6 of its own (4096 x 4096 -> 32768). So a
-// Loss product's sums are taken out of tensor memory every kLossChunk K blocks and added up in registers,
-// rounded: one accumulator is added while the other fills.
-constexpr int kLossChunk = 16;
+// logit's sums are taken out of tensor memory every kLogitChunk K blocks and added up in registers,
+// rounded: one accumulator is added while the other fills. The gradient's logits (DLogits) are summed as the Loss's
+// were, bit for bit: exp(l - lse) - 1 of a row whose target has nearly all of the probability is a difference
+// of neighbours, of which a logit short by 2^-17 leaves nothing right from p = 0.9999 on.
+constexpr int kLogitChunk = 16;
+template <FpEnd END>
+constexpr bool kLogits = END == FpEnd::Loss || END == FpEnd::DLogits;
+
+// Whether a tile with K blocks lo .. hi - 1 is drained in chunks. A DLogits tile of one chunk is not: the sums are the
+// same, and each 32 columns leave as soon as they are read (512 x 512 x 8192, both gradients, us: 26.4, in chunks 27.8).
+template <FpEnd END>
+__device__ __forceinline__ bool in_chunks(int lo, int hi)
+{
+    return END == FpEnd::Loss || (END == FpEnd::DLogits && hi - lo > kLogitChunk);
+}
 
 // K blocks from one drain of the accumulator to the next
 template <FpEnd END>
 __device__ __forceinline__ int chunk_end(int kb, int hi)
 {
-    return END == FpEnd::Loss ? min(hi, kb + kLossChunk) : hi;
+    return kLogits<END> ? min(hi, kb + kLogitChunk) : hi;
 }
 
-// A Loss tile's epilogue: as drain_tile, over all `chunks` of the tile's K range. ready() waits for a chunk's
-// sums and gives their place in tensor memory, done() tells that they are read.
-template <int MAX_COLS, typename Ready, typename Done>
-__device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStage& st, int first, int columns, int col0,
-                                           int row, int chunks, Ready ready, Done done, bool& ok)
+// The epilogue of a tile of logits: as drain_tile, over all `chunks` of the tile's K range. ready() waits for a
+// chunk's sums and gives their place in tensor memory, done() tells that they are read.
+template <FpEnd END, int MAX_COLS, typename Ready, typename Done>
+__device__ __forceinline__ void drain_logits(const FpProblem& p, int slice, FpStage& st, int first, int columns, int col0,
+                                             int row, int chunks, Ready ready, Done done, bool& ok)
 {
     constexpr int GROUPS = MAX_COLS / 64;            // (two warps to a row quarter)
     const FpGemmArgs& a = p.a;
     const int lane = st.lane;
-    LossRow loss{row + lane < a.M ? a.x.targets[row + lane] : -1, -INFINITY, 0.0f};
+    LossRow loss;
+    SlopeRow slope;
+    if (END == FpEnd::Loss) loss = LossRow{row + lane < a.M ? a.x.targets[row + lane] : -1, -INFINITY, 0.0f};
+    else slope.load(a.x, a.M, row + lane, first == 0 && col0 == 0 && a.x.first == 0, a.err);
     float sum[GROUPS][32];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g)
@@ -520,8 +535,13 @@ __device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStag
     for (int g = 0; g < GROUPS; ++g) {
         const int c = (first + 2 * g) * 32;
         if (c >= columns || row >= a.M || col0 + c >= a.N) continue;
-        if (slice < 0) {
+        if (slice < 0 && END == FpEnd::Loss) {
             loss.add(sum[g], col0 + c, a.N - col0 - c, a.x.hit + row + lane);
+            continue;
+        }
+        if (slice < 0) {
+            slope.apply(sum[g], col0 + c);
+            store16(sum[g], a.e.type, &p.Y, true, a.e.y, a.e.ldy, st, col0 + c, row, a.M, a.N);
             continue;
         }
 #pragma unroll
@@ -536,7 +556,7 @@ __device__ __forceinline__ void drain_loss(const FpProblem& p, int slice, FpStag
             }
         }
     }
-    if (slice < 0 && row + lane < a.M)
+    if (END == FpEnd::Loss && slice < 0 && row + lane < a.M)
         a.x.part[(int64_t)(col0 / columns * 2 + first) * a.M + row + lane] = make_float2(loss.m, loss.s);
 }
 
@@ -752,21 +772,23 @@ __global__ void __launch_bounds__(FpCfg<BN>::THREADS, 1) k_fp_gemm(const __grid_
             int tm, tn;
             tiles.coords(w / a.splits, tm, tn);
             const int half = END == FpEnd::Grad && tm >= num_m;
-            if constexpr (END == FpEnd::Loss) {
+            if constexpr (kLogits<END>) {
                 const int lo = (w % a.splits) * a.kb_per_split, hi = min(num_kb, lo + a.kb_per_split);
-                drain_loss<BN>(
-                    p, a.splits > 1 ? w % a.splits : -1, st, part, COLS, tn * COLS, tm * BM + quad * 32,
-                    (hi - lo + kLossChunk - 1) / kLossChunk,
-                    [&](uint32_t& taddr) {
-                        taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
-                        return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err);
-                    },
-                    [&] {
-                        if (lane == 0) mbar_arrive(&acce_bar[buf]);
-                        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
-                    },
-                    ok);
-                continue;
+                if (in_chunks<END>(lo, hi)) {
+                    drain_logits<END, BN>(
+                        p, a.splits > 1 ? w % a.splits : -1, st, part, COLS, tn * COLS, tm * BM + quad * 32,
+                        (hi - lo + kLogitChunk - 1) / kLogitChunk,
+                        [&](uint32_t& taddr) {
+                            taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
+                            return warp_wait(&accf_bar[buf], buf_phase, abort_flag, a.err);
+                        },
+                        [&] {
+                            if (lane == 0) mbar_arrive(&acce_bar[buf]);
+                            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+                        },
+                        ok);
+                    continue;
+                }
             }
             drain_tile<END>(
                 p, a.splits > 1 ? w % a.splits : -1, half, st, part, 2, COLS, tn * COLS,
@@ -1003,22 +1025,24 @@ __global__ void __launch_bounds__(FpPairCfg::THREADS, 1)
             const FpProblem& p = PROBLEMS == 1 || problem == 0 ? work.p[0] : work.p[LAST];
             int row, col, half;
             place(p.a, item, row, col, half);
-            if constexpr (END == FpEnd::Loss) {
+            if constexpr (kLogits<END>) {
                 int lo, hi;
                 k_range(p.a, item, lo, hi);
-                drain_loss<Cfg::MAX_BN>(
-                    p, p.a.splits > 1 ? item % p.a.splits : -1, st, part, p.a.bn, col, row + quad * 32,
-                    (hi - lo + kLossChunk - 1) / kLossChunk,
-                    [&](uint32_t& taddr) {
-                        taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN);
-                        return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err);
-                    },
-                    [&] {
-                        if (lane == 0) mbar_arrive_drained(mapa_shared(smem_u32(&acce_bar[buf]), 0));
-                        if (++buf == 2) { buf = 0; buf_phase ^= 1; }
-                    },
-                    ok);
-                continue;
+                if (in_chunks<END>(lo, hi)) {
+                    drain_logits<END, Cfg::MAX_BN>(
+                        p, p.a.splits > 1 ? item % p.a.splits : -1, st, part, p.a.bn, col, row + quad * 32,
+                        (hi - lo + kLogitChunk - 1) / kLogitChunk,
+                        [&](uint32_t& taddr) {
+                            taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * Cfg::MAX_BN);
+                            return warp_wait(&accf_bar[buf], buf_phase, abort_flag, err);
+                        },
+                        [&] {
+                            if (lane == 0) mbar_arrive_drained(mapa_shared(smem_u32(&acce_bar[buf]), 0));
+                            if (++buf == 2) { buf = 0; buf_phase ^= 1; }
+                        },
+                        ok);
+                    continue;
+                }
             }
             drain_tile<END>(
                 p, p.a.splits > 1 ? item % p.a.splits : -1, half, st, part, Cfg::EPI_WARPS / 4,
@@ -1199,9 +1223,9 @@ static size_t plan_bytes(const FpPlan& p, int M, int N, FpEnd end, int halves)
     return p.splits > 1 ? align256((size_t)p.splits * planes(end, halves) * M * pad4(N) * sizeof(float)) : 0;
 }
 
-size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end, int halves)
+size_t fp_gemm_ws_bytes(int M, int N, int K, bool b_mn, FpEnd end, int halves, int plan_n)
 {
-    return plan_bytes(fp_plan(M, N, K, b_mn, end, halves), M, N, end, halves);
+    return plan_bytes(fp_plan(M, plan_n ? plan_n : N, K, b_mn, end, halves), M, N, end, halves);
 }
 
 int fp_loss_parts(int M, int N, int K)
@@ -1408,7 +1432,7 @@ static int run_products(const FpProduct* c, int n, void* ws, cudaStream_t s)
     FpProblem q[2];
     void* at[2];
     for (int i = 0; i < n; ++i) {
-        p[i] = fp_plan(c[i].M, c[i].N, c[i].K, c[i].B.mn, END, halves_of(c[i]));
+        p[i] = fp_plan(c[i].M, c[i].plan_n ? c[i].plan_n : c[i].N, c[i].K, c[i].B.mn, END, halves_of(c[i]));
         at[i] = ws;
         ws = static_cast<char*>(ws) + plan_bytes(p[i], c[i].M, c[i].N, END, halves_of(c[i]));
         memset(&q[i], 0, sizeof(q[i]));

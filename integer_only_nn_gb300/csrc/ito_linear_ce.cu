@@ -8,10 +8,12 @@
 // the largest sum and the sum of exponentials (8 bytes for 64 to 128 logits), and the target's
 // logit; a second kernel joins them. Logits are never rounded to 16 bits.
 //
-// Backward goes through the vocabulary in pieces: a piece's logits are computed again, their
-// epilogue leaves dl in the operands' type (rounded once; it is an operand of the two products
-// that follow), then dx's and dW's products of the piece share a launch. dx is added up over the
-// pieces in 32 bits and rounded at the last one. Of a few rows the products stream W (ito_fp_few_grad.cu).
+// Backward goes through the vocabulary in pieces: a piece's logits are computed again, by the kernel that the
+// forward pass had and in the same order, so that they are what went into lse in every bit (p - 1 of a target with nearly
+// all of the probability is a difference of neighbours). Their epilogue leaves dl in the operands' type (rounded
+// once; it is an operand of the two products that follow), then dx's and dW's products of the piece share a launch.
+// dx is added up over the pieces in 32 bits and rounded at the last one. Of a few rows the products stream W
+// (ito_fp_few_grad.cu).
 #include "ito_fp_rows.cuh"
 
 namespace ito {
@@ -121,20 +123,21 @@ static int ce_parts(int rows, int d, int classes, bool few)
     return std::max(1, fp_loss_parts(rows, classes, d));
 }
 
-// Backward of a few rows, in one piece: the products stream W (fp_few_grad), and where the logits do so too, W and x are
-// read as they are (5 x 787 x 50001 f16, us: 101; with copies and all in tiles 142).
+// Backward of a few rows, which are in one piece (32 rows: up to 2^22 classes): the products stream W (fp_few_grad), and
+// the logits where the forward pass's did. Where both do, W and x are read as they are (5 x 787 x 50001 f16, us: 101;
+// with copies and all in tiles 142).
 struct CeFew {
     bool grad, logits;
 };
 static CeFew ce_few(const void* x, int64_t ldx, const void* W, int64_t ldw, int rows, int d, int classes)
 {
-    const bool grad = fp_few_grad_rows(rows) && ce_piece(rows, classes) == classes;
-    return CeFew{grad, grad && fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes))};
+    return CeFew{fp_few_grad_rows(rows), fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes))};
 }
 
-static size_t ce_products_bytes(int rows, int d, int n)
+// of a piece of n classes
+static size_t ce_products_bytes(int rows, int d, int classes, int n)
 {
-    return std::max(fp_gemm_ws_bytes(rows, n, d, false, FpEnd::DLogits),
+    return std::max(fp_gemm_ws_bytes(rows, n, d, false, FpEnd::DLogits, 1, classes),
                     fp_gemm_ws_bytes(rows, d, n, true, FpEnd::Grad) + fp_gemm_ws_bytes(n, d, rows, true, FpEnd::Grad));
 }
 
@@ -219,12 +222,12 @@ size_t ito_linear_cross_entropy_bwd_workspace_size(const void* x, int64_t ldx, c
     const int piece = ce_piece(rows, classes), last = (classes - 1) % piece + 1;
     const CeFew few = ce_few(x, ldx, W, ldw, rows, d, classes);
     size_t n = 256 + align256((size_t)rows * ce_ldl(piece) * 2);
-    if (!few.logits) n += fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d);
+    if (!few.logits || !few.grad) n += fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d);
     if (few.grad)
         return n + std::max(few.logits ? 0 : fp_gemm_ws_bytes(rows, classes, d, false, FpEnd::DLogits),
                             fp_few_grad_ws_bytes(rows, classes, d, 1));
     if (piece < classes) n += align256((size_t)rows * pad4(d) * 4);
-    return n + std::max(ce_products_bytes(rows, d, piece), ce_products_bytes(rows, d, last));
+    return n + std::max(ce_products_bytes(rows, d, classes, piece), ce_products_bytes(rows, d, classes, last));
 }
 
 int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int64_t ldw, int type,
@@ -258,7 +261,7 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
     const CeFew few = ce_few(x, ldx, W, ldw, rows, d, classes);
     const void* xa = x;
     const uint16_t* wa = static_cast<const uint16_t*>(W);
-    if (!few.logits) {
+    if (!few.logits || !few.grad) {
         FpCopy copies{};
         xa = fp_aligned_operand(x, &ldx, rows, d, &ws, &copies);
         wa = static_cast<const uint16_t*>(fp_aligned_operand(W, &ldw, classes, d, &ws, &copies));
@@ -290,6 +293,7 @@ int ito_linear_cross_entropy_bwd(const void* x, int64_t ldx, const void* W, int6
         logits.x.g_loss = g_loss;
         logits.x.g_lse = g_lse;
         logits.x.scale = scale;
+        logits.plan_n = classes;
         r = few.logits ? fp_run_rows<FpEnd::DLogits>(xa, ldx, w, ldw, nullptr, 0, rows, d, n, e, logits.x, s)
                        : fp_gemm(&logits, 1, ws, s);
         if (r) return r;

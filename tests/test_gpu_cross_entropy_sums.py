@@ -1,0 +1,108 @@
+"""The linear cross entropy where its sums matter most: rows whose target has nearly all of the probability, so that
+p - 1 is what is left of two values next to one another, and rows of many elements.
+
+Tolerances as in test_gpu_token_ops.py: U = 2^-24, a sum of n products with truncation is off by at most 2 n U sum|terms|."""
+import math
+
+import pytest
+
+from test_gpu_float_ops import TINY, U, f64, normal, within, within_rounded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ito(torch):
+    from gpu_util import import_ito
+    return import_ito()
+
+
+def confident(torch, rows, d, classes, dtype, seed, targets, logits):
+    """x and W of which row r has the logit logits[r] (before x is rounded) for its target, and logits of about a
+    normal distribution for the others."""
+    W = normal(torch, (classes, d), seed + 1, d ** -0.5, dtype)
+    V = W[targets].float()
+    n = normal(torch, (rows, d), seed)
+    along = (logits - (n * V).sum(1)) / (V * V).sum(1)
+    return (n + along[:, None] * V).to(W.dtype), W
+
+
+HALF = {"bfloat16": (2.0 ** -8, 2.0 ** -134), "float16": (2.0 ** -11, 2.0 ** -25)}
+
+
+def check_confident_bwd(torch, x, W, t, dtype, dx, dw):
+    """With l' = l + delta the logits that both passes form (the same sums, |delta| <= eL) and lse' = log sum exp(l')
+    off by `ev` where it is evaluated, the target's dl is exp(l'_t - lse') - 1: off by (1 - p) expm1(2 eL) for the
+    deltas, because 1 - p is a sum of exp(l'_j - l'_t), and by ev, the exponential and the difference. The other
+    classes' are off in proportion. Then the rounding of dl to 16 bits, and the products' sums."""
+    rows, d = x.shape
+    X, V = x.double(), W.double()
+    L = X @ V.T
+    lse = torch.logsumexp(L, 1)
+    span = L.amax(1) - L.amin(1)
+    p = torch.exp(L - lse[:, None])
+    eL = torch.expm1(2 * (2 * (d + 1) * U * (X.abs() @ V.abs().T)).amax(1))
+    ev = U * (224 + 8 * span) + U * lse.abs()       # (as check_ce_fwd of test_gpu_token_ops.py)
+    at = (torch.arange(rows, device="cuda"), t.long())
+    rest = p.clone()
+    rest[at] = 0
+    q = rest.sum(1)
+    assert bool((q < 1e-2).all()) and bool((q > 1e-6).all())
+    dl = rest
+    e = dl * ((eL + ev)[:, None] + 8 * U * (1 + (L - lse[:, None]).abs()))
+    dl[at] = -q
+    e[at] = q * eL + ev + 8 * U
+    half, floor = HALF[dtype]
+    e = e + (dl.abs() + e) * half * (1 + 2.0 ** -20) + floor
+    m = dl.abs() + e
+    if dw is not None:
+        within(dw, f64(dl.T @ X), f64(e.T @ X.abs() + 2 * rows * U * (m.T @ X.abs())), "dW")
+        # a row's dl add up to 0: their sums, from dW's columns' sums by the rows of x (rows < d: they are independent)
+        S = dw.double().sum(0)
+        inv = torch.linalg.inv(X @ X.T) @ X
+        sums = inv @ S
+        tol = e.sum(1) + inv.abs() @ (2 * rows * U * (m.T @ X.abs()).sum(0))
+        within(sums, 0 * f64(sums), f64(tol), "sum of dl")
+    if dx is not None:
+        within_rounded(dx, f64(dl @ V), f64(e @ V.abs() + 2 * W.shape[0] * U * (m @ V.abs())), dtype, "dx")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("rows,d,classes", [(3, 4096, 600), (16, 8192, 640), (20, 4096, 600), (17, 8192, 700), (40, 4096, 600),
+                                            (130, 4095, 611), (300, 8192, 600), (300, 4104, 5000)])
+def test_gradient_of_confident_rows(torch, ito, rows, d, classes, dtype):
+    """1 - p of the targets from 1e-3 to 1e-5."""
+    t = torch.randperm(classes, generator=torch.Generator(device="cuda").manual_seed(rows), device="cuda")[:rows].to(torch.int32)
+    logits = math.log(classes) + 0.5 + torch.linspace(math.log(1e3), math.log(1e5), rows, device="cuda")
+    x, W = confident(torch, rows, d, classes, dtype, rows + d, t.long(), logits)
+    loss, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    g = torch.ones(rows, device="cuda")
+    dx, dw = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, g, dw_dtype=torch.float32)
+    check_confident_bwd(torch, x, W, t, dtype, dx, dw)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_gradient_of_confident_rows_in_a_narrow_last_piece(torch, ito, dtype):
+    """Targets in the last piece of the vocabulary, of 24 classes: their logits are the sums that the forward pass
+    formed, so their gradient is, bit for bit, that of a call of fewer rows, which has the vocabulary in one piece."""
+    rows, d, wide, some = 4200, 4096, 31744, 24
+    classes = wide + some
+    at = torch.arange(some, device="cuda") + wide
+    t = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    t[:some] = at.to(torch.int32)
+    x = normal(torch, (rows, d), 5, 1.0, dtype)
+    logits = math.log(classes) + 0.5 + torch.linspace(math.log(1e3), math.log(1e5), some, device="cuda")
+    first, W = confident(torch, some, d, classes, dtype, 7, at, logits)
+    x[:some] = first
+    loss, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    g = torch.ones(rows, device="cuda")
+    dw = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, g, need_dx=False, dw_dtype=torch.float32)[1]
+    n = 300
+    part = ito.ito_linear_cross_entropy_bwd(x[:n], W, t[:n], lse[:n], g[:n], need_dx=False, dw_dtype=torch.float32)[1]
+    assert torch.equal(dw[wide:], part[wide:])
+    check_confident_bwd(torch, x[:some], W, t[:some], dtype, None, dw)
