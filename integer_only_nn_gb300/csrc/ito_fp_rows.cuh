@@ -54,6 +54,10 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p)      // (read by o
 // warps of a block, at most
 template <FpEnd END, int NT>
 constexpr int kRowsWarps = END == FpEnd::Linear || NT > 2 ? 8 : 16;
+// These products too cut off what a sum's 24 bits cannot hold at each step of 16 k, and a warp's chain of them grows
+// with IC (16384 in 4 warps: a logit of positive products short by 1.3e-5 of itself). So a logit's chains end every 1024 k
+// of a warp, and their sums are added up, rounded. (The linear and the gated layer's results are rounded to 16 bits.)
+constexpr int kRowsChain = 1024;
 // steps of 32 k whose loads of W are in flight together
 template <FpEnd END, bool VEC>
 constexpr int kRowsSteps = END == FpEnd::Linear ? 4 : 2;
@@ -62,8 +66,9 @@ constexpr int kRowsSteps = END == FpEnd::Linear ? 4 : 2;
 // elements come in words and a shift (Eight16; the plain linear layer, whose sums keep their
 // order and so their four steps, loads them one by one). The gated layer
 // streams two weights, 16 rows of each to a block, half as many steps of each ahead (the same bytes
-// in flight and registers). A Loss leaves each row's parts of 16 columns; DLogits are as from the tensor cores' kernels.
-template <FpEnd END, int NT, bool VEC>
+// in flight and registers). LONG: logits of rows that take a warp more than one chain; the sums wait in shared memory, because
+// registers for them cost blocks of an SM (13 x 1531 x 50001 f16 143 us instead of 122). A Loss leaves each row's parts of 16 columns; DLogits are as from the tensor cores' kernels.
+template <FpEnd END, int NT, bool VEC, bool LONG>
 __global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
     k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ W, int64_t ldw,
               const uint16_t* __restrict__ W2, int64_t ldw2, int B, int IC, int OC, const __grid_constant__ FpEpilogue e,
@@ -126,15 +131,31 @@ __global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
         return load_eight(row, k, IC, VEC);
     };
     float c[WS][NT][4];
+    auto clear = [&] {
 #pragma unroll
-    for (int h = 0; h < WS; ++h)
+        for (int h = 0; h < WS; ++h)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[h][n][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) c[h][n][i] = 0.0f;
+    };
+    clear();
+    // this warp's sums, put down or added to what it has put down
+    auto put = [&](bool again) {
+#pragma unroll
+        for (int h = 0; h < WS; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float& at = part[warp][h][(n * 8 + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)];
+                    at = again ? at + c[h][n][i] : c[h][n][i];
+                }
+    };
     Raw a[WS][U], b[WS][U];
     const int stride = warps * U * 32;
-    int k0 = warp * U * 32;
+    int k0 = warp * U * 32, steps = 0;               // (steps of the chain)
+    bool again = false;
 #pragma unroll
     for (int h = 0; h < WS; ++h)
 #pragma unroll
@@ -185,14 +206,14 @@ __global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
                 a[h][u] = an[h][u];
                 b[h][u] = bn[h][u];
             }
+        if (LONG && ++steps == kRowsChain / (U * 32)) {
+            put(again);
+            clear();
+            again = true;
+            steps = 0;
+        }
     }
-#pragma unroll
-    for (int h = 0; h < WS; ++h)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                part[warp][h][(n * 8 + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = c[h][n][i];
+    put(LONG && again);
     __syncthreads();
     // (whole warps go round: 16 x 8 NT sums and the block's threads are multiples of 32)
     for (int i = threadIdx.x; i < 16 * 8 * NT; i += blockDim.x) {
@@ -234,7 +255,10 @@ static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw
     const int most = END == FpEnd::Linear ? 8 : std::min(kRowsWarps<END, NT>, blocks < num_sms() ? 16 : blocks < 2 * num_sms() ? 8 : 4);
     const int step = 32 * (vec ? kRowsSteps<END, true> : kRowsSteps<END, false>);
     const int warps = std::min(most, std::max(1, (IC + step - 1) / step));
-    launch_pdl(vec ? k_fp_rows<END, NT, true> : k_fp_rows<END, NT, false>, (OC + 15) / 16, warps * 32,
+    constexpr bool LOGITS = END == FpEnd::Loss || END == FpEnd::DLogits;
+    auto* kern = vec ? k_fp_rows<END, NT, true, false> : k_fp_rows<END, NT, false, false>;
+    if (LOGITS && IC > warps * kRowsChain) kern = vec ? k_fp_rows<END, NT, true, LOGITS> : k_fp_rows<END, NT, false, LOGITS>;
+    launch_pdl(kern, (OC + 15) / 16, warps * 32,
                (size_t)warps * (END == FpEnd::Gated ? 2 : 1) * 16 * 8 * NT * sizeof(float), s,
                static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(W), ldw,
                static_cast<const uint16_t*>(W2), ldw2, B, IC, OC, e, more, err);

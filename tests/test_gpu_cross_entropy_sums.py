@@ -106,3 +106,28 @@ def test_gradient_of_confident_rows_in_a_narrow_last_piece(torch, ito, dtype):
     part = ito.ito_linear_cross_entropy_bwd(x[:n], W, t[:n], lse[:n], g[:n], need_dx=False, dw_dtype=torch.float32)[1]
     assert torch.equal(dw[wide:], part[wide:])
     check_confident_bwd(torch, x[:some], W, t[:some], dtype, None, dw)
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("rows,d,classes", [(1, 16384, 5000), (1, 65536, 64), (9, 65536, 5000), (12, 32776, 3000), (20, 32768, 100),
+                                            (40, 65536, 300)])
+def test_logits_of_long_rows(torch, ito, rows, d, classes, offset):
+    """Positive products, whose sums only grow, so that what each step of 16 k cuts off adds up. A chain of at most
+    1024 k loses at most 2^-23 of its sum at each of 64 steps; the chains' sums are added rounded: at most d / 1024 and 16
+    (of warps or slices) of them, U each. lse and the logit of the target are off by as much of themselves; what they are
+    evaluated with as in check_ce_fwd of test_gpu_token_ops.py."""
+    x = normal(torch, (rows, d), 1).abs().to(torch.bfloat16)
+    wide = torch.zeros((classes, d + offset), dtype=torch.bfloat16, device="cuda")
+    W = wide[:, offset:]
+    W.copy_(normal(torch, (classes, d), 2).abs() * (100 / d / 0.64))
+    t = (torch.arange(rows, device="cuda") * 7 % classes).to(torch.int32)
+    loss, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    L = x.double() @ W.double().T
+    want = torch.logsumexp(L, 1)
+    span = L.amax(1) - L.amin(1)
+    s = torch.log(torch.exp(L - L.amax(1, keepdim=True)).sum(1))
+    eL = (64 * 2.0 ** -23 + (d / 1024 + 16) * U) * L.amax(1)
+    e = eL + U * (224 + 8 * span) + 2 * U * s.abs() + U * want.abs() + TINY
+    within(lse, f64(want), f64(e), "lse")
+    l = want - L.gather(1, t.long()[:, None])[:, 0]
+    within(loss, f64(l), f64(e + eL + U * l.abs()), "loss")
