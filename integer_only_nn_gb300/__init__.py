@@ -828,6 +828,9 @@ _F32 = None             # torch.float32, once torch is there
 _raw_stream_of = None   # device index -> the current stream's handle
 _current_device = None  # -> the current device's index
 _address = None         # Tensor.data_ptr
+_INT = (1 << 31) - 1    # the largest int of the library: ctypes would pass on the low 32 bits of a larger one
+_LONG = (1 << 63) - 1
+_MOST_CLASSES = 1 << 30 # of an embedding
 
 
 def _float_setup():
@@ -854,7 +857,7 @@ def _type_id(dtype, name):
 
 def _act_id(act):
     r = _ACTS.get(act, act)
-    if not isinstance(r, int):
+    if not isinstance(r, int) or not ITO_ACT_NONE <= r <= ITO_ACT_SILU:
         raise ItoError(ITO_ERR_ARG, "unknown activation %r" % (act,))
     return r
 
@@ -874,15 +877,17 @@ def _elsewhere(t, name, index):
     raise ItoError(ITO_ERR_ARG, "%s: on %s, expected cuda:%d" % (name, t.device, index))
 
 
-def _matrix(t, name, rows, cols, dtype, index):
+def _matrix(t, name, rows, cols, dtype, index, most=_INT):
     """Checks a 2-D tensor on the device `index` whose rows' elements are consecutive (rows, cols,
-    dtype: None for any); -> its row stride."""
+    dtype: None for any; any rows up to `most`, columns up to an int); -> its row stride."""
     shape = t.shape
     if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, expected [%s][%s]" % (
             name, list(shape), "rows" if rows is None else rows, "columns" if cols is None else cols))
     if not shape[0] or not shape[1]:
         raise ItoError(ITO_ERR_SHAPE, "%s: no elements" % name)
+    if shape[1] > _INT or (rows is None and shape[0] > most):
+        raise ItoError(ITO_ERR_SHAPE, "%s: shape %s, a size that 32 bits do not hold" % (name, list(shape)))
     if t.get_device() != index:
         _elsewhere(t, name, index)
     if dtype is not None and t.dtype is not dtype:
@@ -1103,7 +1108,7 @@ def ito_layer_norm_fwd(x, gamma=None, beta=None, eps=1e-5, stream=None):
     if stream is not None:
         return _on_stream(lambda: ito_layer_norm_fwd(x, gamma, beta, eps), stream, x, gamma, beta)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
-    ldx = _matrix(x, "x", None, None, None, index)
+    ldx = _matrix(x, "x", None, None, None, index, _LONG)
     rows, cols = x.shape
     pg, pb = _vector(gamma, "gamma", cols, index, dtype, _F32), _vector(beta, "beta", cols, index, dtype, _F32)
     if pg is not None and pb is not None and gamma.dtype is not beta.dtype:
@@ -1127,7 +1132,7 @@ def ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx=True, need_dw=True, str
         return _on_stream(lambda: ito_layer_norm_bwd(dy, x, gamma, mean, rstd, need_dx, need_dw), stream, dy, x, gamma, mean,
                           rstd)
     dtype, dev, index = x.dtype, x.device, _device_index(x, "x")
-    ldx = _matrix(x, "x", None, None, None, index)
+    ldx = _matrix(x, "x", None, None, None, index, _LONG)
     rows, cols = x.shape
     lddy = _matrix(dy, "dy", rows, cols, dtype, index)
     pg = _vector(gamma, "gamma", cols, index, dtype, _F32)
@@ -1158,7 +1163,7 @@ def ito_token_logprobs_fwd(logits, targets=None, k=0, stream=None):
     if stream is not None:
         return _on_stream(lambda: ito_token_logprobs_fwd(logits, targets, k), stream, logits, targets)
     dev, index = logits.device, _device_index(logits, "logits")
-    ld = _matrix(logits, "logits", None, None, None, index)
+    ld = _matrix(logits, "logits", None, None, None, index, _LONG)
     rows, classes = logits.shape
     pt = _vector(targets, "targets", rows, index, torch.int32)
     if not 0 <= k <= 32:
@@ -1186,7 +1191,7 @@ def ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp=None, g_entropy
         return _on_stream(lambda: ito_token_logprobs_bwd(logits, targets, lse, entropy, g_logp, g_entropy, out), stream, logits,
                           targets, lse, entropy, g_logp, g_entropy, out)
     dtype, dev, index = logits.dtype, logits.device, _device_index(logits, "logits")
-    ld = _matrix(logits, "logits", None, None, None, index)
+    ld = _matrix(logits, "logits", None, None, None, index, _LONG)
     rows, classes = logits.shape
     pt = _vector(targets, "targets", rows, index, torch.int32)
     pl, pe = _vector(lse, "lse", rows, index, _F32), _vector(entropy, "entropy", rows, index, _F32)
@@ -1292,6 +1297,8 @@ def ito_embedding_bwd(dy, ids, classes, scale=1.0, dtype=None, add_to=None, stre
     lddy = _matrix(dy, "dy", n, None, None, index)
     d = dy.shape[1]
     pi = _vector(ids, "ids", n, index, torch.int32)
+    if not 1 <= classes <= _MOST_CLASSES:
+        raise ItoError(ITO_ERR_SHAPE, "classes must be in 1 .. 2^30")
     if add_to is not None:
         if dtype is not None and add_to.dtype is not dtype:
             raise ItoError(ITO_ERR_ARG, "add_to: type %s, expected %s" % (add_to.dtype, dtype))
@@ -1300,8 +1307,6 @@ def ito_embedding_bwd(dy, ids, classes, scale=1.0, dtype=None, add_to=None, stre
         ldt, out = d, None
     oty = _type_id(add_to.dtype if out is not None else _F32 if dtype is None else dtype, "dtype")
     ty = _type_id(dy.dtype, "dy")
-    if classes < 1:
-        raise ItoError(ITO_ERR_SHAPE, "classes must be >= 1")
     if out is None:
         out = torch.empty((classes, d), dtype=_F32 if dtype is None else dtype, device=dev)
     s = _raw_stream_of(index)
