@@ -17,6 +17,7 @@
 // 16384 x 4096 of 32768, because the presence of a token is then not known from the sorted ones).
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "ito_float.cuh"
 
@@ -265,6 +266,32 @@ __global__ void __launch_bounds__(kEmbThreads, 5)
     }
 }
 
+// a row of zeros by a warp: 16 bytes at a time, its ends up to the next 16-byte boundary by elements of 2
+__device__ __forceinline__ void zero_row(char* row, int64_t bytes, int lane)
+{
+    char* const end = row + bytes;
+    char* const a = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(row) + 15) & ~uintptr_t(15));
+    char* const b = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+    for (char* p = a + lane * 16; p < b; p += 512) *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+    char* const head = a < b ? a : end;              // (a row may lie within 32 bytes)
+    if (row + lane * 2 < head) *reinterpret_cast<uint16_t*>(row + lane * 2) = 0;
+    if (a < b && b + lane * 2 < end) *reinterpret_cast<uint16_t*>(b + lane * 2) = 0;
+}
+
+// The rows of places without a token, a warp to a place, after a lookup with a scale that is not finite: the
+// lookup's kernels multiply their zeros by it. (Looked at there, the lookup takes 43.2 us instead of 40.5 for 16384 x 4096
+// bf16 and 37 instead of 31 for 30000 x 1001 from float32.)
+__global__ void __launch_bounds__(kEmbThreads)
+    k_emb_none(const int32_t* __restrict__ ids, int64_t n, int classes, void* y, int64_t pitch_bytes, int64_t row_bytes)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t warps = (int64_t)gridDim.x * (kEmbThreads / 32);
+    for (int64_t i = (int64_t)blockIdx.x * (kEmbThreads / 32) + (threadIdx.x >> 5); i < n; i += warps)
+        if ((unsigned)__ldg(ids + i) >= (unsigned)classes)
+            zero_row(static_cast<char*>(y) + i * pitch_bytes, row_bytes, threadIdx.x & 31);
+}
+
 // ------------------------------------------------------- sorting places by token
 
 // A stable sort by digits of 8 bits, lowest first, by one cluster of 16 blocks or 8: each warp counts the
@@ -461,18 +488,6 @@ __device__ __forceinline__ void emb_sort(const EmbSort& a, SortSums& q)
         }
         cluster_sync();                      // the pass is written, and the blocks' totals are read
     }
-}
-
-// a row of zeros by a warp: 16 bytes at a time, its ends up to the next 16-byte boundary by elements of 2
-__device__ __forceinline__ void zero_row(char* row, int64_t bytes, int lane)
-{
-    char* const end = row + bytes;
-    char* const a = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(row) + 15) & ~uintptr_t(15));
-    char* const b = reinterpret_cast<char*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
-    for (char* p = a + lane * 16; p < b; p += 512) *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
-    char* const head = a < b ? a : end;              // (a row may lie within 32 bytes)
-    if (row + lane * 2 < head) *reinterpret_cast<uint16_t*>(row + lane * 2) = 0;
-    if (a < b && b + lane * 2 < end) *reinterpret_cast<uint16_t*>(b + lane * 2) = 0;
 }
 
 __device__ __forceinline__ void check_ids(const EmbSort& a, int first, int step)
@@ -941,10 +956,15 @@ int ito_embedding_fwd(const int32_t* ids, int64_t n, const void* table, int64_t 
     if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const bool vec = rows_in_eights(table, type, ldt, classes, d) && rows_in_eights(y, out_type, ldy, n, d);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (type == ITO_F32) return run_emb_fwd_to<float>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
-    if (type == ITO_BF16)
-        return run_emb_fwd_to<__nv_bfloat16>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
-    return run_emb_fwd_to<__half>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
+    if (type == ITO_F32) r = run_emb_fwd_to<float>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
+    else if (type == ITO_BF16)
+        r = run_emb_fwd_to<__nv_bfloat16>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
+    else r = run_emb_fwd_to<__half>(out_type, ids, n, table, ldt, classes, d, vec, scale, y, ldy, err, s);
+    if (r || std::isfinite(scale)) return r;
+    const int64_t size = type_bytes(out_type);
+    launch_pdl(k_emb_none, (unsigned)std::min<int64_t>((n + kEmbThreads / 32 - 1) / (kEmbThreads / 32), 8 * num_sms()), kEmbThreads, 0,
+               s, ids, n, classes, y, ldy * size, d * size);
+    return launch_status("embedding");
 }
 
 size_t ito_embedding_bwd_workspace_size(int64_t n, int classes, int d)
