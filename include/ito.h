@@ -937,7 +937,7 @@ size_t ito_linear_cross_entropy_bwd_workspace_size(const void *x, int64_t ldx, c
  *   dl_j = g_loss * (p_j - [j == target]) + g_lse * p_j, rounded once to `type` (it
  *          is an operand of the products below; in ITO_F16 after multiplication by a
  *          power of two that brings the largest |g_loss| + |g_lse| (without g_loss in
- *          rows that have no token) to 2^12 .. 2^13)
+ *          rows that have no token) to 2^12 .. 2^13; 2^126 at most)
  *   dx[row][k] = sum_j dl_j * W[j][k]             in `type` (summed in 32 bits)
  *   dW[j][k] = sum over rows of dl_j * x[row][k]  in `out_type` (type or ITO_F32)
  * lse: as the forward pass wrote it; g_loss: float [rows]; g_lse: float [rows] or

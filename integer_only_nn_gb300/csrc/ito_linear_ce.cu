@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kCeJoinThreads)
 
 // float16 has no room below 6e-8 for the gradients of rare classes: dl carries a power of two that
 // brings the largest |g| to 2^12 .. 2^13, and the products' sums are multiplied by its inverse. What rows without
-// a token hold in g_loss does not count.
+// a token hold in g_loss does not count. (The factor and its inverse are both normal floats: 2^-115 for the largest |g|,
+// 2^126 at most, which leaves those below 2^-114 less than that.)
 // out: [2] that factor and its inverse
 __global__ void __launch_bounds__(1024)
     k_ce_scale(const float* __restrict__ g_loss, const float* __restrict__ g_lse, const int32_t* __restrict__ targets,
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(1024)
     int e = 0;
     if (m > 0.0f && m < INFINITY) {
         frexpf(m, &e);                       // m = f 2^e, f in [1/2, 1)
-        e = min(max(13 - e, -100), 100);
+        e = min(13 - e, 126);               // (e is 128 at most)
     }
     out[0] = ldexpf(1.0f, e);
     out[1] = ldexpf(1.0f, -e);

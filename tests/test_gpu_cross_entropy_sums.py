@@ -131,3 +131,16 @@ def test_logits_of_long_rows(torch, ito, rows, d, classes, offset):
     within(lse, f64(want), f64(e), "lse")
     l = want - L.gather(1, t.long()[:, None])[:, 0]
     within(loss, f64(l), f64(e + eL + U * l.abs()), "loss")
+
+
+@pytest.mark.parametrize("rows", [5, 60])
+@pytest.mark.parametrize("k", [-113, -105, 105, 112, 118, 124])
+def test_large_and_small_factors_in_float16(torch, ito, rows, k):
+    """Factors at both ends of float32: the gradients scale with them exactly (a power of two), which float32 results show."""
+    x, W = normal(torch, (rows, 64), 4, 1.0, "float16"), normal(torch, (2000, 64), 5, 0.25, "float16")
+    t = (torch.arange(rows, device="cuda") * 31 - 1).to(torch.int32)
+    _, lse = ito.ito_linear_cross_entropy_fwd(x, W, t)
+    g = normal(torch, (rows,), 6).abs().clamp(0.1, 3.5)
+    dw = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, g, dw_dtype=torch.float32)[1]
+    far = ito.ito_linear_cross_entropy_bwd(x, W, t, lse, g * 2.0 ** k, dw_dtype=torch.float32)[1]
+    assert bool(torch.isfinite(far).all()) and torch.equal(far, dw * 2.0 ** k)
