@@ -813,7 +813,8 @@ size_t ito_fp_gated_linear_fwd_workspace_size(const void *x, int64_t ldx, const 
  *   h = act(g) * u,  zg = g,  zu = u, each rounded once to `type`
  * type: ITO_BF16 or ITO_F16, of all tensors but the biases; zg, zu: both for the
  * backward pass, or both NULL; bias_type: type or ITO_F32, of bias_g and bias_u
- * [OC] (each may be NULL: none); act: ito_act. A few rows (B up to 16 to 32)
+ * [OC] (each may be NULL: none); act: ito_act. Fewer than 16 rows, and
+ * up to 32 that start on 16-byte boundaries with at most 2^22 elements to a weight,
  * stream both weights once past them. workspace: 256-byte aligned, at least
  * ito_fp_gated_linear_fwd_workspace_size() bytes (may be NULL where that is 0).
  * Errors as ito_fp_linear_fwd. */

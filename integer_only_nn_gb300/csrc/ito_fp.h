@@ -132,6 +132,7 @@ int fp_check_sizes(int B, int IC, int OC);
 int fp_check_tensor(const void* p, int type, int64_t ld, int rows, int cols, const char* name);
 int fp_check_types(int type, int out_type, int act);
 int fp_check_ws(const void* ws, size_t bytes, size_t need);
+inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Whether a few rows of x stream W (see ito_fp_rows.cuh) instead of taking tensor-core tiles: the plain linear

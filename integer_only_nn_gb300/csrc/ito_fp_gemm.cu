@@ -1213,8 +1213,6 @@ static FpPlan fp_plan(int M, int N, int K, bool b_mn, FpEnd end = FpEnd::Linear,
     return best;
 }
 
-static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
-
 // planes of sums that a slice leaves
 static int planes(FpEnd end, int halves) { return end == FpEnd::Gated ? 2 : halves; }
 

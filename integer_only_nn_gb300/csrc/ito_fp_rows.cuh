@@ -59,7 +59,7 @@ constexpr int kRowsWarps = END == FpEnd::Linear || NT > 2 ? 8 : 16;
 // of a warp, and their sums are added up, rounded. (The linear and the gated layer's results are rounded to 16 bits.)
 constexpr int kRowsChain = 1024;
 // steps of 32 k whose loads of W are in flight together
-template <FpEnd END, bool VEC>
+template <FpEnd END>
 constexpr int kRowsSteps = END == FpEnd::Linear ? 4 : 2;
 
 // VEC: both operands' rows start on 16-byte boundaries and IC is a multiple of 8. Of other rows each eight
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
               const uint16_t* __restrict__ W2, int64_t ldw2, int B, int IC, int OC, const __grid_constant__ FpEpilogue e,
               const __grid_constant__ FpMore more, int* err)
 {
-    constexpr int U = kRowsSteps<END, VEC>, WS = END == FpEnd::Gated ? 2 : 1;
+    constexpr int U = kRowsSteps<END>, WS = END == FpEnd::Gated ? 2 : 1;
     constexpr bool SHIFT = !VEC && END != FpEnd::Linear;
     using Raw = typename std::conditional<SHIFT, Eight16, uint4>::type;
     extern __shared__ float rows_part[];
@@ -253,11 +253,14 @@ static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw
     // number of warps is part of the sums' order: the plain linear layer keeps its.)
     const int blocks = (OC + 15) / 16;
     const int most = END == FpEnd::Linear ? 8 : std::min(kRowsWarps<END, NT>, blocks < num_sms() ? 16 : blocks < 2 * num_sms() ? 8 : 4);
-    const int step = 32 * (vec ? kRowsSteps<END, true> : kRowsSteps<END, false>);
+    constexpr int step = 32 * kRowsSteps<END>;
     const int warps = std::min(most, std::max(1, (IC + step - 1) / step));
-    constexpr bool LOGITS = END == FpEnd::Loss || END == FpEnd::DLogits;
-    auto* kern = vec ? k_fp_rows<END, NT, true, false> : k_fp_rows<END, NT, false, false>;
-    if (LOGITS && IC > warps * kRowsChain) kern = vec ? k_fp_rows<END, NT, true, LOGITS> : k_fp_rows<END, NT, false, LOGITS>;
+    // (more than 16 rows at any alignment: the plain linear layer alone, see fp_few_rows; others have one instance)
+    constexpr bool LOGITS = END == FpEnd::Loss || END == FpEnd::DLogits, ANY = END == FpEnd::Linear || NT <= 2;
+    if (!ANY && !vec) return set_error(ITO_ERR_ARG, "rows that do not start on 16-byte boundaries");
+    const bool lengthy = LOGITS && IC > warps * kRowsChain;
+    auto* kern = lengthy ? k_fp_rows<END, NT, true, LOGITS> : k_fp_rows<END, NT, true, false>;
+    if (!vec) kern = lengthy ? k_fp_rows<END, NT, !ANY, LOGITS> : k_fp_rows<END, NT, !ANY, false>;
     launch_pdl(kern, (OC + 15) / 16, warps * 32,
                (size_t)warps * (END == FpEnd::Gated ? 2 : 1) * 16 * 8 * NT * sizeof(float), s,
                static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(W), ldw,

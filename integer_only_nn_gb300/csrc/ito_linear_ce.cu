@@ -116,8 +116,6 @@ static int ce_piece(int rows, int classes)
 // a row of dl: whole lines of 128 bytes, which is what the products' loads take of it at a time
 static int64_t ce_ldl(int64_t piece) { return (piece + 63) & ~int64_t(63); }
 
-static int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
-
 static int ce_parts(int rows, int d, int classes, bool few)
 {
     if (few) return (classes + 15) / 16;
