@@ -136,9 +136,10 @@ inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Whether a few rows of x stream W (see ito_fp_rows.cuh) instead of taking tensor-core tiles: the plain linear
-// layer's rule, and the other ends' (OC: of one of the gated layer's two weights; vec: fp_rows_vec of all operands).
+// layer's rule, the gated layer's (OC: of one of its two weights; vec: fp_rows_vec of all operands), and that of logits.
 bool fp_rows_kernel(int B, int IC, int OC);
 bool fp_few_rows(int B, int IC, int OC, bool vec);
+bool fp_few_logits(int B, int IC, int OC, bool vec);
 // Whether x's and W's rows start on 16-byte boundaries and end with 16 bytes.
 bool fp_rows_vec(const void* x, int64_t ldx, const void* W, int64_t ldw, int B, int IC, int OC);
 

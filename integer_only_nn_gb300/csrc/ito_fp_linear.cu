@@ -36,6 +36,15 @@ bool fp_few_rows(int B, int IC, int OC, bool vec)
     return B < 16 || (vec && B <= 32 && (int64_t)IC * OC <= (1 << 22));
 }
 
+// Logits, forward and in the gradient alike (its logits have to be the same sums). us forward + both gradients, so : in tiles:
+// 24 rows 1024 -> 1000 7.7 + 16.3 : 9.6 + 19.0, 2048 -> 2000 10.0 + 25.4 : 13.7 + 28.0, 512 -> 8000 8.6 + 21.4 : 8.8 + 21.4, 256
+// -> 16000 11.1 + 24.8 : 8.0 + 22.5, 64 -> 8000 8.8 + 17.3 : 6.2 + 15.0, 4096 -> 1000 13.8 + 25.6 : 10.3 + 21.3; 32 rows 1024
+// -> 1000 8.5 + 16.7 : 9.6 + 19.0, 2048 -> 500 11.1 + 17.4 : 9.3 + 16.1, 32768 -> 100 94 + 114 : 17 + 26.
+bool fp_few_logits(int B, int IC, int OC, bool vec)
+{
+    return fp_few_rows(B, IC, OC, vec) && (B <= 16 || (IC >= 512 && IC <= 2048));
+}
+
 // --------------------------------------------------------- element-wise passes
 
 // Eight elements to a thread, which start at any element of their row and go to an aligned place (Eight16).

@@ -66,8 +66,9 @@ constexpr int kRowsSteps = END == FpEnd::Linear ? 4 : 2;
 // elements come in words and a shift (Eight16; the plain linear layer, whose sums keep their
 // order and so their four steps, loads them one by one). The gated layer
 // streams two weights, 16 rows of each to a block, half as many steps of each ahead (the same bytes
-// in flight and registers). LONG: logits of rows that take a warp more than one chain; the sums wait in shared memory, because
-// registers for them cost blocks of an SM (13 x 1531 x 50001 f16 143 us instead of 122). A Loss leaves each row's parts of 16 columns; DLogits are as from the tensor cores' kernels.
+// in flight and registers). LONG: logits of rows that take a warp more than one chain; the sums wait in shared
+// memory, because registers for them cost blocks of an SM (13 x 1531 x 50001 f16 143 us instead of 122). A Loss leaves each
+// row's parts of 16 columns; DLogits are as from the tensor cores' kernels.
 template <FpEnd END, int NT, bool VEC, bool LONG>
 __global__ void __launch_bounds__(kRowsWarps<END, NT> * 32)
     k_fp_rows(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ W, int64_t ldw,
@@ -255,8 +256,9 @@ static int fp_launch_rows(const void* x, int64_t ldx, const void* W, int64_t ldw
     const int most = END == FpEnd::Linear ? 8 : std::min(kRowsWarps<END, NT>, blocks < num_sms() ? 16 : blocks < 2 * num_sms() ? 8 : 4);
     constexpr int step = 32 * kRowsSteps<END>;
     const int warps = std::min(most, std::max(1, (IC + step - 1) / step));
-    // (more than 16 rows at any alignment: the plain linear layer alone, see fp_few_rows; others have one instance)
-    constexpr bool LOGITS = END == FpEnd::Loss || END == FpEnd::DLogits, ANY = END == FpEnd::Linear || NT <= 2;
+    // (more than 16 rows at any alignment: the plain linear layer alone, see fp_few_rows; others have one instance. More
+    // than 16 rows of logits are no longer than a chain of 8 warps, see fp_few_logits)
+    constexpr bool LOGITS = (END == FpEnd::Loss || END == FpEnd::DLogits) && NT <= 2, ANY = END == FpEnd::Linear || NT <= 2;
     if (!ANY && !vec) return set_error(ITO_ERR_ARG, "rows that do not start on 16-byte boundaries");
     const bool lengthy = LOGITS && IC > warps * kRowsChain;
     auto* kern = lengthy ? k_fp_rows<END, NT, true, LOGITS> : k_fp_rows<END, NT, true, false>;

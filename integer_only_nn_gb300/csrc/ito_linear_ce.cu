@@ -130,7 +130,7 @@ struct CeFew {
 };
 static CeFew ce_few(const void* x, int64_t ldx, const void* W, int64_t ldw, int rows, int d, int classes)
 {
-    return CeFew{fp_few_grad_rows(rows), fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes))};
+    return CeFew{fp_few_grad_rows(rows), fp_few_logits(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes))};
 }
 
 // of a piece of n classes
@@ -162,7 +162,7 @@ size_t ito_linear_cross_entropy_fwd_workspace_size(const void* x, int64_t ldx, c
                                                    int d, int classes)
 {
     if (fp_check_sizes(rows, d, classes)) return 0;
-    const bool few = fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
+    const bool few = fp_few_logits(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
     const size_t own = align256((size_t)ce_parts(rows, d, classes, few) * rows * 8) + align256((size_t)rows * 4);
     if (few) return own;
     return own + fp_copy_bytes(x, ldx, rows, d) + fp_copy_bytes(W, ldw, classes, d) +
@@ -183,7 +183,7 @@ int ito_linear_cross_entropy_fwd(const void* x, int64_t ldx, const void* W, int6
     int* err = device_error_word();
     if (!err) return set_error(ITO_ERR_CUDA, "device error word unavailable");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool few = fp_few_rows(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
+    const bool few = fp_few_logits(rows, d, classes, fp_rows_vec(x, ldx, W, ldw, rows, d, classes));
     const int parts = ce_parts(rows, d, classes, few);
     char* ws = static_cast<char*>(workspace);
     FpMore more{};

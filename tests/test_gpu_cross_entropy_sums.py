@@ -73,7 +73,8 @@ def check_confident_bwd(torch, x, W, t, dtype, dx, dw):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
-@pytest.mark.parametrize("rows,d,classes", [(3, 4096, 600), (16, 8192, 640), (20, 4096, 600), (17, 8192, 700), (40, 4096, 600),
+@pytest.mark.parametrize("rows,d,classes", [(3, 4096, 600), (16, 8192, 640), (20, 4096, 600), (17, 8192, 700),
+                                            (24, 2048, 2000), (20, 1024, 4000), (30, 32768, 100), (40, 4096, 600),
                                             (130, 4095, 611), (300, 8192, 600), (300, 4104, 5000)])
 def test_gradient_of_confident_rows(torch, ito, rows, d, classes, dtype):
     """1 - p of the targets from 1e-3 to 1e-5."""
