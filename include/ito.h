@@ -941,8 +941,10 @@ size_t ito_linear_cross_entropy_bwd_workspace_size(const void *x, int64_t ldx, c
  *          rows that have no token) to 2^12 .. 2^13; 2^126 at most)
  *   dx[row][k] = sum_j dl_j * W[j][k]             in `type` (summed in 32 bits)
  *   dW[j][k] = sum over rows of dl_j * x[row][k]  in `out_type` (type or ITO_F32)
- * lse: as the forward pass wrote it; g_loss: float [rows]; g_lse: float [rows] or
- * NULL (none). Targets outside [0, classes) as in the forward pass: no term from
+ * lse: as the forward pass of these rows, x and W (at this alignment) wrote it: their
+ * logits are then formed again as the same sums in every bit, which p - 1 of a target
+ * with nearly all of the probability depends on. g_loss: float [rows]; g_lse: float
+ * [rows] or NULL (none). Targets outside [0, classes) as in the forward pass: no term from
  * g_loss. A row whose lse is -inf, or whose factors are 0, has a gradient of 0.
  * dx or dW may be NULL (not computed). Errors as ito_linear_cross_entropy_fwd. */
 int ito_linear_cross_entropy_bwd(const void *x, int64_t ldx, const void *W, int64_t ldw, int type,

@@ -830,7 +830,7 @@ _current_device = None  # -> the current device's index
 _address = None         # Tensor.data_ptr
 _INT = (1 << 31) - 1    # the largest int of the library: ctypes would pass on the low 32 bits of a larger one
 _LONG = (1 << 63) - 1
-_MOST_CLASSES = 1 << 30 # of an embedding
+_MOST_CLASSES = 1 << 30     # of an embedding
 
 
 def _float_setup():
@@ -1235,7 +1235,8 @@ def ito_linear_cross_entropy_fwd(x, W, targets, stream=None):
 def ito_linear_cross_entropy_bwd(x, W, targets, lse, g_loss, g_lse=None, need_dx=True, need_dw=True, dw_dtype=None,
                                  stream=None):
     """Gradients of sum(g_loss loss + g_lse lse) -> (dx [rows][d] in x's type, dW [classes][d] in dw_dtype (x's type or
-    float32)); None for those not needed. g_loss, g_lse: float32 [rows]."""
+    float32)); None for those not needed. g_loss, g_lse: float32 [rows]. lse: of the forward pass of these rows, x and W, whose
+    sums are formed again."""
     torch = _torch() if _F32 is not None else _float_setup()
     if stream is not None:
         return _on_stream(lambda: ito_linear_cross_entropy_bwd(x, W, targets, lse, g_loss, g_lse, need_dx, need_dw,
